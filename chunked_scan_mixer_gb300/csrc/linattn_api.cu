@@ -1,0 +1,304 @@
+// C ABI of the first-order linear attention with a decay for each head: argument checks, the
+// segmentation of the sequence, and the passes that make up a forward and a backward
+// (linattn_pass.h).  The declarations and their documentation are in include/hla2.h.
+#include <nvtx3/nvToolsExt.h>
+
+#include "linattn_pass.h"
+
+namespace hla2 {
+int set_last_error(int code, const char* fmt, ...);
+}
+
+using namespace hla2;
+
+namespace {
+
+constexpr size_t kStatusBytes = 256;
+
+struct Range {
+    explicit Range(const char* name) { nvtxRangePushA(name); }
+    ~Range() { nvtxRangePop(); }
+    Range(const Range&) = delete;
+    Range& operator=(const Range&) = delete;
+};
+
+int ok() { return set_last_error(HLA2_OK, "%s", ""); }
+int launch_failed(const char* what) {
+    return set_last_error(HLA2_ERR_CUDA, "%s: %s", what, cudaGetErrorString(cudaGetLastError()));
+}
+
+bool lin_dim(int x) { return x == 16 || x == 32 || x == 64 || x == 128; }
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int sm_count() {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    return v;
+}
+
+int elem_size(int dtype) { return dtype == HLA2_BF16 ? 2 : 4; }
+
+// Sizes, types: what the workspace query can check.
+int check_sizes(const char* fn, const hla2_linattn_args* a) {
+    if (!a) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: args must not be NULL", fn);
+    if (a->dtype != HLA2_F32 && a->dtype != HLA2_BF16)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dtype must be HLA2_F32 or HLA2_BF16", fn);
+    if (a->B < 0 || a->H < 0 || a->Hk < 0 || a->n < 0)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: B, H, Hk and n must not be negative", fn);
+    if (!lin_dim(a->d) || !lin_dim(a->dv))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: d and dv must be 16, 32, 64 or 128 (got %d, %d)", fn, a->d,
+                              a->dv);
+    if ((a->Hk == 0) != (a->H == 0) || (a->Hk > 0 && a->H % a->Hk != 0))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: H (%d) must be a multiple of Hk (%d)", fn, a->H, a->Hk);
+    // grid limits and 32-bit head counts
+    if ((long long)a->B * a->H > 0x7fffffff || a->n > 0x7fffff00)
+        return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: B * H and n must fit in 31 bits", fn);
+    return HLA2_OK;
+}
+
+// Strides of dimensions of one element do not matter: they become the packed ones.
+int check_view(const char* fn, const char* name, hla2_view& w, int B, int H, int n, int D, int es) {
+    if (!w.p) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: %s must not be NULL", fn, name);
+    const long long per16 = 16 / es;
+    if (n <= 1) w.sn = D;
+    if (H <= 1) w.sh = w.sn * (n > 1 ? n : 1);
+    if (B <= 1) w.sb = w.sh * (H > 1 ? H : 1);
+    if (!al16(w.p) || w.sn % per16 || w.sh % per16 || w.sb % per16)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: the address and strides of %s must be multiples of 16 bytes", fn,
+                              name);
+    if (w.sn < D || w.sh < D || w.sb < D)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: the strides of %s must be at least its last dimension", fn, name);
+    return HLA2_OK;
+}
+
+struct Extent {
+    uintptr_t lo, hi;
+};
+Extent extent(const hla2_view& w, int B, int H, int n, int D, int es) {
+    const long long last = (B - 1) * w.sb + (H - 1) * w.sh + (n - 1) * w.sn + D;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(w.p);
+    return {lo, lo + (uintptr_t)last * es};
+}
+bool meet(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// ---- plan ----------------------------------------------------------------------------------
+
+struct LinPlan {
+    int W, nchunks, seg_chunks, nseg;
+};
+
+// Segments per state head.  Unit: the time of one chunk of the output pass.  More than one segment
+// adds the summary pass (about half of the output pass: it reads two of four tensors) and about two
+// chunks' time for the scan and its launch; the waves of CTAs count whole.
+LinPlan lin_plan(const hla2_linattn_args* a, int W, int slots) {
+    LinPlan p{W, (a->n + W - 1) / W, 0, 0};
+    const long long heads = (long long)a->B * a->Hk;
+    if (p.nchunks == 0 || heads == 0) return p;
+    double best = 0;
+    long long most = 4LL * slots / heads + 1;
+    if (most > p.nchunks) most = p.nchunks;
+    if (most > 4096) most = 4096;
+    for (long long want = 1; want <= most; ++want) {
+        const int sc = (int)((p.nchunks + want - 1) / want), ns = (p.nchunks + sc - 1) / sc;
+        const long long waves = (heads * ns + slots - 1) / slots;
+        const double cost = (double)waves * sc * (ns > 1 ? 1.5 : 1.0) + (ns > 1 ? 2.0 : 0.0);
+        if (p.nseg == 0 || cost < best) best = cost, p.seg_chunks = sc, p.nseg = ns;
+    }
+    return p;
+}
+
+LinPlan plan_of(const hla2_linattn_args* a) {
+    return lin_plan(a, lin_simt_width(a->d, a->dv), sm_count() * lin_simt_ctas(a->d, a->dv, 1));
+}
+
+size_t state_array_bytes(const hla2_linattn_args* a, const LinPlan& p) {
+    return ((size_t)a->B * a->Hk * p.nseg * a->d * a->dv * sizeof(float) + 255) & ~size_t(255);
+}
+
+int run_pass(const LinPass& a, bool summary, int dtype, cudaStream_t st) {
+    return launch_lin_simt(a, summary, dtype == HLA2_BF16, st);
+}
+
+// Common fields of every pass of one call.
+LinPass base_pass(const hla2_linattn_args* a, const LinPlan& p) {
+    LinPass s{};
+    s.B = a->B;
+    s.Hs = a->Hk;
+    s.rx = s.rk = 1;
+    s.n = a->n;
+    s.W = p.W;
+    s.nchunks = p.nchunks;
+    s.seg_chunks = p.seg_chunks;
+    s.nseg = p.nseg;
+    s.s_intra = s.s_carry = s.s_state = 1.f;
+    s.gamma = a->gamma;
+    s.lengths = a->lengths;
+    s.status = static_cast<int*>(a->workspace);
+    return s;
+}
+
+// Forward states of k, v (reverse: of q, dout): summaries, then the scan; the final state too.
+int states(const hla2_linattn_args* a, const LinPlan& p, LinPass s, float* sums, float* carry, const float* init,
+           float* final_state, cudaStream_t st) {
+    if (p.nseg > 1 || (final_state && p.nseg > 0)) {
+        s.sums = sums;
+        if (run_pass(s, true, a->dtype, st)) return -1;
+    }
+    if (p.nseg > 1 || final_state || init)
+        return launch_lin_scan(sums, p.nseg > 0 ? carry : nullptr, init, final_state, a->gamma, a->lengths, a->B, a->Hk,
+                               a->n, p.seg_chunks * p.W, p.nseg, a->d * a->dv, s.rev, st);
+    return 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t hla2_linattn_workspace_bytes(const hla2_linattn_args* a, int backward, int want_final) {
+    if (check_sizes("hla2_linattn_workspace_bytes", a) != HLA2_OK) return (size_t)-1;
+    ok();
+    const LinPlan p = plan_of(a);
+    if (p.nseg == 0) return 0;
+    const bool fwd_states = p.nseg > 1 || a->init_state || (!backward && want_final);
+    const bool rev_states = backward && (p.nseg > 1 || want_final);
+    return kStatusBytes + 2 * state_array_bytes(a, p) * ((fwd_states ? 1 : 0) + (rev_states ? 1 : 0));
+}
+
+int hla2_linattn_forward(const hla2_linattn_args* args, hla2_view out, float* final_state, hla2_stream_t stream) {
+    static const char* const fn = "hla2_linattn_forward";
+    Range range(fn);
+    if (int rc = check_sizes(fn, args)) return rc;
+    hla2_linattn_args a = *args;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (a.B == 0 || a.H == 0) return ok();
+    const int es = elem_size(a.dtype);
+    if (!al16(a.init_state) || !al16(final_state))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: states must be 16-byte aligned", fn);
+    if (a.n > 0) {
+        if (int rc = check_view(fn, "q", a.q, a.B, a.H, a.n, a.d, es)) return rc;
+        if (int rc = check_view(fn, "k", a.k, a.B, a.Hk, a.n, a.d, es)) return rc;
+        if (int rc = check_view(fn, "v", a.v, a.B, a.Hk, a.n, a.dv, es)) return rc;
+        if (int rc = check_view(fn, "out", out, a.B, a.H, a.n, a.dv, es)) return rc;
+        const Extent eo = extent(out, a.B, a.H, a.n, a.dv, es);
+        if (meet(eo, extent(a.q, a.B, a.H, a.n, a.d, es)) || meet(eo, extent(a.k, a.B, a.Hk, a.n, a.d, es)) ||
+            meet(eo, extent(a.v, a.B, a.Hk, a.n, a.dv, es)))
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps an input", fn);
+    }
+    const size_t need = hla2_linattn_workspace_bytes(&a, 0, final_state != nullptr);
+    if (need > 0 && (!a.workspace || a.workspace_bytes < need || !al16(a.workspace)))
+        return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, need);
+    const LinPlan p = plan_of(&a);
+    float* sums = p.nseg ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kStatusBytes) : nullptr;
+    float* carry = p.nseg ? sums + state_array_bytes(&a, p) / sizeof(float) : nullptr;
+
+    LinPass s = base_pass(&a, p);
+    s.x = a.q, s.k = a.k, s.v = a.v, s.y = out;
+    s.rx = a.H / a.Hk;
+    s.dx = a.d, s.dy = a.dv;
+    s.s_intra = s.s_carry = a.scale;
+    if (states(&a, p, s, sums, carry, a.init_state, final_state, st)) return launch_failed("linear attention states");
+    if (p.nseg == 0) return ok();
+    s.carry = p.nseg > 1 || a.init_state ? carry : nullptr;
+    if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention output pass");
+    return ok();
+}
+
+int hla2_linattn_backward(const hla2_linattn_args* args, hla2_view dout, hla2_view dq, hla2_view dk, hla2_view dv,
+                          const float* dfinal_state, float* dinit_state, hla2_stream_t stream) {
+    static const char* const fn = "hla2_linattn_backward";
+    Range range(fn);
+    if (int rc = check_sizes(fn, args)) return rc;
+    hla2_linattn_args a = *args;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (a.B == 0 || a.H == 0) return ok();
+    const int es = elem_size(a.dtype);
+    if (!al16(a.init_state) || !al16(dfinal_state) || !al16(dinit_state))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: states must be 16-byte aligned", fn);
+    if (a.n > 0) {
+        if (int rc = check_view(fn, "q", a.q, a.B, a.H, a.n, a.d, es)) return rc;
+        if (int rc = check_view(fn, "k", a.k, a.B, a.Hk, a.n, a.d, es)) return rc;
+        if (int rc = check_view(fn, "v", a.v, a.B, a.Hk, a.n, a.dv, es)) return rc;
+        if (int rc = check_view(fn, "dout", dout, a.B, a.H, a.n, a.dv, es)) return rc;
+        if (int rc = check_view(fn, "dq", dq, a.B, a.H, a.n, a.d, es)) return rc;
+        if (int rc = check_view(fn, "dk", dk, a.B, a.Hk, a.n, a.d, es)) return rc;
+        if (int rc = check_view(fn, "dv", dv, a.B, a.Hk, a.n, a.dv, es)) return rc;
+        const Extent in[4] = {extent(a.q, a.B, a.H, a.n, a.d, es), extent(a.k, a.B, a.Hk, a.n, a.d, es),
+                              extent(a.v, a.B, a.Hk, a.n, a.dv, es), extent(dout, a.B, a.H, a.n, a.dv, es)};
+        const Extent go[3] = {extent(dq, a.B, a.H, a.n, a.d, es), extent(dk, a.B, a.Hk, a.n, a.d, es),
+                              extent(dv, a.B, a.Hk, a.n, a.dv, es)};
+        for (const Extent& o : go)
+            for (const Extent& i : in)
+                if (meet(o, i)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps an input", fn);
+        if (dq.p == dk.p || dq.p == dv.p || dk.p == dv.p)
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dq, dk and dv must be distinct", fn);
+    }
+    const bool rev_state = dfinal_state || dinit_state;
+    const size_t need = hla2_linattn_workspace_bytes(&a, 1, rev_state);
+    if (need > 0 && (!a.workspace || a.workspace_bytes < need || !al16(a.workspace)))
+        return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, need);
+    const LinPlan p = plan_of(&a);
+    const size_t sf = state_array_bytes(&a, p) / sizeof(float);
+    float* at = p.nseg ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kStatusBytes) : nullptr;
+    const int group = a.H / a.Hk;
+
+    // forward states of k, v; dq
+    if (p.nseg > 0) {
+        LinPass s = base_pass(&a, p);
+        const bool carried = p.nseg > 1 || a.init_state;
+        s.k = a.k, s.v = a.v;
+        s.dx = a.d, s.dy = a.dv;
+        if (states(&a, p, s, at, at + sf, a.init_state, nullptr, st)) return launch_failed("linear attention states");
+        s.carry = carried ? at + sf : nullptr;
+        if (carried) at += 2 * sf;
+        s.x = dout, s.k = a.v, s.v = a.k, s.y = dq;
+        s.rx = group;
+        s.dx = a.dv, s.dy = a.d;
+        s.carry_t = 1;
+        s.s_intra = s.s_carry = a.scale;
+        if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention dq pass");
+    }
+    // reverse states of q, dout (scaled); dv, dk
+    LinPass s = base_pass(&a, p);
+    s.rev = 1;
+    s.rk = group;
+    s.k = a.q, s.v = dout;
+    s.dx = a.d, s.dy = a.dv;
+    s.s_intra = s.s_state = a.scale;
+    if (states(&a, p, s, at, at + sf, dfinal_state, dinit_state, st))
+        return launch_failed("linear attention reverse states");
+    if (p.nseg == 0) return ok();
+    s.carry = p.nseg > 1 || dfinal_state ? at + sf : nullptr;
+    s.x = a.k, s.y = dv;
+    if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention dv pass");
+    s.x = a.v, s.k = dout, s.v = a.q, s.y = dk;
+    s.dx = a.dv, s.dy = a.d;
+    s.carry_t = 1;
+    if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention dk pass");
+    return ok();
+}
+
+int hla2_linattn_decode_step(float* state, const void* q, const void* k, const void* v, void* out, int N, int H,
+                             int Hk, int d, int dv, const float* gamma, float scale, int dtype,
+                             hla2_stream_t stream) {
+    static const char* const fn = "hla2_linattn_decode_step";
+    Range range(fn);
+    hla2_linattn_args a{};
+    a.dtype = dtype, a.B = N, a.H = H, a.Hk = Hk, a.n = 1, a.d = d, a.dv = dv;
+    if (int rc = check_sizes(fn, &a)) return rc;
+    if (N == 0 || H == 0) return ok();
+    if (!state || !q || !k || !v || !out)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: pointers must not be NULL", fn);
+    if (!al16(state) || !al16(q) || !al16(k) || !al16(v) || !al16(out))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    if (out == q || out == k || out == v)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps an input", fn);
+    if (launch_lin_step(state, q, k, v, out, N, H, Hk, d, dv, gamma, scale, dtype == HLA2_BF16,
+                        reinterpret_cast<cudaStream_t>(stream)))
+        return launch_failed("linear attention step");
+    return ok();
+}
+
+}  // extern "C"

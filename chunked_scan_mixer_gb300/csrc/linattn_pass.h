@@ -1,0 +1,62 @@
+// Internal interface of the first-order linear attention with a decay for each head
+// (linattn_api.cu composes the passes; linattn_simt.cu and linattn_tc.cu run them).
+//
+// Every pass is the same scan over rows t of one state head, forward or in reverse:
+//     y_t = s_intra sum_i g^|t-i| (x_t . k_i) v_i + s_carry g^(distance to the carry) x_t^T Sig
+// over the valid rows i <= t (reverse: i >= t) of t's segment, Sig (dx x dy, float32) being the
+// state that enters the segment:  forward  Sig = sum_i g^(t0-1-i) k_i v_i^T  (the state
+// before the segment's first row t0),  reverse  Sig = sum_i g^(i-t1) k_i v_i^T  (t1 the row
+// after the segment's last).  With
+//     forward output   x = q,    k = k,    v = v
+//     dq               x = dout, k = v,    v = k     (Sig: the forward states, transposed)
+//     dv  (reverse)    x = k,    k = q,    v = dout
+//     dk  (reverse)    x = v,    k = dout, v = q     (Sig: the reverse states, transposed)
+#pragma once
+
+#include "common.cuh"
+
+namespace hla2 {
+
+struct LinPass {
+    hla2_view x, k, v;
+    hla2_view y;               // written
+    int B, Hs;                 // state heads: grid rows are b * Hs + s
+    int rx, rk;                // x / y heads s rx .. and key / value heads s rk .. per state head; one of them is 1
+    int n, dx, dy;
+    int W, nchunks, seg_chunks, nseg;
+    int rev;
+    float s_intra, s_carry, s_state;  // s_state: factor of k v^T in the state
+    const float* gamma;        // [Hs] or NULL
+    const int* lengths;        // [B] or NULL
+    const float* carry;        // [B Hs][nseg] states entering the segments, or NULL (zero)
+    int carry_t;               // they are stored dy x dx
+    float* sums;               // summary pass: [B Hs][nseg][dx dy], each segment's state from zero
+    int* status;               // word that a wait which gave up is recorded in
+};
+
+__host__ __device__ inline int lin_len(const int* lengths, int b, int n) {
+    if (!lengths) return n;
+    const int l = lengths[b];
+    return l < 0 ? 0 : l > n ? n : l;
+}
+
+__device__ __forceinline__ float lin_decay(const LinPass& a, int s) { return a.gamma ? __ldg(a.gamma + s) : 1.0f; }
+
+// SIMT passes (float32 arithmetic, any type and size); W = lin_simt_width(dx, dy).
+int lin_simt_width(int dx, int dy);
+int lin_simt_ctas(int dx, int dy, int rk);  // resident CTAs per SM
+int launch_lin_simt(const LinPass& a, bool summary, bool is_bf16, cudaStream_t st);
+
+// States entering the segments from the segment summaries, in one serial pass over the segments
+// per state element:  carry[s] = cur;  cur = g^(valid rows of s) cur + sums[s]  in the
+// scan's direction.  init (nullable) is the state before the scan; reverse: the gradient of the
+// final state, which enters as init / g.  final (nullable) receives the state after it;
+// reverse: times g, the gradient of the initial state.  sums may be NULL with nseg == 1 and no final.
+int launch_lin_scan(const float* sums, float* carry, const float* init, float* final_state, const float* gamma,
+                    const int* lengths, int B, int Hs, int n, int seg_rows, int nseg, int elems, int rev,
+                    cudaStream_t st);
+
+int launch_lin_step(float* state, const void* q, const void* k, const void* v, void* out, int N, int H, int Hk, int d,
+                    int dv, const float* gamma, float scale, bool is_bf16, cudaStream_t st);
+
+}  // namespace hla2

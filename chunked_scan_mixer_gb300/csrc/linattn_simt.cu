@@ -1,0 +1,341 @@
+// First-order linear attention with a decay for each head: the chunk passes in float32
+// arithmetic (SIMT), the scan over segments, and the step of single tokens.  The mathematics
+// of a pass is in linattn_pass.h.
+//
+// Chunk pass.  One CTA runs the chunks of one segment of one state head.  Per chunk of W rows
+// (Wc of them valid) and state Sig at the chunk's entry, forward:
+//     A = (X K^T) * [j <= i] g^(i-j)          Y = s_intra A V + s_carry diag(g^(i+1)) X Sig
+//     Sig <- g^Wc Sig + s_state (diag(g^(Wc-1-j)) K)^T V
+// and in reverse [j >= i] g^(j-i), g^(Wc-i) and g^j.  X, K^T, V, A and Sig stay in shared memory;
+// every product is register-tiled (simt_tile.cuh).
+#include "linattn_pass.h"
+#include "simt_tile.cuh"
+
+namespace hla2 {
+
+namespace {
+
+using simt::kThreads;
+using simt::pad;
+
+struct LinSmem {
+    int X, Kt, V, A, S, Y, gp, total;
+};
+__host__ __device__ inline LinSmem lin_smem(int dx, int dy, int W, bool keep_y) {
+    LinSmem L;
+    int o = 0;
+    L.X = o;  o += W * pad(dx);
+    L.Kt = o; o += dx * pad(W);
+    L.V = o;  o += W * dy;
+    L.A = o;  o += W * pad(W);
+    L.S = o;  o += dx * dy;
+    L.Y = o;  o += keep_y ? W * dy : 0;
+    L.gp = o; o += W + 4;
+    L.total = o;
+    return L;
+}
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const bf16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+template <typename T>
+__device__ __forceinline__ const T* row_ptr(const hla2_view& w, int b, int h, int row) {
+    return static_cast<const T*>(w.p) + b * w.sb + h * w.sh + row * w.sn;
+}
+
+// rows [row0, row0 + Wc) of a view as W x D floats (leading dimension ld), the rest zero
+template <typename T>
+__device__ __forceinline__ void load_rows(float* dst, int ld, const hla2_view& w, int b, int h, int row0, int W, int Wc,
+                                          int D) {
+    const int nd = D >> 2;
+    for (int e = threadIdx.x; e < W * nd; e += kThreads) {
+        const int i = e / nd, f = (e % nd) * 4;
+        const float4 t = i < Wc ? load4(row_ptr<T>(w, b, h, row0 + i) + f) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(dst + i * ld + f) = t;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void load_rows_t(float* dst, int ld, const hla2_view& w, int b, int h, int row0, int W,
+                                            int Wc, int D) {
+    const int nd = D >> 2;
+    for (int e = threadIdx.x; e < W * nd; e += kThreads) {
+        const int i = e % W, f = (e / W) * 4;  // lanes on rows: the transposed stores fall in distinct banks
+        const float4 t = i < Wc ? load4(row_ptr<T>(w, b, h, row0 + i) + f) : make_float4(0.f, 0.f, 0.f, 0.f);
+        dst[f * ld + i] = t.x;
+        dst[(f + 1) * ld + i] = t.y;
+        dst[(f + 2) * ld + i] = t.z;
+        dst[(f + 3) * ld + i] = t.w;
+    }
+}
+
+template <typename T, bool SUMMARY>
+__global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
+    extern __shared__ __align__(16) float sm[];
+    const int dx = a.dx, dy = a.dy, W = a.W;
+    const bool keep_y = !SUMMARY && a.rk > 1;
+    const LinSmem L = lin_smem(dx, dy, W, keep_y);
+    float *Xs = sm + L.X, *Kt = sm + L.Kt, *Vs = sm + L.V, *As = sm + L.A, *S = sm + L.S, *Ys = sm + L.Y,
+          *gp = sm + L.gp;
+    const int tid = threadIdx.x;
+    const int seg = blockIdx.y, bs = blockIdx.x, b = bs / a.Hs, s = bs % a.Hs;
+    const int len = lin_len(a.lengths, b, a.n);
+    const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
+    const float log2g = log2f(lin_decay(a, s));
+    const bool rev = a.rev != 0;
+    for (int i = tid; i <= W; i += kThreads) gp[i] = pow_decay(log2g, (float)i);
+    const float* carry = SUMMARY || !a.carry ? nullptr : a.carry + ((size_t)bs * a.nseg + seg) * dx * dy;
+    for (int e = tid; e < dx * dy; e += kThreads)
+        S[e] = !carry ? 0.f : a.carry_t ? carry[(e % dy) * dx + e / dy] : carry[e];
+
+    const int items = a.rx > a.rk ? a.rx : a.rk;
+    for (int cc = c0; cc < c1; ++cc) {
+        const int c = rev ? c0 + c1 - 1 - cc : cc;
+        const int row0 = c * W, Wn = min(W, a.n - row0), Wc = max(0, min(Wn, len - row0));
+        if (Wc == 0 && SUMMARY) continue;
+        for (int r = 0; r < items; ++r) {
+            const bool x_new = r == 0 || a.rx > 1, kv_new = r == 0 || a.rk > 1;
+            const bool y_last = a.rx > 1 || r == items - 1, s_now = a.rk > 1 || r == items - 1;
+            const int hx = s * a.rx + (a.rx > 1 ? r : 0), hk = s * a.rk + (a.rk > 1 ? r : 0);
+            __syncthreads();
+            if (!SUMMARY && x_new) load_rows<T>(Xs, pad(dx), a.x, b, hx, row0, W, Wc, dx);
+            if (kv_new) {
+                load_rows_t<T>(Kt, pad(W), a.k, b, hk, row0, W, Wc, dx);
+                load_rows<T>(Vs, dy, a.v, b, hk, row0, W, Wc, dy);
+            }
+            __syncthreads();
+            if (!SUMMARY) {
+                simt::with_rm(W, W, [&](auto RMc) {
+                    constexpr int RM = decltype(RMc)::value;
+                    simt::for_blocks<RM>(W, W, [&](int m0, int n0) {
+                        simt::Acc<RM> acc;
+                        simt::zero<RM>(acc);
+                        const bool any = rev ? n0 + 3 >= m0 : n0 <= m0 + RM - 1;
+                        if (any) simt::mac_r<RM>(acc, Xs + m0 * pad(dx), pad(dx), Kt + n0, pad(W), dx);
+#pragma unroll
+                        for (int i = 0; i < RM; ++i) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int e = rev ? n0 + j - m0 - i : m0 + i - n0 - j;
+                                acc[i][j] = e >= 0 ? acc[i][j] * gp[e] : 0.f;
+                            }
+                            simt::st4(As + (m0 + i) * pad(W) + n0, acc[i]);
+                        }
+                    });
+                });
+                __syncthreads();
+                simt::with_rm(W, dy, [&](auto RMc) {
+                    constexpr int RM = decltype(RMc)::value;
+                    simt::for_blocks<RM>(W, dy, [&](int m0, int n0) {
+                        simt::Acc<RM> acc;
+                        simt::zero<RM>(acc);
+                        if (x_new) {
+                            simt::mac_r<RM>(acc, Xs + m0 * pad(dx), pad(dx), S + n0, dy, dx);
+#pragma unroll
+                            for (int i = 0; i < RM; ++i) {
+                                const int e = rev ? max(Wc - m0 - i, 0) : m0 + i + 1;
+                                simt::scale_row<RM>(acc, i, a.s_carry * gp[e]);
+                            }
+                        }
+                        simt::Acc<RM> in;
+                        simt::zero<RM>(in);
+                        if (rev) {
+                            const int j0 = m0 & ~3;
+                            simt::mac_r<RM>(in, As + m0 * pad(W) + j0, pad(W), Vs + j0 * dy + n0, dy, W - j0);
+                        } else {
+                            simt::mac_r<RM>(in, As + m0 * pad(W), pad(W), Vs + n0, dy, m0 + RM);
+                        }
+#pragma unroll
+                        for (int i = 0; i < RM; ++i) {
+                            const int row = m0 + i;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[i][j] += a.s_intra * in[i][j];
+                            if (keep_y) {
+                                float* p = Ys + row * dy + n0;
+                                if (r > 0) {
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) acc[i][j] += p[j];
+                                }
+                                simt::st4(p, acc[i]);
+                            }
+                            if (y_last && row < Wn) {
+                                if (row >= Wc) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+                                simt::store4(const_cast<T*>(row_ptr<T>(a.y, b, hx, row0 + row)) + n0, acc[i]);
+                            }
+                        }
+                    });
+                });
+            }
+            if (s_now && Wc > 0) {
+                __syncthreads();  // Sig has been read
+                const float rho = r == 0 || a.rk == 1 ? gp[Wc] : 1.f;
+                simt::with_rm(dx, dy, [&](auto RMc) {
+                    constexpr int RM = decltype(RMc)::value;
+                    simt::for_blocks<RM>(dx, dy, [&](int m0, int n0) {
+                        simt::Acc<RM> acc;
+                        simt::zero<RM>(acc);
+                        simt::mac_r<RM>(acc, Kt + m0 * pad(W), pad(W), Vs + n0, dy, Wc,
+                                        [&](int j) { return a.s_state * gp[rev ? j : Wc - 1 - j]; });
+#pragma unroll
+                        for (int i = 0; i < RM; ++i) simt::decay_add4(S + (m0 + i) * dy + n0, rho, acc[i]);
+                    });
+                });
+            }
+        }
+    }
+    if (SUMMARY) {
+        __syncthreads();
+        float* dst = a.sums + ((size_t)bs * a.nseg + seg) * dx * dy;
+        for (int e = tid; e < dx * dy; e += kThreads) dst[e] = S[e];
+    }
+}
+
+template <typename T>
+int launch_simt_t(const LinPass& a, bool summary, cudaStream_t st) {
+    const size_t smem = lin_smem(a.dx, a.dy, a.W, !summary && a.rk > 1).total * sizeof(float);
+    auto kfn = summary ? lin_simt_kernel<T, true> : lin_simt_kernel<T, false>;
+    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -1;
+    kfn<<<dim3(a.B * a.Hs, a.nseg), kThreads, smem, st>>>(a);
+    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+// ---- scan over the segments -----------------------------------------------------------
+
+__global__ void __launch_bounds__(kThreads)
+    lin_scan_kernel(const float* __restrict__ sums, float* __restrict__ carry, const float* __restrict__ init,
+                    float* __restrict__ fin, const float* __restrict__ gamma, const int* __restrict__ lengths, int Hs,
+                    int n, int seg_rows, int nseg, int elems, int rev) {
+    const int bs = blockIdx.x, b = bs / Hs;
+    const int e = blockIdx.y * kThreads + threadIdx.x;
+    if (e >= elems) return;
+    const float g = gamma ? __ldg(gamma + bs % Hs) : 1.f;
+    const float log2g = log2f(g);
+    const int len = lin_len(lengths, b, n);
+    float cur = init ? init[(size_t)bs * elems + e] : 0.f;
+    if (init && rev) cur /= g;
+    const float* src = sums + (size_t)bs * nseg * elems + e;
+    float* dst = carry ? carry + (size_t)bs * nseg * elems + e : nullptr;
+    const bool need_last = fin != nullptr;
+    for (int i = 0; i < nseg; ++i) {
+        const int s = rev ? nseg - 1 - i : i;
+        if (dst) dst[(size_t)s * elems] = cur;
+        if (i == nseg - 1 && !need_last) break;
+        const int rows = max(0, min(seg_rows, len - s * seg_rows));
+        cur = fmaf(pow_decay(log2g, (float)rows), cur, src[(size_t)s * elems]);
+    }
+    if (fin) fin[(size_t)bs * elems + e] = rev ? g * cur : cur;
+}
+
+// ---- step of single tokens -----------------------------------------------------------------
+//
+// One CTA per state; thread t holds the float4 column t % (dv / 4) of every (threads / (dv / 4))-th
+// row, all RP of its loads in flight at once.  The state is read and written once.
+template <typename T, int RP>
+__global__ void __launch_bounds__(kThreads)
+    lin_step_kernel(float* __restrict__ state, const T* __restrict__ q, const T* __restrict__ k,
+                    const T* __restrict__ v, T* __restrict__ out, int Hk, int group, int d, int dv,
+                    const float* __restrict__ gamma, float scale) {
+    __shared__ __align__(16) float qs[128], ks[128], red[kThreads / 32][128];
+    const int head = blockIdx.x, tid = threadIdx.x, NT = blockDim.x;
+    const int lpr = dv >> 2, col = (tid % lpr) * 4, row = tid / lpr, step = NT / lpr;
+    float* P = state + (size_t)head * d * dv;
+    float4 p[RP];
+#pragma unroll
+    for (int j = 0; j < RP; ++j) p[j] = __ldcs(reinterpret_cast<const float4*>(P + (size_t)(row + j * step) * dv + col));
+    const float g = gamma ? __ldg(gamma + head % Hk) : 1.f;
+    for (int i = tid; i < d; i += NT) ks[i] = to_f32(k[(size_t)head * d + i]);
+    float vv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vv[j] = to_f32(v[(size_t)head * dv + col + j]);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < RP; ++j) {
+        const float kk = ks[row + j * step];
+        p[j].x = fmaf(g, p[j].x, kk * vv[0]);
+        p[j].y = fmaf(g, p[j].y, kk * vv[1]);
+        p[j].z = fmaf(g, p[j].z, kk * vv[2]);
+        p[j].w = fmaf(g, p[j].w, kk * vv[3]);
+        __stcs(reinterpret_cast<float4*>(P + (size_t)(row + j * step) * dv + col), p[j]);
+    }
+    for (int r = 0; r < group; ++r) {
+        const size_t hq = (size_t)head * group + r;
+        for (int i = tid; i < d; i += NT) qs[i] = to_f32(q[hq * d + i]);
+        __syncthreads();
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < RP; ++j) {
+            const float qq = qs[row + j * step];
+            s.x = fmaf(qq, p[j].x, s.x);
+            s.y = fmaf(qq, p[j].y, s.y);
+            s.z = fmaf(qq, p[j].z, s.z);
+            s.w = fmaf(qq, p[j].w, s.w);
+        }
+        for (int o = lpr; o < 32; o <<= 1) {
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+            s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+            s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+        }
+        const int warp = tid >> 5, lane = tid & 31;
+        if (lane < lpr) *reinterpret_cast<float4*>(&red[warp][col]) = s;
+        __syncthreads();
+        for (int c = tid; c < dv; c += NT) {
+            float t = 0.f;
+            for (int w = 0; w < NT / 32; ++w) t += red[w][c];
+            out[hq * dv + c] = from_f32<T>(scale * t);
+        }
+    }
+}
+
+template <typename T>
+int launch_step_t(float* state, const void* q, const void* k, const void* v, void* out, int N, int Hk, int group, int d,
+                  int dv, const float* gamma, float scale, cudaStream_t st) {
+    const int vecs = d * dv / 4, threads = vecs < kThreads ? vecs : kThreads, rp = vecs / threads;
+    const unsigned grid = (unsigned)N * (unsigned)Hk;
+    auto go = [&](auto kfn) {
+        kfn<<<grid, threads, 0, st>>>(state, static_cast<const T*>(q), static_cast<const T*>(k),
+                                      static_cast<const T*>(v), static_cast<T*>(out), Hk, group, d, dv, gamma, scale);
+    };
+    switch (rp) {
+        case 1: go(lin_step_kernel<T, 1>); break;
+        case 2: go(lin_step_kernel<T, 2>); break;
+        case 4: go(lin_step_kernel<T, 4>); break;
+        case 8: go(lin_step_kernel<T, 8>); break;
+        case 16: go(lin_step_kernel<T, 16>); break;
+        default: return -1;
+    }
+    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+int lin_simt_width(int dx, int dy) { return dx > 64 || dy > 64 ? 32 : 64; }
+int lin_simt_ctas(int dx, int dy, int rk) {
+    return simt::min_ctas(2, simt::ctas_per_sm(lin_smem(dx, dy, lin_simt_width(dx, dy), rk > 1).total * sizeof(float)));
+}
+
+int launch_lin_simt(const LinPass& a, bool summary, bool is_bf16, cudaStream_t st) {
+    if (a.B * a.Hs == 0 || a.nseg == 0) return 0;
+    return is_bf16 ? launch_simt_t<bf16>(a, summary, st) : launch_simt_t<float>(a, summary, st);
+}
+
+int launch_lin_scan(const float* sums, float* carry, const float* init, float* final_state, const float* gamma,
+                    const int* lengths, int B, int Hs, int n, int seg_rows, int nseg, int elems, int rev,
+                    cudaStream_t st) {
+    if (B * Hs == 0) return 0;
+    lin_scan_kernel<<<dim3(B * Hs, (elems + kThreads - 1) / kThreads), kThreads, 0, st>>>(
+        sums, carry, init, final_state, gamma, lengths, Hs, n, seg_rows, nseg, elems, rev);
+    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_lin_step(float* state, const void* q, const void* k, const void* v, void* out, int N, int H, int Hk, int d,
+                    int dv, const float* gamma, float scale, bool is_bf16, cudaStream_t st) {
+    if (N * Hk == 0) return 0;
+    return is_bf16 ? launch_step_t<bf16>(state, q, k, v, out, N, Hk, H / Hk, d, dv, gamma, scale, st)
+                   : launch_step_t<float>(state, q, k, v, out, N, Hk, H / Hk, d, dv, gamma, scale, st);
+}
+
+}  // namespace hla2

@@ -417,6 +417,121 @@ int hla2_noalloc_status(hla2_stream_t stream);
  */
 int hla2_noalloc_selftest_wait_timeout(hla2_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------------------
+ * Around a mixer layer: first-order linear attention, block norms, 4-bit projections.
+ * ---------------------------------------------------------------------------------------
+ *
+ * First-order linear attention with a decay for each key head.  Per key head, with the
+ * state P (d x dv, float32) and decay g = gamma[head] in (0, 1]:
+ *
+ *   P_t = g P_{t-1} + k_t v_t^T          o_t = scale * P_t^T q_t
+ *
+ * H query heads read Hk key heads, H a multiple of Hk: query head h reads key head
+ * h / (H / Hk), and the heads of such a group share the key head's state.  Sequence b holds
+ * lengths[b] tokens (clamped to [0, n]; NULL: n each).  The rows past its length are padding:
+ * never used, whatever they hold; their outputs and gradients are 0 and they leave the state
+ * alone.  Sums, states and decays are float32.  bf16 calls round, in the products of one chunk
+ * of 128 tokens, the decayed score matrix and the carried state to bf16 as operands (each
+ * about the size of the output's own rounding); the states returned are float32 sums
+ * throughout.  A non-finite value in a valid row may reach every output of its chunk.
+ *
+ * A tensor argument is a base address and the element strides of batch, head and token; the
+ * last dimension is contiguous.  Base and strides are multiples of 16 bytes.
+ */
+typedef struct {
+    const void* p;
+    long long sb, sh, sn; /* element strides of batch, head, token */
+} hla2_view;
+
+typedef struct {
+    int dtype;                       /* HLA2_F32 | HLA2_BF16: q, k, v, out, dout and gradients      */
+    int B, H, Hk, n, d, dv;          /* d, dv in {16, 32, 64, 128}; n >= 0; H a multiple of Hk        */
+    float scale;                     /* factor of the outputs                                         */
+    const float* gamma;              /* device float [Hk], or NULL for no decay                       */
+    const int* lengths;              /* device int [B], or NULL                                       */
+    hla2_view q, k, v;               /* [B, H, n, d], [B, Hk, n, d], [B, Hk, n, dv]                   */
+    const float* init_state;         /* nullable: contiguous [B, Hk, d, dv], the state before token 0 */
+    void* workspace;                 /* device scratch of the size the query gives                    */
+    size_t workspace_bytes;
+} hla2_linattn_args;
+
+/* Scratch bytes of a forward (backward = 0) or a backward (1) with these arguments; the
+ * addresses in *a are not looked at, but for init_state being NULL or not.  want_final: a
+ * final_state (forward) or dinit_state (backward) is asked for, or a dfinal_state is given.
+ * (size_t)-1 for arguments that the call would reject. */
+size_t hla2_linattn_workspace_bytes(const hla2_linattn_args* a, int backward, int want_final);
+
+/* out [B, H, n, dv]; final_state (nullable) receives the contiguous [B, Hk, d, dv] state after
+ * each sequence's last token.  out may not overlap an input. */
+int hla2_linattn_forward(const hla2_linattn_args* a, hla2_view out, float* final_state, hla2_stream_t stream);
+
+/* Gradients of sum(out * dout) + sum(final_state * dfinal_state): dq [B, H, n, d], dk [B, Hk,
+ * n, d], dv [B, Hk, n, dv] (summed over the query heads that share a key head) and, where not
+ * NULL, dinit_state [B, Hk, d, dv].  dfinal_state: nullable.  gamma has no gradient. */
+int hla2_linattn_backward(const hla2_linattn_args* a, hla2_view dout, hla2_view dq, hla2_view dk, hla2_view dv,
+                          const float* dfinal_state, float* dinit_state, hla2_stream_t stream);
+
+/* One token for each of N sequences: state [N, Hk, d, dv] float32 is updated in place, then out
+ * [N, H, dv] = scale * P^T q.  q [N, H, d], k [N, Hk, d], v [N, Hk, dv], all contiguous. */
+int hla2_linattn_decode_step(float* state, const void* q, const void* k, const void* v, void* out, int N, int H,
+                             int Hk, int d, int dv, const float* gamma, float scale, int dtype,
+                             hla2_stream_t stream);
+
+/*
+ * The norms before and after a block, with the block's gate and residual scale, on rows of D
+ * values (1 <= D <= 8192).  norm(t) = t / sqrt(mean(t^2) + eps):
+ *
+ *   r = x + scale * act(gate) * norm(y) * post_weight          (the block's end)
+ *   h = norm(r) * next_weight                                  (the next block's start)
+ *
+ * y NULL: r = x, and only h is formed (the norm before a first block).  next_weight NULL: only
+ * r is formed (after a last block).  gate NULL: act = 1; gate_cols D: a gate for each value; 1:
+ * one for each row.  scale [D] NULL: 1.  Statistics are float32; h is formed from the unrounded
+ * r.  Rows are contiguous and start every *_stride elements; vectors are contiguous.  Every
+ * tensor has the type dtype; any alignment of an element.
+ */
+enum { HLA2_GATE_SIGMOID = 0, HLA2_GATE_SILU = 1 };
+
+typedef struct {
+    int dtype, gate_act, gate_cols;
+    long long rows;
+    int D;
+    float eps;
+    const void* x;            long long x_stride;
+    const void* y;            long long y_stride;
+    const void* gate;         long long gate_stride;
+    const void* post_weight;  /* [D]; needed with y */
+    const void* scale;        /* [D], nullable      */
+    const void* next_weight;  /* [D], nullable      */
+} hla2_block_args;
+
+/* r [rows, D] (NULL with y NULL), h [rows, D] (NULL without next_weight), contiguous. */
+int hla2_block_join(const hla2_block_args* a, void* r, void* h, hla2_stream_t stream);
+
+/* Scratch bytes of hla2_block_join_backward; (size_t)-1 for arguments it would reject. */
+size_t hla2_block_join_backward_workspace_bytes(const hla2_block_args* a);
+
+/* Gradients of sum(r * dr) + sum(h * dh); dr (nullable) and dh (needed with next_weight, else
+ * NULL) are contiguous [rows, D].  dx, dy [rows, D], dgate [rows, gate_cols] have the type dtype;
+ * dpost_weight, dscale, dnext_weight are float32 [D] sums over the rows in a fixed order.  Each
+ * output is needed where its input is there, and NULL elsewhere. */
+int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const void* dh, void* dx, void* dy,
+                             void* dgate, float* dpost_weight, float* dscale, float* dnext_weight, void* workspace,
+                             size_t workspace_bytes, hla2_stream_t stream);
+
+/*
+ * Matrix-vector products with 4-bit weights and group scales, for the projections of a few
+ * tokens: y[m, n] = sum_k x[m, k] (q[n, k] - z[n, k / group]) scales[n, k / group] + bias[n].
+ * qweight [N, K / 2] bytes: value 2 j of a row in the low half of byte j, 2 j + 1 in the high half.
+ * zeros [N, K / group] bytes in 0..15, or NULL for 8.  x [M, K] (rows every x_stride elements),
+ * scales [N, K / group], bias [N] (nullable) and y [M, N] have the type dtype.  1 <= M <= 16;
+ * group 32, 64 or 128, K a multiple of it; N >= 0.  x, its rows and qweight are 16-byte aligned.
+ * The products are exact and the sums float32.
+ */
+int hla2_w4_matvec(const void* x, long long x_stride, const void* qweight, const void* scales, const void* zeros,
+                   const void* bias, void* y, int M, int N, int K, int group, int dtype, hla2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
