@@ -497,6 +497,9 @@ int with_vec(int D, int vec, const Shape& s, F&& f) {
 
 int join_ok() { return set_last_error(HLA2_OK, "%s", ""); }
 
+// Whether the call has a block output; without rows there is no address to go by.
+bool has_y(const hla2_block_args* a) { return a->rows > 0 ? a->y != nullptr : a->post_weight != nullptr; }
+
 int check_join(const char* fn, const hla2_block_args* a) {
     if (!a) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: args must not be NULL", fn);
     if (a->dtype != HLA2_F32 && a->dtype != HLA2_BF16)
@@ -506,10 +509,10 @@ int check_join(const char* fn, const hla2_block_args* a) {
                               fn, kMaxD, a->D);
     if (a->rows < 0 || a->rows > 0x7fffffffLL)
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: rows must be 0 .. 2^31 - 1", fn);
-    if (!a->y && !a->next_weight)
+    if (!has_y(a) && !a->next_weight)
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: nothing to form without y and next_weight", fn);
     if (a->y && !a->post_weight) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: y needs post_weight", fn);
-    if (!a->y && (a->gate || a->scale || a->post_weight))
+    if (!has_y(a) && (a->gate || a->scale || a->post_weight))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: gate, scale and post_weight need y", fn);
     if (a->gate && (a->gate_act != HLA2_GATE_SIGMOID && a->gate_act != HLA2_GATE_SILU))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: unknown gate_act %d", fn, a->gate_act);
@@ -606,9 +609,9 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
     if (int rc = check_join(fn, a)) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const size_t es = a->dtype == HLA2_BF16 ? 2 : 4;
-    if ((a->y && !dpost_weight) || (a->scale && !dscale) || (a->next_weight && !dnext_weight))
+    if ((has_y(a) && !dpost_weight) || (a->scale && !dscale) || (a->next_weight && !dnext_weight))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a weight's gradient is missing", fn);
-    if ((!a->y && (dpost_weight || dy)) || (!a->scale && dscale) || (!a->next_weight && (dnext_weight || dh)) ||
+    if ((!has_y(a) && (dpost_weight || dy)) || (!a->scale && dscale) || (!a->next_weight && (dnext_weight || dh)) ||
         (!a->gate && dgate))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient is asked for without its input", fn);
     if (a->rows > 0) {
