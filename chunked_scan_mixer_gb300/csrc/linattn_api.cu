@@ -54,8 +54,8 @@ int check_sizes(const char* fn, const hla2_linattn_args* a) {
     if ((a->Hk == 0) != (a->H == 0) || (a->Hk > 0 && a->H % a->Hk != 0))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: H (%d) must be a multiple of Hk (%d)", fn, a->H, a->Hk);
     // grid limits and 32-bit head counts
-    if ((long long)a->B * a->H > 0x7fffffff || a->n > 0x7fffff00)
-        return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: B * H and n must fit in 31 bits", fn);
+    if ((long long)a->B * a->H > 0x7fffffff || a->n > 1 << 30)
+        return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: B * H must fit in 31 bits, and n be at most 2^30", fn);
     return HLA2_OK;
 }
 
@@ -111,6 +111,7 @@ LinPlan lin_plan(const hla2_linattn_args* a, int W, int slots) {
 }
 
 LinPlan plan_of(const hla2_linattn_args* a) {
+    if (a->dtype == HLA2_BF16) return lin_plan(a, 128, sm_count());
     return lin_plan(a, lin_simt_width(a->d, a->dv), sm_count() * lin_simt_ctas(a->d, a->dv, 1));
 }
 
@@ -119,7 +120,7 @@ size_t state_array_bytes(const hla2_linattn_args* a, const LinPlan& p) {
 }
 
 int run_pass(const LinPass& a, bool summary, int dtype, cudaStream_t st) {
-    return launch_lin_simt(a, summary, dtype == HLA2_BF16, st);
+    return dtype == HLA2_BF16 ? launch_lin_tc(a, summary, st) : launch_lin_simt(a, summary, false, st);
 }
 
 // Common fields of every pass of one call.

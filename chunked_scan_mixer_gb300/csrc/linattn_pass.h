@@ -47,6 +47,9 @@ int lin_simt_width(int dx, int dy);
 int lin_simt_ctas(int dx, int dy, int rk);  // resident CTAs per SM
 int launch_lin_simt(const LinPass& a, bool summary, bool is_bf16, cudaStream_t st);
 
+// Tensor-core passes (bf16, any size; linattn_tc.cu): W = 128, one CTA per SM.
+int launch_lin_tc(const LinPass& a, bool summary, cudaStream_t st);
+
 // States entering the segments from the segment summaries, in one serial pass over the segments
 // per state element:  carry[s] = cur;  cur = g^(valid rows of s) cur + sums[s]  in the
 // scan's direction.  init (nullable) is the state before the scan; reverse: the gradient of the
