@@ -9,11 +9,13 @@
 // The backward forms the statistics again from x, y and the gate: nothing is kept from the
 // forward, and r enters unrounded.
 //
-// Bound by memory: 5 tensors forward, 8 backward.  A row stays in the registers of its threads
-// (NV vectors of VEC values each) from the one read to the one write.  Rows of at most 32 vectors
-// take a part of a warp (TPR threads), longer ones a whole CTA.  Backward CTAs take rows in a fixed
-// stride and keep their three weight gradients in registers; each writes one partial row, which a
-// second kernel sums in a fixed order.
+// Bound by memory: 5 tensors forward, 8 backward.  Persistent CTAs take rows in a fixed stride.  A thread
+// owns NV vectors of VEC values of every row; it copies them ahead with cp.async into a ring of kStages
+// rows in shared memory that nobody else reads, so the ring needs no barrier, and the bytes in flight do
+// not cost registers (plain loads into registers held 152 of them, one CTA per SM, 1.2 TB/s).
+// Rows of at most 32 vectors take a part of a warp (TPR threads), longer ones a whole CTA.  The backward
+// keeps its three weight gradients in registers; each CTA writes one partial row, which a second
+// kernel sums in a fixed order.
 #include <type_traits>
 
 #include "common.cuh"
@@ -103,7 +105,8 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[32][N], int&
 }
 
 // act(z) and act'(z)
-__device__ __forceinline__ float sigmoidf(float z) { return 1.f / (1.f + __expf(-z)); }
+// (the approximate reciprocal is good to an ulp, and 0 at infinity)
+__device__ __forceinline__ float sigmoidf(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 __device__ __forceinline__ float act_of(float z, int act) {
     const float s = sigmoidf(z);
     return act == HLA2_GATE_SILU ? z * s : s;
@@ -113,86 +116,140 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     return act == HLA2_GATE_SILU ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
 }
 
+// One thread's ring: slot (stage, tensor, j) holds its j-th vector of that tensor's row.
+template <typename T, int VEC, int NV>
+struct Ring {
+    static constexpr int kBytes = VEC * (int)sizeof(T);
+    char* base;       // this thread's first slot
+    uint32_t step;    // bytes between slots: the CTA's threads side by side
+    int tensors;
+    __device__ __forceinline__ Ring(char* sm, int n) : base(sm + threadIdx.x * kBytes), step(blockDim.x * kBytes), tensors(n) {}
+    __device__ __forceinline__ char* at(int stage, int tensor, int j) const {
+        return base + (uint32_t)((stage * tensors + tensor) * NV + j) * step;
+    }
+    __device__ __forceinline__ void copy(int stage, int tensor, int j, const T* p) const {
+        char* d = at(stage, tensor, j);
+        if constexpr (kBytes == 16) {
+            cp_async16(d, p);
+        } else if constexpr (kBytes == 4) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(smem_u32(d)), "l"(p));
+        } else {
+            *reinterpret_cast<T*>(d) = *p;
+        }
+    }
+    __device__ __forceinline__ void get(int stage, int tensor, int j, float (&f)[VEC]) const {
+        unpack(*reinterpret_cast<const Vec<T, VEC>*>(at(stage, tensor, j)), f);
+    }
+};
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N)); }
+
+// The newest `ahead` (0 .. 3) groups may still be in flight.
+__device__ __forceinline__ void cp_async_wait_but(int ahead) {
+    switch (ahead) {
+        case 0: cp_async_wait<0>(); break;
+        case 1: cp_async_wait<1>(); break;
+        case 2: cp_async_wait<2>(); break;
+        default: cp_async_wait<3>(); break;
+    }
+}
+
 template <typename T, int VEC, int NV, int TPR, int MAXT>
-__global__ void __launch_bounds__(MAXT) join_kernel(const hla2_block_args a, T* __restrict__ r_out, T* __restrict__ h_out) {
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 2)
+    join_kernel(const hla2_block_args a, T* __restrict__ r_out, T* __restrict__ h_out, int stages) {
+    extern __shared__ __align__(16) char ring_sm[];
     __shared__ float red[2][32][1];
     int turn = 0;
-    const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr;
-    const long long row = TPR ? (long long)blockIdx.x * (kSmallThreads / (TPR ? TPR : 1)) + threadIdx.x / tpr : blockIdx.x;
-    const bool live = row < a.rows;  // whole sub-warps: lanes of a dead row take part in the shuffles
+    const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr, mine = threadIdx.x / tpr;
+    const int per = TPR ? kSmallThreads / (TPR ? TPR : 1) : 1;
     const int D = a.D;
     const float inv_d = 1.f / (float)D;
-    const T *x = static_cast<const T*>(a.x) + (live ? row * a.x_stride : 0),
-            *y = static_cast<const T*>(a.y) + (live ? row * a.y_stride : 0),
-            *z = static_cast<const T*>(a.gate) + (live ? row * a.gate_stride : 0);
+    const bool full = a.gate && a.gate_cols != 1;
     const T *pw = static_cast<const T*>(a.post_weight), *sc = static_cast<const T*>(a.scale),
             *nw = static_cast<const T*>(a.next_weight);
-    Vec<T, VEC> xv[NV], yv[NV], zv[NV];
-    const bool full = a.gate && a.gate_cols != 1;
+    const Ring<T, VEC, NV> ring(ring_sm, 1 + (a.y ? 1 : 0) + (full ? 1 : 0));
+    const long long stride = (long long)gridDim.x * per;
+    auto fetch = [&](long long row, int stage) {
+        if (row < a.rows) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * tpr + t) * VEC;
-        if (live && c < D) {
-            xv[j] = ldvec<T, VEC>(x + c);
-            if (a.y) yv[j] = ldvec<T, VEC>(y + c);
-            if (full) zv[j] = ldvec<T, VEC>(z + c);
-        }
-    }
-    float r[NV][VEC], sum[1] = {0.f};
-    if (a.y) {
-        const float a_row = a.gate && !full && live ? act_of(to_f32(z[0]), a.gate_act) : 1.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (live && (j * tpr + t) * VEC < D) {
-                float f[VEC];
-                unpack(yv[j], f);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) sum[0] += f[i] * f[i];
-            }
-        row_sum<TPR, 1>(sum, red, turn);
-        const float inv = rsqrtf(sum[0] * inv_d + a.eps);
-        sum[0] = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * tpr + t) * VEC;
-            if (live && c < D) {
-                float fx[VEC], fy[VEC], fz[VEC], fw[VEC], fs[VEC];
-                unpack(xv[j], fx);
-                unpack(yv[j], fy);
-                unpack(ldvec<T, VEC>(pw + c), fw);
-                if (full) unpack(zv[j], fz);
-                if (sc) unpack(ldvec<T, VEC>(sc + c), fs);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float u = fy[i] * inv * fw[i], g = full ? act_of(fz[i], a.gate_act) : a_row;
-                    r[j][i] = fx[i] + (sc ? fs[i] * g * u : g * u);
-                    sum[0] += r[j][i] * r[j][i];
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * tpr + t) * VEC;
+                if (c < D) {
+                    ring.copy(stage, 0, j, static_cast<const T*>(a.x) + row * a.x_stride + c);
+                    if (a.y) ring.copy(stage, 1, j, static_cast<const T*>(a.y) + row * a.y_stride + c);
+                    if (full) ring.copy(stage, 2, j, static_cast<const T*>(a.gate) + row * a.gate_stride + c);
                 }
-                stvec<T, VEC>(r_out + row * D + c, r[j]);
             }
         }
-    } else {
+        cp_async_commit();
+    };
+    const long long row_first = (long long)blockIdx.x * per + mine;
+    for (int i = 0; i + 1 < stages; ++i) fetch(row_first + i * stride, i);
+    int stage = 0;
+    // whole sub-warps: lanes of a row past the last take part in the shuffles
+    for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows; row0 += stride) {
+        const long long row = row0 + mine;
+        const bool live = row < a.rows;
+        const int next = stage == 0 ? stages - 1 : stage - 1;  // the slot of the row before
+        fetch(row + (stages - 1) * stride, next);
+        const float a_row = a.y && a.gate && !full && live
+                                ? act_of(to_f32(static_cast<const T*>(a.gate)[row * a.gate_stride]), a.gate_act) : 1.f;
+        cp_async_wait_but(stages - 1);
+        float r[NV][VEC], sum[1] = {0.f};
+        if (a.y) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (live && (j * tpr + t) * VEC < D) {
-                unpack(xv[j], r[j]);
+            for (int j = 0; j < NV; ++j)
+                if (live && (j * tpr + t) * VEC < D) {
+                    ring.get(stage, 1, j, r[j]);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) sum[0] += r[j][i] * r[j][i];
+                    for (int i = 0; i < VEC; ++i) sum[0] += r[j][i] * r[j][i];
+                }
+            row_sum<TPR, 1>(sum, red, turn);
+            const float inv = rsqrtf(sum[0] * inv_d + a.eps);
+            sum[0] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * tpr + t) * VEC;
+                if (live && c < D) {
+                    float fx[VEC], fz[VEC], fw[VEC], fs[VEC];
+                    ring.get(stage, 0, j, fx);
+                    unpack(ldvec<T, VEC>(pw + c), fw);
+                    if (full) ring.get(stage, 2, j, fz);
+                    if (sc) unpack(ldvec<T, VEC>(sc + c), fs);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const float u = r[j][i] * inv * fw[i], g = full ? act_of(fz[i], a.gate_act) : a_row;
+                        r[j][i] = fx[i] + (sc ? fs[i] * g * u : g * u);
+                        sum[0] += r[j][i] * r[j][i];
+                    }
+                    stvec<T, VEC>(r_out + row * D + c, r[j]);
+                }
             }
-    }
-    if (!h_out) return;
-    row_sum<TPR, 1>(sum, red, turn);
-    const float inv = rsqrtf(sum[0] * inv_d + a.eps);
+        } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * tpr + t) * VEC;
-        if (live && c < D) {
-            float fw[VEC], o[VEC];
-            unpack(ldvec<T, VEC>(nw + c), fw);
+            for (int j = 0; j < NV; ++j)
+                if (live && (j * tpr + t) * VEC < D) {
+                    ring.get(stage, 0, j, r[j]);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = r[j][i] * inv * fw[i];
-            stvec<T, VEC>(h_out + row * D + c, o);
+                    for (int i = 0; i < VEC; ++i) sum[0] += r[j][i] * r[j][i];
+                }
         }
+        if (h_out) {
+            row_sum<TPR, 1>(sum, red, turn);
+            const float inv = rsqrtf(sum[0] * inv_d + a.eps);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * tpr + t) * VEC;
+                if (live && c < D) {
+                    float fw[VEC], o[VEC];
+                    unpack(ldvec<T, VEC>(nw + c), fw);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) o[i] = r[j][i] * inv * fw[i];
+                    stvec<T, VEC>(h_out + row * D + c, o);
+                }
+            }
+        }
+        stage = stage + 1 == stages ? 0 : stage + 1;
     }
 }
 
@@ -204,44 +261,55 @@ struct JoinGrads {
 };
 
 template <typename T, int VEC, int NV, int TPR, int MAXT>
-__global__ void __launch_bounds__(MAXT) join_backward_kernel(const hla2_block_args a, const JoinGrads g) {
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1)
+    join_backward_kernel(const hla2_block_args a, const JoinGrads g, int stages) {
+    extern __shared__ __align__(16) char ring_sm[];  // the ring; at the end, in a sub-warp mapping, [3][D] sums
     __shared__ float red1[2][32][1], red2[2][32][2];
-    extern __shared__ float acc_sm[];  // sub-warp mapping: [3][D]
     int turn1 = 0, turn2 = 0;
-    const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr;
-    const int per = TPR ? kSmallThreads / (TPR ? TPR : 1) : 1, mine = threadIdx.x / tpr;
+    const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr, mine = threadIdx.x / tpr;
+    const int per = TPR ? kSmallThreads / (TPR ? TPR : 1) : 1;
     const int D = a.D;
     const float inv_d = 1.f / (float)D;
     const T *pw = static_cast<const T*>(a.post_weight), *sc = static_cast<const T*>(a.scale),
             *nw = static_cast<const T*>(a.next_weight);
     const bool full = a.gate && a.gate_cols != 1;
+    // ring slots of the tensors that are there
+    int slots = 1;
+    const int ky = a.y ? slots++ : 0, kz = full ? slots++ : 0, kr = g.dr ? slots++ : 0, kh = g.dh ? slots++ : 0;
+    const Ring<T, VEC, NV> ring(ring_sm, slots);
     float gp[NV][VEC], gs[NV][VEC], gn[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) gp[j][i] = gs[j][i] = gn[j][i] = 0.f;
 
-    for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows; row0 += (long long)gridDim.x * per) {
-        const long long row = row0 + mine;
-        const bool live = row < a.rows;
-        const long long at = live ? row : 0;
-        const T *x = static_cast<const T*>(a.x) + at * a.x_stride, *y = static_cast<const T*>(a.y) + at * a.y_stride,
-                *z = static_cast<const T*>(a.gate) + at * a.gate_stride;
-        const T *dr = static_cast<const T*>(g.dr) + at * D, *dh = static_cast<const T*>(g.dh) + at * D;
-        Vec<T, VEC> xv[NV], yv[NV], zv[NV], rv[NV], hv[NV];
+    const long long stride = (long long)gridDim.x * per;
+    auto fetch = [&](long long row, int stage) {
+        if (row < a.rows) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * tpr + t) * VEC;
-            if (live && c < D) {
-                xv[j] = ldvec<T, VEC>(x + c);
-                if (a.y) yv[j] = ldvec<T, VEC>(y + c);
-                if (full) zv[j] = ldvec<T, VEC>(z + c);
-                if (g.dr) rv[j] = ldvec<T, VEC>(dr + c);
-                if (g.dh) hv[j] = ldvec<T, VEC>(dh + c);
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * tpr + t) * VEC;
+                if (c < D) {
+                    ring.copy(stage, 0, j, static_cast<const T*>(a.x) + row * a.x_stride + c);
+                    if (a.y) ring.copy(stage, ky, j, static_cast<const T*>(a.y) + row * a.y_stride + c);
+                    if (full) ring.copy(stage, kz, j, static_cast<const T*>(a.gate) + row * a.gate_stride + c);
+                    if (g.dr) ring.copy(stage, kr, j, static_cast<const T*>(g.dr) + row * D + c);
+                    if (g.dh) ring.copy(stage, kh, j, static_cast<const T*>(g.dh) + row * D + c);
+                }
             }
         }
-        const float z_row = a.gate && !full && live ? to_f32(z[0]) : 0.f;
+        cp_async_commit();
+    };
+    const long long row_first = (long long)blockIdx.x * per + mine;
+    for (int i = 0; i + 1 < stages; ++i) fetch(row_first + i * stride, i);
+    int stage = 0;
+    for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows; row0 += stride) {
+        const long long row = row0 + mine;
+        const bool live = row < a.rows;
+        fetch(row + (stages - 1) * stride, stage == 0 ? stages - 1 : stage - 1);
+        const float z_row = a.gate && !full && live ? to_f32(static_cast<const T*>(a.gate)[row * a.gate_stride]) : 0.f;
         const float a_row = a.gate && !full ? act_of(z_row, a.gate_act) : 1.f;
+        cp_async_wait_but(stages - 1);
         float inv_y = 0.f;
         if (a.y) {
             float s1[1] = {0.f};
@@ -249,7 +317,7 @@ __global__ void __launch_bounds__(MAXT) join_backward_kernel(const hla2_block_ar
             for (int j = 0; j < NV; ++j)
                 if (live && (j * tpr + t) * VEC < D) {
                     float f[VEC];
-                    unpack(yv[j], f);
+                    ring.get(stage, ky, j, f);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) s1[0] += f[i] * f[i];
                 }
@@ -264,27 +332,26 @@ __global__ void __launch_bounds__(MAXT) join_backward_kernel(const hla2_block_ar
             for (int j = 0; j < NV; ++j) {
                 const int c = (j * tpr + t) * VEC;
                 if (live && c < D) {
-                    float fx[VEC], fh[VEC], fn[VEC];
-                    unpack(xv[j], fx);
-                    unpack(hv[j], fh);
-                    unpack(ldvec<T, VEC>(nw + c), fn);
+                    ring.get(stage, 0, j, R[j]);
                     if (a.y) {
                         float fy[VEC], fz[VEC], fw[VEC], fs[VEC];
-                        unpack(yv[j], fy);
+                        ring.get(stage, ky, j, fy);
                         unpack(ldvec<T, VEC>(pw + c), fw);
-                        if (full) unpack(zv[j], fz);
+                        if (full) ring.get(stage, kz, j, fz);
                         if (sc) unpack(ldvec<T, VEC>(sc + c), fs);
 #pragma unroll
                         for (int i = 0; i < VEC; ++i) {
                             const float u = fy[i] * inv_y * fw[i], ga = full ? act_of(fz[i], a.gate_act) : a_row;
-                            fx[i] += sc ? fs[i] * ga * u : ga * u;
+                            R[j][i] += sc ? fs[i] * ga * u : ga * u;
                         }
                     }
+                    float fh[VEC], fn[VEC];
+                    ring.get(stage, kh, j, fh);
+                    unpack(ldvec<T, VEC>(nw + c), fn);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
-                        R[j][i] = fx[i];
-                        s2[0] += fx[i] * fx[i];
-                        s2[1] += fh[i] * fn[i] * fx[i];
+                        s2[0] += R[j][i] * R[j][i];
+                        s2[1] += fh[i] * fn[i] * R[j][i];
                     }
                 }
             }
@@ -298,13 +365,13 @@ __global__ void __launch_bounds__(MAXT) join_backward_kernel(const hla2_block_ar
         for (int j = 0; j < NV; ++j) {
             const int c = (j * tpr + t) * VEC;
             if (live && c < D) {
-                float f[VEC], fr[VEC];
+                float fr[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) fr[i] = 0.f;
-                if (g.dr) unpack(rv[j], fr);
+                if (g.dr) ring.get(stage, kr, j, fr);
                 if (g.dh) {
-                    float fn[VEC];
-                    unpack(hv[j], f);
+                    float f[VEC], fn[VEC];
+                    ring.get(stage, kh, j, f);
                     unpack(ldvec<T, VEC>(nw + c), fn);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
@@ -316,18 +383,24 @@ __global__ void __launch_bounds__(MAXT) join_backward_kernel(const hla2_block_ar
                 stvec<T, VEC>(static_cast<T*>(g.dx) + row * D + c, fr);
                 if (a.y) {
                     float fy[VEC], fz[VEC], fw[VEC], fs[VEC], dz[VEC];
-                    unpack(yv[j], fy);
+                    ring.get(stage, ky, j, fy);
                     unpack(ldvec<T, VEC>(pw + c), fw);
-                    if (full) unpack(zv[j], fz);
+                    if (full) ring.get(stage, kz, j, fz);
                     if (sc) unpack(ldvec<T, VEC>(sc + c), fs);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
-                        const float ny = fy[i] * inv_y, u = ny * fw[i], ga = full ? act_of(fz[i], a.gate_act) : a_row;
+                        const float ny = fy[i] * inv_y, u = ny * fw[i];
+                        float ga = a_row, slope = 0.f;
+                        if (full) {
+                            const float sg = sigmoidf(fz[i]);
+                            ga = a.gate_act == HLA2_GATE_SILU ? fz[i] * sg : sg;
+                            slope = a.gate_act == HLA2_GATE_SILU ? sg * (1.f + fz[i] * (1.f - sg)) : sg * (1.f - sg);
+                        }
                         const float Rs = sc ? fr[i] * fs[i] : fr[i];
                         gs[j][i] += fr[i] * ga * u;
                         const float du = Rs * ga;
                         gp[j][i] += du * ny;
-                        if (full) dz[i] = Rs * u * act_slope(fz[i], a.gate_act);
+                        if (full) dz[i] = Rs * u * slope;
                         else s3[1] += Rs * u;
                         R[j][i] = du * fw[i];  // gradient of ny
                         s3[0] += R[j][i] * ny;
@@ -344,7 +417,7 @@ __global__ void __launch_bounds__(MAXT) join_backward_kernel(const hla2_block_ar
                 const int c = (j * tpr + t) * VEC;
                 if (live && c < D) {
                     float fy[VEC], o[VEC];
-                    unpack(yv[j], fy);
+                    ring.get(stage, ky, j, fy);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) o[i] = inv_y * (R[j][i] - fy[i] * inv_y * m);
                     stvec<T, VEC>(static_cast<T*>(g.dy) + row * D + c, o);
@@ -353,10 +426,15 @@ __global__ void __launch_bounds__(MAXT) join_backward_kernel(const hla2_block_ar
             if (a.gate && !full && live && t == 0)
                 static_cast<T*>(g.dgate)[row] = from_f32<T>(s3[1] * act_slope(z_row, a.gate_act));
         }
+        stage = stage + 1 == stages ? 0 : stage + 1;
     }
+    cp_async_wait_all();
+    // this CTA's partial sums: post_weight and scale with y, next_weight with dh
     float* dst = g.partial + (size_t)blockIdx.x * 3 * D;
     if (TPR) {  // the CTA's row groups one after another, so that the order is fixed
+        float* acc = reinterpret_cast<float*>(ring_sm);
         for (int who = 0; who < per; ++who) {
+            __syncthreads();
             if (mine == who) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
@@ -364,15 +442,15 @@ __global__ void __launch_bounds__(MAXT) join_backward_kernel(const hla2_block_ar
                     for (int i = 0; i < VEC; ++i) {
                         const int c = (j * tpr + t) * VEC + i;
                         if (c < D) {
-                            acc_sm[c] = (who ? acc_sm[c] : 0.f) + gp[j][i];
-                            acc_sm[D + c] = (who ? acc_sm[D + c] : 0.f) + gs[j][i];
-                            acc_sm[2 * D + c] = (who ? acc_sm[2 * D + c] : 0.f) + gn[j][i];
+                            acc[c] = (who ? acc[c] : 0.f) + gp[j][i];
+                            acc[D + c] = (who ? acc[D + c] : 0.f) + gs[j][i];
+                            acc[2 * D + c] = (who ? acc[2 * D + c] : 0.f) + gn[j][i];
                         }
                     }
             }
-            __syncthreads();
         }
-        for (int c = threadIdx.x; c < 3 * D; c += kSmallThreads) dst[c] = acc_sm[c];
+        __syncthreads();
+        for (int c = threadIdx.x; c < 3 * D; c += kSmallThreads) dst[c] = acc[c];
     } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -380,9 +458,9 @@ __global__ void __launch_bounds__(MAXT) join_backward_kernel(const hla2_block_ar
             for (int i = 0; i < VEC; ++i) {
                 const int c = (j * tpr + t) * VEC + i;
                 if (c < D) {
-                    dst[c] = gp[j][i];
-                    dst[D + c] = gs[j][i];
-                    dst[2 * D + c] = gn[j][i];
+                    if (a.y) dst[c] = gp[j][i];
+                    if (sc) dst[D + c] = gs[j][i];
+                    if (g.dh) dst[2 * D + c] = gn[j][i];
                 }
             }
     }
@@ -398,8 +476,17 @@ __global__ void __launch_bounds__(1024) partial_sum_kernel(const float* __restri
     float* dst = which == 0 ? d0 : which == 1 ? d1 : d2;
     if (!dst) return;
     float s = 0.f;
-    if (c < D)
-        for (int p = w; p < partials; p += 32) s += partial[((size_t)p * 3 + which) * D + c];
+    if (c < D) {
+        const float* src = partial + (size_t)which * D + c;
+        int p = w;
+        for (; p + 7 * 32 < partials; p += 8 * 32) {  // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = src[(size_t)(p + 32 * i) * 3 * D];
+            s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        }
+        for (; p < partials; p += 32) s += src[(size_t)p * 3 * D];
+    }
     sm[w][lane] = s;
     __syncthreads();
     for (int o = 16; o; o >>= 1) {
@@ -540,12 +627,39 @@ int sms() {
     return v;
 }
 
-// CTAs of the backward: at most four per SM, no more than there are rows for.
-int backward_ctas(const hla2_block_args* a, const Shape& s) {
+// Persistent CTAs and their ring.  Stages: as many rows ahead as fit in the SM's shared memory beside
+// the CTAs that the registers allow (512 threads of the backward, 1024 of the forward), at most
+// four; one stage copies and waits.
+struct Work {
+    int ctas, stages;
+    size_t smem;
+};
+Work work_of(const hla2_block_args* a, const Shape& s, int vec, int tensors, int threads_per_sm, size_t least) {
+    const size_t slot = (size_t)vec * (a->dtype == HLA2_BF16 ? 2 : 4);
+    const size_t stage = slot * s.threads * s.nv * tensors, room = 220 * 1024;
+    int each = threads_per_sm / s.threads;
+    if (each < 1) each = 1;
+    if (each > 16) each = 16;
+    Work w;
+    w.stages = 4;
+    while (w.stages > 1 && (w.stages * stage + 2048) * each > room && !(each == 1 && w.stages * stage <= room)) --w.stages;
+    while (each > 1 && (w.stages * stage + 2048) * each > room) --each;
+    w.smem = w.stages * stage > least ? w.stages * stage : least;
     const int per = s.tpr ? kSmallThreads / s.tpr : 1;
-    long long need = (a->rows + per - 1) / per;
-    const long long most = 4LL * sms();
-    return (int)(need < most ? need : most);
+    const long long need = (a->rows + per - 1) / per, most = (long long)each * sms();
+    w.ctas = (int)(need < most ? need : most);
+    return w;
+}
+constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512;
+
+Work backward_work(const hla2_block_args* a, const Shape& s, int vec, int tensors) {
+    return work_of(a, s, vec, tensors, kBwdThreadsPerSm, s.tpr ? 3 * (size_t)a->D * sizeof(float) : 0);
+}
+
+template <class K>
+bool set_smem(K kernel, size_t bytes) {
+    return bytes <= 40 * 1024 ||  // 48 KB with the static part
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
 }  // namespace
@@ -570,20 +684,21 @@ int hla2_block_join(const hla2_block_args* a, void* r, void* h, hla2_stream_t st
     const int vec = vec_of(a, outs, 2);
     const Shape s = shape_of(a->D, vec);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int tensors = 1 + (a->y ? 1 : 0) + (a->y && a->gate && a->gate_cols != 1 ? 1 : 0);
+    const Work w = work_of(a, s, vec, tensors, kFwdThreadsPerSm, 0);
     auto launch = [&](auto v, auto nv, auto tpr, auto maxt) {
         constexpr int VEC = decltype(v)::value, NV = decltype(nv)::value, TPR = decltype(tpr)::value,
                       MAXT = decltype(maxt)::value;
-        const unsigned grid = TPR ? (unsigned)((a->rows + kSmallThreads / TPR - 1) / (kSmallThreads / TPR)) : (unsigned)a->rows;
-        if constexpr (VEC == 8 || VEC == 2) {
-            join_kernel<bf16, VEC, NV, TPR, MAXT><<<grid, s.threads, 0, st>>>(*a, static_cast<bf16*>(r), static_cast<bf16*>(h));
-        } else if constexpr (VEC == 4) {
-            join_kernel<float, VEC, NV, TPR, MAXT><<<grid, s.threads, 0, st>>>(*a, static_cast<float*>(r), static_cast<float*>(h));
-        } else if (a->dtype == HLA2_BF16) {
-            join_kernel<bf16, 1, NV, TPR, MAXT><<<grid, s.threads, 0, st>>>(*a, static_cast<bf16*>(r), static_cast<bf16*>(h));
-        } else {
-            join_kernel<float, 1, NV, TPR, MAXT><<<grid, s.threads, 0, st>>>(*a, static_cast<float*>(r), static_cast<float*>(h));
-        }
-        return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+        auto go = [&](auto zero) {
+            using T = decltype(zero);
+            auto k = join_kernel<T, VEC, NV, TPR, MAXT>;
+            if (!set_smem(k, w.smem)) return -1;
+            k<<<w.ctas, s.threads, w.smem, st>>>(*a, static_cast<T*>(r), static_cast<T*>(h), w.stages);
+            return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+        };
+        if constexpr (VEC == 8 || VEC == 2) return go(bf16{});
+        else if constexpr (VEC == 4) return go(float{});
+        else return a->dtype == HLA2_BF16 ? go(bf16{}) : go(float{});
     };
     if (with_vec(a->D, vec, s, launch))
         return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));
@@ -596,8 +711,10 @@ size_t hla2_block_join_backward_workspace_bytes(const hla2_block_args* a) {
     size_t most = 0;
     const int wide = a->dtype == HLA2_BF16 ? 8 : 4;
     for (int vec : {1, 2, wide}) {  // whichever the addresses allow
-        const size_t c = (size_t)backward_ctas(a, shape_of(a->D, vec));
-        if (c > most) most = c;
+        for (int tensors = 2; tensors <= 5; ++tensors) {
+            const size_t c = (size_t)backward_work(a, shape_of(a->D, vec), vec, tensors).ctas;
+            if (c > most) most = c;
+        }
     }
     return most * 3 * (size_t)a->D * sizeof(float);
 }
@@ -629,21 +746,22 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
         const void* outs[5] = {dr, dh, dx, dy, a->gate_cols != 1 ? dgate : nullptr};
         const int vec = vec_of(a, outs, 5);
         const Shape s = shape_of(a->D, vec);
-        g.partials = backward_ctas(a, s);
+        const int tensors = 1 + (a->y ? 1 : 0) + (a->y && a->gate && a->gate_cols != 1 ? 1 : 0) + (dr ? 1 : 0) + (dh ? 1 : 0);
+        const Work w = backward_work(a, s, vec, tensors);
+        g.partials = w.ctas;
         auto launch = [&](auto v, auto nv, auto tpr, auto maxt) {
             constexpr int VEC = decltype(v)::value, NV = decltype(nv)::value, TPR = decltype(tpr)::value,
-                      MAXT = decltype(maxt)::value;
-            const size_t smem = TPR ? 3 * (size_t)a->D * sizeof(float) : 0;
-            if constexpr (VEC == 8 || VEC == 2) {
-                join_backward_kernel<bf16, VEC, NV, TPR, MAXT><<<g.partials, s.threads, smem, st>>>(*a, g);
-            } else if constexpr (VEC == 4) {
-                join_backward_kernel<float, VEC, NV, TPR, MAXT><<<g.partials, s.threads, smem, st>>>(*a, g);
-            } else if (a->dtype == HLA2_BF16) {
-                join_backward_kernel<bf16, 1, NV, TPR, MAXT><<<g.partials, s.threads, smem, st>>>(*a, g);
-            } else {
-                join_backward_kernel<float, 1, NV, TPR, MAXT><<<g.partials, s.threads, smem, st>>>(*a, g);
-            }
-            return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+                          MAXT = decltype(maxt)::value;
+            auto go = [&](auto zero) {
+                using T = decltype(zero);
+                auto k = join_backward_kernel<T, VEC, NV, TPR, MAXT>;
+                if (!set_smem(k, w.smem)) return -1;
+                k<<<w.ctas, s.threads, w.smem, st>>>(*a, g, w.stages);
+                return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+            };
+            if constexpr (VEC == 8 || VEC == 2) return go(bf16{});
+            else if constexpr (VEC == 4) return go(float{});
+            else return a->dtype == HLA2_BF16 ? go(bf16{}) : go(float{});
         };
         if (with_vec(a->D, vec, s, launch))
             return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));

@@ -98,10 +98,12 @@ LinPlan lin_plan(const hla2_linattn_args* a, int W, int slots) {
     const long long heads = (long long)a->B * a->Hk;
     if (p.nchunks == 0 || heads == 0) return p;
     double best = 0;
-    long long most = 4LL * slots / heads + 1;
-    if (most > p.nchunks) most = p.nchunks;
-    if (most > 4096) most = 4096;
-    for (long long want = 1; want <= most; ++want) {
+    // one segment, and as many as fill one to four waves
+    for (int wave = 0; wave <= 4; ++wave) {
+        long long want = wave == 0 ? 1 : (long long)wave * slots / heads;
+        if (want < 1) continue;
+        if (want > p.nchunks) want = p.nchunks;
+        if (want > 4096) want = 4096;
         const int sc = (int)((p.nchunks + want - 1) / want), ns = (p.nchunks + sc - 1) / sc;
         const long long waves = (heads * ns + slots - 1) / slots;
         const double cost = (double)waves * sc * (ns > 1 ? 1.5 : 1.0) + (ns > 1 ? 2.0 : 0.0);

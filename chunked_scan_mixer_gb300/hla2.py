@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple, Optional
 
@@ -56,24 +57,7 @@ class View(ctypes.Structure):
                 ("sn", ctypes.c_longlong)]
 
 
-class LinattnArgs(ctypes.Structure):
-    _fields_ = [
-        ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("n", ctypes.c_int),
-        ("d", ctypes.c_int), ("dv", ctypes.c_int), ("scale", ctypes.c_float), ("gamma", ctypes.c_void_p),
-        ("lengths", ctypes.c_void_p), ("q", View), ("k", View), ("v", View), ("init_state", ctypes.c_void_p),
-        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
-    ]
-
-
-class BlockArgs(ctypes.Structure):
-    _fields_ = [
-        ("dtype", ctypes.c_int), ("gate_act", ctypes.c_int), ("gate_cols", ctypes.c_int),
-        ("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("eps", ctypes.c_float),
-        ("x", ctypes.c_void_p), ("x_stride", ctypes.c_longlong), ("y", ctypes.c_void_p), ("y_stride", ctypes.c_longlong),
-        ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_longlong), ("post_weight", ctypes.c_void_p),
-        ("scale", ctypes.c_void_p), ("next_weight", ctypes.c_void_p),
-    ]
-
+_SIZE_MAX = ctypes.c_size_t(-1).value
 
 FLAG_SAVE_FOR_BACKWARD = 1
 FLAG_STATES_SAVED = 2
@@ -157,20 +141,19 @@ def lib():
         L.hla2_mq_head_state_floats.restype = Z
         L.hla2_decode_step_mq.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, I, P, ctypes.POINTER(Opts)]
         L.hla2_decode_step_mq.restype = I
-        LA, BA = ctypes.POINTER(LinattnArgs), ctypes.POINTER(BlockArgs)
-        L.hla2_linattn_workspace_bytes.argtypes = [LA, I, I]
+        L.hla2_linattn_workspace_bytes.argtypes = [P, I, I]
         L.hla2_linattn_workspace_bytes.restype = Z
-        L.hla2_linattn_forward.argtypes = [LA, View, P, P]
+        L.hla2_linattn_forward.argtypes = [P, View, P, P]
         L.hla2_linattn_forward.restype = I
-        L.hla2_linattn_backward.argtypes = [LA, View, View, View, View, P, P, P]
+        L.hla2_linattn_backward.argtypes = [P, View, View, View, View, P, P, P]
         L.hla2_linattn_backward.restype = I
         L.hla2_linattn_decode_step.argtypes = [P, P, P, P, P, I, I, I, I, I, P, F, I, P]
         L.hla2_linattn_decode_step.restype = I
-        L.hla2_block_join.argtypes = [BA, P, P, P]
+        L.hla2_block_join.argtypes = [P, P, P, P]
         L.hla2_block_join.restype = I
-        L.hla2_block_join_backward_workspace_bytes.argtypes = [BA]
+        L.hla2_block_join_backward_workspace_bytes.argtypes = [P]
         L.hla2_block_join_backward_workspace_bytes.restype = Z
-        L.hla2_block_join_backward.argtypes = [BA, P, P, P, P, P, P, P, P, P, Z, P]
+        L.hla2_block_join_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, Z, P]
         L.hla2_block_join_backward.restype = I
         L.hla2_w4_matvec.argtypes = [P, ctypes.c_longlong, P, P, P, P, P, I, I, I, I, I, P]
         L.hla2_w4_matvec.restype = I
@@ -676,42 +659,64 @@ def ahla_backward(q, k, v, dout, gamma=None, chunk=32):
 # Around a mixer layer: first-order linear attention, block norms, 4-bit projections
 # ---------------------------------------------------------------------------------------
 
-def _need_cuda(*tensors):
-    """All given tensors are CUDA tensors of one device and one supported type."""
-    first = tensors[0]
-    if first.device.type != "cuda" or first.dtype not in _DTYPES:
+# These calls are short on the GPU (a step of one sequence takes a few microseconds), so their host
+# side is kept lean: addresses go to the library as plain integers and the argument blocks as
+# packed bytes in the C layout.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(device).cuda_stream without the object
+
+_LINATTN_ARGS = struct.Struct("@7if2P" + 3 * "P3q" + "PPN")   # hla2_linattn_args
+_BLOCK_ARGS = struct.Struct("@3iqifPqPqPqPPP")                # hla2_block_args
+
+
+def _need_cuda(first, *others):
+    """Device index of CUDA tensors that share one device and one supported type."""
+    dtype = first.dtype
+    if not first.is_cuda or dtype not in _DTYPES:
         raise TypeError("tensors must be float32 or bfloat16 CUDA tensors")
-    for t in tensors:
-        if t is not None and (t.dtype != first.dtype or t.device != first.device):
+    index = first.get_device()
+    for t in others:
+        if t is not None and (t.dtype != dtype or t.get_device() != index):
             raise TypeError("tensors must all have the same type and device")
-    return first.device
+    return index
 
 
-def _scratch(nbytes, device, stream_handle):
+def _scratch(nbytes, device, stream):
     """_workspace, but under graph capture a buffer of the graph's own: the cached one is shared with
     eager calls on the stream, which a replay would race with.  The first bytes are the status
     word (see hla2_workspace_status), 0 in a new buffer."""
-    if nbytes == 0:
-        return None
-    if torch.cuda.is_current_stream_capturing():
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        buf[:256].zero_()
-        return buf
-    known = _ws_cache.get((device.index, stream_handle.value))
-    buf = _workspace(nbytes, device, stream_handle)
-    if buf is not known:
-        buf[:256].zero_()
+    key = (device.index, stream or None)  # as _workspace and check_status have it
+    known = _ws_cache.get(key)
+    if known is not None and known.numel() >= nbytes and not torch.cuda.is_current_stream_capturing():
+        return known
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    buf[:256].zero_()
+    if not torch.cuda.is_current_stream_capturing():
+        _ws_cache[key] = buf
     return buf
 
 
+def _float_vector(gamma, H, device):
+    """_gamma_tensor; a tensor that already is what the kernels read goes through as it is."""
+    if gamma is None:
+        return None
+    if (isinstance(gamma, torch.Tensor) and gamma.dtype == torch.float32 and gamma.is_cuda and gamma.dim() == 1
+            and gamma.shape[0] == H and gamma.stride(0) == 1 and gamma.device == device):
+        return gamma
+    return _gamma_tensor(gamma, H, device)
+
+
 def _view4(t):
-    """(tensor, View) of [B, H, n, D]: the tensor itself where its strides serve, else a copy."""
-    es, (B, H, n, D) = t.element_size(), t.shape
-    rows = [(s, x) for s, x in zip(t.stride()[:3], t.shape[:3]) if x > 1]
-    if (t.numel() and (t.stride(3) != 1 and D > 1 or t.data_ptr() % 16
-                       or any(s * es % 16 or s < D for s, _ in rows))):
+    """(tensor, address, strides of batch, head, token) of [B, H, n, D]: the tensor itself where its
+    strides serve, else a copy."""
+    (B, H, n, D), (sb, sh, sn, sd) = t.shape, t.stride()
+    p = t.data_ptr()
+    per16 = 16 // t.element_size()
+    if (p % 16 or sd != 1 and D > 1 or B > 1 and (sb % per16 or sb < D) or H > 1 and (sh % per16 or sh < D)
+            or n > 1 and (sn % per16 or sn < D)):
         t = t.clone(memory_format=torch.contiguous_format)
-    return t, View(t.data_ptr() or None, *t.stride()[:3])
+        p, (sb, sh, sn, _) = t.data_ptr(), t.stride()
+    return t, p, sb, sh, sn
 
 
 def _out4(name, out, like, shape):
@@ -729,31 +734,57 @@ def _out4(name, out, like, shape):
 
 
 def _plain_view(t):
-    return View(t.data_ptr() or None, *t.stride()[:3])
+    return View(t.data_ptr(), *t.stride()[:3])
 
 
-def _linattn_args(q, k, v, gamma, scale, lengths, init_state):
-    device = _need_cuda(q, k, v)
+class _Lin(NamedTuple):
+    """One checked call: sizes, the packed argument block and the tensors that it points into."""
+    B: int
+    H: int
+    Hk: int
+    n: int
+    d: int
+    dv: int
+    device: torch.device
+    stream: int
+    args: bytes
+    keep: tuple
+
+
+def _linattn_args(q, k, v, gamma, scale, lengths, init_state, backward, want_final):
+    index = _need_cuda(q, k, v)
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k, v must be [B, heads, n, dim]")
+    device = q.device
     B, H, n, d = q.shape
-    Hk, dv = k.shape[1], v.shape[-1]
-    if tuple(k.shape) != (B, Hk, n, d) or tuple(v.shape) != (B, Hk, n, dv):
+    Hk, dv = k.shape[1], v.shape[3]
+    if k.shape != (B, Hk, n, d) or v.shape != (B, Hk, n, dv):
         raise ValueError("shape mismatch between q, k, v")
     if (Hk == 0) != (H == 0) or (Hk and H % Hk):
         raise ValueError("the query heads must be a multiple of the key heads")
-    g = _gamma_tensor(gamma, Hk, device)
-    if lengths is not None:
+    g = _float_vector(gamma, Hk, device)
+    if lengths is not None and not (isinstance(lengths, torch.Tensor) and lengths.dtype == torch.int32
+                                    and lengths.device == device and lengths.is_contiguous()):
         lengths = torch.as_tensor(lengths, device=device)
-        if lengths.dtype not in (torch.int32, torch.int64) or tuple(lengths.shape) != (B,):
-            raise ValueError("lengths must be B integers")
+        if lengths.dtype not in (torch.int32, torch.int64):
+            raise ValueError("lengths must be integers")
         lengths = lengths.to(torch.int32).contiguous()
+    if lengths is not None and lengths.shape != (B,):
+        raise ValueError("lengths must be B integers")
     init = _state_arg("init_state", init_state, (B, Hk, d, dv), device)
-    (qt, qv), (kt, kv), (vt, vv) = (_view4(t) for t in (q, k, v))
-    a = LinattnArgs(_DTYPES[q.dtype], B, H, Hk, n, d, dv, float(scale), None if g is None else g.data_ptr(),
-                    None if lengths is None else lengths.data_ptr(), qv, kv, vv,
-                    None if init is None else init.data_ptr() or None, None, 0)
-    return a, device, (qt, kt, vt, g, lengths, init)  # the tensors live as long as the call
+    qt, *qv = _view4(q)
+    kt, *kv = _view4(k)
+    vt, *vv = _view4(v)
+    head = (_DTYPES[q.dtype], B, H, Hk, n, d, dv, scale, 0 if g is None else g.data_ptr(),
+            0 if lengths is None else lengths.data_ptr(), *qv, *kv, *vv, 0 if init is None else init.data_ptr())
+    args = _LINATTN_ARGS.pack(*head, 0, 0)
+    stream = _raw_stream(index)
+    nbytes = lib().hla2_linattn_workspace_bytes(args, backward, want_final)
+    ws = None
+    if nbytes != _SIZE_MAX and nbytes > 0:  # else the call itself says what is wrong
+        ws = _scratch(nbytes, device, stream)
+        args = _LINATTN_ARGS.pack(*head, ws.data_ptr(), nbytes)
+    return _Lin(B, H, Hk, n, d, dv, device, stream, args, (qt, kt, vt, g, lengths, init, ws))
 
 
 def _state_arg(name, state, shape, device):
@@ -762,15 +793,6 @@ def _state_arg(name, state, shape, device):
     if tuple(state.shape) != shape or state.dtype != torch.float32 or state.device != device:
         raise ValueError(f"{name} must be a float32 {shape} tensor on the inputs' device")
     return state.contiguous()
-
-
-def _linattn_workspace(a, backward, want_final, device, sh):
-    nbytes = lib().hla2_linattn_workspace_bytes(ctypes.byref(a), backward, int(want_final))
-    if nbytes == ctypes.c_size_t(-1).value:
-        return None  # the call itself says what is wrong
-    ws = _scratch(int(nbytes), device, sh)
-    a.workspace, a.workspace_bytes = None if ws is None else ws.data_ptr(), int(nbytes)
-    return ws
 
 
 def linattn_forward(q, k, v, gamma=None, scale=1.0, lengths=None, init_state=None, return_final_state=False, out=None):
@@ -785,12 +807,12 @@ def linattn_forward(q, k, v, gamma=None, scale=1.0, lengths=None, init_state=Non
     to continue from.  Returns out [B,H,n,dv], in q's token / head order, and with
     ``return_final_state`` the float32 state after each sequence's last token, which
     linattn_decode_step goes on from."""
-    a, device, keep = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
+    a = _linattn_args(q, k, v, gamma, scale, lengths, init_state, 0, 1 if return_final_state else 0)
     o = _out4("out", out, q, (a.B, a.H, a.n, a.dv))
-    fin = torch.empty((a.B, a.Hk, a.d, a.dv), dtype=torch.float32, device=device) if return_final_state else None
-    sh = _stream_handle(device)
-    ws = _linattn_workspace(a, 0, return_final_state, device, sh)  # noqa: F841 (kept until the call is enqueued)
-    _check("hla2_linattn_forward", lib().hla2_linattn_forward(ctypes.byref(a), _plain_view(o), _ptr(fin), sh))
+    fin = torch.empty((a.B, a.Hk, a.d, a.dv), dtype=torch.float32, device=a.device) if return_final_state else None
+    rc = lib().hla2_linattn_forward(a.args, _plain_view(o), None if fin is None else fin.data_ptr(), a.stream)
+    if rc:
+        _check("hla2_linattn_forward", rc)
     return (o, fin) if return_final_state else o
 
 
@@ -800,46 +822,56 @@ def linattn_backward(q, k, v, dout, gamma=None, scale=1.0, lengths=None, init_st
     dfinal_state (None: zero) of its final state.  Returns (dq, dk, dv), dk and dv summed over
     the query heads that share a key head, and with an init_state also its float32 gradient.
     gamma has no gradient."""
-    a, device, keep = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
+    a = _linattn_args(q, k, v, gamma, scale, lengths, init_state, 1,
+                      1 if init_state is not None or dfinal_state is not None else 0)
     _need_cuda(q, dout)
-    if tuple(dout.shape) != (a.B, a.H, a.n, a.dv):
+    if dout.shape != (a.B, a.H, a.n, a.dv):
         raise ValueError("dout must be [B, H, n, dv]")
-    dfin = _state_arg("dfinal_state", dfinal_state, (a.B, a.Hk, a.d, a.dv), device)
-    dot, dov = _view4(dout)
+    states = (a.B, a.Hk, a.d, a.dv)
+    dfin = _state_arg("dfinal_state", dfinal_state, states, a.device)
+    dot, *dov = _view4(dout)
     gq = _out4("dq", dq, q, (a.B, a.H, a.n, a.d))
     gk = _out4("dk", dk, k, (a.B, a.Hk, a.n, a.d))
     gv = _out4("dv", dv, v, (a.B, a.Hk, a.n, a.dv))
-    dinit = torch.empty((a.B, a.Hk, a.d, a.dv), dtype=torch.float32, device=device) if init_state is not None else None
-    sh = _stream_handle(device)
-    ws = _linattn_workspace(a, 1, dinit is not None or dfin is not None, device, sh)  # noqa: F841
-    _check("hla2_linattn_backward",
-           lib().hla2_linattn_backward(ctypes.byref(a), dov, _plain_view(gq), _plain_view(gk), _plain_view(gv),
-                                       _ptr(dfin), _ptr(dinit), sh))
+    dinit = torch.empty(states, dtype=torch.float32, device=a.device) if init_state is not None else None
+    rc = lib().hla2_linattn_backward(a.args, View(*dov), _plain_view(gq), _plain_view(gk), _plain_view(gv),
+                                     None if dfin is None else dfin.data_ptr(),
+                                     None if dinit is None else dinit.data_ptr(), a.stream)
+    if rc:
+        _check("hla2_linattn_backward", rc)
     return (gq, gk, gv) if dinit is None else (gq, gk, gv, dinit)
 
 
 def linattn_decode_step(state, q, k, v, gamma=None, scale=1.0, out=None):
     """One token for each of N sequences: ``state`` [N,Hk,d,dv] float32 on the GPU is updated in
     place.  q [N,H,d]; k [N,Hk,d]; v [N,Hk,dv].  Returns out [N,H,dv] = scale * P^T q."""
-    if state.device.type != "cuda" or state.dtype != torch.float32 or not state.is_contiguous():
+    if not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor")
-    device = _need_cuda(q, k, v)
+    index = _need_cuda(q, k, v)
     N, H, d = q.shape
-    Hk, dv = k.shape[1], v.shape[-1]
-    if (tuple(k.shape) != (N, Hk, d) or tuple(v.shape) != (N, Hk, dv) or tuple(state.shape) != (N, Hk, d, dv)
-            or state.device != device):
+    Hk, dv = k.shape[1], v.shape[2]
+    if (k.shape != (N, Hk, d) or v.shape != (N, Hk, dv) or state.shape != (N, Hk, d, dv)
+            or state.get_device() != index):
         raise ValueError("shape or device mismatch between state, q, k, v")
-    qd, kd, vd = (t.contiguous() for t in (q, k, v))
-    qd, kd, vd = (t if t.data_ptr() % 16 == 0 else t.clone() for t in (qd, kd, vd))
-    g = _gamma_tensor(gamma, Hk, device)
-    if out is not None and (tuple(out.shape) != (N, H, dv) or out.dtype != q.dtype or not out.is_contiguous()
-                            or out.device != device):
+    q, k, v = _packed16(q), _packed16(k), _packed16(v)
+    g = _float_vector(gamma, Hk, q.device)
+    if out is None:
+        out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+    elif out.shape != (N, H, dv) or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != index:
         raise ValueError("out must be a contiguous [N, H, dv] tensor of the inputs' type")
-    o = out if out is not None else torch.empty((N, H, dv), dtype=q.dtype, device=device)
-    _check("hla2_linattn_decode_step",
-           lib().hla2_linattn_decode_step(_ptr(state), _ptr(qd), _ptr(kd), _ptr(vd), _ptr(o), N, H, Hk, d, dv, _ptr(g),
-                                          float(scale), _DTYPES[q.dtype], _stream_handle(device)))
-    return o
+    rc = lib().hla2_linattn_decode_step(state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), N, H,
+                                        Hk, d, dv, None if g is None else g.data_ptr(), scale, _DTYPES[q.dtype],
+                                        _raw_stream(index))
+    if rc:
+        _check("hla2_linattn_decode_step", rc)
+    return out
+
+
+def _packed16(t):
+    """The tensor, or a copy where it is not contiguous at a 16-byte address."""
+    if not t.is_contiguous():
+        return t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 GATE_ACTS = {"sigmoid": 0, "silu": 1}
@@ -857,63 +889,75 @@ class BlockJoinGrads(NamedTuple):
 
 
 def _rows(t, D):
-    """(rows tensor, row stride) of [..., D]: in place where all leading dimensions are one stride."""
-    if t.dim() == 0 or t.shape[-1] != D:
+    """(rows tensor, rows, row stride) of [..., D]: in place where all leading dimensions are one stride."""
+    if t.dim() != 2:
+        if t.dim() == 0:
+            raise ValueError(f"the last dimension must be {D}")
+        t = t.reshape(-1, D) if D else t.reshape(0, 0)  # a view where the strides allow it
+    rows, cols = t.shape
+    if cols != D:
         raise ValueError(f"the last dimension must be {D}")
-    if t.dim() == 2 and (D == 1 or t.stride(1) == 1):
-        return t, t.stride(0) if t.shape[0] > 1 else D
-    t2 = t.reshape(-1, D)  # a view where the strides allow it
-    if D > 1 and t2.stride(1) != 1:
-        t2 = t2.contiguous()
-    return t2, t2.stride(0) if t2.shape[0] > 1 else D
+    if D > 1 and t.stride(1) != 1:
+        t = t.contiguous()
+    return t, rows, t.stride(0) if rows > 1 else D
+
+
+def _vector(name, w, D):
+    if w is None:
+        return None
+    if w.shape != (D,):
+        raise ValueError(f"{name} must be [{D}]")
+    return w if w.is_contiguous() else w.contiguous()
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps):
-    device = _need_cuda(x, y, post_weight, gate, scale, next_weight)
-    if gate_act not in GATE_ACTS:
+    """(packed argument block, D, device index, tensors to keep)"""
+    index = _need_cuda(x, y, post_weight, gate, scale, next_weight)
+    act = GATE_ACTS.get(gate_act)
+    if act is None:
         raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}")
-    D = x.shape[-1]
-    if y is not None and y.shape != x.shape:
-        raise ValueError("y must have x's shape")
-    for name, w in (("post_weight", post_weight), ("scale", scale), ("next_weight", next_weight)):
-        if w is not None and tuple(w.shape) != (D,):
-            raise ValueError(f"{name} must be [{D}]")
-    cols = 0
+    shape = x.shape
+    D = shape[-1] if x.dim() else 0
+    pw, sc, nw = _vector("post_weight", post_weight, D), _vector("scale", scale, D), _vector("next_weight", next_weight, D)
+    xr, rows, xs = _rows(x, D)
+    yr = zr = None
+    ys = zs = cols = 0
+    if y is not None:
+        if y.shape != shape:
+            raise ValueError("y must have x's shape")
+        yr, _, ys = _rows(y, D)
     if gate is not None:
-        if gate.shape[:-1] != x.shape[:-1] or gate.shape[-1] not in (1, D):
+        cols = gate.shape[-1] if gate.dim() else 0
+        if gate.shape[:-1] != shape[:-1] or cols not in (1, D):
             raise ValueError("gate must have x's shape, or one value a row")
-        cols = gate.shape[-1]
-    keep = [w.contiguous() if w is not None else None for w in (post_weight, scale, next_weight)]
-    xr, xs = _rows(x, D)
-    yr, ys = _rows(y, D) if y is not None else (None, 0)
-    zr, zs = _rows(gate, cols) if gate is not None else (None, 0)
-    ptr = [None if t is None else t.data_ptr() or None for t in (xr, yr, zr, *keep)]
-    a = BlockArgs(_DTYPES[x.dtype], GATE_ACTS[gate_act], cols, xr.shape[0], D, float(eps), ptr[0], xs, ptr[1], ys,
-                  ptr[2], zs, *ptr[3:])
-    return a, device, (xr, yr, zr, keep)
+        zr, _, zs = _rows(gate, cols)
+    args = _BLOCK_ARGS.pack(_DTYPES[x.dtype], act, cols, rows, D, eps, xr.data_ptr(), xs, _addr(yr), ys, _addr(zr), zs,
+                            _addr(pw), _addr(sc), _addr(nw))
+    return args, D, index, (xr, yr, zr, pw, sc, nw)
 
 
 def block_norm(x, weight, eps=1e-6, out=None):
     """The norm before a block: x / sqrt(mean(x^2) + eps) * weight over the last dimension (1 to
     8192 values; float32 or bfloat16 on the GPU)."""
-    a, device, keep = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
-    h = _row_out("out", out, x)
-    _check("hla2_block_join", lib().hla2_block_join(ctypes.byref(a), None, _ptr(h), _stream_handle(device)))
-    return h
-
-
-def _row_out(name, out, x):
+    args, _, index, keep = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of x's shape, type and device")
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of x's shape, type and device")
+    rc = lib().hla2_block_join(args, None, out.data_ptr(), _raw_stream(index))
+    if rc:
+        _check("hla2_block_join", rc)
     return out
 
 
 def block_norm_backward(x, weight, dout, eps=1e-6):
     """(dx, dweight) of block_norm; dweight is a float32 sum over the rows."""
-    a, device, keep = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
-    g = _block_backward(a, device, x, None, None, weight, None, dout)
+    args = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
+    g = _block_backward(args, x, None, None, None, None, weight, None, dout)
     return g.dx, g.dnext_weight
 
 
@@ -925,36 +969,40 @@ def block_join(x, y, post_weight, gate=None, gate_act="sigmoid", scale=None, nex
     next_weight [D]; all of one type, float32 or bfloat16 on the GPU.  Returns (r, h)."""
     if y is None:
         raise ValueError("block_join needs y (block_norm is the norm alone)")
-    a, device, keep = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
-    r = torch.empty(x.shape, dtype=x.dtype, device=device)
-    h = torch.empty(x.shape, dtype=x.dtype, device=device) if next_weight is not None else None
-    _check("hla2_block_join", lib().hla2_block_join(ctypes.byref(a), _ptr(r), _ptr(h), _stream_handle(device)))
+    args, _, index, keep = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
+    r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if next_weight is not None else None
+    rc = lib().hla2_block_join(args, r.data_ptr(), None if h is None else h.data_ptr(), _raw_stream(index))
+    if rc:
+        _check("hla2_block_join", rc)
     return r, h
 
 
-def _block_backward(a, device, x, y, gate, next_weight, dr, dh):
-    D = a.D
+def _block_backward(checked, x, y, gate, post_weight, scale, next_weight, dr, dh):
+    args, D, index, keep = checked
+    device = x.device
     for name, t in (("dr", dr), ("dh", dh)):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != device):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.get_device() != index):
             raise ValueError(f"{name} must have x's shape, type and device")
-    if next_weight is not None and dh is None or next_weight is None and dh is not None:
+    if (next_weight is None) != (dh is None):
         raise ValueError("dh is needed with next_weight, and only then")
     if dr is None and dh is None:
         raise ValueError("dr or dh is needed")
     dr, dh = (None if t is None else t.contiguous() for t in (dr, dh))
     new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)  # noqa: E731
     dx, dy, dgate = new(x), new(y), new(gate)
-    dpw, dsc, dnw = (torch.empty(D, dtype=torch.float32, device=device) if p else None
-                     for p in (a.post_weight, a.scale, a.next_weight))
-    sh = _stream_handle(device)
-    nbytes = lib().hla2_block_join_backward_workspace_bytes(ctypes.byref(a))
-    nbytes = 0 if nbytes == ctypes.c_size_t(-1).value else int(nbytes)
-    # floats of its own after the status word, which belongs to the calls with bounded waits
-    ws = _scratch(nbytes + 256, device, sh) if nbytes else None
-    wp = None if ws is None else ctypes.c_void_p(ws.data_ptr() + 256)
-    _check("hla2_block_join_backward",
-           lib().hla2_block_join_backward(ctypes.byref(a), _ptr(dr), _ptr(dh), _ptr(dx), _ptr(dy), _ptr(dgate),
-                                          _ptr(dpw), _ptr(dsc), _ptr(dnw), wp, nbytes, sh))
+    sums = torch.empty((3, D), dtype=torch.float32, device=device)
+    dpw, dsc, dnw = (None if w is None else g for g, w in zip(sums, (post_weight, scale, next_weight)))
+    stream = _raw_stream(index)
+    nbytes = lib().hla2_block_join_backward_workspace_bytes(args)
+    ws = 0
+    if nbytes != _SIZE_MAX and nbytes > 0:
+        # after the status word, which belongs to the calls with bounded waits
+        ws = _scratch(nbytes + 256, device, stream).data_ptr() + 256
+    rc = lib().hla2_block_join_backward(args, _addr(dr), _addr(dh), _addr(dx), _addr(dy), _addr(dgate), _addr(dpw),
+                                        _addr(dsc), _addr(dnw), ws, nbytes, stream)
+    if rc:
+        _check("hla2_block_join_backward", rc)
     return BlockJoinGrads(dx, dy, dgate, dpw, dsc, dnw)
 
 
@@ -964,8 +1012,8 @@ def block_join_backward(x, y, post_weight, gate=None, gate_act="sigmoid", scale=
     (needed with next_weight).  Nothing is kept from the forward."""
     if y is None:
         raise ValueError("block_join_backward needs y (block_norm_backward is the norm alone)")
-    a, device, keep = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
-    return _block_backward(a, device, x, y, gate, next_weight, dr, dh)
+    args = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
+    return _block_backward(args, x, y, gate, post_weight, scale, next_weight, dr, dh)
 
 
 def w4_matvec(x, qweight, scales, zeros=None, bias=None, out=None):
@@ -976,31 +1024,30 @@ def w4_matvec(x, qweight, scales, zeros=None, bias=None, out=None):
     byte j and 2 j + 1 in the high half; scales [N, K / group], group 32, 64 or 128; zeros uint8
     [N, K / group] in 0..15 (None: 8); bias [N].  x, scales and bias float32 or bfloat16
     of one type on the GPU.  Returns y [..., N].  The products are exact and the sums float32."""
-    device = _need_cuda(x, scales, bias)
-    K = x.shape[-1]
-    if qweight.dim() != 2 or qweight.dtype != torch.uint8 or qweight.shape[1] * 2 != K or qweight.device != device:
+    index = _need_cuda(x, scales, bias)
+    shape = x.shape
+    K = shape[-1] if x.dim() else 0
+    if qweight.dim() != 2 or qweight.dtype != torch.uint8 or qweight.shape[1] * 2 != K or qweight.get_device() != index:
         raise ValueError("qweight must be uint8 [N, K / 2] on x's device")
     N = qweight.shape[0]
     if scales.dim() != 2 or scales.shape[0] != N or scales.shape[1] == 0 or K % scales.shape[1]:
         raise ValueError("scales must be [N, K / group]")
     group = K // scales.shape[1]
-    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape or zeros.device != device):
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape or zeros.get_device() != index):
         raise ValueError("zeros must be uint8 of scales' shape")
-    if bias is not None and tuple(bias.shape) != (N,):
+    if bias is not None and bias.shape != (N,):
         raise ValueError("bias must be [N]")
-    x2, stride = _rows(x, K)
-    M = x2.shape[0]
+    x2, M, stride = _rows(x, K)
     if x2.data_ptr() % 16 or M > 1 and stride * x2.element_size() % 16:
-        x2 = x2.clone(memory_format=torch.contiguous_format)
-        stride = K
-    qw, sc = qweight.contiguous(), scales.contiguous()
-    qw = qw if qw.data_ptr() % 16 == 0 else qw.clone()
-    ze, bi = (None if t is None else t.contiguous() for t in (zeros, bias))
-    y = out if out is not None else torch.empty((*x.shape[:-1], N), dtype=x.dtype, device=device)
-    if out is not None and (tuple(out.shape) != (*x.shape[:-1], N) or out.dtype != x.dtype or out.device != device
-                            or not out.is_contiguous()):
+        x2, stride = x2.clone(memory_format=torch.contiguous_format), K
+    qweight, scales = _packed16(qweight), scales.contiguous()
+    zeros, bias = (None if t is None else t.contiguous() for t in (zeros, bias))
+    if out is None:
+        out = torch.empty((*shape[:-1], N), dtype=x.dtype, device=x.device)
+    elif out.shape != (*shape[:-1], N) or out.dtype != x.dtype or out.get_device() != index or not out.is_contiguous():
         raise ValueError("out must be a contiguous [..., N] tensor of x's type and device")
-    _check("hla2_w4_matvec",
-           lib().hla2_w4_matvec(_ptr(x2), stride, _ptr(qw), _ptr(sc), _ptr(ze), _ptr(bi), _ptr(y), M, N, K, group,
-                                _DTYPES[x.dtype], _stream_handle(device)))
-    return y
+    rc = lib().hla2_w4_matvec(x2.data_ptr(), stride, qweight.data_ptr(), scales.data_ptr(), _addr(zeros), _addr(bias),
+                              out.data_ptr(), M, N, K, group, _DTYPES[x.dtype], _raw_stream(index))
+    if rc:
+        _check("hla2_w4_matvec", rc)
+    return out

@@ -6,12 +6,41 @@ import pytest
 import torch
 
 import chunked_scan_mixer_gb300 as hla
-from chunked_scan_mixer_gb300.hla2 import BlockArgs, LinattnArgs, View
+from chunked_scan_mixer_gb300.hla2 import _BLOCK_ARGS, _LINATTN_ARGS, View
 
 
 @pytest.fixture(scope="module")
 def L():
     return hla.lib()
+
+
+class LinattnArgs(ctypes.Structure):
+    """hla2_linattn_args, field by field."""
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("n", ctypes.c_int),
+        ("d", ctypes.c_int), ("dv", ctypes.c_int), ("scale", ctypes.c_float), ("gamma", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p), ("q", View), ("k", View), ("v", View), ("init_state", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class BlockArgs(ctypes.Structure):
+    """hla2_block_args, field by field."""
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("gate_act", ctypes.c_int), ("gate_cols", ctypes.c_int),
+        ("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("eps", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("x_stride", ctypes.c_longlong), ("y", ctypes.c_void_p), ("y_stride", ctypes.c_longlong),
+        ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_longlong), ("post_weight", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p), ("next_weight", ctypes.c_void_p),
+    ]
+
+
+def test_packed_argument_blocks_have_the_c_layout():
+    a = LinattnArgs(1, 2, 6, 3, 5, 16, 32, 0.5, 8, 9, View(10, 11, 12, 13), View(14, 15, 16, 17), View(18, 19, 20, 21),
+                    22, 23, 24)
+    assert _LINATTN_ARGS.pack(1, 2, 6, 3, 5, 16, 32, 0.5, *range(8, 25)) == bytes(a)
+    b = BlockArgs(1, 0, 64, 3, 64, 0.25, 6, 7, 8, 9, 10, 11, 12, 13, 14)
+    assert _BLOCK_ARGS.pack(1, 0, 64, 3, 64, 0.25, *range(6, 15)) == bytes(b)
 
 
 def view(p, B, H, n, D):
