@@ -1,0 +1,343 @@
+// The backward of the block norms; the mathematics is in block_join.cu.
+#include "block_join.cuh"
+
+namespace hla2 {
+namespace {
+
+struct JoinGrads {
+    const void *dr, *dh;
+    void *dx, *dy, *dgate;
+    float* partial;  // [partials][3][D]: post_weight, scale, next_weight
+    int partials;
+};
+
+template <typename T, int VEC, int NV, int TPR, int MAXT, int MODE>
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1)
+    join_backward_kernel(const hla2_block_args a, const JoinGrads g, int stages) {
+    extern __shared__ __align__(16) char ring_sm[];  // the ring; at the end, in a sub-warp mapping, [3][D] sums
+    __shared__ float red1[2][16][1], red2[2][16][2];
+    int turn1 = 0, turn2 = 0;
+    const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr, mine = threadIdx.x / tpr;
+    constexpr int per = TPR ? kSmallThreads / (TPR ? TPR : 1) : 1;
+    const int D = a.D;
+    const float inv_d = 1.f / (float)D;
+    constexpr bool has_y = MODE != kNormOnly;
+    const bool full = MODE == kAll || (MODE == kAny && a.gate && a.gate_cols != 1);
+    const bool scaled = MODE == kAll || (MODE == kAny && a.scale);
+    const bool has_dr = MODE == kAll || g.dr, has_dh = MODE != kAny || g.dh;
+    const bool silu = a.gate_act == HLA2_GATE_SILU;
+    const T *pw = static_cast<const T*>(a.post_weight) + t * VEC, *sc = static_cast<const T*>(a.scale) + t * VEC,
+            *nw = static_cast<const T*>(a.next_weight) + t * VEC;
+    // ring slots of the tensors that are there
+    int slots = 1;
+    const int ky = has_y ? slots++ : 0, kz = full ? slots++ : 0, kr = has_dr ? slots++ : 0, kh = has_dh ? slots++ : 0;
+    const Ring<T, VEC, NV> ring(ring_sm, slots);
+    float gp[NV][VEC], gs[NV][VEC], gn[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) gp[j][i] = gs[j][i] = gn[j][i] = 0.f;
+
+    const long long stride = (long long)gridDim.x * per, row_first = (long long)blockIdx.x * per + mine;
+    const T *xf = static_cast<const T*>(a.x) + row_first * a.x_stride + t * VEC,
+            *yf = static_cast<const T*>(a.y) + row_first * a.y_stride + t * VEC,
+            *zf = static_cast<const T*>(a.gate) + row_first * a.gate_stride + t * VEC;
+    const long long xs = stride * a.x_stride, ys = stride * a.y_stride, zs = stride * a.gate_stride;
+    long long left = row_first < a.rows ? (a.rows - 1 - row_first) / stride + 1 : 0;  // rows still to copy
+    long long af = row_first * D + t * VEC;
+    const int d_left = D - t * VEC;
+    auto fetch = [&](int stage) {
+        if (left > 0) {
+            --left;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = j * tpr * VEC;
+                if (c < d_left) {
+                    ring.copy(stage, 0, j, xf + c);
+                    if (has_y) ring.copy(stage, ky, j, yf + c);
+                    if (full) ring.copy(stage, kz, j, zf + c);
+                    if (has_dr) ring.copy(stage, kr, j, static_cast<const T*>(g.dr) + af + c);
+                    if (has_dh) ring.copy(stage, kh, j, static_cast<const T*>(g.dh) + af + c);
+                }
+            }
+            xf += xs;
+            if (has_y) yf += ys;
+            if (full) zf += zs;
+            af += stride * D;
+        }
+        cp_async_commit();
+    };
+    for (int i = 0; i + 1 < stages; ++i) fetch(i);
+    int stage = 0;
+    long long at = row_first * D + t * VEC;
+    for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows; row0 += stride, at += stride * D) {
+        const bool live = row0 + mine < a.rows;
+        const int cols = live ? d_left : 0;
+        fetch(stage == 0 ? stages - 1 : stage - 1);
+        float a_row = 1.f, slope_row = 0.f;
+        if (MODE == kAny && a.gate && !full && live)
+            a_row = gate_of(to_f32(static_cast<const T*>(a.gate)[(row0 + mine) * a.gate_stride]), silu, slope_row);
+        cp_async_wait_but(stages - 1);
+        float ny[NV][VEC], ga[NV][VEC], dz[NV][VEC], inv_y = 0.f;  // norm(y), scale act(gate), scale act'(gate) u
+        if (has_y) {
+            float s1[1] = {0.f};
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (j * tpr * VEC < cols) {
+                    ring.get(stage, ky, j, ny[j]);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) s1[0] += ny[j][i] * ny[j][i];
+                }
+            row_sum<TPR, 1>(s1, red1, turn1);
+            inv_y = rsqrtf(s1[0] * inv_d + a.eps);
+        }
+        // r again, sum r^2 and sum (dh w) r
+        float R[NV][VEC], s2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = j * tpr * VEC;
+            if (c < cols) {
+                ring.get(stage, 0, j, R[j]);
+                if (has_y) {
+                    float fz[VEC], fw[VEC];
+                    unpack(ldvec<T, VEC>(pw + c), fw);
+                    if (full) ring.get(stage, kz, j, fz);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        ny[j][i] *= inv_y;
+                        const float u = ny[j][i] * fw[i];
+                        float slope = 0.f;
+                        ga[j][i] = full ? gate_of(fz[i], silu, slope) : a_row;
+                        dz[j][i] = full ? slope * u : u;
+                    }
+                    if (scaled) {
+                        float fs[VEC];
+                        unpack(ldvec<T, VEC>(sc + c), fs);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) {
+                            R[j][i] = fmaf(fs[i] * ga[j][i], ny[j][i] * fw[i], R[j][i]);
+                            dz[j][i] *= fs[i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) R[j][i] = fmaf(ga[j][i], ny[j][i] * fw[i], R[j][i]);
+                    }
+                }
+                if (has_dh) {
+                    float fh[VEC], fn[VEC];
+                    ring.get(stage, kh, j, fh);
+                    unpack(ldvec<T, VEC>(nw + c), fn);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        s2[0] += R[j][i] * R[j][i];
+                        s2[1] += fh[i] * fn[i] * R[j][i];
+                    }
+                }
+            }
+        }
+        float inv_r = 0.f, dot = 0.f;
+        if (has_dh) {
+            row_sum<TPR, 2>(s2, red2, turn2);
+            inv_r = rsqrtf(s2[0] * inv_d + a.eps);
+            dot = s2[1] * inv_r * inv_d;
+        }
+        // the gradient of r; of the gate, the scale and y's norm
+        float s3[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = j * tpr * VEC;
+            if (c < cols) {
+                float fr[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) fr[i] = 0.f;
+                if (has_dr) ring.get(stage, kr, j, fr);
+                if (has_dh) {
+                    float f[VEC], fn[VEC];
+                    ring.get(stage, kh, j, f);
+                    unpack(ldvec<T, VEC>(nw + c), fn);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const float nr = R[j][i] * inv_r;
+                        gn[j][i] = fmaf(f[i], nr, gn[j][i]);
+                        fr[i] = fmaf(inv_r, fmaf(-nr, dot, f[i] * fn[i]), fr[i]);
+                    }
+                }
+                stvec<T, VEC>(static_cast<T*>(g.dx) + at + c, fr);
+                if (has_y) {
+                    float fw[VEC], fs[VEC];
+                    unpack(ldvec<T, VEC>(pw + c), fw);
+                    if (scaled) unpack(ldvec<T, VEC>(sc + c), fs);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const float rg = fr[i] * ga[j][i], v = rg * ny[j][i];
+                        gs[j][i] = fmaf(v, fw[i], gs[j][i]);
+                        gp[j][i] = scaled ? fmaf(v, fs[i], gp[j][i]) : gp[j][i] + v;
+                        dz[j][i] *= fr[i];
+                        R[j][i] = scaled ? rg * fs[i] * fw[i] : rg * fw[i];  // gradient of ny
+                        s3[0] = fmaf(R[j][i], ny[j][i], s3[0]);
+                        if (MODE == kAny) s3[1] += dz[j][i];
+                    }
+                    if (full) stvec<T, VEC>(static_cast<T*>(g.dgate) + at + c, dz[j]);
+                }
+            }
+        }
+        if (has_y) {
+            row_sum<TPR, 2>(s3, red2, turn2);
+            const float m = s3[0] * inv_d;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = j * tpr * VEC;
+                if (c < cols) {
+                    float o[VEC];
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) o[i] = inv_y * fmaf(-ny[j][i], m, R[j][i]);
+                    stvec<T, VEC>(static_cast<T*>(g.dy) + at + c, o);
+                }
+            }
+            if (MODE == kAny && a.gate && !full && live && t == 0)
+                static_cast<T*>(g.dgate)[row0 + mine] = from_f32<T>(s3[1] * slope_row);
+        }
+        stage = stage + 1 == stages ? 0 : stage + 1;
+    }
+    cp_async_wait_all();
+    // this CTA's partial sums: post_weight and scale with y, next_weight with dh
+    float* dst = g.partial + (size_t)blockIdx.x * 3 * D;
+    if (TPR) {  // the CTA's row groups one after another, so that the order is fixed
+        float* acc = reinterpret_cast<float*>(ring_sm);
+        for (int who = 0; who < per; ++who) {
+            __syncthreads();
+            if (mine == who) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const int c = (j * tpr + t) * VEC + i;
+                        if (c < D) {
+                            acc[c] = (who ? acc[c] : 0.f) + gp[j][i];
+                            acc[D + c] = (who ? acc[D + c] : 0.f) + gs[j][i];
+                            acc[2 * D + c] = (who ? acc[2 * D + c] : 0.f) + gn[j][i];
+                        }
+                    }
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < 3 * D; c += kSmallThreads) dst[c] = acc[c];
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int c = (j * tpr + t) * VEC + i;
+                if (c < D) {
+                    if (has_y) dst[c] = gp[j][i];
+                    if (scaled) dst[D + c] = gs[j][i];
+                    if (has_dh) dst[2 * D + c] = gn[j][i];
+                }
+            }
+    }
+}
+
+// Sums the partial rows: 32 columns a CTA, 32 row lanes, then a tree over them in a fixed order.
+__global__ void __launch_bounds__(1024) partial_sum_kernel(const float* __restrict__ partial, int partials, int D,
+                                                           float* __restrict__ d0, float* __restrict__ d1,
+                                                           float* __restrict__ d2) {
+    __shared__ float sm[32][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
+    float* dst = which == 0 ? d0 : which == 1 ? d1 : d2;
+    if (!dst) return;
+    float s = 0.f;
+    if (c < D) {
+        const float* src = partial + (size_t)which * D + c;
+        int p = w;
+        for (; p + 7 * 32 < partials; p += 8 * 32) {  // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = src[(size_t)(p + 32 * i) * 3 * D];
+            s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        }
+        for (; p < partials; p += 32) s += src[(size_t)p * 3 * D];
+    }
+    sm[w][lane] = s;
+    __syncthreads();
+    for (int o = 16; o; o >>= 1) {
+        if (w < o) sm[w][lane] += sm[w + o][lane];
+        __syncthreads();
+    }
+    if (w == 0 && c < D) dst[c] = sm[0][lane];
+}
+
+Work backward_work(const hla2_block_args* a, const Shape& s, int vec, int tensors) {
+    return work_of(a, s, vec, tensors, kBwdThreadsPerSm, s.tpr ? 3 * (size_t)a->D * sizeof(float) : 0);
+}
+
+}  // namespace
+}  // namespace hla2
+
+using namespace hla2;
+
+extern "C" {
+
+size_t hla2_block_join_backward_workspace_bytes(const hla2_block_args* a) {
+    if (check_join("hla2_block_join_backward_workspace_bytes", a) != HLA2_OK) return (size_t)-1;
+    join_ok();
+    size_t most = 0;
+    const int wide = a->dtype == HLA2_BF16 ? 8 : 4;
+    for (int vec : {1, 2, wide}) {  // whichever the addresses allow
+        for (int tensors = 2; tensors <= 5; ++tensors) {
+            const size_t c = (size_t)backward_work(a, shape_of(a->D, vec), vec, tensors).ctas;
+            if (c > most) most = c;
+        }
+    }
+    return most * 3 * (size_t)a->D * sizeof(float);
+}
+
+int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const void* dh, void* dx, void* dy, void* dgate,
+                             float* dpost_weight, float* dscale, float* dnext_weight, void* workspace,
+                             size_t workspace_bytes, hla2_stream_t stream) {
+    static const char* const fn = "hla2_block_join_backward";
+    if (int rc = check_join(fn, a)) return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const size_t es = a->dtype == HLA2_BF16 ? 2 : 4;
+    if ((has_y(a) && !dpost_weight) || (a->scale && !dscale) || (a->next_weight && !dnext_weight))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a weight's gradient is missing", fn);
+    if ((!has_y(a) && (dpost_weight || dy)) || (!a->scale && dscale) || (!a->next_weight && (dnext_weight || dh)) ||
+        (!a->gate && dgate))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient is asked for without its input", fn);
+    if (a->rows > 0) {
+        if (!dx || (a->y && !dy) || (a->gate && !dgate) || (a->next_weight && !dh) || (!dr && !dh))
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient of rows is missing", fn);
+        if (!al(dr, es) || !al(dh, es) || !al(dx, es) || !al(dy, es) || !al(dgate, es) || !al(dpost_weight, 4) ||
+            !al(dscale, 4) || !al(dnext_weight, 4))
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
+    }
+    const size_t need = hla2_block_join_backward_workspace_bytes(a);
+    if (need > 0 && (!workspace || workspace_bytes < need || !al(workspace, 16)))
+        return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, need);
+    JoinGrads g{dr, dh, dx, dy, dgate, static_cast<float*>(workspace), 0};
+    if (a->rows > 0) {
+        const void* outs[5] = {dr, dh, dx, dy, a->gate_cols != 1 ? dgate : nullptr};
+        const int vec = vec_of(a, outs, 5);
+        const Shape s = shape_of(a->D, vec);
+        const int tensors = 1 + (a->y ? 1 : 0) + (a->y && a->gate && a->gate_cols != 1 ? 1 : 0) + (dr ? 1 : 0) + (dh ? 1 : 0);
+        const Work w = backward_work(a, s, vec, tensors);
+        g.partials = w.ctas;
+        auto launch = [&](auto v, auto nv, auto tpr, auto maxt, auto mode, auto zero) {
+            using T = decltype(zero);
+            auto k = join_backward_kernel<T, decltype(v)::value, decltype(nv)::value, decltype(tpr)::value,
+                                          decltype(maxt)::value, decltype(mode)::value>;
+            if (!set_smem(k, w.smem)) return -1;
+            k<<<w.ctas, s.threads, w.smem, st>>>(*a, g, w.stages);
+            return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+        };
+        if (dispatch(a, mode_of(a, dr), vec, s, launch))
+            return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));
+    }
+    partial_sum_kernel<<<dim3((a->D + 31) / 32, 3), 1024, 0, st>>>(g.partial, g.partials, a->D, dpost_weight, dscale,
+                                                                   dnext_weight);
+    if (cudaPeekAtLastError() != cudaSuccess)
+        return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));
+    return join_ok();
+}
+
+}  // extern "C"

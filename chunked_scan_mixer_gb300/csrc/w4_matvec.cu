@@ -2,19 +2,22 @@
 // hla2_w4_matvec):  y[m, n] = sum_k x[m, k] (q[n, k] - z[n, k / group]) s[n, k / group] + bias[n].
 //
 // Bound by reading the weights: half a byte each.  The products run on mma.sync.m16n8k16 with 16
-// weight rows as A and up to eight columns of x as B, which turns the 4-bit values into operands at
-// one logic instruction a pair: (w >> 4 i) & 0x000f000f | 0x43004300 is the bf16 pair (128 + q_i, 128 +
-// q_{i+4}), and subtracting the pair (128 + z) is exact.  bf16 products are exact in float32,
-// so the only roundings are the float32 sums: one group of k is summed unscaled in the
-// accumulator, then scaled by the row's float32 scale and added.  A float32 x is split into three
-// bf16 columns (8 + 8 + 8 bits), summed at the end.
+// weight rows as A and up to eight columns of x as B, which turns the 4-bit values into operands at a
+// shift and a logic instruction a pair: (w << 3) & 0x00780078 | 0x41804180 is the bf16 pair
+// (16 + q_i, 16 + q_{i+4}), exactly.  One group of k is summed unscaled in float32, and
+//     sum (q - z) x = sum (16 + q) x - (16 + z) sum x,
+// with sum x from the same product with a row of ones: two instructions a group and column instead
+// of a subtraction a pair.  The cancellation costs a factor of about five of float32's rounding, far
+// below bf16's.  A float32 x takes the subtraction instead, exactly, and is split into three bf16
+// columns (8 + 8 + 8 bits) whose sums meet at the end.  The row's scale multiplies in float32.
 //
-// Within 32 values of k, lane (g, c) = (lane / 4, lane % 4) owns k = 8 c .. 8 c + 7 of rows g and g + 8:
-// one 32-bit word of each row.  The order of k inside a product is free as long as A and B agree; the
-// word's pairs are (k, k + 4), so x is paired the same way.
+// Within a group of G values of k, lane (g, c) = (lane / 4, lane % 4) owns k = c G / 4 ..
+// (c + 1) G / 4 - 1 of rows g and g + 8: one load of G / 8 bytes of each row, so a warp reads whole
+// 32-byte sectors from G = 64 on.  The order of k inside a product is free as long as A and B agree;
+// a word's pairs are (k, k + 4), and x is paired the same way.
 //
-// One CTA forms 16 outputs; its warps take every kWarps-th block of 128 k and the partial sums meet in
-// shared memory, in a fixed order.
+// A CTA forms 16 RT outputs; its eight warps take every eighth batch of k, the next batch's weights in
+// flight while one is computed, and their sums meet in shared memory in a fixed order.
 #include "common.cuh"
 
 namespace hla2 {
@@ -58,80 +61,210 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-template <typename T, int NT>
-__global__ void __launch_bounds__(kWarps * 32) w4_kernel(const W4Args a) {
-    constexpr int kPieces = sizeof(T) == 4 ? 3 : 1;
-    __shared__ float red[kWarps][16][NT * 8];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int n0 = blockIdx.x * 16;
-    const int r0 = min(n0 + g, a.N - 1), r1 = min(n0 + g + 8, a.N - 1);
-    const int gpr = a.K / a.group;
-    const uint8_t *w0 = a.w + (size_t)r0 * (a.K / 2), *w1 = a.w + (size_t)r1 * (a.K / 2);
-    const T *s0 = static_cast<const T*>(a.scales) + (size_t)r0 * gpr, *s1 = static_cast<const T*>(a.scales) + (size_t)r1 * gpr;
-    const uint8_t *z0 = a.zeros + (size_t)r0 * gpr, *z1 = a.zeros + (size_t)r1 * gpr;
-    const int cols = a.M * kPieces;
-    float sum[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) sum[t][0] = sum[t][1] = sum[t][2] = sum[t][3] = 0.f;
+// k per warp step: what a double buffer of a warp's weights takes of its registers
+__host__ __device__ constexpr int batch_of(int RT) { return RT == 2 ? 128 : 256; }
 
-    const int step = a.group;  // one group at a time, groups dealt out to the warps
-    for (int k0 = warp * step; k0 < a.K; k0 += kWarps * step) {
-        const int gi = k0 / a.group;
-        const float f0 = to_f32(s0[gi]), f1 = to_f32(s1[gi]);
-        const uint32_t q0 = 0x43004300u | (a.zeros ? z0[gi] * 0x00010001u : 0x00080008u);
-        const uint32_t q1 = 0x43004300u | (a.zeros ? z1[gi] * 0x00010001u : 0x00080008u);
-        float acc[NT][4];
+// U consecutive values of a row's scales or zero points
+template <typename T, int U>
+struct Few {
+    T v[U];
+};
+template <int B>
+struct Bytes;
+template <> struct Bytes<1> { using type = uint8_t; };
+template <> struct Bytes<2> { using type = uint16_t; };
+template <> struct Bytes<4> { using type = uint32_t; };
+template <> struct Bytes<8> { using type = uint2; };
+template <> struct Bytes<16> { using type = uint4; };
+template <typename T, int U>
+__device__ __forceinline__ void load_few(Few<T, U>& f, const T* p, int count, bool aligned) {
+    constexpr int kBytes = U * (int)sizeof(T);
+    if (aligned && count >= U) {
+        if constexpr (kBytes <= 16) {
+            using V = typename Bytes<kBytes>::type;
+            *reinterpret_cast<V*>(f.v) = *reinterpret_cast<const V*>(p);
+        } else {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-        for (int k = k0; k < k0 + step; k += 32) {
-            const uint32_t u0 = *reinterpret_cast<const uint32_t*>(w0 + k / 2 + 4 * c);
-            const uint32_t u1 = *reinterpret_cast<const uint32_t*>(w1 + k / 2 + 4 * c);
-            uint32_t a0[4], a1[4];
+            for (int i = 0; i < kBytes / 16; ++i)
+                reinterpret_cast<uint4*>(f.v)[i] = reinterpret_cast<const uint4*>(p)[i];
+        }
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a0[i] = sub2(((u0 >> (4 * i)) & 0x000f000fu) | 0x43004300u, q0);
-                a1[i] = sub2(((u1 >> (4 * i)) & 0x000f000fu) | 0x43004300u, q1);
-            }
-            const uint32_t A0[4] = {a0[0], a1[0], a0[1], a1[1]}, A1[4] = {a0[2], a1[2], a0[3], a1[3]};
+        for (int i = 0; i < U; ++i) f.v[i] = i < count ? p[i] : T{};
+    }
+}
+
+// What a warp reads of 16 RT rows for one batch
+template <typename T, int G, int RT>
+struct Weights {
+    static constexpr int U = batch_of(RT) / G, J = G / 32;  // groups, words of a row and group
+    uint32_t w[RT][2][U][J];
+    alignas(16) Few<T, U> s[RT][2];
+    alignas(16) Few<uint8_t, U> z[RT][2];
+};
+
+template <typename T, int NT, int G, int RT>
+__global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const W4Args a, const bool aligned) {
+    constexpr int kPieces = sizeof(T) == 4 ? 3 : 1, U = batch_of(RT) / G, J = G / 32, kBatch = batch_of(RT);
+    __shared__ float red[kWarps][16 * RT][NT * 8 + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int n0 = blockIdx.x * 16 * RT, gpr = a.K / G;
+    const T* scales = static_cast<const T*>(a.scales);
+    int row[RT][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int col = t * 8 + g;
-                uint32_t b[4] = {0u, 0u, 0u, 0u};
-                if (col < cols) {
-                    const T* xp = static_cast<const T*>(a.x) + (col / kPieces) * a.x_stride + k + 8 * c;
-                    if constexpr (kPieces == 1) {
-                        pair_x(*reinterpret_cast<const uint4*>(xp), b);
+    for (int t = 0; t < RT; ++t) {
+        row[t][0] = min(n0 + 16 * t + g, a.N - 1);
+        row[t][1] = min(n0 + 16 * t + g + 8, a.N - 1);
+    }
+    const int cols = a.M * kPieces;
+    float sum[RT][NT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sum[r][t][0] = sum[r][t][1] = sum[r][t][2] = sum[r][t][3] = 0.f;
+
+    auto load = [&](Weights<T, G, RT>& b, int k0) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t* p = a.w + (size_t)row[r][h] * (a.K / 2) + (k0 + c * (G / 4)) / 2;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool in = k0 + u * G < a.K;
+                    if constexpr (J == 4) {
+                        const uint4 v = in ? __ldcs(reinterpret_cast<const uint4*>(p + u * G / 2)) : make_uint4(0, 0, 0, 0);
+                        b.w[r][h][u][0] = v.x, b.w[r][h][u][1] = v.y, b.w[r][h][u][2] = v.z, b.w[r][h][u][3] = v.w;
+                    } else if constexpr (J == 2) {
+                        const uint2 v = in ? __ldcs(reinterpret_cast<const uint2*>(p + u * G / 2)) : make_uint2(0, 0);
+                        b.w[r][h][u][0] = v.x, b.w[r][h][u][1] = v.y;
                     } else {
-                        const float4 l = *reinterpret_cast<const float4*>(xp), h = *reinterpret_cast<const float4*>(xp + 4);
-                        const int p = col % 3;
-                        b[0] = pack_bf16x2(piece(l.x, p), piece(h.x, p));
-                        b[1] = pack_bf16x2(piece(l.y, p), piece(h.y, p));
-                        b[2] = pack_bf16x2(piece(l.z, p), piece(h.z, p));
-                        b[3] = pack_bf16x2(piece(l.w, p), piece(h.w, p));
+                        b.w[r][h][u][0] = in ? __ldcs(reinterpret_cast<const uint32_t*>(p + u * G / 2)) : 0u;
                     }
                 }
-                mma_16816(acc[t], A0, b[0], b[1]);
-                mma_16816(acc[t], A1, b[2], b[3]);
+                const size_t at = (size_t)row[r][h] * gpr + k0 / G;
+                const int count = min(U, gpr - k0 / G);
+                load_few<T, U>(b.s[r][h], scales + at, count, aligned);
+                if (a.zeros) load_few<uint8_t, U>(b.z[r][h], a.zeros + at, count, aligned);
+            }
+    };
+    auto compute = [&](const Weights<T, G, RT>& b, int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k0 + u * G >= a.K) break;
+            float acc[RT][NT][4], xs[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                xs[t][0] = xs[t][1] = xs[t][2] = xs[t][3] = 0.f;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) acc[r][t][0] = acc[r][t][1] = acc[r][t][2] = acc[r][t][3] = 0.f;
+            }
+            float zf[RT][2];
+            uint32_t zz[RT][2];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t z = a.zeros ? b.z[r][h].v[u] : 8u;
+                    zf[r][h] = (float)(16u + z);
+                    zz[r][h] = 0x41804180u | (z * 0x00080008u);
+                }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                uint32_t x[NT][4];
+                const int k = k0 + u * G + c * (G / 4) + 8 * j;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int col = t * 8 + g;
+                    x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0u;
+                    if (col < cols) {
+                        const T* xp = static_cast<const T*>(a.x) + (col / kPieces) * a.x_stride + k;
+                        if constexpr (kPieces == 1) {
+                            pair_x(*reinterpret_cast<const uint4*>(xp), x[t]);
+                        } else {
+                            const float4 l = *reinterpret_cast<const float4*>(xp), h = *reinterpret_cast<const float4*>(xp + 4);
+                            const int p = col % 3;
+                            x[t][0] = pack_bf16x2(piece(l.x, p), piece(h.x, p));
+                            x[t][1] = pack_bf16x2(piece(l.y, p), piece(h.y, p));
+                            x[t][2] = pack_bf16x2(piece(l.z, p), piece(h.z, p));
+                            x[t][3] = pack_bf16x2(piece(l.w, p), piece(h.w, p));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    uint32_t q[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t w = b.w[r][h][u][j];
+                        q[h][0] = ((w << 3) & 0x00780078u) | 0x41804180u;
+                        q[h][1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
+                        q[h][2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
+                        q[h][3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+                        if (kPieces == 3)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) q[h][i] = sub2(q[h][i], zz[r][h]);
+                    }
+                    const uint32_t A0[4] = {q[0][0], q[1][0], q[0][1], q[1][1]}, A1[4] = {q[0][2], q[1][2], q[0][3], q[1][3]};
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        mma_16816(acc[r][t], A0, x[t][0], x[t][1]);
+                        mma_16816(acc[r][t], A1, x[t][2], x[t][3]);
+                    }
+                }
+                if (kPieces == 1) {
+                    const uint32_t one[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        mma_16816(xs[t], one, x[t][0], x[t][1]);
+                        mma_16816(xs[t], one, x[t][2], x[t][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const float f0 = to_f32(b.s[r][0].v[u]), f1 = to_f32(b.s[r][1].v[u]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (kPieces == 1) {
+                        acc[r][t][0] = fmaf(-zf[r][0], xs[t][0], acc[r][t][0]);
+                        acc[r][t][1] = fmaf(-zf[r][0], xs[t][1], acc[r][t][1]);
+                        acc[r][t][2] = fmaf(-zf[r][1], xs[t][0], acc[r][t][2]);
+                        acc[r][t][3] = fmaf(-zf[r][1], xs[t][1], acc[r][t][3]);
+                    }
+                    sum[r][t][0] = fmaf(f0, acc[r][t][0], sum[r][t][0]);
+                    sum[r][t][1] = fmaf(f0, acc[r][t][1], sum[r][t][1]);
+                    sum[r][t][2] = fmaf(f1, acc[r][t][2], sum[r][t][2]);
+                    sum[r][t][3] = fmaf(f1, acc[r][t][3], sum[r][t][3]);
+                }
             }
         }
+    };
+    Weights<T, G, RT> b0, b1;
+    const int step = kWarps * kBatch;
+    int k0 = warp * kBatch;
+    if (k0 < a.K) load(b0, k0);
+    for (; k0 < a.K; k0 += 2 * step) {
+        if (k0 + step < a.K) load(b1, k0 + step);
+        compute(b0, k0);
+        if (k0 + step >= a.K) break;
+        if (k0 + 2 * step < a.K) load(b0, k0 + 2 * step);
+        compute(b1, k0 + step);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            sum[t][0] = fmaf(f0, acc[t][0], sum[t][0]);
-            sum[t][1] = fmaf(f0, acc[t][1], sum[t][1]);
-            sum[t][2] = fmaf(f1, acc[t][2], sum[t][2]);
-            sum[t][3] = fmaf(f1, acc[t][3], sum[t][3]);
+            float* p = &red[warp][16 * r + g][t * 8 + 2 * c];
+            p[0] = sum[r][t][0];
+            p[1] = sum[r][t][1];
+            p = &red[warp][16 * r + g + 8][t * 8 + 2 * c];
+            p[0] = sum[r][t][2];
+            p[1] = sum[r][t][3];
         }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        red[warp][g][t * 8 + 2 * c] = sum[t][0];
-        red[warp][g][t * 8 + 2 * c + 1] = sum[t][1];
-        red[warp][g + 8][t * 8 + 2 * c] = sum[t][2];
-        red[warp][g + 8][t * 8 + 2 * c + 1] = sum[t][3];
-    }
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * a.M; e += kWarps * 32) {
-        const int r = e & 15, m = e >> 4;
+    for (int e = threadIdx.x; e < 16 * RT * a.M; e += kWarps * 32) {
+        const int r = e % (16 * RT), m = e / (16 * RT);
         if (n0 + r >= a.N) continue;
         float t = 0.f;
 #pragma unroll
@@ -142,10 +275,25 @@ __global__ void __launch_bounds__(kWarps * 32) w4_kernel(const W4Args a) {
     }
 }
 
+template <typename T, int NT, int G>
+int launch_w4_g(const W4Args& a, cudaStream_t st) {
+    const bool aligned = (a.K / G) % (256 / G) == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 15u) == 0 &&
+                         (reinterpret_cast<uintptr_t>(a.zeros) & 15u) == 0;
+    // 32 rows share x's loads and pairing; 16 fill the GPU sooner.  float32 x (up to six columns of
+    // eight) has no registers for 32.
+    if (NT <= 2 && sizeof(T) == 2 && (a.N + 31) / 32 >= 2 * 152)
+        w4_kernel<T, NT, G, (NT <= 2 && sizeof(T) == 2) ? 2 : 1><<<(a.N + 31) / 32, kWarps * 32, 0, st>>>(a, aligned);
+    else
+        w4_kernel<T, NT, G, 1><<<(a.N + 15) / 16, kWarps * 32, 0, st>>>(a, aligned);
+    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
 template <typename T, int NT>
 int launch_w4(const W4Args& a, cudaStream_t st) {
-    w4_kernel<T, NT><<<(a.N + 15) / 16, kWarps * 32, 0, st>>>(a);
-    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+    switch (a.group) {
+        case 32: return launch_w4_g<T, NT, 32>(a, st);
+        case 64: return launch_w4_g<T, NT, 64>(a, st);
+        default: return launch_w4_g<T, NT, 128>(a, st);
+    }
 }
 
 int w4_ok() { return set_last_error(HLA2_OK, "%s", ""); }
@@ -182,14 +330,8 @@ extern "C" int hla2_w4_matvec(const void* x, long long x_stride, const void* qwe
     if (dtype == HLA2_BF16) {
         rc = M <= 8 ? launch_w4<bf16, 1>(a, st) : launch_w4<bf16, 2>(a, st);
     } else {
-        switch ((3 * M + 7) / 8) {
-            case 1: rc = launch_w4<float, 1>(a, st); break;
-            case 2: rc = launch_w4<float, 2>(a, st); break;
-            case 3: rc = launch_w4<float, 3>(a, st); break;
-            case 4: rc = launch_w4<float, 4>(a, st); break;
-            case 5: rc = launch_w4<float, 5>(a, st); break;
-            default: rc = launch_w4<float, 6>(a, st); break;
-        }
+        rc = M <= 2 ? launch_w4<float, 1>(a, st) : M <= 5 ? launch_w4<float, 2>(a, st)
+             : M <= 8 ? launch_w4<float, 3>(a, st) : launch_w4<float, 6>(a, st);
     }
     if (rc) return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));
     return w4_ok();
