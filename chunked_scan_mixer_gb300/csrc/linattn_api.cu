@@ -92,7 +92,8 @@ struct LinPlan {
 
 // Segments per state head.  Unit: the time of one chunk of the output pass.  More than one segment
 // adds the summary pass (about half of the output pass: it reads two of four tensors) and about two
-// chunks' time for the scan and its launch; the waves of CTAs count whole.
+// chunks' time for the scan and its launch.  The waves of CTAs count whole, each with about two chunks'
+// time to start and to end.
 LinPlan lin_plan(const hla2_linattn_args* a, int W, int slots) {
     LinPlan p{W, (a->n + W - 1) / W, 0, 0};
     const long long heads = (long long)a->B * a->Hk;
@@ -106,7 +107,7 @@ LinPlan lin_plan(const hla2_linattn_args* a, int W, int slots) {
         if (want > 4096) want = 4096;
         const int sc = (int)((p.nchunks + want - 1) / want), ns = (p.nchunks + sc - 1) / sc;
         const long long waves = (heads * ns + slots - 1) / slots;
-        const double cost = (double)waves * sc * (ns > 1 ? 1.5 : 1.0) + (ns > 1 ? 2.0 : 0.0);
+        const double cost = (double)waves * (sc + 2) * (ns > 1 ? 1.5 : 1.0) + (ns > 1 ? 2.0 : 0.0);
         if (p.nseg == 0 || cost < best) best = cost, p.seg_chunks = sc, p.nseg = ns;
     }
     return p;

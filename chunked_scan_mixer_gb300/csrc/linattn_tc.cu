@@ -25,10 +25,22 @@
 // and the state are loaded and formed once per chunk for all its items; with rk > 1 X, Y and the state
 // are, and Y and dSig accumulate over the items in tensor memory.
 //
-// Roles (512 threads, one CTA per SM): warp 0 allocates tensor memory and one thread issues every
-// MMA; warp 1 issues the loads, warp 2 the stores; warps 4..7 (A: one row per thread) run EPI-1, EPI-C and
-// EPI-Y; warps 8..15 (B) run KT and EPI-S.  The chains A and B only meet in Sig~.  Every wait is
-// bounded; one that gives up records its site in the status word, and every role drains.
+// Roles (640 threads, one CTA per SM): warp 0 allocates tensor memory and issues MMA-G, MMA-C and
+// MMA-Y, warp 3 MMA-S; warp 1 issues the loads, warp 2 the stores; warps 4..11 (A: a row and half
+// of its columns per thread) run EPI-1, EPI-C and EPI-Y, the next item's EPI-1 while this one's MMA-Y
+// runs; warps 12..19 (B) run KT and EPI-S.  The chains A and B only meet in Sig~.
+//
+// What a hand-over costs decides the time of a chunk (measured, in SM cycles: issuing one MMA 49, a
+// commit 52, a wait on an mbarrier whose phase is already complete 45 to 90 and twice that while
+// sixteen warps poll, a named barrier 16).  So: threads meet in named barriers; only commits and copies
+// signal mbarriers, which one lane of one warp of A or of B polls for its group; a commit is made where
+// someone waits for it, and slots are released by the epilogue that saw the commit.  Every poll is
+// bounded; one that gives up records its site in the status word, and every role runs on to its
+// end without waiting (each meets the same named barriers on any path).
+//
+// The loops are kept short on purpose.  The roles run different code side by side, straight through it once a
+// chunk, so together they have to fit the SM's instruction cache: fully unrolled they took
+// 102 KB, half of all instruction fetches missed, and the epilogues ran at 20 cycles an instruction.
 //
 // D = 64 stacks the two key pieces as one 128-row A operand (rows 0..63 the high piece's
 // features, 64..127 the low one's), so MMA-S has full height; the two halves of the state stay
@@ -43,8 +55,8 @@ namespace {
 namespace lt {
 
 constexpr int kW = 128;
-constexpr int kThreads = 512;
-constexpr int kA0 = 4, kAWarps = 4, kB0 = 8, kBWarps = 8;
+constexpr int kThreads = 640;
+constexpr int kA0 = 4, kAWarps = 8, kB0 = 12, kBWarps = 8;
 constexpr uint32_t kBlk = la_common::kBlk;  // [128 rows][64 bf16]
 
 struct Maps {
@@ -63,11 +75,9 @@ __device__ __forceinline__ void store_4d(const CUtensorMap* m, const void* src, 
                  : "memory");
 }
 
-// Wait for the phase of the given parity.  The waiting warp is suspended in hardware between
-// polls (it has others to leave the issue slots to); after about two seconds it gives up.
+// Wait of one thread for the phase of the given parity; after about two seconds it gives up.
 constexpr long long kWaitClocks = 4LL * 1000 * 1000 * 1000;
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int where) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int where) {
     const long long t0 = clock64();
     while (!tc::mbar_try_wait(bar, parity)) {
         if (*abort) return false;
@@ -79,29 +89,44 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     }
     return true;
 }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int where) {
+    return tc::mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, status, where);
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Named barriers (0 is __syncthreads)
+enum { kNbGT = 5, kNbKT = 7, kNbSP = 8, kNbYR = 9, kNbVZ = 10, kNbA = 12, kNbB = 13 };
 
 template <int D>
 struct Out {  // shared memory of the output kernel
     static constexpr uint32_t kTile = (uint32_t)(D / 64) * kBlk;
-    static constexpr int NX = D == 64 ? 3 : 2, NK = D == 64 ? 3 : 2, NV = D == 64 ? 3 : 1;
+    static constexpr int NX = D == 64 ? 4 : 2, NK = NX, NV = D == 64 ? 4 : 1;
     static constexpr uint32_t oX = 0, oK = oX + NX * kTile, oV = oK + NK * kTile, oM = oV + NV * kTile, oS = oM + kTile;
-    static constexpr uint32_t oGp = oS + kTile;          // g^0 .. g^128
-    static constexpr uint32_t oT = oGp + 528;            // g^(31 - j) (reverse g^j), j = 0 .. 31
-    static constexpr uint32_t oBar = oT + 128;
+    static constexpr uint32_t oGp = oS + kTile;          // 128 zeros, then g^0 .. g^128
+    static constexpr uint32_t oBar = oGp + 4 * 260;
     enum {
-        XF = 0, XE = XF + NX, OS = XE + NX, KF = OS + NX, KE = KF + NK, VF = KE + NK, VE = VF + NV, VZ = VE + NV,
-        BG = VZ + NV, BGK = BG + 2, GT = BGK + 2, KT = GT + 2, BC, YD, YR, SD, SP, ME, kBars
+        XF = 0, XE = XF + NX, OS = XE + NX, KF = OS + NX, VF = KF + NK, E = VF + NV, BG = E + NK, BGK = BG + 4, BC, YL, YD,
+        YI, SD, kBars
     };
     static constexpr uint32_t oMisc = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oMisc + 16 + 1024;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
-// Tensor memory columns of the output kernel: two Gram regions, Y, dSig.
+// Tensor memory columns of the output kernel: two Gram regions, Y (two regions where they fit), dSig.
 template <int D>
 struct Cols {
+    static constexpr int NY = D == 64 ? 2 : 1;
     __device__ static constexpr uint32_t G(int i) { return (uint32_t)(i & 1) * 128; }
-    static constexpr uint32_t Y = 256, S = Y + D;
+    __device__ static constexpr uint32_t Y(int g) { return 256 + (uint32_t)(g % NY) * D; }
+    static constexpr uint32_t S = 256 + NY * D;
 };
 
 struct Where {  // the CTA's state head, segment and valid chunks
@@ -117,6 +142,9 @@ __device__ __forceinline__ Where locate(const LinPass& a) {
     const int end = min(w.c0 + a.seg_chunks, a.nchunks);
     w.c1 = min(end, (w.len + kW - 1) / kW);
     w.nit = max(0, w.c1 - w.c0);
+    w.len = uniform(w.len);
+    w.c1 = uniform(w.c1);
+    w.nit = uniform(w.nit);
     return w;
 }
 
@@ -161,16 +189,15 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
     constexpr int kBlocks = D / 64;
     constexpr int kSC = D / 2;  // state columns per B thread
     extern __shared__ unsigned char smem_raw[];
-    unsigned char* sm =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* gp = reinterpret_cast<float*>(sm + L::oGp);
-    float* tt = reinterpret_cast<float*>(sm + L::oT);
+    // an offset, not a rounded pointer: the compiler then still knows the address space
+    unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float* gp = reinterpret_cast<float*>(sm + L::oGp) + kW;  // gp[distance]; 0 for a negative one
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + L::oMisc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::oMisc + 4);
     int* status = a.status;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = lt::uniform(tid >> 5), lane = tid & 31;
     const lt::Where w = lt::locate(a);
     const bool rev = a.rev != 0, mode_a = a.rx > 1, mode_b = a.rk > 1;
     const int items = mode_a ? a.rx : a.rk, total = w.nit * items;
@@ -188,13 +215,12 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
     }
     if (w.nit == 0) return;
 
-    for (int i = tid; i <= kW; i += lt::kThreads) gp[i] = pow_decay(log2g, (float)i);
-    if (tid < 32) tt[tid] = pow_decay(log2g, (float)(rev ? tid : 31 - tid));
+    if (tid < 2 * kW + 1) gp[tid - kW] = tid < kW ? 0.f : pow_decay(log2g, (float)(tid - kW));
     if (tid == 0) {
         for (int i = 0; i < L::kBars; ++i) {
-            const bool by_a = (i >= L::OS && i < L::OS + L::NX) || i == L::GT || i == L::GT + 1 || i == L::YR;
-            const bool by_b = (i >= L::VZ && i < L::VZ + L::NV) || i == L::KT || i == L::SP;
-            tc::mbar_init(&bars[i], by_a ? lt::kAWarps : by_b ? lt::kBWarps : 1);
+            const bool by_a = i >= L::OS && i < L::OS + L::NX;   // one arrival per A warp
+            const bool by_two = i >= L::E && i < L::E + L::NK;   // A (or MMA-Y's commit) and B
+            tc::mbar_init(&bars[i], by_a ? lt::kAWarps : by_two ? 2 : 1);
         }
         *abort = 0;
         tc::mbar_fence_init();
@@ -211,14 +237,15 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
             *reinterpret_cast<uint4*>(sm + L::oS + la_off(sc0 / 64, sr, (sc0 % 64) / 8 + j)) = la_pack8(&sig[8 * j]);
     };
     if (warp >= lt::kB0) {
+        // D = 64: dx <= 64, so only the high half takes the carry
+        const bool has = a.carry && sr < a.dx;
+        const float* src = a.carry + ((size_t)w.bs * a.nseg + blockIdx.y) * a.dx * a.dy +
+                           (a.carry_t ? sc0 * a.dx + sr : sr * a.dy + sc0);
+        const int step = a.carry_t ? a.dx : 1;
 #pragma unroll
-        for (int j = 0; j < kSC; ++j) sig[j] = 0.f;
-        if (a.carry && sr < a.dx) {  // D = 64: dx <= 64, so only the high half takes it
-            const float* src = a.carry + ((size_t)w.bs * a.nseg + blockIdx.y) * a.dx * a.dy;
-#pragma unroll
-            for (int j = 0; j < kSC; ++j)
-                if (sc0 + j < a.dy)
-                    sig[j] = a.carry_t ? src[(size_t)(sc0 + j) * a.dx + sr] : src[(size_t)sr * a.dy + sc0 + j];
+        for (int j = 0; j < kSC; ++j) {
+            sig[j] = has && sc0 + (j & ~15) < a.dy ? *src : 0.f;  // dy is a multiple of 16
+            src += step;
         }
         publish();
         tc::fence_proxy_async();
@@ -226,147 +253,165 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = (uint32_t)lt::uniform((int)*tmem_holder);
     auto chunk_of = [&](int ci) { return rev ? w.c1 - 1 - ci : w.c0 + ci; };
     auto valid_of = [&](int ci) { return min(kW, w.len - chunk_of(ci) * kW); };
     volatile int never = 0;
 
+    constexpr int kAThreads = 32 * lt::kAWarps, kBThreads = 32 * lt::kBWarps;
+    constexpr uint32_t T = L::kTile >> 4;    // descriptor units (16 bytes): a slot, and 16 rows MN-major
+    constexpr uint64_t kMK = 2048 >> 4;
+    auto kstep = [](int ks) { return (uint64_t)(((ks >> 2) * lt::kBlk + (ks & 3) * 32) >> 4); };  // K-major
+
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------------------------- MMA issue
-            constexpr uint32_t I_G = tc::idesc_bf16(128, 128, 0, 0), I_C = tc::idesc_bf16(128, D, 0, 1),
-                               I_Y = tc::idesc_bf16(128, D, 0, 1), I_S = tc::idesc_bf16(128, D, 1, 1);
-            const uint32_t sX = smem_u32(sm + L::oX), sK = smem_u32(sm + L::oK), sV = smem_u32(sm + L::oV),
-                           sM = smem_u32(sm + L::oM), sS = smem_u32(sm + L::oS);
-            auto x_of = [&](int it) { return mode_b ? it / items : it; };
-            auto kv_of = [&](int it) { return mode_b ? it : it / items; };
-            auto issue_g = [&](int it) {
-                const int r = it % items, xi = x_of(it), ki = kv_of(it), xs = xi % L::NX, ks_ = ki % L::NK;
-                if (!mode_b || r == 0) lt::wait(&bars[L::XF + xs], (xi / L::NX) & 1, abort, status, 301);
-                if (!mode_a || r == 0) lt::wait(&bars[L::KF + ks_], (ki / L::NK) & 1, abort, status, 302);
-                tc::fence_after_sync();
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc::mma_ss(tmem + C::G(it), lt::kdesc(sX + xs * L::kTile, ks), lt::kdesc(sK + ks_ * L::kTile, ks), I_G,
-                               ks > 0);
-                tc::mma_commit(&bars[L::BG + (it & 1)]);
-                if (!mode_a || r == items - 1) tc::mma_commit(&bars[L::BGK + (ki & 1)]);
-            };
-            issue_g(0);
-            int groups = 0;  // Y regions begun
-            for (int it = 0; it < total; ++it) {
-                const int r = it % items, ci = it / items, xi = x_of(it), ki = kv_of(it);
-                const int vs = ki % L::NV, ks_ = ki % L::NK;
-                const bool first = r == 0, last = r == items - 1;
-                const bool new_y = !mode_b || first, end_y = !mode_b || last;
-                const bool state_now = (!mode_a || last) && ci + 1 < w.nit;
-                if (new_y) {
-                    if (first && ci > 0) lt::wait(&bars[L::SP], (ci - 1) & 1, abort, status, 303);
-                    if (groups > 0) lt::wait(&bars[L::YR], (groups - 1) & 1, abort, status, 304);
+        // ----------------------------------------------------------- MMA-G, MMA-C, MMA-Y
+        constexpr uint32_t I_G = tc::idesc_bf16(128, 128, 0, 0), I_Y = tc::idesc_bf16(128, D, 0, 1);
+        const uint64_t dX = lt::kdesc(smem_u32(sm + L::oX), 0), dK = lt::kdesc(smem_u32(sm + L::oK), 0),
+                       dV = lt::mdesc(smem_u32(sm + L::oV), 0), dS = lt::mdesc(smem_u32(sm + L::oS), 0);
+        int groups = 0;  // Y regions begun
+        int r = -1, ci = 0;
+#pragma unroll 1
+        for (int it = -1; it < total; ++it) {
+            // item it = (chunk ci, r); -1: only the first Gram
+            const bool first = r == 0, last = r == items - 1;
+            const bool new_y = it >= 0 && (!mode_b || first), end_y = !mode_b || last;
+            const int ki = it < 0 ? 0 : mode_b ? it : ci, vs = ki % L::NV;
+            __syncwarp();
+            if (new_y) {
+                if (first && ci > 0) tc::named_bar(lt::kNbSP, kBThreads + 32);
+                // With two Y regions the last reading of this one is over: A met kNbGT for the item before.
+                if (C::NY == 1 && groups > 0) tc::named_bar(lt::kNbYR, kAThreads + 32);
+                if (lane == 0) {
                     tc::fence_after_sync();
-                    ++groups;
-                    const uint32_t x = sX + (xi % L::NX) * L::kTile;
+                    const uint64_t x = dX + (groups % L::NX) * T;  // one x tile a group
+#pragma unroll
                     for (int ks = 0; ks < 8; ++ks)  // D = 64: the two halves of the state in turn
-                        tc::mma_ss(tmem + C::Y, lt::kdesc(x, D == 64 ? ks & 3 : ks), lt::mdesc(sS, ks), I_C, ks > 0);
+                        tc::mma_ss(tmem + C::Y(groups), x + kstep(D == 64 ? ks & 3 : ks), dS + ks * kMK, I_Y, ks > 0);
                     tc::mma_commit(&bars[L::BC]);
+                    if (mode_a && last) tc::mma_commit(&bars[L::YL]);
                 }
-                // The next Gram overwrites the region that MMA-Y of the item before this one read: done with
-                // the wait for YR above, else (the later items of a chunk) by that item's own commit.
-                if (mode_b && !first)
-                    lt::wait(&bars[L::KE + (it - 1) % L::NK], ((it - 1) / L::NK) & 1, abort, status, 308);
-                if (it + 1 < total) issue_g(it + 1);
-                if (!mode_a || first) {
-                    lt::wait(&bars[L::VF + vs], (ki / L::NV) & 1, abort, status, 305);
-                    if (a.lengths) lt::wait(&bars[L::VZ + vs], (ki / L::NV) & 1, abort, status, 306);
-                }
-                bool y_done = false, s_done = !state_now;
-                const uint32_t v = sV + vs * L::kTile;
-                const long long t0 = clock64();
-                while (!y_done || !s_done) {
-                    if (!y_done && tc::mbar_test_wait(&bars[L::GT + (it & 1)], (it >> 1) & 1)) {
-                        tc::fence_after_sync();
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc::mma_ts(tmem + C::Y, tmem + C::G(it) + 8 * ks, lt::mdesc(v, ks), I_Y, 1);
-                        if (end_y) tc::mma_commit(&bars[L::YD]);
-                        y_done = true;
+                ++groups;
+            }
+            if (lane == 0 && it + 1 < total) {  // MMA-G: takes the region that MMA-Y of it - 1 read
+                if (it > 0) lt::wait(&bars[mode_b ? L::YI : L::YD], (it - 1) & 1, abort, status, 308);
+                const bool wrap = last || it < 0;  // the next item begins a chunk
+                const int rn = wrap ? 0 : r + 1, cn = it < 0 ? 0 : ci + (last ? 1 : 0);
+                const int xi = mode_b ? cn : it + 1, kn = mode_a ? cn : it + 1;
+                if (!mode_b || rn == 0) lt::wait(&bars[L::XF + xi % L::NX], (xi / L::NX) & 1, abort, status, 301);
+                if (!mode_a || rn == 0) lt::wait(&bars[L::KF + kn % L::NK], (kn / L::NK) & 1, abort, status, 302);
+                tc::fence_after_sync();
+                const uint64_t x = dX + (xi % L::NX) * T, k = dK + (kn % L::NK) * T;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc::mma_ss(tmem + C::G(it + 1), x + kstep(ks), k + kstep(ks), I_G, ks > 0);
+                tc::mma_commit(&bars[L::BG + ((it + 1) & 3)]);  // four: B may be three tiles behind
+                if (mode_a && rn == items - 1) tc::mma_commit(&bars[L::BGK]);
+            }
+            if (it >= 0) {
+                if (lane == 0 && (!mode_a || first)) lt::wait(&bars[L::VF + vs], (ki / L::NV) & 1, abort, status, 305);
+                __syncwarp();
+                if (a.lengths && (!mode_a || first)) tc::named_bar(lt::kNbVZ + (ki & 1), kBThreads + 64);
+                tc::named_bar(lt::kNbGT + (it & 1), kAThreads + 32);
+                if (lane == 0) {
+                    tc::fence_after_sync();
+                    const uint64_t v = dV + vs * T;
+                    const uint32_t ty = tmem + C::Y(groups - 1), tg = tmem + C::G(it);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)  // G~: columns 0..63 of the rows' Gram in its first 32, the rest from 64 on
+                        tc::mma_ts(ty, tg + 8 * (ks & 3) + (ks >> 2) * 64, v + ks * kMK, I_Y, 1);
+                    if (end_y) tc::mma_commit(&bars[L::YD]);
+                    if (mode_b) {
+                        tc::mma_commit(&bars[L::E + ki % L::NK]);
+                        tc::mma_commit(&bars[L::YI]);
                     }
-                    if (!s_done && tc::mbar_test_wait(&bars[L::KT], ki & 1)) {
-                        tc::fence_after_sync();
-                        const uint32_t k = sK + ks_ * L::kTile, acc = mode_b && !first;
-                        if (D == 64) {
-                            for (int ks = 0; ks < 8; ++ks)
-                                tc::mma_ss(tmem + C::S, lt::mdesc(k, ks, sM - k), lt::mdesc(v, ks), I_S, acc || ks > 0);
-                        } else {
-                            for (int ks = 0; ks < 8; ++ks)
-                                tc::mma_ss(tmem + C::S, lt::mdesc(k, ks), lt::mdesc(v, ks), I_S, acc || ks > 0);
-                            for (int ks = 0; ks < 8; ++ks)
-                                tc::mma_ss(tmem + C::S, lt::mdesc(sM, ks), lt::mdesc(v, ks), I_S, 1);
-                        }
-                        tc::mma_commit(&bars[L::ME]);
-                        if (last) tc::mma_commit(&bars[L::SD]);
-                        s_done = true;
-                    }
-                    if (*abort) break;
-                    if (clock64() - t0 > lt::kWaitClocks) {
-                        *abort = 1;
-                        if (status) atomicCAS(status, 0, 307);
-                        break;
-                    }
-                }
-                if (!mode_a || last) {  // the keys and values have been read
-                    tc::mma_commit(&bars[L::KE + ks_]);
-                    tc::mma_commit(&bars[L::VE + vs]);
                 }
             }
-            // drain: the last commit covers every MMA before it
-            const int kl = kv_of(total - 1);
-            lt::wait(&bars[L::VE + kl % L::NV], (kl / L::NV) & 1, &never, nullptr, 0);
+            if (++r == items) r = 0, ++ci;
+            if (it < 0) r = 0, ci = 0;
         }
+        // drain: the last commit covers every MMA of this thread
+        if (lane == 0) lt::wait(&bars[mode_b ? L::YI : L::YD], (total - 1) & 1, &never, nullptr, 0);
+    } else if (warp == 3) {
+        // --------------------------------------------------------------------------- MMA-S
+        constexpr uint32_t I_S = tc::idesc_bf16(128, D, 1, 1);
+        const uint32_t sK = smem_u32(sm + L::oK), sM = smem_u32(sm + L::oM);
+        const uint64_t dK = lt::mdesc(sK, 0, D == 64 ? sM - sK : lt::kBlk), dM = lt::mdesc(sM, 0),
+                       dV = lt::mdesc(smem_u32(sm + L::oV), 0);
+        const int tiles = mode_a ? w.nit : total, per = mode_a ? 1 : items;
+#pragma unroll 1
+        for (int ki = 0, r = 0, ci = 0; ki < tiles; ++ki, ci += ++r == per, r = r == per ? 0 : r) {
+            const int vs = ki % L::NV, ks_ = ki % L::NK;
+            if (a.lengths) tc::named_bar(lt::kNbVZ + (ki & 1), kBThreads + 64);
+            if (ci + 1 >= w.nit) continue;  // no state after the last chunk
+            tc::named_bar(lt::kNbKT, kBThreads + 32);
+            if (lane == 0) {
+                lt::wait(&bars[L::VF + vs], (ki / L::NV) & 1, abort, status, 306);
+                tc::fence_after_sync();
+                const uint32_t acc = r > 0;
+                const uint64_t v = dV + vs * T;
+                // D = 64: the low piece's tile is the second 64-row block of A, at a distance (the block
+                // stride field) that shrinks with the slot
+                const uint64_t k = dK + ks_ * T - (D == 64 ? (uint64_t)(ks_ * T) << 16 : 0);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tc::mma_ss(tmem + C::S, k + ks * kMK, v + ks * kMK, I_S, ks > 0 ? 1u : acc);
+                if (D != 64)
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) tc::mma_ss(tmem + C::S, dM + ks * kMK, v + ks * kMK, I_S, 1);
+                tc::mma_commit(&bars[L::SD]);
+            }
+            __syncwarp();
+        }
+        const int done = w.nit > 1 ? (w.nit - 1) * per : 0;
+        if (lane == 0 && done > 0) lt::wait(&bars[L::SD], (done - 1) & 1, &never, nullptr, 0);
     } else if (warp == 1) {
         if (lane == 0) {
             // ----------------------------------------------------------------------- loads
-            int nx = 0, nkv = 0;
+            int nx = 0, nkv = 0, nv = 0;
             auto load = [&](uint32_t slot, const CUtensorMap* m, int row, int h, uint64_t* bar) {
                 tc::mbar_arrive_expect_tx(bar, L::kTile);
                 for (int i = 0; i < kBlocks; ++i) lt::load_4d(sm + slot + i * lt::kBlk, m, 64 * i, row, h, w.b, bar);
             };
-            for (int it = 0; it < total && !*abort; ++it) {
-                const int r = it % items, row = chunk_of(it / items) * kW;
-                const bool lx = !mode_b || r == 0, lkv = !mode_a || r == 0;
-                const int xs = nx % L::NX, ks_ = nkv % L::NK, vs = nkv % L::NV;
-                if (lx) {
+            // key / value tile ki is released (its slots of either kind may be loaded again)
+            auto released = [&](int ki) {
+                return lt::wait(&bars[L::E + ki % L::NK], (ki / L::NK) & 1, abort, status, 312);
+            };
+#pragma unroll 1
+            for (int it = 0, r = 0, ci = 0; it < total; ++it, ci += ++r == items, r = r == items ? 0 : r) {
+                const int row = chunk_of(ci) * kW;
+                if (!mode_b || r == 0) {
+                    const int xs = nx % L::NX;
                     if (nx >= L::NX && !lt::wait(&bars[L::XE + xs], (nx / L::NX - 1) & 1, abort, status, 311)) break;
                     load(L::oX + xs * L::kTile, &maps.x, row, w.s * a.rx + (mode_a ? r : 0), &bars[L::XF + xs]);
                     ++nx;
                 }
-                if (lkv) {
-                    const int h = w.s * a.rk + (mode_b ? r : 0);
-                    if (nkv >= L::NK && !lt::wait(&bars[L::KE + ks_], (nkv / L::NK - 1) & 1, abort, status, 312)) break;
+                if (!mode_a || r == 0) {
+                    const int h = w.s * a.rk + (mode_b ? r : 0), ks_ = nkv % L::NK, vs = nkv % L::NV;
+                    if (nkv >= L::NK && !released(nkv - L::NK)) break;
                     load(L::oK + ks_ * L::kTile, &maps.k, row, h, &bars[L::KF + ks_]);
-                    if (nkv >= L::NV && !lt::wait(&bars[L::VE + vs], (nkv / L::NV - 1) & 1, abort, status, 313)) {
-                        ++nkv;  // the K load is in flight; its V is not
-                        break;
-                    }
-                    load(L::oV + vs * L::kTile, &maps.v, row, h, &bars[L::VF + vs]);
                     ++nkv;
+                    if (nv >= L::NV && !released(nv - L::NV)) break;
+                    load(L::oV + vs * L::kTile, &maps.v, row, h, &bars[L::VF + vs]);
+                    ++nv;
                 }
             }
-            // drain: every load has landed.  A wait for a load that was not issued (after an abort)
-            // runs out; the others return at once.
+            // drain: every load has landed
             for (int i = max(0, nx - L::NX); i < nx; ++i)
                 lt::wait(&bars[L::XF + i % L::NX], (i / L::NX) & 1, &never, nullptr, 0);
             for (int i = max(0, nkv - L::NK); i < nkv; ++i)
                 lt::wait(&bars[L::KF + i % L::NK], (i / L::NK) & 1, &never, nullptr, 0);
-            for (int i = max(0, nkv - L::NV); i < nkv; ++i)
+            for (int i = max(0, nv - L::NV); i < nv; ++i)
                 lt::wait(&bars[L::VF + i % L::NV], (i / L::NV) & 1, &never, nullptr, 0);
         }
     } else if (warp == 2) {
         if (lane == 0) {
             // ---------------------------------------------------------------------- stores
-            const int groups = mode_b ? w.nit : total;
-            for (int g = 0; g < groups; ++g) {
+            const int groups = mode_b ? w.nit : total, per = mode_a ? items : 1;
+#pragma unroll 1
+            for (int g = 0, r = 0, ci = 0; g < groups; ++g, ci += ++r == per, r = r == per ? 0 : r) {
                 const int slot = g % L::NX;
                 if (!lt::wait(&bars[L::OS + slot], (g / L::NX) & 1, abort, status, 321)) break;
-                const int row = chunk_of(mode_a ? g / items : g) * kW, h = w.s * a.rx + (mode_a ? g % items : 0);
+                const int row = chunk_of(ci) * kW, h = w.s * a.rx + r;
                 for (int i = 0; i < kBlocks; ++i)
                     if (64 * i < a.dy)
                         lt::store_4d(&maps.y, sm + L::oX + slot * L::kTile + i * lt::kBlk, 64 * i, row, h, w.b);
@@ -376,172 +421,195 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
             }
             tc::bulk_wait_all();
         }
-    } else if (warp >= lt::kA0 && warp < lt::kB0) {
-        // ---------------------------------------------------- A: row i of the chunk per thread
-        const int i = 32 * q4 + lane, row0 = 32 * q4;
+    } else if (warp < lt::kB0) {
+        // ------------------------ A: row i of the chunk, half ah of the columns per thread
+        const int i = 32 * q4 + lane, row0 = 32 * q4, ah = (warp - lt::kA0) >> 2;
         const uint32_t lanes = (uint32_t)row0 << 16;
-        int groups = 0;
-        for (int it = 0; it < total && !*abort; ++it) {
-            const int r = it % items, ci = it / items, Wc = valid_of(ci);
-            const bool new_y = !mode_b || r == 0, end_y = !mode_b || r == items - 1;
-            const uint32_t tg = tmem + lanes + C::G(it);
-            lt::wait(&bars[L::BG + (it & 1)], (it >> 1) & 1, abort, status, 331);
+        const bool poller = warp == lt::kA0 && lane == 0;
+        auto wait_a = [&](int bar, int parity, int where) {
+            if (poller) lt::wait(&bars[bar], parity, abort, status, where);
+            __syncwarp();
+            tc::named_bar(lt::kNbA, kAThreads);
             tc::fence_after_sync();
-            // EPI-1: 32 columns at a time.  A block is entirely kept (factor g^(i-cb-31) g^(31-j)),
-            // entirely dropped, or the diagonal one (a factor per element).
+        };
+        int groups = 0, r = -1, ci = 0;
 #pragma unroll 1
-            for (int cb = 0; cb < kW; cb += 32) {
-                uint32_t pk[16];
-                if (rev ? cb < row0 : cb > row0) {
+        for (int it = -1; it < total; ++it) {
+            // item it = (chunk ci, r); -1: only the first Gram's EPI-1
+            const int Wc = valid_of(ci);
+            const bool last = r == items - 1, end_y = it >= 0 && (!mode_b || last);
+            const uint32_t ty = tmem + lanes + C::Y(groups) + ah * (D / 2);
+            if (it >= 0) {
+                if (!mode_b || r == 0) {  // EPI-C
+                    wait_a(L::BC, groups & 1, 332);
+                    const float f = a.s_carry * gp[rev ? max(Wc - i, 0) : i + 1];
+#pragma unroll 1
+                    for (int cb = 0; cb < D / 2; cb += 16) {
+                        uint32_t y[16];
+                        tc::tmem_ld16(ty + cb, y);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) pk[j] = 0u;
-                } else {
-                    uint32_t g[32];
-                    tc::tmem_ld32(tg + cb, g);
-                    tc::tmem_wait_ld();
-                    if (cb == row0) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            float f[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int dist = rev ? cb + j + e - i : i - cb - j - e;
-                                const bool keep = dist >= 0 && (!rev || cb + j + e < Wc);
-                                f[e] = keep ? __uint_as_float(g[j + e]) * (a.s_intra * gp[max(dist, 0)]) : 0.f;
-                            }
-                            pk[j / 2] = pack_bf16x2(f[0], f[1]);
-                        }
-                    } else {
-                        const float base = a.s_intra * gp[rev ? cb - i : i - cb - 31];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 t = *reinterpret_cast<const float4*>(tt + j);
-                            float f0 = __uint_as_float(g[j]) * (base * t.x), f1 = __uint_as_float(g[j + 1]) * (base * t.y),
-                                  f2 = __uint_as_float(g[j + 2]) * (base * t.z), f3 = __uint_as_float(g[j + 3]) * (base * t.w);
-                            if (rev && Wc < kW) {  // columns past the sequence hold anything
-                                f0 = cb + j < Wc ? f0 : 0.f;
-                                f1 = cb + j + 1 < Wc ? f1 : 0.f;
-                                f2 = cb + j + 2 < Wc ? f2 : 0.f;
-                                f3 = cb + j + 3 < Wc ? f3 : 0.f;
-                            }
-                            pk[j / 2] = pack_bf16x2(f0, f1);
-                            pk[j / 2 + 1] = pack_bf16x2(f2, f3);
-                        }
+                        for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(f * __uint_as_float(y[j]));
+                        tc::tmem_st16(ty + cb, y);
                     }
                 }
-                tc::tmem_st16(tg + cb / 2, pk);  // columns that this thread has read
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::named_arrive(lt::kNbGT + (it & 1), kAThreads + 32);
             }
-            if (new_y) {  // EPI-C
-                lt::wait(&bars[L::BC], groups & 1, abort, status, 332);
-                tc::fence_after_sync();
-                const float f = a.s_carry * gp[rev ? max(Wc - i, 0) : i + 1];
+            if (it + 1 < total) {
+                // EPI-1 of the next item: columns 64 ah .. 64 ah + 63, 16 at a time, packed over the first
+                // half of them.  The factor of a column on the masked side is 0 in the table, and its product is
+                // selected away (the column may hold anything past the sequence).
+                const int Wn = valid_of(it >= 0 && last ? ci + 1 : ci);
+                const uint32_t tg = tmem + lanes + C::G(it + 1) + 64 * ah;
+                wait_a(L::BG + ((it + 1) & 3), ((it + 1) >> 2) & 1, 331);
+                const int limit = rev ? Wn : kW, sgn = rev ? 1 : -1;
+                const float* fac = gp + (rev ? 64 * ah - i : i - 64 * ah);
 #pragma unroll 1
-                for (int cb = 0; cb < D; cb += 16) {
+                for (int cb = 0; cb < 64; cb += 16) {
+                    const int c = 64 * ah + cb;
+                    uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                    if (rev ? c + 15 >= row0 : c <= row0 + 31) {  // some column of it is kept for some row
+                        uint32_t g[16];
+                        tc::tmem_ld16(tg + cb, g);
+                        float f[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[j] = a.s_intra * fac[sgn * (cb + j)];
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float v = f[j] * __uint_as_float(g[j]);
+                            f[j] = f[j] != 0.f && c + j < limit ? v : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) pk[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+                    }
+                    lt::tmem_st8(tg + cb / 2, pk);  // columns that this thread has read
+                }
+            }
+            if (end_y) {
+                // EPI-Y, into the X tile, which the products have read
+                wait_a(L::YD, groups & 1, 333);
+                if (poller && !mode_b && last) tc::mbar_arrive(&bars[L::E + (mode_a ? ci : it) % L::NK]);
+                unsigned char* st = sm + L::oX + (groups % L::NX) * L::kTile;
+                const bool live = i < Wc;
+#pragma unroll 1
+                for (int cb = 0; cb < D / 2; cb += 16) {
                     uint32_t y[16];
-                    tc::tmem_ld16(tmem + lanes + C::Y + cb, y);
+                    tc::tmem_ld16(ty + cb, y);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(f * __uint_as_float(y[j]));
-                    tc::tmem_st16(tmem + lanes + C::Y + cb, y);
-                }
-            }
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[L::GT + (it & 1)]);
-            if (!end_y) continue;
-            // EPI-Y, into the X tile, which the products have read
-            lt::wait(&bars[L::YD], groups & 1, abort, status, 333);
-            tc::fence_after_sync();
-            unsigned char* st = sm + L::oX + (groups % L::NX) * L::kTile;
-            const bool live = i < Wc;
-#pragma unroll 1
-            for (int cb = 0; cb < D; cb += 32) {
-                uint32_t y[32];
-                tc::tmem_ld32(tmem + lanes + C::Y + cb, y);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                    uint4 o = make_uint4(0, 0, 0, 0);
-                    if (live) {
-                        o.x = pack_bf16x2(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
-                        o.y = pack_bf16x2(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
-                        o.z = pack_bf16x2(__uint_as_float(y[j + 4]), __uint_as_float(y[j + 5]));
-                        o.w = pack_bf16x2(__uint_as_float(y[j + 6]), __uint_as_float(y[j + 7]));
+                    for (int j = 0; j < 16; j += 8) {
+                        uint4 o = make_uint4(0, 0, 0, 0);
+                        if (live) {
+                            o.x = pack_bf16x2(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                            o.y = pack_bf16x2(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
+                            o.z = pack_bf16x2(__uint_as_float(y[j + 4]), __uint_as_float(y[j + 5]));
+                            o.w = pack_bf16x2(__uint_as_float(y[j + 6]), __uint_as_float(y[j + 7]));
+                        }
+                        const int col = ah * (D / 2) + cb + j;
+                        *reinterpret_cast<uint4*>(st + la_off(col / 64, i, (col % 64) / 8)) = o;
                     }
-                    *reinterpret_cast<uint4*>(st + la_off((cb + j) / 64, i, ((cb + j) % 64) / 8)) = o;
                 }
+                tc::fence_before_sync();
+                tc::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars[L::OS + groups % L::NX]);
+                ++groups;
+                // MMA-C of the next group may overwrite the region (with one; it meets this before every group
+                // but the first, so not after the last)
+                if (C::NY == 1 && it + 1 < total) tc::named_arrive(lt::kNbYR, kAThreads + 32);
             }
-            tc::fence_before_sync();
-            tc::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-                tc::mbar_arrive(&bars[L::YR]);
-                tc::mbar_arrive(&bars[L::OS + groups % L::NX]);
-            }
-            ++groups;
+            if (++r == items) r = 0, ++ci;
+            if (it < 0) r = 0, ci = 0;
         }
-    } else if (warp >= lt::kB0) {
+    } else {
         // -------------------------------------------- B: keys' pieces, the values' padding, the state
         const int row = 32 * q4 + lane;             // KT: row of the chunk; 16-byte chunks of it below
         constexpr int kC = D / 16;                  // 16-byte chunks per thread
         const int c0 = half * kC;                   // chunk index over the whole row: block c / 8, chunk c % 8
         const uint32_t lanes = (uint32_t)(32 * q4) << 16;
-        int nk = 0;  // key / value tiles seen
-        for (int it = 0; it < total && !*abort; ++it) {
-            const int r = it % items, ci = it / items, Wc = valid_of(ci);
-            if (mode_a && r > 0 && r < items - 1) continue;
-            const int vs = nk % L::NV, ks_ = nk % L::NK;
-            if (a.lengths && (!mode_a || r == 0)) {
-                lt::wait(&bars[L::VF + vs], (nk / L::NV) & 1, abort, status, 341);
+        const bool poller = warp == lt::kB0 && lane == 0;
+        auto meet = [&]() {  // after the poller's waits
+            __syncwarp();
+            tc::named_bar(lt::kNbB, kBThreads);
+        };
+        const int tiles = mode_a ? w.nit : total, per = mode_a ? 1 : items;
+#pragma unroll 1
+        for (int ki = 0, r = 0, ci = 0; ki < tiles; ++ki, ci += ++r == per, r = r == per ? 0 : r) {
+            const int Wc = valid_of(ci), vs = ki % L::NV, ks_ = ki % L::NK;
+            const bool state_now = ci + 1 < w.nit, last = r == per - 1;
+            // The Gram products that read K: with shared keys (mode a) of the chunk's last item, and then the
+            // values' padding is cleared before that.
+            if (mode_a && a.lengths) {
+                if (poller) lt::wait(&bars[L::VF + vs], (ki / L::NV) & 1, abort, status, 341);
+                meet();
+            }
+            if (!mode_a) {
+                if (poller) {
+                    lt::wait(&bars[L::KF + ks_], (ki / L::NK) & 1, abort, status, 342);
+                    lt::wait(&bars[L::BG + (ki & 3)], (ki >> 2) & 1, abort, status, 343);
+                    if (a.lengths) lt::wait(&bars[L::VF + vs], (ki / L::NV) & 1, abort, status, 341);
+                }
+                meet();
+            }
+            if (a.lengths) {
                 if (Wc < min(kW, a.n - chunk_of(ci) * kW) && row >= Wc) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = c0; c < c0 + kC; ++c)
                         *reinterpret_cast<uint4*>(sm + L::oV + vs * L::kTile + la_off(c >> 3, row, c & 7)) =
                             make_uint4(0, 0, 0, 0);
                 }
                 tc::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars[L::VZ + vs]);
+                tc::named_arrive(lt::kNbVZ + (ki & 1), kBThreads + 64);
             }
-            if (mode_a && r < items - 1) continue;
-            if (ci + 1 < w.nit) {
-                lt::wait(&bars[L::KF + ks_], (nk / L::NK) & 1, abort, status, 342);
-                lt::wait(&bars[L::BGK + (nk & 1)], (nk >> 1) & 1, abort, status, 343);  // the Gram products have read K
-                if (nk > 0) lt::wait(&bars[L::ME], (nk - 1) & 1, abort, status, 344);   // the low piece has been read
-                const float wt = row < Wc ? a.s_state * gp[rev ? row : Wc - 1 - row] : 0.f;
-                unsigned char *kt = sm + L::oK + ks_ * L::kTile, *mt = sm + L::oM;
-#pragma unroll
-                for (int c = c0; c < c0 + kC; ++c) {
-                    const uint32_t at = la_off(c >> 3, row, c & 7);
-                    uint4 p[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                    if (row < Wc) lt::pieces8<2>(*reinterpret_cast<const uint4*>(kt + at), wt, p);
-                    *reinterpret_cast<uint4*>(kt + at) = p[0];
-                    *reinterpret_cast<uint4*>(mt + at) = p[1];
-                }
-                tc::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars[L::KT]);
-                if (r == items - 1) {  // EPI-S
-                    lt::wait(&bars[L::SD], ci & 1, abort, status, 345);
-                    tc::fence_after_sync();
-                    const float rho = gp[Wc];
-#pragma unroll
-                    for (int cb = 0; cb < kSC; cb += 16) {
-                        uint32_t d[16];
-                        tc::tmem_ld16(tmem + lanes + C::S + sc0 + cb, d);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) sig[cb + j] = fmaf(rho, sig[cb + j], __uint_as_float(d[j]));
-                    }
-                    publish();
-                    tc::fence_before_sync();
-                    tc::fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bars[L::SP]);
-                }
+            if (!state_now) {  // no product of ours reads this tile
+                if (poller) tc::mbar_arrive(&bars[L::E + ks_]);
+                continue;
             }
-            ++nk;
+            if (mode_a) {
+                if (poller) {
+                    lt::wait(&bars[L::KF + ks_], (ki / L::NK) & 1, abort, status, 342);
+                    lt::wait(&bars[L::BGK], ki & 1, abort, status, 343);
+                }
+                meet();
+            }
+            const float wt = row < Wc ? a.s_state * gp[rev ? row : Wc - 1 - row] : 0.f;
+            unsigned char *kt = sm + L::oK + ks_ * L::kTile, *mt = sm + L::oM;
+#pragma unroll 2
+            for (int c = c0; c < c0 + kC; ++c) {
+                const uint32_t at = la_off(c >> 3, row, c & 7);
+                uint4 p[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (row < Wc) lt::pieces8<2>(*reinterpret_cast<const uint4*>(kt + at), wt, p);
+                *reinterpret_cast<uint4*>(kt + at) = p[0];
+                *reinterpret_cast<uint4*>(mt + at) = p[1];
+            }
+            tc::fence_proxy_async();
+            tc::named_arrive(lt::kNbKT, kBThreads + 32);
+            if (poller) {  // the product is done: the tile is released, the low piece may be overwritten
+                lt::wait(&bars[L::SD], ki & 1, abort, status, 345);
+                tc::mbar_arrive(&bars[L::E + ks_]);
+                // MMA-C of this chunk has read the state that publish() overwrites
+                if (last) lt::wait(&bars[mode_a ? L::YL : L::BC], ci & 1, abort, status, 347);
+            }
+            if (!last) continue;
+            // EPI-S
+            meet();
+            tc::fence_after_sync();
+            const float rho = gp[Wc];
+#pragma unroll
+            for (int cb = 0; cb < kSC; cb += 16) {
+                uint32_t d[16];
+                tc::tmem_ld16(tmem + lanes + C::S + sc0 + cb, d);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sig[cb + j] = fmaf(rho, sig[cb + j], __uint_as_float(d[j]));
+            }
+            publish();
+            tc::fence_before_sync();
+            tc::fence_proxy_async();
+            tc::named_arrive(lt::kNbSP, kBThreads + 32);
         }
     }
     __syncwarp();
@@ -553,38 +621,41 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
 
 // ----------------------------------------------------------------------------------------
 // Summary kernel: Sig_B = s_state sum_i g^(distance to the segment's end) k_i v_i^T over the
-// segment's rows (all key / value heads of the state), weights relative to the segment, so the
-// products accumulate in tensor memory from the first tile to the last.
+// segment's rows (all key / value heads of the state).  The weights are relative to the segment, so
+// nothing decays from tile to tile.  A tile's products accumulate in tensor memory (two regions in
+// turn) and are added to float32 registers: tensor-memory accumulation cuts bits off at every step,
+// which over thousands of rows would cost a digit of the returned state.  The pieces are made and
+// multiplied by halves of a tile (64 rows), one half while the other's products run.
 // ----------------------------------------------------------------------------------------
 namespace lt {
 template <int D>
 struct Sum {
     static constexpr uint32_t kTile = (uint32_t)(D / 64) * kBlk;
-    static constexpr int NS = D == 64 ? 3 : 2;   // key / value slots
-    static constexpr int NP = D == 64 ? 2 : 1;   // buffers of the two lower pieces
-    static constexpr uint32_t oK = 0, oV = oK + NS * kTile, oM = oV + NS * kTile, oL = oM + NP * kTile,
-                              oZ = oL + NP * kTile;  // D = 64: a tile of zeros beside the third piece
+    static constexpr int NS = D == 64 ? 4 : 2;  // key / value slots
+    static constexpr uint32_t oK = 0, oV = oK + NS * kTile, oM = oV + NS * kTile, oL = oM + kTile,
+                              oZ = oL + kTile;  // D = 64: a tile of zeros beside the third piece
     static constexpr uint32_t oBar = oZ + (D == 64 ? kTile : 0);
-    enum { KF = 0, VF = KF + NS, E = VF + NS, KT = E + NS, PE = KT + NP, kBars = PE + NP };
+    enum { KF = 0, VF = KF + NS, E = VF + NS, PE = E + NS, AD, kBars = AD + 2 };
     static constexpr uint32_t oMisc = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oMisc + 16 + 1024;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
-constexpr int kSumThreads = 384;  // warp 0 MMA, warp 1 loads, warps 4..11 pieces
+constexpr int kSumThreads = 640, kSumB0 = 4, kSumBWarps = 16;  // warp 0 MMA, warp 1 loads, warps 4..19 pieces and sums
 }  // namespace lt
 
 template <int D>
 __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __grid_constant__ lt::Maps maps, const LinPass a) {
     using L = lt::Sum<D>;
-    constexpr int kW = lt::kW, kBlocks = D / 64, kC = D / 16;
+    constexpr int kW = lt::kW, kBlocks = D / 64, kC = D / 64;  // kC: 16-byte chunks per thread and half tile
+    constexpr int kCols = D / 4;                               // sums per thread
     extern __shared__ unsigned char smem_raw[];
-    unsigned char* sm =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // an offset, not a rounded pointer: the compiler then still knows the address space
+    unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + L::oMisc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::oMisc + 4);
     int* status = a.status;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q4 = warp & 3;
+    const int tid = threadIdx.x, warp = lt::uniform(tid >> 5), lane = tid & 31, q4 = warp & 3;
     const lt::Where w = lt::locate(a);
     const bool rev = a.rev != 0;
     const int items = a.rk, total = w.nit * items;
@@ -595,11 +666,11 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
     }
     const float log2g = log2f(lin_decay(a, w.s));
     if (tid == 0) {
-        for (int i = 0; i < L::kBars; ++i) tc::mbar_init(&bars[i], i >= L::KT && i < L::KT + L::NP ? lt::kBWarps : 1);
+        for (int i = 0; i < L::kBars; ++i) tc::mbar_init(&bars[i], 1);
         *abort = 0;
         tc::mbar_fence_init();
     }
-    if (warp == 0) tc::tmem_alloc(tmem_holder, 128);
+    if (warp == 0) tc::tmem_alloc(tmem_holder, 2 * D);
     if (D == 64) {
         for (int e = tid; e < (int)(L::kTile / 16); e += lt::kSumThreads)
             *reinterpret_cast<uint4*>(sm + L::oZ + 16 * e) = make_uint4(0, 0, 0, 0);
@@ -608,31 +679,48 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = (uint32_t)lt::uniform((int)*tmem_holder);
     volatile int never = 0;
     const int seg_rows = min(w.len, w.c1 * kW) - w.c0 * kW;  // valid rows of the segment
+    float sum[kCols];
+
+    constexpr int kBThreads = 32 * lt::kSumBWarps;
+    enum { kNbKT = 2, kNbDR = 4, kNbAll = 1 };  // named barriers (two each of KT: a half tile; DR: a sum region)
 
     if (warp == 0) {
-        if (lane == 0) {
-            constexpr uint32_t I_S = tc::idesc_bf16(128, D, 1, 1);
-            const uint32_t sK = smem_u32(sm + L::oK), sV = smem_u32(sm + L::oV), sM = smem_u32(sm + L::oM),
-                           sL = smem_u32(sm + L::oL), sZ = smem_u32(sm + L::oZ);
-            for (int it = 0; it < total; ++it) {
-                const int s = it % L::NS, p = it % L::NP;
-                lt::wait(&bars[L::VF + s], (it / L::NS) & 1, abort, status, 351);
-                lt::wait(&bars[L::KT + p], (it / L::NP) & 1, abort, status, 352);
-                tc::fence_after_sync();
-                const uint32_t k = sK + s * L::kTile, v = sV + s * L::kTile, m = sM + p * L::kTile, l = sL + p * L::kTile;
-                for (int ks = 0; ks < 8; ++ks)
-                    tc::mma_ss(tmem, D == 64 ? lt::mdesc(k, ks, m - k) : lt::mdesc(k, ks), lt::mdesc(v, ks), I_S,
-                               it > 0 || ks > 0);
-                if (D != 64)
-                    for (int ks = 0; ks < 8; ++ks) tc::mma_ss(tmem, lt::mdesc(m, ks), lt::mdesc(v, ks), I_S, 1);
-                for (int ks = 0; ks < 8; ++ks)
-                    tc::mma_ss(tmem, D == 64 ? lt::mdesc(l, ks, sZ - l) : lt::mdesc(l, ks), lt::mdesc(v, ks), I_S, 1);
-                tc::mma_commit(&bars[L::E + s]);
-                tc::mma_commit(&bars[L::PE + p]);
+        constexpr uint32_t I_S = tc::idesc_bf16(128, D, 1, 1);
+        constexpr uint32_t T = L::kTile >> 4;
+        constexpr uint64_t kMK = 2048 >> 4;
+        const uint32_t sK = smem_u32(sm + L::oK), sM = smem_u32(sm + L::oM), sL = smem_u32(sm + L::oL),
+                       sZ = smem_u32(sm + L::oZ);
+        const uint64_t dK = lt::mdesc(sK, 0, D == 64 ? sM - sK : lt::kBlk), dV = lt::mdesc(smem_u32(sm + L::oV), 0),
+                       dM = lt::mdesc(sM, 0), dL = lt::mdesc(sL, 0, D == 64 ? sZ - sL : lt::kBlk);
+        for (int it = 0; it < total; ++it) {
+            const int s = it % L::NS;
+            const uint32_t acc = tmem + (it & 1) * D;
+            const uint64_t v = dV + s * T, k = dK + s * T - (D == 64 ? (uint64_t)(s * T) << 16 : 0);
+            if (lane == 0) lt::wait(&bars[L::VF + s], (it / L::NS) & 1, abort, status, 351);
+            __syncwarp();
+            if (it >= 2) tc::named_bar(kNbDR + (it & 1), kBThreads + 32);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                __syncwarp();
+                tc::named_bar(kNbKT + h, kBThreads + 32);
+                if (lane == 0) {
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                        tc::mma_ss(acc, k + ks * kMK, v + ks * kMK, I_S, ks > 0);
+                    if (D != 64)
+#pragma unroll
+                        for (int ks = 4 * h; ks < 4 * h + 4; ++ks) tc::mma_ss(acc, dM + ks * kMK, v + ks * kMK, I_S, 1);
+#pragma unroll
+                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks) tc::mma_ss(acc, dL + ks * kMK, v + ks * kMK, I_S, 1);
+                    tc::mma_commit(&bars[h == 0 ? L::PE : L::AD + (it & 1)]);
+                    if (h == 1) tc::mma_commit(&bars[L::E + s]);
+                }
             }
+            __syncwarp();
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -653,74 +741,96 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
                 lt::wait(&bars[L::VF + i % L::NS], (i / L::NS) & 1, &never, nullptr, 0);
             }
         }
-    } else if (warp >= 4) {
-        const int half = (warp - 4) >> 2, row = 32 * q4 + lane, c0 = half * kC;
-        for (int it = 0; it < total && !*abort; ++it) {
-            const int s = it % L::NS, p = it % L::NP, ci = it / items;
-            const int r0 = (rev ? w.c1 - 1 - ci : w.c0 + ci) * kW, Wc = min(kW, w.len - r0);
-            lt::wait(&bars[L::KF + s], (it / L::NS) & 1, abort, status, 354);
-            if (it >= L::NP) lt::wait(&bars[L::PE + p], (it / L::NP - 1) & 1, abort, status, 355);
-            const int at_seg = r0 - w.c0 * kW + row;  // row within the segment
-            const float wt = row < Wc ? a.s_state * pow_decay(log2g, (float)(rev ? at_seg : seg_rows - 1 - at_seg)) : 0.f;
-            unsigned char *kt = sm + L::oK + s * L::kTile, *mt = sm + L::oM + p * L::kTile, *lo = sm + L::oL + p * L::kTile;
-#pragma unroll
-            for (int c = c0; c < c0 + kC; ++c) {
-                const uint32_t at = la_off(c >> 3, row, c & 7);
-                uint4 x[3] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                if (row < Wc) lt::pieces8<3>(*reinterpret_cast<const uint4*>(kt + at), wt, x);
-                *reinterpret_cast<uint4*>(kt + at) = x[0];
-                *reinterpret_cast<uint4*>(mt + at) = x[1];
-                *reinterpret_cast<uint4*>(lo + at) = x[2];
-            }
-            if (Wc < min(kW, a.n - r0)) {  // padding rows of the values may hold anything
-                lt::wait(&bars[L::VF + s], (it / L::NS) & 1, abort, status, 356);
-                if (row >= Wc)
-#pragma unroll
-                    for (int c = c0; c < c0 + kC; ++c)
-                        *reinterpret_cast<uint4*>(sm + L::oV + s * L::kTile + la_off(c >> 3, row, c & 7)) =
-                            make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_proxy_async();
+    } else if (warp >= lt::kSumB0) {
+        const int wb = warp - lt::kSumB0;
+        const int r64 = 32 * (wb & 1) + lane, c0 = (wb >> 1) * kC;  // row of the half tile, first chunk
+        const uint32_t ta = tmem + ((uint32_t)(32 * q4) << 16) + (wb >> 2) * kCols;
+        const bool poller = wb == 0 && lane == 0;
+        auto meet = [&]() {  // after the poller's waits
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[L::KT + p]);
+            tc::named_bar(kNbAll, kBThreads);
+        };
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) sum[j] = 0.f;
+        // tile it's products are done: the sums go to registers, the region is released
+        auto drain = [&](int it) {
+            tc::fence_after_sync();
+#pragma unroll
+            for (int cb = 0; cb < kCols; cb += 16) {
+                uint32_t d[16];
+                tc::tmem_ld16(ta + (it & 1) * D + cb, d);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[cb + j] += __uint_as_float(d[j]);
+            }
+            tc::fence_before_sync();
+            if (it + 2 < total) tc::named_arrive(kNbDR + (it & 1), kBThreads + 32);
+        };
+        for (int it = 0; it < total; ++it) {
+            const int s = it % L::NS, ci = it / items;
+            const int r0 = (rev ? w.c1 - 1 - ci : w.c0 + ci) * kW, Wc = min(kW, w.len - r0);
+            unsigned char *kt = sm + L::oK + s * L::kTile, *mt = sm + L::oM, *lo = sm + L::oL;
+            const bool padded = Wc < min(kW, a.n - r0);  // padding rows of the values may hold anything
+            if (poller) {
+                lt::wait(&bars[L::KF + s], (it / L::NS) & 1, abort, status, 354);
+                if (padded) lt::wait(&bars[L::VF + s], (it / L::NS) & 1, abort, status, 356);
+                if (it > 0) lt::wait(&bars[L::PE], (it - 1) & 1, abort, status, 355);  // half 0's lower pieces are free
+            }
+            meet();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = 64 * h + r64, at_seg = r0 - w.c0 * kW + row;  // row within the segment
+                const float wt =
+                    row < Wc ? a.s_state * pow_decay(log2g, (float)(rev ? at_seg : seg_rows - 1 - at_seg)) : 0.f;
+                if (h == 1 && it > 0) {  // tile it - 1 is done as a whole
+                    if (poller) lt::wait(&bars[L::AD + ((it - 1) & 1)], ((it - 1) >> 1) & 1, abort, status, 357);
+                    meet();
+                }
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    uint4 x[3] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                    const uint32_t at = la_off((c0 + c) >> 3, row, (c0 + c) & 7);
+                    if (row < Wc) lt::pieces8<3>(*reinterpret_cast<const uint4*>(kt + at), wt, x);
+                    *reinterpret_cast<uint4*>(kt + at) = x[0];
+                    *reinterpret_cast<uint4*>(mt + at) = x[1];
+                    *reinterpret_cast<uint4*>(lo + at) = x[2];
+                    if (padded && row >= Wc)
+                        *reinterpret_cast<uint4*>(sm + L::oV + s * L::kTile + at) = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async();
+                tc::named_arrive(kNbKT + h, kBThreads + 32);
+            }
+            if (it > 0) drain(it - 1);
         }
+        if (poller) lt::wait(&bars[L::AD + ((total - 1) & 1)], ((total - 1) >> 1) & 1, &never, status, 358);
+        meet();
+        drain(total - 1);
     }
     __syncwarp();
-    // the sums: every product is done once the last tile's commit is
-    const int lt_ = total - 1;
-    lt::wait(&bars[L::PE + lt_ % L::NP], (lt_ / L::NP) & 1, &never, status, 357);
-    tc::fence_after_sync();
     __syncthreads();
-    if (warp >= 4) {
-        constexpr int kCols = D / 2;
-        const int half = (warp - 4) >> 2, row = 32 * q4 + lane, col = half * kCols;
-        float* ex = reinterpret_cast<float*>(sm);  // D = 64: the low pieces' rows, [64][65]
+    if (warp >= lt::kSumB0) {
+        const int row = 32 * q4 + lane, col = ((warp - lt::kSumB0) >> 2) * kCols;
+        float* ex = reinterpret_cast<float*>(sm);  // D = 64: the middle pieces' rows, [64][65]
+        if (D == 64) {
+            if (row >= 64)
 #pragma unroll
-        for (int cb = 0; cb < kCols; cb += 16) {
-            uint32_t d[16];
-            tc::tmem_ld16(tmem + ((uint32_t)(32 * q4) << 16) + col + cb, d);
-            tc::tmem_wait_ld();
-            if (D == 64) {
-                if (row >= 64)
+                for (int j = 0; j < kCols; ++j) ex[(row - 64) * 65 + col + j] = sum[j];
+            tc::named_bar(kNbAll, kBThreads);
+            if (row < 64)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) ex[(row - 64) * 65 + col + cb + j] = __uint_as_float(d[j]);
-                tc::named_bar(1, 256);
-                if (row < a.dx)
+                for (int j = 0; j < kCols; ++j) sum[j] += ex[row * 65 + col + j];
+        }
+        if (row < a.dx) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (col + cb + j < a.dy)
-                            dst[row * a.dy + col + cb + j] = __uint_as_float(d[j]) + ex[row * 65 + col + cb + j];
-            } else if (row < a.dx) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (col + cb + j < a.dy) dst[row * a.dy + col + cb + j] = __uint_as_float(d[j]);
-            }
+            for (int j = 0; j < kCols; j += 4)  // dy is a multiple of 16
+                if (col + j < a.dy)
+                    *reinterpret_cast<float4*>(dst + row * a.dy + col + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
         }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 0) tc::tmem_dealloc(tmem, 128);
+    if (warp == 0) tc::tmem_dealloc(tmem, 2 * D);
 }
 
 // [B][heads][n][Dreal] bf16 view, box of 128 rows x 64 columns (128-byte swizzle); columns past
