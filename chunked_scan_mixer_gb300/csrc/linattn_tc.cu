@@ -7,9 +7,8 @@
 // mirrors the decays):
 //   MMA-G   G = X K^T                                   128 x 128 float32 in tensor memory
 //   EPI-1   G~ = mask(G) s_intra g^(i-j) -> bf16, over G's own columns: A operand of MMA-Y
-//   MMA-C   Y = X Sig~ (Sig~ = bf16 of Sig);   EPI-C   Y <- s_carry g^(i+1) Y, in tensor memory
-//   MMA-Y   Y += G~ V
-//   EPI-Y   Y -> bf16 tile -> TMA store
+//   MMA-C   Yc = X Sig~ (Sig~ = bf16 of Sig)       MMA-Y   Y = G~ V
+//   EPI-Y   s_carry g^(i+1) Yc + Y -> bf16 tile -> TMA store
 //   KT      K~ = s_state g^(Wc-1-j) K in pieces of bf16, in shared memory
 //   MMA-S   dSig = K~^T V;   EPI-S   Sig <- g^Wc Sig + dSig  (float32 registers), publish Sig~
 //
@@ -25,10 +24,11 @@
 // and the state are loaded and formed once per chunk for all its items; with rk > 1 X, Y and the state
 // are, and Y and dSig accumulate over the items in tensor memory.
 //
-// Roles (640 threads, one CTA per SM): warp 0 allocates tensor memory and issues MMA-G, MMA-C and
-// MMA-Y, warp 3 MMA-S; warp 1 issues the loads, warp 2 the stores; warps 4..11 (A: a row and half
-// of its columns per thread) run EPI-1, EPI-C and EPI-Y, the next item's EPI-1 while this one's MMA-Y
-// runs; warps 12..19 (B) run KT and EPI-S.  The chains A and B only meet in Sig~.
+// Roles (one CTA per SM): warp 0 allocates tensor memory and issues MMA-G, MMA-C and MMA-Y, warp 3
+// MMA-S; warp 1 issues the loads, warp 2 the stores; warps 4..11 (A: a row and half of its columns
+// per thread) run EPI-1 and EPI-Y; warps 12.. (B) run KT and EPI-S.  The chains A and B only meet in
+// Sig~.  D = 64 has two Gram regions, and EPI-1 of the next item runs while this one's products do;
+// D = 128 has tensor memory for one, and EPI-Y runs while the next Gram does.
 //
 // What a hand-over costs decides the time of a chunk (measured, in SM cycles: issuing one MMA 49, a
 // commit 52, a wait on an mbarrier whose phase is already complete 45 to 90 and twice that while
@@ -44,7 +44,9 @@
 //
 // D = 64 stacks the two key pieces as one 128-row A operand (rows 0..63 the high piece's
 // features, 64..127 the low one's), so MMA-S has full height; the two halves of the state stay
-// apart and MMA-C takes both (K = 128), which costs nothing there.
+// apart and MMA-C takes both (K = 128), which costs nothing there.  D = 128 has no shared memory
+// for a second piece beside two slots of each tile: the high piece replaces the keys, and once it has
+// been multiplied the low one, kept in registers, replaces it.
 #include "fo_common.cuh"
 #include "linattn_pass.h"
 
@@ -55,8 +57,9 @@ namespace {
 namespace lt {
 
 constexpr int kW = 128;
-constexpr int kThreads = 640;
-constexpr int kA0 = 4, kAWarps = 8, kB0 = 12, kBWarps = 8;
+constexpr int kA0 = 4, kAWarps = 8, kB0 = 12;
+__host__ __device__ constexpr int b_warps(int D) { return D == 64 ? 8 : 16; }
+__host__ __device__ constexpr int threads(int D) { return 32 * (kB0 + b_warps(D)); }
 constexpr uint32_t kBlk = la_common::kBlk;  // [128 rows][64 bf16]
 
 struct Maps {
@@ -99,34 +102,43 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
+// Two float32 products in one instruction
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b, float c, float d) {
+    uint64_t p, q, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(q) : "f"(c), "f"(d));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(p), "l"(q));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Named barriers (0 is __syncthreads)
-enum { kNbGT = 5, kNbKT = 7, kNbSP = 8, kNbYR = 9, kNbVZ = 10, kNbA = 12, kNbB = 13 };
+enum { kNbGT = 5, kNbKT = 7, kNbSP = 8, kNbVZ = 10, kNbA = 12, kNbB = 13 };
 
 template <int D>
 struct Out {  // shared memory of the output kernel
     static constexpr uint32_t kTile = (uint32_t)(D / 64) * kBlk;
-    static constexpr int NX = D == 64 ? 4 : 2, NK = NX, NV = D == 64 ? 4 : 1;
-    static constexpr uint32_t oX = 0, oK = oX + NX * kTile, oV = oK + NK * kTile, oM = oV + NV * kTile, oS = oM + kTile;
-    static constexpr uint32_t oGp = oS + kTile;          // 128 zeros, then g^0 .. g^128
-    static constexpr uint32_t oBar = oGp + 4 * 260;
-    enum {
-        XF = 0, XE = XF + NX, OS = XE + NX, KF = OS + NX, VF = KF + NK, E = VF + NV, BG = E + NK, BGK = BG + 4, BC, YL, YD,
-        YI, SD, kBars
-    };
+    static constexpr int NS = D == 64 ? 4 : 2;           // slots of each of x, k, v
+    static constexpr uint32_t oX = 0, oK = oX + NS * kTile, oV = oK + NS * kTile, oM = oV + NS * kTile,
+                              oS = oM + (D == 64 ? kTile : 0);
+    static constexpr uint32_t oGs = oS + kTile;          // s_intra g^distance, 0 for the 128 negative ones
+    static constexpr uint32_t oGp = oGs + 4 * 260;       // g^0 .. g^128
+    static constexpr uint32_t oT = oGp + 4 * 132;        // g^(15 - j) (reverse g^j), j = 0 .. 15
+    static constexpr uint32_t oBar = oT + 64;
+    enum { XF = 0, XE = XF + NS, OS = XE + NS, KF = OS + NS, VF = KF + NS, E = VF + NS, BG = E + NS, BGK = BG + 4, YL, YD,
+           YI, SH, SD, kBars };
     static constexpr uint32_t oMisc = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oMisc + 16 + 1024;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
-// Tensor memory columns of the output kernel: two Gram regions, Y (two regions where they fit), dSig.
+// Tensor memory columns of the output kernel: one or two Gram regions, Y, Yc, dSig.
 template <int D>
 struct Cols {
-    static constexpr int NY = D == 64 ? 2 : 1;
-    __device__ static constexpr uint32_t G(int i) { return (uint32_t)(i & 1) * 128; }
-    __device__ static constexpr uint32_t Y(int g) { return 256 + (uint32_t)(g % NY) * D; }
-    static constexpr uint32_t S = 256 + NY * D;
+    static constexpr int NG = D == 64 ? 2 : 1;
+    __device__ static constexpr uint32_t G(int i) { return NG == 2 ? (uint32_t)(i & 1) * 128 : 0u; }
+    static constexpr uint32_t Y = NG * 128, YC = Y + D, S = YC + D;
 };
 
 struct Where {  // the CTA's state head, segment and valid chunks
@@ -182,16 +194,19 @@ __device__ __forceinline__ uint64_t mdesc(uint32_t base, int ks, uint32_t lbo = 
 // Output kernel
 // ----------------------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __grid_constant__ lt::Maps maps, const LinPass a) {
+__global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __grid_constant__ lt::Maps maps, const LinPass a) {
     using L = lt::Out<D>;
     using C = lt::Cols<D>;
-    constexpr int kW = lt::kW;
+    constexpr int kW = lt::kW, kThreads = lt::threads(D), kBWarps = lt::b_warps(D);
     constexpr int kBlocks = D / 64;
-    constexpr int kSC = D / 2;  // state columns per B thread
+    constexpr int kSC = D / (kBWarps / 4);  // state columns per B thread
+    constexpr int NS = L::NS;
     extern __shared__ unsigned char smem_raw[];
     // an offset, not a rounded pointer: the compiler then still knows the address space
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float* gp = reinterpret_cast<float*>(sm + L::oGp) + kW;  // gp[distance]; 0 for a negative one
+    float* gs = reinterpret_cast<float*>(sm + L::oGs) + kW;
+    float* gp = reinterpret_cast<float*>(sm + L::oGp);
+    float* tt = reinterpret_cast<float*>(sm + L::oT);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + L::oMisc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::oMisc + 4);
@@ -209,17 +224,22 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
         const int per = a.dy / 8, count = max(0, z1 - z0) * per;
         for (int h = 0; h < a.rx; ++h) {
             bf16* y = static_cast<bf16*>(const_cast<void*>(a.y.p)) + w.b * a.y.sb + (long long)(w.s * a.rx + h) * a.y.sh;
-            for (int e = tid; e < count; e += lt::kThreads)
+            for (int e = tid; e < count; e += kThreads)
                 *reinterpret_cast<uint4*>(y + (long long)(z0 + e / per) * a.y.sn + (e % per) * 8) = make_uint4(0, 0, 0, 0);
         }
     }
     if (w.nit == 0) return;
 
-    if (tid < 2 * kW + 1) gp[tid - kW] = tid < kW ? 0.f : pow_decay(log2g, (float)(tid - kW));
+    if (tid < 2 * kW + 1) {
+        const float g = tid < kW ? 0.f : pow_decay(log2g, (float)(tid - kW));
+        gs[tid - kW] = a.s_intra * g;
+        if (tid >= kW) gp[tid - kW] = g;
+    }
+    if (tid < 16) tt[tid] = pow_decay(log2g, (float)(rev ? tid : 15 - tid));
     if (tid == 0) {
         for (int i = 0; i < L::kBars; ++i) {
-            const bool by_a = i >= L::OS && i < L::OS + L::NX;   // one arrival per A warp
-            const bool by_two = i >= L::E && i < L::E + L::NK;   // A (or MMA-Y's commit) and B
+            const bool by_a = i >= L::OS && i < L::OS + NS;   // one arrival per A warp
+            const bool by_two = i >= L::E && i < L::E + NS;   // A (or MMA-Y's commit) and B
             tc::mbar_init(&bars[i], by_a ? lt::kAWarps : by_two ? 2 : 1);
         }
         *abort = 0;
@@ -228,8 +248,8 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
     if (warp == 0) tc::tmem_alloc(tmem_holder, 512);
 
     // B thread: state row sr, columns sc0 .. sc0 + kSC - 1.  D = 64: rows 64.. hold the low pieces' sums.
-    const int q4 = warp & 3, half = (warp - lt::kB0) >> 2;
-    const int sr = 32 * q4 + lane, sc0 = half * kSC;
+    const int q4 = warp & 3, part = (warp - lt::kB0) >> 2;
+    const int sr = 32 * q4 + lane, sc0 = part * kSC;
     float sig[kSC];
     auto publish = [&]() {
 #pragma unroll
@@ -258,7 +278,7 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
     auto valid_of = [&](int ci) { return min(kW, w.len - chunk_of(ci) * kW); };
     volatile int never = 0;
 
-    constexpr int kAThreads = 32 * lt::kAWarps, kBThreads = 32 * lt::kBWarps;
+    constexpr int kAThreads = 32 * lt::kAWarps, kBThreads = 32 * kBWarps;
     constexpr uint32_t T = L::kTile >> 4;    // descriptor units (16 bytes): a slot, and 16 rows MN-major
     constexpr uint64_t kMK = 2048 >> 4;
     auto kstep = [](int ks) { return (uint64_t)(((ks >> 2) * lt::kBlk + (ks & 3) * 32) >> 4); };  // K-major
@@ -268,64 +288,63 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
         constexpr uint32_t I_G = tc::idesc_bf16(128, 128, 0, 0), I_Y = tc::idesc_bf16(128, D, 0, 1);
         const uint64_t dX = lt::kdesc(smem_u32(sm + L::oX), 0), dK = lt::kdesc(smem_u32(sm + L::oK), 0),
                        dV = lt::mdesc(smem_u32(sm + L::oV), 0), dS = lt::mdesc(smem_u32(sm + L::oS), 0);
-        int groups = 0;  // Y regions begun
         int r = -1, ci = 0;
 #pragma unroll 1
         for (int it = -1; it < total; ++it) {
             // item it = (chunk ci, r); -1: only the first Gram
             const bool first = r == 0, last = r == items - 1;
-            const bool new_y = it >= 0 && (!mode_b || first), end_y = !mode_b || last;
-            const int ki = it < 0 ? 0 : mode_b ? it : ci, vs = ki % L::NV;
+            const bool new_y = !mode_b || first, end_y = !mode_b || last;
+            const int ki = mode_b ? it : ci, xi = mode_b ? ci : it;
             __syncwarp();
-            if (new_y) {
+            auto products = [&]() {
                 if (first && ci > 0) tc::named_bar(lt::kNbSP, kBThreads + 32);
-                // With two Y regions the last reading of this one is over: A met kNbGT for the item before.
-                if (C::NY == 1 && groups > 0) tc::named_bar(lt::kNbYR, kAThreads + 32);
+                tc::named_bar(lt::kNbGT + (it & 1), kAThreads + 32);  // also: Y and Yc of the item before are read
                 if (lane == 0) {
                     tc::fence_after_sync();
-                    const uint64_t x = dX + (groups % L::NX) * T;  // one x tile a group
+                    if (new_y) {
+                        const uint64_t x = dX + (xi % NS) * T;
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)  // D = 64: the two halves of the state in turn
-                        tc::mma_ss(tmem + C::Y(groups), x + kstep(D == 64 ? ks & 3 : ks), dS + ks * kMK, I_Y, ks > 0);
-                    tc::mma_commit(&bars[L::BC]);
-                    if (mode_a && last) tc::mma_commit(&bars[L::YL]);
+                        for (int ks = 0; ks < 8; ++ks)  // D = 64: the two halves of the state in turn
+                            tc::mma_ss(tmem + C::YC, x + kstep(D == 64 ? ks & 3 : ks), dS + ks * kMK, I_Y, ks > 0);
+                    }
+                    if (!mode_a || first) lt::wait(&bars[L::VF + ki % NS], (ki / NS) & 1, abort, status, 305);
                 }
-                ++groups;
-            }
-            if (lane == 0 && it + 1 < total) {  // MMA-G: takes the region that MMA-Y of it - 1 read
-                if (it > 0) lt::wait(&bars[mode_b ? L::YI : L::YD], (it - 1) & 1, abort, status, 308);
+                __syncwarp();
+                if (a.lengths && (!mode_a || first)) tc::named_bar(lt::kNbVZ + (ki & 1), kBThreads + 64);
+                if (lane == 0) {
+                    tc::fence_after_sync();
+                    const uint64_t v = dV + (ki % NS) * T;
+                    const uint32_t tg = tmem + C::G(it), acc = !new_y;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)  // G~: columns 0..63 of the Gram in its first 32, the rest from 64 on
+                        tc::mma_ts(tmem + C::Y, tg + 8 * (ks & 3) + (ks >> 2) * 64, v + ks * kMK, I_Y, ks > 0 ? 1u : acc);
+                    if (end_y) tc::mma_commit(&bars[L::YD]);
+                    if (mode_a && last) tc::mma_commit(&bars[L::YL]);
+                    if (mode_b) {
+                        tc::mma_commit(&bars[L::E + ki % NS]);
+                        tc::mma_commit(&bars[L::YI]);
+                    }
+                }
+            };
+            if (C::NG == 1 && it >= 0) products();
+            if (lane == 0 && it + 1 < total) {  // MMA-G, into the region that MMA-Y of `before` read
+                const int before = C::NG == 1 ? it : it - 1;
+                if (before >= 0) lt::wait(&bars[mode_b ? L::YI : L::YD], before & 1, abort, status, 308);
                 const bool wrap = last || it < 0;  // the next item begins a chunk
                 const int rn = wrap ? 0 : r + 1, cn = it < 0 ? 0 : ci + (last ? 1 : 0);
-                const int xi = mode_b ? cn : it + 1, kn = mode_a ? cn : it + 1;
-                if (!mode_b || rn == 0) lt::wait(&bars[L::XF + xi % L::NX], (xi / L::NX) & 1, abort, status, 301);
-                if (!mode_a || rn == 0) lt::wait(&bars[L::KF + kn % L::NK], (kn / L::NK) & 1, abort, status, 302);
+                const int xn = mode_b ? cn : it + 1, kn = mode_a ? cn : it + 1;
+                if (!mode_b || rn == 0) lt::wait(&bars[L::XF + xn % NS], (xn / NS) & 1, abort, status, 301);
+                if (!mode_a || rn == 0) lt::wait(&bars[L::KF + kn % NS], (kn / NS) & 1, abort, status, 302);
                 tc::fence_after_sync();
-                const uint64_t x = dX + (xi % L::NX) * T, k = dK + (kn % L::NK) * T;
+                const uint64_t x = dX + (xn % NS) * T, k = dK + (kn % NS) * T;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     tc::mma_ss(tmem + C::G(it + 1), x + kstep(ks), k + kstep(ks), I_G, ks > 0);
                 tc::mma_commit(&bars[L::BG + ((it + 1) & 3)]);  // four: B may be three tiles behind
                 if (mode_a && rn == items - 1) tc::mma_commit(&bars[L::BGK]);
             }
-            if (it >= 0) {
-                if (lane == 0 && (!mode_a || first)) lt::wait(&bars[L::VF + vs], (ki / L::NV) & 1, abort, status, 305);
-                __syncwarp();
-                if (a.lengths && (!mode_a || first)) tc::named_bar(lt::kNbVZ + (ki & 1), kBThreads + 64);
-                tc::named_bar(lt::kNbGT + (it & 1), kAThreads + 32);
-                if (lane == 0) {
-                    tc::fence_after_sync();
-                    const uint64_t v = dV + vs * T;
-                    const uint32_t ty = tmem + C::Y(groups - 1), tg = tmem + C::G(it);
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)  // G~: columns 0..63 of the rows' Gram in its first 32, the rest from 64 on
-                        tc::mma_ts(ty, tg + 8 * (ks & 3) + (ks >> 2) * 64, v + ks * kMK, I_Y, 1);
-                    if (end_y) tc::mma_commit(&bars[L::YD]);
-                    if (mode_b) {
-                        tc::mma_commit(&bars[L::E + ki % L::NK]);
-                        tc::mma_commit(&bars[L::YI]);
-                    }
-                }
-            }
+            __syncwarp();
+            if (C::NG == 2 && it >= 0) products();
             if (++r == items) r = 0, ++ci;
             if (it < 0) r = 0, ci = 0;
         }
@@ -335,32 +354,31 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
         // --------------------------------------------------------------------------- MMA-S
         constexpr uint32_t I_S = tc::idesc_bf16(128, D, 1, 1);
         const uint32_t sK = smem_u32(sm + L::oK), sM = smem_u32(sm + L::oM);
-        const uint64_t dK = lt::mdesc(sK, 0, D == 64 ? sM - sK : lt::kBlk), dM = lt::mdesc(sM, 0),
-                       dV = lt::mdesc(smem_u32(sm + L::oV), 0);
+        const uint64_t dK = lt::mdesc(sK, 0, D == 64 ? sM - sK : lt::kBlk), dV = lt::mdesc(smem_u32(sm + L::oV), 0);
         const int tiles = mode_a ? w.nit : total, per = mode_a ? 1 : items;
 #pragma unroll 1
         for (int ki = 0, r = 0, ci = 0; ki < tiles; ++ki, ci += ++r == per, r = r == per ? 0 : r) {
-            const int vs = ki % L::NV, ks_ = ki % L::NK;
+            const int slot = ki % NS;
             if (a.lengths) tc::named_bar(lt::kNbVZ + (ki & 1), kBThreads + 64);
             if (ci + 1 >= w.nit) continue;  // no state after the last chunk
-            tc::named_bar(lt::kNbKT, kBThreads + 32);
-            if (lane == 0) {
-                lt::wait(&bars[L::VF + vs], (ki / L::NV) & 1, abort, status, 306);
-                tc::fence_after_sync();
-                const uint32_t acc = r > 0;
-                const uint64_t v = dV + vs * T;
-                // D = 64: the low piece's tile is the second 64-row block of A, at a distance (the block
-                // stride field) that shrinks with the slot
-                const uint64_t k = dK + ks_ * T - (D == 64 ? (uint64_t)(ks_ * T) << 16 : 0);
+            const uint64_t v = dV + slot * T;
+            // D = 64: the low piece's tile is the second 64-row block of A, at a distance (the block
+            // stride field) that shrinks with the slot
+            const uint64_t k = dK + slot * T - (D == 64 ? (uint64_t)(slot * T) << 16 : 0);
+#pragma unroll 1
+            for (int piece = 0; piece < (D == 64 ? 1 : 2); ++piece) {
+                tc::named_bar(lt::kNbKT, kBThreads + 32);
+                if (lane == 0) {
+                    lt::wait(&bars[L::VF + slot], (ki / NS) & 1, abort, status, 306);
+                    tc::fence_after_sync();
+                    const uint32_t acc = r > 0 || piece > 0;
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    tc::mma_ss(tmem + C::S, k + ks * kMK, v + ks * kMK, I_S, ks > 0 ? 1u : acc);
-                if (D != 64)
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) tc::mma_ss(tmem + C::S, dM + ks * kMK, v + ks * kMK, I_S, 1);
-                tc::mma_commit(&bars[L::SD]);
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc::mma_ss(tmem + C::S, k + ks * kMK, v + ks * kMK, I_S, ks > 0 ? 1u : acc);
+                    tc::mma_commit(&bars[D == 64 || piece > 0 ? L::SD : L::SH]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         const int done = w.nit > 1 ? (w.nit - 1) * per : 0;
         if (lane == 0 && done > 0) lt::wait(&bars[L::SD], (done - 1) & 1, &never, nullptr, 0);
@@ -370,38 +388,35 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
             int nx = 0, nkv = 0, nv = 0;
             auto load = [&](uint32_t slot, const CUtensorMap* m, int row, int h, uint64_t* bar) {
                 tc::mbar_arrive_expect_tx(bar, L::kTile);
+#pragma unroll 1
                 for (int i = 0; i < kBlocks; ++i) lt::load_4d(sm + slot + i * lt::kBlk, m, 64 * i, row, h, w.b, bar);
-            };
-            // key / value tile ki is released (its slots of either kind may be loaded again)
-            auto released = [&](int ki) {
-                return lt::wait(&bars[L::E + ki % L::NK], (ki / L::NK) & 1, abort, status, 312);
             };
 #pragma unroll 1
             for (int it = 0, r = 0, ci = 0; it < total; ++it, ci += ++r == items, r = r == items ? 0 : r) {
                 const int row = chunk_of(ci) * kW;
                 if (!mode_b || r == 0) {
-                    const int xs = nx % L::NX;
-                    if (nx >= L::NX && !lt::wait(&bars[L::XE + xs], (nx / L::NX - 1) & 1, abort, status, 311)) break;
-                    load(L::oX + xs * L::kTile, &maps.x, row, w.s * a.rx + (mode_a ? r : 0), &bars[L::XF + xs]);
+                    const int slot = nx % NS;
+                    if (nx >= NS && !lt::wait(&bars[L::XE + slot], (nx / NS - 1) & 1, abort, status, 311)) break;
+                    load(L::oX + slot * L::kTile, &maps.x, row, w.s * a.rx + (mode_a ? r : 0), &bars[L::XF + slot]);
                     ++nx;
                 }
                 if (!mode_a || r == 0) {
-                    const int h = w.s * a.rk + (mode_b ? r : 0), ks_ = nkv % L::NK, vs = nkv % L::NV;
-                    if (nkv >= L::NK && !released(nkv - L::NK)) break;
-                    load(L::oK + ks_ * L::kTile, &maps.k, row, h, &bars[L::KF + ks_]);
+                    const int h = w.s * a.rk + (mode_b ? r : 0), slot = nkv % NS;
+                    if (nkv >= NS && !lt::wait(&bars[L::E + slot], (nkv / NS - 1) & 1, abort, status, 312)) break;
+                    load(L::oK + slot * L::kTile, &maps.k, row, h, &bars[L::KF + slot]);
+                    load(L::oV + slot * L::kTile, &maps.v, row, h, &bars[L::VF + slot]);
                     ++nkv;
-                    if (nv >= L::NV && !released(nv - L::NV)) break;
-                    load(L::oV + vs * L::kTile, &maps.v, row, h, &bars[L::VF + vs]);
-                    ++nv;
                 }
             }
+            nv = nkv;
             // drain: every load has landed
-            for (int i = max(0, nx - L::NX); i < nx; ++i)
-                lt::wait(&bars[L::XF + i % L::NX], (i / L::NX) & 1, &never, nullptr, 0);
-            for (int i = max(0, nkv - L::NK); i < nkv; ++i)
-                lt::wait(&bars[L::KF + i % L::NK], (i / L::NK) & 1, &never, nullptr, 0);
-            for (int i = max(0, nv - L::NV); i < nv; ++i)
-                lt::wait(&bars[L::VF + i % L::NV], (i / L::NV) & 1, &never, nullptr, 0);
+#pragma unroll 1
+            for (int i = max(0, nx - NS); i < nx; ++i) lt::wait(&bars[L::XF + i % NS], (i / NS) & 1, &never, nullptr, 0);
+#pragma unroll 1
+            for (int i = max(0, nv - NS); i < nv; ++i) {
+                lt::wait(&bars[L::KF + i % NS], (i / NS) & 1, &never, nullptr, 0);
+                lt::wait(&bars[L::VF + i % NS], (i / NS) & 1, &never, nullptr, 0);
+            }
         }
     } else if (warp == 2) {
         if (lane == 0) {
@@ -409,9 +424,10 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
             const int groups = mode_b ? w.nit : total, per = mode_a ? items : 1;
 #pragma unroll 1
             for (int g = 0, r = 0, ci = 0; g < groups; ++g, ci += ++r == per, r = r == per ? 0 : r) {
-                const int slot = g % L::NX;
-                if (!lt::wait(&bars[L::OS + slot], (g / L::NX) & 1, abort, status, 321)) break;
+                const int slot = g % NS;
+                if (!lt::wait(&bars[L::OS + slot], (g / NS) & 1, abort, status, 321)) break;
                 const int row = chunk_of(ci) * kW, h = w.s * a.rx + r;
+#pragma unroll 1
                 for (int i = 0; i < kBlocks; ++i)
                     if (64 * i < a.dy)
                         lt::store_4d(&maps.y, sm + L::oX + slot * L::kTile + i * lt::kBlk, 64 * i, row, h, w.b);
@@ -432,94 +448,93 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
             tc::named_bar(lt::kNbA, kAThreads);
             tc::fence_after_sync();
         };
+        // EPI-1 of item it (rows valid up to Wc): columns 64 ah .. 64 ah + 63, 16 at a time, packed over
+        // the first half of them.  Columns that every row of the warp keeps take the factor
+        // g^(i-c-15) g^(15-j); across the diagonal each has its own, 0 in the table on the masked side, where
+        // the product is selected away (the column may hold anything past the sequence).
+        auto epi1 = [&](int it, int Wc) {
+            const uint32_t tg = tmem + lanes + C::G(it) + 64 * ah;
+            wait_a(L::BG + (it & 3), (it >> 2) & 1, 331);
+            const int limit = rev ? Wc : kW, sgn = rev ? 1 : -1;
+#pragma unroll 1
+            for (int cb = 0; cb < 64; cb += 16) {
+                const int c = 64 * ah + cb;
+                uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                if (rev ? c + 15 >= row0 : c <= row0 + 31) {  // some row keeps some column
+                    uint32_t g[16];
+                    float f[16];
+                    tc::tmem_ld16(tg + cb, g);
+                    if ((rev ? c > row0 + 31 : c + 15 < row0) && c + 15 < limit) {
+                        const float base = gs[rev ? c - i : i - c - 15];
+                        float t[16];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<float4*>(t + j) = *reinterpret_cast<const float4*>(tt + j);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) lt::mul2(t[j], t[j + 1], t[j], t[j + 1], base, base);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2)
+                            lt::mul2(f[j], f[j + 1], t[j], t[j + 1], __uint_as_float(g[j]), __uint_as_float(g[j + 1]));
+                    } else {
+                        const float* fac = gs + (rev ? c - i : i - c);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[j] = fac[sgn * j];
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            f[j] = f[j] != 0.f && c + j < limit ? f[j] * __uint_as_float(g[j]) : 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) pk[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+                }
+                lt::tmem_st8(tg + cb / 2, pk);  // columns that this thread has read
+            }
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+        };
         int groups = 0, r = -1, ci = 0;
 #pragma unroll 1
         for (int it = -1; it < total; ++it) {
-            // item it = (chunk ci, r); -1: only the first Gram's EPI-1
-            const int Wc = valid_of(ci);
+            // item it = (chunk ci, r); -1: only the first EPI-1
             const bool last = r == items - 1, end_y = it >= 0 && (!mode_b || last);
-            const uint32_t ty = tmem + lanes + C::Y(groups) + ah * (D / 2);
-            if (it >= 0) {
-                if (!mode_b || r == 0) {  // EPI-C
-                    wait_a(L::BC, groups & 1, 332);
+            const int Wc = valid_of(ci), Wn = valid_of(it >= 0 && last ? ci + 1 : ci);
+            if (it >= 0) tc::named_arrive(lt::kNbGT + (it & 1), kAThreads + 32);
+#pragma unroll 1
+            for (int step = 0; step < 2; ++step) {
+                // two Gram regions: the next EPI-1, then EPI-Y; one: the other way round
+                if ((step == 0) == (C::NG == 2)) {
+                    if (it + 1 < total) epi1(it + 1, Wn);
+                } else if (end_y) {
+                    // EPI-Y, into the X tile, which the products have read
+                    wait_a(L::YD, groups & 1, 333);
+                    if (poller && !mode_b && last) tc::mbar_arrive(&bars[L::E + (mode_a ? ci : it) % NS]);
+                    unsigned char* st = sm + L::oX + (groups % NS) * L::kTile;
+                    const uint32_t ty = tmem + lanes + C::Y + ah * (D / 2);
                     const float f = a.s_carry * gp[rev ? max(Wc - i, 0) : i + 1];
+                    const bool live = i < Wc;
 #pragma unroll 1
                     for (int cb = 0; cb < D / 2; cb += 16) {
-                        uint32_t y[16];
+                        uint32_t y[16], yc[16];
                         tc::tmem_ld16(ty + cb, y);
+                        tc::tmem_ld16(ty + (C::YC - C::Y) + cb, yc);
                         tc::tmem_wait_ld();
+                        float o[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(f * __uint_as_float(y[j]));
-                        tc::tmem_st16(ty + cb, y);
-                    }
-                }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                tc::named_arrive(lt::kNbGT + (it & 1), kAThreads + 32);
-            }
-            if (it + 1 < total) {
-                // EPI-1 of the next item: columns 64 ah .. 64 ah + 63, 16 at a time, packed over the first
-                // half of them.  The factor of a column on the masked side is 0 in the table, and its product is
-                // selected away (the column may hold anything past the sequence).
-                const int Wn = valid_of(it >= 0 && last ? ci + 1 : ci);
-                const uint32_t tg = tmem + lanes + C::G(it + 1) + 64 * ah;
-                wait_a(L::BG + ((it + 1) & 3), ((it + 1) >> 2) & 1, 331);
-                const int limit = rev ? Wn : kW, sgn = rev ? 1 : -1;
-                const float* fac = gp + (rev ? 64 * ah - i : i - 64 * ah);
-#pragma unroll 1
-                for (int cb = 0; cb < 64; cb += 16) {
-                    const int c = 64 * ah + cb;
-                    uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                    if (rev ? c + 15 >= row0 : c <= row0 + 31) {  // some column of it is kept for some row
-                        uint32_t g[16];
-                        tc::tmem_ld16(tg + cb, g);
-                        float f[16];
+                        for (int j = 0; j < 16; ++j)
+                            o[j] = live ? fmaf(f, __uint_as_float(yc[j]), __uint_as_float(y[j])) : 0.f;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) f[j] = a.s_intra * fac[sgn * (cb + j)];
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float v = f[j] * __uint_as_float(g[j]);
-                            f[j] = f[j] != 0.f && c + j < limit ? v : 0.f;
+                        for (int j = 0; j < 16; j += 8) {
+                            const int col = ah * (D / 2) + cb + j;
+                            *reinterpret_cast<uint4*>(st + la_off(col / 64, i, (col % 64) / 8)) = la_pack8(o + j);
                         }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) pk[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
                     }
-                    lt::tmem_st8(tg + cb / 2, pk);  // columns that this thread has read
+                    tc::fence_before_sync();
+                    tc::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bars[L::OS + groups % NS]);
+                    ++groups;
                 }
-            }
-            if (end_y) {
-                // EPI-Y, into the X tile, which the products have read
-                wait_a(L::YD, groups & 1, 333);
-                if (poller && !mode_b && last) tc::mbar_arrive(&bars[L::E + (mode_a ? ci : it) % L::NK]);
-                unsigned char* st = sm + L::oX + (groups % L::NX) * L::kTile;
-                const bool live = i < Wc;
-#pragma unroll 1
-                for (int cb = 0; cb < D / 2; cb += 16) {
-                    uint32_t y[16];
-                    tc::tmem_ld16(ty + cb, y);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        uint4 o = make_uint4(0, 0, 0, 0);
-                        if (live) {
-                            o.x = pack_bf16x2(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
-                            o.y = pack_bf16x2(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
-                            o.z = pack_bf16x2(__uint_as_float(y[j + 4]), __uint_as_float(y[j + 5]));
-                            o.w = pack_bf16x2(__uint_as_float(y[j + 6]), __uint_as_float(y[j + 7]));
-                        }
-                        const int col = ah * (D / 2) + cb + j;
-                        *reinterpret_cast<uint4*>(st + la_off(col / 64, i, (col % 64) / 8)) = o;
-                    }
-                }
-                tc::fence_before_sync();
-                tc::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars[L::OS + groups % L::NX]);
-                ++groups;
-                // MMA-C of the next group may overwrite the region (with one; it meets this before every group
-                // but the first, so not after the last)
-                if (C::NY == 1 && it + 1 < total) tc::named_arrive(lt::kNbYR, kAThreads + 32);
             }
             if (++r == items) r = 0, ++ci;
             if (it < 0) r = 0, ci = 0;
@@ -527,8 +542,8 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
     } else {
         // -------------------------------------------- B: keys' pieces, the values' padding, the state
         const int row = 32 * q4 + lane;             // KT: row of the chunk; 16-byte chunks of it below
-        constexpr int kC = D / 16;                  // 16-byte chunks per thread
-        const int c0 = half * kC;                   // chunk index over the whole row: block c / 8, chunk c % 8
+        constexpr int kC = D / 8 / (kBWarps / 4);   // 16-byte chunks per thread
+        const int c0 = part * kC;                   // chunk index over the whole row: block c / 8, chunk c % 8
         const uint32_t lanes = (uint32_t)(32 * q4) << 16;
         const bool poller = warp == lt::kB0 && lane == 0;
         auto meet = [&]() {  // after the poller's waits
@@ -538,19 +553,19 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
         const int tiles = mode_a ? w.nit : total, per = mode_a ? 1 : items;
 #pragma unroll 1
         for (int ki = 0, r = 0, ci = 0; ki < tiles; ++ki, ci += ++r == per, r = r == per ? 0 : r) {
-            const int Wc = valid_of(ci), vs = ki % L::NV, ks_ = ki % L::NK;
+            const int Wc = valid_of(ci), slot = ki % NS;
             const bool state_now = ci + 1 < w.nit, last = r == per - 1;
-            // The Gram products that read K: with shared keys (mode a) of the chunk's last item, and then the
-            // values' padding is cleared before that.
+            // The Gram products have to have read K: with shared keys (mode a) those of the chunk's last item, and
+            // then the values' padding is cleared before that.
             if (mode_a && a.lengths) {
-                if (poller) lt::wait(&bars[L::VF + vs], (ki / L::NV) & 1, abort, status, 341);
+                if (poller) lt::wait(&bars[L::VF + slot], (ki / NS) & 1, abort, status, 341);
                 meet();
             }
             if (!mode_a) {
                 if (poller) {
-                    lt::wait(&bars[L::KF + ks_], (ki / L::NK) & 1, abort, status, 342);
+                    lt::wait(&bars[L::KF + slot], (ki / NS) & 1, abort, status, 342);
                     lt::wait(&bars[L::BG + (ki & 3)], (ki >> 2) & 1, abort, status, 343);
-                    if (a.lengths) lt::wait(&bars[L::VF + vs], (ki / L::NV) & 1, abort, status, 341);
+                    if (a.lengths) lt::wait(&bars[L::VF + slot], (ki / NS) & 1, abort, status, 341);
                 }
                 meet();
             }
@@ -558,40 +573,51 @@ __global__ void __launch_bounds__(lt::kThreads, 1) lin_out_tc_kernel(const __gri
                 if (Wc < min(kW, a.n - chunk_of(ci) * kW) && row >= Wc) {
 #pragma unroll 1
                     for (int c = c0; c < c0 + kC; ++c)
-                        *reinterpret_cast<uint4*>(sm + L::oV + vs * L::kTile + la_off(c >> 3, row, c & 7)) =
+                        *reinterpret_cast<uint4*>(sm + L::oV + slot * L::kTile + la_off(c >> 3, row, c & 7)) =
                             make_uint4(0, 0, 0, 0);
                 }
                 tc::fence_proxy_async();
                 tc::named_arrive(lt::kNbVZ + (ki & 1), kBThreads + 64);
             }
             if (!state_now) {  // no product of ours reads this tile
-                if (poller) tc::mbar_arrive(&bars[L::E + ks_]);
+                if (poller) tc::mbar_arrive(&bars[L::E + slot]);
                 continue;
             }
             if (mode_a) {
                 if (poller) {
-                    lt::wait(&bars[L::KF + ks_], (ki / L::NK) & 1, abort, status, 342);
+                    lt::wait(&bars[L::KF + slot], (ki / NS) & 1, abort, status, 342);
                     lt::wait(&bars[L::BGK], ki & 1, abort, status, 343);
                 }
                 meet();
             }
             const float wt = row < Wc ? a.s_state * gp[rev ? row : Wc - 1 - row] : 0.f;
-            unsigned char *kt = sm + L::oK + ks_ * L::kTile, *mt = sm + L::oM;
-#pragma unroll 2
-            for (int c = c0; c < c0 + kC; ++c) {
-                const uint32_t at = la_off(c >> 3, row, c & 7);
+            unsigned char *kt = sm + L::oK + slot * L::kTile, *mt = sm + L::oM;
+            uint4 low[D == 64 ? 1 : kC];
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const uint32_t at = la_off((c0 + c) >> 3, row, (c0 + c) & 7);
                 uint4 p[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
                 if (row < Wc) lt::pieces8<2>(*reinterpret_cast<const uint4*>(kt + at), wt, p);
                 *reinterpret_cast<uint4*>(kt + at) = p[0];
-                *reinterpret_cast<uint4*>(mt + at) = p[1];
+                if (D == 64) *reinterpret_cast<uint4*>(mt + at) = p[1];
+                else low[c] = p[1];
             }
             tc::fence_proxy_async();
             tc::named_arrive(lt::kNbKT, kBThreads + 32);
-            if (poller) {  // the product is done: the tile is released, the low piece may be overwritten
+            if (D != 64) {  // the low piece replaces the high one
+                if (poller) lt::wait(&bars[L::SH], ki & 1, abort, status, 346);
+                meet();
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                    *reinterpret_cast<uint4*>(kt + la_off((c0 + c) >> 3, row, (c0 + c) & 7)) = low[c];
+                tc::fence_proxy_async();
+                tc::named_arrive(lt::kNbKT, kBThreads + 32);
+            }
+            if (poller) {  // the products are done: the tile is released, the low piece may be overwritten
                 lt::wait(&bars[L::SD], ki & 1, abort, status, 345);
-                tc::mbar_arrive(&bars[L::E + ks_]);
+                tc::mbar_arrive(&bars[L::E + slot]);
                 // MMA-C of this chunk has read the state that publish() overwrites
-                if (last) lt::wait(&bars[mode_a ? L::YL : L::BC], ci & 1, abort, status, 347);
+                if (last) lt::wait(&bars[mode_a ? L::YL : L::YD], ci & 1, abort, status, 347);
             }
             if (!last) continue;
             // EPI-S
@@ -864,7 +890,7 @@ int launch_tc(const LinPass& a, bool summary, cudaStream_t st) {
         if (cudaFuncSetAttribute(lin_out_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, lt::Out<D>::kBytes) !=
             cudaSuccess)
             return -1;
-        lin_out_tc_kernel<D><<<grid, lt::kThreads, lt::Out<D>::kBytes, st>>>(m, a);
+        lin_out_tc_kernel<D><<<grid, lt::threads(D), lt::Out<D>::kBytes, st>>>(m, a);
     }
     return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
