@@ -149,6 +149,7 @@ int states(const hla2_linattn_args* a, const LinPlan& p, LinPass s, float* sums,
            float* final_state, cudaStream_t st) {
     if (p.nseg > 1 || (final_state && p.nseg > 0)) {
         s.sums = sums;
+        s.exact_sums = final_state != nullptr;
         if (run_pass(s, true, a->dtype, st)) return -1;
     }
     if (p.nseg > 1 || final_state || init)

@@ -30,6 +30,7 @@ struct LinPass {
     const int* lengths;        // [B] or NULL
     const float* carry;        // [B Hs][nseg] states entering the segments, or NULL (zero)
     int carry_t;               // they are stored dy x dx
+    int exact_sums;            // the sums end in a state that is returned: exact to float32
     float* sums;               // summary pass: [B Hs][nseg][dx dy], each segment's state from zero
     int* status;               // word that a wait which gave up is recorded in
 };

@@ -648,20 +648,22 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
 // ----------------------------------------------------------------------------------------
 // Summary kernel: Sig_B = s_state sum_i g^(distance to the segment's end) k_i v_i^T over the
 // segment's rows (all key / value heads of the state).  The weights are relative to the segment, so
-// nothing decays from tile to tile.  A tile's products accumulate in tensor memory (two regions in
-// turn) and are added to float32 registers: tensor-memory accumulation cuts bits off at every step,
-// which over thousands of rows would cost a digit of the returned state.  The pieces are made and
-// multiplied by halves of a tile (64 rows), one half while the other's products run.
+// nothing decays from tile to tile.  The decayed keys are cut into P pieces of bf16: three where the sums end in a
+// state that is returned (exact to float32), two where they only feed the carries.  A tile's products
+// accumulate in tensor memory (two regions in turn) and are added to float32 registers: accumulation
+// there cuts bits off at every step, which over thousands of rows would cost a digit of the state.
 // ----------------------------------------------------------------------------------------
 namespace lt {
-template <int D>
+template <int D, int P>
 struct Sum {
     static constexpr uint32_t kTile = (uint32_t)(D / 64) * kBlk;
-    static constexpr int NS = D == 64 ? 4 : 2;  // key / value slots
-    static constexpr uint32_t oK = 0, oV = oK + NS * kTile, oM = oV + NS * kTile, oL = oM + kTile,
-                              oZ = oL + kTile;  // D = 64: a tile of zeros beside the third piece
-    static constexpr uint32_t oBar = oZ + (D == 64 ? kTile : 0);
-    enum { KF = 0, VF = KF + NS, E = VF + NS, PE = E + NS, AD, kBars = AD + 2 };
+    static constexpr int NS = D == 64 ? 4 : 2;               // key / value slots
+    static constexpr int NP = D == 128 && P == 3 ? 1 : 2;    // buffers of the lower pieces
+    static constexpr uint32_t oK = 0, oV = oK + NS * kTile, oM = oV + NS * kTile, oL = oM + NP * kTile,
+                              oZ = oL + (P == 3 ? NP : 0) * kTile;  // D = 64: a tile of zeros beside the third piece
+    static constexpr uint32_t oGp = oZ + (D == 64 && P == 3 ? kTile : 0);  // g^0 .. g^127
+    static constexpr uint32_t oBar = oGp + 512;
+    enum { KF = 0, VF = KF + NS, E = VF + NS, AD = E + NS, kBars = AD + 2 };
     static constexpr uint32_t oMisc = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oMisc + 16 + 1024;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
@@ -669,14 +671,15 @@ struct Sum {
 constexpr int kSumThreads = 640, kSumB0 = 4, kSumBWarps = 16;  // warp 0 MMA, warp 1 loads, warps 4..19 pieces and sums
 }  // namespace lt
 
-template <int D>
+template <int D, int P>
 __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __grid_constant__ lt::Maps maps, const LinPass a) {
-    using L = lt::Sum<D>;
-    constexpr int kW = lt::kW, kBlocks = D / 64, kC = D / 64;  // kC: 16-byte chunks per thread and half tile
+    using L = lt::Sum<D, P>;
+    constexpr int kW = lt::kW, kBlocks = D / 64, kC = D / 32;  // kC: 16-byte chunks per thread and tile
     constexpr int kCols = D / 4;                               // sums per thread
     extern __shared__ unsigned char smem_raw[];
     // an offset, not a rounded pointer: the compiler then still knows the address space
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float* gp = reinterpret_cast<float*>(sm + L::oGp);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + L::oMisc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::oMisc + 4);
@@ -691,13 +694,14 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
         return;
     }
     const float log2g = log2f(lin_decay(a, w.s));
+    if (tid < kW) gp[tid] = pow_decay(log2g, (float)tid);
     if (tid == 0) {
         for (int i = 0; i < L::kBars; ++i) tc::mbar_init(&bars[i], 1);
         *abort = 0;
         tc::mbar_fence_init();
     }
     if (warp == 0) tc::tmem_alloc(tmem_holder, 2 * D);
-    if (D == 64) {
+    if (D == 64 && P == 3) {
         for (int e = tid; e < (int)(L::kTile / 16); e += lt::kSumThreads)
             *reinterpret_cast<uint4*>(sm + L::oZ + 16 * e) = make_uint4(0, 0, 0, 0);
         tc::fence_proxy_async();
@@ -709,9 +713,8 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
     volatile int never = 0;
     const int seg_rows = min(w.len, w.c1 * kW) - w.c0 * kW;  // valid rows of the segment
     float sum[kCols];
-
     constexpr int kBThreads = 32 * lt::kSumBWarps;
-    enum { kNbKT = 2, kNbDR = 4, kNbAll = 1 };  // named barriers (two each of KT: a half tile; DR: a sum region)
+    enum { kNbAll = 1, kNbKT = 2, kNbDR = 4 };  // named barriers (two of each of KT, DR: by tile parity)
 
     if (warp == 0) {
         constexpr uint32_t I_S = tc::idesc_bf16(128, D, 1, 1);
@@ -719,49 +722,56 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
         constexpr uint64_t kMK = 2048 >> 4;
         const uint32_t sK = smem_u32(sm + L::oK), sM = smem_u32(sm + L::oM), sL = smem_u32(sm + L::oL),
                        sZ = smem_u32(sm + L::oZ);
+        // D = 64: the middle piece's tile is the second 64-row block of the high one's A, the tile of zeros
+        // that of the third piece's; the distance (the block stride field, bits 16 ..) follows the slots
         const uint64_t dK = lt::mdesc(sK, 0, D == 64 ? sM - sK : lt::kBlk), dV = lt::mdesc(smem_u32(sm + L::oV), 0),
                        dM = lt::mdesc(sM, 0), dL = lt::mdesc(sL, 0, D == 64 ? sZ - sL : lt::kBlk);
+#pragma unroll 1
         for (int it = 0; it < total; ++it) {
-            const int s = it % L::NS;
+            const int s = it % L::NS, p = it % L::NP;
             const uint32_t acc = tmem + (it & 1) * D;
-            const uint64_t v = dV + s * T, k = dK + s * T - (D == 64 ? (uint64_t)(s * T) << 16 : 0);
             if (lane == 0) lt::wait(&bars[L::VF + s], (it / L::NS) & 1, abort, status, 351);
             __syncwarp();
             if (it >= 2) tc::named_bar(kNbDR + (it & 1), kBThreads + 32);
+            tc::named_bar(kNbKT + (it & 1), kBThreads + 32);
+            if (lane == 0) {
+                tc::fence_after_sync();
+                const uint64_t v = dV + s * T;
+                const uint64_t k = dK + s * T + (D == 64 ? ((uint64_t)(p * T) << 16) - ((uint64_t)(s * T) << 16) : 0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                __syncwarp();
-                tc::named_bar(kNbKT + h, kBThreads + 32);
-                if (lane == 0) {
-                    tc::fence_after_sync();
+                for (int ks = 0; ks < 8; ++ks) tc::mma_ss(acc, k + ks * kMK, v + ks * kMK, I_S, ks > 0);
+                if (D != 64) {
+                    const uint64_t m = dM + p * T;
 #pragma unroll
-                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                        tc::mma_ss(acc, k + ks * kMK, v + ks * kMK, I_S, ks > 0);
-                    if (D != 64)
-#pragma unroll
-                        for (int ks = 4 * h; ks < 4 * h + 4; ++ks) tc::mma_ss(acc, dM + ks * kMK, v + ks * kMK, I_S, 1);
-#pragma unroll
-                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks) tc::mma_ss(acc, dL + ks * kMK, v + ks * kMK, I_S, 1);
-                    tc::mma_commit(&bars[h == 0 ? L::PE : L::AD + (it & 1)]);
-                    if (h == 1) tc::mma_commit(&bars[L::E + s]);
+                    for (int ks = 0; ks < 8; ++ks) tc::mma_ss(acc, m + ks * kMK, v + ks * kMK, I_S, 1);
                 }
+                if (P == 3) {
+                    const uint64_t l = dL + p * T - (D == 64 ? (uint64_t)(p * T) << 16 : 0);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) tc::mma_ss(acc, l + ks * kMK, v + ks * kMK, I_S, 1);
+                }
+                tc::mma_commit(&bars[L::E + s]);
+                tc::mma_commit(&bars[L::AD + (it & 1)]);
             }
             __syncwarp();
         }
     } else if (warp == 1) {
         if (lane == 0) {
             int it = 0;
-            for (; it < total && !*abort; ++it) {
+#pragma unroll 1
+            for (; it < total; ++it) {
                 const int s = it % L::NS, ci = it / items, h = w.s * a.rk + it % items;
                 const int row = (rev ? w.c1 - 1 - ci : w.c0 + ci) * kW;
                 if (it >= L::NS && !lt::wait(&bars[L::E + s], (it / L::NS - 1) & 1, abort, status, 353)) break;
                 tc::mbar_arrive_expect_tx(&bars[L::KF + s], L::kTile);
                 tc::mbar_arrive_expect_tx(&bars[L::VF + s], L::kTile);
+#pragma unroll 1
                 for (int i = 0; i < kBlocks; ++i) {
                     lt::load_4d(sm + L::oK + s * L::kTile + i * lt::kBlk, &maps.k, 64 * i, row, h, w.b, &bars[L::KF + s]);
                     lt::load_4d(sm + L::oV + s * L::kTile + i * lt::kBlk, &maps.v, 64 * i, row, h, w.b, &bars[L::VF + s]);
                 }
             }
+#pragma unroll 1
             for (int i = max(0, it - L::NS); i < it; ++i) {
                 lt::wait(&bars[L::KF + i % L::NS], (i / L::NS) & 1, &never, nullptr, 0);
                 lt::wait(&bars[L::VF + i % L::NS], (i / L::NS) & 1, &never, nullptr, 0);
@@ -769,7 +779,7 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
         }
     } else if (warp >= lt::kSumB0) {
         const int wb = warp - lt::kSumB0;
-        const int r64 = 32 * (wb & 1) + lane, c0 = (wb >> 1) * kC;  // row of the half tile, first chunk
+        const int row = 32 * q4 + lane, c0 = (wb >> 2) * kC;  // row of the tile, first chunk of it
         const uint32_t ta = tmem + ((uint32_t)(32 * q4) << 16) + (wb >> 2) * kCols;
         const bool poller = wb == 0 && lane == 0;
         auto meet = [&]() {  // after the poller's waits
@@ -778,8 +788,11 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
         };
 #pragma unroll
         for (int j = 0; j < kCols; ++j) sum[j] = 0.f;
-        // tile it's products are done: the sums go to registers, the region is released
+        // tile it's products are done (so its pieces' buffers are free): the sums go to registers, the
+        // region is released
         auto drain = [&](int it) {
+            if (poller) lt::wait(&bars[L::AD + (it & 1)], (it >> 1) & 1, abort, status, 357);
+            meet();
             tc::fence_after_sync();
 #pragma unroll
             for (int cb = 0; cb < kCols; cb += 16) {
@@ -792,45 +805,42 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
             tc::fence_before_sync();
             if (it + 2 < total) tc::named_arrive(kNbDR + (it & 1), kBThreads + 32);
         };
-        for (int it = 0; it < total; ++it) {
-            const int s = it % L::NS, ci = it / items;
-            const int r0 = (rev ? w.c1 - 1 - ci : w.c0 + ci) * kW, Wc = min(kW, w.len - r0);
-            unsigned char *kt = sm + L::oK + s * L::kTile, *mt = sm + L::oM, *lo = sm + L::oL;
-            const bool padded = Wc < min(kW, a.n - r0);  // padding rows of the values may hold anything
-            if (poller) {
-                lt::wait(&bars[L::KF + s], (it / L::NS) & 1, abort, status, 354);
-                if (padded) lt::wait(&bars[L::VF + s], (it / L::NS) & 1, abort, status, 356);
-                if (it > 0) lt::wait(&bars[L::PE], (it - 1) & 1, abort, status, 355);  // half 0's lower pieces are free
-            }
-            meet();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = 64 * h + r64, at_seg = r0 - w.c0 * kW + row;  // row within the segment
-                const float wt =
-                    row < Wc ? a.s_state * pow_decay(log2g, (float)(rev ? at_seg : seg_rows - 1 - at_seg)) : 0.f;
-                if (h == 1 && it > 0) {  // tile it - 1 is done as a whole
-                    if (poller) lt::wait(&bars[L::AD + ((it - 1) & 1)], ((it - 1) >> 1) & 1, abort, status, 357);
-                    meet();
+#pragma unroll 1
+        for (int it = 0, r = 0, ci = 0; it <= total; ++it, ci += ++r == items, r = r == items ? 0 : r) {
+            if (L::NP == 1 && it > 0) drain(it - 1);
+            if (it < total) {
+                const int s = it % L::NS;
+                const int r0 = (rev ? w.c1 - 1 - ci : w.c0 + ci) * kW, Wc = min(kW, w.len - r0);
+                const bool padded = Wc < min(kW, a.n - r0);  // padding rows of the values may hold anything
+                if (poller) {
+                    lt::wait(&bars[L::KF + s], (it / L::NS) & 1, abort, status, 354);
+                    if (padded) lt::wait(&bars[L::VF + s], (it / L::NS) & 1, abort, status, 356);
                 }
+                // g^(distance): of the tile's near end, and within the tile
+                const int first = r0 - w.c0 * kW;  // the tile's first row in the segment
+                const float near = pow_decay(log2g, (float)(rev ? first : seg_rows - first - Wc));
+                const float wt = row < Wc ? a.s_state * near * gp[rev ? row : Wc - 1 - row] : 0.f;
+                unsigned char *kt = sm + L::oK + s * L::kTile, *mt = sm + L::oM + (it % L::NP) * L::kTile,
+                              *lo = sm + L::oL + (it % L::NP) * L::kTile;
+                meet();
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
-                    uint4 x[3] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                    uint4 x[P];
+#pragma unroll
+                    for (int p = 0; p < P; ++p) x[p] = make_uint4(0, 0, 0, 0);
                     const uint32_t at = la_off((c0 + c) >> 3, row, (c0 + c) & 7);
-                    if (row < Wc) lt::pieces8<3>(*reinterpret_cast<const uint4*>(kt + at), wt, x);
+                    if (row < Wc) lt::pieces8<P>(*reinterpret_cast<const uint4*>(kt + at), wt, x);
                     *reinterpret_cast<uint4*>(kt + at) = x[0];
                     *reinterpret_cast<uint4*>(mt + at) = x[1];
-                    *reinterpret_cast<uint4*>(lo + at) = x[2];
+                    if (P == 3) *reinterpret_cast<uint4*>(lo + at) = x[P - 1];
                     if (padded && row >= Wc)
                         *reinterpret_cast<uint4*>(sm + L::oV + s * L::kTile + at) = make_uint4(0, 0, 0, 0);
                 }
                 tc::fence_proxy_async();
-                tc::named_arrive(kNbKT + h, kBThreads + 32);
+                tc::named_arrive(kNbKT + (it & 1), kBThreads + 32);
             }
-            if (it > 0) drain(it - 1);
+            if (L::NP == 2 && it > 0) drain(it - 1);
         }
-        if (poller) lt::wait(&bars[L::AD + ((total - 1) & 1)], ((total - 1) >> 1) & 1, &never, status, 358);
-        meet();
-        drain(total - 1);
     }
     __syncwarp();
     __syncthreads();
@@ -873,25 +883,38 @@ bool lin_map(CUtensorMap* m, const hla2_view& w, int B, int heads, int n, int Dr
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The dynamic shared memory limit of a kernel, set once per device.
+template <class K>
+bool allow_smem(K kernel, uint32_t bytes, bool (&done)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 64 && done[dev]) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    if (dev < 64) done[dev] = true;
+    return true;
+}
+
+template <int D, int P>
+int launch_sum(const lt::Maps& m, const LinPass& a, cudaStream_t st) {
+    static bool done[64];
+    if (!allow_smem(lin_sum_tc_kernel<D, P>, lt::Sum<D, P>::kBytes, done)) return -1;
+    lin_sum_tc_kernel<D, P><<<dim3(a.B * a.Hs, a.nseg), lt::kSumThreads, lt::Sum<D, P>::kBytes, st>>>(m, a);
+    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
 template <int D>
 int launch_tc(const LinPass& a, bool summary, cudaStream_t st) {
     lt::Maps m;
     const int xh = a.Hs * a.rx, kh = a.Hs * a.rk;
     if (!lin_map(&m.k, a.k, a.B, kh, a.n, a.dx) || !lin_map(&m.v, a.v, a.B, kh, a.n, a.dy)) return -1;
-    const dim3 grid(a.B * a.Hs, a.nseg);
     if (summary) {
         m.x = m.y = m.k;
-        if (cudaFuncSetAttribute(lin_sum_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, lt::Sum<D>::kBytes) !=
-            cudaSuccess)
-            return -1;
-        lin_sum_tc_kernel<D><<<grid, lt::kSumThreads, lt::Sum<D>::kBytes, st>>>(m, a);
-    } else {
-        if (!lin_map(&m.x, a.x, a.B, xh, a.n, a.dx) || !lin_map(&m.y, a.y, a.B, xh, a.n, a.dy)) return -1;
-        if (cudaFuncSetAttribute(lin_out_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, lt::Out<D>::kBytes) !=
-            cudaSuccess)
-            return -1;
-        lin_out_tc_kernel<D><<<grid, lt::threads(D), lt::Out<D>::kBytes, st>>>(m, a);
+        return a.exact_sums ? launch_sum<D, 3>(m, a, st) : launch_sum<D, 2>(m, a, st);
     }
+    if (!lin_map(&m.x, a.x, a.B, xh, a.n, a.dx) || !lin_map(&m.y, a.y, a.B, xh, a.n, a.dy)) return -1;
+    static bool done[64];
+    if (!allow_smem(lin_out_tc_kernel<D>, lt::Out<D>::kBytes, done)) return -1;
+    lin_out_tc_kernel<D><<<dim3(a.B * a.Hs, a.nseg), lt::threads(D), lt::Out<D>::kBytes, st>>>(m, a);
     return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
