@@ -16,7 +16,7 @@
 // 32-byte sectors from G = 64 on.  The order of k inside a product is free as long as A and B agree;
 // a word's pairs are (k, k + 4), and x is paired the same way.
 //
-// A CTA forms 16 RT outputs; its eight warps take every eighth batch of k, the next batch's weights in
+// A CTA forms 16 outputs; its eight warps take every eighth batch of k, the next batch's weights in
 // flight while one is computed, and their sums meet in shared memory in a fixed order.
 #include "common.cuh"
 
@@ -61,8 +61,7 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// k per warp step: what a double buffer of a warp's weights takes of its registers
-__host__ __device__ constexpr int batch_of(int RT) { return RT == 2 ? 128 : 256; }
+constexpr int kBatch = 128;  // k per warp step
 
 // U consecutive values of a row's scales or zero points
 template <typename T, int U>
@@ -94,80 +93,68 @@ __device__ __forceinline__ void load_few(Few<T, U>& f, const T* p, int count, bo
     }
 }
 
-// What a warp reads of 16 RT rows for one batch
-template <typename T, int G, int RT>
+// What a warp reads of 16 rows for one batch
+template <typename T, int G>
 struct Weights {
-    static constexpr int U = batch_of(RT) / G, J = G / 32;  // groups, words of a row and group
-    uint32_t w[RT][2][U][J];
-    alignas(16) Few<T, U> s[RT][2];
-    alignas(16) Few<uint8_t, U> z[RT][2];
+    static constexpr int U = kBatch / G, J = G / 32;  // groups, words of a row and group
+    uint32_t w[2][U][J];
+    alignas(16) Few<T, U> s[2];
+    alignas(16) Few<uint8_t, U> z[2];
 };
 
-template <typename T, int NT, int G, int RT>
-__global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const W4Args a, const bool aligned) {
-    constexpr int kPieces = sizeof(T) == 4 ? 3 : 1, U = batch_of(RT) / G, J = G / 32, kBatch = batch_of(RT);
-    __shared__ float red[kWarps][16 * RT][NT * 8 + 1];
+template <typename T, int NT, int G>
+__global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 3 : 2) w4_kernel(const W4Args a, const bool aligned) {
+    constexpr int kPieces = sizeof(T) == 4 ? 3 : 1, U = kBatch / G, J = G / 32;
+    __shared__ float red[kWarps][16][NT * 8 + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int n0 = blockIdx.x * 16 * RT, gpr = a.K / G;
+    const int n0 = blockIdx.x * 16, gpr = a.K / G;
     const T* scales = static_cast<const T*>(a.scales);
-    int row[RT][2];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        row[t][0] = min(n0 + 16 * t + g, a.N - 1);
-        row[t][1] = min(n0 + 16 * t + g + 8, a.N - 1);
-    }
+    const int row[2] = {min(n0 + g, a.N - 1), min(n0 + g + 8, a.N - 1)};
     const int cols = a.M * kPieces;
-    float sum[RT][NT][4];
+    float sum[NT][4];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) sum[r][t][0] = sum[r][t][1] = sum[r][t][2] = sum[r][t][3] = 0.f;
+    for (int t = 0; t < NT; ++t) sum[t][0] = sum[t][1] = sum[t][2] = sum[t][3] = 0.f;
 
-    auto load = [&](Weights<T, G, RT>& b, int k0) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
+    auto load = [&](Weights<T, G>& b, int k0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint8_t* p = a.w + (size_t)row[r][h] * (a.K / 2) + (k0 + c * (G / 4)) / 2;
+                const uint8_t* p = a.w + (size_t)row[h] * (a.K / 2) + (k0 + c * (G / 4)) / 2;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const bool in = k0 + u * G < a.K;
                     if constexpr (J == 4) {
                         const uint4 v = in ? __ldcs(reinterpret_cast<const uint4*>(p + u * G / 2)) : make_uint4(0, 0, 0, 0);
-                        b.w[r][h][u][0] = v.x, b.w[r][h][u][1] = v.y, b.w[r][h][u][2] = v.z, b.w[r][h][u][3] = v.w;
+                        b.w[h][u][0] = v.x, b.w[h][u][1] = v.y, b.w[h][u][2] = v.z, b.w[h][u][3] = v.w;
                     } else if constexpr (J == 2) {
                         const uint2 v = in ? __ldcs(reinterpret_cast<const uint2*>(p + u * G / 2)) : make_uint2(0, 0);
-                        b.w[r][h][u][0] = v.x, b.w[r][h][u][1] = v.y;
+                        b.w[h][u][0] = v.x, b.w[h][u][1] = v.y;
                     } else {
-                        b.w[r][h][u][0] = in ? __ldcs(reinterpret_cast<const uint32_t*>(p + u * G / 2)) : 0u;
+                        b.w[h][u][0] = in ? __ldcs(reinterpret_cast<const uint32_t*>(p + u * G / 2)) : 0u;
                     }
                 }
-                const size_t at = (size_t)row[r][h] * gpr + k0 / G;
+                const size_t at = (size_t)row[h] * gpr + k0 / G;
                 const int count = min(U, gpr - k0 / G);
-                load_few<T, U>(b.s[r][h], scales + at, count, aligned);
-                if (a.zeros) load_few<uint8_t, U>(b.z[r][h], a.zeros + at, count, aligned);
+                load_few<T, U>(b.s[h], scales + at, count, aligned);
+                if (a.zeros) load_few<uint8_t, U>(b.z[h], a.zeros + at, count, aligned);
             }
     };
-    auto compute = [&](const Weights<T, G, RT>& b, int k0) {
+    auto compute = [&](const Weights<T, G>& b, int k0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (k0 + u * G >= a.K) break;
-            float acc[RT][NT][4], xs[NT][4];
+            float acc[NT][4], xs[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 xs[t][0] = xs[t][1] = xs[t][2] = xs[t][3] = 0.f;
-#pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r][t][0] = acc[r][t][1] = acc[r][t][2] = acc[r][t][3] = 0.f;
+                acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
             }
-            float zf[RT][2];
-            uint32_t zz[RT][2];
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
+            float zf[2];
+            uint32_t zz[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t z = a.zeros ? b.z[r][h].v[u] : 8u;
-                    zf[r][h] = (float)(16u + z);
-                    zz[r][h] = 0x41804180u | (z * 0x00080008u);
+                    const uint32_t z = a.zeros ? b.z[h].v[u] : 8u;
+                    zf[h] = (float)(16u + z);
+                    zz[h] = 0x41804180u | (z * 0x00080008u);
                 }
 #pragma unroll
             for (int j = 0; j < J; ++j) {
@@ -191,25 +178,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const W4Args a, cons
                         }
                     }
                 }
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
+                {
                     uint32_t q[2][4];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t w = b.w[r][h][u][j];
+                        const uint32_t w = b.w[h][u][j];
                         q[h][0] = ((w << 3) & 0x00780078u) | 0x41804180u;
                         q[h][1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
                         q[h][2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
                         q[h][3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
                         if (kPieces == 3)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) q[h][i] = sub2(q[h][i], zz[r][h]);
+                            for (int i = 0; i < 4; ++i) q[h][i] = sub2(q[h][i], zz[h]);
                     }
                     const uint32_t A0[4] = {q[0][0], q[1][0], q[0][1], q[1][1]}, A1[4] = {q[0][2], q[1][2], q[0][3], q[1][3]};
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        mma_16816(acc[r][t], A0, x[t][0], x[t][1]);
-                        mma_16816(acc[r][t], A1, x[t][2], x[t][3]);
+                        mma_16816(acc[t], A0, x[t][0], x[t][1]);
+                        mma_16816(acc[t], A1, x[t][2], x[t][3]);
                     }
                 }
                 if (kPieces == 1) {
@@ -221,26 +207,25 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const W4Args a, cons
                     }
                 }
             }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const float f0 = to_f32(b.s[r][0].v[u]), f1 = to_f32(b.s[r][1].v[u]);
+            {
+                const float f0 = to_f32(b.s[0].v[u]), f1 = to_f32(b.s[1].v[u]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     if (kPieces == 1) {
-                        acc[r][t][0] = fmaf(-zf[r][0], xs[t][0], acc[r][t][0]);
-                        acc[r][t][1] = fmaf(-zf[r][0], xs[t][1], acc[r][t][1]);
-                        acc[r][t][2] = fmaf(-zf[r][1], xs[t][0], acc[r][t][2]);
-                        acc[r][t][3] = fmaf(-zf[r][1], xs[t][1], acc[r][t][3]);
+                        acc[t][0] = fmaf(-zf[0], xs[t][0], acc[t][0]);
+                        acc[t][1] = fmaf(-zf[0], xs[t][1], acc[t][1]);
+                        acc[t][2] = fmaf(-zf[1], xs[t][0], acc[t][2]);
+                        acc[t][3] = fmaf(-zf[1], xs[t][1], acc[t][3]);
                     }
-                    sum[r][t][0] = fmaf(f0, acc[r][t][0], sum[r][t][0]);
-                    sum[r][t][1] = fmaf(f0, acc[r][t][1], sum[r][t][1]);
-                    sum[r][t][2] = fmaf(f1, acc[r][t][2], sum[r][t][2]);
-                    sum[r][t][3] = fmaf(f1, acc[r][t][3], sum[r][t][3]);
+                    sum[t][0] = fmaf(f0, acc[t][0], sum[t][0]);
+                    sum[t][1] = fmaf(f0, acc[t][1], sum[t][1]);
+                    sum[t][2] = fmaf(f1, acc[t][2], sum[t][2]);
+                    sum[t][3] = fmaf(f1, acc[t][3], sum[t][3]);
                 }
             }
         }
     };
-    Weights<T, G, RT> b0, b1;
+    Weights<T, G> b0, b1;
     const int step = kWarps * kBatch;
     int k0 = warp * kBatch;
     if (k0 < a.K) load(b0, k0);
@@ -252,19 +237,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const W4Args a, cons
         compute(b1, k0 + step);
     }
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float* p = &red[warp][16 * r + g][t * 8 + 2 * c];
-            p[0] = sum[r][t][0];
-            p[1] = sum[r][t][1];
-            p = &red[warp][16 * r + g + 8][t * 8 + 2 * c];
-            p[0] = sum[r][t][2];
-            p[1] = sum[r][t][3];
+            float* p = &red[warp][g][t * 8 + 2 * c];
+            p[0] = sum[t][0];
+            p[1] = sum[t][1];
+            p = &red[warp][g + 8][t * 8 + 2 * c];
+            p[0] = sum[t][2];
+            p[1] = sum[t][3];
         }
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * RT * a.M; e += kWarps * 32) {
-        const int r = e % (16 * RT), m = e / (16 * RT);
+    for (int e = threadIdx.x; e < 16 * a.M; e += kWarps * 32) {
+        const int r = e & 15, m = e >> 4;
         if (n0 + r >= a.N) continue;
         float t = 0.f;
 #pragma unroll
@@ -277,14 +260,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const W4Args a, cons
 
 template <typename T, int NT, int G>
 int launch_w4_g(const W4Args& a, cudaStream_t st) {
-    const bool aligned = (a.K / G) % (256 / G) == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 15u) == 0 &&
+    const bool aligned = (a.K / G) % (kBatch / G) == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 15u) == 0 &&
                          (reinterpret_cast<uintptr_t>(a.zeros) & 15u) == 0;
-    // 32 rows share x's loads and pairing; 16 fill the GPU sooner.  float32 x (up to six columns of
-    // eight) has no registers for 32.
-    if (NT <= 2 && sizeof(T) == 2 && (a.N + 31) / 32 >= 2 * 152)
-        w4_kernel<T, NT, G, (NT <= 2 && sizeof(T) == 2) ? 2 : 1><<<(a.N + 31) / 32, kWarps * 32, 0, st>>>(a, aligned);
-    else
-        w4_kernel<T, NT, G, 1><<<(a.N + 15) / 16, kWarps * 32, 0, st>>>(a, aligned);
+    w4_kernel<T, NT, G><<<(a.N + 15) / 16, kWarps * 32, 0, st>>>(a, aligned);
     return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 template <typename T, int NT>
