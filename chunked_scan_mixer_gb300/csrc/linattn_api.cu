@@ -115,7 +115,8 @@ LinPlan lin_plan(const hla2_linattn_args* a, int W, int slots) {
 
 LinPlan plan_of(const hla2_linattn_args* a) {
     if (a->dtype == HLA2_BF16) return lin_plan(a, 128, sm_count());
-    return lin_plan(a, lin_simt_width(a->d, a->dv), sm_count() * lin_simt_ctas(a->d, a->dv, 1));
+    const int sms = sm_count(), W = lin_simt_width(a->d, a->dv, (long long)a->B * a->Hk, a->n, sms);
+    return lin_plan(a, W, sms * lin_simt_ctas(a->d, a->dv, W));
 }
 
 size_t state_array_bytes(const hla2_linattn_args* a, const LinPlan& p) {

@@ -43,9 +43,15 @@ __host__ __device__ inline int lin_len(const int* lengths, int b, int n) {
 
 __device__ __forceinline__ float lin_decay(const LinPass& a, int s) { return a.gamma ? __ldg(a.gamma + s) : 1.0f; }
 
-// SIMT passes (float32 arithmetic, any type and size); W = lin_simt_width(dx, dy).
-int lin_simt_width(int dx, int dy);
-int lin_simt_ctas(int dx, int dy, int rk);  // resident CTAs per SM
+// Every kernel here is launched so that it may start while the one before it on the stream drains
+// (launch_pdl): it sets itself up, then waits (pdl_wait) before it touches global memory.
+
+// SIMT passes (float32 arithmetic, any type and size); W = lin_simt_width(dx, dy, state heads, n, SMs):
+// 64 rows (32 where a dimension is 128, for the shared memory), and half or a quarter of that while the
+// chunks of all heads would not give every SM one.  Two heads of 1023 rows, d = 32, dv = 64: the output
+// pass took 31 us with 64 rows a chunk (32 CTAs), 8 us with 16 (128 CTAs).
+int lin_simt_width(int dx, int dy, long long heads, int n, int sms);
+int lin_simt_ctas(int dx, int dy, int W);  // resident CTAs per SM
 int launch_lin_simt(const LinPass& a, bool summary, bool is_bf16, cudaStream_t st);
 
 // Tensor-core passes (bf16, any size; linattn_tc.cu): W = 128, one CTA per SM.

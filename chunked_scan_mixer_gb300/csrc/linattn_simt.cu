@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
           *gp = sm + L.gp;
     const int tid = threadIdx.x;
     const int seg = blockIdx.y, bs = blockIdx.x, b = bs / a.Hs, s = bs % a.Hs;
+    pdl_trigger();
+    pdl_wait();
     const int len = lin_len(a.lengths, b, a.n);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
     const float log2g = log2f(lin_decay(a, s));
@@ -198,8 +200,7 @@ int launch_simt_t(const LinPass& a, bool summary, cudaStream_t st) {
     const size_t smem = lin_smem(a.dx, a.dy, a.W, !summary && a.rk > 1).total * sizeof(float);
     auto kfn = summary ? lin_simt_kernel<T, true> : lin_simt_kernel<T, false>;
     if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -1;
-    kfn<<<dim3(a.B * a.Hs, a.nseg), kThreads, smem, st>>>(a);
-    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+    return launch_pdl(kfn, dim3(a.B * a.Hs, a.nseg), dim3(kThreads), smem, st, a) == cudaSuccess ? 0 : -1;
 }
 
 // ---- scan over the segments -----------------------------------------------------------
@@ -210,6 +211,8 @@ __global__ void __launch_bounds__(kThreads)
                     int n, int seg_rows, int nseg, int elems, int rev) {
     const int bs = blockIdx.x, b = bs / Hs;
     const int e = blockIdx.y * kThreads + threadIdx.x;
+    pdl_trigger();
+    pdl_wait();
     if (e >= elems) return;
     const float g = gamma ? __ldg(gamma + bs % Hs) : 1.f;
     const float log2g = log2f(g);
@@ -218,13 +221,26 @@ __global__ void __launch_bounds__(kThreads)
     if (init && rev) cur /= g;
     const float* src = sums + (size_t)bs * nseg * elems + e;
     float* dst = carry ? carry + (size_t)bs * nseg * elems + e : nullptr;
-    const bool need_last = fin != nullptr;
-    for (int i = 0; i < nseg; ++i) {
-        const int s = rev ? nseg - 1 - i : i;
-        if (dst) dst[(size_t)s * elems] = cur;
-        if (i == nseg - 1 && !need_last) break;
-        const int rows = max(0, min(seg_rows, len - s * seg_rows));
-        cur = fmaf(pow_decay(log2g, (float)rows), cur, src[(size_t)s * elems]);
+    const int steps = fin ? nseg : nseg - 1;  // the last sum only enters the final state
+    constexpr int kAhead = 8;                 // loads in flight
+    for (int i0 = 0; i0 < nseg; i0 += kAhead) {
+        float v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+            v[j] = i < steps ? src[(size_t)(rev ? nseg - 1 - i : i) * elems] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+            if (i >= nseg) break;
+            const int s = rev ? nseg - 1 - i : i;
+            if (dst) dst[(size_t)s * elems] = cur;
+            if (i < steps) {
+                const int rows = max(0, min(seg_rows, len - s * seg_rows));
+                cur = fmaf(pow_decay(log2g, (float)rows), cur, v[j]);
+            }
+        }
     }
     if (fin) fin[(size_t)bs * elems + e] = rev ? g * cur : cur;
 }
@@ -312,9 +328,13 @@ int launch_step_t(float* state, const void* q, const void* k, const void* v, voi
 
 }  // namespace
 
-int lin_simt_width(int dx, int dy) { return dx > 64 || dy > 64 ? 32 : 64; }
-int lin_simt_ctas(int dx, int dy, int rk) {
-    return simt::min_ctas(2, simt::ctas_per_sm(lin_smem(dx, dy, lin_simt_width(dx, dy), rk > 1).total * sizeof(float)));
+int lin_simt_width(int dx, int dy, long long heads, int n, int sms) {
+    int W = dx > 64 || dy > 64 ? 32 : 64;
+    while (W > 16 && heads * ((n + W - 1) / W) < sms) W /= 2;
+    return W;
+}
+int lin_simt_ctas(int dx, int dy, int W) {
+    return simt::min_ctas(2, simt::ctas_per_sm(lin_smem(dx, dy, W, false).total * sizeof(float)));
 }
 
 int launch_lin_simt(const LinPass& a, bool summary, bool is_bf16, cudaStream_t st) {
@@ -326,9 +346,10 @@ int launch_lin_scan(const float* sums, float* carry, const float* init, float* f
                     const int* lengths, int B, int Hs, int n, int seg_rows, int nseg, int elems, int rev,
                     cudaStream_t st) {
     if (B * Hs == 0) return 0;
-    lin_scan_kernel<<<dim3(B * Hs, (elems + kThreads - 1) / kThreads), kThreads, 0, st>>>(
-        sums, carry, init, final_state, gamma, lengths, Hs, n, seg_rows, nseg, elems, rev);
-    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+    return launch_pdl(lin_scan_kernel, dim3(B * Hs, (elems + kThreads - 1) / kThreads), dim3(kThreads), 0, st, sums, carry,
+                      init, final_state, gamma, lengths, Hs, n, seg_rows, nseg, elems, rev) == cudaSuccess
+               ? 0
+               : -1;
 }
 
 int launch_lin_step(float* state, const void* q, const void* k, const void* v, void* out, int N, int H, int Hk, int d,

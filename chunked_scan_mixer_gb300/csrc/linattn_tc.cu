@@ -213,6 +213,17 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
     int* status = a.status;
 
     const int tid = threadIdx.x, warp = lt::uniform(tid >> 5), lane = tid & 31;
+    pdl_trigger();
+    if (tid == 0) {
+        for (int i = 0; i < L::kBars; ++i) {
+            const bool by_a = i >= L::OS && i < L::OS + NS;   // one arrival per A warp
+            const bool by_two = i >= L::E && i < L::E + NS;   // A (or MMA-Y's commit) and B
+            tc::mbar_init(&bars[i], by_a ? lt::kAWarps : by_two ? 2 : 1);
+        }
+        *abort = 0;
+        tc::mbar_fence_init();
+    }
+    pdl_wait();
     const lt::Where w = lt::locate(a);
     const bool rev = a.rev != 0, mode_a = a.rx > 1, mode_b = a.rk > 1;
     const int items = mode_a ? a.rx : a.rk, total = w.nit * items;
@@ -236,15 +247,6 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
         if (tid >= kW) gp[tid - kW] = g;
     }
     if (tid < 16) tt[tid] = pow_decay(log2g, (float)(rev ? tid : 15 - tid));
-    if (tid == 0) {
-        for (int i = 0; i < L::kBars; ++i) {
-            const bool by_a = i >= L::OS && i < L::OS + NS;   // one arrival per A warp
-            const bool by_two = i >= L::E && i < L::E + NS;   // A (or MMA-Y's commit) and B
-            tc::mbar_init(&bars[i], by_a ? lt::kAWarps : by_two ? 2 : 1);
-        }
-        *abort = 0;
-        tc::mbar_fence_init();
-    }
     if (warp == 0) tc::tmem_alloc(tmem_holder, 512);
 
     // B thread: state row sr, columns sc0 .. sc0 + kSC - 1.  D = 64: rows 64.. hold the low pieces' sums.
@@ -685,6 +687,13 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::oMisc + 4);
     int* status = a.status;
     const int tid = threadIdx.x, warp = lt::uniform(tid >> 5), lane = tid & 31, q4 = warp & 3;
+    pdl_trigger();
+    if (tid == 0) {
+        for (int i = 0; i < L::kBars; ++i) tc::mbar_init(&bars[i], 1);
+        *abort = 0;
+        tc::mbar_fence_init();
+    }
+    pdl_wait();
     const lt::Where w = lt::locate(a);
     const bool rev = a.rev != 0;
     const int items = a.rk, total = w.nit * items;
@@ -695,11 +704,6 @@ __global__ void __launch_bounds__(lt::kSumThreads, 1) lin_sum_tc_kernel(const __
     }
     const float log2g = log2f(lin_decay(a, w.s));
     if (tid < kW) gp[tid] = pow_decay(log2g, (float)tid);
-    if (tid == 0) {
-        for (int i = 0; i < L::kBars; ++i) tc::mbar_init(&bars[i], 1);
-        *abort = 0;
-        tc::mbar_fence_init();
-    }
     if (warp == 0) tc::tmem_alloc(tmem_holder, 2 * D);
     if (D == 64 && P == 3) {
         for (int e = tid; e < (int)(L::kTile / 16); e += lt::kSumThreads)
@@ -898,8 +902,10 @@ template <int D, int P>
 int launch_sum(const lt::Maps& m, const LinPass& a, cudaStream_t st) {
     static bool done[64];
     if (!allow_smem(lin_sum_tc_kernel<D, P>, lt::Sum<D, P>::kBytes, done)) return -1;
-    lin_sum_tc_kernel<D, P><<<dim3(a.B * a.Hs, a.nseg), lt::kSumThreads, lt::Sum<D, P>::kBytes, st>>>(m, a);
-    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+    return launch_pdl(lin_sum_tc_kernel<D, P>, dim3(a.B * a.Hs, a.nseg), dim3(lt::kSumThreads), lt::Sum<D, P>::kBytes, st, m,
+                      a) == cudaSuccess
+               ? 0
+               : -1;
 }
 
 template <int D>
@@ -914,8 +920,10 @@ int launch_tc(const LinPass& a, bool summary, cudaStream_t st) {
     if (!lin_map(&m.x, a.x, a.B, xh, a.n, a.dx) || !lin_map(&m.y, a.y, a.B, xh, a.n, a.dy)) return -1;
     static bool done[64];
     if (!allow_smem(lin_out_tc_kernel<D>, lt::Out<D>::kBytes, done)) return -1;
-    lin_out_tc_kernel<D><<<dim3(a.B * a.Hs, a.nseg), lt::threads(D), lt::Out<D>::kBytes, st>>>(m, a);
-    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+    return launch_pdl(lin_out_tc_kernel<D>, dim3(a.B * a.Hs, a.nseg), dim3(lt::threads(D)), lt::Out<D>::kBytes, st, m, a) ==
+                   cudaSuccess
+               ? 0
+               : -1;
 }
 
 }  // namespace
