@@ -138,7 +138,7 @@ LinPass base_pass(const hla2_linattn_args* a, const LinPlan& p) {
     s.nchunks = p.nchunks;
     s.seg_chunks = p.seg_chunks;
     s.nseg = p.nseg;
-    s.s_intra = s.s_carry = s.s_state = 1.f;
+    s.s_col = s.s_fin = s.s_state = 1.f;
     s.gamma = a->gamma;
     s.lengths = a->lengths;
     s.status = static_cast<int*>(a->workspace);
@@ -204,7 +204,7 @@ int hla2_linattn_forward(const hla2_linattn_args* args, hla2_view out, float* fi
     s.x = a.q, s.k = a.k, s.v = a.v, s.y = out;
     s.rx = a.H / a.Hk;
     s.dx = a.d, s.dy = a.dv;
-    s.s_intra = s.s_carry = a.scale;
+    s.s_fin = a.scale;
     if (states(&a, p, s, sums, carry, a.init_state, final_state, st)) return launch_failed("linear attention states");
     if (p.nseg == 0) return ok();
     s.carry = p.nseg > 1 || a.init_state ? carry : nullptr;
@@ -263,7 +263,7 @@ int hla2_linattn_backward(const hla2_linattn_args* args, hla2_view dout, hla2_vi
         s.rx = group;
         s.dx = a.dv, s.dy = a.d;
         s.carry_t = 1;
-        s.s_intra = s.s_carry = a.scale;
+        s.s_fin = a.scale;
         if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention dq pass");
     }
     // reverse states of q, dout (scaled); dv, dk
@@ -272,7 +272,7 @@ int hla2_linattn_backward(const hla2_linattn_args* args, hla2_view dout, hla2_vi
     s.rk = group;
     s.k = a.q, s.v = dout;
     s.dx = a.d, s.dy = a.dv;
-    s.s_intra = s.s_state = a.scale;
+    s.s_col = s.s_state = a.scale;
     if (states(&a, p, s, at, at + sf, dfinal_state, dinit_state, st))
         return launch_failed("linear attention reverse states");
     if (p.nseg == 0) return ok();

@@ -2,7 +2,7 @@
 // (linattn_api.cu composes the passes; linattn_simt.cu and linattn_tc.cu run them).
 //
 // Every pass is the same scan over rows t of one state head, forward or in reverse:
-//     y_t = s_intra sum_i g^|t-i| (x_t . k_i) v_i + s_carry g^(distance to the carry) x_t^T Sig
+//     y_t = s_fin (s_col sum_i g^|t-i| (x_t . k_i) v_i + g^(distance to the carry) x_t^T Sig)
 // over the valid rows i <= t (reverse: i >= t) of t's segment, Sig (dx x dy, float32) being the
 // state that enters the segment:  forward  Sig = sum_i g^(t0-1-i) k_i v_i^T  (the state
 // before the segment's first row t0),  reverse  Sig = sum_i g^(i-t1) k_i v_i^T  (t1 the row
@@ -25,7 +25,7 @@ struct LinPass {
     int n, dx, dy;
     int W, nchunks, seg_chunks, nseg;
     int rev;
-    float s_intra, s_carry, s_state;  // s_state: factor of k v^T in the state
+    float s_col, s_fin, s_state;  // s_state: factor of k v^T in the state
     const float* gamma;        // [Hs] or NULL
     const int* lengths;        // [B] or NULL
     const float* carry;        // [B Hs][nseg] states entering the segments, or NULL (zero)

@@ -4,7 +4,7 @@
 //
 // Chunk pass.  One CTA runs the chunks of one segment of one state head.  Per chunk of W rows
 // (Wc of them valid) and state Sig at the chunk's entry, forward:
-//     A = (X K^T) * [j <= i] g^(i-j)          Y = s_intra A V + s_carry diag(g^(i+1)) X Sig
+//     A = (X K^T) * [j <= i] g^(i-j)          Y = s_fin (s_col A V + diag(g^(i+1)) X Sig)
 //     Sig <- g^Wc Sig + s_state (diag(g^(Wc-1-j)) K)^T V
 // and in reverse [j >= i] g^(j-i), g^(Wc-i) and g^j.  X, K^T, V, A and Sig stay in shared memory;
 // every product is register-tiled (simt_tile.cuh).
@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
     const float log2g = log2f(lin_decay(a, s));
     const bool rev = a.rev != 0;
+    const float s_in = a.s_fin * a.s_col;
     for (int i = tid; i <= W; i += kThreads) gp[i] = pow_decay(log2g, (float)i);
     const float* carry = SUMMARY || !a.carry ? nullptr : a.carry + ((size_t)bs * a.nseg + seg) * dx * dy;
     for (int e = tid; e < dx * dy; e += kThreads)
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
 #pragma unroll
                             for (int i = 0; i < RM; ++i) {
                                 const int e = rev ? max(Wc - m0 - i, 0) : m0 + i + 1;
-                                simt::scale_row<RM>(acc, i, a.s_carry * gp[e]);
+                                simt::scale_row<RM>(acc, i, a.s_fin * gp[e]);
                             }
                         }
                         simt::Acc<RM> in;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
                         for (int i = 0; i < RM; ++i) {
                             const int row = m0 + i;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[i][j] += a.s_intra * in[i][j];
+                            for (int j = 0; j < 4; ++j) acc[i][j] += s_in * in[i][j];
                             if (keep_y) {
                                 float* p = Ys + row * dy + n0;
                                 if (r > 0) {

@@ -6,11 +6,17 @@
 // covers every pair of sizes.  Per chunk, with Sig the state at its entry (forward; reverse
 // mirrors the decays):
 //   MMA-G   G = X K^T                                   128 x 128 float32 in tensor memory
-//   EPI-1   G~ = mask(G) s_intra g^(i-j) -> bf16, over G's own columns: A operand of MMA-Y
-//   MMA-C   Yc = X Sig~ (Sig~ = bf16 of Sig)       MMA-Y   Y = G~ V
-//   EPI-Y   s_carry g^(i+1) Yc + Y -> bf16 tile -> TMA store
+//   EPI-1   G~ = mask(G) s_col g^(64-a_j) -> bf16, over G's own columns: A operand of MMA-Y
+//   MMA-C   Y = X Sig~ (Sig~ = bf16 of g^64 Sig)   MMA-Y   Y += G~ V
+//   EPI-Y   s_fin g^(a_i-64) Y -> bf16 tile -> TMA store
 //   KT      K~ = s_state g^(Wc-1-j) K in pieces of bf16, in shared memory
 //   MMA-S   dSig = K~^T V;   EPI-S   Sig <- g^Wc Sig + dSig  (float32 registers), publish Sig~
+// with a_i = i + 1 (reverse: 128 - i), the distance of row i to the carry (reverse: of a whole chunk; a
+// shorter one, which comes first, takes its carry times g^(Wc-128) more).  g^(i-j) = g^(a_i-64) g^(64-a_j):
+// the row's factor waits for the end, so both products share one accumulator and EPI-1 needs a
+// factor per column only.  Its powers stay within g^(+-64), which float32 and bf16 hold as long as g
+// >= 2^(-60/64) = 0.52; a head that decays faster ("steep") takes g^(i-j) itself in EPI-1 and has MMA-C's
+// result scaled in tensor memory (EPI-C) before MMA-Y adds to it.
 //
 // Roundings to bf16.  G~ and Sig~ are operands of one product each and are rounded once, which
 // adds to the output about its own rounding (measured against 64 bits: 2.3e-3 relative where
@@ -27,8 +33,8 @@
 // Roles (one CTA per SM): warp 0 allocates tensor memory and issues MMA-G, MMA-C and MMA-Y, warp 3
 // MMA-S; warp 1 issues the loads, warp 2 the stores; warps 4..11 (A: a row and half of its columns
 // per thread) run EPI-1 and EPI-Y; warps 12.. (B) run KT and EPI-S.  The chains A and B only meet in
-// Sig~.  D = 64 has two Gram regions, and EPI-1 of the next item runs while this one's products do;
-// D = 128 has tensor memory for one, and EPI-Y runs while the next Gram does.
+// Sig~.  There are two Gram regions: the next item's Gram (at D = 64 also its EPI-1) runs while this one's
+// products do.
 //
 // What a hand-over costs decides the time of a chunk (measured, in SM cycles: issuing one MMA 49, a
 // commit 52, a wait on an mbarrier whose phase is already complete 45 to 90 and twice that while
@@ -114,7 +120,9 @@ __device__ __forceinline__ void mul2(float& x, float& y, float a, float b, float
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Named barriers (0 is __syncthreads)
-enum { kNbGT = 5, kNbKT = 7, kNbSP = 8, kNbVZ = 10, kNbA = 12, kNbB = 13 };
+enum { kNbSC = 4, kNbGT = 5, kNbKT = 7, kNbSP = 8, kNbVZ = 10, kNbA = 12, kNbB = 13 };
+constexpr int kRef = 64;                  // the middle of the row factors
+constexpr float kSteep = -60.f / kRef;    // log2 of the decay below which the factors are not split
 
 template <int D>
 struct Out {  // shared memory of the output kernel
@@ -122,23 +130,24 @@ struct Out {  // shared memory of the output kernel
     static constexpr int NS = D == 64 ? 4 : 2;           // slots of each of x, k, v
     static constexpr uint32_t oX = 0, oK = oX + NS * kTile, oV = oK + NS * kTile, oM = oV + NS * kTile,
                               oS = oM + (D == 64 ? kTile : 0);
-    static constexpr uint32_t oGs = oS + kTile;          // s_intra g^distance, 0 for the 128 negative ones
-    static constexpr uint32_t oGp = oGs + 4 * 260;       // g^0 .. g^128
-    static constexpr uint32_t oT = oGp + 4 * 132;        // g^(15 - j) (reverse g^j), j = 0 .. 15
-    static constexpr uint32_t oBar = oT + 64;
-    enum { XF = 0, XE = XF + NS, OS = XE + NS, KF = OS + NS, VF = KF + NS, E = VF + NS, BG = E + NS, BGK = BG + 4, YL, YD,
+    static constexpr uint32_t oGp = oS + kTile;          // g^0 .. g^128
+    static constexpr uint32_t oCol = oGp + 4 * 132;      // s_col g^(64 - a_j), j = 0 .. 127
+    static constexpr uint32_t oBar = oCol + 4 * 128;
+    enum { XF = 0, XE = XF + NS, OS = XE + NS, KF = OS + NS, VF = KF + NS, E = VF + NS, BG = E + NS, BGK = BG + 4, BC, YL, YD,
            YI, SH, SD, kBars };
     static constexpr uint32_t oMisc = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oMisc + 16 + 1024;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
-// Tensor memory columns of the output kernel: one or two Gram regions, Y, Yc, dSig.
+// Tensor memory columns of the output kernel: two Gram regions, Y, dSig.
 template <int D>
 struct Cols {
-    static constexpr int NG = D == 64 ? 2 : 1;
-    __device__ static constexpr uint32_t G(int i) { return NG == 2 ? (uint32_t)(i & 1) * 128 : 0u; }
-    static constexpr uint32_t Y = NG * 128, YC = Y + D, S = YC + D;
+    // Whether the next Gram and its EPI-1 come before this item's products.  At D = 128 its tiles, of
+    // which there are two slots only, arrive too late for that.
+    static constexpr bool kEarly = D == 64;
+    __device__ static constexpr uint32_t G(int i) { return (uint32_t)(i & 1) * 128; }
+    static constexpr uint32_t Y = 256, S = Y + D;
 };
 
 struct Where {  // the CTA's state head, segment and valid chunks
@@ -204,9 +213,8 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
     extern __shared__ unsigned char smem_raw[];
     // an offset, not a rounded pointer: the compiler then still knows the address space
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float* gs = reinterpret_cast<float*>(sm + L::oGs) + kW;
     float* gp = reinterpret_cast<float*>(sm + L::oGp);
-    float* tt = reinterpret_cast<float*>(sm + L::oT);
+    float* colf = reinterpret_cast<float*>(sm + L::oCol);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + L::oMisc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::oMisc + 4);
@@ -233,30 +241,34 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
     {
         const int z0 = max(w.c0, w.c1) * kW, z1 = min((w.c0 + a.seg_chunks) * kW, a.n);
         const int per = a.dy / 8, count = max(0, z1 - z0) * per;
+#pragma unroll 1
         for (int h = 0; h < a.rx; ++h) {
             bf16* y = static_cast<bf16*>(const_cast<void*>(a.y.p)) + w.b * a.y.sb + (long long)(w.s * a.rx + h) * a.y.sh;
+#pragma unroll 1
             for (int e = tid; e < count; e += kThreads)
                 *reinterpret_cast<uint4*>(y + (long long)(z0 + e / per) * a.y.sn + (e % per) * 8) = make_uint4(0, 0, 0, 0);
         }
     }
     if (w.nit == 0) return;
 
-    if (tid < 2 * kW + 1) {
-        const float g = tid < kW ? 0.f : pow_decay(log2g, (float)(tid - kW));
-        gs[tid - kW] = a.s_intra * g;
-        if (tid >= kW) gp[tid - kW] = g;
-    }
-    if (tid < 16) tt[tid] = pow_decay(log2g, (float)(rev ? tid : 15 - tid));
+    const bool steep = log2g < lt::kSteep;
+    auto dist = [&](int i) { return rev ? kW - i : i + 1; };  // a_i
+    if (tid <= kW) gp[tid] = pow_decay(log2g, (float)tid);
+    if (tid < kW) colf[tid] = steep ? 0.f : a.s_col * pow_decay(log2g, (float)(lt::kRef - dist(tid)));
     if (warp == 0) tc::tmem_alloc(tmem_holder, 512);
 
     // B thread: state row sr, columns sc0 .. sc0 + kSC - 1.  D = 64: rows 64.. hold the low pieces' sums.
     const int q4 = warp & 3, part = (warp - lt::kB0) >> 2;
     const int sr = 32 * q4 + lane, sc0 = part * kSC;
     float sig[kSC];
-    auto publish = [&]() {
+    auto publish = [&](float pub) {  // pub: g^64
 #pragma unroll
-        for (int j = 0; j < kSC / 8; ++j)
-            *reinterpret_cast<uint4*>(sm + L::oS + la_off(sc0 / 64, sr, (sc0 % 64) / 8 + j)) = la_pack8(&sig[8 * j]);
+        for (int j = 0; j < kSC / 8; ++j) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = pub * sig[8 * j + i];
+            *reinterpret_cast<uint4*>(sm + L::oS + la_off(sc0 / 64, sr, (sc0 % 64) / 8 + j)) = la_pack8(f);
+        }
     };
     if (warp >= lt::kB0) {
         // D = 64: dx <= 64, so only the high half takes the carry
@@ -269,7 +281,8 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
             sig[j] = has && sc0 + (j & ~15) < a.dy ? *src : 0.f;  // dy is a multiple of 16
             src += step;
         }
-        publish();
+        const int first = rev ? w.c1 - 1 : w.c0, Wc = min(kW, w.len - first * kW);
+        publish(steep ? 1.f : pow_decay(log2g, (float)(lt::kRef - (rev ? kW - Wc : 0))));
         tc::fence_proxy_async();
     }
     tc::fence_before_sync();
@@ -300,26 +313,28 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
             __syncwarp();
             auto products = [&]() {
                 if (first && ci > 0) tc::named_bar(lt::kNbSP, kBThreads + 32);
-                tc::named_bar(lt::kNbGT + (it & 1), kAThreads + 32);  // also: Y and Yc of the item before are read
+                tc::named_bar(lt::kNbGT + (it & 1), kAThreads + 32);  // also: Y of the item before is read
                 if (lane == 0) {
                     tc::fence_after_sync();
                     if (new_y) {
                         const uint64_t x = dX + (xi % NS) * T;
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)  // D = 64: the two halves of the state in turn
-                            tc::mma_ss(tmem + C::YC, x + kstep(D == 64 ? ks & 3 : ks), dS + ks * kMK, I_Y, ks > 0);
+                            tc::mma_ss(tmem + C::Y, x + kstep(D == 64 ? ks & 3 : ks), dS + ks * kMK, I_Y, ks > 0);
+                        if (steep) tc::mma_commit(&bars[L::BC]);
                     }
                     if (!mode_a || first) lt::wait(&bars[L::VF + ki % NS], (ki / NS) & 1, abort, status, 305);
                 }
                 __syncwarp();
                 if (a.lengths && (!mode_a || first)) tc::named_bar(lt::kNbVZ + (ki & 1), kBThreads + 64);
+                if (steep && new_y) tc::named_bar(lt::kNbSC, kAThreads + 32);
                 if (lane == 0) {
                     tc::fence_after_sync();
                     const uint64_t v = dV + (ki % NS) * T;
-                    const uint32_t tg = tmem + C::G(it), acc = !new_y;
+                    const uint32_t tg = tmem + C::G(it);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)  // G~: columns 0..63 of the Gram in its first 32, the rest from 64 on
-                        tc::mma_ts(tmem + C::Y, tg + 8 * (ks & 3) + (ks >> 2) * 64, v + ks * kMK, I_Y, ks > 0 ? 1u : acc);
+                        tc::mma_ts(tmem + C::Y, tg + 8 * (ks & 3) + (ks >> 2) * 64, v + ks * kMK, I_Y, 1);
                     if (end_y) tc::mma_commit(&bars[L::YD]);
                     if (mode_a && last) tc::mma_commit(&bars[L::YL]);
                     if (mode_b) {
@@ -328,10 +343,11 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
                     }
                 }
             };
-            if (C::NG == 1 && it >= 0) products();
-            if (lane == 0 && it + 1 < total) {  // MMA-G, into the region that MMA-Y of `before` read
-                const int before = C::NG == 1 ? it : it - 1;
-                if (before >= 0) lt::wait(&bars[mode_b ? L::YI : L::YD], before & 1, abort, status, 308);
+            // (in turn, before the next commit on it)
+            if (lane == 0 && it > 0 && it + 1 < total)
+                lt::wait(&bars[mode_b ? L::YI : L::YD], (it - 1) & 1, abort, status, 308);
+            if (!C::kEarly && it >= 0) products();
+            if (lane == 0 && it + 1 < total) {  // MMA-G, into the region that MMA-Y of it - 1 read
                 const bool wrap = last || it < 0;  // the next item begins a chunk
                 const int rn = wrap ? 0 : r + 1, cn = it < 0 ? 0 : ci + (last ? 1 : 0);
                 const int xn = mode_b ? cn : it + 1, kn = mode_a ? cn : it + 1;
@@ -346,7 +362,7 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
                 if (mode_a && rn == items - 1) tc::mma_commit(&bars[L::BGK]);
             }
             __syncwarp();
-            if (C::NG == 2 && it >= 0) products();
+            if (C::kEarly && it >= 0) products();
             if (++r == items) r = 0, ++ci;
             if (it < 0) r = 0, ci = 0;
         }
@@ -450,42 +466,39 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
             tc::named_bar(lt::kNbA, kAThreads);
             tc::fence_after_sync();
         };
-        // EPI-1 of item it (rows valid up to Wc): columns 64 ah .. 64 ah + 63, 16 at a time, packed over
-        // the first half of them.  Columns that every row of the warp keeps take the factor
-        // g^(i-c-15) g^(15-j); across the diagonal each has its own, 0 in the table on the masked side, where
-        // the product is selected away (the column may hold anything past the sequence).
+        // EPI-1 of item it (Wc valid rows): columns 64 ah .. 64 ah + 63, 16 at a time, packed over the first
+        // half of them.  Products of masked columns are selected away (past the sequence they may be
+        // anything).
         auto epi1 = [&](int it, int Wc) {
             const uint32_t tg = tmem + lanes + C::G(it) + 64 * ah;
             wait_a(L::BG + (it & 3), (it >> 2) & 1, 331);
-            const int limit = rev ? Wc : kW, sgn = rev ? 1 : -1;
+            const int limit = rev ? Wc : kW;
 #pragma unroll 1
             for (int cb = 0; cb < 64; cb += 16) {
                 const int c = 64 * ah + cb;
+                const bool some = rev ? c + 15 >= row0 : c <= row0 + 31;  // some row keeps some column
+                const bool all = (rev ? c > row0 + 31 : c + 15 < row0) && c + 15 < limit;
                 uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                if (rev ? c + 15 >= row0 : c <= row0 + 31) {  // some row keeps some column
+                if (some) {
                     uint32_t g[16];
                     float f[16];
                     tc::tmem_ld16(tg + cb, g);
-                    if ((rev ? c > row0 + 31 : c + 15 < row0) && c + 15 < limit) {
-                        const float base = gs[rev ? c - i : i - c - 15];
-                        float t[16];
+                    if (steep) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[j] = a.s_col * gp[abs(i - c - j)];
+                    } else {
 #pragma unroll
                         for (int j = 0; j < 16; j += 4)
-                            *reinterpret_cast<float4*>(t + j) = *reinterpret_cast<const float4*>(tt + j);
+                            *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(colf + c + j);
+                    }
+                    tc::tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) lt::mul2(t[j], t[j + 1], t[j], t[j + 1], base, base);
-                        tc::tmem_wait_ld();
+                    for (int j = 0; j < 16; j += 2)
+                        lt::mul2(f[j], f[j + 1], f[j], f[j + 1], __uint_as_float(g[j]), __uint_as_float(g[j + 1]));
+                    if (!all) {
+                        const int lo = rev ? i - c : 0, hi = rev ? limit - c : i - c + 1;  // kept: lo <= j < hi
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2)
-                            lt::mul2(f[j], f[j + 1], t[j], t[j + 1], __uint_as_float(g[j]), __uint_as_float(g[j + 1]));
-                    } else {
-                        const float* fac = gs + (rev ? c - i : i - c);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) f[j] = fac[sgn * j];
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            f[j] = f[j] != 0.f && c + j < limit ? f[j] * __uint_as_float(g[j]) : 0.f;
+                        for (int j = 0; j < 16; ++j) f[j] = j >= lo && j < hi ? f[j] : 0.f;
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) pk[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
@@ -495,37 +508,51 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
             tc::tmem_wait_st();
             tc::fence_before_sync();
         };
+        const float fin = a.s_fin * (steep ? 1.f : pow_decay(log2g, (float)(dist(i) - lt::kRef)));
         int groups = 0, r = -1, ci = 0;
 #pragma unroll 1
         for (int it = -1; it < total; ++it) {
             // item it = (chunk ci, r); -1: only the first EPI-1
-            const bool last = r == items - 1, end_y = it >= 0 && (!mode_b || last);
+            const bool last = r == items - 1, new_y = it >= 0 && (!mode_b || r == 0), end_y = it >= 0 && (!mode_b || last);
             const int Wc = valid_of(ci), Wn = valid_of(it >= 0 && last ? ci + 1 : ci);
+            const uint32_t ty = tmem + lanes + C::Y + ah * (D / 2);
             if (it >= 0) tc::named_arrive(lt::kNbGT + (it & 1), kAThreads + 32);
+            if (steep && new_y) {  // EPI-C
+                wait_a(L::BC, groups & 1, 332);
+                const float f = gp[rev ? max(Wc - i, 0) : i + 1];
+#pragma unroll 1
+                for (int cb = 0; cb < D / 2; cb += 16) {
+                    uint32_t y[16];
+                    tc::tmem_ld16(ty + cb, y);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(f * __uint_as_float(y[j]));
+                    tc::tmem_st16(ty + cb, y);
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::named_arrive(lt::kNbSC, kAThreads + 32);
+            }
 #pragma unroll 1
             for (int step = 0; step < 2; ++step) {
-                // two Gram regions: the next EPI-1, then EPI-Y; one: the other way round
-                if ((step == 0) == (C::NG == 2)) {
+                if ((step == 0) == C::kEarly) {
                     if (it + 1 < total) epi1(it + 1, Wn);
                 } else if (end_y) {
                     // EPI-Y, into the X tile, which the products have read
                     wait_a(L::YD, groups & 1, 333);
                     if (poller && !mode_b && last) tc::mbar_arrive(&bars[L::E + (mode_a ? ci : it) % NS]);
                     unsigned char* st = sm + L::oX + (groups % NS) * L::kTile;
-                    const uint32_t ty = tmem + lanes + C::Y + ah * (D / 2);
-                    const float f = a.s_carry * gp[rev ? max(Wc - i, 0) : i + 1];
                     const bool live = i < Wc;
-#pragma unroll 1
+                    uint32_t y[16];
+                    tc::tmem_ld16(ty, y);
+    #pragma unroll 1
                     for (int cb = 0; cb < D / 2; cb += 16) {
-                        uint32_t y[16], yc[16];
-                        tc::tmem_ld16(ty + cb, y);
-                        tc::tmem_ld16(ty + (C::YC - C::Y) + cb, yc);
-                        tc::tmem_wait_ld();
                         float o[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            o[j] = live ? fmaf(f, __uint_as_float(yc[j]), __uint_as_float(y[j])) : 0.f;
-#pragma unroll
+                        tc::tmem_wait_ld();
+    #pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = live ? fin * __uint_as_float(y[j]) : 0.f;
+                        if (cb + 16 < D / 2) tc::tmem_ld16(ty + cb + 16, y);
+    #pragma unroll
                         for (int j = 0; j < 16; j += 8) {
                             const int col = ah * (D / 2) + cb + j;
                             *reinterpret_cast<uint4*>(st + la_off(col / 64, i, (col % 64) / 8)) = la_pack8(o + j);
@@ -548,6 +575,7 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
         const int c0 = part * kC;                   // chunk index over the whole row: block c / 8, chunk c % 8
         const uint32_t lanes = (uint32_t)(32 * q4) << 16;
         const bool poller = warp == lt::kB0 && lane == 0;
+        const float pub = steep ? 1.f : gp[lt::kRef];
         auto meet = [&]() {  // after the poller's waits
             __syncwarp();
             tc::named_bar(lt::kNbB, kBThreads);
@@ -595,7 +623,7 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
             const float wt = row < Wc ? a.s_state * gp[rev ? row : Wc - 1 - row] : 0.f;
             unsigned char *kt = sm + L::oK + slot * L::kTile, *mt = sm + L::oM;
             uint4 low[D == 64 ? 1 : kC];
-#pragma unroll
+#pragma unroll(D == 64 ? 2 : kC)
             for (int c = 0; c < kC; ++c) {
                 const uint32_t at = la_off((c0 + c) >> 3, row, (c0 + c) & 7);
                 uint4 p[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
@@ -634,7 +662,7 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
 #pragma unroll
                 for (int j = 0; j < 16; ++j) sig[cb + j] = fmaf(rho, sig[cb + j], __uint_as_float(d[j]));
             }
-            publish();
+            publish(pub);
             tc::fence_before_sync();
             tc::fence_proxy_async();
             tc::named_arrive(lt::kNbSP, kBThreads + 32);
