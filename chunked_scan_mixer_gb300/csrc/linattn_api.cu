@@ -124,7 +124,7 @@ size_t state_array_bytes(const hla2_linattn_args* a, const LinPlan& p) {
 }
 
 int run_pass(const LinPass& a, bool summary, int dtype, cudaStream_t st) {
-    return dtype == HLA2_BF16 ? launch_lin_tc(a, summary, st) : launch_lin_simt(a, summary, false, st);
+    return dtype == HLA2_BF16 ? launch_lin_tc(a, summary, st) : launch_lin_simt(a, summary, st);
 }
 
 // Common fields of every pass of one call.

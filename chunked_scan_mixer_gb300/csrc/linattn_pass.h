@@ -46,20 +46,19 @@ __device__ __forceinline__ float lin_decay(const LinPass& a, int s) { return a.g
 // Every kernel here is launched so that it may start while the one before it on the stream drains
 // (launch_pdl): it sets itself up, then waits (pdl_wait) before it touches global memory.
 
-// SIMT passes (float32 arithmetic, any type and size); W = lin_simt_width(dx, dy, state heads, n, SMs):
+// SIMT passes (float32, any size); W = lin_simt_width(dx, dy, state heads, n, SMs):
 // 64 rows (32 where a dimension is 128, for the shared memory), and half or a quarter of that while the
 // chunks of all heads would not give every SM one.  Two heads of 1023 rows, d = 32, dv = 64: the output
-// pass took 31 us with 64 rows a chunk (32 CTAs), 8 us with 16 (128 CTAs).
+// pass took 31 us with 64 rows a chunk (32 CTAs), 14 us with 16 (128 CTAs).
 int lin_simt_width(int dx, int dy, long long heads, int n, int sms);
 int lin_simt_ctas(int dx, int dy, int W);  // resident CTAs per SM
-int launch_lin_simt(const LinPass& a, bool summary, bool is_bf16, cudaStream_t st);
+int launch_lin_simt(const LinPass& a, bool summary, cudaStream_t st);
 
 // Tensor-core passes (bf16, any size; linattn_tc.cu): W = 128, one CTA per SM.
 int launch_lin_tc(const LinPass& a, bool summary, cudaStream_t st);
 
-// States entering the segments from the segment summaries, in one serial pass over the segments
-// per state element:  carry[s] = cur;  cur = g^(valid rows of s) cur + sums[s]  in the
-// scan's direction.  init (nullable) is the state before the scan; reverse: the gradient of the
+// States entering the segments from the segment summaries, for each state element:
+// carry[s] = cur;  cur = g^(valid rows of s) cur + sums[s]  in the scan's direction.  init (nullable) is the state before the scan; reverse: the gradient of the
 // final state, which enters as init / g.  final (nullable) receives the state after it;
 // reverse: times g, the gradient of the initial state.  sums may be NULL with nseg == 1 and no final.
 int launch_lin_scan(const float* sums, float* carry, const float* init, float* final_state, const float* gamma,

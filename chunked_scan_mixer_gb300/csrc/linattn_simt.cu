@@ -36,35 +36,27 @@ __host__ __device__ inline LinSmem lin_smem(int dx, int dy, int W, bool keep_y) 
 }
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const bf16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xFFFF0000u));
-}
 
-template <typename T>
-__device__ __forceinline__ const T* row_ptr(const hla2_view& w, int b, int h, int row) {
-    return static_cast<const T*>(w.p) + b * w.sb + h * w.sh + row * w.sn;
+__device__ __forceinline__ const float* row_ptr(const hla2_view& w, int b, int h, int row) {
+    return static_cast<const float*>(w.p) + b * w.sb + h * w.sh + row * w.sn;
 }
 
 // rows [row0, row0 + Wc) of a view as W x D floats (leading dimension ld), the rest zero
-template <typename T>
 __device__ __forceinline__ void load_rows(float* dst, int ld, const hla2_view& w, int b, int h, int row0, int W, int Wc,
                                           int D) {
     const int nd = D >> 2;
     for (int e = threadIdx.x; e < W * nd; e += kThreads) {
         const int i = e / nd, f = (e % nd) * 4;
-        const float4 t = i < Wc ? load4(row_ptr<T>(w, b, h, row0 + i) + f) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 t = i < Wc ? load4(row_ptr(w, b, h, row0 + i) + f) : make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<float4*>(dst + i * ld + f) = t;
     }
 }
-template <typename T>
 __device__ __forceinline__ void load_rows_t(float* dst, int ld, const hla2_view& w, int b, int h, int row0, int W,
                                             int Wc, int D) {
     const int nd = D >> 2;
     for (int e = threadIdx.x; e < W * nd; e += kThreads) {
         const int i = e % W, f = (e / W) * 4;  // lanes on rows: the transposed stores fall in distinct banks
-        const float4 t = i < Wc ? load4(row_ptr<T>(w, b, h, row0 + i) + f) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 t = i < Wc ? load4(row_ptr(w, b, h, row0 + i) + f) : make_float4(0.f, 0.f, 0.f, 0.f);
         dst[f * ld + i] = t.x;
         dst[(f + 1) * ld + i] = t.y;
         dst[(f + 2) * ld + i] = t.z;
@@ -72,7 +64,7 @@ __device__ __forceinline__ void load_rows_t(float* dst, int ld, const hla2_view&
     }
 }
 
-template <typename T, bool SUMMARY>
+template <bool SUMMARY>
 __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
     extern __shared__ __align__(16) float sm[];
     const int dx = a.dx, dy = a.dy, W = a.W;
@@ -104,10 +96,10 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
             const bool y_last = a.rx > 1 || r == items - 1, s_now = a.rk > 1 || r == items - 1;
             const int hx = s * a.rx + (a.rx > 1 ? r : 0), hk = s * a.rk + (a.rk > 1 ? r : 0);
             __syncthreads();
-            if (!SUMMARY && x_new) load_rows<T>(Xs, pad(dx), a.x, b, hx, row0, W, Wc, dx);
+            if (!SUMMARY && x_new) load_rows(Xs, pad(dx), a.x, b, hx, row0, W, Wc, dx);
             if (kv_new) {
-                load_rows_t<T>(Kt, pad(W), a.k, b, hk, row0, W, Wc, dx);
-                load_rows<T>(Vs, dy, a.v, b, hk, row0, W, Wc, dy);
+                load_rows_t(Kt, pad(W), a.k, b, hk, row0, W, Wc, dx);
+                load_rows(Vs, dy, a.v, b, hk, row0, W, Wc, dy);
             }
             __syncthreads();
             if (!SUMMARY) {
@@ -166,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
                             }
                             if (y_last && row < Wn) {
                                 if (row >= Wc) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-                                simt::store4(const_cast<T*>(row_ptr<T>(a.y, b, hx, row0 + row)) + n0, acc[i]);
+                                simt::store4(const_cast<float*>(row_ptr(a.y, b, hx, row0 + row)) + n0, acc[i]);
                             }
                         }
                     });
@@ -196,54 +188,86 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
     }
 }
 
-template <typename T>
-int launch_simt_t(const LinPass& a, bool summary, cudaStream_t st) {
-    const size_t smem = lin_smem(a.dx, a.dy, a.W, !summary && a.rk > 1).total * sizeof(float);
-    auto kfn = summary ? lin_simt_kernel<T, true> : lin_simt_kernel<T, false>;
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -1;
-    return launch_pdl(kfn, dim3(a.B * a.Hs, a.nseg), dim3(kThreads), smem, st, a) == cudaSuccess ? 0 : -1;
-}
-
 // ---- scan over the segments -----------------------------------------------------------
+//
+// A thread owns four state elements.  PARTS threads share them where there are many segments: each
+// sums its run of segments, they pass the runs' sums on through shared memory, and each then scans its
+// run.  Up to kScanAhead segments a run stay in registers between the two.  Bound by latency: 2 heads x
+// 64 segments of 32 x 64 states take 6.8 us (12.4 us with one thread an element and serial runs), 64
+// heads x 2 segments of 128 x 128 take 6.5 us (14 us with one element a thread).
+constexpr int kScanAhead = 8, kScanParts = 8;
 
+template <int PARTS>
 __global__ void __launch_bounds__(kThreads)
     lin_scan_kernel(const float* __restrict__ sums, float* __restrict__ carry, const float* __restrict__ init,
                     float* __restrict__ fin, const float* __restrict__ gamma, const int* __restrict__ lengths, int Hs,
                     int n, int seg_rows, int nseg, int elems, int rev) {
-    const int bs = blockIdx.x, b = bs / Hs;
-    const int e = blockIdx.y * kThreads + threadIdx.x;
+    constexpr int kOwners = kThreads / PARTS;
+    __shared__ float4 run_sum[PARTS][kOwners];
+    const int bs = blockIdx.x, b = bs / Hs, owner = threadIdx.x % kOwners, part = threadIdx.x / kOwners;
+    const int e = (blockIdx.y * kOwners + owner) * 4;
+    const bool live = e < elems;
     pdl_trigger();
     pdl_wait();
-    if (e >= elems) return;
     const float g = gamma ? __ldg(gamma + bs % Hs) : 1.f;
     const float log2g = log2f(g);
     const int len = lin_len(lengths, b, n);
-    float cur = init ? init[(size_t)bs * elems + e] : 0.f;
-    if (init && rev) cur /= g;
-    const float* src = sums + (size_t)bs * nseg * elems + e;
-    float* dst = carry ? carry + (size_t)bs * nseg * elems + e : nullptr;
+    // valid rows of the first i segments in the scan's direction
+    auto rows_before = [&](int i) {
+        return rev ? len - (int)min((long long)len, (long long)(nseg - i) * seg_rows)
+                   : (int)min((long long)len, (long long)i * seg_rows);
+    };
+    auto decay = [&](int from, int to) { return pow_decay(log2g, (float)(rows_before(to) - rows_before(from))); };
+    auto step = [](float4& c, float f, const float4& v) {
+        c = make_float4(fmaf(f, c.x, v.x), fmaf(f, c.y, v.y), fmaf(f, c.z, v.z), fmaf(f, c.w, v.w));
+    };
+    const size_t base = (size_t)bs * nseg * elems + e;
     const int steps = fin ? nseg : nseg - 1;  // the last sum only enters the final state
-    constexpr int kAhead = 8;                 // loads in flight
-    for (int i0 = 0; i0 < nseg; i0 += kAhead) {
-        float v[kAhead];
+    const int run = (nseg + PARTS - 1) / PARTS, lo = min(nseg, part * run), hi = min(nseg, lo + run);
+    float4 v[kScanAhead];
+    auto fetch = [&](int i0) {
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
+        for (int j = 0; j < kScanAhead; ++j) {
             const int i = i0 + j;
-            v[j] = i < steps ? src[(size_t)(rev ? nseg - 1 - i : i) * elems] : 0.f;
+            v[j] = live && i < hi && i < steps
+                       ? *reinterpret_cast<const float4*>(sums + base + (size_t)(rev ? nseg - 1 - i : i) * elems)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+    };
+    float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (init && live) {
+        cur = *reinterpret_cast<const float4*>(init + (size_t)bs * elems + e);
+        if (rev) cur = make_float4(cur.x / g, cur.y / g, cur.z / g, cur.w / g);
+    }
+    if (PARTS > 1) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = lo; i0 < hi; i0 += kScanAhead) {
+            fetch(i0);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
+            for (int j = 0; j < kScanAhead; ++j)
+                if (i0 + j < hi) step(sum, decay(i0 + j, i0 + j + 1), v[j]);
+        }
+        run_sum[part][owner] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < PARTS - 1; ++p)
+            if (p < part) step(cur, decay(min(nseg, p * run), min(nseg, (p + 1) * run)), run_sum[p][owner]);
+    }
+    if (!live) return;
+    for (int i0 = lo; i0 < hi; i0 += kScanAhead) {
+        if (PARTS == 1 || run > kScanAhead) fetch(i0);
+#pragma unroll
+        for (int j = 0; j < kScanAhead; ++j) {
             const int i = i0 + j;
-            if (i >= nseg) break;
-            const int s = rev ? nseg - 1 - i : i;
-            if (dst) dst[(size_t)s * elems] = cur;
-            if (i < steps) {
-                const int rows = max(0, min(seg_rows, len - s * seg_rows));
-                cur = fmaf(pow_decay(log2g, (float)rows), cur, v[j]);
-            }
+            if (i >= hi) break;
+            if (carry) *reinterpret_cast<float4*>(carry + base + (size_t)(rev ? nseg - 1 - i : i) * elems) = cur;
+            if (i < steps) step(cur, decay(i, i + 1), v[j]);
         }
     }
-    if (fin) fin[(size_t)bs * elems + e] = rev ? g * cur : cur;
+    if (fin && part == PARTS - 1) {
+        if (rev) cur = make_float4(g * cur.x, g * cur.y, g * cur.z, g * cur.w);
+        *reinterpret_cast<float4*>(fin + (size_t)bs * elems + e) = cur;
+    }
 }
 
 // ---- step of single tokens -----------------------------------------------------------------
@@ -338,19 +362,26 @@ int lin_simt_ctas(int dx, int dy, int W) {
     return simt::min_ctas(2, simt::ctas_per_sm(lin_smem(dx, dy, W, false).total * sizeof(float)));
 }
 
-int launch_lin_simt(const LinPass& a, bool summary, bool is_bf16, cudaStream_t st) {
+int launch_lin_simt(const LinPass& a, bool summary, cudaStream_t st) {
     if (a.B * a.Hs == 0 || a.nseg == 0) return 0;
-    return is_bf16 ? launch_simt_t<bf16>(a, summary, st) : launch_simt_t<float>(a, summary, st);
+    const size_t smem = lin_smem(a.dx, a.dy, a.W, !summary && a.rk > 1).total * sizeof(float);
+    auto kfn = summary ? lin_simt_kernel<true> : lin_simt_kernel<false>;
+    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -1;
+    return launch_pdl(kfn, dim3(a.B * a.Hs, a.nseg), dim3(kThreads), smem, st, a) == cudaSuccess ? 0 : -1;
 }
 
 int launch_lin_scan(const float* sums, float* carry, const float* init, float* final_state, const float* gamma,
                     const int* lengths, int B, int Hs, int n, int seg_rows, int nseg, int elems, int rev,
                     cudaStream_t st) {
     if (B * Hs == 0) return 0;
-    return launch_pdl(lin_scan_kernel, dim3(B * Hs, (elems + kThreads - 1) / kThreads), dim3(kThreads), 0, st, sums, carry,
-                      init, final_state, gamma, lengths, Hs, n, seg_rows, nseg, elems, rev) == cudaSuccess
-               ? 0
-               : -1;
+    auto go = [&](auto kernel, int parts) {
+        const int each = kThreads / parts * 4;  // elements of a CTA; a head's are a multiple of four
+        return launch_pdl(kernel, dim3(B * Hs, (elems + each - 1) / each), dim3(kThreads), 0, st, sums, carry, init,
+                          final_state, gamma, lengths, Hs, n, seg_rows, nseg, elems, rev) == cudaSuccess
+                   ? 0
+                   : -1;
+    };
+    return nseg > kScanAhead ? go(lin_scan_kernel<kScanParts>, kScanParts) : go(lin_scan_kernel<1>, 1);
 }
 
 int launch_lin_step(float* state, const void* q, const void* k, const void* v, void* out, int N, int H, int Hk, int d,
