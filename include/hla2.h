@@ -438,6 +438,9 @@ int hla2_noalloc_selftest_wait_timeout(hla2_stream_t stream);
  *
  * A tensor argument is a base address and the element strides of batch, head and token; the
  * last dimension is contiguous.  Base and strides are multiples of 16 bytes.
+ *
+ * The workspace starts with the status word that hla2_workspace_status reads.  These calls do not clear
+ * it: it is 0 in a workspace that is new to them, and a wait that gave up stays recorded.
  */
 typedef struct {
     const void* p;
@@ -446,7 +449,7 @@ typedef struct {
 
 typedef struct {
     int dtype;                       /* HLA2_F32 | HLA2_BF16: q, k, v, out, dout and gradients      */
-    int B, H, Hk, n, d, dv;          /* d, dv in {16, 32, 64, 128}; n >= 0; H a multiple of Hk        */
+    int B, H, Hk, n, d, dv;          /* d, dv in {16, 32, 64, 128}; 0 <= n <= 2^30; H a multiple of Hk */
     float scale;                     /* factor of the outputs                                         */
     const float* gamma;              /* device float [Hk], or NULL for no decay                       */
     const int* lengths;              /* device int [B], or NULL                                       */
@@ -527,7 +530,8 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
  * zeros [N, K / group] bytes in 0..15, or NULL for 8.  x [M, K] (rows every x_stride elements),
  * scales [N, K / group], bias [N] (nullable) and y [M, N] have the type dtype.  1 <= M <= 16;
  * group 32, 64 or 128, K a multiple of it; N >= 0.  x, its rows and qweight are 16-byte aligned.
- * The products are exact and the sums float32.
+ * The products are exact and the sums float32.  A bf16 x is multiplied by 16 + q and its group's sum by
+ * 16 + z: an infinite value, or a group whose sum of 32 |x| passes float32, gives NaN.
  */
 int hla2_w4_matvec(const void* x, long long x_stride, const void* qweight, const void* scales, const void* zeros,
                    const void* bias, void* y, int M, int N, int K, int group, int dtype, hla2_stream_t stream);
