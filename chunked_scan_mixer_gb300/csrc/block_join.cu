@@ -158,7 +158,7 @@ int hla2_block_join(const hla2_block_args* a, void* r, void* h, hla2_stream_t st
     const Shape s = shape_of(a->D, vec);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int tensors = 1 + (a->y ? 1 : 0) + (a->y && a->gate && a->gate_cols != 1 ? 1 : 0);
-    const Work w = work_of(a, s, vec, tensors, kFwdThreadsPerSm, 0);
+    const Work w = work_of(a, s, vec, tensors, kFwdThreadsPerSm, 0, sm_count());
     auto launch = [&](auto v, auto nv, auto tpr, auto maxt, auto mode, auto zero) {
         using T = decltype(zero);
         auto k = join_kernel<T, decltype(v)::value, decltype(nv)::value, decltype(tpr)::value, decltype(maxt)::value,

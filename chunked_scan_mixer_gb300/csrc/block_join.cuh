@@ -268,24 +268,15 @@ int check_join(const char* fn, const hla2_block_args* a) {
     return HLA2_OK;
 }
 
-int sms() {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    return v;
-}
-
 // Persistent CTAs and their ring.  Stages: as many rows ahead as fit in the SM's shared memory beside
 // the CTAs that the registers allow (512 threads of the backward, 1024 of the forward), at most
-// four; one stage copies and waits.
+// four, and no more than a CTA has rounds; one stage copies and waits.
 struct Work {
     int ctas, stages;
     size_t smem;
 };
-Work work_of(const hla2_block_args* a, const Shape& s, int vec, int tensors, int threads_per_sm, size_t least) {
+Work work_of(const hla2_block_args* a, const Shape& s, int vec, int tensors, int threads_per_sm, size_t least,
+             int sms) {
     const size_t slot = (size_t)vec * (a->dtype == HLA2_BF16 ? 2 : 4);
     const size_t stage = slot * s.threads * s.nv * tensors, room = 220 * 1024;
     int each = threads_per_sm / s.threads;
@@ -295,10 +286,11 @@ Work work_of(const hla2_block_args* a, const Shape& s, int vec, int tensors, int
     w.stages = 4;
     while (w.stages > 1 && (w.stages * stage + 2048) * each > room && !(each == 1 && w.stages * stage <= room)) --w.stages;
     while (each > 1 && (w.stages * stage + 2048) * each > room) --each;
-    w.smem = w.stages * stage > least ? w.stages * stage : least;
     const int per = s.tpr ? kSmallThreads / s.tpr : 1;
-    const long long need = (a->rows + per - 1) / per, most = (long long)each * sms();
+    const long long need = (a->rows + per - 1) / per, most = (long long)each * sms;
     w.ctas = (int)(need < most ? need : most);
+    if (w.ctas > 0 && need < (long long)w.stages * w.ctas) w.stages = (int)((need + w.ctas - 1) / w.ctas);
+    w.smem = w.stages * stage > least ? w.stages * stage : least;
     return w;
 }
 constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512;

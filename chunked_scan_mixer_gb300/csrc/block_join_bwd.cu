@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(1024) partial_sum_kernel(const float* __restri
     if (w == 0 && c < D) dst[c] = sm[0][lane];
 }
 
-Work backward_work(const hla2_block_args* a, const Shape& s, int vec, int tensors) {
-    return work_of(a, s, vec, tensors, kBwdThreadsPerSm, s.tpr ? 3 * (size_t)a->D * sizeof(float) : 0);
+Work backward_work(const hla2_block_args* a, const Shape& s, int vec, int tensors, int sms) {
+    return work_of(a, s, vec, tensors, kBwdThreadsPerSm, s.tpr ? 3 * (size_t)a->D * sizeof(float) : 0, sms);
 }
 
 }  // namespace
@@ -282,10 +282,11 @@ size_t hla2_block_join_backward_workspace_bytes(const hla2_block_args* a) {
     if (check_join("hla2_block_join_backward_workspace_bytes", a) != HLA2_OK) return (size_t)-1;
     join_ok();
     size_t most = 0;
+    const int sms = sm_count();
     const int wide = a->dtype == HLA2_BF16 ? 8 : 4;
     for (int vec : {1, 2, wide}) {  // whichever the addresses allow
         for (int tensors = 2; tensors <= 5; ++tensors) {
-            const size_t c = (size_t)backward_work(a, shape_of(a->D, vec), vec, tensors).ctas;
+            const size_t c = (size_t)backward_work(a, shape_of(a->D, vec), vec, tensors, sms).ctas;
             if (c > most) most = c;
         }
     }
@@ -320,7 +321,7 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
         const int vec = vec_of(a, outs, 5);
         const Shape s = shape_of(a->D, vec);
         const int tensors = 1 + (a->y ? 1 : 0) + (a->y && a->gate && a->gate_cols != 1 ? 1 : 0) + (dr ? 1 : 0) + (dh ? 1 : 0);
-        const Work w = backward_work(a, s, vec, tensors);
+        const Work w = backward_work(a, s, vec, tensors, sm_count());
         g.partials = w.ctas;
         auto launch = [&](auto v, auto nv, auto tpr, auto maxt, auto mode, auto zero) {
             using T = decltype(zero);

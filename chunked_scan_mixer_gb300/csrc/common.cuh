@@ -168,6 +168,20 @@ __device__ __forceinline__ float head_decay(const float* gamma, int bh, int H) {
     return gamma ? __ldg(gamma + (bh % H)) : 1.0f;
 }
 
+// SMs of the current device, asked for once per thread and device (152 where the query fails).
+inline int sm_count() {
+    thread_local int known = -1, sms = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev == known) return sms;
+    int v = 0;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    known = dev, sms = v;
+    return v;
+}
+
 // ---------------------------------------------------------------------------
 // Programmatic dependent launch.  A kernel launched with launch_pdl may start while the
 // kernel before it on the stream is still running (once every CTA of that kernel has run

@@ -30,15 +30,6 @@ int launch_failed(const char* what) {
 bool lin_dim(int x) { return x == 16 || x == 32 || x == 64 || x == 128; }
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int sm_count() {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    return v;
-}
-
 int elem_size(int dtype) { return dtype == HLA2_BF16 ? 2 : 4; }
 
 // Sizes, types: what the workspace query can check.

@@ -681,19 +681,36 @@ def _need_cuda(first, *others):
     return index
 
 
-def _scratch(nbytes, device, stream):
-    """_workspace, but under graph capture a buffer of the graph's own: the cached one is shared with
-    eager calls on the stream, which a replay would race with.  The first bytes are the status
-    word (see hla2_workspace_status), 0 in a new buffer."""
-    key = (device.index, stream or None)  # as _workspace and check_status have it
-    known = _ws_cache.get(key)
-    if known is not None and known.numel() >= nbytes and not torch.cuda.is_current_stream_capturing():
-        return known
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+_ERR_WORKSPACE = -3
+
+
+def _with_scratch(call, query, index, stream):
+    """Return code of ``call(address, bytes)`` with scratch memory of at least ``query()`` bytes.  The stream's
+    cached buffer is tried first: the library checks its size before it launches anything.  Under
+    graph capture the buffer is the graph's own: the cached one is shared with eager calls on the
+    stream, which a replay would race with.  The first bytes are the status word (see
+    hla2_workspace_status), 0 in a new buffer.  Every rejection without memory is the call's."""
+    key = (index, stream or None)  # as _workspace and check_status have it
+    capturing = _capturing()
+    if not capturing:
+        known = _ws_cache.get(key)
+        if known is not None:
+            rc = call(known.data_ptr(), known.numel())
+            if rc != _ERR_WORKSPACE:
+                return rc
+    nbytes = query()
+    if nbytes == _SIZE_MAX or nbytes == 0:
+        return call(0, 0)
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
     buf[:256].zero_()
-    if not torch.cuda.is_current_stream_capturing():
+    if not capturing:
         _ws_cache[key] = buf
-    return buf
+    return call(buf.data_ptr(), nbytes)
+
+
+def _contiguous_like(t):
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _float_vector(gamma, H, device):
@@ -738,7 +755,8 @@ def _plain_view(t):
 
 
 class _Lin(NamedTuple):
-    """One checked call: sizes, the packed argument block and the tensors that it points into."""
+    """One checked call: sizes, the fields of its argument block but for the workspace, and the
+    tensors that they point into."""
     B: int
     H: int
     Hk: int
@@ -746,12 +764,20 @@ class _Lin(NamedTuple):
     d: int
     dv: int
     device: torch.device
-    stream: int
-    args: bytes
+    index: int
+    head: tuple
     keep: tuple
 
+    def run(self, fn, backward, want_final, *rest):
+        stream = _raw_stream(self.index)
+        rc = _with_scratch(lambda p, nbytes: fn(_LINATTN_ARGS.pack(*self.head, p, nbytes), *rest, stream),
+                           lambda: lib().hla2_linattn_workspace_bytes(_LINATTN_ARGS.pack(*self.head, 0, 0), backward,
+                                                                      want_final), self.index, stream)
+        if rc:
+            _check(fn.__name__, rc)
 
-def _linattn_args(q, k, v, gamma, scale, lengths, init_state, backward, want_final):
+
+def _linattn_args(q, k, v, gamma, scale, lengths, init_state):
     index = _need_cuda(q, k, v)
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k, v must be [B, heads, n, dim]")
@@ -777,14 +803,7 @@ def _linattn_args(q, k, v, gamma, scale, lengths, init_state, backward, want_fin
     vt, *vv = _view4(v)
     head = (_DTYPES[q.dtype], B, H, Hk, n, d, dv, scale, 0 if g is None else g.data_ptr(),
             0 if lengths is None else lengths.data_ptr(), *qv, *kv, *vv, 0 if init is None else init.data_ptr())
-    args = _LINATTN_ARGS.pack(*head, 0, 0)
-    stream = _raw_stream(index)
-    nbytes = lib().hla2_linattn_workspace_bytes(args, backward, want_final)
-    ws = None
-    if nbytes != _SIZE_MAX and nbytes > 0:  # else the call itself says what is wrong
-        ws = _scratch(nbytes, device, stream)
-        args = _LINATTN_ARGS.pack(*head, ws.data_ptr(), nbytes)
-    return _Lin(B, H, Hk, n, d, dv, device, stream, args, (qt, kt, vt, g, lengths, init, ws))
+    return _Lin(B, H, Hk, n, d, dv, device, index, head, (qt, kt, vt, g, lengths, init))
 
 
 def _state_arg(name, state, shape, device):
@@ -807,12 +826,10 @@ def linattn_forward(q, k, v, gamma=None, scale=1.0, lengths=None, init_state=Non
     to continue from.  Returns out [B,H,n,dv], in q's token / head order, and with
     ``return_final_state`` the float32 state after each sequence's last token, which
     linattn_decode_step goes on from."""
-    a = _linattn_args(q, k, v, gamma, scale, lengths, init_state, 0, 1 if return_final_state else 0)
+    a = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
     o = _out4("out", out, q, (a.B, a.H, a.n, a.dv))
     fin = torch.empty((a.B, a.Hk, a.d, a.dv), dtype=torch.float32, device=a.device) if return_final_state else None
-    rc = lib().hla2_linattn_forward(a.args, _plain_view(o), None if fin is None else fin.data_ptr(), a.stream)
-    if rc:
-        _check("hla2_linattn_forward", rc)
+    a.run(lib().hla2_linattn_forward, 0, 0 if fin is None else 1, _plain_view(o), None if fin is None else fin.data_ptr())
     return (o, fin) if return_final_state else o
 
 
@@ -822,8 +839,7 @@ def linattn_backward(q, k, v, dout, gamma=None, scale=1.0, lengths=None, init_st
     dfinal_state (None: zero) of its final state.  Returns (dq, dk, dv), dk and dv summed over
     the query heads that share a key head, and with an init_state also its float32 gradient.
     gamma has no gradient."""
-    a = _linattn_args(q, k, v, gamma, scale, lengths, init_state, 1,
-                      1 if init_state is not None or dfinal_state is not None else 0)
+    a = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
     _need_cuda(q, dout)
     if dout.shape != (a.B, a.H, a.n, a.dv):
         raise ValueError("dout must be [B, H, n, dv]")
@@ -834,11 +850,9 @@ def linattn_backward(q, k, v, dout, gamma=None, scale=1.0, lengths=None, init_st
     gk = _out4("dk", dk, k, (a.B, a.Hk, a.n, a.d))
     gv = _out4("dv", dv, v, (a.B, a.Hk, a.n, a.dv))
     dinit = torch.empty(states, dtype=torch.float32, device=a.device) if init_state is not None else None
-    rc = lib().hla2_linattn_backward(a.args, View(*dov), _plain_view(gq), _plain_view(gk), _plain_view(gv),
-                                     None if dfin is None else dfin.data_ptr(),
-                                     None if dinit is None else dinit.data_ptr(), a.stream)
-    if rc:
-        _check("hla2_linattn_backward", rc)
+    a.run(lib().hla2_linattn_backward, 1, 0 if dinit is None and dfin is None else 1, View(*dov), _plain_view(gq),
+          _plain_view(gk), _plain_view(gv), None if dfin is None else dfin.data_ptr(),
+          None if dinit is None else dinit.data_ptr())
     return (gq, gk, gv) if dinit is None else (gq, gk, gv, dinit)
 
 
@@ -945,7 +959,7 @@ def block_norm(x, weight, eps=1e-6, out=None):
     8192 values; float32 or bfloat16 on the GPU)."""
     args, _, index, keep = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _contiguous_like(x)
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of x's shape, type and device")
     rc = lib().hla2_block_join(args, None, out.data_ptr(), _raw_stream(index))
@@ -970,8 +984,8 @@ def block_join(x, y, post_weight, gate=None, gate_act="sigmoid", scale=None, nex
     if y is None:
         raise ValueError("block_join needs y (block_norm is the norm alone)")
     args, _, index, keep = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
-    r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if next_weight is not None else None
+    r = _contiguous_like(x)
+    h = _contiguous_like(x) if next_weight is not None else None
     rc = lib().hla2_block_join(args, r.data_ptr(), None if h is None else h.data_ptr(), _raw_stream(index))
     if rc:
         _check("hla2_block_join", rc)
@@ -989,18 +1003,24 @@ def _block_backward(checked, x, y, gate, post_weight, scale, next_weight, dr, dh
     if dr is None and dh is None:
         raise ValueError("dr or dh is needed")
     dr, dh = (None if t is None else t.contiguous() for t in (dr, dh))
-    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)  # noqa: E731
-    dx, dy, dgate = new(x), new(y), new(gate)
-    sums = torch.empty((3, D), dtype=torch.float32, device=device)
-    dpw, dsc, dnw = (None if w is None else g for g, w in zip(sums, (post_weight, scale, next_weight)))
+    dx, dy, dgate = (None if t is None else _contiguous_like(t) for t in (x, y, gate))
+    if y is None:
+        dpw = dsc = None
+        dnw = torch.empty(D, dtype=torch.float32, device=device)
+    else:
+        sums = torch.empty((3, D), dtype=torch.float32, device=device)
+        dpw, dsc, dnw = (None if w is None else g for g, w in zip(sums, (post_weight, scale, next_weight)))
     stream = _raw_stream(index)
-    nbytes = lib().hla2_block_join_backward_workspace_bytes(args)
-    ws = 0
-    if nbytes != _SIZE_MAX and nbytes > 0:
-        # after the status word, which belongs to the calls with bounded waits
-        ws = _scratch(nbytes + 256, device, stream).data_ptr() + 256
-    rc = lib().hla2_block_join_backward(args, _addr(dr), _addr(dh), _addr(dx), _addr(dy), _addr(dgate), _addr(dpw),
-                                        _addr(dsc), _addr(dnw), ws, nbytes, stream)
+    L = lib()
+    outs = (_addr(dr), _addr(dh), _addr(dx), _addr(dy), _addr(dgate), _addr(dpw), _addr(dsc), _addr(dnw))
+    skip = 256  # the status word belongs to the calls with bounded waits
+
+    def query():
+        nbytes = L.hla2_block_join_backward_workspace_bytes(args)
+        return nbytes if nbytes in (0, _SIZE_MAX) else nbytes + skip
+
+    rc = _with_scratch(lambda p, nbytes: L.hla2_block_join_backward(args, *outs, p and p + skip, max(nbytes - skip, 0), stream),
+                       query, index, stream)
     if rc:
         _check("hla2_block_join_backward", rc)
     return BlockJoinGrads(dx, dy, dgate, dpw, dsc, dnw)
