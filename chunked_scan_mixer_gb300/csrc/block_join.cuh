@@ -33,80 +33,149 @@ struct Vec<float, 4> {
     float4 v;
 };
 
+// A thread's values in float32, two to a register pair: one packed instruction for both halves its
+// instructions, which bound these kernels beside the memory.  Single elements stay floats.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma_(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float fma_(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sum_of(F2 a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ float sum_of(float a) { return a; }
+
+// VEC values as N of P
+template <int VEC>
+struct Lanes {
+    using P = F2;
+    static constexpr int N = VEC / 2;
+    static __device__ __forceinline__ P all(float f) { return pair(f, f); }
+};
+template <>
+struct Lanes<1> {
+    using P = float;
+    static constexpr int N = 1;
+    static __device__ __forceinline__ P all(float f) { return f; }
+};
+
 template <typename T>
 __device__ __forceinline__ void unpack(const Vec<T, 1>& a, float (&f)[1]) { f[0] = to_f32(a.v); }
-__device__ __forceinline__ void unpack2(uint32_t u, float* f) {
-    f[0] = __uint_as_float(u << 16);
-    f[1] = __uint_as_float(u & 0xFFFF0000u);
+__device__ __forceinline__ F2 unpack2(uint32_t u) { return pair(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)); }
+__device__ __forceinline__ void unpack(const Vec<bf16, 2>& a, F2 (&f)[1]) { f[0] = unpack2(a.v); }
+__device__ __forceinline__ void unpack(const Vec<bf16, 8>& a, F2 (&f)[4]) {
+    f[0] = unpack2(a.v.x), f[1] = unpack2(a.v.y), f[2] = unpack2(a.v.z), f[3] = unpack2(a.v.w);
 }
-__device__ __forceinline__ void unpack(const Vec<bf16, 2>& a, float (&f)[2]) { unpack2(a.v, f); }
-__device__ __forceinline__ void unpack(const Vec<bf16, 8>& a, float (&f)[8]) {
-    unpack2(a.v.x, f);
-    unpack2(a.v.y, f + 2);
-    unpack2(a.v.z, f + 4);
-    unpack2(a.v.w, f + 6);
-}
-__device__ __forceinline__ void unpack(const Vec<float, 4>& a, float (&f)[4]) {
-    f[0] = a.v.x, f[1] = a.v.y, f[2] = a.v.z, f[3] = a.v.w;
+__device__ __forceinline__ void unpack(const Vec<float, 4>& a, F2 (&f)[2]) {
+    f[0] = pair(a.v.x, a.v.y), f[1] = pair(a.v.z, a.v.w);
 }
 template <typename T>
 __device__ __forceinline__ void pack(Vec<T, 1>& a, const float (&f)[1]) { a.v = from_f32<T>(f[0]); }
-__device__ __forceinline__ void pack(Vec<bf16, 2>& a, const float (&f)[2]) { a.v = pack_bf16x2(f[0], f[1]); }
-__device__ __forceinline__ void pack(Vec<bf16, 8>& a, const float (&f)[8]) {
-    a.v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint32_t pack2(F2 a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return pack_bf16x2(lo, hi);
 }
-__device__ __forceinline__ void pack(Vec<float, 4>& a, const float (&f)[4]) { a.v = make_float4(f[0], f[1], f[2], f[3]); }
+__device__ __forceinline__ void pack(Vec<bf16, 2>& a, const F2 (&f)[1]) { a.v = pack2(f[0]); }
+__device__ __forceinline__ void pack(Vec<bf16, 8>& a, const F2 (&f)[4]) {
+    a.v = make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+__device__ __forceinline__ void pack(Vec<float, 4>& a, const F2 (&f)[2]) {
+    split(f[0], a.v.x, a.v.y);
+    split(f[1], a.v.z, a.v.w);
+}
 
 template <typename T, int VEC>
 __device__ __forceinline__ Vec<T, VEC> ldvec(const T* p) { return *reinterpret_cast<const Vec<T, VEC>*>(p); }
-template <typename T, int VEC>
-__device__ __forceinline__ void stvec(T* p, const float (&f)[VEC]) {
+template <typename T, int VEC, typename P, int N>
+__device__ __forceinline__ void stvec(T* p, const P (&f)[N]) {
     Vec<T, VEC> a;
     pack(a, f);
     *reinterpret_cast<Vec<T, VEC>*>(p) = a;
 }
 
 // Sums of N values over the threads of a row: TPR lanes of a warp, or (TPR == 0) the CTA.
-// `red` alternates between two halves, so one barrier a call is enough.
+// `red` alternates between two halves, so one barrier a call is enough.  Two values share a warp's
+// steps: after an exchange each half of the lanes sums one of them.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[16][N], int& turn) {
+    const int lane = threadIdx.x & 31;
+    constexpr bool halves = N == 2 && (TPR == 0 || TPR == 32);
+    if constexpr (halves) {
+        const bool up = lane & 16;
+        const float give = up ? v[0] : v[1];
+        v[0] = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, give, 16);
 #pragma unroll
-    for (int o = (TPR ? TPR : 32) / 2; o; o >>= 1)
+        for (int o = 8; o; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (TPR == 0) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5, mask = nw > 8 ? 15 : 7;
-        if (lane == 0)
+        for (int o = (TPR ? TPR : 32) / 2; o; o >>= 1)
 #pragma unroll
-            for (int i = 0; i < N; ++i) red[turn][warp][i] = v[i];
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
+    if constexpr (TPR == 0) {
+        const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5, mask = nw > 8 ? 15 : 7;  // at most 16 warps
+        const int which = halves ? lane >> 4 : 0;
+        if (lane == 16 * which) red[turn][warp][which] = v[0];
         __syncthreads();
+        v[0] = (lane & mask) < nw ? red[turn][lane & mask][which] : 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = (lane & mask) < nw ? red[turn][lane & mask][i] : 0.f;
-#pragma unroll
-        for (int o = 8; o; o >>= 1)  // at most 16 warps
-            if (o < 8 || nw > 8)
-#pragma unroll
-                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        for (int o = 8; o; o >>= 1)
+            if (o < 8 || nw > 8) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
         turn ^= 1;
+    }
+    if constexpr (halves) {
+        const float mine = v[0];
+        v[0] = __shfl_sync(0xffffffffu, mine, 0);
+        v[1] = __shfl_sync(0xffffffffu, mine, 16);
     }
 }
 
 // e^x and 1 / x by the approximate units (good to about an ulp; 0 and infinity where the exact ones are)
-__device__ __forceinline__ float fast_exp(float x) {
+__device__ __forceinline__ float fast_exp2(float x) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float fast_exp(float x) { return fast_exp2(x * 1.4426950408889634f); }
 __device__ __forceinline__ float fast_rcp(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// act(z), and act'(z) into slope
+// act(z), and act'(z) into slope: with s = sigmoid(z) and t = 1 - s, act = p s and act' = s (t p + e),
+// where p = z, e = 1 for the SiLU and p = 1, e = 0 for the sigmoid
 __device__ __forceinline__ float gate_of(float z, bool silu, float& slope) {
-    const float s = fast_rcp(1.f + fast_exp(-z)), t = 1.f - s;
-    slope = silu ? fmaf(z * s, t, s) : s * t;
-    return silu ? z * s : s;
+    const float s = fast_rcp(1.f + fast_exp(-z)), t = 1.f - s, p = silu ? z : 1.f;
+    slope = s * fmaf(t, p, silu ? 1.f : 0.f);
+    return p * s;
+}
+__device__ __forceinline__ F2 gate_of(F2 z, bool silu, F2& slope) {
+    float lo, hi;
+    const F2 one = pair(1.f, 1.f);
+    split(z * pair(-1.4426950408889634f, -1.4426950408889634f), lo, hi);
+    split(fma_(pair(fast_exp2(lo), fast_exp2(hi)), one, one), lo, hi);
+    const F2 s = pair(fast_rcp(lo), fast_rcp(hi)), t = fma_(s, pair(-1.f, -1.f), one);
+    const F2 p = silu ? z : one;
+    slope = s * fma_(t, p, silu ? one : pair(0.f, 0.f));
+    return p * s;
 }
 
 // What a call has: no block output (the norm alone); a block output with a gate for each value, a
@@ -134,7 +203,8 @@ struct Ring {
             *reinterpret_cast<T*>(d) = *p;
         }
     }
-    __device__ __forceinline__ void get(int stage, int tensor, int j, float (&f)[VEC]) const {
+    template <typename P, int N>
+    __device__ __forceinline__ void get(int stage, int tensor, int j, P (&f)[N]) const {
         unpack(*reinterpret_cast<const Vec<T, VEC>*>(at(stage, tensor, j)), f);
     }
 };
@@ -269,8 +339,9 @@ int check_join(const char* fn, const hla2_block_args* a) {
 }
 
 // Persistent CTAs and their ring.  Stages: as many rows ahead as fit in the SM's shared memory beside
-// the CTAs that the registers allow (512 threads of the backward, 1024 of the forward), at most
-// four, and no more than a CTA has rounds; one stage copies and waits.
+// the CTAs that the registers allow (1024 threads of the forward, 512 of the backward, 768 where there
+// is no block output), at most four, and no more than a CTA has rounds; one stage copies and waits.
+// The backward with a block output at 768 threads spills: 272 us against 223 for 32768 rows of 2048.
 struct Work {
     int ctas, stages;
     size_t smem;
@@ -293,7 +364,7 @@ Work work_of(const hla2_block_args* a, const Shape& s, int vec, int tensors, int
     w.smem = w.stages * stage > least ? w.stages * stage : least;
     return w;
 }
-constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512;
+constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512, kNormBwdThreadsPerSm = 768;
 
 template <class K>
 bool set_smem(K kernel, size_t bytes) {

@@ -1,4 +1,6 @@
-// The backward of the block norms; the mathematics is in block_join.cu.
+// The backward of the block norms; the mathematics is in block_join.cu.  The gradients of post_weight
+// and scale are one sum over the rows, V = sum R a ny, times the other of the two: a thread keeps V and
+// dw_next of its columns.
 #include "block_join.cuh"
 
 namespace hla2 {
@@ -7,14 +9,18 @@ namespace {
 struct JoinGrads {
     const void *dr, *dh;
     void *dx, *dy, *dgate;
-    float* partial;  // [partials][3][D]: post_weight, scale, next_weight
+    float* partial;  // [partials][2][D]: V, next_weight
     int partials;
 };
 
 template <typename T, int VEC, int NV, int TPR, int MAXT, int MODE>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1)
+__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 : 2)
     join_backward_kernel(const hla2_block_args a, const JoinGrads g, int stages) {
-    extern __shared__ __align__(16) char ring_sm[];  // the ring; at the end, in a sub-warp mapping, [3][D] sums
+    pdl_trigger();
+    using L = Lanes<VEC>;
+    using P = typename L::P;
+    constexpr int N = L::N;
+    extern __shared__ __align__(16) char ring_sm[];  // the ring; at the end, in a sub-warp mapping, [2][D] sums
     __shared__ float red1[2][16][1], red2[2][16][2];
     int turn1 = 0, turn2 = 0;
     const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr, mine = threadIdx.x / tpr;
@@ -32,11 +38,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1)
     int slots = 1;
     const int ky = has_y ? slots++ : 0, kz = full ? slots++ : 0, kr = has_dr ? slots++ : 0, kh = has_dh ? slots++ : 0;
     const Ring<T, VEC, NV> ring(ring_sm, slots);
-    float gp[NV][VEC], gs[NV][VEC], gn[NV][VEC];
+    P gv[NV][N], gn[NV][N];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) gp[j][i] = gs[j][i] = gn[j][i] = 0.f;
+        for (int i = 0; i < N; ++i) gv[j][i] = gn[j][i] = L::all(0.f);
 
     const long long stride = (long long)gridDim.x * per, row_first = (long long)blockIdx.x * per + mine;
     const T *xf = static_cast<const T*>(a.x) + row_first * a.x_stride + t * VEC,
@@ -68,6 +74,24 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1)
         cp_async_commit();
     };
     for (int i = 0; i + 1 < stages; ++i) fetch(i);
+    // the norm alone has registers for its weights, and for dh until its second use
+    P kept[has_y ? 1 : NV][N], held[has_y ? 1 : NV][N];
+    if (!has_y) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (j * tpr * VEC < d_left) unpack(ldvec<T, VEC>(nw + j * tpr * VEC), kept[has_y ? 0 : j]);
+    }
+    // dh and next_weight of a vector
+    auto get_h = [&](int stage, int j, int c, bool again, P (&f)[N], P (&w)[N]) {
+        if constexpr (has_y) {
+            ring.get(stage, kh, j, f);
+            unpack(ldvec<T, VEC>(nw + c), w);
+        } else {
+            if (!again) ring.get(stage, kh, j, held[j]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = held[j][i], w[i] = kept[j][i];
+        }
+    };
     int stage = 0;
     long long at = row_first * D + t * VEC;
     for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows; row0 += stride, at += stride * D) {
@@ -78,119 +102,117 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1)
         if (MODE == kAny && a.gate && !full && live)
             a_row = gate_of(to_f32(static_cast<const T*>(a.gate)[(row0 + mine) * a.gate_stride]), silu, slope_row);
         cp_async_wait_but(stages - 1);
-        float ny[NV][VEC], ga[NV][VEC], dz[NV][VEC], inv_y = 0.f;  // norm(y), scale act(gate), scale act'(gate) u
+        P ny[NV][N], ga[NV][N], dz[NV][N], acc = L::all(0.f);  // norm(y), act(gate), scale act'(gate) u
+        float inv_y = 0.f;
         if (has_y) {
-            float s1[1] = {0.f};
 #pragma unroll
             for (int j = 0; j < NV; ++j)
                 if (j * tpr * VEC < cols) {
                     ring.get(stage, ky, j, ny[j]);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) s1[0] += ny[j][i] * ny[j][i];
+                    for (int i = 0; i < N; ++i) acc = fma_(ny[j][i], ny[j][i], acc);
                 }
+            float s1[1] = {sum_of(acc)};
             row_sum<TPR, 1>(s1, red1, turn1);
             inv_y = rsqrtf(s1[0] * inv_d + a.eps);
         }
         // r again, sum r^2 and sum (dh w) r
-        float R[NV][VEC], s2[2] = {0.f, 0.f};
+        P R[NV][N], rr = L::all(0.f), hr = L::all(0.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = j * tpr * VEC;
             if (c < cols) {
                 ring.get(stage, 0, j, R[j]);
                 if (has_y) {
-                    float fz[VEC], fw[VEC];
+                    P fz[N], fw[N], fs[N];
                     unpack(ldvec<T, VEC>(pw + c), fw);
                     if (full) ring.get(stage, kz, j, fz);
+                    if (scaled) unpack(ldvec<T, VEC>(sc + c), fs);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        ny[j][i] *= inv_y;
-                        const float u = ny[j][i] * fw[i];
-                        float slope = 0.f;
-                        ga[j][i] = full ? gate_of(fz[i], silu, slope) : a_row;
-                        dz[j][i] = full ? slope * u : u;
-                    }
-                    if (scaled) {
-                        float fs[VEC];
-                        unpack(ldvec<T, VEC>(sc + c), fs);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) {
-                            R[j][i] = fmaf(fs[i] * ga[j][i], ny[j][i] * fw[i], R[j][i]);
-                            dz[j][i] *= fs[i];
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) R[j][i] = fmaf(ga[j][i], ny[j][i] * fw[i], R[j][i]);
+                    for (int i = 0; i < N; ++i) {
+                        if (!scaled) fs[i] = L::all(1.f);
+                        ny[j][i] = ny[j][i] * L::all(inv_y);
+                        const P u = ny[j][i] * fw[i];
+                        P slope = L::all(1.f);
+                        ga[j][i] = full ? gate_of(fz[i], silu, slope) : L::all(a_row);
+                        dz[j][i] = slope * u * fs[i];
+                        R[j][i] = fma_(fs[i] * ga[j][i], u, R[j][i]);
                     }
                 }
                 if (has_dh) {
-                    float fh[VEC], fn[VEC];
-                    ring.get(stage, kh, j, fh);
-                    unpack(ldvec<T, VEC>(nw + c), fn);
+                    P fh[N], fn[N];
+                    get_h(stage, j, c, false, fh, fn);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        s2[0] += R[j][i] * R[j][i];
-                        s2[1] += fh[i] * fn[i] * R[j][i];
+                    for (int i = 0; i < N; ++i) {
+                        rr = fma_(R[j][i], R[j][i], rr);
+                        hr = fma_(fh[i] * fn[i], R[j][i], hr);
                     }
                 }
             }
         }
         float inv_r = 0.f, dot = 0.f;
         if (has_dh) {
+            float s2[2] = {sum_of(rr), sum_of(hr)};
             row_sum<TPR, 2>(s2, red2, turn2);
             inv_r = rsqrtf(s2[0] * inv_d + a.eps);
             dot = s2[1] * inv_r * inv_d;
         }
         // the gradient of r; of the gate, the scale and y's norm
-        float s3[2] = {0.f, 0.f};
+        P dn = L::all(0.f), dg = L::all(0.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = j * tpr * VEC;
             if (c < cols) {
-                float fr[VEC];
+                P fr[N];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) fr[i] = 0.f;
+                for (int i = 0; i < N; ++i) fr[i] = L::all(0.f);
                 if (has_dr) ring.get(stage, kr, j, fr);
                 if (has_dh) {
-                    float f[VEC], fn[VEC];
-                    ring.get(stage, kh, j, f);
-                    unpack(ldvec<T, VEC>(nw + c), fn);
+                    P fh[N], fn[N];
+                    get_h(stage, j, c, true, fh, fn);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const float nr = R[j][i] * inv_r;
-                        gn[j][i] = fmaf(f[i], nr, gn[j][i]);
-                        fr[i] = fmaf(inv_r, fmaf(-nr, dot, f[i] * fn[i]), fr[i]);
+                    for (int i = 0; i < N; ++i) {
+                        const P nr = R[j][i] * L::all(inv_r);
+                        gn[j][i] = fma_(fh[i], nr, gn[j][i]);
+                        fr[i] = fma_(L::all(inv_r), fma_(nr, L::all(-dot), fh[i] * fn[i]), fr[i]);
                     }
                 }
                 stvec<T, VEC>(static_cast<T*>(g.dx) + at + c, fr);
                 if (has_y) {
-                    float fw[VEC], fs[VEC];
+                    P fw[N], fs[N];
                     unpack(ldvec<T, VEC>(pw + c), fw);
                     if (scaled) unpack(ldvec<T, VEC>(sc + c), fs);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const float rg = fr[i] * ga[j][i], v = rg * ny[j][i];
-                        gs[j][i] = fmaf(v, fw[i], gs[j][i]);
-                        gp[j][i] = scaled ? fmaf(v, fs[i], gp[j][i]) : gp[j][i] + v;
-                        dz[j][i] *= fr[i];
-                        R[j][i] = scaled ? rg * fs[i] * fw[i] : rg * fw[i];  // gradient of ny
-                        s3[0] = fmaf(R[j][i], ny[j][i], s3[0]);
-                        if (MODE == kAny) s3[1] += dz[j][i];
+                    for (int i = 0; i < N; ++i) {
+                        if (!scaled) fs[i] = L::all(1.f);
+                        const P rg = fr[i] * ga[j][i];
+                        gv[j][i] = fma_(rg, ny[j][i], gv[j][i]);
+                        dz[j][i] = dz[j][i] * fr[i];
+                        R[j][i] = rg * (fs[i] * fw[i]);  // gradient of ny
+                        dn = fma_(R[j][i], ny[j][i], dn);
+                        if (MODE == kAny) dg = fma_(dz[j][i], L::all(1.f), dg);
                     }
                     if (full) stvec<T, VEC>(static_cast<T*>(g.dgate) + at + c, dz[j]);
                 }
             }
         }
         if (has_y) {
-            row_sum<TPR, 2>(s3, red2, turn2);
-            const float m = s3[0] * inv_d;
+            float s3[2] = {sum_of(dn), sum_of(dg)};
+            if (MODE == kAny) {
+                row_sum<TPR, 2>(s3, red2, turn2);
+            } else {
+                float s4[1] = {s3[0]};
+                row_sum<TPR, 1>(s4, red1, turn1);
+                s3[0] = s4[0];
+            }
+            const P m = L::all(-s3[0] * inv_d);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = j * tpr * VEC;
                 if (c < cols) {
-                    float o[VEC];
+                    P o[N];
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) o[i] = inv_y * fmaf(-ny[j][i], m, R[j][i]);
+                    for (int i = 0; i < N; ++i) o[i] = L::all(inv_y) * fma_(ny[j][i], m, R[j][i]);
                     stvec<T, VEC>(static_cast<T*>(g.dy) + at + c, o);
                 }
             }
@@ -200,8 +222,17 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1)
         stage = stage + 1 == stages ? 0 : stage + 1;
     }
     cp_async_wait_all();
-    // this CTA's partial sums: post_weight and scale with y, next_weight with dh
-    float* dst = g.partial + (size_t)blockIdx.x * 3 * D;
+    auto at_of = [](const P (&v)[N], int i) {
+        if constexpr (VEC == 1) {
+            return v[0];
+        } else {
+            float lo, hi;
+            split(v[i / 2], lo, hi);
+            return i % 2 ? hi : lo;
+        }
+    };
+    // this CTA's partial sums: V with y, next_weight with dh
+    float* dst = g.partial + (size_t)blockIdx.x * 2 * D;
     if (TPR) {  // the CTA's row groups one after another, so that the order is fixed
         float* acc = reinterpret_cast<float*>(ring_sm);
         for (int who = 0; who < per; ++who) {
@@ -213,15 +244,14 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1)
                     for (int i = 0; i < VEC; ++i) {
                         const int c = (j * tpr + t) * VEC + i;
                         if (c < D) {
-                            acc[c] = (who ? acc[c] : 0.f) + gp[j][i];
-                            acc[D + c] = (who ? acc[D + c] : 0.f) + gs[j][i];
-                            acc[2 * D + c] = (who ? acc[2 * D + c] : 0.f) + gn[j][i];
+                            acc[c] = (who ? acc[c] : 0.f) + at_of(gv[j], i);
+                            acc[D + c] = (who ? acc[D + c] : 0.f) + at_of(gn[j], i);
                         }
                     }
             }
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < 3 * D; c += kSmallThreads) dst[c] = acc[c];
+        for (int c = threadIdx.x; c < 2 * D; c += kSmallThreads) dst[c] = acc[c];
     } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -229,23 +259,24 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1)
             for (int i = 0; i < VEC; ++i) {
                 const int c = (j * tpr + t) * VEC + i;
                 if (c < D) {
-                    if (has_y) dst[c] = gp[j][i];
-                    if (scaled) dst[D + c] = gs[j][i];
-                    if (has_dh) dst[2 * D + c] = gn[j][i];
+                    if (has_y) dst[c] = at_of(gv[j], i);
+                    if (has_dh) dst[D + c] = at_of(gn[j], i);
                 }
             }
     }
 }
 
 // Sums the partial rows: 32 columns a CTA, 32 row lanes, then a tree over them in a fixed order.
-__global__ void __launch_bounds__(1024) partial_sum_kernel(const float* __restrict__ partial, int partials, int D,
-                                                           float* __restrict__ d0, float* __restrict__ d1,
-                                                           float* __restrict__ d2) {
+template <typename T>
+__global__ void __launch_bounds__(1024)
+    partial_sum_kernel(const float* __restrict__ partial, int partials, int D, const T* __restrict__ post_weight,
+                       const T* __restrict__ scale, float* __restrict__ d_post, float* __restrict__ d_scale,
+                       float* __restrict__ d_next) {
     __shared__ float sm[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
-    float* dst = which == 0 ? d0 : which == 1 ? d1 : d2;
-    if (!dst) return;
+    pdl_wait();
+    if (!(which == 0 ? d_post : d_next)) return;
     float s = 0.f;
     if (c < D) {
         const float* src = partial + (size_t)which * D + c;
@@ -253,10 +284,10 @@ __global__ void __launch_bounds__(1024) partial_sum_kernel(const float* __restri
         for (; p + 7 * 32 < partials; p += 8 * 32) {  // eight loads in flight
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = src[(size_t)(p + 32 * i) * 3 * D];
+            for (int i = 0; i < 8; ++i) v[i] = src[(size_t)(p + 32 * i) * 2 * D];
             s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
-        for (; p < partials; p += 32) s += src[(size_t)p * 3 * D];
+        for (; p < partials; p += 32) s += src[(size_t)p * 2 * D];
     }
     sm[w][lane] = s;
     __syncthreads();
@@ -264,11 +295,18 @@ __global__ void __launch_bounds__(1024) partial_sum_kernel(const float* __restri
         if (w < o) sm[w][lane] += sm[w + o][lane];
         __syncthreads();
     }
-    if (w == 0 && c < D) dst[c] = sm[0][lane];
+    if (w == 0 && c < D) {
+        if (which == 1) {
+            d_next[c] = sm[0][lane];
+        } else {
+            d_post[c] = scale ? sm[0][lane] * to_f32(scale[c]) : sm[0][lane];
+            if (d_scale) d_scale[c] = sm[0][lane] * to_f32(post_weight[c]);
+        }
+    }
 }
 
 Work backward_work(const hla2_block_args* a, const Shape& s, int vec, int tensors, int sms) {
-    return work_of(a, s, vec, tensors, kBwdThreadsPerSm, s.tpr ? 3 * (size_t)a->D * sizeof(float) : 0, sms);
+    return work_of(a, s, vec, tensors, has_y(a) ? kBwdThreadsPerSm : kNormBwdThreadsPerSm, s.tpr ? 2 * (size_t)a->D * sizeof(float) : 0, sms);
 }
 
 }  // namespace
@@ -290,7 +328,7 @@ size_t hla2_block_join_backward_workspace_bytes(const hla2_block_args* a) {
             if (c > most) most = c;
         }
     }
-    return most * 3 * (size_t)a->D * sizeof(float);
+    return most * 2 * (size_t)a->D * sizeof(float);
 }
 
 int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const void* dh, void* dx, void* dy, void* dgate,
@@ -334,9 +372,13 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
         if (dispatch(a, mode_of(a, dr), vec, s, launch))
             return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));
     }
-    partial_sum_kernel<<<dim3((a->D + 31) / 32, 3), 1024, 0, st>>>(g.partial, g.partials, a->D, dpost_weight, dscale,
-                                                                   dnext_weight);
-    if (cudaPeekAtLastError() != cudaSuccess)
+    auto join_sums = [&](auto zero) {
+        using T = decltype(zero);
+        return launch_pdl(partial_sum_kernel<T>, dim3((a->D + 31) / 32, 2), dim3(1024), 0, st, g.partial, g.partials, a->D,
+                          static_cast<const T*>(a->post_weight), static_cast<const T*>(a->scale), dpost_weight, dscale,
+                          dnext_weight);
+    };
+    if ((a->dtype == HLA2_BF16 ? join_sums(bf16{}) : join_sums(0.f)) != cudaSuccess)
         return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));
     return join_ok();
 }
