@@ -136,14 +136,28 @@ LinPass base_pass(const hla2_linattn_args* a, const LinPlan& p) {
     return s;
 }
 
-// Forward states of k, v (reverse: of q, dout): summaries, then the scan; the final state too.
-int states(const hla2_linattn_args* a, const LinPlan& p, LinPass s, float* sums, float* carry, const float* init,
+// Whether the output pass joins the segments' sums itself.  (Eight segments of 64 x 64 states: one launch
+// and 5.5 us less than the scan.)
+bool joins(const hla2_linattn_args* a, const LinPlan& p) {
+    return a->dtype == HLA2_BF16 && p.nseg > 0 && p.nseg <= kLinJoin;
+}
+
+// Forward states of k, v (reverse: of q, dout): summaries, then the scan, the final state too; `s` gets what
+// the output passes take of them (the final state with the first pass that joins them).
+int states(const hla2_linattn_args* a, const LinPlan& p, LinPass& s, float* sums, float* carry, const float* init,
            float* final_state, cudaStream_t st) {
     if (p.nseg > 1 || (final_state && p.nseg > 0)) {
         s.sums = sums;
         s.exact_sums = final_state != nullptr;
         if (run_pass(s, true, a->dtype, st)) return -1;
     }
+    if (joins(a, p)) {
+        s.prior = sums;
+        s.init = init;
+        s.fin = final_state;
+        return 0;
+    }
+    if (p.nseg > 1 || init) s.carry = carry;
     if (p.nseg > 1 || final_state || init)
         return launch_lin_scan(sums, p.nseg > 0 ? carry : nullptr, init, final_state, a->gamma, a->lengths, a->B, a->Hk,
                                a->n, p.seg_chunks * p.W, p.nseg, a->d * a->dv, s.rev, st);
@@ -198,7 +212,6 @@ int hla2_linattn_forward(const hla2_linattn_args* args, hla2_view out, float* fi
     s.s_fin = a.scale;
     if (states(&a, p, s, sums, carry, a.init_state, final_state, st)) return launch_failed("linear attention states");
     if (p.nseg == 0) return ok();
-    s.carry = p.nseg > 1 || a.init_state ? carry : nullptr;
     if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention output pass");
     return ok();
 }
@@ -248,7 +261,6 @@ int hla2_linattn_backward(const hla2_linattn_args* args, hla2_view dout, hla2_vi
         s.k = a.k, s.v = a.v;
         s.dx = a.d, s.dy = a.dv;
         if (states(&a, p, s, at, at + sf, a.init_state, nullptr, st)) return launch_failed("linear attention states");
-        s.carry = carried ? at + sf : nullptr;
         if (carried) at += 2 * sf;
         s.x = dout, s.k = a.v, s.v = a.k, s.y = dq;
         s.rx = group;
@@ -267,9 +279,9 @@ int hla2_linattn_backward(const hla2_linattn_args* args, hla2_view dout, hla2_vi
     if (states(&a, p, s, at, at + sf, dfinal_state, dinit_state, st))
         return launch_failed("linear attention reverse states");
     if (p.nseg == 0) return ok();
-    s.carry = p.nseg > 1 || dfinal_state ? at + sf : nullptr;
     s.x = a.k, s.y = dv;
     if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention dv pass");
+    s.fin = nullptr;
     s.x = a.v, s.k = dout, s.v = a.q, s.y = dk;
     s.dx = a.dv, s.dy = a.d;
     s.carry_t = 1;

@@ -30,6 +30,10 @@ struct LinPass {
     const int* lengths;        // [B] or NULL
     const float* carry;        // [B Hs][nseg] states entering the segments, or NULL (zero)
     int carry_t;               // they are stored dy x dx
+    // Tensor-core output pass, in place of carry and with the meaning that launch_lin_scan gives them: the
+    // segments' sums, the state before the scan, and where the one after it goes.  Each may be NULL.
+    const float *prior, *init;
+    float* fin;
     int exact_sums;            // the sums end in a state that is returned: exact to float32
     float* sums;               // summary pass: [B Hs][nseg][dx dy], each segment's state from zero
     int* status;               // word that a wait which gave up is recorded in
@@ -39,6 +43,12 @@ __host__ __device__ inline int lin_len(const int* lengths, int b, int n) {
     if (!lengths) return n;
     const int l = lengths[b];
     return l < 0 ? 0 : l > n ? n : l;
+}
+
+// Valid rows of the first i segments in the scan's direction
+__device__ __forceinline__ int lin_rows_before(int len, int rev, int i, int nseg, int seg_rows) {
+    return rev ? len - (int)min((long long)len, (long long)(nseg - i) * seg_rows)
+               : (int)min((long long)len, (long long)i * seg_rows);
 }
 
 __device__ __forceinline__ float lin_decay(const LinPass& a, int s) { return a.gamma ? __ldg(a.gamma + s) : 1.0f; }
@@ -54,7 +64,9 @@ int lin_simt_width(int dx, int dy, long long heads, int n, int sms);
 int lin_simt_ctas(int dx, int dy, int W);  // resident CTAs per SM
 int launch_lin_simt(const LinPass& a, bool summary, cudaStream_t st);
 
-// Tensor-core passes (bf16, any size; linattn_tc.cu): W = 128, one CTA per SM.
+// Tensor-core passes (bf16, any size; linattn_tc.cu): W = 128, one CTA per SM.  With up to kLinJoin
+// segments the output pass joins their sums itself.
+constexpr int kLinJoin = 8;
 int launch_lin_tc(const LinPass& a, bool summary, cudaStream_t st);
 
 // States entering the segments from the segment summaries, for each state element:

@@ -212,11 +212,7 @@ __global__ void __launch_bounds__(kThreads)
     const float g = gamma ? __ldg(gamma + bs % Hs) : 1.f;
     const float log2g = log2f(g);
     const int len = lin_len(lengths, b, n);
-    // valid rows of the first i segments in the scan's direction
-    auto rows_before = [&](int i) {
-        return rev ? len - (int)min((long long)len, (long long)(nseg - i) * seg_rows)
-                   : (int)min((long long)len, (long long)i * seg_rows);
-    };
+    auto rows_before = [&](int i) { return lin_rows_before(len, rev, i, nseg, seg_rows); };
     auto decay = [&](int from, int to) { return pow_decay(log2g, (float)(rows_before(to) - rows_before(from))); };
     auto step = [](float4& c, float f, const float4& v) {
         c = make_float4(fmaf(f, c.x, v.x), fmaf(f, c.y, v.y), fmaf(f, c.z, v.z), fmaf(f, c.w, v.w));

@@ -190,6 +190,56 @@ __device__ __forceinline__ void pieces8(uint4 c, float w, uint4 (&out)[P]) {
     }
 }
 
+// The state that enters the CTA's segment, into shared memory as it is stored (rows padded by four
+// floats), and the state after the scan.  Coalesced, by all threads: read by the threads that keep it, a
+// lane to a row, 128 x 128 states took 8 us of each CTA.
+__device__ __forceinline__ void stage_carry(const LinPass& a, const Where& w, float* to, float log2g, int tid, int threads) {
+    const int elems = a.dx * a.dy, inner = (a.carry_t ? a.dx : a.dy) / 4;
+    const int order = a.rev ? a.nseg - 1 - (int)blockIdx.y : blockIdx.y, seg_rows = a.seg_chunks * kW;
+    const bool ends = a.fin && order == a.nseg - 1;
+    const size_t head = (size_t)w.bs * elems;
+    const float g = lin_decay(a, w.s);
+    auto decay = [&](int i) {
+        return pow_decay(log2g, (float)(lin_rows_before(w.len, a.rev, i + 1, a.nseg, seg_rows) -
+                                        lin_rows_before(w.len, a.rev, i, a.nseg, seg_rows)));
+    };
+    auto step = [](float4& c, float f, const float4& v) {
+        c = make_float4(fmaf(f, c.x, v.x), fmaf(f, c.y, v.y), fmaf(f, c.z, v.z), fmaf(f, c.w, v.w));
+    };
+    auto scaled = [](const float4& c, float f) { return make_float4(f * c.x, f * c.y, f * c.z, f * c.w); };
+#pragma unroll 1
+    for (int e = tid; e < elems / 4; e += threads) {
+        float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a.carry) {
+            cur = reinterpret_cast<const float4*>(a.carry + (head * a.nseg + (size_t)blockIdx.y * elems))[e];
+        } else {
+            if (a.init) {
+                cur = reinterpret_cast<const float4*>(a.init + head)[e];
+                if (a.rev) cur = make_float4(cur.x / g, cur.y / g, cur.z / g, cur.w / g);
+            }
+            const float4* sums = reinterpret_cast<const float4*>(a.prior + head * a.nseg) + e;
+            const int count = order + (ends ? 1 : 0);  // sums to read: kLinJoin at most
+            float4 f = cur;
+#pragma unroll 1
+            for (int i0 = 0; i0 < count; i0 += 4) {
+                float4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i0 + i < count) v[i] = sums[(size_t)(a.rev ? a.nseg - 1 - i0 - i : i0 + i) * (elems / 4)];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i0 + i >= count) break;
+                    cur = f;
+                    step(f, decay(i0 + i), v[i]);
+                }
+            }
+            if (ends) reinterpret_cast<float4*>(a.fin + head)[e] = a.rev ? scaled(f, g) : f;
+            else cur = f;
+        }
+        *reinterpret_cast<float4*>(to + (e / inner) * (inner + 1) * 4 + e % inner * 4) = cur;
+    }
+}
+
 __device__ __forceinline__ uint64_t kdesc(uint32_t base, int ks) {  // K-major, K step of 16 features
     return tc::smem_desc(base + (uint32_t)(ks >> 2) * kBlk + (uint32_t)(ks & 3) * 32, 16, 1024);
 }
@@ -249,6 +299,10 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
                 *reinterpret_cast<uint4*>(y + (long long)(z0 + e / per) * a.y.sn + (e % per) * 8) = make_uint4(0, 0, 0, 0);
         }
     }
+    const bool carried = a.carry || a.init || (a.prior && (rev ? blockIdx.y + 1 < a.nseg : blockIdx.y > 0));
+    const bool ends = a.fin && blockIdx.y == (rev ? 0 : a.nseg - 1);
+    float* const stage = reinterpret_cast<float*>(sm + L::oX);  // before the first copy arrives there
+    if ((carried && w.nit > 0) || ends) lt::stage_carry(a, w, stage, log2g, tid, kThreads);
     if (w.nit == 0) return;
 
     const bool steep = log2g < lt::kSteep;
@@ -270,21 +324,24 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
             *reinterpret_cast<uint4*>(sm + L::oS + la_off(sc0 / 64, sr, (sc0 % 64) / 8 + j)) = la_pack8(f);
         }
     };
+    __syncthreads();
     if (warp >= lt::kB0) {
         // D = 64: dx <= 64, so only the high half takes the carry
-        const bool has = a.carry && sr < a.dx;
-        const float* src = a.carry + ((size_t)w.bs * a.nseg + blockIdx.y) * a.dx * a.dy +
-                           (a.carry_t ? sc0 * a.dx + sr : sr * a.dy + sc0);
-        const int step = a.carry_t ? a.dx : 1;
+        const bool has = carried && sr < a.dx;
+        const float* src = stage + (a.carry_t ? sc0 * (a.dx + 4) + sr : sr * (a.dy + 4) + sc0);
+        const int step = a.carry_t ? a.dx + 4 : 1;
 #pragma unroll
-        for (int j = 0; j < kSC; ++j) {
-            sig[j] = has && sc0 + (j & ~15) < a.dy ? *src : 0.f;  // dy is a multiple of 16
-            src += step;
+        for (int j = 0; j < kSC; j += 4) {
+            const bool in = has && sc0 + (j & ~15) < a.dy;  // dy is a multiple of 16
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in && !a.carry_t) v = *reinterpret_cast<const float4*>(src + j);
+            else if (in) v = make_float4(src[j * step], src[(j + 1) * step], src[(j + 2) * step], src[(j + 3) * step]);
+            sig[j] = v.x, sig[j + 1] = v.y, sig[j + 2] = v.z, sig[j + 3] = v.w;
         }
         const int first = rev ? w.c1 - 1 : w.c0, Wc = min(kW, w.len - first * kW);
         publish(steep ? 1.f : pow_decay(log2g, (float)(lt::kRef - (rev ? kW - Wc : 0))));
-        tc::fence_proxy_async();
     }
+    tc::fence_proxy_async();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
