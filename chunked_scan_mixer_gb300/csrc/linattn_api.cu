@@ -81,9 +81,16 @@ struct LinPlan {
     int W, nchunks, seg_chunks, nseg;
 };
 
+// Whether the output pass joins the segments' sums itself: the last segment's CTA then reads all of them, at
+// about 100 GB/s, where the scan takes 6 to 8 us and a launch.  So: up to 512 KB of states, and 16 of them.
+// (Eight segments of 64 x 64: 24.6 -> 20.6 us for the call.)
+bool joins(const hla2_linattn_args* a, int nseg) {
+    return a->dtype == HLA2_BF16 && nseg > 0 && nseg <= 16 && (long long)nseg * a->d * a->dv <= 128 * 1024;
+}
+
 // Segments per state head.  Unit: the time of one chunk of the output pass.  More than one segment
-// adds the summary pass (about half of the output pass: it reads two of four tensors) and about two
-// chunks' time for the scan and its launch.  The waves of CTAs count whole, each with about two chunks'
+// adds the summary pass (about half of the output pass: it reads two of four tensors) and, where there is
+// one, about two chunks' time for the scan and its launch.  The waves of CTAs count whole, each with about two chunks'
 // time to start and to end.
 LinPlan lin_plan(const hla2_linattn_args* a, int W, int slots) {
     LinPlan p{W, (a->n + W - 1) / W, 0, 0};
@@ -98,7 +105,7 @@ LinPlan lin_plan(const hla2_linattn_args* a, int W, int slots) {
         if (want > 4096) want = 4096;
         const int sc = (int)((p.nchunks + want - 1) / want), ns = (p.nchunks + sc - 1) / sc;
         const long long waves = (heads * ns + slots - 1) / slots;
-        const double cost = (double)waves * (sc + 2) * (ns > 1 ? 1.5 : 1.0) + (ns > 1 ? 2.0 : 0.0);
+        const double cost = (double)waves * (sc + 2) * (ns > 1 ? 1.5 : 1.0) + (ns > 1 && !joins(a, ns) ? 2.0 : 0.0);
         if (p.nseg == 0 || cost < best) best = cost, p.seg_chunks = sc, p.nseg = ns;
     }
     return p;
@@ -136,11 +143,6 @@ LinPass base_pass(const hla2_linattn_args* a, const LinPlan& p) {
     return s;
 }
 
-// Whether the output pass joins the segments' sums itself.  (Eight segments of 64 x 64 states: one launch
-// and 5.5 us less than the scan.)
-bool joins(const hla2_linattn_args* a, const LinPlan& p) {
-    return a->dtype == HLA2_BF16 && p.nseg > 0 && p.nseg <= kLinJoin;
-}
 
 // Forward states of k, v (reverse: of q, dout): summaries, then the scan, the final state too; `s` gets what
 // the output passes take of them (the final state with the first pass that joins them).
@@ -151,7 +153,7 @@ int states(const hla2_linattn_args* a, const LinPlan& p, LinPass& s, float* sums
         s.exact_sums = final_state != nullptr;
         if (run_pass(s, true, a->dtype, st)) return -1;
     }
-    if (joins(a, p)) {
+    if (joins(a, p.nseg)) {
         s.prior = sums;
         s.init = init;
         s.fin = final_state;

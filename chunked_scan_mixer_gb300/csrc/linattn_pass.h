@@ -64,9 +64,8 @@ int lin_simt_width(int dx, int dy, long long heads, int n, int sms);
 int lin_simt_ctas(int dx, int dy, int W);  // resident CTAs per SM
 int launch_lin_simt(const LinPass& a, bool summary, cudaStream_t st);
 
-// Tensor-core passes (bf16, any size; linattn_tc.cu): W = 128, one CTA per SM.  With up to kLinJoin
-// segments the output pass joins their sums itself.
-constexpr int kLinJoin = 8;
+// Tensor-core passes (bf16, any size; linattn_tc.cu): W = 128, one CTA per SM.  Its output pass
+// can join the segments' sums itself.
 int launch_lin_tc(const LinPass& a, bool summary, cudaStream_t st);
 
 // States entering the segments from the segment summaries, for each state element:

@@ -218,7 +218,7 @@ __device__ __forceinline__ void stage_carry(const LinPass& a, const Where& w, fl
                 if (a.rev) cur = make_float4(cur.x / g, cur.y / g, cur.z / g, cur.w / g);
             }
             const float4* sums = reinterpret_cast<const float4*>(a.prior + head * a.nseg) + e;
-            const int count = order + (ends ? 1 : 0);  // sums to read: kLinJoin at most
+            const int count = order + (ends ? 1 : 0);  // sums to read
             float4 f = cur;
 #pragma unroll 1
             for (int i0 = 0; i0 < count; i0 += 4) {
