@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
                     });
                 });
             }
-            if (s_now && Wc > 0) {
+            if (s_now && Wc > 0 && (SUMMARY || cc + 1 < c1)) {  // no row reads the state after the last chunk
                 __syncthreads();  // Sig has been read
                 const float rho = r == 0 || a.rk == 1 ? gp[Wc] : 1.f;
                 simt::with_rm(dx, dy, [&](auto RMc) {
