@@ -41,31 +41,41 @@ __device__ __forceinline__ const float* row_ptr(const hla2_view& w, int b, int h
     return static_cast<const float*>(w.p) + b * w.sb + h * w.sh + row * w.sn;
 }
 
-// rows [row0, row0 + Wc) of a view as W x D floats (leading dimension ld), the rest zero
+// rows [row0, row0 + Wc) of a view as W x D floats (leading dimension ld), the rest zero; W and D are
+// powers of two
 __device__ __forceinline__ void load_rows(float* dst, int ld, const hla2_view& w, int b, int h, int row0, int W, int Wc,
                                           int D) {
-    const int nd = D >> 2;
-    for (int e = threadIdx.x; e < W * nd; e += kThreads) {
-        const int i = e / nd, f = (e % nd) * 4;
+    const int sh = 29 - __clz(D);  // log2(D / 4)
+    for (int e = threadIdx.x; e < W << sh; e += kThreads) {
+        const int i = e >> sh, f = (e - (i << sh)) * 4;
         const float4 t = i < Wc ? load4(row_ptr(w, b, h, row0 + i) + f) : make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<float4*>(dst + i * ld + f) = t;
     }
 }
+// the same, transposed, row i times weight(i)
+template <class Weight>
 __device__ __forceinline__ void load_rows_t(float* dst, int ld, const hla2_view& w, int b, int h, int row0, int W,
-                                            int Wc, int D) {
-    const int nd = D >> 2;
-    for (int e = threadIdx.x; e < W * nd; e += kThreads) {
-        const int i = e % W, f = (e / W) * 4;  // lanes on rows: the transposed stores fall in distinct banks
+                                            int Wc, int D, Weight weight) {
+    const int sh = 31 - __clz(W);
+    for (int e = threadIdx.x; e < (D >> 2) << sh; e += kThreads) {
+        const int i = e & (W - 1), f = (e >> sh) * 4;  // lanes on rows: the transposed stores fall in distinct banks
         const float4 t = i < Wc ? load4(row_ptr(w, b, h, row0 + i) + f) : make_float4(0.f, 0.f, 0.f, 0.f);
-        dst[f * ld + i] = t.x;
-        dst[(f + 1) * ld + i] = t.y;
-        dst[(f + 2) * ld + i] = t.z;
-        dst[(f + 3) * ld + i] = t.w;
+        const float m = weight(i);
+        dst[f * ld + i] = m * t.x;
+        dst[(f + 1) * ld + i] = m * t.y;
+        dst[(f + 2) * ld + i] = m * t.z;
+        dst[(f + 3) * ld + i] = m * t.w;
     }
+}
+// the rows' lines towards the L2, for the loads of the next chunk
+__device__ __forceinline__ void prefetch_rows(const hla2_view& w, int b, int h, int row0, int rows, int D) {
+    const int sh = D > 32 ? 26 - __clz(D) : 0;  // log2 of a row's 128-byte lines
+    for (int e = threadIdx.x; e < rows << sh; e += kThreads)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row_ptr(w, b, h, row0 + (e >> sh)) + (e & ((1 << sh) - 1)) * 32));
 }
 
 template <bool SUMMARY>
-__global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
+__global__ void __launch_bounds__(kThreads, 3) lin_simt_kernel(const LinPass a) {
     extern __shared__ __align__(16) float sm[];
     const int dx = a.dx, dy = a.dy, W = a.W;
     const bool keep_y = !SUMMARY && a.rk > 1;
@@ -98,10 +108,17 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
             __syncthreads();
             if (!SUMMARY && x_new) load_rows(Xs, pad(dx), a.x, b, hx, row0, W, Wc, dx);
             if (kv_new) {
-                load_rows_t(Kt, pad(W), a.k, b, hk, row0, W, Wc, dx);
+                load_rows_t(Kt, pad(W), a.k, b, hk, row0, W, Wc, dx,
+                            [&](int i) { return !SUMMARY || i >= Wc ? 1.f : a.s_state * gp[rev ? i : Wc - 1 - i]; });
                 load_rows(Vs, dy, a.v, b, hk, row0, W, Wc, dy);
             }
             __syncthreads();
+            if (r == items - 1 && cc + 1 < c1) {  // (of the first heads, where there are several)
+                const int next = (rev ? c - 1 : c + 1) * W, rows = min(W, len - next);
+                if (!SUMMARY) prefetch_rows(a.x, b, s * a.rx, next, rows, dx);
+                prefetch_rows(a.k, b, s * a.rk, next, rows, dx);
+                prefetch_rows(a.v, b, s * a.rk, next, rows, dy);
+            }
             if (!SUMMARY) {
                 simt::with_rm(W, W, [&](auto RMc) {
                     constexpr int RM = decltype(RMc)::value;
@@ -172,8 +189,11 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinPass a) {
                     simt::for_blocks<RM>(dx, dy, [&](int m0, int n0) {
                         simt::Acc<RM> acc;
                         simt::zero<RM>(acc);
-                        simt::mac_r<RM>(acc, Kt + m0 * pad(W), pad(W), Vs + n0, dy, Wc,
-                                        [&](int j) { return a.s_state * gp[rev ? j : Wc - 1 - j]; });
+                        if (SUMMARY)
+                            simt::mac_r<RM>(acc, Kt + m0 * pad(W), pad(W), Vs + n0, dy, Wc);
+                        else
+                            simt::mac_r<RM>(acc, Kt + m0 * pad(W), pad(W), Vs + n0, dy, Wc,
+                                            [&](int j) { return a.s_state * gp[rev ? j : Wc - 1 - j]; });
 #pragma unroll
                         for (int i = 0; i < RM; ++i) simt::decay_add4(S + (m0 + i) * dy + n0, rho, acc[i]);
                     });
@@ -355,7 +375,7 @@ int lin_simt_width(int dx, int dy, long long heads, int n, int sms) {
     return W;
 }
 int lin_simt_ctas(int dx, int dy, int W) {
-    return simt::min_ctas(2, simt::ctas_per_sm(lin_smem(dx, dy, W, false).total * sizeof(float)));
+    return simt::min_ctas(3, simt::ctas_per_sm(lin_smem(dx, dy, W, false).total * sizeof(float)));
 }
 
 int launch_lin_simt(const LinPass& a, bool summary, cudaStream_t st) {
