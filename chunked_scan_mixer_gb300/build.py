@@ -4,7 +4,9 @@ Every translation unit is compiled by nvcc in parallel, then linked into
 ``chunked_scan_mixer_gb300/_build/libhla2.so``.  Nothing is installed.  ``--debug`` builds
 the bounds-checking variant (HLA2_DEBUG: global-memory indices checked against the buffer
 extents, a failed check recorded and the access skipped; see hla2_debug_status) into
-``chunked_scan_mixer_gb300/_build_debug/libhla2.so``.
+``chunked_scan_mixer_gb300/_build_debug/libhla2.so``.  The normal build also makes the Python module of
+the short calls' host side (csrc/host_calls.cpp), which the binding goes without where it cannot be
+built.
 
     python -m chunked_scan_mixer_gb300.build [--force] [--ptxas-v] [--debug]
 """
@@ -23,6 +25,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libhla2.so")
+HOST = os.path.join(BUILD, "_hla2_host.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(BUILD_DEBUG, "libhla2.so")
 
@@ -54,6 +57,36 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_host(force: bool = False) -> bool:
+    """Compiles csrc/host_calls.cpp against the torch that is installed; False where that fails."""
+    src = os.path.join(CSRC, "host_calls.cpp")
+    if not force and not _stale(HOST, [src] + _headers()):
+        return True
+    import sysconfig
+
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    include = [os.path.join(at, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
+               os.path.join(ROOT, "include")]
+    tmp = HOST + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *("-I" + i for i in include), src, "-o", tmp, "-L" + os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        r = subprocess.CompletedProcess(cmd, 1, "", str(e))
+    if r.returncode != 0:
+        sys.stderr.write(f"host_calls.cpp was not built; the binding does without it:\n{r.stderr[-2000:]}\n")
+        if os.path.exists(HOST):
+            os.remove(HOST)
+        return False
+    os.replace(tmp, HOST)
+    return True
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = None, debug: bool = False) -> str:
     nvcc = _nvcc()
     build_dir, lib = (BUILD_DEBUG, LIB_DEBUG) if debug else (BUILD, LIB)
@@ -78,6 +111,10 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
             raise RuntimeError(f"nvcc failed on {os.path.basename(s)}:\n{r.stderr}")
         return r.stderr
 
+    host = None
+    if not debug:
+        host = cf.ThreadPoolExecutor(max_workers=1)
+        host.submit(build_host, force)
     if todo:
         with cf.ThreadPoolExecutor(max_workers=jobs or min(len(todo), os.cpu_count() or 4)) as ex:
             for log in ex.map(compile_one, todo):
@@ -90,6 +127,8 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, lib)
+    if host is not None:
+        host.shutdown(wait=True)
     return lib
 
 

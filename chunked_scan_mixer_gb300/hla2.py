@@ -7,10 +7,15 @@ has not been built, every call raises ``RuntimeError``; there is no other code p
 Tensors given on the CPU are copied to the current CUDA device, processed there and
 copied back (the end-to-end path); CUDA tensors are processed in place on the
 current stream.
+
+The calls around a layer take a few microseconds on the GPU; their ordinary forms are marshalled by
+a compiled module (csrc/host_calls.cpp) which calls the same library.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 import threading
@@ -161,7 +166,27 @@ def lib():
             getattr(L, name).argtypes = [P, P, I, I, I, I, P]
             getattr(L, name).restype = I
         _lib = L
+        _load_host(L)
         return L
+
+
+HOST_PATH = os.path.join(_HERE, "_build", "_hla2_host.so")
+_host = None  # module of csrc/host_calls.cpp
+
+
+def _load_host(L):
+    """The compiled host side of the short calls, bound to the library's entry points; without it
+    they take the way through this file."""
+    global _host
+    if not os.path.exists(HOST_PATH):
+        return
+    loader = importlib.machinery.ExtensionFileLoader("_hla2_host", HOST_PATH)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_hla2_host", loader))
+    loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.hla2_linattn_forward, L.hla2_linattn_backward, L.hla2_linattn_decode_step, L.hla2_block_join,
+        L.hla2_block_join_backward, L.hla2_w4_matvec)))
+    _host = mod
 
 
 EXPORTED_SYMBOLS = (
@@ -659,9 +684,9 @@ def ahla_backward(q, k, v, dout, gamma=None, chunk=32):
 # Around a mixer layer: first-order linear attention, block norms, 4-bit projections
 # ---------------------------------------------------------------------------------------
 
-# These calls are short on the GPU (a step of one sequence takes a few microseconds), so their host
-# side is kept lean: addresses go to the library as plain integers and the argument blocks as
-# packed bytes in the C layout.
+# These calls are short on the GPU (a step of one sequence takes a few microseconds), so the compiled
+# module takes their ordinary forms (_quick), and the rest is kept lean: addresses go to the library as plain
+# integers and the argument blocks as packed bytes in the C layout.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(device).cuda_stream without the object
 
@@ -707,6 +732,22 @@ def _with_scratch(call, query, index, stream):
     if not capturing:
         _ws_cache[key] = buf
     return call(buf.data_ptr(), nbytes)
+
+
+def _cached_scratch(t):
+    """The buffer that _with_scratch would try first for a call on t's device, or None."""
+    index = t.get_device()
+    return None if index < 0 or _capturing() else _ws_cache.get((index, _raw_stream(index) or None))
+
+
+def _quick(name, *args):
+    """The call by the compiled host side; None where it is not an ordinary one (host_calls.cpp)."""
+    if _host is None:
+        if _lib is None and os.path.exists(LIB_PATH):
+            lib()
+        if _host is None:
+            return None
+    return getattr(_host, name)(*args)
 
 
 def _contiguous_like(t):
@@ -826,6 +867,11 @@ def linattn_forward(q, k, v, gamma=None, scale=1.0, lengths=None, init_state=Non
     to continue from.  Returns out [B,H,n,dv], in q's token / head order, and with
     ``return_final_state`` the float32 state after each sequence's last token, which
     linattn_decode_step goes on from."""
+    if out is None:
+        res = _quick("linattn_forward", q, k, v, gamma, scale, lengths, init_state, bool(return_final_state),
+                     _cached_scratch(q))
+        if res is not None:
+            return res
     a = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
     o = _out4("out", out, q, (a.B, a.H, a.n, a.dv))
     fin = torch.empty((a.B, a.Hk, a.d, a.dv), dtype=torch.float32, device=a.device) if return_final_state else None
@@ -839,6 +885,10 @@ def linattn_backward(q, k, v, dout, gamma=None, scale=1.0, lengths=None, init_st
     dfinal_state (None: zero) of its final state.  Returns (dq, dk, dv), dk and dv summed over
     the query heads that share a key head, and with an init_state also its float32 gradient.
     gamma has no gradient."""
+    if dq is None and dk is None and dv is None:
+        res = _quick("linattn_backward", q, k, v, gamma, scale, lengths, init_state, dout, dfinal_state, _cached_scratch(q))
+        if res is not None:
+            return res
     a = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
     _need_cuda(q, dout)
     if dout.shape != (a.B, a.H, a.n, a.dv):
@@ -859,6 +909,10 @@ def linattn_backward(q, k, v, dout, gamma=None, scale=1.0, lengths=None, init_st
 def linattn_decode_step(state, q, k, v, gamma=None, scale=1.0, out=None):
     """One token for each of N sequences: ``state`` [N,Hk,d,dv] float32 on the GPU is updated in
     place.  q [N,H,d]; k [N,Hk,d]; v [N,Hk,dv].  Returns out [N,H,dv] = scale * P^T q."""
+    if out is None:
+        res = _quick("linattn_decode_step", state, q, k, v, gamma, scale)
+        if res is not None:
+            return res
     if not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor")
     index = _need_cuda(q, k, v)
@@ -957,6 +1011,10 @@ def _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps):
 def block_norm(x, weight, eps=1e-6, out=None):
     """The norm before a block: x / sqrt(mean(x^2) + eps) * weight over the last dimension (1 to
     8192 values; float32 or bfloat16 on the GPU)."""
+    if out is None and weight is not None:
+        res = _quick("block_join", x, None, None, None, 0, None, weight, eps)
+        if res is not None:
+            return res[1]
     args, _, index, keep = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
     if out is None:
         out = _contiguous_like(x)
@@ -970,6 +1028,9 @@ def block_norm(x, weight, eps=1e-6, out=None):
 
 def block_norm_backward(x, weight, dout, eps=1e-6):
     """(dx, dweight) of block_norm; dweight is a float32 sum over the rows."""
+    res = _quick("block_join_backward", x, None, None, None, 0, None, weight, eps, None, dout, _cached_scratch(x))
+    if res is not None:
+        return res[0], res[5]
     args = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
     g = _block_backward(args, x, None, None, None, None, weight, None, dout)
     return g.dx, g.dnext_weight
@@ -983,6 +1044,11 @@ def block_join(x, y, post_weight, gate=None, gate_act="sigmoid", scale=None, nex
     next_weight [D]; all of one type, float32 or bfloat16 on the GPU.  Returns (r, h)."""
     if y is None:
         raise ValueError("block_join needs y (block_norm is the norm alone)")
+    act = GATE_ACTS.get(gate_act)
+    if act is not None:
+        res = _quick("block_join", x, y, post_weight, gate, act, scale, next_weight, eps)
+        if res is not None:
+            return res
     args, _, index, keep = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
     r = _contiguous_like(x)
     h = _contiguous_like(x) if next_weight is not None else None
@@ -1032,6 +1098,11 @@ def block_join_backward(x, y, post_weight, gate=None, gate_act="sigmoid", scale=
     (needed with next_weight).  Nothing is kept from the forward."""
     if y is None:
         raise ValueError("block_join_backward needs y (block_norm_backward is the norm alone)")
+    act = GATE_ACTS.get(gate_act)
+    if act is not None:
+        res = _quick("block_join_backward", x, y, post_weight, gate, act, scale, next_weight, eps, dr, dh, _cached_scratch(x))
+        if res is not None:
+            return BlockJoinGrads(*res)
     args = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
     return _block_backward(args, x, y, gate, post_weight, scale, next_weight, dr, dh)
 
@@ -1044,6 +1115,10 @@ def w4_matvec(x, qweight, scales, zeros=None, bias=None, out=None):
     byte j and 2 j + 1 in the high half; scales [N, K / group], group 32, 64 or 128; zeros uint8
     [N, K / group] in 0..15 (None: 8); bias [N].  x, scales and bias float32 or bfloat16
     of one type on the GPU.  Returns y [..., N].  The products are exact and the sums float32."""
+    if out is None:
+        res = _quick("w4_matvec", x, qweight, scales, zeros, bias)
+        if res is not None:
+            return res
     index = _need_cuda(x, scales, bias)
     shape = x.shape
     K = shape[-1] if x.dim() else 0
