@@ -30,6 +30,7 @@ namespace {
 template <typename T, int VEC, int NV, int TPR, int MAXT, int MODE>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 2)
     join_kernel(const hla2_block_args a, T* __restrict__ r_out, T* __restrict__ h_out, int stages) {
+    pdl_trigger();
     using L = Lanes<VEC>;
     using P = typename L::P;
     constexpr int N = L::N;
@@ -73,6 +74,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 2)
         }
         cp_async_commit();
     };
+    pdl_wait();
     for (int i = 0; i + 1 < stages; ++i) fetch(i);
     // the norm alone has registers for its weights
     P kept[has_y ? 1 : NV][N];
@@ -189,8 +191,7 @@ int hla2_block_join(const hla2_block_args* a, void* r, void* h, hla2_stream_t st
         auto k = join_kernel<T, decltype(v)::value, decltype(nv)::value, decltype(tpr)::value, decltype(maxt)::value,
                              decltype(mode)::value>;
         if (!set_smem(k, w.smem)) return -1;
-        k<<<w.ctas, s.threads, w.smem, st>>>(*a, static_cast<T*>(r), static_cast<T*>(h), w.stages);
-        return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+        return launch_rows(a, k, w, s.threads, st, *a, static_cast<T*>(r), static_cast<T*>(h), w.stages) ? 0 : -1;
     };
     if (dispatch(a, mode_of(a, h), vec, s, launch))
         return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));

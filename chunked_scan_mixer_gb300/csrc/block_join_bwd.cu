@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 :
         }
         cp_async_commit();
     };
+    pdl_wait();
     for (int i = 0; i + 1 < stages; ++i) fetch(i);
     // the norm alone has registers for its weights, and for dh until its second use
     P kept[has_y ? 1 : NV][N], held[has_y ? 1 : NV][N];
@@ -366,8 +367,7 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
             auto k = join_backward_kernel<T, decltype(v)::value, decltype(nv)::value, decltype(tpr)::value,
                                           decltype(maxt)::value, decltype(mode)::value>;
             if (!set_smem(k, w.smem)) return -1;
-            k<<<w.ctas, s.threads, w.smem, st>>>(*a, g, w.stages);
-            return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+            return launch_rows(a, k, w, s.threads, st, *a, g, w.stages) ? 0 : -1;
         };
         if (dispatch(a, mode_of(a, dr), vec, s, launch))
             return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));

@@ -299,6 +299,8 @@ __global__ void __launch_bounds__(kThreads)
     const int head = blockIdx.x, tid = threadIdx.x, NT = blockDim.x;
     const int lpr = dv >> 2, col = (tid % lpr) * 4, row = tid / lpr, step = NT / lpr;
     float* P = state + (size_t)head * d * dv;
+    pdl_trigger();
+    pdl_wait();
     float4 p[RP];
 #pragma unroll
     for (int j = 0; j < RP; ++j) p[j] = __ldcs(reinterpret_cast<const float4*>(P + (size_t)(row + j * step) * dv + col));
@@ -353,18 +355,19 @@ int launch_step_t(float* state, const void* q, const void* k, const void* v, voi
     const int vecs = d * dv / 4, threads = vecs < kThreads ? vecs : kThreads, rp = vecs / threads;
     const unsigned grid = (unsigned)N * (unsigned)Hk;
     auto go = [&](auto kfn) {
-        kfn<<<grid, threads, 0, st>>>(state, static_cast<const T*>(q), static_cast<const T*>(k),
-                                      static_cast<const T*>(v), static_cast<T*>(out), Hk, group, d, dv, gamma, scale);
+        return launch_pdl(kfn, dim3(grid), dim3(threads), 0, st, state, static_cast<const T*>(q), static_cast<const T*>(k),
+                          static_cast<const T*>(v), static_cast<T*>(out), Hk, group, d, dv, gamma, scale) == cudaSuccess
+                   ? 0
+                   : -1;
     };
     switch (rp) {
-        case 1: go(lin_step_kernel<T, 1>); break;
-        case 2: go(lin_step_kernel<T, 2>); break;
-        case 4: go(lin_step_kernel<T, 4>); break;
-        case 8: go(lin_step_kernel<T, 8>); break;
-        case 16: go(lin_step_kernel<T, 16>); break;
+        case 1: return go(lin_step_kernel<T, 1>);
+        case 2: return go(lin_step_kernel<T, 2>);
+        case 4: return go(lin_step_kernel<T, 4>);
+        case 8: return go(lin_step_kernel<T, 8>);
+        case 16: return go(lin_step_kernel<T, 16>);
         default: return -1;
     }
-    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace

@@ -104,6 +104,7 @@ struct Weights {
 
 template <typename T, int NT, int G>
 __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 3 : 2) w4_kernel(const W4Args a, const bool aligned) {
+    pdl_trigger();
     constexpr int kPieces = sizeof(T) == 4 ? 3 : 1, U = kBatch / G, J = G / 32;
     __shared__ float red[kWarps][16][NT * 8 + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 3 : 2) w4_kernel(const 
             }
         }
     };
+    pdl_wait();
     Weights<T, G> b0, b1;
     const int step = kWarps * kBatch;
     int k0 = warp * kBatch;
@@ -262,8 +264,7 @@ template <typename T, int NT, int G>
 int launch_w4_g(const W4Args& a, cudaStream_t st) {
     const bool aligned = (a.K / G) % (kBatch / G) == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 15u) == 0 &&
                          (reinterpret_cast<uintptr_t>(a.zeros) & 15u) == 0;
-    w4_kernel<T, NT, G><<<(a.N + 15) / 16, kWarps * 32, 0, st>>>(a, aligned);
-    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+    return launch_pdl(w4_kernel<T, NT, G>, dim3((a.N + 15) / 16), dim3(kWarps * 32), 0, st, a, aligned) == cudaSuccess ? 0 : -1;
 }
 template <typename T, int NT>
 int launch_w4(const W4Args& a, cudaStream_t st) {
