@@ -121,8 +121,12 @@ size_t state_array_bytes(const hla2_linattn_args* a, const LinPlan& p) {
     return ((size_t)a->B * a->Hk * p.nseg * a->d * a->dv * sizeof(float) + 255) & ~size_t(255);
 }
 
-int run_pass(const LinPass& a, bool summary, int dtype, cudaStream_t st) {
-    return dtype == HLA2_BF16 ? launch_lin_tc(a, summary, st) : launch_lin_simt(a, summary, st);
+// Passes that do not wait for each other
+int run_passes(const LinPass* p, int count, bool summary, int dtype, cudaStream_t st) {
+    if (dtype != HLA2_BF16) return launch_lin_simt(p, count, summary, st);
+    for (int i = 0; i < count; ++i)
+        if (launch_lin_tc(p[i], summary, st)) return -1;
+    return 0;
 }
 
 // Common fields of every pass of one call.
@@ -144,26 +148,40 @@ LinPass base_pass(const hla2_linattn_args* a, const LinPlan& p) {
 }
 
 
-// Forward states of k, v (reverse: of q, dout): summaries, then the scan, the final state too; `s` gets what
-// the output passes take of them (the final state with the first pass that joins them).
-int states(const hla2_linattn_args* a, const LinPlan& p, LinPass& s, float* sums, float* carry, const float* init,
-           float* final_state, cudaStream_t st) {
-    if (p.nseg > 1 || (final_state && p.nseg > 0)) {
-        s.sums = sums;
-        s.exact_sums = final_state != nullptr;
-        if (run_pass(s, true, a->dtype, st)) return -1;
-    }
+// Forward states of k, v, or reverse ones of q, dout, before the output passes: what has to run for them.
+struct States {
+    LinPass pass;  // of the summaries
+    LinScan scan;
+    bool sums, scans;
+};
+// `s` holds the states' fields and gets what the output passes take of them (the final state with the first
+// pass that joins them).
+States states(const hla2_linattn_args* a, const LinPlan& p, LinPass& s, float* sums, float* carry, const float* init,
+              float* final_state) {
+    States x{s, {sums, p.nseg > 0 ? carry : nullptr, init, final_state, s.rev}, false, false};
+    x.sums = p.nseg > 1 || (final_state && p.nseg > 0);
+    x.pass.sums = sums;
+    x.pass.exact_sums = final_state != nullptr;
     if (joins(a, p.nseg)) {
         s.prior = sums;
         s.init = init;
         s.fin = final_state;
-        return 0;
+    } else {
+        x.scans = p.nseg > 1 || final_state || init;
+        if (p.nseg > 1 || init) s.carry = carry;
     }
-    if (p.nseg > 1 || init) s.carry = carry;
-    if (p.nseg > 1 || final_state || init)
-        return launch_lin_scan(sums, p.nseg > 0 ? carry : nullptr, init, final_state, a->gamma, a->lengths, a->B, a->Hk,
-                               a->n, p.seg_chunks * p.W, p.nseg, a->d * a->dv, s.rev, st);
-    return 0;
+    return x;
+}
+int run_states(const hla2_linattn_args* a, const LinPlan& p, const States* x, int count, cudaStream_t st) {
+    LinPass passes[2];
+    LinScan scans[2];
+    int np = 0, ns = 0;
+    for (int i = 0; i < count; ++i) {
+        if (x[i].sums) passes[np++] = x[i].pass;
+        if (x[i].scans) scans[ns++] = x[i].scan;
+    }
+    if (run_passes(passes, np, true, a->dtype, st)) return -1;
+    return launch_lin_scan(scans, ns, a->gamma, a->lengths, a->B, a->Hk, a->n, p.seg_chunks * p.W, p.nseg, a->d * a->dv, st);
 }
 
 }  // namespace
@@ -212,9 +230,10 @@ int hla2_linattn_forward(const hla2_linattn_args* args, hla2_view out, float* fi
     s.rx = a.H / a.Hk;
     s.dx = a.d, s.dy = a.dv;
     s.s_fin = a.scale;
-    if (states(&a, p, s, sums, carry, a.init_state, final_state, st)) return launch_failed("linear attention states");
+    const States x = states(&a, p, s, sums, carry, a.init_state, final_state);
+    if (run_states(&a, p, &x, 1, st)) return launch_failed("linear attention states");
     if (p.nseg == 0) return ok();
-    if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention output pass");
+    if (run_passes(&s, 1, false, a.dtype, st)) return launch_failed("linear attention output pass");
     return ok();
 }
 
@@ -256,38 +275,37 @@ int hla2_linattn_backward(const hla2_linattn_args* args, hla2_view dout, hla2_vi
     float* at = p.nseg ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kStatusBytes) : nullptr;
     const int group = a.H / a.Hk;
 
-    // forward states of k, v; dq
-    if (p.nseg > 0) {
-        LinPass s = base_pass(&a, p);
-        const bool carried = p.nseg > 1 || a.init_state;
-        s.k = a.k, s.v = a.v;
-        s.dx = a.d, s.dy = a.dv;
-        if (states(&a, p, s, at, at + sf, a.init_state, nullptr, st)) return launch_failed("linear attention states");
-        if (carried) at += 2 * sf;
-        s.x = dout, s.k = a.v, s.v = a.k, s.y = dq;
-        s.rx = group;
-        s.dx = a.dv, s.dy = a.d;
-        s.carry_t = 1;
-        s.s_fin = a.scale;
-        if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention dq pass");
-    }
-    // reverse states of q, dout (scaled); dv, dk
-    LinPass s = base_pass(&a, p);
-    s.rev = 1;
-    s.rk = group;
-    s.k = a.q, s.v = dout;
-    s.dx = a.d, s.dy = a.dv;
-    s.s_col = s.s_state = a.scale;
-    if (states(&a, p, s, at, at + sf, dfinal_state, dinit_state, st))
-        return launch_failed("linear attention reverse states");
+    // forward states of k, v, for dq; reverse states of q, dout (scaled), for dv and dk
+    const bool carried = p.nseg > 1 || a.init_state;
+    LinPass q = base_pass(&a, p), v = base_pass(&a, p);
+    q.k = a.k, q.v = a.v;
+    q.dx = a.d, q.dy = a.dv;
+    v.rev = 1;
+    v.rk = group;
+    v.k = a.q, v.v = dout;
+    v.dx = a.d, v.dy = a.dv;
+    v.s_col = v.s_state = a.scale;
+    States x[2];
+    int nx = 0;
+    if (p.nseg > 0) x[nx++] = states(&a, p, q, at, at + sf, a.init_state, nullptr);
+    if (carried) at += 2 * sf;
+    x[nx++] = states(&a, p, v, at, at + sf, dfinal_state, dinit_state);
+    if (run_states(&a, p, x, nx, st)) return launch_failed("linear attention states");
     if (p.nseg == 0) return ok();
-    s.x = a.k, s.y = dv;
-    if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention dv pass");
-    s.fin = nullptr;
-    s.x = a.v, s.k = dout, s.v = a.q, s.y = dk;
-    s.dx = a.dv, s.dy = a.d;
-    s.carry_t = 1;
-    if (run_pass(s, false, a.dtype, st)) return launch_failed("linear attention dk pass");
+
+    q.x = dout, q.k = a.v, q.v = a.k, q.y = dq;
+    q.rx = group;
+    q.dx = a.dv, q.dy = a.d;
+    q.carry_t = 1;
+    q.s_fin = a.scale;
+    v.x = a.k, v.y = dv;
+    LinPass k = v;
+    k.fin = nullptr;
+    k.x = a.v, k.k = dout, k.v = a.q, k.y = dk;
+    k.dx = a.dv, k.dy = a.d;
+    k.carry_t = 1;
+    const LinPass passes[3] = {q, v, k};
+    if (run_passes(passes, 3, false, a.dtype, st)) return launch_failed("linear attention gradients");
     return ok();
 }
 

@@ -62,7 +62,13 @@ __device__ __forceinline__ float lin_decay(const LinPass& a, int s) { return a.g
 // pass took 31 us with 64 rows a chunk (32 CTAs), 14 us with 16 (128 CTAs).
 int lin_simt_width(int dx, int dy, long long heads, int n, int sms);
 int lin_simt_ctas(int dx, int dy, int W);  // resident CTAs per SM
-int launch_lin_simt(const LinPass& a, bool summary, cudaStream_t st);
+// Passes of one call that do not wait for each other go in one launch where they are small: the training step of
+// 2 heads of 1023 rows took 67 us in ten launches and takes 49 us in six.
+constexpr int kLinPasses = 3;
+struct LinPasses {
+    LinPass p[kLinPasses];
+};
+int launch_lin_simt(const LinPass* passes, int count, bool summary, cudaStream_t st);
 
 // Tensor-core passes (bf16, any size; linattn_tc.cu): W = 128, one CTA per SM.  Its output pass
 // can join the segments' sums itself.
@@ -72,9 +78,16 @@ int launch_lin_tc(const LinPass& a, bool summary, cudaStream_t st);
 // carry[s] = cur;  cur = g^(valid rows of s) cur + sums[s]  in the scan's direction.  init (nullable) is the state before the scan; reverse: the gradient of the
 // final state, which enters as init / g.  final (nullable) receives the state after it;
 // reverse: times g, the gradient of the initial state.  sums may be NULL with nseg == 1 and no final.
-int launch_lin_scan(const float* sums, float* carry, const float* init, float* final_state, const float* gamma,
-                    const int* lengths, int B, int Hs, int n, int seg_rows, int nseg, int elems, int rev,
-                    cudaStream_t st);
+// `count` scans (1 or 2) of the same sizes in one launch.
+struct LinScan {
+    const float* sums;
+    float* carry;
+    const float* init;
+    float* final_state;
+    int rev;
+};
+int launch_lin_scan(const LinScan* scans, int count, const float* gamma, const int* lengths, int B, int Hs, int n,
+                    int seg_rows, int nseg, int elems, cudaStream_t st);
 
 int launch_lin_step(float* state, const void* q, const void* k, const void* v, void* out, int N, int H, int Hk, int d,
                     int dv, const float* gamma, float scale, bool is_bf16, cudaStream_t st);

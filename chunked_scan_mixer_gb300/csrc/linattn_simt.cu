@@ -74,8 +74,11 @@ __device__ __forceinline__ void prefetch_rows(const hla2_view& w, int b, int h, 
         asm volatile("prefetch.global.L2 [%0];" ::"l"(row_ptr(w, b, h, row0 + (e >> sh)) + (e & ((1 << sh) - 1)) * 32));
 }
 
-template <bool SUMMARY>
-__global__ void __launch_bounds__(kThreads, 3) lin_simt_kernel(const LinPass a) {
+// MANY: several passes in one launch.  Their fields are loaded by an index at every use then (231 against
+// 198 us for 32 heads x 4000 rows of 64), so one pass goes by a constant address.
+template <bool SUMMARY, bool MANY>
+__global__ void __launch_bounds__(kThreads, 3) lin_simt_kernel(const __grid_constant__ LinPasses all) {
+    const LinPass& a = all.p[MANY ? blockIdx.z : 0];
     extern __shared__ __align__(16) float sm[];
     const int dx = a.dx, dy = a.dy, W = a.W;
     const bool keep_y = !SUMMARY && a.rk > 1;
@@ -219,9 +222,14 @@ constexpr int kScanAhead = 8, kScanParts = 8;
 
 template <int PARTS>
 __global__ void __launch_bounds__(kThreads)
-    lin_scan_kernel(const float* __restrict__ sums, float* __restrict__ carry, const float* __restrict__ init,
-                    float* __restrict__ fin, const float* __restrict__ gamma, const int* __restrict__ lengths, int Hs,
-                    int n, int seg_rows, int nseg, int elems, int rev) {
+    lin_scan_kernel(const LinScan s0, const LinScan s1, const float* __restrict__ gamma,
+                    const int* __restrict__ lengths, int Hs, int n, int seg_rows, int nseg, int elems) {
+    const bool second = blockIdx.z > 0;
+    const float* __restrict__ sums = second ? s1.sums : s0.sums;
+    float* __restrict__ carry = second ? s1.carry : s0.carry;
+    const float* __restrict__ init = second ? s1.init : s0.init;
+    float* __restrict__ fin = second ? s1.final_state : s0.final_state;
+    const int rev = second ? s1.rev : s0.rev;
     constexpr int kOwners = kThreads / PARTS;
     __shared__ float4 run_sum[PARTS][kOwners];
     const int bs = blockIdx.x, b = bs / Hs, owner = threadIdx.x % kOwners, part = threadIdx.x / kOwners;
@@ -381,22 +389,36 @@ int lin_simt_ctas(int dx, int dy, int W) {
     return simt::min_ctas(3, simt::ctas_per_sm(lin_smem(dx, dy, W, false).total * sizeof(float)));
 }
 
-int launch_lin_simt(const LinPass& a, bool summary, cudaStream_t st) {
-    if (a.B * a.Hs == 0 || a.nseg == 0) return 0;
-    const size_t smem = lin_smem(a.dx, a.dy, a.W, !summary && a.rk > 1).total * sizeof(float);
-    auto kfn = summary ? lin_simt_kernel<true> : lin_simt_kernel<false>;
+int launch_lin_simt(const LinPass* passes, int count, bool summary, cudaStream_t st) {
+    const LinPass& a = passes[0];  // they share the sizes of the grid
+    if (count == 0 || a.B * a.Hs == 0 || a.nseg == 0) return 0;
+    // one launch where the GPU holds all its CTAs at once, else it would gain nothing
+    if (count > 1 && (long long)a.B * a.Hs * a.nseg * count > 3LL * sm_count()) {
+        for (int i = 0; i < count; ++i)
+            if (launch_lin_simt(passes + i, 1, summary, st)) return -1;
+        return 0;
+    }
+    LinPasses all{};
+    size_t smem = 0;
+    for (int i = 0; i < count; ++i) {
+        all.p[i] = passes[i];
+        const LinPass& s = passes[i];
+        const size_t b = lin_smem(s.dx, s.dy, s.W, !summary && s.rk > 1).total * sizeof(float);
+        if (b > smem) smem = b;
+    }
+    auto kfn = count > 1 ? summary ? lin_simt_kernel<true, true> : lin_simt_kernel<false, true>
+                         : summary ? lin_simt_kernel<true, false> : lin_simt_kernel<false, false>;
     if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -1;
-    return launch_pdl(kfn, dim3(a.B * a.Hs, a.nseg), dim3(kThreads), smem, st, a) == cudaSuccess ? 0 : -1;
+    return launch_pdl(kfn, dim3(a.B * a.Hs, a.nseg, count), dim3(kThreads), smem, st, all) == cudaSuccess ? 0 : -1;
 }
 
-int launch_lin_scan(const float* sums, float* carry, const float* init, float* final_state, const float* gamma,
-                    const int* lengths, int B, int Hs, int n, int seg_rows, int nseg, int elems, int rev,
-                    cudaStream_t st) {
-    if (B * Hs == 0) return 0;
+int launch_lin_scan(const LinScan* scans, int count, const float* gamma, const int* lengths, int B, int Hs, int n,
+                    int seg_rows, int nseg, int elems, cudaStream_t st) {
+    if (count == 0 || B * Hs == 0) return 0;
     auto go = [&](auto kernel, int parts) {
         const int each = kThreads / parts * 4;  // elements of a CTA; a head's are a multiple of four
-        return launch_pdl(kernel, dim3(B * Hs, (elems + each - 1) / each), dim3(kThreads), 0, st, sums, carry, init,
-                          final_state, gamma, lengths, Hs, n, seg_rows, nseg, elems, rev) == cudaSuccess
+        return launch_pdl(kernel, dim3(B * Hs, (elems + each - 1) / each, count), dim3(kThreads), 0, st, scans[0],
+                          scans[count - 1], gamma, lengths, Hs, n, seg_rows, nseg, elems) == cudaSuccess
                    ? 0
                    : -1;
     };
