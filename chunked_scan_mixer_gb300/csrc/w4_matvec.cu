@@ -104,7 +104,6 @@ struct Weights {
 
 template <typename T, int NT, int G>
 __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 3 : 2) w4_kernel(const W4Args a, const bool aligned) {
-    pdl_trigger();
     constexpr int kPieces = sizeof(T) == 4 ? 3 : 1, U = kBatch / G, J = G / 32;
     __shared__ float red[kWarps][16][NT * 8 + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -238,6 +237,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 3 : 2) w4_kernel(const 
         if (k0 + 2 * step < a.K) load(b0, k0 + 2 * step);
         compute(b1, k0 + step);
     }
+    // Not earlier: the next kernel's CTAs would crowd on the SMs that are free while this one runs (128 CTAs, K = 8192:
+    // 9.7 us became 12.2).
+    pdl_trigger();
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float* p = &red[warp][g][t * 8 + 2 * c];
