@@ -30,7 +30,6 @@ namespace {
 template <typename T, int VEC, int NV, int TPR, int MAXT, int MODE>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 2)
     join_kernel(const hla2_block_args a, T* __restrict__ r_out, T* __restrict__ h_out, int stages) {
-    pdl_trigger();
     using L = Lanes<VEC>;
     using P = typename L::P;
     constexpr int N = L::N;
@@ -160,6 +159,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 2)
         }
         stage = stage + 1 == stages ? 0 : stage + 1;
     }
+    pdl_trigger();
 }
 
 }  // namespace

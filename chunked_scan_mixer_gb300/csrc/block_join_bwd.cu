@@ -16,7 +16,6 @@ struct JoinGrads {
 template <typename T, int VEC, int NV, int TPR, int MAXT, int MODE>
 __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 : 2)
     join_backward_kernel(const hla2_block_args a, const JoinGrads g, int stages) {
-    pdl_trigger();
     using L = Lanes<VEC>;
     using P = typename L::P;
     constexpr int N = L::N;
@@ -223,6 +222,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 :
         stage = stage + 1 == stages ? 0 : stage + 1;
     }
     cp_async_wait_all();
+    pdl_trigger();
     auto at_of = [](const P (&v)[N], int i) {
         if constexpr (VEC == 1) {
             return v[0];

@@ -87,7 +87,6 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt_kernel(const __grid_cons
           *gp = sm + L.gp;
     const int tid = threadIdx.x;
     const int seg = blockIdx.y, bs = blockIdx.x, b = bs / a.Hs, s = bs % a.Hs;
-    pdl_trigger();
     pdl_wait();
     const int len = lin_len(a.lengths, b, a.n);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
@@ -204,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt_kernel(const __grid_cons
             }
         }
     }
+    pdl_trigger();  // at the end: CTAs of the next kernel would crowd on the SMs that are free before
     if (SUMMARY) {
         __syncthreads();
         float* dst = a.sums + ((size_t)bs * a.nseg + seg) * dx * dy;
