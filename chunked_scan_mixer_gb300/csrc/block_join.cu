@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 2)
         }
         stage = stage + 1 == stages ? 0 : stage + 1;
     }
+    // At the end (as the backward): from the start on, CTAs of the next kernel crowd on the SMs that are free
+    // first (32768 rows of 2048, forward and backward: 357 us, 339 now, 344 without).
     pdl_trigger();
 }
 
@@ -191,7 +193,10 @@ int hla2_block_join(const hla2_block_args* a, void* r, void* h, hla2_stream_t st
         auto k = join_kernel<T, decltype(v)::value, decltype(nv)::value, decltype(tpr)::value, decltype(maxt)::value,
                              decltype(mode)::value>;
         if (!set_smem(k, w.smem)) return -1;
-        return launch_rows(a, k, w, s.threads, st, *a, static_cast<T*>(r), static_cast<T*>(h), w.stages) ? 0 : -1;
+        return launch_pdl(k, dim3(w.ctas), dim3(s.threads), w.smem, st, *a, static_cast<T*>(r), static_cast<T*>(h),
+                          w.stages) == cudaSuccess
+                   ? 0
+                   : -1;
     };
     if (dispatch(a, mode_of(a, h), vec, s, launch))
         return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));

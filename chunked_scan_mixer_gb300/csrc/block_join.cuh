@@ -373,17 +373,6 @@ bool set_smem(K kernel, size_t bytes) {
 }
 
 
-// Launches that start while the kernel before drains pay where a call is short: 5000 float32 rows of 999, the
-// norm forward and backward, took 35 us without and 30 us with it, 32768 bf16 rows of 2048, the join, 344
-// and 357 us (its CTAs then start unevenly over the SMs).
-template <class... KArgs, class... Args>
-bool launch_rows(const hla2_block_args* a, void (*kernel)(KArgs...), const Work& w, int threads, cudaStream_t st, Args... args) {
-    if (a->rows * a->D * (a->dtype == HLA2_BF16 ? 2 : 4) <= 32 << 20)
-        return launch_pdl(kernel, dim3(w.ctas), dim3(threads), w.smem, st, args...) == cudaSuccess;
-    kernel<<<w.ctas, threads, w.smem, st>>>(args...);
-    return cudaPeekAtLastError() == cudaSuccess;
-}
-
 // Which kernel serves the call.
 int mode_of(const hla2_block_args* a, const void* dr_or_h) {
     if (!a->y) return kNormOnly;

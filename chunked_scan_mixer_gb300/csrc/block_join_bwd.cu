@@ -367,7 +367,7 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
             auto k = join_backward_kernel<T, decltype(v)::value, decltype(nv)::value, decltype(tpr)::value,
                                           decltype(maxt)::value, decltype(mode)::value>;
             if (!set_smem(k, w.smem)) return -1;
-            return launch_rows(a, k, w, s.threads, st, *a, g, w.stages) ? 0 : -1;
+            return launch_pdl(k, dim3(w.ctas), dim3(s.threads), w.smem, st, *a, g, w.stages) == cudaSuccess ? 0 : -1;
         };
         if (dispatch(a, mode_of(a, dr), vec, s, launch))
             return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));

@@ -59,7 +59,7 @@ __device__ __forceinline__ float lin_decay(const LinPass& a, int s) { return a.g
 // SIMT passes (float32, any size); W = lin_simt_width(dx, dy, state heads, n, SMs):
 // 64 rows (32 where a dimension is 128, for the shared memory), and half or a quarter of that while the
 // chunks of all heads would not give every SM one.  Two heads of 1023 rows, d = 32, dv = 64: the output
-// pass took 31 us with 64 rows a chunk (32 CTAs), 14 us with 16 (128 CTAs).
+// pass took 31 us with 64 rows a chunk (32 CTAs), 12 us with 16 (128 CTAs).
 int lin_simt_width(int dx, int dy, long long heads, int n, int sms);
 int lin_simt_ctas(int dx, int dy, int W);  // resident CTAs per SM
 // Passes of one call that do not wait for each other go in one launch where they are small: the training step of
