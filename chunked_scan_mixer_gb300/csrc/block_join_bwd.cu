@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 :
     };
     // this CTA's partial sums: V with y, next_weight with dh
     float* dst = g.partial + (size_t)blockIdx.x * 2 * D;
-    if (TPR) {  // the CTA's row groups one after another, so that the order is fixed
+    if (TPR && TPR <= 32) {  // the CTA's row groups one after another, so that the order is fixed
         float* acc = reinterpret_cast<float*>(ring_sm);
         for (int who = 0; who < per; ++who) {
             __syncthreads();
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(1024)
 }
 
 Work backward_work(const hla2_block_args* a, const Shape& s, int vec, int tensors, int sms) {
-    return work_of(a, s, vec, tensors, has_y(a) ? kBwdThreadsPerSm : kNormBwdThreadsPerSm, s.tpr ? 2 * (size_t)a->D * sizeof(float) : 0, sms);
+    return work_of(a, s, vec, tensors, has_y(a) ? kBwdThreadsPerSm : kNormBwdThreadsPerSm, s.tpr && s.tpr <= 32 ? 2 * (size_t)a->D * sizeof(float) : 0, sms);
 }
 
 }  // namespace
