@@ -55,16 +55,38 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 2)
     const long long xs = stride * a.x_stride, ys = stride * a.y_stride, zs = stride * a.gate_stride;
     long long left = row_first < a.rows ? (a.rows - 1 - row_first) / stride + 1 : 0;  // rows still to copy
     const int d_left = D - t * VEC;  // columns from this thread's first on
+    constexpr bool holds = kHolds<T, VEC, NV>;
+    T held[3][holds ? NV : 1];
+    int held_stage = -1;
+    auto put_held = [&]() {
+        if (!holds || held_stage < 0) return;
+#pragma unroll
+        for (int j = 0; j < (holds ? NV : 1); ++j)
+            if (j * tpr * VEC < d_left) {
+                ring.put(held_stage, 0, j, held[0][j]);
+                if (has_y) ring.put(held_stage, 1, j, held[1][j]);
+                if (full) ring.put(held_stage, 2, j, held[2][j]);
+            }
+        held_stage = -1;
+    };
     auto fetch = [&](int stage) {
+        put_held();
         if (left > 0) {
             --left;
+            if (holds) held_stage = stage;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = j * tpr * VEC;
                 if (c < d_left) {
-                    ring.copy(stage, 0, j, xf + c);
-                    if (has_y) ring.copy(stage, 1, j, yf + c);
-                    if (full) ring.copy(stage, 2, j, zf + c);
+                    if constexpr (holds) {
+                        held[0][j] = xf[c];
+                        if (has_y) held[1][j] = yf[c];
+                        if (full) held[2][j] = zf[c];
+                    } else {
+                        ring.copy(stage, 0, j, xf + c);
+                        if (has_y) ring.copy(stage, 1, j, yf + c);
+                        if (full) ring.copy(stage, 2, j, zf + c);
+                    }
                 }
             }
             xf += xs;
@@ -89,6 +111,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 2)
         const bool live = row0 + mine < a.rows;
         const int cols = live ? d_left : 0;
         fetch(stage == 0 ? stages - 1 : stage - 1);  // into the slot of the row before
+        if (stages == 1) put_held();
         float a_row = 1.f, slope;
         if (MODE == kAny && a.gate && !full && live)
             a_row = gate_of(to_f32(static_cast<const T*>(a.gate)[(row0 + mine) * a.gate_stride]), silu, slope);

@@ -183,6 +183,11 @@ __device__ __forceinline__ F2 gate_of(F2 z, bool silu, F2& slope) {
 // scale and a next norm (and dr); or a block output with any of them, told at run time.
 enum { kNormOnly = 0, kAll = 1, kAny = 2 };
 
+// Single bf16 elements, which cp.async does not copy: they wait in registers while a row is worked on and
+// go to the ring (put) before the next row's loads.  With more than four a thread they go there at once.
+template <typename T, int VEC, int NV>
+constexpr bool kHolds = VEC * sizeof(T) == 2 && NV <= 4;
+
 // One thread's ring: slot (stage, tensor, j) holds its j-th vector of that tensor's row.
 template <typename T, int VEC, int NV>
 struct Ring {
@@ -204,6 +209,7 @@ struct Ring {
             *reinterpret_cast<T*>(d) = *p;
         }
     }
+    __device__ __forceinline__ void put(int stage, int tensor, int j, T v) const { *reinterpret_cast<T*>(at(stage, tensor, j)) = v; }
     template <typename P, int N>
     __device__ __forceinline__ void get(int stage, int tensor, int j, P (&f)[N]) const {
         unpack(*reinterpret_cast<const Vec<T, VEC>*>(at(stage, tensor, j)), f);
@@ -361,7 +367,7 @@ Work work_of(const hla2_block_args* a, const Shape& s, int vec, int tensors, int
     if (each < 1) each = 1;
     if (each > 16) each = 16;
     Work w;
-    w.stages = 4;
+    w.stages = slot == 2 && s.nv > 4 ? 1 : 4;  // copied at once (kHolds): no use in a ring, which would leave the L1 little
     while (w.stages > 1 && (w.stages * stage + 2048) * each > room && !(each == 1 && w.stages * stage <= room)) --w.stages;
     while (each > 1 && (w.stages * stage + 2048) * each > room) --each;
     const int per = s.tpr ? kSmallThreads / s.tpr : 1;

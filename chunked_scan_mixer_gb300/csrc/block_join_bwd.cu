@@ -51,18 +51,45 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 :
     long long left = row_first < a.rows ? (a.rows - 1 - row_first) / stride + 1 : 0;  // rows still to copy
     long long af = row_first * D + t * VEC;
     const int d_left = D - t * VEC;
+    constexpr bool holds = kHolds<T, VEC, NV>;
+    T held_in[5][holds ? NV : 1];
+    int held_stage = -1;
+    auto put_held = [&]() {
+        if (!holds || held_stage < 0) return;
+#pragma unroll
+        for (int j = 0; j < (holds ? NV : 1); ++j)
+            if (j * tpr * VEC < d_left) {
+                ring.put(held_stage, 0, j, held_in[0][j]);
+                if (has_y) ring.put(held_stage, ky, j, held_in[1][j]);
+                if (full) ring.put(held_stage, kz, j, held_in[2][j]);
+                if (has_dr) ring.put(held_stage, kr, j, held_in[3][j]);
+                if (has_dh) ring.put(held_stage, kh, j, held_in[4][j]);
+            }
+        held_stage = -1;
+    };
     auto fetch = [&](int stage) {
+        put_held();
         if (left > 0) {
             --left;
+            if (holds) held_stage = stage;
+            const T *drf = static_cast<const T*>(g.dr) + af, *dhf = static_cast<const T*>(g.dh) + af;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = j * tpr * VEC;
                 if (c < d_left) {
-                    ring.copy(stage, 0, j, xf + c);
-                    if (has_y) ring.copy(stage, ky, j, yf + c);
-                    if (full) ring.copy(stage, kz, j, zf + c);
-                    if (has_dr) ring.copy(stage, kr, j, static_cast<const T*>(g.dr) + af + c);
-                    if (has_dh) ring.copy(stage, kh, j, static_cast<const T*>(g.dh) + af + c);
+                    if constexpr (holds) {
+                        held_in[0][j] = xf[c];
+                        if (has_y) held_in[1][j] = yf[c];
+                        if (full) held_in[2][j] = zf[c];
+                        if (has_dr) held_in[3][j] = drf[c];
+                        if (has_dh) held_in[4][j] = dhf[c];
+                    } else {
+                        ring.copy(stage, 0, j, xf + c);
+                        if (has_y) ring.copy(stage, ky, j, yf + c);
+                        if (full) ring.copy(stage, kz, j, zf + c);
+                        if (has_dr) ring.copy(stage, kr, j, drf + c);
+                        if (has_dh) ring.copy(stage, kh, j, dhf + c);
+                    }
                 }
             }
             xf += xs;
@@ -98,19 +125,38 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 :
         const bool live = row0 + mine < a.rows;
         const int cols = live ? d_left : 0;
         fetch(stage == 0 ? stages - 1 : stage - 1);
+        if (stages == 1) put_held();
         float a_row = 1.f, slope_row = 0.f;
         if (MODE == kAny && a.gate && !full && live)
             a_row = gate_of(to_f32(static_cast<const T*>(a.gate)[(row0 + mine) * a.gate_stride]), silu, slope_row);
         cp_async_wait_but(stages - 1);
-        P ny[NV][N], ga[NV][N], dz[NV][N], acc = L::all(0.f);  // norm(y), act(gate), scale act'(gate) u
+        // norm(y), act(gate), scale act'(gate) u; with 16 values a thread they are formed again from the ring where
+        // they are used: kept, they spill (4000 bf16 rows of 5001, forward and backward: 1030 us, 658 so)
+        constexpr bool again = NV * VEC >= 16;
+        P ny[again ? 1 : NV][N], ga[again ? 1 : NV][N], dz[again ? 1 : NV][N], acc = L::all(0.f);
         float inv_y = 0.f;
+        auto gates = [&](int j, int c, P (&n)[N], P (&act)[N], P (&d)[N], P (&w)[N], P (&s)[N]) {  // n: y on entry
+            P z[N];
+            unpack(ldvec<T, VEC>(pw + c), w);
+            if (full) ring.get(stage, kz, j, z);
+            if (scaled) unpack(ldvec<T, VEC>(sc + c), s);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (!scaled) s[i] = L::all(1.f);
+                n[i] = n[i] * L::all(inv_y);
+                P slope = L::all(1.f);
+                act[i] = full ? gate_of(z[i], silu, slope) : L::all(a_row);
+                d[i] = slope * (n[i] * w[i]) * s[i];
+            }
+        };
         if (has_y) {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
                 if (j * tpr * VEC < cols) {
-                    ring.get(stage, ky, j, ny[j]);
+                    P(&n)[N] = ny[again ? 0 : j];
+                    ring.get(stage, ky, j, n);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) acc = fma_(ny[j][i], ny[j][i], acc);
+                    for (int i = 0; i < N; ++i) acc = fma_(n[i], n[i], acc);
                 }
             float s1[1] = {sum_of(acc)};
             row_sum<TPR, 1>(s1, red1, turn1);
@@ -124,20 +170,11 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 :
             if (c < cols) {
                 ring.get(stage, 0, j, R[j]);
                 if (has_y) {
-                    P fz[N], fw[N], fs[N];
-                    unpack(ldvec<T, VEC>(pw + c), fw);
-                    if (full) ring.get(stage, kz, j, fz);
-                    if (scaled) unpack(ldvec<T, VEC>(sc + c), fs);
+                    P fw[N], fs[N], (&n)[N] = ny[again ? 0 : j], (&act)[N] = ga[again ? 0 : j];
+                    if (again) ring.get(stage, ky, j, n);
+                    gates(j, c, n, act, dz[again ? 0 : j], fw, fs);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        if (!scaled) fs[i] = L::all(1.f);
-                        ny[j][i] = ny[j][i] * L::all(inv_y);
-                        const P u = ny[j][i] * fw[i];
-                        P slope = L::all(1.f);
-                        ga[j][i] = full ? gate_of(fz[i], silu, slope) : L::all(a_row);
-                        dz[j][i] = slope * u * fs[i];
-                        R[j][i] = fma_(fs[i] * ga[j][i], u, R[j][i]);
-                    }
+                    for (int i = 0; i < N; ++i) R[j][i] = fma_(fs[i] * act[i], n[i] * fw[i], R[j][i]);
                 }
                 if (has_dh) {
                     P fh[N], fn[N];
@@ -179,20 +216,25 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 :
                 }
                 stvec<T, VEC>(static_cast<T*>(g.dx) + at + c, fr);
                 if (has_y) {
-                    P fw[N], fs[N];
-                    unpack(ldvec<T, VEC>(pw + c), fw);
-                    if (scaled) unpack(ldvec<T, VEC>(sc + c), fs);
+                    P fw[N], fs[N], (&n)[N] = ny[again ? 0 : j], (&act)[N] = ga[again ? 0 : j], (&d)[N] = dz[again ? 0 : j];
+                    if (again) {
+                        ring.get(stage, ky, j, n);
+                        gates(j, c, n, act, d, fw, fs);
+                    } else {
+                        unpack(ldvec<T, VEC>(pw + c), fw);
+                        if (scaled) unpack(ldvec<T, VEC>(sc + c), fs);
+                    }
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
                         if (!scaled) fs[i] = L::all(1.f);
-                        const P rg = fr[i] * ga[j][i];
-                        gv[j][i] = fma_(rg, ny[j][i], gv[j][i]);
-                        dz[j][i] = dz[j][i] * fr[i];
+                        const P rg = fr[i] * act[i];
+                        gv[j][i] = fma_(rg, n[i], gv[j][i]);
+                        d[i] = d[i] * fr[i];
                         R[j][i] = rg * (fs[i] * fw[i]);  // gradient of ny
-                        dn = fma_(R[j][i], ny[j][i], dn);
-                        if (MODE == kAny) dg = fma_(dz[j][i], L::all(1.f), dg);
+                        dn = fma_(R[j][i], n[i], dn);
+                        if (MODE == kAny) dg = fma_(d[i], L::all(1.f), dg);
                     }
-                    if (full) stvec<T, VEC>(static_cast<T*>(g.dgate) + at + c, dz[j]);
+                    if (full) stvec<T, VEC>(static_cast<T*>(g.dgate) + at + c, d);
                 }
             }
         }
@@ -210,9 +252,14 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : MODE == kNormOnly ? 3 :
             for (int j = 0; j < NV; ++j) {
                 const int c = j * tpr * VEC;
                 if (c < cols) {
-                    P o[N];
+                    P o[N], (&n)[N] = ny[again ? 0 : j];
+                    if (again) {
+                        ring.get(stage, ky, j, n);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) o[i] = L::all(inv_y) * fma_(ny[j][i], m, R[j][i]);
+                        for (int i = 0; i < N; ++i) n[i] = n[i] * L::all(inv_y);
+                    }
+#pragma unroll
+                    for (int i = 0; i < N; ++i) o[i] = L::all(inv_y) * fma_(n[i], m, R[j][i]);
                     stvec<T, VEC>(static_cast<T*>(g.dy) + at + c, o);
                 }
             }
