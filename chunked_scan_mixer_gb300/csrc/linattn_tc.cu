@@ -133,7 +133,7 @@ struct Out {  // shared memory of the output kernel
     static constexpr uint32_t oGp = oS + kTile;          // g^0 .. g^128
     static constexpr uint32_t oCol = oGp + 4 * 132;      // s_col g^(64 - a_j), j = 0 .. 127
     static constexpr uint32_t oBar = oCol + 4 * 128;
-    enum { XF = 0, XE = XF + NS, OS = XE + NS, KF = OS + NS, VF = KF + NS, E = VF + NS, BG = E + NS, BGK = BG + 4, BC, YL, YD,
+    enum { XF = 0, XE = XF + NS, OS = XE + NS, KF = OS + NS, VF = KF + NS, E = VF + NS, BG = E + NS, BGK = BG + 4, BC = BGK + 2, YL, YD,
            YI, SH, SD, kBars };
     static constexpr uint32_t oMisc = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oMisc + 16 + 1024;
@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
                 for (int ks = 0; ks < D / 16; ++ks)
                     tc::mma_ss(tmem + C::G(it + 1), x + kstep(ks), k + kstep(ks), I_G, ks > 0);
                 tc::mma_commit(&bars[L::BG + ((it + 1) & 3)]);  // four: B may be three tiles behind
-                if (mode_a && rn == items - 1) tc::mma_commit(&bars[L::BGK]);
+                // two: with two items a chunk, B may be waiting for the chunk before
+                if (mode_a && rn == items - 1) tc::mma_commit(&bars[L::BGK + (cn & 1)]);
             }
             __syncwarp();
             if (C::kEarly && it >= 0) products();
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
             if (mode_a) {
                 if (poller) {
                     lt::wait(&bars[L::KF + slot], (ki / NS) & 1, abort, status, 342);
-                    lt::wait(&bars[L::BGK], ki & 1, abort, status, 343);
+                    lt::wait(&bars[L::BGK + (ki & 1)], (ki >> 1) & 1, abort, status, 343);
                 }
                 meet();
             }
