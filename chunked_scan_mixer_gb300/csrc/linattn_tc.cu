@@ -400,8 +400,9 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
                     }
                 }
             };
-            // (in turn, before the next commit on it)
-            if (lane == 0 && it > 0 && it + 1 < total)
+            // (in turn, before the next commit on it: nobody else waits for YI, and the drain would take its phase
+            // before the last one for the last)
+            if (lane == 0 && it > 0 && (mode_b || it + 1 < total))
                 lt::wait(&bars[mode_b ? L::YI : L::YD], (it - 1) & 1, abort, status, 308);
             if (!C::kEarly && it >= 0) products();
             if (lane == 0 && it + 1 < total) {  // MMA-G, into the region that MMA-Y of it - 1 read
@@ -425,7 +426,8 @@ __global__ void __launch_bounds__(lt::threads(D), 1) lin_out_tc_kernel(const __g
             if (it < 0) r = 0, ci = 0;
         }
         // drain: the last commit covers every MMA of this thread
-        if (lane == 0) lt::wait(&bars[mode_b ? L::YI : L::YD], (total - 1) & 1, &never, nullptr, 0);
+        if (lane == 0)
+            lt::wait(&bars[mode_b ? L::YI : mode_a ? L::YL : L::YD], ((mode_a ? w.nit : total) - 1) & 1, &never, nullptr, 0);
     } else if (warp == 3) {
         // --------------------------------------------------------------------------- MMA-S
         constexpr uint32_t I_S = tc::idesc_bf16(128, D, 1, 1);

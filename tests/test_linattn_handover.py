@@ -146,7 +146,7 @@ def output_pass(D, kind, items, nit, lengths, steep, held):
                     m.commit("E", ki % NS)
                     m.commit("YI", 0)
 
-            if it > 0 and it + 1 < total:
+            if it > 0 and (mode_b or it + 1 < total):
                 yield "wait", ("YI" if mode_b else "YD", 0), it - 1
             if not early and it >= 0:
                 yield from products()
@@ -162,6 +162,8 @@ def output_pass(D, kind, items, nit, lengths, steep, held):
                     m.commit("BGK", cn % n["BGK"])
             if early and it >= 0:
                 yield from products()
+        yield "wait", ("YI" if mode_b else "YL" if mode_a else "YD", 0), (nit if mode_a else total) - 1
+        assert not any(c[0] in ("YD", "YL", "YI", "E", "BG", "BGK") for c in m.queue), "the CTA would end before a commit"
 
     def mma_s():
         tiles, per = (nit, 1) if mode_a else (total, items)
