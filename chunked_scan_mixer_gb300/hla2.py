@@ -221,6 +221,16 @@ def _stream_handle(device):
 
 _ws_cache: dict = {}
 
+# Held while a call launches the kernels that pass their sums through a cached buffer: ctypes lets other threads run
+# during the call, and one of them on the same stream would launch its own kernels on the buffer in between.
+_scratch_lock = threading.RLock()
+
+
+def _alone(fn, *args):
+    """Result of a library call on cached scratch, with no other such call's launches in between."""
+    with _scratch_lock:
+        return fn(*args)
+
 
 def _workspace(nbytes, device, stream_handle):
     """Scratch reused per (device, stream); grown on demand."""
@@ -422,8 +432,8 @@ def forward(q, k, v, gamma=None, normalize=False, chunk=64, eps=1e-6, init_state
         ev = (ctypes.c_void_p * len(phase_events))(*[e.cuda_event for e in phase_events])
         opts.phase_events = ctypes.cast(ev, ctypes.POINTER(ctypes.c_void_p))
         opts.n_phase_events = len(phase_events)
-    rc = L.hla2_forward(_ptr(qd), _ptr(kd), _ptr(vd), _ptr(o), B, H, n, d, dv, _ptr(g), int(normalize),
-                        chunk, sh, ctypes.byref(opts))
+    rc = _alone(L.hla2_forward, _ptr(qd), _ptr(kd), _ptr(vd), _ptr(o), B, H, n, d, dv, _ptr(g), int(normalize), chunk, sh,
+                ctypes.byref(opts))
     _check("hla2_forward", rc)
     if save_for_backward:
         saved = SavedForBackward(ws, int(nbytes), (B, H, n, d, dv, chunk, q.dtype, device))
@@ -476,8 +486,8 @@ def ahla_forward(q, k, v, gamma=None, normalize=False, chunk=64, eps=1e-6, out=N
         ev = (ctypes.c_void_p * len(phase_events))(*[e.cuda_event for e in phase_events])
         opts.phase_events = ctypes.cast(ev, ctypes.POINTER(ctypes.c_void_p))
         opts.n_phase_events = len(phase_events)
-    _check("hla2_ahla_forward", L.hla2_ahla_forward(_ptr(qd), _ptr(kd), _ptr(vd), _ptr(o), B, H, n, d, dv, _ptr(g),
-                                                    int(normalize), chunk, sh, ctypes.byref(opts)))
+    _check("hla2_ahla_forward", _alone(L.hla2_ahla_forward, _ptr(qd), _ptr(kd), _ptr(vd), _ptr(o), B, H, n, d, dv, _ptr(g),
+                                       int(normalize), chunk, sh, ctypes.byref(opts)))
     return (o, fin) if return_final_state else o
 
 
@@ -529,8 +539,8 @@ def backward(q, k, v, dout, gamma=None, chunk=64, dq=None, dk=None, dv=None, sav
         ws = _workspace(int(nbytes), device, sh)
     opts = Opts(_DTYPES[q.dtype], float(eps), None if ws is None else ws.data_ptr(), int(nbytes), None, None,
                 None, 0, flags)
-    rc = L.hla2_backward(_ptr(qd), _ptr(kd), _ptr(vd), _ptr(dod), _ptr(gq), _ptr(gk), _ptr(gv), B, H, n, d,
-                         dvdim, _ptr(g), int(normalize), chunk, sh, ctypes.byref(opts))
+    rc = _alone(L.hla2_backward, _ptr(qd), _ptr(kd), _ptr(vd), _ptr(dod), _ptr(gq), _ptr(gk), _ptr(gv), B, H, n, d, dvdim,
+                _ptr(g), int(normalize), chunk, sh, ctypes.byref(opts))
     _check("hla2_backward", rc)
     if host:
         return gq.cpu(), gk.cpu(), gv.cpu()
@@ -632,8 +642,8 @@ def hla3_forward(q, k, v, normalize=False, chunk=64, eps=1e-6, out=None, return_
     fin = torch.empty((B, H, state_floats(d, dv)), dtype=torch.float32, device=device) if return_final_state else None
     opts = Opts(_DTYPES[q.dtype], float(eps), None if ws is None else ws.data_ptr(), int(nbytes), None,
                 None if fin is None else fin.data_ptr(), None, 0, 0)
-    _check("hla2_hla3_forward", L.hla2_hla3_forward(_ptr(qd), _ptr(kd), _ptr(vd), _ptr(o), B, H, n, d, dv, None,
-                                                    int(normalize), chunk, sh, ctypes.byref(opts)))
+    _check("hla2_hla3_forward", _alone(L.hla2_hla3_forward, _ptr(qd), _ptr(kd), _ptr(vd), _ptr(o), B, H, n, d, dv, None,
+                                       int(normalize), chunk, sh, ctypes.byref(opts)))
     return (o, fin) if return_final_state else o
 
 
@@ -674,9 +684,8 @@ def ahla_backward(q, k, v, dout, gamma=None, chunk=32):
         nbytes = 0
     ws = _workspace(int(nbytes), device, sh)
     opts = Opts(_DTYPES[q.dtype], 1e-6, None if ws is None else ws.data_ptr(), int(nbytes), None, None, None, 0, 0)
-    _check("hla2_ahla_backward", L.hla2_ahla_backward(_ptr(qd), _ptr(kd), _ptr(vd), _ptr(od), _ptr(gq), _ptr(gk),
-                                                      _ptr(gv), B, H, n, d, dv, _ptr(g), 0, chunk, sh,
-                                                      ctypes.byref(opts)))
+    _check("hla2_ahla_backward", _alone(L.hla2_ahla_backward, _ptr(qd), _ptr(kd), _ptr(vd), _ptr(od), _ptr(gq), _ptr(gk),
+                                        _ptr(gv), B, H, n, d, dv, _ptr(g), 0, chunk, sh, ctypes.byref(opts)))
     return gq, gk, gv
 
 
@@ -721,7 +730,7 @@ def _with_scratch(call, query, index, stream):
     if not capturing:
         known = _ws_cache.get(key)
         if known is not None:
-            rc = call(known.data_ptr(), known.numel())
+            rc = _alone(call, known.data_ptr(), known.numel())
             if rc != _ERR_WORKSPACE:
                 return rc
     nbytes = query()
@@ -731,7 +740,7 @@ def _with_scratch(call, query, index, stream):
     buf[:256].zero_()
     if not capturing:
         _ws_cache[key] = buf
-    return call(buf.data_ptr(), nbytes)
+    return _alone(call, buf.data_ptr(), nbytes)
 
 
 def _cached_scratch(t):
@@ -748,6 +757,12 @@ def _quick(name, *args):
         if _host is None:
             return None
     return getattr(_host, name)(*args)
+
+
+def _quick_scratch(name, t, *args):
+    """_quick for a call on the cached scratch of t's device and stream."""
+    with _scratch_lock:
+        return _quick(name, *args, _cached_scratch(t))
 
 
 def _contiguous_like(t):
@@ -868,8 +883,7 @@ def linattn_forward(q, k, v, gamma=None, scale=1.0, lengths=None, init_state=Non
     ``return_final_state`` the float32 state after each sequence's last token, which
     linattn_decode_step goes on from."""
     if out is None:
-        res = _quick("linattn_forward", q, k, v, gamma, scale, lengths, init_state, bool(return_final_state),
-                     _cached_scratch(q))
+        res = _quick_scratch("linattn_forward", q, q, k, v, gamma, scale, lengths, init_state, bool(return_final_state))
         if res is not None:
             return res
     a = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
@@ -886,7 +900,7 @@ def linattn_backward(q, k, v, dout, gamma=None, scale=1.0, lengths=None, init_st
     the query heads that share a key head, and with an init_state also its float32 gradient.
     gamma has no gradient."""
     if dq is None and dk is None and dv is None:
-        res = _quick("linattn_backward", q, k, v, gamma, scale, lengths, init_state, dout, dfinal_state, _cached_scratch(q))
+        res = _quick_scratch("linattn_backward", q, q, k, v, gamma, scale, lengths, init_state, dout, dfinal_state)
         if res is not None:
             return res
     a = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
@@ -1028,7 +1042,7 @@ def block_norm(x, weight, eps=1e-6, out=None):
 
 def block_norm_backward(x, weight, dout, eps=1e-6):
     """(dx, dweight) of block_norm; dweight is a float32 sum over the rows."""
-    res = _quick("block_join_backward", x, None, None, None, 0, None, weight, eps, None, dout, _cached_scratch(x))
+    res = _quick_scratch("block_join_backward", x, x, None, None, None, 0, None, weight, eps, None, dout)
     if res is not None:
         return res[0], res[5]
     args = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
@@ -1100,7 +1114,7 @@ def block_join_backward(x, y, post_weight, gate=None, gate_act="sigmoid", scale=
         raise ValueError("block_join_backward needs y (block_norm_backward is the norm alone)")
     act = GATE_ACTS.get(gate_act)
     if act is not None:
-        res = _quick("block_join_backward", x, y, post_weight, gate, act, scale, next_weight, eps, dr, dh, _cached_scratch(x))
+        res = _quick_scratch("block_join_backward", x, x, y, post_weight, gate, act, scale, next_weight, eps, dr, dh)
         if res is not None:
             return BlockJoinGrads(*res)
     args = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
