@@ -244,7 +244,7 @@ template <typename T, int MODE>
 int ab_pass(const AhlaBwdArgs& a, cudaStream_t st) {
     const size_t smem = ab_smem(a.d, a.W).total * sizeof(float);
     auto kfn = ahla_bwd_kernel<T, MODE>;
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -1;
+    if (raise_smem(kfn, smem) != cudaSuccess) return -1;
     kfn<<<dim3(a.nseg, a.BH), kAbThreads, smem, st>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }

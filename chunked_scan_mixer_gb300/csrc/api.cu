@@ -9,6 +9,8 @@
 #include <string.h>
 
 #include <functional>
+#include <map>
+#include <mutex>
 #include <string>
 
 #include <nvtx3/nvToolsExt.h>
@@ -140,6 +142,19 @@ int set_last_error(int code, const char* fmt, ...) {
     va_end(ap);
     g_last_error = buf;
     return code;
+}
+
+cudaError_t raise_smem(const void* kernel, size_t bytes) {
+    static std::mutex lock;
+    static std::map<std::pair<const void*, int>, size_t> raised;  // by kernel and device
+    int dev = 0;
+    if (const cudaError_t e = cudaGetDevice(&dev)) return e;
+    const std::lock_guard<std::mutex> hold(lock);
+    size_t& known = raised[{kernel, dev}];
+    if (known >= bytes) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) known = bytes;
+    return e;
 }
 }  // namespace hla2
 

@@ -381,10 +381,8 @@ constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512, kNormBwdThreadsPe
 
 template <class K>
 bool set_smem(K kernel, size_t bytes) {
-    return bytes <= 40 * 1024 ||  // 48 KB with the static part
-           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+    return bytes <= 40 * 1024 /* 48 KB with the static part */ || raise_smem(kernel, bytes) == cudaSuccess;
 }
-
 
 // Which kernel serves the call.
 int mode_of(const hla2_block_args* a, const void* dr_or_h) {

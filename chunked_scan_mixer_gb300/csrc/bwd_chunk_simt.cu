@@ -331,7 +331,7 @@ int launch_bwd_chunk_simt(const BwdArgsF& a, int d, int dv, bool rsum, cudaStrea
     if ((d & 15) || (dv & 15) || (a.W & 15)) return -1;
     const size_t smem = bwd_chunk_simt_smem(d, dv, a.W);
     auto kfn = rsum ? bwd_chunk_simt_kernel<true> : bwd_chunk_simt_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = raise_smem(kfn, smem);
     if (e != cudaSuccess) return -1;
     kfn<<<dim3(a.nseg, a.BH), kThreads, smem, st>>>(a, d, dv);
     return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;

@@ -182,6 +182,14 @@ inline int sm_count() {
     return v;
 }
 
+// Raises a kernel's dynamic shared memory limit on the current device to at least `bytes`, and never lowers it: another
+// host thread may be about to launch the same kernel with more (api.cu).
+cudaError_t raise_smem(const void* kernel, size_t bytes);
+template <class K>
+inline cudaError_t raise_smem(K* kernel, size_t bytes) {
+    return raise_smem(reinterpret_cast<const void*>(kernel), bytes);
+}
+
 // ---------------------------------------------------------------------------
 // Programmatic dependent launch.  A kernel launched with launch_pdl may start while the
 // kernel before it on the stream is still running (once every CTA of that kernel has run

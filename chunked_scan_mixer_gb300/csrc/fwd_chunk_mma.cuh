@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(MmaCfg<D, DV, W>::NT)
 template <int D, int DV, int W, int MODE, bool CM, bool UM = false>
 cudaError_t launch_mode(const ChunkArgs& a, size_t smem, cudaStream_t st) {
     auto kfn = fwd_chunk_mma_kernel<D, DV, W, MODE, CM, UM>;
-    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = raise_smem(kfn, smem);
     if (e != cudaSuccess) return e;
     kfn<<<dim3(a.nseg_launch, a.BH), MmaCfg<D, DV, W>::NT, smem, st>>>(a);
     return cudaPeekAtLastError();

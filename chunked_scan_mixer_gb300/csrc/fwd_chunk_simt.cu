@@ -376,11 +376,11 @@ int launch_fwd_chunk_simt(const ChunkArgs& a, int d, int dv, int W, bool summary
     cudaError_t e;
     if (is_bf16) {
         auto kfn = fwd_chunk_simt_kernel<bf16>;
-        e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = raise_smem(kfn, smem);
         if (e == cudaSuccess) kfn<<<grid, block, smem, st>>>(a, d, dv, W, summary, cm);
     } else {
         auto kfn = fwd_chunk_simt_kernel<float>;
-        e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = raise_smem(kfn, smem);
         if (e == cudaSuccess) kfn<<<grid, block, smem, st>>>(a, d, dv, W, summary, cm);
     }
     if (e != cudaSuccess) return -1;

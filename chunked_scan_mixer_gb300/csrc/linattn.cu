@@ -140,7 +140,7 @@ int la_pass(const LaArgs& a, bool summary, int count, cudaStream_t st) {
     if (count <= 0) return 0;
     const size_t smem = la_smem(a.d, a.dv, a.W).total * sizeof(float);
     auto kfn = summary ? la_chunk_kernel<T, true> : la_chunk_kernel<T, false>;
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -1;
+    if (raise_smem(kfn, smem) != cudaSuccess) return -1;
     kfn<<<dim3(count, a.BH), kLaThreads, smem, st>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }

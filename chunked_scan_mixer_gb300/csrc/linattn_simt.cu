@@ -408,7 +408,7 @@ int launch_lin_simt(const LinPass* passes, int count, bool summary, cudaStream_t
     }
     auto kfn = count > 1 ? summary ? lin_simt_kernel<true, true> : lin_simt_kernel<false, true>
                          : summary ? lin_simt_kernel<true, false> : lin_simt_kernel<false, false>;
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -1;
+    if (raise_smem(kfn, smem) != cudaSuccess) return -1;
     return launch_pdl(kfn, dim3(a.B * a.Hs, a.nseg, count), dim3(kThreads), smem, st, all) == cudaSuccess ? 0 : -1;
 }
 

@@ -975,21 +975,9 @@ bool lin_map(CUtensorMap* m, const hla2_view& w, int B, int heads, int n, int Dr
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The dynamic shared memory limit of a kernel, set once per device.
-template <class K>
-bool allow_smem(K kernel, uint32_t bytes, bool (&done)[64]) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    if (dev < 64 && done[dev]) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
-    if (dev < 64) done[dev] = true;
-    return true;
-}
-
 template <int D, int P>
 int launch_sum(const lt::Maps& m, const LinPass& a, cudaStream_t st) {
-    static bool done[64];
-    if (!allow_smem(lin_sum_tc_kernel<D, P>, lt::Sum<D, P>::kBytes, done)) return -1;
+    if (raise_smem(lin_sum_tc_kernel<D, P>, lt::Sum<D, P>::kBytes) != cudaSuccess) return -1;
     return launch_pdl(lin_sum_tc_kernel<D, P>, dim3(a.B * a.Hs, a.nseg), dim3(lt::kSumThreads), lt::Sum<D, P>::kBytes, st, m,
                       a) == cudaSuccess
                ? 0
@@ -1006,8 +994,7 @@ int launch_tc(const LinPass& a, bool summary, cudaStream_t st) {
         return a.exact_sums ? launch_sum<D, 3>(m, a, st) : launch_sum<D, 2>(m, a, st);
     }
     if (!lin_map(&m.x, a.x, a.B, xh, a.n, a.dx) || !lin_map(&m.y, a.y, a.B, xh, a.n, a.dy)) return -1;
-    static bool done[64];
-    if (!allow_smem(lin_out_tc_kernel<D>, lt::Out<D>::kBytes, done)) return -1;
+    if (raise_smem(lin_out_tc_kernel<D>, lt::Out<D>::kBytes) != cudaSuccess) return -1;
     return launch_pdl(lin_out_tc_kernel<D>, dim3(a.B * a.Hs, a.nseg), dim3(lt::threads(D)), lt::Out<D>::kBytes, st, m, a) ==
                    cudaSuccess
                ? 0

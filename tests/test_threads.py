@@ -105,3 +105,17 @@ def test_two_threads_on_the_default_stream(dtype):
     for i, got in kept:
         for a, b in zip(got, work[i][1]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_calls_of_different_sizes_do_not_lower_each_others_limit():
+    """Widths that share a kernel but not its shared memory, from threads that run during each other's calls."""
+    xs = [torch.randn((4000, D), device="cuda") for D in (8192, 4100, 6000)]
+    ws = [torch.ones(x.shape[1], device="cuda") for x in xs]
+    outs = [torch.empty_like(x) for x in xs]
+    want = [hla.block_norm(x, w) for x, w in zip(xs, ws)]
+    torch.cuda.synchronize()
+    together(*(lambda i=i: hla.block_norm(xs[i], ws[i], out=outs[i]) for i in range(3)), each=1500)
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert torch.equal(a, b)
