@@ -14,6 +14,7 @@ a compiled module (csrc/host_calls.cpp) which calls the same library.
 from __future__ import annotations
 
 import ctypes
+import functools
 import importlib.machinery
 import importlib.util
 import os
@@ -219,6 +220,22 @@ def _stream_handle(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _on_its_device(f):
+    """``f`` with the device of its first CUDA tensor made current: the library launches on the current device, and
+    the default stream's handle means that device's."""
+    @functools.wraps(f)
+    def call(*args, **kw):
+        for t in (*args, *kw.values()):
+            if getattr(t, "is_cuda", False):
+                index = t.get_device()
+                if index != torch.cuda.current_device():
+                    with torch.cuda.device(index):
+                        return f(*args, **kw)
+                break
+        return f(*args, **kw)
+    return call
+
+
 _ws_cache: dict = {}
 
 # Held while a call launches the kernels that pass their sums through a cached buffer: ctypes lets other threads run
@@ -248,10 +265,13 @@ def check_status(device=None):
     """Raise HLA2Error if a kernel that used this stream's cached workspace reported a
     timed-out wait.  Synchronises the current stream."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    device = torch.device(device)
     sh = _stream_handle(device)
-    buf = _ws_cache.get((device.index, sh.value))
+    index = torch.cuda.current_device() if device.index is None else device.index
+    buf = _ws_cache.get((index, sh.value))
     if buf is not None:
-        _check("hla2_workspace_status", lib().hla2_workspace_status(ctypes.c_void_p(buf.data_ptr()), sh))
+        with torch.cuda.device(index):
+            _check("hla2_workspace_status", lib().hla2_workspace_status(ctypes.c_void_p(buf.data_ptr()), sh))
 
 
 def state_floats(d, dv, compact=False):
@@ -259,6 +279,7 @@ def state_floats(d, dv, compact=False):
     return int(lib().hla2_compact_state_floats(d, dv) if compact else lib().hla2_state_floats(d, dv))
 
 
+@_on_its_device
 def _convert_state(src, d, dv, to_compact):
     if src.device.type != "cuda" or src.dtype != torch.float32 or not src.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor")
@@ -374,6 +395,7 @@ def _pipelined_host_forward(q, k, v, gamma, normalize, chunk, eps, out, masked=T
     return res
 
 
+@_on_its_device
 def forward(q, k, v, gamma=None, normalize=False, chunk=64, eps=1e-6, init_state=None,
             return_final_state=False, out=None, phase_events=None, save_for_backward=False, masked=True):
     """Masked HLA-2 forward.  q, k [B,H,n,d]; v [B,H,n,dv] (float32 or bfloat16).
@@ -448,6 +470,7 @@ def ahla_state_floats(d, dv):
     return int(lib().hla2_ahla_state_floats(d, dv))
 
 
+@_on_its_device
 def ahla_forward(q, k, v, gamma=None, normalize=False, chunk=64, eps=1e-6, out=None, phase_events=None,
                  return_final_state=False, init_state=None):
     """Asymmetric HLA forward (the masked left-cascaded product Q (K^T Q)(K^T V)).
@@ -491,6 +514,7 @@ def ahla_forward(q, k, v, gamma=None, normalize=False, chunk=64, eps=1e-6, out=N
     return (o, fin) if return_final_state else o
 
 
+@_on_its_device
 def ahla_decode_step(state, q, k, v, gamma=None, normalize=False, eps=1e-6, out=None):
     """One AHLA step; ``state`` [N,H,ahla_state_floats] float32 on the GPU is updated in
     place.  q, k [N,H,d]; v [N,H,dv].  Returns out [N,H,dv]."""
@@ -510,6 +534,7 @@ def ahla_decode_step(state, q, k, v, gamma=None, normalize=False, eps=1e-6, out=
     return o
 
 
+@_on_its_device
 def backward(q, k, v, dout, gamma=None, chunk=64, dq=None, dk=None, dv=None, saved=None, normalize=False,
              eps=1e-6):
     """Gradients (dq, dk, dv) for upstream dout of the unnormalised forward, or with
@@ -547,6 +572,7 @@ def backward(q, k, v, dout, gamma=None, chunk=64, dq=None, dk=None, dv=None, sav
     return gq, gk, gv
 
 
+@_on_its_device
 def decode_step(state, q, k, v, gamma=None, normalize=False, eps=1e-6, out=None, compact=False, masked=True):
     """One decode step; ``state`` [N,H,state_floats(d, dv, compact)] float32 on the GPU is
     updated in place (compact: the block-triangular S layout).  q, k [N,H,d]; v [N,H,dv].
@@ -593,6 +619,7 @@ def mq_merge_state(key_state, head_state, d, dv):
     return torch.cat([S, head_state], dim=-1).contiguous()
 
 
+@_on_its_device
 def decode_step_mq(key_state, head_state, q, k, v, gamma=None, normalize=False, eps=1e-6, out=None, masked=True):
     """One decode step with one key moment per key group (multi-query sharing).
     key_state [N,Hk,d*d] and head_state [N,H,mq_head_state_floats(d, dv)] float32 on the GPU
@@ -618,6 +645,7 @@ def decode_step_mq(key_state, head_state, q, k, v, gamma=None, normalize=False, 
     return o
 
 
+@_on_its_device
 def hla3_forward(q, k, v, normalize=False, chunk=64, eps=1e-6, out=None, return_final_state=False):
     """Masked third-order output at gamma = 1 (every factor of A A^T A and the partial product
     of the first two causally masked).  q, k [B,H,n,d]; v [B,H,n,dv] on the GPU, float32 or
@@ -647,6 +675,7 @@ def hla3_forward(q, k, v, normalize=False, chunk=64, eps=1e-6, out=None, return_
     return (o, fin) if return_final_state else o
 
 
+@_on_its_device
 def hla3_decode_step(state, q, k, v, normalize=False, eps=1e-6, out=None):
     """One third-order streaming step (gamma = 1).  state [N,H,state_floats(d, dv)] float32 on
     the GPU, laid out S^K | P^KV | Y | m^K | y, updated in place; q, k [N,H,d]; v [N,H,dv].
@@ -666,6 +695,7 @@ def hla3_decode_step(state, q, k, v, normalize=False, eps=1e-6, out=None):
     return o
 
 
+@_on_its_device
 def ahla_backward(q, k, v, dout, gamma=None, chunk=32):
     """Gradients (dq, dk, dv) of the unnormalised AHLA output for upstream dout.  float32 or
     bfloat16 CUDA tensors [B,H,n,d] (d == dv)."""
@@ -886,6 +916,11 @@ def linattn_forward(q, k, v, gamma=None, scale=1.0, lengths=None, init_state=Non
         res = _quick_scratch("linattn_forward", q, q, k, v, gamma, scale, lengths, init_state, bool(return_final_state))
         if res is not None:
             return res
+    return _linattn_forward(q, k, v, gamma, scale, lengths, init_state, return_final_state, out)
+
+
+@_on_its_device
+def _linattn_forward(q, k, v, gamma, scale, lengths, init_state, return_final_state, out):
     a = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
     o = _out4("out", out, q, (a.B, a.H, a.n, a.dv))
     fin = torch.empty((a.B, a.Hk, a.d, a.dv), dtype=torch.float32, device=a.device) if return_final_state else None
@@ -903,6 +938,11 @@ def linattn_backward(q, k, v, dout, gamma=None, scale=1.0, lengths=None, init_st
         res = _quick_scratch("linattn_backward", q, q, k, v, gamma, scale, lengths, init_state, dout, dfinal_state)
         if res is not None:
             return res
+    return _linattn_backward(q, k, v, dout, gamma, scale, lengths, init_state, dfinal_state, dq, dk, dv)
+
+
+@_on_its_device
+def _linattn_backward(q, k, v, dout, gamma, scale, lengths, init_state, dfinal_state, dq, dk, dv):
     a = _linattn_args(q, k, v, gamma, scale, lengths, init_state)
     _need_cuda(q, dout)
     if dout.shape != (a.B, a.H, a.n, a.dv):
@@ -927,6 +967,11 @@ def linattn_decode_step(state, q, k, v, gamma=None, scale=1.0, out=None):
         res = _quick("linattn_decode_step", state, q, k, v, gamma, scale)
         if res is not None:
             return res
+    return _linattn_decode_step(state, q, k, v, gamma, scale, out)
+
+
+@_on_its_device
+def _linattn_decode_step(state, q, k, v, gamma, scale, out):
     if not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor")
     index = _need_cuda(q, k, v)
@@ -1029,6 +1074,11 @@ def block_norm(x, weight, eps=1e-6, out=None):
         res = _quick("block_join", x, None, None, None, 0, None, weight, eps)
         if res is not None:
             return res[1]
+    return _block_norm(x, weight, eps, out)
+
+
+@_on_its_device
+def _block_norm(x, weight, eps, out):
     args, _, index, keep = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
     if out is None:
         out = _contiguous_like(x)
@@ -1045,8 +1095,7 @@ def block_norm_backward(x, weight, dout, eps=1e-6):
     res = _quick_scratch("block_join_backward", x, x, None, None, None, 0, None, weight, eps, None, dout)
     if res is not None:
         return res[0], res[5]
-    args = _block_args(x, None, None, None, "sigmoid", None, weight, eps)
-    g = _block_backward(args, x, None, None, None, None, weight, None, dout)
+    g = _block_backward(x, None, None, None, "sigmoid", None, weight, None, dout, eps)
     return g.dx, g.dnext_weight
 
 
@@ -1063,6 +1112,11 @@ def block_join(x, y, post_weight, gate=None, gate_act="sigmoid", scale=None, nex
         res = _quick("block_join", x, y, post_weight, gate, act, scale, next_weight, eps)
         if res is not None:
             return res
+    return _block_join(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
+
+
+@_on_its_device
+def _block_join(x, y, post_weight, gate, gate_act, scale, next_weight, eps):
     args, _, index, keep = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
     r = _contiguous_like(x)
     h = _contiguous_like(x) if next_weight is not None else None
@@ -1072,8 +1126,9 @@ def block_join(x, y, post_weight, gate=None, gate_act="sigmoid", scale=None, nex
     return r, h
 
 
-def _block_backward(checked, x, y, gate, post_weight, scale, next_weight, dr, dh):
-    args, D, index, keep = checked
+@_on_its_device
+def _block_backward(x, y, post_weight, gate, gate_act, scale, next_weight, dr, dh, eps):
+    args, D, index, keep = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
     device = x.device
     for name, t in (("dr", dr), ("dh", dh)):
         if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.get_device() != index):
@@ -1117,8 +1172,7 @@ def block_join_backward(x, y, post_weight, gate=None, gate_act="sigmoid", scale=
         res = _quick_scratch("block_join_backward", x, x, y, post_weight, gate, act, scale, next_weight, eps, dr, dh)
         if res is not None:
             return BlockJoinGrads(*res)
-    args = _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps)
-    return _block_backward(args, x, y, gate, post_weight, scale, next_weight, dr, dh)
+    return _block_backward(x, y, post_weight, gate, gate_act, scale, next_weight, dr, dh, eps)
 
 
 def w4_matvec(x, qweight, scales, zeros=None, bias=None, out=None):
@@ -1133,6 +1187,11 @@ def w4_matvec(x, qweight, scales, zeros=None, bias=None, out=None):
         res = _quick("w4_matvec", x, qweight, scales, zeros, bias)
         if res is not None:
             return res
+    return _w4_matvec(x, qweight, scales, zeros, bias, out)
+
+
+@_on_its_device
+def _w4_matvec(x, qweight, scales, zeros, bias, out):
     index = _need_cuda(x, scales, bias)
     shape = x.shape
     K = shape[-1] if x.dim() else 0
