@@ -74,6 +74,10 @@ Extent extent(const hla2_view& w, int B, int H, int n, int D, int es) {
     return {lo, lo + (uintptr_t)last * es};
 }
 bool meet(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
+Extent state_extent(const hla2_linattn_args* a, const float* p) {  // empty for NULL
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, lo + (p ? (uintptr_t)a->B * a->Hk * a->d * a->dv * sizeof(float) : 0)};
+}
 
 // ---- plan ----------------------------------------------------------------------------------
 
@@ -208,6 +212,9 @@ int hla2_linattn_forward(const hla2_linattn_args* args, hla2_view out, float* fi
     const int es = elem_size(a.dtype);
     if (!al16(a.init_state) || !al16(final_state))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: states must be 16-byte aligned", fn);
+    // the segments' CTAs read the one while the last segment's writes the other
+    if (meet(state_extent(&a, final_state), state_extent(&a, a.init_state)))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: final_state overlaps init_state", fn);
     if (a.n > 0) {
         if (int rc = check_view(fn, "q", a.q, a.B, a.H, a.n, a.d, es)) return rc;
         if (int rc = check_view(fn, "k", a.k, a.B, a.Hk, a.n, a.d, es)) return rc;
@@ -248,6 +255,10 @@ int hla2_linattn_backward(const hla2_linattn_args* args, hla2_view dout, hla2_vi
     const int es = elem_size(a.dtype);
     if (!al16(a.init_state) || !al16(dfinal_state) || !al16(dinit_state))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: states must be 16-byte aligned", fn);
+    // several passes read the states, the first of them writes dinit_state
+    if (meet(state_extent(&a, dinit_state), state_extent(&a, dfinal_state)) ||
+        meet(state_extent(&a, dinit_state), state_extent(&a, a.init_state)))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dinit_state overlaps another state", fn);
     if (a.n > 0) {
         if (int rc = check_view(fn, "q", a.q, a.B, a.H, a.n, a.d, es)) return rc;
         if (int rc = check_view(fn, "k", a.k, a.B, a.Hk, a.n, a.d, es)) return rc;

@@ -466,12 +466,13 @@ typedef struct {
 size_t hla2_linattn_workspace_bytes(const hla2_linattn_args* a, int backward, int want_final);
 
 /* out [B, H, n, dv]; final_state (nullable) receives the contiguous [B, Hk, d, dv] state after
- * each sequence's last token.  out may not overlap an input. */
+ * each sequence's last token.  out may not overlap an input, nor final_state init_state. */
 int hla2_linattn_forward(const hla2_linattn_args* a, hla2_view out, float* final_state, hla2_stream_t stream);
 
 /* Gradients of sum(out * dout) + sum(final_state * dfinal_state): dq [B, H, n, d], dk [B, Hk,
  * n, d], dv [B, Hk, n, dv] (summed over the query heads that share a key head) and, where not
- * NULL, dinit_state [B, Hk, d, dv].  dfinal_state: nullable.  gamma has no gradient. */
+ * NULL, dinit_state [B, Hk, d, dv].  dfinal_state: nullable.  gamma has no gradient.  No gradient may
+ * overlap an input, dinit_state neither dfinal_state nor init_state. */
 int hla2_linattn_backward(const hla2_linattn_args* a, hla2_view dout, hla2_view dq, hla2_view dk, hla2_view dv,
                           const float* dfinal_state, float* dinit_state, hla2_stream_t stream);
 

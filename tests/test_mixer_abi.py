@@ -100,6 +100,25 @@ def test_linattn_backward_refuses_shared_outputs(L):
     assert call(dq, dk, View(0x90000000, 2 * 9 * 32, 9 * 32, 30)) == -1
 
 
+def test_linattn_refuses_states_in_place(L):
+    """The state is read by CTAs that run beside the one that writes it."""
+    size = 2 * 2 * 16 * 32 * 4  # bytes of [B, Hk, d, dv]
+    init = 0x50000000
+    a, out = lin(init_state=init)
+    for at in (init, init + size - 16, init - size + 16):
+        assert L.hla2_linattn_forward(ctypes.byref(a), out, at, None) == -1
+        assert b"overlaps" in L.hla2_last_error()
+    assert L.hla2_linattn_forward(ctypes.byref(a), out, init + size, None) == -3  # only the workspace is missing
+    g = [view(0x70000000, 2, 4, 9, 16), view(0x80000000, 2, 2, 9, 16), view(0x90000000, 2, 2, 9, 32)]
+    dout = view(0x40000000, 2, 4, 9, 32)
+    back = lambda dfinal, dinit: L.hla2_linattn_backward(ctypes.byref(a), dout, *g, dfinal, dinit, None)  # noqa: E731
+    for dinit in (init, init + size - 16, 0xA0000000, 0xA0000000 - size + 16):
+        assert back(0xA0000000, dinit) == -1
+        assert b"overlaps" in L.hla2_last_error()
+    assert back(0xA0000000, 0xA0000000 + size) == -3
+    assert back(None, init) == -1 and back(None, 0xA0000000) == -3
+
+
 def test_linattn_empty_calls_succeed(L):
     for kw in (dict(B=0), dict(H=0, Hk=0), dict(n=0, q=view(None, 2, 4, 0, 16), k=view(None, 2, 2, 0, 16),
                                                 v=view(None, 2, 2, 0, 32), out=view(None, 2, 4, 0, 32))):
