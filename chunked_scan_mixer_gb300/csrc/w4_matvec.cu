@@ -4,21 +4,20 @@
 // Bound by reading the weights: half a byte each.  The products run on mma.sync.m16n8k16 with 16
 // weight rows as A and up to eight columns of x as B, which turns the 4-bit values into operands at a
 // shift and a logic instruction a pair: (w << 3) & 0x00780078 | 0x41804180 is the bf16 pair
-// (16 + q_i, 16 + q_{i+4}), exactly.  One group of k is summed unscaled in float32, and
-//     sum (q - z) x = sum (16 + q) x - (16 + z) sum x,
-// with sum x from the same product with a row of ones: two instructions a group and column instead
-// of a subtraction a pair.  The cancellation costs a factor of about five of float32's rounding, far
-// below bf16's.  A float32 x takes the subtraction instead, exactly, and is split into three bf16
-// columns (8 + 8 + 8 bits) whose sums meet at the end.  The row's scale multiplies in float32.
+// (16 + q_i, 16 + q_{i+4}), exactly, and so is its difference from (16 + z, 16 + z).  (To sum 16 + q and take (16 + z)
+// sum x off would round at the size of 24 sum |x|, whatever is left of it: more than the output's own rounding
+// where most weights sit at their zero point.)  A group of k is summed unscaled in float32, and the row's scale
+// multiplies there.  A float32 x is split into three bf16 columns (8 + 8 + 8 bits) whose sums meet at the end.
 //
 // Within a group of G values of k, lane (g, c) = (lane / 4, lane % 4) owns k = c G / 4 ..
 // (c + 1) G / 4 - 1 of rows g and g + 8: one load of G / 8 bytes of each row, so a warp reads whole
 // 32-byte sectors from G = 64 on.  The order of k inside a product is free as long as A and B agree;
 // a word's pairs are (k, k + 4), and x is paired the same way.
 //
-// Measured: 1 x 8192 x 2048, groups of 128: 4.8 us (8.8 MB; floor 1.3).  12 x 10001 x 8192, groups of 64: 32 us (44 MB; floor
-// 6.5), where 90 instructions for each 512 weights bound it, and x, which every CTA reads: 123 MB through the L2.
-// Copies of x in shared memory, 32 outputs a CTA and three batches in flight were slower (38, 37 and 35 us).
+// Measured: 1 x 8192 x 2048, groups of 128: 5.2 to 5.8 us a call (8.8 MB; floor 1.3).  12 x 10001 x 8192, groups of 64, no
+// zero points: 27 us (44 MB; floor 6.5; 32 us with the sums of x from a product with ones), bound by its instructions and by
+// x, which every CTA reads: 123 MB through the L2.  Copies of x in shared memory, 32 outputs a CTA and three batches
+// in flight were slower (38, 37 and 35 us against 32).
 //
 // A CTA forms 16 outputs; its eight warps take every eighth batch of k, the next batch's weights in
 // flight while one is computed, and their sums meet in shared memory in a fixed order.
@@ -146,20 +145,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 3 : 2) w4_kernel(const 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (k0 + u * G >= a.K) break;
-            float acc[NT][4], xs[NT][4];
+            float acc[NT][4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                xs[t][0] = xs[t][1] = xs[t][2] = xs[t][3] = 0.f;
-                acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-            }
-            float zf[2];
-            uint32_t zz[2];
+            for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+            uint32_t zz[2];  // the pair (16 + z, 16 + z)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t z = a.zeros ? b.z[h].v[u] : 8u;
-                    zf[h] = (float)(16u + z);
-                    zz[h] = 0x41804180u | (z * 0x00080008u);
-                }
+            for (int h = 0; h < 2; ++h) zz[h] = 0x41804180u | ((a.zeros ? b.z[h].v[u] : 8u) * 0x00080008u);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 uint32_t x[NT][4];
@@ -191,9 +182,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 3 : 2) w4_kernel(const 
                         q[h][1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
                         q[h][2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
                         q[h][3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
-                        if (kPieces == 3)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) q[h][i] = sub2(q[h][i], zz[h]);
+                        for (int i = 0; i < 4; ++i) q[h][i] = sub2(q[h][i], zz[h]);
                     }
                     const uint32_t A0[4] = {q[0][0], q[1][0], q[0][1], q[1][1]}, A1[4] = {q[0][2], q[1][2], q[0][3], q[1][3]};
 #pragma unroll
@@ -202,25 +192,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 3 : 2) w4_kernel(const 
                         mma_16816(acc[t], A1, x[t][2], x[t][3]);
                     }
                 }
-                if (kPieces == 1) {
-                    const uint32_t one[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        mma_16816(xs[t], one, x[t][0], x[t][1]);
-                        mma_16816(xs[t], one, x[t][2], x[t][3]);
-                    }
-                }
             }
             {
                 const float f0 = to_f32(b.s[0].v[u]), f1 = to_f32(b.s[1].v[u]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    if (kPieces == 1) {
-                        acc[t][0] = fmaf(-zf[0], xs[t][0], acc[t][0]);
-                        acc[t][1] = fmaf(-zf[0], xs[t][1], acc[t][1]);
-                        acc[t][2] = fmaf(-zf[1], xs[t][0], acc[t][2]);
-                        acc[t][3] = fmaf(-zf[1], xs[t][1], acc[t][3]);
-                    }
                     sum[t][0] = fmaf(f0, acc[t][0], sum[t][0]);
                     sum[t][1] = fmaf(f0, acc[t][1], sum[t][1]);
                     sum[t][2] = fmaf(f1, acc[t][2], sum[t][2]);

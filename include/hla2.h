@@ -531,8 +531,7 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
  * zeros [N, K / group] bytes in 0..15, or NULL for 8.  x [M, K] (rows every x_stride elements),
  * scales [N, K / group], bias [N] (nullable) and y [M, N] have the type dtype.  1 <= M <= 16;
  * group 32, 64 or 128, K a multiple of it; N >= 0.  x, its rows and qweight are 16-byte aligned.
- * The products are exact and the sums float32.  A bf16 x is multiplied by 16 + q and its group's sum by
- * 16 + z: an infinite value, or a group whose sum of 32 |x| passes float32, gives NaN.
+ * The products (q - z) x are exact and the sums float32.
  */
 int hla2_w4_matvec(const void* x, long long x_stride, const void* qweight, const void* scales, const void* zeros,
                    const void* bias, void* y, int M, int N, int K, int group, int dtype, hla2_stream_t stream);

@@ -79,6 +79,55 @@ def test_large_values_and_float32_digits():
     assert y[0, 0] == 2.0 ** -23 and y[1, 0] == x[1, 3]
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 8, 12])
+def test_weights_at_their_zero_point(dtype, group, M):
+    """Nearly every weight is zero and x has a mean: the sums count against |q - z| |x| s, not against |q| or |x|."""
+    K, N = 8192, 64
+    g = torch.Generator().manual_seed(M + group)
+    x = (1 + 0.5 * torch.randn((M, K), generator=g)).to(dtype)
+    z = torch.randint(0, 16, (N, K // group), generator=g, dtype=torch.uint8)
+    q = z.repeat_interleave(group, 1)
+    at = torch.randint(0, K, (N, 3), generator=g)
+    q.scatter_(1, at, torch.randint(0, 16, (N, 3), generator=g, dtype=torch.uint8))
+    w = (q[:, 0::2] | (q[:, 1::2] << 4)).contiguous()
+    s = (0.01 + torch.rand((N, K // group), generator=g)).to(dtype)
+    n = [np64(x), w.numpy().astype(np.int64), np64(s), z.numpy()]
+    want = O.w4_matvec(*n)
+    terms = np.abs(n[0]) @ (np.abs(q.numpy().astype(np.float64) - z.repeat_interleave(group, 1).numpy())
+                            * np.repeat(n[2], group, axis=1)).T
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    lim = half * np.abs(want) + 2.0 ** -24 * (16 + 2 * math.sqrt(K)) * terms
+    y = np64(hla.w4_matvec(x.cuda(), w.cuda(), s.cuda(), zeros=z.cuda()).cpu())
+    assert (np.abs(y - want) <= lim).all(), float((np.abs(y - want) / np.maximum(lim, 1e-300)).max())
+    # without any zero point given, and all weights at 8: exactly nothing
+    eights = torch.full((N, K // 2), 0x88, dtype=torch.uint8)
+    assert not hla.w4_matvec(x.cuda(), eights.cuda(), s.cuda()).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M", [1, 9])
+def test_infinite_and_large_values(dtype, M):
+    """An infinity goes to its outputs with the sign of its weight (NaN where that is zero), and to no other row;
+    values whose products by 16 and more would pass float32 stay finite where the output is."""
+    K, N, group = 256, 6, 64
+    q = torch.full((N, K), 8, dtype=torch.uint8)
+    q[0, 70], q[1, 70], q[2, 70] = 11, 3, 8
+    q[3, 130], q[4, 131] = 9, 7
+    w = q[:, 0::2] | (q[:, 1::2] << 4)
+    s = torch.ones((N, K // group), dtype=dtype)
+    x = torch.zeros((M, K), dtype=dtype)
+    x[0, 70] = float("inf")
+    y = hla.w4_matvec(x.cuda(), w.cuda(), s.cuda()).cpu().float()
+    assert y[0, 0] == float("inf") and y[0, 1] == float("-inf") and y[0, 2:].isnan().all()
+    assert not y[1:].any()
+    x[0, 70] = 0
+    x[0, 130] = x[0, 131] = torch.tensor(3.0e38, dtype=dtype)
+    y = hla.w4_matvec(x.cuda(), w.cuda(), s.cuda()).cpu()
+    assert y[0, 3] == x[0, 130] and y[0, 4] == -x[0, 131] and not y[0, [0, 1, 2, 5]].any()
+
+
 def test_views_and_leading_dimensions():
     x, w, s, z, b = (t.cuda() for t in draw(6, 40, 256, 64, BF))
     want = hla.w4_matvec(x, w, s, zeros=z, bias=b)
