@@ -57,15 +57,26 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def host_stale(target: str, deps: list[str], torch_version: str) -> bool:
+    """Whether the host module is older than its sources, or was built against another torch (named in a file beside it)."""
+    if _stale(target, deps):
+        return True
+    try:
+        with open(target + ".torch") as f:
+            return f.read() != torch_version
+    except OSError:
+        return True
+
+
 def build_host(force: bool = False) -> bool:
     """Compiles csrc/host_calls.cpp against the torch that is installed; False where that fails."""
-    src = os.path.join(CSRC, "host_calls.cpp")
-    if not force and not _stale(HOST, [src] + _headers()):
-        return True
     import sysconfig
 
     import torch
 
+    src = os.path.join(CSRC, "host_calls.cpp")
+    if not force and not host_stale(HOST, [src] + _headers(), torch.__version__):
+        return True
     at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     include = [os.path.join(at, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
@@ -84,6 +95,8 @@ def build_host(force: bool = False) -> bool:
             os.remove(HOST)
         return False
     os.replace(tmp, HOST)
+    with open(HOST + ".torch", "w") as f:
+        f.write(torch.__version__)
     return True
 
 

@@ -20,6 +20,7 @@ import importlib.util
 import os
 import struct
 import threading
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -176,17 +177,21 @@ _host = None  # module of csrc/host_calls.cpp
 
 
 def _load_host(L):
-    """The compiled host side of the short calls, bound to the library's entry points; without it
-    they take the way through this file."""
+    """The compiled host side of the short calls, bound to the library's entry points; without it (or where it does
+    not load, say beside another torch than it was built with) they take the way through this file."""
     global _host
     if not os.path.exists(HOST_PATH):
         return
-    loader = importlib.machinery.ExtensionFileLoader("_hla2_host", HOST_PATH)
-    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_hla2_host", loader))
-    loader.exec_module(mod)
-    mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        L.hla2_linattn_forward, L.hla2_linattn_backward, L.hla2_linattn_decode_step, L.hla2_block_join,
-        L.hla2_block_join_backward, L.hla2_w4_matvec)))
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_hla2_host", HOST_PATH)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_hla2_host", loader))
+        loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.hla2_linattn_forward, L.hla2_linattn_backward, L.hla2_linattn_decode_step, L.hla2_block_join,
+            L.hla2_block_join_backward, L.hla2_w4_matvec)))
+    except Exception as e:
+        warnings.warn(f"{HOST_PATH} does not load, short calls take longer on the host: {e}", RuntimeWarning)
+        return
     _host = mod
 
 

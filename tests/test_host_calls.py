@@ -33,6 +33,32 @@ def test_bind_checks_its_arguments(host):
         host.bind(1, 2)
 
 
+def test_a_module_that_does_not_load_is_gone_without(monkeypatch, tmp_path):
+    bad = tmp_path / "_hla2_host.so"
+    bad.write_bytes(b"not a shared object")
+    for name, value in (("_lib", None), ("_host", None), ("HOST_PATH", str(bad))):
+        monkeypatch.setattr(hla2, name, value)
+    with pytest.warns(RuntimeWarning, match="does not load"):
+        L = hla2.lib()
+    assert L is hla2.lib() and hla2._host is None and L.hla2_version() > 0
+    with pytest.raises(TypeError):  # the way through the binding
+        hla.block_norm(torch.zeros(2, 8), torch.zeros(8))
+
+
+def test_the_module_is_built_again_for_another_torch(tmp_path):
+    from chunked_scan_mixer_gb300 import build
+
+    src, so = tmp_path / "a.cpp", tmp_path / "a.so"
+    src.write_text("")
+    so.write_text("")
+    assert build.host_stale(str(so), [str(src)], "2.9.1")  # nobody knows what it was built against
+    (tmp_path / "a.so.torch").write_text("2.9.1")
+    assert not build.host_stale(str(so), [str(src)], "2.9.1")
+    assert build.host_stale(str(so), [str(src)], "2.11.0")
+    with open(build.HOST + ".torch") as f:
+        assert f.read() == torch.__version__
+
+
 def both(monkeypatch, call):
     """The call by the module, which has to take it, and without it."""
     class Seen:
