@@ -242,6 +242,8 @@ def _on_its_device(f):
 
 
 _ws_cache: dict = {}
+# The same for the calls around a layer, whose status word nobody clears (_with_scratch)
+_scratch_cache: dict = {}
 
 # Held while a call launches the kernels that pass their sums through a cached buffer: ctypes lets other threads run
 # during the call, and one of them on the same stream would launch its own kernels on the buffer in between.
@@ -267,16 +269,18 @@ def _workspace(nbytes, device, stream_handle):
 
 
 def check_status(device=None):
-    """Raise HLA2Error if a kernel that used this stream's cached workspace reported a
-    timed-out wait.  Synchronises the current stream."""
+    """Raise HLA2Error if a kernel that used this stream's cached workspaces reported a
+    timed-out wait.  Synchronises the current stream.  (The replays of a captured graph use a workspace of
+    the graph's own.)"""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     device = torch.device(device)
     sh = _stream_handle(device)
     index = torch.cuda.current_device() if device.index is None else device.index
-    buf = _ws_cache.get((index, sh.value))
-    if buf is not None:
-        with torch.cuda.device(index):
-            _check("hla2_workspace_status", lib().hla2_workspace_status(ctypes.c_void_p(buf.data_ptr()), sh))
+    for cache in (_ws_cache, _scratch_cache):
+        buf = cache.get((index, sh.value))
+        if buf is not None:
+            with torch.cuda.device(index):
+                _check("hla2_workspace_status", lib().hla2_workspace_status(ctypes.c_void_p(buf.data_ptr()), sh))
 
 
 def state_floats(d, dv, compact=False):
@@ -752,6 +756,7 @@ def _need_cuda(first, *others):
 
 _capturing = torch._C._cuda_isCurrentStreamCapturing
 _ERR_WORKSPACE = -3
+_STATUS_BYTES = 256  # at a workspace's start, for the calls with bounded waits
 
 
 def _with_scratch(call, query, index, stream):
@@ -759,29 +764,37 @@ def _with_scratch(call, query, index, stream):
     cached buffer is tried first: the library checks its size before it launches anything.  Under
     graph capture the buffer is the graph's own: the cached one is shared with eager calls on the
     stream, which a replay would race with.  The first bytes are the status word (see
-    hla2_workspace_status), 0 in a new buffer.  Every rejection without memory is the call's."""
-    key = (index, stream or None)  # as _workspace and check_status have it
+    hla2_workspace_status): 0 in a first buffer, taken along to a larger one, so that a wait that gave up stays
+    recorded.  Every rejection without memory is the call's."""
+    key = (index, stream or None)  # as check_status has it
     capturing = _capturing()
-    if not capturing:
-        known = _ws_cache.get(key)
-        if known is not None:
-            rc = _alone(call, known.data_ptr(), known.numel())
-            if rc != _ERR_WORKSPACE:
-                return rc
+    known = None if capturing else _scratch_cache.get(key)
+    if known is not None:
+        rc = _alone(call, known.data_ptr(), known.numel())
+        if rc != _ERR_WORKSPACE:
+            return rc
     nbytes = query()
     if nbytes == _SIZE_MAX or nbytes == 0:
         return call(0, 0)
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-    buf[:256].zero_()
-    if not capturing:
-        _ws_cache[key] = buf
-    return _alone(call, buf.data_ptr(), nbytes)
+    with _scratch_lock:
+        known = None if capturing else _scratch_cache.get(key)  # another thread's call may have grown it
+        if known is None or known.numel() < nbytes:
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+            if known is None:
+                buf[:_STATUS_BYTES].zero_()
+            else:
+                buf[:_STATUS_BYTES].copy_(known[:_STATUS_BYTES])
+            if not capturing:
+                _scratch_cache[key] = buf
+        else:
+            buf = known
+        return call(buf.data_ptr(), buf.numel())
 
 
 def _cached_scratch(t):
     """The buffer that _with_scratch would try first for a call on t's device, or None."""
     index = t.get_device()
-    return None if index < 0 or _capturing() else _ws_cache.get((index, _raw_stream(index) or None))
+    return None if index < 0 or _capturing() else _scratch_cache.get((index, _raw_stream(index) or None))
 
 
 def _quick(name, *args):
@@ -1153,7 +1166,7 @@ def _block_backward(x, y, post_weight, gate, gate_act, scale, next_weight, dr, d
     stream = _raw_stream(index)
     L = lib()
     outs = (_addr(dr), _addr(dh), _addr(dx), _addr(dy), _addr(dgate), _addr(dpw), _addr(dsc), _addr(dnw))
-    skip = 256  # the status word belongs to the calls with bounded waits
+    skip = _STATUS_BYTES
 
     def query():
         nbytes = L.hla2_block_join_backward_workspace_bytes(args)

@@ -55,7 +55,7 @@ def test_calls_on_cached_scratch_do_not_overlap(monkeypatch):
 
     monkeypatch.setattr(hla2, "_host", Host)
     monkeypatch.setattr(hla2, "_capturing", lambda: False)
-    monkeypatch.setitem(hla2._ws_cache, (0, None), buf)
+    monkeypatch.setitem(hla2._scratch_cache, (0, None), buf)
     t = torch.zeros(1)
     together(lambda: hla2._with_scratch(busy, lambda: 512, 0, 0), lambda: hla.linattn_forward(t, t, t),
              lambda: hla2._alone(busy), lambda: hla2._with_scratch(busy, lambda: 512, 0, 0))
