@@ -898,7 +898,7 @@ def _linattn_args(q, k, v, gamma, scale, lengths, init_state):
         lengths = torch.as_tensor(lengths, device=device)
         if lengths.dtype not in (torch.int32, torch.int64):
             raise ValueError("lengths must be integers")
-        lengths = lengths.to(torch.int32).contiguous()
+        lengths = (lengths.clamp(0, n) if lengths.dtype == torch.int64 else lengths).to(torch.int32).contiguous()
     if lengths is not None and lengths.shape != (B,):
         raise ValueError("lengths must be B integers")
     init = _state_arg("init_state", init_state, (B, Hk, d, dv), device)

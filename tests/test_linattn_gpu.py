@@ -166,6 +166,16 @@ def test_lengths_outside_the_sequence_are_clamped():
     assert all(torch.equal(s, t) for s, t in zip(a, b))
 
 
+def test_lengths_past_32_bits_are_clamped_too():
+    x = cuda(draw(2, 2, 2, 200, 64, 64, BF, seed=12))
+    kw = dict(gamma=x["gamma"], return_final_state=True)
+    want = hla.linattn_forward(x["q"], x["k"], x["v"], lengths=torch.tensor([200, 0], device="cuda"), **kw)
+    far = [2 ** 32 + 5, -2 ** 32 + 7]
+    for lengths in (far, torch.tensor(far), torch.tensor(far, device="cuda")):
+        got = hla.linattn_forward(x["q"], x["k"], x["v"], lengths=lengths, **kw)
+        assert all(torch.equal(s, t) for s, t in zip(got, want))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_views_are_read_in_place_and_others_copied(dtype):
     g = torch.Generator().manual_seed(21)
