@@ -915,7 +915,7 @@ def _state_arg(name, state, shape, device):
         return None
     if tuple(state.shape) != shape or state.dtype != torch.float32 or state.device != device:
         raise ValueError(f"{name} must be a float32 {shape} tensor on the inputs' device")
-    return state.contiguous()
+    return _packed16(state)
 
 
 def linattn_forward(q, k, v, gamma=None, scale=1.0, lengths=None, init_state=None, return_final_state=False, out=None):

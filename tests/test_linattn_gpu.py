@@ -195,6 +195,23 @@ def test_views_are_read_in_place_and_others_copied(dtype):
                        hla.linattn_forward(q, one.contiguous(), v, gamma=0.97))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_states_at_odd_addresses_are_copied(dtype):
+    x = cuda(draw(2, 4, 2, 200, 32, 64, dtype, seed=22, state=True))
+    odd = {k: torch.zeros(x[k].numel() + 1, device="cuda")[1:].view(x[k].shape).copy_(x[k]) for k in ("init", "dfinal")}
+
+    def calls(init, dfinal):
+        return (*hla.linattn_forward(x["q"], x["k"], x["v"], gamma=x["gamma"], init_state=init, return_final_state=True),
+                *hla.linattn_backward(x["q"], x["k"], x["v"], x["dout"], gamma=x["gamma"], init_state=init,
+                                      dfinal_state=dfinal))
+
+    for a, b in zip(calls(x["init"], x["dfinal"]), calls(odd["init"], odd["dfinal"])):
+        assert torch.equal(a, b)
+    swapped = {k: x[k].transpose(0, 1).contiguous().transpose(0, 1) for k in odd}
+    for a, b in zip(calls(x["init"], x["dfinal"]), calls(swapped["init"], swapped["dfinal"])):
+        assert torch.equal(a, b)
+
+
 def test_same_bits_on_every_call_and_on_a_side_stream():
     x = cuda(draw(2, 8, 2, 1500, 64, 64, BF, seed=30, state=True))
 
