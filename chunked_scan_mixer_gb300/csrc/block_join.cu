@@ -204,7 +204,11 @@ int hla2_block_join(const hla2_block_args* a, void* r, void* h, hla2_stream_t st
     if (a->rows == 0) return join_ok();
     const size_t es = a->dtype == HLA2_BF16 ? 2 : 4;
     if (!al(r, es) || !al(h, es)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: misaligned output", fn);
-    if (r && r == h) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: r and h must be distinct", fn);
+    const RowsOf ro{r, a->D, a->D}, ho{h, a->D, a->D};
+    if (r && h && meet(rows_extent(a, ro), rows_extent(a, ho)))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: r and h must be distinct", fn);
+    if ((r && spoils(a, ro, nullptr, 0)) || (h && spoils(a, ho, nullptr, 0)))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: an output overlaps an input other than in its place", fn);
     const void* outs[2] = {r, h};
     const int vec = vec_of(a, outs, 2);
     const Shape s = shape_of(a->D, vec);

@@ -351,6 +351,32 @@ int check_join(const char* fn, const hla2_block_args* a) {
     return HLA2_OK;
 }
 
+// Rows of cols elements, `stride` apart
+struct RowsOf {
+    const void* p;
+    long long stride;
+    int cols;
+};
+Extent rows_extent(const hla2_block_args* a, const RowsOf& t) {
+    return extent_of(t.p, (size_t)((a->rows - 1) * t.stride + t.cols) * (a->dtype == HLA2_BF16 ? 2 : 4));
+}
+// Whether contiguous rows that are written overlap what the call reads in another way than as exactly the same rows: a
+// row is read whole before it is written, but its neighbours may be read earlier or later.
+bool spoils(const hla2_block_args* a, const RowsOf& out, const RowsOf* more, int nmore) {
+    const Extent eo = rows_extent(a, out);
+    auto hits = [&](const RowsOf& t) {
+        return t.p && meet(eo, rows_extent(a, t)) &&
+               !(t.p == out.p && t.cols == out.cols && (t.stride == out.cols || a->rows == 1));
+    };
+    const RowsOf in[6] = {{a->x, a->x_stride, a->D}, {a->y, a->y_stride, a->D}, {a->gate, a->gate_stride, a->gate_cols},
+                          {a->post_weight, 0, a->D}, {a->scale, 0, a->D}, {a->next_weight, 0, a->D}};
+    for (int i = 0; i < 6; ++i)
+        if (i < 3 ? hits(in[i]) : in[i].p && meet(eo, rows_extent(a, in[i]))) return true;
+    for (int i = 0; i < nmore; ++i)
+        if (hits(more[i])) return true;
+    return false;
+}
+
 // Persistent CTAs and their ring.  Stages: as many rows ahead as fit in the SM's shared memory beside
 // the CTAs that the registers allow (1024 threads of the forward, 512 of the backward, 768 where there
 // is no block output), at most four, and no more than a CTA has rounds; one stage copies and waits.

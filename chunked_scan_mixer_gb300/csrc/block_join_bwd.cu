@@ -398,6 +398,25 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
             !al(dscale, 4) || !al(dnext_weight, 4))
             return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
     }
+    {
+        const RowsOf grads[2] = {{dr, a->D, a->D}, {dh, a->D, a->D}};
+        const RowsOf out[3] = {{dx, a->D, a->D}, {dy, a->D, a->D}, {dgate, a->gate_cols, a->gate_cols}};
+        const size_t vb = (size_t)a->D * sizeof(float);
+        const Extent sums[3] = {extent_of(dpost_weight, vb), extent_of(dscale, vb), extent_of(dnext_weight, vb)};
+        bool bad = false;
+        for (int i = 0; i < 3; ++i) {
+            for (int j = 0; j < i; ++j) bad |= meet(sums[i], sums[j]);
+            for (const void* w : {a->post_weight, a->scale, a->next_weight}) bad |= meet(sums[i], extent_of(w, a->D * es));
+            if (a->rows == 0) continue;
+            for (const RowsOf& t : {RowsOf{a->x, a->x_stride, a->D}, RowsOf{a->y, a->y_stride, a->D},
+                                    RowsOf{a->gate, a->gate_stride, a->gate_cols}, grads[0], grads[1], out[0], out[1], out[2]})
+                bad |= t.p && meet(sums[i], rows_extent(a, t));
+            if (!out[i].p) continue;
+            bad |= spoils(a, out[i], grads, 2);
+            for (int j = 0; j < i; ++j) bad |= out[j].p && meet(rows_extent(a, out[i]), rows_extent(a, out[j]));
+        }
+        if (bad) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps another tensor other than in its place", fn);
+    }
     const size_t need = hla2_block_join_backward_workspace_bytes(a);
     if (need > 0 && (!workspace || workspace_bytes < need || !al(workspace, 16)))
         return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, need);

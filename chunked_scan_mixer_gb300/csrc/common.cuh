@@ -168,6 +168,16 @@ __device__ __forceinline__ float head_decay(const float* gamma, int bh, int H) {
     return gamma ? __ldg(gamma + (bh % H)) : 1.0f;
 }
 
+// Bytes [lo, hi) of a tensor; none for NULL
+struct Extent {
+    uintptr_t lo, hi;
+};
+inline Extent extent_of(const void* p, size_t bytes) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, lo + (p ? bytes : 0)};
+}
+inline bool meet(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
+
 // SMs of the current device, asked for once per thread and device (152 where the query fails).
 inline int sm_count() {
     thread_local int known = -1, sms = 0;

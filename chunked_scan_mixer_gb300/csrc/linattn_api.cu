@@ -65,18 +65,11 @@ int check_view(const char* fn, const char* name, hla2_view& w, int B, int H, int
     return HLA2_OK;
 }
 
-struct Extent {
-    uintptr_t lo, hi;
-};
 Extent extent(const hla2_view& w, int B, int H, int n, int D, int es) {
-    const long long last = (B - 1) * w.sb + (H - 1) * w.sh + (n - 1) * w.sn + D;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(w.p);
-    return {lo, lo + (uintptr_t)last * es};
+    return extent_of(w.p, (size_t)((B - 1) * w.sb + (H - 1) * w.sh + (n - 1) * w.sn + D) * es);
 }
-bool meet(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
-Extent state_extent(const hla2_linattn_args* a, const float* p) {  // empty for NULL
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, lo + (p ? (uintptr_t)a->B * a->Hk * a->d * a->dv * sizeof(float) : 0)};
+Extent state_extent(const hla2_linattn_args* a, const float* p) {
+    return extent_of(p, (size_t)a->B * a->Hk * a->d * a->dv * sizeof(float));
 }
 
 // ---- plan ----------------------------------------------------------------------------------
@@ -333,8 +326,13 @@ int hla2_linattn_decode_step(float* state, const void* q, const void* k, const v
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: pointers must not be NULL", fn);
     if (!al16(state) || !al16(q) || !al16(k) || !al16(v) || !al16(out))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
-    if (out == q || out == k || out == v)
-        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps an input", fn);
+    const size_t es = elem_size(dtype), nh = (size_t)N * H, nk = (size_t)N * Hk;
+    const Extent in[3] = {extent_of(q, nh * d * es), extent_of(k, nk * d * es), extent_of(v, nk * dv * es)};
+    const Extent eo = extent_of(out, nh * dv * es), est = extent_of(state, nk * d * dv * sizeof(float));
+    if (meet(eo, est)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps the state", fn);
+    for (const Extent& i : in)
+        if (meet(i, eo) || meet(i, est))
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out or the state overlaps an input", fn);
     if (launch_lin_step(state, q, k, v, out, N, H, Hk, d, dv, gamma, scale, dtype == HLA2_BF16,
                         reinterpret_cast<cudaStream_t>(stream)))
         return launch_failed("linear attention step");

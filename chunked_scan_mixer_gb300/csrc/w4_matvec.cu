@@ -284,6 +284,11 @@ extern "C" int hla2_w4_matvec(const void* x, long long x_stride, const void* qwe
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: x, its rows and qweight must be 16-byte aligned", fn);
     if (!al(scales, es) || !al(bias, es) || !al(y, es))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
+    const Extent ey = extent_of(y, (size_t)M * N * es);
+    for (const Extent& i : {extent_of(x, (size_t)((M - 1) * x_stride + K) * es), extent_of(qweight, (size_t)N * (K / 2)),
+                            extent_of(scales, (size_t)N * (K / group) * es), extent_of(zeros, (size_t)N * (K / group)),
+                            extent_of(bias, N * es)})
+        if (meet(ey, i)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: y overlaps an input", fn);
     const W4Args a{x, x_stride, static_cast<const uint8_t*>(qweight), scales, static_cast<const uint8_t*>(zeros),
                    bias, y, M, N, K, group};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -1087,7 +1087,7 @@ def _block_args(x, y, post_weight, gate, gate_act, scale, next_weight, eps):
 
 def block_norm(x, weight, eps=1e-6, out=None):
     """The norm before a block: x / sqrt(mean(x^2) + eps) * weight over the last dimension (1 to
-    8192 values; float32 or bfloat16 on the GPU)."""
+    8192 values; float32 or bfloat16 on the GPU).  out may be x itself."""
     if out is None and weight is not None:
         res = _quick("block_join", x, None, None, None, 0, None, weight, eps)
         if res is not None:

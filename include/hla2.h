@@ -477,7 +477,8 @@ int hla2_linattn_backward(const hla2_linattn_args* a, hla2_view dout, hla2_view 
                           const float* dfinal_state, float* dinit_state, hla2_stream_t stream);
 
 /* One token for each of N sequences: state [N, Hk, d, dv] float32 is updated in place, then out
- * [N, H, dv] = scale * P^T q.  q [N, H, d], k [N, Hk, d], v [N, Hk, dv], all contiguous. */
+ * [N, H, dv] = scale * P^T q.  q [N, H, d], k [N, Hk, d], v [N, Hk, dv], all contiguous.  Neither out
+ * nor the state may overlap another of them. */
 int hla2_linattn_decode_step(float* state, const void* q, const void* k, const void* v, void* out, int N, int H,
                              int Hk, int d, int dv, const float* gamma, float scale, int dtype,
                              hla2_stream_t stream);
@@ -510,7 +511,8 @@ typedef struct {
     const void* next_weight;  /* [D], nullable      */
 } hla2_block_args;
 
-/* r [rows, D] (NULL with y NULL), h [rows, D] (NULL without next_weight), contiguous. */
+/* r [rows, D] (NULL with y NULL), h [rows, D] (NULL without next_weight), contiguous.  Each may be
+ * exactly the rows of x, y or a gate of D columns (in place), and overlap nothing else. */
 int hla2_block_join(const hla2_block_args* a, void* r, void* h, hla2_stream_t stream);
 
 /* Scratch bytes of hla2_block_join_backward; (size_t)-1 for arguments it would reject. */
@@ -519,7 +521,8 @@ size_t hla2_block_join_backward_workspace_bytes(const hla2_block_args* a);
 /* Gradients of sum(r * dr) + sum(h * dh); dr (nullable) and dh (needed with next_weight, else
  * NULL) are contiguous [rows, D].  dx, dy [rows, D], dgate [rows, gate_cols] have the type dtype;
  * dpost_weight, dscale, dnext_weight are float32 [D] sums over the rows in a fixed order.  Each
- * output is needed where its input is there, and NULL elsewhere. */
+ * output is needed where its input is there, and NULL elsewhere.  dx, dy and dgate may be exactly the
+ * rows of an input or of dr or dh; else no output overlaps an input or another output. */
 int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const void* dh, void* dx, void* dy,
                              void* dgate, float* dpost_weight, float* dscale, float* dnext_weight, void* workspace,
                              size_t workspace_bytes, hla2_stream_t stream);
@@ -531,7 +534,7 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
  * zeros [N, K / group] bytes in 0..15, or NULL for 8.  x [M, K] (rows every x_stride elements),
  * scales [N, K / group], bias [N] (nullable) and y [M, N] have the type dtype.  1 <= M <= 16;
  * group 32, 64 or 128, K a multiple of it; N >= 0.  x, its rows and qweight are 16-byte aligned.
- * The products (q - z) x are exact and the sums float32.
+ * The products (q - z) x are exact and the sums float32.  y may not overlap an input.
  */
 int hla2_w4_matvec(const void* x, long long x_stride, const void* qweight, const void* scales, const void* zeros,
                    const void* bias, void* y, int M, int N, int K, int group, int dtype, hla2_stream_t stream);

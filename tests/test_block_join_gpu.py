@@ -187,6 +187,20 @@ def test_same_bits_every_time():
     assert all(torch.equal(s, t) for s, t in zip(a, b))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows, D", [(3000, 256), (2003, 439), (45001, 7), (600, 4096)])
+def test_norm_in_place(dtype, rows, D):
+    x = torch.randn((rows, D), device="cuda").to(dtype)
+    w = torch.randn(D, device="cuda").to(dtype)
+    want = hla.block_norm(x, w)
+    assert hla.block_norm(x, w, out=x) is x and torch.equal(x, want)
+    both = torch.randn((rows + 1, D), device="cuda").to(dtype)
+    with pytest.raises(hla.HLA2Error):
+        hla.block_norm(both[1:], w, out=both[:-1])
+    with pytest.raises(hla.HLA2Error):
+        hla.block_norm(x, x[1], out=x)
+
+
 def test_refusals():
     x = torch.zeros((2, 64), device="cuda")
     w = torch.zeros(64, device="cuda")

@@ -188,6 +188,55 @@ def test_block_join_refuses_outputs_that_do_not_match(L):
     assert L.hla2_block_join_backward(ctypes.byref(a), 0x11000, 0x12000, *grads, 0x19000, 16, None) == -3
 
 
+def join_backward(L, a, **kw):
+    c = dict(dr=0x11000, dh=0x12000, dx=0x13000, dy=0x14000, dgate=0x15000, dpw=0x16000, dsc=0x17000, dnw=0x18000, ws=None,
+             size=0, stream=None)
+    c.update(kw)
+    return L.hla2_block_join_backward(ctypes.byref(a), *c.values())
+
+
+def test_block_join_refuses_overlaps_but_rows_in_place(L):
+    """Without a device a call that passes the checks fails later: in the backward for want of a workspace (-3), in the
+    forward at its launch (-4)."""
+    a = block()
+    size = 3 * 64 * 2
+    call = lambda r, h, b=a: L.hla2_block_join(ctypes.byref(b), r, h, None)  # noqa: E731
+    for r, h in ((0x70000, 0x70000 + size - 16), (0x10000 + 128, 0x80000), (0x70000, 0x20000 - 128), (0x30000 + 2, 0x80000),
+                 (0x40000, 0x80000), (0x70000, 0x50000 + 64), (0x60000 - size + 16, 0x80000)):
+        assert call(r, h) == -1, (hex(r), hex(h))
+    wide = block(x_stride=128)  # rows of x between those that are written
+    assert call(0x10000, 0x80000, wide) == -1
+    row_gate = block(gate_cols=1, gate_stride=1)
+    assert call(0x30000, 0x80000, row_gate) == -1
+    if not torch.cuda.is_available():
+        assert call(0x10000, 0x20000) == -4 and call(0x30000, 0x10000) == -4 and call(0x70000, 0x70000 + size) == -4
+    assert join_backward(L, a) == -3
+    for kw in (dict(dx=0x10000), dict(dx=0x11000, dy=0x12000), dict(dx=0x20000, dy=0x10000), dict(dgate=0x30000),
+               dict(dx=0x12000, dy=0x11000, dgate=0x10000)):
+        assert join_backward(L, a, **kw) == -3, kw
+    assert join_backward(L, row_gate, dgate=0x30000) == -3
+    for kw in (dict(dx=0x10000 + 128), dict(dx=0x11000 - 128), dict(dx=0x14000 + 16), dict(dy=0x15000), dict(dgate=0x13000 + 16),
+               dict(dpw=0x17000 + 128), dict(dnw=0x16000), dict(dsc=0x13000 + size - 4), dict(dpw=0x40000), dict(dnw=0x12000),
+               dict(dx=0x60000)):
+        assert join_backward(L, a, **kw) == -1, kw
+
+
+def test_w4_and_step_refuse_overlaps(L):
+    ok = dict(x=0x10000, x_stride=256, w=0x20000, s=0x30000, z=0x34000, b=0x38000, y=0x40000, M=2, N=5, K=256, group=64,
+              dtype=1, stream=None)
+    call = lambda **kw: L.hla2_w4_matvec(*{**ok, **kw}.values())  # noqa: E731
+    for y in (0x10000, 0x10000 + 2 * 512 - 2, 0x10000 - 18, 0x20000, 0x20000 + 5 * 128 - 2, 0x30000, 0x34000, 0x38000 + 8):
+        assert call(y=y) == -1, hex(y)
+        assert b"overlaps" in L.hla2_last_error()
+    step = dict(state=0x10000, q=0x20000, k=0x30000, v=0x40000, out=0x50000, N=2, H=4, Hk=2, d=16, dv=32, gamma=None,
+                scale=1.0, dtype=1, stream=None)
+    call = lambda **kw: L.hla2_linattn_decode_step(*{**step, **kw}.values())  # noqa: E731
+    for kw in (dict(out=0x20000 + 240), dict(out=0x30000 - 16), dict(out=0x40000 + 16), dict(out=0x10000 + 8176),
+               dict(state=0x20000 + 240), dict(state=0x40000 - 16)):
+        assert call(**kw) == -1, kw
+        assert b"overlaps" in L.hla2_last_error()
+
+
 def test_w4_refuses(L):
     ok = dict(x=0x10000, x_stride=256, w=0x20000, s=0x30000, z=None, b=None, y=0x40000, M=2, N=5, K=256, group=64,
               dtype=1, stream=None)

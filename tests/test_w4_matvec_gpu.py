@@ -169,3 +169,10 @@ def test_refusals():
         hla.w4_matvec(torch.zeros((17, 128), dtype=BF, device="cuda"), w, s)
     with pytest.raises(hla.HLA2Error):
         hla.w4_matvec(x, w, s.repeat(1, 4))  # groups of 16
+
+
+def test_output_over_the_input_is_refused():
+    x = torch.zeros((2, 128), dtype=BF, device="cuda")
+    square = torch.randint(0, 256, (128, 64), device="cuda", dtype=torch.uint8)
+    with pytest.raises(hla.HLA2Error):
+        hla.w4_matvec(x, square, torch.ones((128, 2), dtype=BF, device="cuda"), out=x)  # other CTAs still read x
