@@ -149,7 +149,9 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[16][N], int&
     }
 }
 
-// e^x and 1 / x by the approximate units (good to about an ulp; 0 and infinity where the exact ones are)
+// e^x and 1 / x by the approximate units.  1 / x is good to an ulp; e^x to about 2^-22 + 2^-24 |x| relative, the latter from
+// rounding x log2 e, which shows in a sigmoid only where it is e^z, small itself (float32 gates of -20: 6e-7 relative).
+// Subnormal results are 0, and overflow is infinity, as with the exact ones.
 __device__ __forceinline__ float fast_exp2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

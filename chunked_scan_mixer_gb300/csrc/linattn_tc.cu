@@ -19,8 +19,9 @@
 // result scaled in tensor memory (EPI-C) before MMA-Y adds to it.
 //
 // Roundings to bf16.  G~ and Sig~ are operands of one product each and are rounded once, which
-// adds to the output about its own rounding (measured against 64 bits: 2.3e-3 relative where
-// a float32 form rounded at the end has 1.65e-3).  The decayed keys are cut into two pieces (16
+// adds to the output about its own rounding (measured against 64 bits: 2.3e-3 to 2.5e-3 relative where
+// a float32 form rounded at the end has 1.65e-3).  A second operand for what is cut off would double those
+// products, and the state's has no room beside the slots at either size (226 of 227 KB are used).  The decayed keys are cut into two pieces (16
 // bits, 2^-17) here, where they only feed Sig~, and into three (24 bits, exact to float32) in the
 // summary kernel, whose sums become the states that are returned.  Decays stay float32 and out of
 // the operands everywhere else.
