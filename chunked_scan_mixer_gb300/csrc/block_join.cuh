@@ -265,8 +265,11 @@ Shape shape_of(int D, int vec) {
     if (nvec <= 32) {
         return {nvec <= 8 ? 8 : 32, kSmallThreads, 1};
     }
-    // Rows of single elements: a width that the compiler knows, for the offsets of a thread's 4 or 8 elements
-    // (5000 float32 rows of 999, the norm forward and backward: 30.2 -> 28.1 us)
+    // Rows of single elements: a width that the compiler knows, for the offsets of a thread's 4 or 8 elements.  Ten million
+    // values without and with it, us, at D = 513, 777, 999, 1281, 2047: norm forward and backward, float32 61/57/52/60/54
+    // and 68/54/49/53/50, bf16 68/63/55/69/62 and 74/55/47/63/48; join backward, bf16 145/150/127/186/145 and 111/88/77/100/78.
+    // (It loses where the last of the four or eight is mostly idle, up to 12 % just above 512, and up to 10 % in the float32
+    // join's forward above 1024.)
     if (vec == 1 && D > 512 && D <= kNarrowD) return {256, 256, D <= 1024 ? 4 : 8};
     const int most = D <= kNarrowD ? 256 : 512;
     int nv = 1;
