@@ -9,7 +9,6 @@
 #include <string.h>
 
 #include <functional>
-#include <map>
 #include <mutex>
 #include <string>
 
@@ -145,16 +144,37 @@ int set_last_error(int code, const char* fmt, ...) {
 }
 
 cudaError_t raise_smem(const void* kernel, size_t bytes) {
+    // limits by kernel and device, in a fixed table (nothing here allocates or throws); past its end the limit is asked for
+    struct Entry {
+        const void* kernel;
+        int dev;
+        size_t bytes;
+    };
+    constexpr size_t kEntries = 4096;
     static std::mutex lock;
-    static std::map<std::pair<const void*, int>, size_t> raised;  // by kernel and device
+    static Entry table[kEntries];
+    static size_t used = 0;
     int dev = 0;
     if (const cudaError_t e = cudaGetDevice(&dev)) return e;
     const std::lock_guard<std::mutex> hold(lock);
-    size_t& known = raised[{kernel, dev}];
+    size_t at = (reinterpret_cast<uintptr_t>(kernel) / 16 + 31 * (size_t)dev) % kEntries;
+    while (table[at].kernel && (table[at].kernel != kernel || table[at].dev != dev)) at = (at + 1) % kEntries;
+    size_t known = table[at].bytes;
+    if (!table[at].kernel && used + 1 == kEntries) {  // one stays free, for the search to end at
+        cudaFuncAttributes now;
+        if (const cudaError_t e = cudaFuncGetAttributes(&now, kernel)) return e;
+        known = (size_t)now.maxDynamicSharedSizeBytes;
+    }
     if (known >= bytes) return cudaSuccess;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) known = bytes;
-    return e;
+    if (e != cudaSuccess) return e;
+    if (table[at].kernel) {
+        table[at].bytes = bytes;
+    } else if (used + 1 < kEntries) {
+        table[at] = {kernel, dev, bytes};
+        ++used;
+    }
+    return cudaSuccess;
 }
 }  // namespace hla2
 

@@ -20,7 +20,11 @@
  * Conventions shared by every entry point
  *   - Every pointer is a DEVICE pointer unless stated otherwise; the caller owns every
  *     buffer.  The library allocates no device or host memory and keeps no state
- *     across calls except a thread-local error message.
+ *     across calls except a thread-local error message and the shared memory limits of
+ *     its kernels, which it only raises.
+ *   - The current device is the one of the tensors and the stream.  Several host threads may
+ *     call at once, each call with a workspace of its own; calls that share a workspace are
+ *     made on one stream, one after another.
  *   - Tensors are contiguous, head-major, row-vector layout:
  *       q, k [B, H, n, d];  v, out, dout [B, H, n, dv];  dq, dk [B, H, n, d];
  *       dv [B, H, n, dv].  Element type given by hla2_opts.dtype (HLA2_F32 or
