@@ -1,6 +1,6 @@
 // The host side of the short calls around a layer, for Python (module _hla2_host).  These calls take a few
 // microseconds on the GPU, less than their checks and allocations take in the interpreter: a step of one sequence
-// takes 12 to 15 us a call there and 4.7 to 7.4 us here, four rows of a join 15 to 18 us and 6.0 to 8.8 us.
+// takes 12 to 15 us a call there and 4.7 to 8.2 us here, four rows of a join 15 to 18 us and 6.0 to 9.6 us.
 //
 // Each function takes the tensors as the binding (hla2.py) does and covers the ordinary call: tensors of
 // the current device and a supported type, contiguous or with strides that the kernels read in place, nothing

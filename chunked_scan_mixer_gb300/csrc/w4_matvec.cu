@@ -14,7 +14,7 @@
 // 32-byte sectors from G = 64 on.  The order of k inside a product is free as long as A and B agree;
 // a word's pairs are (k, k + 4), and x is paired the same way.
 //
-// Measured: 1 x 8192 x 2048, groups of 128: 4.7 to 5.7 us a call (8.8 MB; floor 1.3).  12 x 10001 x 8192, groups of 64, no
+// Measured: 1 x 8192 x 2048, groups of 128: 4.7 to 7.8 us a call (8.8 MB; floor 1.3).  12 x 10001 x 8192, groups of 64, no
 // zero points: 26 us (44 MB; floor 6.5), bound by its instructions (84 for each 512 weights) and by x, which every CTA
 // reads: 123 MB through the L2.  Copies of x in shared memory, 32 outputs a CTA and three batches in flight were slower
 // (38, 37 and 35 us against 32, with sums of x from a product with ones, since replaced by the exact subtraction).
