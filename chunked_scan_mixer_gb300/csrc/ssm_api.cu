@@ -1,0 +1,358 @@
+// C ABI of the selective scan: argument checks, the segmentation of the sequence and the passes of a call (ssm.cuh).
+// The declarations and their documentation are in include/hla2.h.
+#include <nvtx3/nvToolsExt.h>
+
+#include "ssm.cuh"
+
+namespace hla2 {
+int set_last_error(int code, const char* fmt, ...);
+}
+
+using namespace hla2;
+
+namespace {
+
+struct Range {
+    explicit Range(const char* name) { nvtxRangePushA(name); }
+    ~Range() { nvtxRangePop(); }
+    Range(const Range&) = delete;
+    Range& operator=(const Range&) = delete;
+};
+
+int ok() { return set_last_error(HLA2_OK, "%s", ""); }
+int launch_failed(const char* what) {
+    return set_last_error(HLA2_ERR_CUDA, "%s: %s", what, cudaGetErrorString(cudaGetLastError()));
+}
+bool al(const void* p, size_t b) { return (reinterpret_cast<uintptr_t>(p) & (b - 1)) == 0; }
+int elem_size(int dtype) { return dtype == HLA2_BF16 ? 2 : 4; }
+
+// Sizes and types: what the workspace query can check.
+int check_sizes(const char* fn, const hla2_ssm_args* a) {
+    if (!a) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: args must not be NULL", fn);
+    if (a->dtype != HLA2_F32 && a->dtype != HLA2_BF16)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dtype must be HLA2_F32 or HLA2_BF16", fn);
+    if (a->B < 0 || a->n < 0 || a->D < 0)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: B, n and D must not be negative", fn);
+    if (a->N != 8 && a->N != 16 && a->N != 32 && a->N != 64)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: N must be 8, 16, 32 or 64 (got %d)", fn, a->N);
+    if (a->G < 1 || a->D % a->G != 0)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: D (%d) must be a multiple of G (%d)", fn, a->D, a->G);
+    if (a->softplus != 0 && a->softplus != 1)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: softplus must be 0 or 1", fn);
+    const long long tiles = a->D ? (long long)a->G * ((a->D / a->G + kSsmChannels - 1) / kSsmChannels) : 0;
+    if (tiles * a->B > 0x7fffffffLL || (long long)a->B * a->D > 0x7fffffffLL || a->n > 1 << 30)
+        return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: B * D must fit in 31 bits, and n be at most 2^30", fn);
+    return HLA2_OK;
+}
+
+// A tensor of the call with its strides of batch, group and token; those of dimensions of one element become packed ones.
+struct Tensor {
+    const char* name;
+    const void* p;
+    long long sb, sh, sn;
+    int B, H, n, cols;
+
+    Extent extent(int es) const {
+        return extent_of(p, (size_t)((B - 1) * sb + (H - 1) * sh + (n - 1) * sn + cols) * es);
+    }
+    bool vec(int v, int es) const {
+        return al(p, (size_t)v * es) && cols % v == 0 && sb % v == 0 && sh % v == 0 && sn % v == 0;
+    }
+    // whether no element has two places
+    bool apart() const {
+        struct Dim { long long stride; int size; } d[3] = {{sn, n}, {sh, H}, {sb, B}};
+        for (int i = 0; i < 2; ++i)
+            for (int j = 0; j < 2 - i; ++j)
+                if (d[j].stride > d[j + 1].stride) { const Dim t = d[j]; d[j] = d[j + 1], d[j + 1] = t; }
+        long long span = cols;
+        for (const Dim& x : d) {
+            if (x.size > 1 && x.stride < span) return false;
+            if (x.size > 1) span += (x.size - 1) * x.stride;
+        }
+        return true;
+    }
+};
+Tensor rows(const char* name, const hla2_rows& r, int B, int n, int cols) {
+    Tensor t{name, r.p, B > 1 ? r.sb : 0, 0, n > 1 ? r.sn : 0, B, 1, n, cols};
+    return t;
+}
+Tensor view(const char* name, const hla2_view& r, int B, int H, int n, int cols) {
+    Tensor t{name, r.p, B > 1 ? r.sb : 0, H > 1 ? r.sh : 0, n > 1 ? r.sn : 0, B, H, n, cols};
+    return t;
+}
+
+int check_tensor(const char* fn, const Tensor& t, int es, bool written) {
+    if (!t.p) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: %s must not be NULL", fn, t.name);
+    if (!al(t.p, es)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: %s is not aligned to its type", fn, t.name);
+    if (t.sb < 0 || t.sh < 0 || t.sn < 0)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: the strides of %s must not be negative", fn, t.name);
+    if (written && !t.apart()) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: rows of %s overlap", fn, t.name);
+    return HLA2_OK;
+}
+
+// The inputs of a call; the extents of everything that it reads
+struct Inputs {
+    Tensor t[5] = {};
+    int count = 0;
+    Extent read[12];
+    int reads = 0;
+    int check(const char* fn, const hla2_ssm_args* a, int n) {
+        const int es = elem_size(a->dtype);
+        t[count++] = rows("x", a->x, a->B, n, a->D);
+        t[count++] = rows("dt", a->dt, a->B, n, a->D);
+        t[count++] = view("b", a->b, a->B, a->G, n, a->N);
+        t[count++] = view("c", a->c, a->B, a->G, n, a->N);
+        if (a->gate.p) t[count++] = rows("gate", a->gate, a->B, n, a->D);
+        for (int i = 0; i < count; ++i) {
+            if (int rc = check_tensor(fn, t[i], es, false)) return rc;
+            read[reads++] = t[i].extent(es);
+        }
+        return HLA2_OK;
+    }
+    int check_params(const char* fn, const hla2_ssm_args* a) {
+        if (!a->a) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a must not be NULL", fn);
+        if (!al(a->a, 16) || !al(a->init_state, 16))
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a and the states must be 16-byte aligned", fn);
+        if (!al(a->skip, 4) || !al(a->dt_bias, 4) || !al(a->lengths, 4))
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
+        const size_t d = (size_t)a->D * sizeof(float);
+        read[reads++] = extent_of(a->a, d * a->N);
+        read[reads++] = extent_of(a->skip, d);
+        read[reads++] = extent_of(a->dt_bias, d);
+        read[reads++] = extent_of(a->lengths, (size_t)a->B * sizeof(int));
+        read[reads++] = extent_of(a->init_state, d * a->B * a->N);
+        return HLA2_OK;
+    }
+    bool meets(const Extent& e) const {
+        for (int i = 0; i < reads; ++i)
+            if (meet(e, read[i])) return true;
+        return false;
+    }
+    // whether every tensor allows vectors of v elements of the staged rows, within a group's channels too
+    bool vec(const hla2_ssm_args* a, int v) const {
+        for (int i = 0; i < count; ++i)
+            if (!t[i].vec(v, elem_size(a->dtype))) return false;
+        return a->D / a->G % v == 0;
+    }
+};
+
+SsmRows dev(const Tensor& t) { return {t.p, t.sb, t.sn}; }
+hla2_view dev4(const Tensor& t) { return {t.p, t.sb, t.sh, t.sn}; }
+
+// ---- plan ----------------------------------------------------------------------------------
+
+struct SsmPlan {
+    int tiles, nseg, seg_tokens;
+};
+
+// Segments of each sequence.  Unit: sixteen tokens of the output pass by a CTA that has its SM nearly to itself.  CTAs
+// beside one another cost 0.35 of it each once they fill the SM.  More than one segment adds the pass of their sums,
+// about 0.7 of the output pass, a launch and the joining of the segments before, which a CTA reads one after another.
+SsmPlan ssm_plan(const hla2_ssm_args* a) {
+    SsmPlan p{(a->D / a->G + kSsmChannels - 1) / kSsmChannels, 1, kSsmTokens};
+    const int steps = (a->n + kSsmTokens - 1) / kSsmTokens, sms = sm_count();
+    const long long ctas = (long long)a->B * a->G * p.tiles;
+    const double beside = 0.35 * a->N / 16;
+    double best = 0;
+    for (int want = 1; want <= steps && want <= 1024; want = want < 4 ? want + 1 : want * 5 / 4) {
+        const int each = (steps + want - 1) / want, nseg = (steps + each - 1) / each;
+        const long long per_sm = (ctas * nseg + sms - 1) / sms;
+        const double load = per_sm * beside > 1 ? per_sm * beside : 1;
+        const double cost = nseg == 1 ? each * load : each * load * 1.7 + 3 + 0.1 * nseg;
+        if (want == 1 || cost < best) best = cost, p.nseg = nseg, p.seg_tokens = each * kSsmTokens;
+    }
+    return p;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Scratch of the segments, by sequence, tile and segment: states, sums of the steps; for a backward what SsmGrads has
+struct Scratch {
+    size_t sums, steps, marks, mark_steps, rsums, bc, params, total;
+};
+Scratch scratch_of(const hla2_ssm_args* a, const SsmPlan& p, bool backward) {
+    Scratch s{};
+    const size_t slots = (size_t)a->B * a->G * p.tiles * p.nseg;
+    if (p.nseg > 1) {
+        s.sums = s.total, s.total += up256(slots * kSsmChannels * a->N * sizeof(float));
+        s.steps = s.total, s.total += up256(slots * kSsmChannels * sizeof(float));
+    }
+    if (backward) {
+        const size_t marks = slots * (p.seg_tokens / kSsmTokens), state = kSsmChannels * a->N * sizeof(float);
+        s.marks = s.total, s.total += up256(marks * state);
+        if (p.nseg > 1) {
+            s.mark_steps = s.total, s.total += up256(marks * kSsmChannels * sizeof(float));
+            s.rsums = s.total, s.total += up256(slots * state);
+        }
+        s.bc = s.total, s.total += up256((size_t)a->B * a->n * a->G * p.tiles * 2 * a->N * sizeof(float));
+        s.params = s.total, s.total += up256((size_t)a->B * p.nseg * a->D * (a->N + 2) * sizeof(float));
+    }
+    return s;
+}
+
+SsmPass base_pass(const hla2_ssm_args* a, const Inputs& in, const SsmPlan& pl) {
+    SsmPass p{};
+    p.B = a->B, p.n = a->n, p.D = a->D, p.N = a->N, p.G = a->G;
+    p.per = a->D / a->G;
+    p.tiles = pl.tiles, p.nseg = pl.nseg, p.seg_tokens = pl.seg_tokens;
+    p.softplus = a->softplus;
+    p.x = dev(in.t[0]), p.dt = dev(in.t[1]);
+    p.b = dev4(in.t[2]), p.c = dev4(in.t[3]);
+    if (a->gate.p) p.gate = dev(in.t[4]);
+    p.a = a->a, p.skip = a->skip, p.dt_bias = a->dt_bias;
+    p.lengths = a->lengths;
+    p.init = a->init_state;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t hla2_ssm_workspace_bytes(const hla2_ssm_args* a, int backward) {
+    if (check_sizes("hla2_ssm_workspace_bytes", a) != HLA2_OK) return (size_t)-1;
+    ok();
+    if (a->D == 0 || (a->B == 0 && !backward)) return 0;
+    return scratch_of(a, ssm_plan(a), backward != 0).total;
+}
+
+int hla2_ssm_forward(const hla2_ssm_args* a, hla2_rows out, float* final_state, hla2_stream_t stream) {
+    static const char* const fn = "hla2_ssm_forward";
+    Range range(fn);
+    if (int rc = check_sizes(fn, a)) return rc;
+    if (a->B == 0 || a->D == 0) return ok();
+    const int es = elem_size(a->dtype);
+    Inputs in;
+    if (int rc = in.check_params(fn, a)) return rc;
+    const Extent fin = extent_of(final_state, (size_t)a->B * a->D * a->N * sizeof(float));
+    if (!al(final_state, 16)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a and the states must be 16-byte aligned", fn);
+    bool vec = true;
+    Tensor o = rows("out", out, a->B, a->n, a->D);
+    if (a->n > 0) {
+        if (int rc = in.check(fn, a, a->n)) return rc;
+        if (int rc = check_tensor(fn, o, es, true)) return rc;
+        if (in.meets(o.extent(es)) || meet(o.extent(es), fin))
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps another tensor", fn);
+        const int v = 16 / es;
+        vec = in.vec(a, v) && o.vec(v, es);
+    } else if (!final_state) {
+        return ok();
+    }
+    if (in.meets(fin)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: final_state overlaps an input", fn);
+    const SsmPlan pl = ssm_plan(a);
+    const Scratch s = scratch_of(a, pl, false);
+    if (s.total > 0 && (!a->workspace || a->workspace_bytes < s.total || !al(a->workspace, 16)))
+        return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, s.total);
+    SsmPass p = base_pass(a, in, pl);
+    p.out = dev(o);
+    p.fin = final_state;
+    char* ws = static_cast<char*>(a->workspace);
+    if (pl.nseg > 1) {
+        p.sums = reinterpret_cast<float*>(ws + s.sums);
+        p.steps = reinterpret_cast<float*>(ws + s.steps);
+    }
+    if (launch_ssm_forward(p, a->dtype == HLA2_BF16, vec, reinterpret_cast<cudaStream_t>(stream)))
+        return launch_failed("selective scan");
+    return ok();
+}
+
+int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfinal_state, const hla2_ssm_grads* grads,
+                      hla2_stream_t stream) {
+    static const char* const fn = "hla2_ssm_backward";
+    Range range(fn);
+    if (int rc = check_sizes(fn, a)) return rc;
+    if (!grads) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: grads must not be NULL", fn);
+    if (a->D == 0) return ok();
+    const int es = elem_size(a->dtype);
+    Inputs in;
+    if (int rc = in.check_params(fn, a)) return rc;
+    const size_t db = (size_t)a->D * sizeof(float);
+    in.read[in.reads++] = extent_of(dfinal_state, db * a->B * a->N);
+    if (!grads->da || (a->skip != nullptr) != (grads->dskip != nullptr) ||
+        (a->dt_bias != nullptr) != (grads->ddt_bias != nullptr))
+        return set_last_error(HLA2_ERR_INVALID_ARG,
+                              "%s: da is needed, dskip and ddt_bias with their inputs, and neither without", fn);
+    if (!al(dfinal_state, 16) || !al(grads->dinit_state, 16))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a and the states must be 16-byte aligned", fn);
+    if (!al(grads->da, 4) || !al(grads->dskip, 4) || !al(grads->ddt_bias, 4))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
+    Extent written[9];
+    int count = 0;
+    written[count++] = extent_of(grads->da, db * a->N);
+    written[count++] = extent_of(grads->dskip, db);
+    written[count++] = extent_of(grads->ddt_bias, db);
+    written[count++] = extent_of(grads->dinit_state, db * a->B * a->N);
+    bool vec = true;
+    Tensor o[6] = {};
+    if (a->n > 0 && a->B > 0) {
+        if (int rc = in.check(fn, a, a->n)) return rc;
+        int outs = 0;
+        o[outs++] = rows("dout", dout, a->B, a->n, a->D);
+        o[outs++] = rows("dx", grads->dx, a->B, a->n, a->D);
+        o[outs++] = rows("ddt", grads->ddt, a->B, a->n, a->D);
+        o[outs++] = view("db", grads->db, a->B, a->G, a->n, a->N);
+        o[outs++] = view("dc", grads->dc, a->B, a->G, a->n, a->N);
+        if (a->gate.p) o[outs++] = rows("dgate", grads->dgate, a->B, a->n, a->D);
+        vec = in.vec(a, 16 / es);
+        for (int i = 0; i < outs; ++i) {
+            if (int rc = check_tensor(fn, o[i], es, i > 0)) return rc;
+            if (i == 0) in.read[in.reads++] = o[i].extent(es);
+            else written[count++] = o[i].extent(es);
+            vec = vec && o[i].vec(16 / es, es);
+        }
+    }
+    if ((a->gate.p != nullptr) != (grads->dgate.p != nullptr) && a->n > 0 && a->B > 0)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dgate is needed with gate, and only then", fn);
+    for (int i = 0; i < count; ++i) {
+        if (in.meets(written[i])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps an input", fn);
+        for (int j = 0; j < i; ++j)
+            if (meet(written[i], written[j])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: gradients overlap", fn);
+    }
+    const SsmPlan pl = ssm_plan(a);
+    const Scratch s = scratch_of(a, pl, true);
+    if (s.total > 0 && (!a->workspace || a->workspace_bytes < s.total || !al(a->workspace, 16)))
+        return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, s.total);
+    SsmPass p = base_pass(a, in, pl);
+    SsmGrads g{};
+    g.dout = dev(o[0]), g.dx = dev(o[1]), g.ddt = dev(o[2]);
+    g.db = dev4(o[3]), g.dc = dev4(o[4]);
+    if (a->gate.p) g.dgate = dev(o[5]);
+    g.da = grads->da, g.dskip = grads->dskip, g.ddt_bias = grads->ddt_bias, g.dinit = grads->dinit_state;
+    g.dfinal = dfinal_state;
+    g.macros = pl.seg_tokens / kSsmTokens;
+    auto at = [&](size_t offset) { return reinterpret_cast<float*>(static_cast<char*>(a->workspace) + offset); };
+    g.marks = at(s.marks), g.bc = at(s.bc), g.params = at(s.params);
+    if (pl.nseg > 1) p.sums = at(s.sums), p.steps = at(s.steps), g.mark_steps = at(s.mark_steps), g.rsums = at(s.rsums);
+    if (launch_ssm_backward(p, g, a->dtype == HLA2_BF16, vec, reinterpret_cast<cudaStream_t>(stream)))
+        return launch_failed("selective scan gradients");
+    return ok();
+}
+
+int hla2_ssm_decode_step(const hla2_ssm_args* a, float* state, hla2_rows out, hla2_stream_t stream) {
+    static const char* const fn = "hla2_ssm_decode_step";
+    Range range(fn);
+    if (int rc = check_sizes(fn, a)) return rc;
+    if (a->B == 0 || a->D == 0) return ok();
+    if (a->lengths || a->init_state)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: lengths and init_state must be NULL", fn);
+    const int es = elem_size(a->dtype);
+    Inputs in;
+    if (int rc = in.check_params(fn, a)) return rc;
+    if (int rc = in.check(fn, a, 1)) return rc;
+    if (!state || !al(state, 16))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: the state must be a 16-byte aligned address", fn);
+    const Tensor o = rows("out", out, a->B, 1, a->D);
+    if (int rc = check_tensor(fn, o, es, true)) return rc;
+    const Extent eo = o.extent(es), est = extent_of(state, (size_t)a->B * a->D * a->N * sizeof(float));
+    if (meet(eo, est) || in.meets(eo) || in.meets(est))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out or the state overlaps another tensor", fn);
+    SsmPass p = base_pass(a, in, SsmPlan{1, 1, 1});
+    p.out = dev(o);
+    // four values of b and c at a time
+    const bool vec = in.t[2].vec(4, es) && in.t[3].vec(4, es);
+    if (launch_ssm_step(p, state, a->dtype == HLA2_BF16, vec, reinterpret_cast<cudaStream_t>(stream)))
+        return launch_failed("selective scan step");
+    return ok();
+}
+
+}  // extern "C"

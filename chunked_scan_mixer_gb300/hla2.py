@@ -64,6 +64,11 @@ class View(ctypes.Structure):
                 ("sn", ctypes.c_longlong)]
 
 
+class Rows(ctypes.Structure):
+    """Base address and element strides of batch and token (hla2_rows)."""
+    _fields_ = [("p", ctypes.c_void_p), ("sb", ctypes.c_longlong), ("sn", ctypes.c_longlong)]
+
+
 _SIZE_MAX = ctypes.c_size_t(-1).value
 
 FLAG_SAVE_FOR_BACKWARD = 1
@@ -164,6 +169,14 @@ def lib():
         L.hla2_block_join_backward.restype = I
         L.hla2_w4_matvec.argtypes = [P, ctypes.c_longlong, P, P, P, P, P, I, I, I, I, I, P]
         L.hla2_w4_matvec.restype = I
+        L.hla2_ssm_workspace_bytes.argtypes = [P, I]
+        L.hla2_ssm_workspace_bytes.restype = Z
+        L.hla2_ssm_forward.argtypes = [P, Rows, P, P]
+        L.hla2_ssm_forward.restype = I
+        L.hla2_ssm_backward.argtypes = [P, Rows, P, P, P]
+        L.hla2_ssm_backward.restype = I
+        L.hla2_ssm_decode_step.argtypes = [P, P, Rows, P]
+        L.hla2_ssm_decode_step.restype = I
         for name in ("hla2_state_to_compact", "hla2_state_from_compact"):
             getattr(L, name).argtypes = [P, P, I, I, I, I, P]
             getattr(L, name).restype = I
@@ -206,6 +219,7 @@ EXPORTED_SYMBOLS = (
     "hla2_noalloc_selftest_wait_timeout", "hla2_debug_status", "hla2_debug_selftest",
     "hla2_linattn_workspace_bytes", "hla2_linattn_forward", "hla2_linattn_backward", "hla2_linattn_decode_step",
     "hla2_block_join", "hla2_block_join_backward_workspace_bytes", "hla2_block_join_backward", "hla2_w4_matvec",
+    "hla2_ssm_workspace_bytes", "hla2_ssm_forward", "hla2_ssm_backward", "hla2_ssm_decode_step",
 )
 
 FLAG_COMPACT_STATE = 4
@@ -1236,4 +1250,194 @@ def _w4_matvec(x, qweight, scales, zeros, bias, out):
                               out.data_ptr(), M, N, K, group, _DTYPES[x.dtype], _raw_stream(index))
     if rc:
         _check("hla2_w4_matvec", rc)
+    return out
+
+
+# ---------------------------------------------------------------------------------------
+# A selective state space layer: the scan, the short convolution before it, and layer norm
+# ---------------------------------------------------------------------------------------
+
+_SSM_ARGS = struct.Struct("@7i" + 3 * "P2q" + 2 * "P3q" + "5P" + "PN")   # hla2_ssm_args
+_SSM_GRADS = struct.Struct("@" + 3 * "P2q" + 2 * "P3q" + "4P")           # hla2_ssm_grads
+
+
+class SsmGrads(NamedTuple):
+    """Gradients of ssm_forward's inputs (None where the input was None); those of a, skip, dt_bias and the state
+    are float32."""
+    dx: torch.Tensor
+    ddt: torch.Tensor
+    da: torch.Tensor
+    db: torch.Tensor
+    dc: torch.Tensor
+    dskip: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    ddt_bias: Optional[torch.Tensor]
+    dinit_state: Optional[torch.Tensor]
+
+
+def _last_dense(t):
+    """The tensor, or a copy where its last dimension is not contiguous."""
+    return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+def _token_rows(name, t, shape):
+    """(tensor, (address, strides of batch and token)) of [B, n, D]"""
+    if t is None:
+        return None, (0, 0, 0)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}")
+    t = _last_dense(t)
+    return t, (t.data_ptr(), *t.stride()[:2])
+
+
+def _float_param(name, t, shape, index):
+    """A float32 parameter as the kernels read it."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.get_device() != index:
+        raise ValueError(f"{name} must be {shape} on the inputs' device")
+    return _packed16(t.to(torch.float32))
+
+
+def _length_tensor(lengths, B, n, device):
+    """Token counts as the kernels read them: int32 on the device."""
+    if lengths is None:
+        return None
+    if not (isinstance(lengths, torch.Tensor) and lengths.dtype == torch.int32 and lengths.device == device
+            and lengths.is_contiguous()):
+        lengths = torch.as_tensor(lengths, device=device)
+        if lengths.dtype not in (torch.int32, torch.int64):
+            raise ValueError("lengths must be integers")
+        lengths = (lengths.clamp(0, n) if lengths.dtype == torch.int64 else lengths).to(torch.int32).contiguous()
+    if lengths.shape != (B,):
+        raise ValueError("lengths must be B integers")
+    return lengths
+
+
+class _Ssm(NamedTuple):
+    """One checked call: sizes, the fields of its argument block but for the workspace, and the tensors
+    that they point into."""
+    B: int
+    n: int
+    D: int
+    N: int
+    G: int
+    device: torch.device
+    index: int
+    head: tuple
+    keep: tuple
+
+    def run(self, fn, backward, call):
+        stream = _raw_stream(self.index)
+        skip = _STATUS_BYTES  # the cached buffer's status word is other calls'
+
+        def query():
+            nbytes = lib().hla2_ssm_workspace_bytes(_SSM_ARGS.pack(*self.head, 0, 0), backward)
+            return nbytes if nbytes in (0, _SIZE_MAX) else nbytes + skip
+
+        rc = _with_scratch(lambda p, nbytes: call(_SSM_ARGS.pack(*self.head, p and p + skip, max(nbytes - skip, 0)), stream),
+                           query, self.index, stream)
+        if rc:
+            _check(fn, rc)
+
+
+def _ssm_args(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state):
+    index = _need_cuda(x, dt, b, c, gate)
+    if x.dim() != 3 or b.dim() not in (3, 4) or c.shape != b.shape or a.dim() != 2:
+        raise ValueError("x must be [B, n, D], a [D, N], b and c [B, n, N] or [B, n, G, N]")
+    B, n, D = x.shape
+    if b.dim() == 3:
+        b, c = b.unsqueeze(2), c.unsqueeze(2)
+    G, N = b.shape[2:]
+    if b.shape[:2] != (B, n) or G == 0 or D % G:
+        raise ValueError("b and c must be [B, n, N] or [B, n, G, N] with G dividing the channels")
+    (x, xr), (dt, dr), (gate, gr) = (_token_rows(name, t, x.shape) for name, t in (("x", x), ("dt", dt), ("gate", gate)))
+    b, c = _last_dense(b), _last_dense(c)
+    bv, cv = ((t.data_ptr(), t.stride(0), t.stride(2), t.stride(1)) for t in (b, c))
+    a = _float_param("a", a, (D, N), index)
+    skip, dt_bias = _float_param("skip", skip, (D,), index), _float_param("dt_bias", dt_bias, (D,), index)
+    device = x.device
+    lengths = _length_tensor(lengths, B, n, device)
+    init = _state_arg("init_state", init_state, (B, D, N), device)
+    head = (_DTYPES[x.dtype], B, n, D, N, G, int(bool(dt_softplus)), *xr, *dr, *gr, *bv, *cv, a.data_ptr(), _addr(skip),
+            _addr(dt_bias), _addr(lengths), _addr(init))
+    return _Ssm(B, n, D, N, G, device, index, head, (x, dt, gate, b, c, a, skip, dt_bias, lengths, init))
+
+
+def ssm_forward(x, dt, a, b, c, skip=None, gate=None, dt_bias=None, dt_softplus=True, lengths=None, init_state=None,
+                return_final_state=False):
+    """The selective scan: a state of N values for each channel whose decay, input and output depend on the token,
+    delta_t = softplus(dt_t + dt_bias), h_t = exp(delta_t a) h_{t-1} + delta_t x_t b_t,
+    out_t = (sum_N c_t h_t + skip x_t) silu(gate_t).
+
+    x, dt, gate [B,n,D]; b, c [B,n,N], or [B,n,G,N] for G groups of D / G channels; float32 or bfloat16 of
+    one type on the GPU, any strides (a contiguous last dimension is read in place, as the parts of a projection are).
+    a [D,N] with N 8, 16, 32 or 64 (negative values decay); skip and dt_bias [D]; these three are used as float32.
+    dt_softplus=False: delta = dt + dt_bias.  lengths: None or B token counts; the rows past a sequence's length are
+    padding, whatever they hold: 0 in the output, and not in the state.  init_state: float32 [B,D,N] to continue from.
+    Returns out [B,n,D] and with ``return_final_state`` the float32 state after each sequence's last token,
+    which ssm_decode_step goes on from."""
+    return _ssm_forward(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state, return_final_state)
+
+
+@_on_its_device
+def _ssm_forward(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state, return_final_state):
+    s = _ssm_args(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state)
+    out = torch.empty((s.B, s.n, s.D), dtype=x.dtype, device=s.device)
+    fin = torch.empty((s.B, s.D, s.N), dtype=torch.float32, device=s.device) if return_final_state else None
+    L = lib()
+    s.run("hla2_ssm_forward", 0, lambda args, stream: L.hla2_ssm_forward(args, Rows(out.data_ptr(), *out.stride()[:2]),
+                                                                         _addr(fin), stream))
+    return (out, fin) if return_final_state else out
+
+
+def ssm_backward(x, dt, a, b, c, dout, skip=None, gate=None, dt_bias=None, dt_softplus=True, lengths=None,
+                 init_state=None, dfinal_state=None):
+    """SsmGrads of ssm_forward for the upstream gradient dout [B,n,D] of its output and dfinal_state (None: zero) of its
+    final state.  Nothing is kept from the forward."""
+    return _ssm_backward(x, dt, a, b, c, dout, skip, gate, dt_bias, dt_softplus, lengths, init_state, dfinal_state)
+
+
+@_on_its_device
+def _ssm_backward(x, dt, a, b, c, dout, skip, gate, dt_bias, dt_softplus, lengths, init_state, dfinal_state):
+    s = _ssm_args(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state)
+    _need_cuda(x, dout)
+    dout, do_rows = _token_rows("dout", dout, x.shape)
+    dfin = _state_arg("dfinal_state", dfinal_state, (s.B, s.D, s.N), s.device)
+    new = lambda *shape, dtype=x.dtype: torch.empty(shape, dtype=dtype, device=s.device)  # noqa: E731
+    f32 = torch.float32
+    dx, ddt = new(s.B, s.n, s.D), new(s.B, s.n, s.D)
+    dgate = None if gate is None else new(s.B, s.n, s.D)
+    db, dc = new(s.B, s.n, s.G, s.N), new(s.B, s.n, s.G, s.N)
+    da = new(s.D, s.N, dtype=f32)
+    dskip, dbias = (None if t is None else new(s.D, dtype=f32) for t in (skip, dt_bias))
+    dinit = None if init_state is None else new(s.B, s.D, s.N, dtype=f32)
+    rows, groups = (s.n * s.D, s.D), (s.n * s.G * s.N, s.N, s.G * s.N)
+    grads = _SSM_GRADS.pack(dx.data_ptr(), *rows, ddt.data_ptr(), *rows, _addr(dgate), *rows, db.data_ptr(), *groups,
+                            dc.data_ptr(), *groups, da.data_ptr(), _addr(dskip), _addr(dbias), _addr(dinit))
+    L = lib()
+    s.run("hla2_ssm_backward", 1, lambda args, stream: L.hla2_ssm_backward(args, Rows(*do_rows), _addr(dfin), grads, stream))
+    return SsmGrads(dx, ddt, da, db.view(b.shape), dc.view(b.shape), dskip, dgate, dbias, dinit)
+
+
+def ssm_decode_step(state, x, dt, a, b, c, skip=None, gate=None, dt_bias=None, dt_softplus=True):
+    """One token of the selective scan for each of B sequences: ``state`` [B,D,N] float32 on the GPU is updated in
+    place.  x, dt, gate [B,D]; b, c [B,N] or [B,G,N]; the rest as ssm_forward has it.  Returns out [B,D]."""
+    return _ssm_decode_step(state, x, dt, a, b, c, skip, gate, dt_bias, dt_softplus)
+
+
+@_on_its_device
+def _ssm_decode_step(state, x, dt, a, b, c, skip, gate, dt_bias, dt_softplus):
+    if x.dim() != 2 or b.dim() not in (2, 3) or c.shape != b.shape:
+        raise ValueError("x must be [B, D], b and c [B, N] or [B, G, N]")
+    one = lambda t: None if t is None else t.unsqueeze(1)  # noqa: E731
+    s = _ssm_args(one(x), one(dt), a, one(b), one(c), skip, one(gate), dt_bias, dt_softplus, None, None)
+    if (tuple(state.shape) != (s.B, s.D, s.N) or state.dtype != torch.float32 or state.get_device() != s.index
+            or not state.is_contiguous()):
+        raise ValueError(f"state must be a contiguous float32 {(s.B, s.D, s.N)} tensor on the inputs' device")
+    out = torch.empty((s.B, s.D), dtype=x.dtype, device=s.device)
+    rc = lib().hla2_ssm_decode_step(_SSM_ARGS.pack(*s.head, 0, 0), state.data_ptr(), Rows(out.data_ptr(), s.D, 0),
+                                    _raw_stream(s.index))
+    if rc:
+        _check("hla2_ssm_decode_step", rc)
     return out

@@ -543,6 +543,73 @@ int hla2_block_join_backward(const hla2_block_args* a, const void* dr, const voi
 int hla2_w4_matvec(const void* x, long long x_stride, const void* qweight, const void* scales, const void* zeros,
                    const void* bias, void* y, int M, int N, int K, int group, int dtype, hla2_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------------------
+ * A selective state space layer: the scan, the short convolution before it, and layer norm.
+ * ---------------------------------------------------------------------------------------
+ *
+ * The selective scan: every channel d has a state h of N values, whose decay, input and output depend on
+ * the token.  Per channel and token t, with n = 0 .. N - 1 and the channel's group g = d / (D / G):
+ *
+ *   delta_t = softplus(dt_t + dt_bias)        (softplus 0: dt_t + dt_bias)
+ *   h_t[n] = exp(delta_t a[n]) h_{t-1}[n] + delta_t x_t b_t[g, n]
+ *   y_t = sum_n c_t[g, n] h_t[n] + skip x_t,  out_t = y_t silu(gate_t)
+ *
+ * Sequence s holds lengths[s] tokens (clamped to [0, n]; NULL: n each).  The rows past its length are
+ * padding: never used, whatever they hold; their outputs and gradients are 0 and they leave the state alone.
+ * Steps, decays, states and sums are float32 whatever the tensors' type.  A non-finite value in a valid row may reach
+ * everything after it in its sequence (in b or c: of its group, else of its channel), and in a backward everything of its
+ * sequence.
+ *
+ * Rows of tokens are a base address and the element strides of batch and token; the last dimension is
+ * contiguous.  Inputs may have any non-negative strides and any alignment of an element; 16-byte ones are faster.
+ * These calls have no device-side waits; their workspace has no status word and needs no initial contents.
+ */
+typedef struct {
+    const void* p;
+    long long sb, sn; /* element strides of batch and token */
+} hla2_rows;
+
+typedef struct {
+    int dtype;                 /* HLA2_F32 | HLA2_BF16: x, dt, gate, b, c, out, dout and their gradients */
+    int B, n, D, N, G;         /* N 8, 16, 32 or 64; D a multiple of G; 0 <= n <= 2^30                   */
+    int softplus;              /* 0 or 1                                                                 */
+    hla2_rows x, dt, gate;     /* [B, n, D]; gate.p NULL: none                                           */
+    hla2_view b, c;            /* [B, G, n, N]: strides of batch, group and token                        */
+    const float* a;            /* [D, N], 16-byte aligned as the states are                              */
+    const float *skip, *dt_bias; /* [D], nullable                                                        */
+    const int* lengths;        /* device int [B], or NULL                                                */
+    const float* init_state;   /* nullable: contiguous [B, D, N], the state before token 0               */
+    void* workspace;           /* device scratch of the size the query gives, 16-byte aligned            */
+    size_t workspace_bytes;
+} hla2_ssm_args;
+
+/* Scratch bytes of a forward (backward = 0) or a backward (1); the addresses in *a are not looked at.
+ * (size_t)-1 for arguments that the call would reject. */
+size_t hla2_ssm_workspace_bytes(const hla2_ssm_args* a, int backward);
+
+/* out [B, n, D]; final_state (nullable) receives the contiguous [B, D, N] state after each sequence's last token.
+ * out may not overlap an input, nor final_state init_state or out. */
+int hla2_ssm_forward(const hla2_ssm_args* a, hla2_rows out, float* final_state, hla2_stream_t stream);
+
+/* Gradients of sum(out * dout) + sum(final_state * dfinal_state).  da [D, N], dskip and ddt_bias [D] are float32 sums over
+ * sequences and tokens in a fixed order; dinit_state [B, D, N] float32.  db and dc are sums over the channels of a group.
+ * dgate is needed with gate, dskip with skip, ddt_bias with dt_bias, and each is NULL without; dinit_state is nullable. */
+typedef struct {
+    hla2_rows dx, ddt, dgate; /* [B, n, D]    */
+    hla2_view db, dc;         /* [B, G, n, N] */
+    float *da, *dskip, *ddt_bias, *dinit_state;
+} hla2_ssm_grads;
+
+/* Nothing is kept from the forward.  dfinal_state: nullable.  No gradient may overlap another tensor of the call. */
+int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfinal_state, const hla2_ssm_grads* grads,
+                      hla2_stream_t stream);
+
+/* One token for each of B sequences: state [B, D, N] float32 is updated in place, out [B, D] written.  n, the token
+ * strides and the workspace are not looked at; lengths and init_state are NULL.  Neither out nor the state may overlap another
+ * tensor of the call. */
+int hla2_ssm_decode_step(const hla2_ssm_args* a, float* state, hla2_rows out, hla2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

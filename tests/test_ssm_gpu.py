@@ -1,0 +1,241 @@
+"""The selective scan on the GPU against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import chunked_scan_mixer_gb300 as hla
+from oracle import ssm_oracle as O
+
+from .ssm_cases import BF, F32, close, f64, make_ssm
+
+pytestmark = pytest.mark.gpu
+
+
+def oracle_args(c, **kw):
+    d = {k: f64(v) for k, v in c.items()}
+    d.update(kw)
+    return d
+
+
+def check_forward(c, lengths=None, **kw):
+    lens = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, fin = hla.ssm_forward(**c, lengths=lens, return_final_state=True, **kw)
+    want, wfin = O.ssm_forward(**oracle_args(c, lengths=lengths, **kw))
+    assert out.dtype == c["x"].dtype and fin.dtype == F32
+    close(out, want, "out")
+    close(fin, wfin, "final state")
+    if lengths is not None:
+        for s, m in enumerate(lengths):
+            assert (out[s, max(m, 0):] == 0).all()
+    return out, fin
+
+
+def check_backward(c, lengths=None, dfinal=True, seed=1, **kw):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dout = torch.randn(c["x"].shape, generator=g, device="cuda").to(c["x"].dtype)
+    B, n, D = c["x"].shape
+    dfin = torch.randn((B, D, c["a"].shape[1]), generator=g, device="cuda") if dfinal else None
+    lens = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    got = hla.ssm_backward(dout=dout, dfinal_state=dfin, lengths=lens, **c, **kw)
+    want = O.ssm_backward(**oracle_args(c, dout=f64(dout), dfinal_state=f64(dfin), lengths=lengths, **kw))
+    for name in got._fields:
+        t = getattr(got, name)
+        source = {"dskip": "skip", "dgate": "gate", "ddt_bias": "dt_bias", "dinit_state": "init_state"}.get(name)
+        if source and c[source] is None:
+            assert t is None
+        else:
+            close(t, want[name], name)
+    return got
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 100])
+def test_forward(dtype, N, n):
+    check_forward(make_ssm(2, n, 72, N, dtype=dtype, seed=n))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("D, G", [(1, 1), (7, 1), (63, 1), (65, 1), (128, 2), (66, 2), (12, 4), (200, 1)])
+def test_channels_and_groups(dtype, D, G):
+    c = make_ssm(2, 37, D, 16, G, dtype=dtype, seed=D)
+    check_forward(c)
+    check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("n", [1, 4, 16, 33, 100])
+def test_backward(dtype, N, n):
+    check_backward(make_ssm(2, n, 72, N, dtype=dtype, seed=n))
+
+
+@pytest.mark.parametrize("have", ["", "gate", "skip", "bias", "state"])
+@pytest.mark.parametrize("softplus", [True, False])
+def test_optional_inputs(have, softplus):
+    c = make_ssm(2, 40, 24, 16, **{k: k == have for k in ("gate", "skip", "bias", "state")})
+    if not softplus:
+        c["dt"] = c["dt"].abs() * 0.1
+        if c["dt_bias"] is not None:  # about -5, for the softplus: as a step it would grow past 64 bits, e^80 a token
+            c["dt_bias"] = c["dt_bias"].abs() * 0.01
+    check_forward(c, dt_softplus=softplus)
+    check_backward(c, dt_softplus=softplus, dfinal=have == "state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lengths", [[0, 40, 17], [40, -3, 1], [99, 16, 0]])
+def test_lengths(dtype, lengths):
+    c = make_ssm(3, 40, 24, 16, dtype=dtype, seed=5)
+    for s, m in enumerate(lengths):  # padding holds anything
+        for k in ("x", "dt", "b", "c", "gate"):
+            c[k][s, max(m, 0):] = float("nan") if s % 2 else float("inf")
+    out, fin = check_forward(c, lengths)
+    g = check_backward(c, lengths)
+    for t in (g.dx, g.ddt, g.dgate, g.db, g.dc):
+        for s, m in enumerate(lengths):
+            assert (t[s, max(m, 0):] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n", [700, 1500])
+def test_segments(dtype, n):
+    """Few channels and many tokens: the sequence is cut into segments."""
+    c = make_ssm(1, n, 24, 16, dtype=dtype, seed=n)
+    assert hla.lib().hla2_ssm_workspace_bytes  # the plan is the library's own
+    check_forward(c)
+    check_forward(c, [n // 3])
+    check_backward(c)
+    check_backward(c, [n - n // 3])
+
+
+def test_fast_and_slow_steps():
+    """Steps from next to nothing, where softplus is e^x, to ones that forget at once."""
+    c = make_ssm(1, 64, 32, 16, dt_scale=8.0, seed=9)
+    c["dt"][:, :, 0] = -30.0
+    c["dt"][:, :, 1] = 60.0
+    c["dt"][:, :, 2] = -200.0
+    check_forward(c)
+    check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("B, D, G", [(1, 64, 1), (3, 50, 2), (300, 96, 1)])
+def test_step_follows_the_forward(dtype, N, B, D, G):
+    c = make_ssm(B, 3, D, N, G, dtype=dtype, seed=B)
+    state = c.pop("init_state")
+    want, wst = O.ssm_forward(**oracle_args(c, init_state=f64(state)))
+    for t in range(3):
+        one = {k: c[k][:, t] if k in ("x", "dt", "b", "c", "gate") else c[k] for k in c}
+        close(hla.ssm_decode_step(state, **one), want[:, t], f"token {t}")
+    close(state, wst, "state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_strides(dtype):
+    """Parts of a projection, tokens before sequences, odd offsets and a broadcast: the values of contiguous copies."""
+    B, n, D, G, N = 2, 50, 40, 2, 16
+    c = make_ssm(B, n, D, N, G, dtype=dtype, seed=3)
+    want = hla.ssm_forward(**c, return_final_state=True)
+    dout = torch.randn(B, n, D, device="cuda").to(dtype)
+    grads = hla.ssm_backward(dout=dout, **c)
+    xz = torch.empty(B, n, 2 * D + 1, device="cuda", dtype=dtype)
+    odd = torch.empty(n, B, 3 + D + 2 * G * N, device="cuda", dtype=dtype).transpose(0, 1)
+    v = dict(c)
+    v["x"], v["gate"], v["dt"] = xz[..., :D], xz[..., D + 1:], odd[..., 3:3 + D]
+    v["b"] = odd[..., 3 + D:3 + D + G * N].unflatten(-1, (G, N))
+    v["c"] = odd[..., 3 + D + G * N:].unflatten(-1, (G, N))
+    for k in ("x", "gate", "dt", "b", "c"):
+        v[k].copy_(c[k])
+    got = hla.ssm_forward(**v, return_final_state=True)
+    dv = torch.empty(B, D, n, device="cuda", dtype=dtype).transpose(1, 2)  # copied: the last dimension is strided
+    dv.copy_(dout)
+    for u, w in zip((*got, *hla.ssm_backward(dout=dv, **v)), (*want, *grads)):
+        assert torch.equal(u, w)
+    # one gate row for all tokens, one b for all sequences
+    v["gate"] = c["gate"][:, :1].expand(B, n, D)
+    v["b"] = c["b"][:1].expand(B, n, G, N)
+    same = {**c, "gate": v["gate"].contiguous(), "b": v["b"].contiguous()}
+    for u, w in zip(hla.ssm_backward(dout=dout, **v), hla.ssm_backward(dout=dout, **same)):
+        assert torch.equal(u, w)
+
+
+def test_three_dimensional_b_and_c():
+    c = make_ssm(2, 20, 24, 8)
+    flat = {**c, "b": c["b"][:, :, 0], "c": c["c"][:, :, 0]}
+    assert torch.equal(hla.ssm_forward(**c), hla.ssm_forward(**flat))
+    dout = torch.randn(2, 20, 24, device="cuda")
+    u, v = hla.ssm_backward(dout=dout, **c), hla.ssm_backward(dout=dout, **flat)
+    assert v.db.shape == flat["b"].shape and torch.equal(u.db[:, :, 0], v.db) and torch.equal(u.dc[:, :, 0], v.dc)
+
+
+def test_empty():
+    c = make_ssm(2, 0, 24, 16)
+    out, fin = hla.ssm_forward(**c, return_final_state=True)
+    assert out.shape == (2, 0, 24) and torch.equal(fin, c["init_state"])
+    dfin = torch.randn_like(fin)
+    g = hla.ssm_backward(dout=out, dfinal_state=dfin, **c)
+    assert torch.equal(g.dinit_state, dfin) and not g.da.any() and not g.dskip.any() and not g.ddt_bias.any()
+    c = make_ssm(0, 5, 24, 16)
+    assert hla.ssm_forward(**c).shape == (0, 5, 24)
+    g = hla.ssm_backward(dout=c["x"], **c)
+    assert g.db.shape == (0, 5, 1, 16) and not g.da.any() and not g.ddt_bias.any()
+
+
+def test_gradients_are_differences():
+    """The kernels' own forward, differenced in float32 along a few directions: the truncation is of second order and the
+    rounding of the loss, about 1e-6 of its terms, is divided by the step 1e-2."""
+    c = make_ssm(1, 30, 16, 8, seed=11)
+    dout = torch.randn(1, 30, 16, device="cuda")
+    g = hla.ssm_backward(dout=dout, **c)
+
+    def loss(d):
+        return (hla.ssm_forward(**d).double() * dout.double()).sum().item()
+
+    eps = 1e-2
+    for name in ("x", "dt", "a", "b", "c", "skip", "gate", "dt_bias", "init_state"):
+        u = torch.randn_like(c[name])
+        u = u / u.norm()
+        diff = (loss({**c, name: c[name] + eps * u}) - loss({**c, name: c[name] - eps * u})) / (2 * eps)
+        want = (getattr(g, "d" + name).double() * u.double()).sum().item()
+        terms = (hla.ssm_forward(**c).abs().double() * dout.abs().double()).sum().item()
+        assert abs(diff - want) <= 1e-6 * terms / eps + 1e-3 * abs(want) + 1e-3, (name, diff, want)
+
+
+def test_repeatable_and_on_another_stream():
+    c = make_ssm(2, 600, 64, 16, dtype=BF)
+    dout = torch.randn_like(c["x"])
+    want = (*hla.ssm_forward(**c, return_final_state=True), *hla.ssm_backward(dout=dout, **c))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = (*hla.ssm_forward(**c, return_final_state=True), *hla.ssm_backward(dout=dout, **c))
+    side.synchronize()
+    for u, v in zip(got, want):
+        assert torch.equal(u, v)
+
+
+def test_captured():
+    """Forward, backward and step in one graph, replayed on other values, with eager calls of the same sizes between."""
+    c = make_ssm(1, 900, 64, 16, dtype=BF)
+    d = make_ssm(1, 900, 64, 16, dtype=BF, seed=7)
+    dout = torch.randn_like(c["x"])
+    static = {k: v.clone() for k, v in c.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        hla.ssm_forward(**static)
+        hla.ssm_backward(dout=dout, **static)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, fin = hla.ssm_forward(**static, return_final_state=True)
+        grads = hla.ssm_backward(dout=dout, **static)
+    for case in (d, c):
+        for k, v in static.items():
+            v.copy_(case[k])
+        graph.replay()
+        want = (*hla.ssm_forward(**case, return_final_state=True), *hla.ssm_backward(dout=dout, **case))
+        graph.replay()
+        for u, v in zip((out, fin, *grads), want):
+            assert torch.equal(u, v)
