@@ -10,6 +10,7 @@ from .hla2 import (BlockJoinGrads, HLA2Error, ahla_backward, ahla_decode_step, a
                    state_to_compact)
 from .hla2 import (block_join, block_join_backward, block_norm, block_norm_backward, linattn_backward,  # noqa: F401
                    linattn_decode_step, linattn_forward, w4_matvec)
-from .hla2 import SsmGrads, ssm_backward, ssm_decode_step, ssm_forward  # noqa: F401
+from .hla2 import (ShortConvGrads, SsmGrads, layer_norm, layer_norm_backward, short_conv_backward,  # noqa: F401
+                   short_conv_decode_step, short_conv_forward, ssm_backward, ssm_decode_step, ssm_forward)
 
 __version__ = "0.1.0"

@@ -1,5 +1,5 @@
 // Shared by the forward and the backward of the block norms (block_join.cu, block_join_bwd.cu):
-// vectors of a row, sums over its threads, the ring of rows copied ahead, and the launch shapes.
+// sums over a row's threads, the ring of rows copied ahead, and the launch shapes.
 #pragma once
 
 #include <type_traits>
@@ -14,75 +14,6 @@ namespace {
 
 constexpr int kMaxD = 8192;
 constexpr int kSmallThreads = 256;  // CTA size of the sub-warp mapping
-
-template <typename T, int VEC>
-struct Vec;
-template <typename T>
-struct Vec<T, 1> {
-    T v;
-};
-template <>
-struct Vec<bf16, 2> {
-    uint32_t v;
-};
-template <>
-struct Vec<bf16, 8> {
-    uint4 v;
-};
-template <>
-struct Vec<float, 4> {
-    float4 v;
-};
-
-// A thread's values in float32, as VEC / 2 pairs; single elements stay floats.
-// VEC values as N of P
-template <int VEC>
-struct Lanes {
-    using P = F2;
-    static constexpr int N = VEC / 2;
-    static __device__ __forceinline__ P all(float f) { return pair(f, f); }
-};
-template <>
-struct Lanes<1> {
-    using P = float;
-    static constexpr int N = 1;
-    static __device__ __forceinline__ P all(float f) { return f; }
-};
-
-template <typename T>
-__device__ __forceinline__ void unpack(const Vec<T, 1>& a, float (&f)[1]) { f[0] = to_f32(a.v); }
-__device__ __forceinline__ F2 unpack2(uint32_t u) { return pair(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)); }
-__device__ __forceinline__ void unpack(const Vec<bf16, 2>& a, F2 (&f)[1]) { f[0] = unpack2(a.v); }
-__device__ __forceinline__ void unpack(const Vec<bf16, 8>& a, F2 (&f)[4]) {
-    f[0] = unpack2(a.v.x), f[1] = unpack2(a.v.y), f[2] = unpack2(a.v.z), f[3] = unpack2(a.v.w);
-}
-__device__ __forceinline__ void unpack(const Vec<float, 4>& a, F2 (&f)[2]) {
-    f[0] = pair(a.v.x, a.v.y), f[1] = pair(a.v.z, a.v.w);
-}
-template <typename T>
-__device__ __forceinline__ void pack(Vec<T, 1>& a, const float (&f)[1]) { a.v = from_f32<T>(f[0]); }
-__device__ __forceinline__ uint32_t pack2(F2 a) {
-    float lo, hi;
-    split(a, lo, hi);
-    return pack_bf16x2(lo, hi);
-}
-__device__ __forceinline__ void pack(Vec<bf16, 2>& a, const F2 (&f)[1]) { a.v = pack2(f[0]); }
-__device__ __forceinline__ void pack(Vec<bf16, 8>& a, const F2 (&f)[4]) {
-    a.v = make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
-}
-__device__ __forceinline__ void pack(Vec<float, 4>& a, const F2 (&f)[2]) {
-    split(f[0], a.v.x, a.v.y);
-    split(f[1], a.v.z, a.v.w);
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ Vec<T, VEC> ldvec(const T* p) { return *reinterpret_cast<const Vec<T, VEC>*>(p); }
-template <typename T, int VEC, typename P, int N>
-__device__ __forceinline__ void stvec(T* p, const P (&f)[N]) {
-    Vec<T, VEC> a;
-    pack(a, f);
-    *reinterpret_cast<Vec<T, VEC>*>(p) = a;
-}
 
 // Sums of N values over the threads of a row: TPR lanes of a warp, or the CTA (TPR == 0, or > 32: of that
 // many threads).
@@ -120,24 +51,6 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[16][N], int&
         v[0] = __shfl_sync(0xffffffffu, mine, 0);
         v[1] = __shfl_sync(0xffffffffu, mine, 16);
     }
-}
-
-// act(z), and act'(z) into slope: with s = sigmoid(z) and t = 1 - s, act = p s and act' = s (t p + e),
-// where p = z, e = 1 for the SiLU and p = 1, e = 0 for the sigmoid
-__device__ __forceinline__ float gate_of(float z, bool silu, float& slope) {
-    const float s = fast_rcp(1.f + fast_exp(-z)), t = 1.f - s, p = silu ? z : 1.f;
-    slope = s * fmaf(t, p, silu ? 1.f : 0.f);
-    return p * s;
-}
-__device__ __forceinline__ F2 gate_of(F2 z, bool silu, F2& slope) {
-    float lo, hi;
-    const F2 one = pair(1.f, 1.f);
-    split(z * pair(-1.4426950408889634f, -1.4426950408889634f), lo, hi);
-    split(fma_(pair(fast_exp2(lo), fast_exp2(hi)), one, one), lo, hi);
-    const F2 s = pair(fast_rcp(lo), fast_rcp(hi)), t = fma_(s, pair(-1.f, -1.f), one);
-    const F2 p = silu ? z : one;
-    slope = s * fma_(t, p, silu ? one : pair(0.f, 0.f));
-    return p * s;
 }
 
 // What a call has: no block output (the norm alone); a block output with a gate for each value, a

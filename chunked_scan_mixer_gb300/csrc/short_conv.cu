@@ -1,0 +1,532 @@
+// The short causal convolution of each channel with W = 2, 3 or 4 taps, forward, backward and single tokens, and its C ABI
+// (include/hla2.h, hla2_short_conv_*):
+//   p_t = bias + sum_j w_j x_{t - W + 1 + j},  y_t = act(p_t)
+//   dp = dy act'(p),  dx_s = sum_j w_j dp_{s + W - 1 - j},  dw_j = sum_t dp_t x_{t - W + 1 + j},  dbias = sum_t dp_t.
+//
+// Bytes bound all of them: x read and y written once, x and dy read and dx written in the backward, which forms p again.
+// A thread has one vector of channels and walks over a run of tokens with the last W - 1 inputs (and dp's) in registers,
+// several tokens' loads ahead; the runs' edges are read twice.  The backward's sums of a thread go through shared memory to
+// one partial row a CTA, which a second kernel adds in a fixed order.
+#include <type_traits>
+
+#include "packed.cuh"
+#include "rows.h"
+
+namespace hla2 {
+namespace {
+
+struct ConvPass {
+    int B, n, D, W, silu;
+    int cols, run, runs;  // vectors of a row, tokens of a run, runs of a sequence
+    long long x_sb, x_sn, o_sb, o_sn, g_sb, g_sn;
+    const void *x, *weight, *bias, *init;
+    const int* lengths;
+    void* out;    // y, or dx
+    void* fin;    // the state after the last token, or the gradient of the one before the first
+    const void *dout, *dfinal;
+    float* partial;  // [rows][D][W + 1]
+};
+
+constexpr int kAhead = 8;  // tokens in flight
+
+__device__ __forceinline__ int length_of(const int* lengths, int b, int n) {
+    return lengths ? max(0, min(__ldg(lengths + b), n)) : n;
+}
+
+// weights of VEC channels as N of P for each tap
+template <typename T, int VEC, int W, typename P, int N>
+__device__ __forceinline__ void load_taps(const T* w, P (&taps)[W][N]) {
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (VEC == 1) taps[j][i] = to_f32(w[j]);
+            else taps[j][i] = pair(to_f32(w[(2 * i) * W + j]), to_f32(w[(2 * i + 1) * W + j]));
+        }
+}
+
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(128) conv_kernel(const ConvPass a) {
+    using L = Lanes<VEC>;
+    using P = typename L::P;
+    constexpr int N = L::N;
+    pdl_wait();
+    const long long i0 = (long long)blockIdx.x * 128 + threadIdx.x, i1 = i0 / a.cols;
+    const int c = (int)(i0 - i1 * a.cols) * VEC, b = (int)(i1 / a.runs), run = (int)(i1 - (long long)b * a.runs);
+    if (b >= a.B) return;
+    const int len = length_of(a.lengths, b, a.n);
+    const int t0 = run * a.run, t1 = min(t0 + a.run, a.n);
+    const T* x = static_cast<const T*>(a.x) + b * a.x_sb + c;
+    T* out = static_cast<T*>(a.out) + b * a.o_sb + c;
+    const T* init = a.init ? static_cast<const T*>(a.init) + (long long)b * (W - 1) * a.D + c : nullptr;
+    auto input = [&](int t) {  // at a token that may be before the first, as the state has it
+        Vec<T, VEC> v{};
+        if (t >= 0) v = ldvec<T, VEC>(x + t * a.x_sn);
+        else if (init) v = ldvec<T, VEC>(init + (long long)(t + W - 1) * a.D);
+        return v;
+    };
+    P taps[W][N], bias[N], win[W][N];
+    load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
+#pragma unroll
+    for (int i = 0; i < N; ++i) bias[i] = L::all(0.f);
+    if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), bias);
+    if (t0 < len) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) unpack(input(t0 - (W - 1) + j), win[j + 1]);
+    }
+    for (int t = t0; t < t1; t += kAhead) {
+        Vec<T, VEC> v[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (t + u < min(len, t1)) v[u] = ldvec<T, VEC>(x + (t + u) * a.x_sn);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (t + u >= t1) break;
+            P y[N];
+            if (t + u < len) {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) win[j][i] = win[j + 1][i];
+                unpack(v[u], win[W - 1]);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    y[i] = bias[i];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) y[i] = fma_(taps[j][i], win[j][i], y[i]);
+                    P slope;
+                    if (a.silu) y[i] = gate_of(y[i], true, slope);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) y[i] = L::all(0.f);
+            }
+            stvec<T, VEC>(out + (t + u) * a.o_sn, y);
+        }
+    }
+    pdl_trigger();
+    if (run == 0 && a.fin) {
+        T* fin = static_cast<T*>(a.fin) + (long long)b * (W - 1) * a.D + c;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            *reinterpret_cast<Vec<T, VEC>*>(fin + (long long)j * a.D) = input(len - (W - 1) + j);
+    }
+}
+
+// Eight runs a CTA, 32 vectors of channels
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(256) conv_backward_kernel(const ConvPass a) {
+    using L = Lanes<VEC>;
+    using P = typename L::P;
+    constexpr int N = L::N;
+    __shared__ float sums[8][32 * VEC + 1];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = (blockIdx.x * 32 + lane) * VEC;
+    const int per_b = (a.runs + 7) / 8, b = blockIdx.y / per_b, run = (blockIdx.y - b * per_b) * 8 + w;
+    const bool on = c < a.D && run < a.runs;
+    P taps[W][N], bias[N], dw[W][N], db[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        bias[i] = db[i] = L::all(0.f);
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][i] = L::all(0.f);
+    }
+    if (on) {
+        const int len = length_of(a.lengths, b, a.n), t0 = run * a.run, t1 = min(t0 + a.run, a.n);
+        const T *x = static_cast<const T*>(a.x) + b * a.x_sb + c, *dout = static_cast<const T*>(a.dout) + b * a.g_sb + c;
+        T* dx = static_cast<T*>(a.out) + b * a.o_sb + c;
+        const long long at = (long long)b * (W - 1) * a.D + c;
+        const T *init = a.init ? static_cast<const T*>(a.init) + at : nullptr,
+                *dfin = a.dfinal ? static_cast<const T*>(a.dfinal) + at : nullptr;
+        T* dinit = a.fin ? static_cast<T*>(a.fin) + at : nullptr;
+        load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
+        if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), bias);
+        P win[W][N], dp[W][N];  // inputs up to t, and dp from s = t - W + 1 to t
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) win[j][i] = dp[j][i] = L::all(0.f);
+        if (t0 < len) {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                const int t = t0 - (W - 1) + j;
+                if (t >= 0) unpack(ldvec<T, VEC>(x + t * a.x_sn), win[j + 1]);
+                else if (init) unpack(ldvec<T, VEC>(init + (long long)(t + W - 1) * a.D), win[j + 1]);
+            }
+        }
+        const int first = run == 0 ? -(W - 1) : t0, last = t1 + W - 1;  // s from first to t1
+        const int live = min(len, last);
+        constexpr int U = kAhead / 2;
+        for (int t = t0; t < last; t += U) {
+            Vec<T, VEC> vx[U], vg[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (t + u < live) vx[u] = ldvec<T, VEC>(x + (t + u) * a.x_sn), vg[u] = ldvec<T, VEC>(dout + (t + u) * a.g_sn);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t + u >= last) break;
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) win[j][i] = win[j + 1][i], dp[j][i] = dp[j + 1][i];
+                if (t + u < live) {
+                    P g[N];
+                    unpack(vx[u], win[W - 1]);
+                    unpack(vg[u], g);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        P p = bias[i], slope = L::all(1.f);
+                        if (a.silu) {
+#pragma unroll
+                            for (int j = 0; j < W; ++j) p = fma_(taps[j][i], win[j][i], p);
+                            gate_of(p, true, slope);
+                        }
+                        dp[W - 1][i] = g[i] * slope;
+                        if (t + u < t1) {
+                            db[i] = fma_(dp[W - 1][i], L::all(1.f), db[i]);
+#pragma unroll
+                            for (int j = 0; j < W; ++j) dw[j][i] = fma_(dp[W - 1][i], win[j][i], dw[j][i]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) win[W - 1][i] = dp[W - 1][i] = L::all(0.f);
+                }
+                const int s = t + u - (W - 1);
+                if (s < first) continue;
+                P o[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) o[i] = L::all(0.f);
+                if (s < len) {
+                    const int k = s - (len - (W - 1));  // its place in the state after the last token
+                    if (dfin && k >= 0) unpack(ldvec<T, VEC>(dfin + (long long)k * a.D), o);
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+#pragma unroll
+                        for (int j = 0; j < W; ++j) o[i] = fma_(taps[j][i], dp[W - 1 - j][i], o[i]);
+                }
+                if (s >= 0) stvec<T, VEC>(dx + s * a.o_sn, o);
+                else if (dinit) stvec<T, VEC>(dinit + (long long)(s + W - 1) * a.D, o);
+            }
+        }
+    }
+    pdl_trigger();
+    // the eight runs' sums, one tap after another
+    float* dst = a.partial + (long long)blockIdx.y * a.D * (W + 1);
+#pragma unroll
+    for (int j = 0; j <= W; ++j) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const P v = j < W ? dw[j < W ? j : 0][i / 2 * (VEC > 1)] : db[i / 2 * (VEC > 1)];
+            float f;
+            if constexpr (VEC == 1) {
+                f = v;
+            } else {
+                float lo, hi;
+                split(v, lo, hi);
+                f = i % 2 ? hi : lo;
+            }
+            sums[w][i * 32 + lane] = f;
+        }
+        __syncthreads();
+        for (int k = threadIdx.x; k < 32 * VEC; k += 256) {
+            float s = 0.f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) s += sums[r][k];
+            const int ch = (blockIdx.x * 32 + k % 32) * VEC + k / 32;
+            if (ch < a.D) dst[(long long)j * a.D + ch] = s;
+        }
+        __syncthreads();
+    }
+}
+
+// dweight [D, W] and dbias [D]: the partial rows [W + 1][D], 32 columns a CTA with 16 row lanes
+__global__ void __launch_bounds__(512) conv_sums_kernel(const ConvPass a, int rows, float* __restrict__ dweight, float* __restrict__ dbias) {
+    __shared__ float sm[16][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const long long cols = (long long)a.D * (a.W + 1), c = (long long)blockIdx.x * 32 + lane;
+    pdl_wait();
+    float s = 0.f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int r = w; r < rows; r += 16) s += a.partial[r * cols + c];
+    }
+    sm[w][lane] = s;
+    __syncthreads();
+    for (int o = 8; o; o >>= 1) {
+        if (w < o) sm[w][lane] += sm[w + o][lane];
+        __syncthreads();
+    }
+    if (w || c >= cols) return;
+    const int j = (int)(c / a.D), d = (int)(c - (long long)j * a.D);
+    if (j < a.W) dweight[(long long)d * a.W + j] = sm[0][lane];
+    else if (dbias) dbias[d] = sm[0][lane];
+}
+
+// One token: the state moves up by one
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(128) conv_step_kernel(const ConvPass a, T* __restrict__ state) {
+    using L = Lanes<VEC>;
+    using P = typename L::P;
+    constexpr int N = L::N;
+    pdl_trigger();
+    pdl_wait();
+    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
+    const int b = (int)(i / a.cols), c = (int)(i - (long long)b * a.cols) * VEC;
+    if (b >= a.B) return;
+    T* st = state + (long long)b * (W - 1) * a.D + c;
+    Vec<T, VEC> v[W];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) v[j] = ldvec<T, VEC>(st + (long long)j * a.D);
+    v[W - 1] = ldvec<T, VEC>(static_cast<const T*>(a.x) + b * a.x_sb + c);
+    P taps[W][N], y[N];
+    load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
+#pragma unroll
+    for (int k = 0; k < N; ++k) y[k] = L::all(0.f);
+    if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), y);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        P x[N];
+        unpack(v[j], x);
+#pragma unroll
+        for (int k = 0; k < N; ++k) y[k] = fma_(taps[j][k], x[k], y[k]);
+        if (j > 0) *reinterpret_cast<Vec<T, VEC>*>(st + (long long)(j - 1) * a.D) = v[j];
+    }
+    P slope;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (a.silu) y[k] = gate_of(y[k], true, slope);
+    stvec<T, VEC>(static_cast<T*>(a.out) + b * a.o_sb + c, y);
+}
+
+// ---- launch ----------------------------------------------------------------------------------
+
+// f(zero of the type, VEC, W) as integral constants; `wide` elements a vector where the tensors allow it
+template <int V> using Int = std::integral_constant<int, V>;
+template <int BF_VEC, class F>
+int with_conv(int dtype, bool vec, int W, F&& f) {
+    auto taps = [&](auto zero, auto v) {
+        switch (W) {
+            case 2: return f(zero, v, Int<2>{});
+            case 3: return f(zero, v, Int<3>{});
+            default: return f(zero, v, Int<4>{});
+        }
+    };
+    if (dtype == HLA2_BF16) return vec ? taps(bf16{}, Int<BF_VEC>{}) : taps(bf16{}, Int<1>{});
+    return vec ? taps(0.f, Int<4>{}) : taps(0.f, Int<1>{});
+}
+
+int check_conv(const char* fn, const hla2_conv_args* a) {
+    if (!a) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: args must not be NULL", fn);
+    if (a->dtype != HLA2_F32 && a->dtype != HLA2_BF16)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dtype must be HLA2_F32 or HLA2_BF16", fn);
+    if (a->B < 0 || a->n < 0 || a->D < 0)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: B, n and D must not be negative", fn);
+    if (a->W < 2 || a->W > 4) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: W must be 2, 3 or 4 (got %d)", fn, a->W);
+    if (a->silu != 0 && a->silu != 1) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: silu must be 0 or 1", fn);
+    if ((long long)a->B * a->D > 0x7fffffffLL || a->n > 1 << 30)
+        return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: B * D must fit in 31 bits, and n be at most 2^30", fn);
+    return HLA2_OK;
+}
+
+// Tokens of a run: as many as leave `threads` threads an SM, 8 to 64
+int run_of(const hla2_conv_args* a, int vec, int threads) {
+    const long long all = (long long)a->B * ((a->D + vec - 1) / vec) * a->n, want = (long long)threads * sm_count();
+    const long long run = (all / want + kAhead - 1) / kAhead * kAhead;
+    return run < kAhead ? kAhead : run > 64 ? 64 : (int)run;
+}
+// of the backward, whose grid has a row for eight runs
+int backward_run(const hla2_conv_args* a) {
+    int run = run_of(a, 4, 768);
+    while ((long long)a->B * ((a->n + 8LL * run - 1) / (8LL * run)) > 65535) run *= 2;
+    return run;
+}
+int backward_rows(const hla2_conv_args* a) {
+    const int run = backward_run(a), runs = (int)(((long long)a->n + run - 1) / run);
+    return a->B * ((runs + 7) / 8);
+}
+
+struct ConvInputs {
+    Extent read[7];
+    int reads = 0;
+    bool vec = true;
+    int es;
+    explicit ConvInputs(const hla2_conv_args* a) : es(elem_size(a->dtype)) {}
+    // a contiguous tensor; `wide`: vectors of it are read
+    void add(const void* p, size_t elems, int D, bool wide) {
+        read[reads++] = extent_of(p, elems * es);
+        if (wide && p) vec = vec && al(p, 16) && D % (16 / es) == 0;
+    }
+    bool meets(const Extent& e) const {
+        for (int i = 0; i < reads; ++i)
+            if (meet(e, read[i])) return true;
+        return false;
+    }
+    int rows(const char* fn, const Tensor& t, bool written) {
+        if (int rc = check_tensor(fn, t, es, written)) return rc;
+        vec = vec && t.vec(16 / es, es);
+        if (!written) read[reads++] = t.extent(es);
+        return HLA2_OK;
+    }
+    int params(const char* fn, const hla2_conv_args* a) {
+        if (!a->weight) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: weight must not be NULL", fn);
+        if (!al(a->weight, es) || !al(a->bias, es) || !al(a->init_state, es) || !al(a->lengths, 4))
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
+        add(a->weight, (size_t)a->D * a->W, a->D, false);
+        add(a->bias, a->D, a->D, true);
+        add(a->init_state, (size_t)a->B * (a->W - 1) * a->D, a->D, true);
+        read[reads++] = extent_of(a->lengths, (size_t)a->B * sizeof(int));
+        return HLA2_OK;
+    }
+};
+
+ConvPass base_pass(const hla2_conv_args* a) {
+    ConvPass p{};
+    p.B = a->B, p.n = a->n, p.D = a->D, p.W = a->W, p.silu = a->silu;
+    p.x = a->x.p, p.weight = a->weight, p.bias = a->bias, p.init = a->init_state;
+    p.x_sb = a->x.sb, p.x_sn = a->x.sn;
+    p.lengths = a->lengths;
+    return p;
+}
+
+}  // namespace
+}  // namespace hla2
+
+using namespace hla2;
+
+extern "C" {
+
+int hla2_short_conv_forward(const hla2_conv_args* a, hla2_rows out, void* final_state, hla2_stream_t stream) {
+    static const char* const fn = "hla2_short_conv_forward";
+    Range range(fn);
+    if (int rc = check_conv(fn, a)) return rc;
+    if (a->B == 0 || a->D == 0) return ok();
+    ConvInputs in(a);
+    if (int rc = in.params(fn, a)) return rc;
+    const Tensor o = rows("out", out, a->B, a->n, a->D);
+    const Extent fin = extent_of(final_state, (size_t)a->B * (a->W - 1) * a->D * in.es);
+    if (!al(final_state, in.es)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
+    if (final_state) in.vec = in.vec && al(final_state, 16);
+    if (a->n > 0) {
+        if (int rc = in.rows(fn, rows("x", a->x, a->B, a->n, a->D), false)) return rc;
+        if (int rc = in.rows(fn, o, true)) return rc;
+        if (in.meets(o.extent(in.es)) || meet(o.extent(in.es), fin))
+            return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps another tensor", fn);
+    } else if (!final_state) {
+        return ok();
+    }
+    if (in.meets(fin)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: final_state overlaps an input", fn);
+    ConvPass p = base_pass(a);
+    p.out = const_cast<void*>(out.p), p.o_sb = out.sb, p.o_sn = out.sn;
+    p.fin = final_state;
+    const int v = in.vec ? 16 / in.es : 1;
+    p.run = run_of(a, v, 2048);
+    p.runs = a->n > 0 ? (int)(((long long)a->n + p.run - 1) / p.run) : 1;
+    p.cols = (a->D + v - 1) / v;
+    const long long threads = (long long)p.cols * p.runs * a->B;
+    if ((threads + 127) / 128 > 0x7fffffffLL) return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: too many values", fn);
+    const int rc = with_conv<8>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
+        using T = decltype(zero);
+        return launch_pdl(conv_kernel<T, decltype(vec)::value, decltype(taps)::value>, dim3((unsigned)((threads + 127) / 128)),
+                          dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), p) == cudaSuccess ? 0 : -1;
+    });
+    return rc ? launch_failed("short convolution") : ok();
+}
+
+size_t hla2_short_conv_backward_workspace_bytes(const hla2_conv_args* a) {
+    if (check_conv("hla2_short_conv_backward_workspace_bytes", a) != HLA2_OK) return (size_t)-1;
+    ok();
+    return (size_t)backward_rows(a) * a->D * (a->W + 1) * sizeof(float);
+}
+
+int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void* dfinal_state, hla2_rows dx, float* dweight,
+                             float* dbias, void* dinit_state, hla2_stream_t stream) {
+    static const char* const fn = "hla2_short_conv_backward";
+    Range range(fn);
+    if (int rc = check_conv(fn, a)) return rc;
+    if (a->D == 0) return ok();
+    ConvInputs in(a);
+    if (int rc = in.params(fn, a)) return rc;
+    const size_t state = (size_t)a->B * (a->W - 1) * a->D;
+    if (!al(dfinal_state, in.es) || !al(dinit_state, in.es) || !al(dweight, 4) || !al(dbias, 4))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
+    if (!dweight || (a->bias != nullptr) != (dbias != nullptr))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dweight is needed, dbias with bias, and only then", fn);
+    in.add(dfinal_state, state, a->D, true);
+    if (dinit_state) in.vec = in.vec && al(dinit_state, 16) && a->D % (16 / in.es) == 0;
+    Extent written[4] = {extent_of(dweight, (size_t)a->D * a->W * sizeof(float)), extent_of(dbias, (size_t)a->D * sizeof(float)),
+                         extent_of(dinit_state, state * in.es), {0, 0}};
+    if (a->n > 0 && a->B > 0) {
+        if (int rc = in.rows(fn, rows("x", a->x, a->B, a->n, a->D), false)) return rc;
+        if (int rc = in.rows(fn, rows("dout", dout, a->B, a->n, a->D), false)) return rc;
+        const Tensor o = rows("dx", dx, a->B, a->n, a->D);
+        if (int rc = in.rows(fn, o, true)) return rc;
+        written[3] = o.extent(in.es);
+    }
+    for (int i = 0; i < 4; ++i) {
+        if (in.meets(written[i])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps an input", fn);
+        for (int j = 0; j < i; ++j)
+            if (meet(written[i], written[j])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: gradients overlap", fn);
+    }
+    const size_t need = hla2_short_conv_backward_workspace_bytes(a);
+    if (need > 0 && (!a->workspace || a->workspace_bytes < need || !al(a->workspace, 16)))
+        return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, need);
+    ConvPass p = base_pass(a);
+    p.out = const_cast<void*>(dx.p), p.o_sb = dx.sb, p.o_sn = dx.sn;
+    p.dout = dout.p, p.g_sb = dout.sb, p.g_sn = dout.sn;
+    p.fin = dinit_state, p.dfinal = dfinal_state;
+    p.partial = static_cast<float*>(a->workspace);
+    p.run = backward_run(a);
+    p.runs = (int)(((long long)a->n + p.run - 1) / p.run);
+    const int grid_rows = backward_rows(a);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    int rc = 0;
+    if (grid_rows > 0)
+        rc = with_conv<4>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
+            using T = decltype(zero);
+            constexpr int V = decltype(vec)::value;
+            return launch_pdl(conv_backward_kernel<T, V, decltype(taps)::value>, dim3((a->D + 32 * V - 1) / (32 * V), grid_rows),
+                              dim3(256), 0, st, p) == cudaSuccess ? 0 : -1;
+        });
+    else if (dinit_state && a->B > 0)  // no tokens: the state after the last is the one before the first
+        rc = (dfinal_state ? cudaMemcpyAsync(dinit_state, dfinal_state, state * in.es, cudaMemcpyDeviceToDevice, st)
+                           : cudaMemsetAsync(dinit_state, 0, state * in.es, st)) == cudaSuccess ? 0 : -1;
+    const long long cols = (long long)a->D * (a->W + 1);
+    if (rc == 0)
+        rc = launch_pdl(conv_sums_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(512), 0, st, p, grid_rows, dweight, dbias) == cudaSuccess
+                 ? 0 : -1;
+    return rc ? launch_failed("short convolution gradients") : ok();
+}
+
+int hla2_short_conv_decode_step(const hla2_conv_args* a, void* state, hla2_rows out, hla2_stream_t stream) {
+    static const char* const fn = "hla2_short_conv_decode_step";
+    Range range(fn);
+    if (int rc = check_conv(fn, a)) return rc;
+    if (a->B == 0 || a->D == 0) return ok();
+    if (a->lengths || a->init_state)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: lengths and init_state must be NULL", fn);
+    ConvInputs in(a);
+    if (int rc = in.params(fn, a)) return rc;
+    if (int rc = in.rows(fn, rows("x", a->x, a->B, 1, a->D), false)) return rc;
+    const Tensor o = rows("out", out, a->B, 1, a->D);
+    if (int rc = in.rows(fn, o, true)) return rc;
+    if (!state || !al(state, in.es))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: the state must be an address aligned to its type", fn);
+    in.vec = in.vec && al(state, 16);
+    const Extent est = extent_of(state, (size_t)a->B * (a->W - 1) * a->D * in.es), eo = o.extent(in.es);
+    if (meet(eo, est) || in.meets(eo) || in.meets(est))
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out or the state overlaps another tensor", fn);
+    ConvPass p = base_pass(a);
+    p.out = const_cast<void*>(out.p), p.o_sb = out.sb;
+    const int v = in.vec ? 16 / in.es : 1;
+    p.cols = (a->D + v - 1) / v;
+    const long long threads = (long long)p.cols * a->B;
+    const int rc = with_conv<8>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
+        using T = decltype(zero);
+        return launch_pdl(conv_step_kernel<T, decltype(vec)::value, decltype(taps)::value>, dim3((unsigned)((threads + 127) / 128)),
+                          dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), p, static_cast<T*>(state)) == cudaSuccess ? 0 : -1;
+    });
+    return rc ? launch_failed("short convolution step") : ok();
+}
+
+}  // extern "C"

@@ -177,6 +177,20 @@ def lib():
         L.hla2_ssm_backward.restype = I
         L.hla2_ssm_decode_step.argtypes = [P, P, Rows, P]
         L.hla2_ssm_decode_step.restype = I
+        L.hla2_short_conv_forward.argtypes = [P, Rows, P, P]
+        L.hla2_short_conv_forward.restype = I
+        L.hla2_short_conv_backward_workspace_bytes.argtypes = [P]
+        L.hla2_short_conv_backward_workspace_bytes.restype = Z
+        L.hla2_short_conv_backward.argtypes = [P, Rows, P, Rows, P, P, P, P]
+        L.hla2_short_conv_backward.restype = I
+        L.hla2_short_conv_decode_step.argtypes = [P, P, Rows, P]
+        L.hla2_short_conv_decode_step.restype = I
+        L.hla2_layer_norm.argtypes = [P, P, P]
+        L.hla2_layer_norm.restype = I
+        L.hla2_layer_norm_backward_workspace_bytes.argtypes = [P]
+        L.hla2_layer_norm_backward_workspace_bytes.restype = Z
+        L.hla2_layer_norm_backward.argtypes = [P, P, P, P, P, P, Z, P]
+        L.hla2_layer_norm_backward.restype = I
         for name in ("hla2_state_to_compact", "hla2_state_from_compact"):
             getattr(L, name).argtypes = [P, P, I, I, I, I, P]
             getattr(L, name).restype = I
@@ -220,6 +234,8 @@ EXPORTED_SYMBOLS = (
     "hla2_linattn_workspace_bytes", "hla2_linattn_forward", "hla2_linattn_backward", "hla2_linattn_decode_step",
     "hla2_block_join", "hla2_block_join_backward_workspace_bytes", "hla2_block_join_backward", "hla2_w4_matvec",
     "hla2_ssm_workspace_bytes", "hla2_ssm_forward", "hla2_ssm_backward", "hla2_ssm_decode_step",
+    "hla2_short_conv_forward", "hla2_short_conv_backward_workspace_bytes", "hla2_short_conv_backward",
+    "hla2_short_conv_decode_step", "hla2_layer_norm", "hla2_layer_norm_backward_workspace_bytes", "hla2_layer_norm_backward",
 )
 
 FLAG_COMPACT_STATE = 4
@@ -1314,6 +1330,20 @@ def _length_tensor(lengths, B, n, device):
     return lengths
 
 
+def _run_on_scratch(fn, index, call, query):
+    """A library call on the cached scratch behind its status word, which belongs to other calls."""
+    stream = _raw_stream(index)
+    skip = _STATUS_BYTES
+
+    def padded():
+        nbytes = query()
+        return nbytes if nbytes in (0, _SIZE_MAX) else nbytes + skip
+
+    rc = _with_scratch(lambda p, nbytes: call(p and p + skip, max(nbytes - skip, 0), stream), padded, index, stream)
+    if rc:
+        _check(fn, rc)
+
+
 class _Ssm(NamedTuple):
     """One checked call: sizes, the fields of its argument block but for the workspace, and the tensors
     that they point into."""
@@ -1328,17 +1358,8 @@ class _Ssm(NamedTuple):
     keep: tuple
 
     def run(self, fn, backward, call):
-        stream = _raw_stream(self.index)
-        skip = _STATUS_BYTES  # the cached buffer's status word is other calls'
-
-        def query():
-            nbytes = lib().hla2_ssm_workspace_bytes(_SSM_ARGS.pack(*self.head, 0, 0), backward)
-            return nbytes if nbytes in (0, _SIZE_MAX) else nbytes + skip
-
-        rc = _with_scratch(lambda p, nbytes: call(_SSM_ARGS.pack(*self.head, p and p + skip, max(nbytes - skip, 0)), stream),
-                           query, self.index, stream)
-        if rc:
-            _check(fn, rc)
+        _run_on_scratch(fn, self.index, lambda p, nbytes, stream: call(_SSM_ARGS.pack(*self.head, p, nbytes), stream),
+                        lambda: lib().hla2_ssm_workspace_bytes(_SSM_ARGS.pack(*self.head, 0, 0), backward))
 
 
 def _ssm_args(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state):
@@ -1441,3 +1462,168 @@ def _ssm_decode_step(state, x, dt, a, b, c, skip, gate, dt_bias, dt_softplus):
     if rc:
         _check("hla2_ssm_decode_step", rc)
     return out
+
+
+_CONV_ARGS = struct.Struct("@6iP2q4PPN")   # hla2_conv_args
+_NORM_ARGS = struct.Struct("@iqifPqPP")    # hla2_norm_args
+CONV_ACTS = {"silu": 1, "none": 0, None: 0}
+
+
+class ShortConvGrads(NamedTuple):
+    """Gradients of short_conv_forward's inputs (None where the input was None); those of the weight and the bias are
+    float32."""
+    dx: torch.Tensor
+    dweight: torch.Tensor
+    dbias: Optional[torch.Tensor]
+    dinit_state: Optional[torch.Tensor]
+
+
+def _same_state(name, t, shape, like):
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be {shape} of x's type and device")
+    return t.contiguous()
+
+
+def _conv_args(x, weight, bias, act, lengths, init_state):
+    """(device index, the fields of the argument block but for the workspace, tensors that they point into)"""
+    index = _need_cuda(x, weight, bias)
+    if act not in CONV_ACTS:
+        raise ValueError("act must be 'silu' or 'none'")
+    if x.dim() != 3 or weight.dim() != 2 or weight.shape[0] != x.shape[2]:
+        raise ValueError("x must be [B, n, D] and weight [D, W]")
+    B, n, D = x.shape
+    W = weight.shape[1]
+    x, xr = _token_rows("x", x, x.shape)
+    weight = weight.contiguous()
+    bias = _vector("bias", bias, D)
+    lengths = _length_tensor(lengths, B, n, x.device)
+    init = _same_state("init_state", init_state, (B, W - 1, D), x)
+    head = (_DTYPES[x.dtype], B, n, D, W, CONV_ACTS[act], *xr, weight.data_ptr(), _addr(bias), _addr(lengths), _addr(init))
+    return index, head, (x, weight, bias, lengths, init)
+
+
+def short_conv_forward(x, weight, bias=None, act="silu", lengths=None, init_state=None, return_final_state=False):
+    """The short causal convolution of each channel, out_t = act(bias + sum_j weight[:, j] x_{t - W + 1 + j}).
+
+    x [B,n,D]; weight [D,W] with 2 to 4 taps, the last one the token's own; bias [D]; float32 or bfloat16 of one
+    type on the GPU; x may have any strides (a contiguous last dimension is read in place).  act "silu" or "none".  lengths:
+    None or B token counts; the rows past a sequence's length are padding, whatever they hold, and 0 in the
+    output.  init_state [B,W-1,D] of x's type: the inputs before token 0, oldest first (None: zeros).  Returns out [B,n,D] and
+    with ``return_final_state`` each sequence's last W-1 inputs, which short_conv_decode_step goes on from."""
+    return _short_conv_forward(x, weight, bias, act, lengths, init_state, return_final_state)
+
+
+@_on_its_device
+def _short_conv_forward(x, weight, bias, act, lengths, init_state, return_final_state):
+    index, head, keep = _conv_args(x, weight, bias, act, lengths, init_state)
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    B, _, D = x.shape
+    fin = torch.empty((B, weight.shape[1] - 1, D), dtype=x.dtype, device=x.device) if return_final_state else None
+    rc = lib().hla2_short_conv_forward(_CONV_ARGS.pack(*head, 0, 0), Rows(out.data_ptr(), *out.stride()[:2]), _addr(fin),
+                                       _raw_stream(index))
+    if rc:
+        _check("hla2_short_conv_forward", rc)
+    return (out, fin) if return_final_state else out
+
+
+def short_conv_backward(x, weight, dout, bias=None, act="silu", lengths=None, init_state=None, dfinal_state=None):
+    """ShortConvGrads of short_conv_forward for the upstream gradient dout [B,n,D] of its output and dfinal_state (None:
+    zero) of its final state.  Nothing is kept from the forward."""
+    return _short_conv_backward(x, weight, dout, bias, act, lengths, init_state, dfinal_state)
+
+
+@_on_its_device
+def _short_conv_backward(x, weight, dout, bias, act, lengths, init_state, dfinal_state):
+    index, head, keep = _conv_args(x, weight, bias, act, lengths, init_state)
+    _need_cuda(x, dout)
+    B, n, D = x.shape
+    W = weight.shape[1]
+    dout, do_rows = _token_rows("dout", dout, x.shape)
+    dfin = _same_state("dfinal_state", dfinal_state, (B, W - 1, D), x)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = torch.empty((D, W), dtype=torch.float32, device=x.device)
+    db = None if bias is None else torch.empty(D, dtype=torch.float32, device=x.device)
+    dinit = None if init_state is None else torch.empty((B, W - 1, D), dtype=x.dtype, device=x.device)
+    L = lib()
+    _run_on_scratch("hla2_short_conv_backward", index,
+                    lambda p, nbytes, stream: L.hla2_short_conv_backward(
+                        _CONV_ARGS.pack(*head, p, nbytes), Rows(*do_rows), _addr(dfin), Rows(dx.data_ptr(), n * D, D),
+                        dw.data_ptr(), _addr(db), _addr(dinit), stream),
+                    lambda: L.hla2_short_conv_backward_workspace_bytes(_CONV_ARGS.pack(*head, 0, 0)))
+    return ShortConvGrads(dx, dw, db, dinit)
+
+
+def short_conv_decode_step(state, x, weight, bias=None, act="silu"):
+    """One token of the short convolution for each of B sequences: ``state`` [B,W-1,D] of x's type on the GPU is updated
+    in place.  x [B,D]; the rest as short_conv_forward has it.  Returns out [B,D]."""
+    return _short_conv_decode_step(state, x, weight, bias, act)
+
+
+@_on_its_device
+def _short_conv_decode_step(state, x, weight, bias, act):
+    if x.dim() != 2:
+        raise ValueError("x must be [B, D]")
+    index, head, keep = _conv_args(x.unsqueeze(1), weight, bias, act, None, None)
+    B, D = x.shape
+    shape = (B, weight.shape[1] - 1, D)
+    if tuple(state.shape) != shape or state.dtype != x.dtype or state.device != x.device or not state.is_contiguous():
+        raise ValueError(f"state must be a contiguous {shape} tensor of x's type and device")
+    out = torch.empty((B, D), dtype=x.dtype, device=x.device)
+    rc = lib().hla2_short_conv_decode_step(_CONV_ARGS.pack(*head, 0, 0), state.data_ptr(), Rows(out.data_ptr(), D, 0),
+                                           _raw_stream(index))
+    if rc:
+        _check("hla2_short_conv_decode_step", rc)
+    return out
+
+
+def _norm_args(x, weight, bias, eps):
+    """(packed argument block, device index, tensors to keep)"""
+    index = _need_cuda(x, weight, bias)
+    D = x.shape[-1] if x.dim() else 0
+    w, b = _vector("weight", weight, D), _vector("bias", bias, D)
+    xr, rows, stride = _rows(x, D)
+    return _NORM_ARGS.pack(_DTYPES[x.dtype], rows, D, eps, xr.data_ptr(), stride, _addr(w), _addr(b)), index, (xr, w, b)
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5, out=None):
+    """Layer norm over the last dimension (1 to 8192 values; float32 or bfloat16 on the GPU): (x - mean) / sqrt(mean((x -
+    mean)^2) + eps) * weight + bias.  weight and bias [D] of x's type.  out may be x itself."""
+    return _layer_norm(x, weight, bias, eps, out)
+
+
+@_on_its_device
+def _layer_norm(x, weight, bias, eps, out):
+    args, index, keep = _norm_args(x, weight, bias, eps)
+    if out is None:
+        out = _contiguous_like(x)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of x's shape, type and device")
+    rc = lib().hla2_layer_norm(args, out.data_ptr(), _raw_stream(index))
+    if rc:
+        _check("hla2_layer_norm", rc)
+    return out
+
+
+def layer_norm_backward(x, weight, dout, eps=1e-5):
+    """(dx, dweight, dbias) of layer_norm; dweight and dbias are float32 sums over the rows.  They do not depend on the
+    bias, and nothing is kept from the forward."""
+    return _layer_norm_backward(x, weight, dout, eps)
+
+
+@_on_its_device
+def _layer_norm_backward(x, weight, dout, eps):
+    args, index, keep = _norm_args(x, weight, None, eps)
+    if dout.shape != x.shape or dout.dtype != x.dtype or dout.get_device() != index:
+        raise ValueError("dout must have x's shape, type and device")
+    dout = dout.contiguous()
+    dx = _contiguous_like(x)
+    sums = torch.empty((2, x.shape[-1]), dtype=torch.float32, device=x.device)
+    dw, db = sums[0], sums[1]
+    L = lib()
+    _run_on_scratch("hla2_layer_norm_backward", index,
+                    lambda p, nbytes, stream: L.hla2_layer_norm_backward(args, dout.data_ptr(), dx.data_ptr(), dw.data_ptr(),
+                                                                         db.data_ptr(), p, nbytes, stream),
+                    lambda: L.hla2_layer_norm_backward_workspace_bytes(args))
+    return dx, dw, db

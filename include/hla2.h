@@ -610,6 +610,71 @@ int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfina
  * tensor of the call. */
 int hla2_ssm_decode_step(const hla2_ssm_args* a, float* state, hla2_rows out, hla2_stream_t stream);
 
+/*
+ * The short causal convolution of each channel before such a scan, W = 2, 3 or 4 taps, the last one the token's own:
+ *
+ *   out_t = act(bias + sum_j weight[j] x_{t - W + 1 + j}),  act the SiLU or none
+ *
+ * lengths as above.  The state of a sequence is its last W - 1 inputs, oldest first, contiguous [B, W - 1, D] of
+ * the tensors' type (zeros before a first token).  Sums are float32.
+ */
+typedef struct {
+    int dtype;              /* HLA2_F32 | HLA2_BF16: every tensor but the sums of a backward */
+    int B, n, D, W;
+    int silu;               /* 0 or 1                                                         */
+    hla2_rows x;            /* [B, n, D]                                                      */
+    const void *weight, *bias; /* contiguous [D, W]; [D], nullable                            */
+    const int* lengths;     /* device int [B], or NULL                                        */
+    const void* init_state; /* nullable: the state before token 0                             */
+    void* workspace;        /* device scratch (backward only), 16-byte aligned                */
+    size_t workspace_bytes;
+} hla2_conv_args;
+
+/* out [B, n, D]; final_state (nullable) receives the state after each sequence's last token.  Neither may overlap another
+ * tensor of the call. */
+int hla2_short_conv_forward(const hla2_conv_args* a, hla2_rows out, void* final_state, hla2_stream_t stream);
+
+/* Scratch bytes of a backward; (size_t)-1 for arguments that it would reject. */
+size_t hla2_short_conv_backward_workspace_bytes(const hla2_conv_args* a);
+
+/* Gradients of sum(out * dout) + sum(final_state * dfinal_state): dx [B, n, D] and dinit_state (nullable) of the tensors' type;
+ * dweight [D, W] and dbias [D] (needed with bias, NULL without) float32 sums over sequences and tokens in a fixed order.  No
+ * gradient may overlap another tensor of the call. */
+int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void* dfinal_state, hla2_rows dx,
+                             float* dweight, float* dbias, void* dinit_state, hla2_stream_t stream);
+
+/* One token for each of B sequences: state [B, W - 1, D] is updated in place, out [B, D] written.  n, the token
+ * strides and the workspace are not looked at; lengths and init_state are NULL.  Neither out nor the state may overlap another
+ * tensor of the call. */
+int hla2_short_conv_decode_step(const hla2_conv_args* a, void* state, hla2_rows out, hla2_stream_t stream);
+
+/*
+ * Layer norm on rows of D values (1 <= D <= 8192): out = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * weight + bias.
+ * Statistics are float32, the squares summed about the mean.  Rows of x start every x_stride elements; out, dout and
+ * dx are contiguous [rows, D].  Every tensor but the sums has the type dtype; any alignment of an element.
+ */
+typedef struct {
+    int dtype;
+    long long rows;
+    int D;
+    float eps;
+    const void* x;      long long x_stride;
+    const void* weight; /* [D]           */
+    const void* bias;   /* [D], nullable */
+} hla2_norm_args;
+
+/* out may be exactly the rows of x (in place), and overlap nothing else. */
+int hla2_layer_norm(const hla2_norm_args* a, void* out, hla2_stream_t stream);
+
+/* Scratch bytes of hla2_layer_norm_backward; (size_t)-1 for arguments it would reject. */
+size_t hla2_layer_norm_backward_workspace_bytes(const hla2_norm_args* a);
+
+/* Gradients of sum(out * dout): dx [rows, D] of the type dtype; dweight and dbias (nullable) float32 [D], sums over the rows
+ * in a fixed order.  The bias is not read.  dx may be exactly the rows of x or of dout; else no output overlaps an input or
+ * another output. */
+int hla2_layer_norm_backward(const hla2_norm_args* a, const void* dout, void* dx, float* dweight, float* dbias,
+                             void* workspace, size_t workspace_bytes, hla2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,16 +24,17 @@ def make_ssm(B, n, D, N, G=1, dtype=F32, gate=True, skip=True, bias=True, state=
     return c
 
 
-def close(got, want, what="", f32_tol=1e-4):
+def close(got, want, what="", f32_tol=1e-4, terms=0.0):
     """The arithmetic is float32: a state's error is at most the tokens that it remembers, a few hundred here, times the
     rounding of a decay, an input and a sum, 2^-21.5 together, so 1e-4 of the largest value; sums over channels and tokens
-    are of that kind.  An output in bfloat16 is rounded once: 2^-8 of the value."""
+    are of that kind.  An output in bfloat16 is rounded once: 2^-8 of the value.  ``terms``: the size of the terms of
+    outputs that are their difference, where it says more than that of the outputs."""
     g, want = f64(got), np.asarray(want)
     assert g.shape == want.shape, (what, g.shape, want.shape)
     if want.size == 0:
         return
     top = np.abs(want).max()
-    tol = f32_tol * top + 1e-30 + (2.0 ** -8 * np.abs(want) if got.dtype == BF else 0.0)
+    tol = f32_tol * np.maximum(top, terms) + 1e-30 + (2.0 ** -8 * np.abs(want) if got.dtype == BF else 0.0)
     bad = ~(np.abs(g - want) <= tol)
     assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {np.nanmax(np.abs(g - want)):.3g} of {top:.3g}, " \
                           f"first at {np.argwhere(bad)[0].tolist()}"
