@@ -13,13 +13,31 @@ namespace {
 template <typename T, int V, int N, bool SUMS>
 __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threads) ssm_kernel(const SsmPass p) {
     constexpr int SL = SsmShape<N>::lanes, NT = SsmShape<N>::threads, TT = SsmShape<N>::tokens, CT = kSsmChannels;
-    constexpr int VB = V > N ? N : V;
-    __shared__ __align__(16) float sd[TT][CT], su[TT][CT], sy[SUMS ? 1 : TT][CT], sb[TT][2 * N], sc[SUMS ? 1 : TT][2 * N],
+    using L = Lanes<V>;
+    using P = typename L::P;
+    using Sums = LaneRows<N>;
+    __shared__ __align__(16) float sd[TT][CT], su[TT][CT], sy[SUMS ? 1 : TT][Sums::token], sb[TT][2 * N], sc[SUMS ? 1 : TT][2 * N],
         sskip[CT], sbias[CT];
     const int tid = threadIdx.x, sl = tid % SL, cg = tid / SL;
     pdl_wait();
     const SsmPlace at(p);
     const int chans = at.cols - 4 * cg;  // of the thread's four, those that there are
+    const T *x = static_cast<const T*>(p.x.p) + at.b * p.x.sb + at.c0, *dt = static_cast<const T*>(p.dt.p) + at.b * p.dt.sb + at.c0,
+            *z = p.gate.p ? static_cast<const T*>(p.gate.p) + at.b * p.gate.sb + at.c0 : nullptr,
+            *b = static_cast<const T*>(p.b.p) + at.b * p.b.sb + at.group * p.b.sh,
+            *c = static_cast<const T*>(p.c.p) + at.b * p.c.sb + at.group * p.c.sh;
+    T* out = SUMS ? nullptr : static_cast<T*>(const_cast<void*>(p.out.p)) + at.b * p.out.sb + at.c0;
+    using Chan = Tile<T, V, TT, CT, NT>;
+    using Stat = Tile<T, V, TT, N, NT>;
+    Chan xn, dn, xc, zc;
+    Stat bn, cn;
+    auto fetch = [&](int t0) {
+        xn.load(x, p.x.sn, t0, at.live_end, at.cols);
+        dn.load(dt, p.dt.sn, t0, at.live_end, at.cols);
+        bn.load(b, p.b.sn, t0, at.live_end, N);
+        if (!SUMS) cn.load(c, p.c.sn, t0, at.live_end, N);
+    };
+    fetch(at.t0);
     for (int i = tid; i < CT; i += NT) {
         sskip[i] = p.skip && i < at.cols ? p.skip[at.c0 + i] : 0.f;
         sbias[i] = p.dt_bias && i < at.cols ? p.dt_bias[at.c0 + i] : 0.f;
@@ -30,56 +48,22 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
     h.zero();
     if (!SUMS) {
         if (p.init) h.load(p.init + ((long long)at.b * p.D + at.c0 + 4 * cg) * N + 4 * sl, N, chans);
-        for (int s = 0; s < at.seg; ++s) {
-            const long long slot = at.slot(p, s);
-            const SsmPair2 steps = ld4(p.steps + slot * CT + 4 * cg);
-            SsmState w;
-            w.get(p.sums + slot * (CT * N), NT);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                h.v[k][0] = fma_(ex2_(steps.lo * a.v[k][0]), h.v[k][0], w.v[k][0]);
-                h.v[k][1] = fma_(ex2_(steps.hi * a.v[k][1]), h.v[k][1], w.v[k][1]);
-            }
-        }
+        join_segments<N>(p, at, h, a, p.sums, cg, 0, at.seg, 1);
     }
-    const T *x = static_cast<const T*>(p.x.p) + at.b * p.x.sb + at.c0, *dt = static_cast<const T*>(p.dt.p) + at.b * p.dt.sb + at.c0,
-            *z = p.gate.p ? static_cast<const T*>(p.gate.p) + at.b * p.gate.sb + at.c0 : nullptr,
-            *b = static_cast<const T*>(p.b.p) + at.b * p.b.sb + at.group * p.b.sh,
-            *c = static_cast<const T*>(p.c.p) + at.b * p.c.sb + at.group * p.c.sh;
-    T* out = SUMS ? nullptr : static_cast<T*>(const_cast<void*>(p.out.p)) + at.b * p.out.sb + at.c0;
-    using Chan = Tile<T, V, TT, CT, NT>;
-    using Stat = Tile<T, VB, TT, N, NT>;
-    Chan xn, dn, xc, zc;
-    Stat bn, cn;
-    auto fetch = [&](int t0) {
-        xn.load(x, p.x.sn, t0, at.live_end, at.cols);
-        dn.load(dt, p.dt.sn, t0, at.live_end, at.cols);
-        bn.load(b, p.b.sn, t0, at.live_end, N);
-        if (!SUMS) cn.load(c, p.c.sn, t0, at.live_end, N);
-    };
     F2 sum01 = pair(0.f, 0.f), sum23 = sum01;
-    if (at.t0 < at.live_end) fetch(at.t0);
     __syncthreads();
     for (int t0 = at.t0; t0 < at.live_end; t0 += TT) {
         Chan::parts([&](int k, int r, int ch) {
-            const bool on = t0 + r < at.live_end && ch < at.cols;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float v = to_f32(dn.v[k].v[i]) + sbias[ch + i];
-                const float d = on ? p.softplus ? softplus_of(v) : v : 0.f;
-                sd[r][ch + i] = d;
-                su[r][ch + i] = d * to_f32(xn.v[k].v[i]);
-            }
+            stage<T, V, false>(xn.v[k], dn.v[k], xn.v[k], xn.v[k], false, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
+                               &sd[r][ch], &su[r][ch], nullptr);
         });
         Stat::parts([&](int k, int r, int s) {
-#pragma unroll
-            for (int i = 0; i < VB; ++i) {
-                const float fb = to_f32(bn.v[k].v[i]);
-                *reinterpret_cast<float2*>(&sb[r][2 * (s + i)]) = make_float2(fb, fb);
-                if (!SUMS) {
-                    const float fc = to_f32(cn.v[k].v[i]);
-                    *reinterpret_cast<float2*>(&sc[r][2 * (s + i)]) = make_float2(fc, fc);
-                }
+            P f[L::N];
+            unpack(bn.v[k], f);
+            put_twice<V>(&sb[r][2 * s], f);
+            if (!SUMS) {
+                unpack(cn.v[k], f);
+                put_twice<V>(&sc[r][2 * s], f);
             }
         });
         if (!SUMS) {
@@ -103,33 +87,32 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
                     const F2 bk = j ? bb.hi : bb.lo, ck = j ? cc.hi : cc.lo;
                     hk[0] = fma_(ex2_(d.lo * a.v[k + j][0]), hk[0], u.lo * bk);
                     hk[1] = fma_(ex2_(d.hi * a.v[k + j][1]), hk[1], u.hi * bk);
-                    if (!SUMS) y01 = fma_(hk[0], ck, y01), y23 = fma_(hk[1], ck, y23);
+                    if (!SUMS) y01 = k + j ? fma_(hk[0], ck, y01) : hk[0] * ck, y23 = k + j ? fma_(hk[1], ck, y23) : hk[1] * ck;
                 }
             }
-            if (SUMS) {
-                sum01 = sum01 + d.lo, sum23 = sum23 + d.hi;
-            } else {
-                float y[2];
-                state_sum<SL>(y01, y23, sl, y);
-                put_state_sum<SL>(sy[t], cg, sl, y);
-            }
+            if (SUMS) sum01 = sum01 + d.lo, sum23 = sum23 + d.hi;
+            else Sums::put(sy[t], cg, sl, y01, y23);
         }
         __syncthreads();
         if (!SUMS)
             Chan::parts([&](int k, int r, int ch) {
                 if (t0 + r >= at.t_end || ch >= at.cols) return;
-                Pack<T, V> o;
-                const bool on = t0 + r < at.live_end;
+                P y[L::N], fx[L::N], fs[L::N];
+                Sums::template get<V>(&sy[r][ch], y);
+                unpack(xc.v[k], fx);
+                get_values<V>(sskip + ch, fs);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float y = fmaf(sskip[ch + i], to_f32(xc.v[k].v[i]), sy[r][ch + i]);
-                    if (z) {
-                        const float g = to_f32(zc.v[k].v[i]);
-                        y *= g * sigmoid_of(g);
-                    }
-                    o.v[i] = from_f32<T>(on ? y : 0.f);
+                for (int i = 0; i < L::N; ++i) y[i] = fma_(fs[i], fx[i], y[i]);
+                if (z) {
+                    unpack(zc.v[k], fx);
+#pragma unroll
+                    for (int i = 0; i < L::N; ++i) y[i] = times_silu(y[i], fx[i]);
                 }
-                *reinterpret_cast<Pack<T, V>*>(out + (long long)(t0 + r) * p.out.sn + ch) = o;
+                if (t0 + r >= at.live_end) {
+#pragma unroll
+                    for (int i = 0; i < L::N; ++i) y[i] = L::all(0.f);
+                }
+                stvec<T, V>(out + (long long)(t0 + r) * p.out.sn + ch, y);
             });
     }
     pdl_trigger();
@@ -140,12 +123,13 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
         return;
     }
     // padding past the last staged token
-    Pack<T, V> zero;
-    clear(zero);
+    P zero[L::N];
+#pragma unroll
+    for (int i = 0; i < L::N; ++i) zero[i] = L::all(0.f);
     const int first = at.t0 + (at.live_end - at.t0 + TT - 1) / TT * TT;
     for (long long i = tid; i < (long long)(at.t_end - first) * (CT / V); i += NT) {
         const int t = first + (int)(i / (CT / V)), ch = (int)(i % (CT / V)) * V;
-        if (ch < at.cols) *reinterpret_cast<Pack<T, V>*>(out + (long long)t * p.out.sn + ch) = zero;
+        if (ch < at.cols) stvec<T, V>(out + (long long)t * p.out.sn + ch, zero);
     }
     if (p.fin && at.seg == p.nseg - 1) h.store(p.fin + ((long long)at.b * p.D + at.c0 + 4 * cg) * N + 4 * sl, N, chans);
 }
@@ -173,6 +157,18 @@ int forward_v(const SsmPass& p, cudaStream_t st) {
 //
 // A thread holds four states of J channels, N / 4 threads apart in a row of blockDim: the state is read and written once,
 // all J loads in flight together, and bounds the step.
+template <typename T, int V>
+__device__ __forceinline__ void four(const T* p, float (&f)[4]) {
+    if constexpr (V == 4) {
+        F2 a[2];
+        unpack(ldvec<T, 4>(p), a);
+        split(a[0], f[0], f[1]), split(a[1], f[2], f[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = to_f32(p[k]);
+    }
+}
+
 template <typename T, int V, int N, int J>
 __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmPass p, float* __restrict__ state) {
     constexpr int SL = N / 4, PC = 256 / SL;  // channels of one round of the CTA
@@ -196,20 +192,16 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmPass p, float* _
         const float delta = p.softplus ? softplus_of(v) : v, u = delta * xv;
         const float4 a = *reinterpret_cast<const float4*>(p.a + (long long)d * N + 4 * sl);
         const T *bp = b + s * p.b.sb + g * p.b.sh + 4 * sl, *cp = c + s * p.c.sb + g * p.c.sh + 4 * sl;
-        Pack<T, 4> bv, cv;
-        if (V > 1) {
-            bv = ld_pack<T, 4>(bp), cv = ld_pack<T, 4>(cp);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) bv.v[k] = bp[k], cv.v[k] = cp[k];
-        }
+        float bv[4], cv[4];
+        four<T, V>(bp, bv);
+        four<T, V>(cp, cv);
         const float e = delta * kLog2E;
-        h[j].x = fmaf(fast_exp2(e * a.x), h[j].x, u * to_f32(bv.v[0]));
-        h[j].y = fmaf(fast_exp2(e * a.y), h[j].y, u * to_f32(bv.v[1]));
-        h[j].z = fmaf(fast_exp2(e * a.z), h[j].z, u * to_f32(bv.v[2]));
-        h[j].w = fmaf(fast_exp2(e * a.w), h[j].w, u * to_f32(bv.v[3]));
+        h[j].x = fmaf(fast_exp2(e * a.x), h[j].x, u * bv[0]);
+        h[j].y = fmaf(fast_exp2(e * a.y), h[j].y, u * bv[1]);
+        h[j].z = fmaf(fast_exp2(e * a.z), h[j].z, u * bv[2]);
+        h[j].w = fmaf(fast_exp2(e * a.w), h[j].w, u * bv[3]);
         __stcs(reinterpret_cast<float4*>(state + i * N + 4 * sl), h[j]);
-        float y = fmaf(h[j].x, to_f32(cv.v[0]), h[j].y * to_f32(cv.v[1])) + fmaf(h[j].z, to_f32(cv.v[2]), h[j].w * to_f32(cv.v[3]));
+        float y = fmaf(h[j].x, cv[0], h[j].y * cv[1]) + fmaf(h[j].z, cv[2], h[j].w * cv[3]);
         const unsigned lanes = (SL == 32 ? 0xffffffffu : (1u << SL) - 1) << (threadIdx.x & 31 & ~(SL - 1));
 #pragma unroll
         for (int m = 1; m < SL; m <<= 1) y += __shfl_xor_sync(lanes, y, m);
@@ -248,7 +240,7 @@ int step_v(const SsmPass& p, float* state, cudaStream_t st) {
 }  // namespace
 
 int launch_ssm_forward(const SsmPass& p, bool is_bf16, bool vec, cudaStream_t st) {
-    if (is_bf16) return vec ? forward_v<bf16, 8>(p, st) : forward_v<bf16, 1>(p, st);
+    if (is_bf16) return vec ? forward_v<bf16, 4>(p, st) : forward_v<bf16, 1>(p, st);
     return vec ? forward_v<float, 4>(p, st) : forward_v<float, 1>(p, st);
 }
 

@@ -85,53 +85,86 @@ __device__ __forceinline__ F2 ex2_(F2 a) {
 
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// e^-|x| to about 2^-22 relative: x log2 e in two parts, as its rounding alone would cost |x| 2^-24
-__device__ __forceinline__ float exp_neg_abs(float x) {
-    const float m = -fabsf(x), t = m * kLog2E;
-    if (!(t > -126.f)) return x != x ? x : 0.f;
-    const float lo = fmaf(m, 1.925963033500e-8f, fmaf(m, kLog2E, -t));
-    const float e = fast_exp2(t);
-    return fmaf(e, lo * kLn2, e);
+// max(x, 0), NaN where x is
+__device__ __forceinline__ float positive_part(float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ F2 positive_part(F2 x) {
+    float lo, hi;
+    split(x, lo, hi);
+    return pair(positive_part(lo), positive_part(hi));
+}
+__device__ __forceinline__ float rcp_(float x) { return fast_rcp(x); }
+__device__ __forceinline__ F2 rcp_(F2 x) {
+    float lo, hi;
+    split(x, lo, hi);
+    return pair(fast_rcp(lo), fast_rcp(hi));
+}
+__device__ __forceinline__ float neg_abs(float x) { return fmaxf(-fabsf(x), -120.f); }
+__device__ __forceinline__ F2 neg_abs(F2 x) {
+    float lo, hi;
+    split(x, lo, hi);
+    return pair(neg_abs(lo), neg_abs(hi));
+}
+__device__ __forceinline__ float ex2_neg(float x) { return fast_exp2(-x); }
+__device__ __forceinline__ F2 ex2_neg(F2 x) {
+    float lo, hi;
+    split(x, lo, hi);
+    return pair(fast_exp2(-lo), fast_exp2(-hi));
+}
+template <typename P>
+__device__ __forceinline__ P all_(float f) {
+    if constexpr (sizeof(P) == sizeof(float)) return f;
+    else return pair(f, f);
+}
+
+// e^-|x| to about 2^-22 relative (e^-120 below that): x log2 e in two parts, as its rounding alone would cost |x| 2^-24.
+// P: a float, or a pair of them
+template <typename P>
+__device__ __forceinline__ P exp_neg_abs(P x) {
+    const P m = neg_abs(x), nt = m * all_<P>(-kLog2E);
+    const P lo = fma_(m, all_<P>(1.925963033500e-8f), fma_(m, all_<P>(kLog2E), nt));
+    const P e = ex2_neg(nt);
+    return fma_(e, lo * all_<P>(kLn2), e);
+}
+// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x|; log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3: s times a polynomial
+// in s^2 fitted to 2 artanh(s) / s over that range, 8e-9 off at most.  (log of a rounded 1 + e would lose the small
+// steps that such layers start with.)
+template <typename P>
+__device__ __forceinline__ P softplus_of(P x) {
+    const P e = exp_neg_abs(x), s = e * rcp_(fma_(e, all_<P>(1.f), all_<P>(2.f))), q = s * s;
+    P p = all_<P>(0.2817833423614502f);
+    p = fma_(p, q, all_<P>(0.27960601449012756f));
+    p = fma_(p, q, all_<P>(0.40024909377098083f));
+    p = fma_(p, q, all_<P>(0.6666631698608398f));
+    p = fma_(p, q, all_<P>(2.f));
+    return fma_(p, s, positive_part(x));
 }
 // 1 / (1 + e^-x)
 __device__ __forceinline__ float sigmoid_of(float x) {
     const float e = exp_neg_abs(x), r = fast_rcp(1.f + e);
     return x < 0.f ? e * r : r;
 }
-// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x|; log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3, by its series up
-// to s^15, which leaves 2e-8 relative.  (log of a rounded 1 + e would lose the small steps that such layers start with.)
-__device__ __forceinline__ float softplus_of(float x) {
-    const float e = exp_neg_abs(x), s = e * fast_rcp(2.f + e), q = s * s;
-    float p = 2.f / 15;
-    p = fmaf(p, q, 2.f / 13);
-    p = fmaf(p, q, 2.f / 11);
-    p = fmaf(p, q, 2.f / 9);
-    p = fmaf(p, q, 2.f / 7);
-    p = fmaf(p, q, 2.f / 5);
-    p = fmaf(p, q, 2.f / 3);
-    p = fmaf(p, q, 2.f);
-    return fmaf(p, s, x < 0.f ? 0.f : x);
+__device__ __forceinline__ F2 sigmoid_of(F2 x) {
+    const F2 e = exp_neg_abs(x), r = rcp_(fma_(e, pair(1.f, 1.f), pair(1.f, 1.f))), er = e * r;
+    float x0, x1, r0, r1, e0, e1;
+    split(x, x0, x1), split(r, r0, r1), split(er, e0, e1);
+    return pair(x0 < 0.f ? e0 : r0, x1 < 0.f ? e1 : r1);
 }
-
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-    T v[V];
-};
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> ld_pack(const T* p) {
-    return *reinterpret_cast<const Pack<T, V>*>(p);
-}
-template <typename T, int V>
-__device__ __forceinline__ void clear(Pack<T, V>& a) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) a.v[i] = from_f32<T>(0.f);
+// x silu(z)
+template <typename P>
+__device__ __forceinline__ P times_silu(P x, P z) {
+    P slope;
+    return x * gate_of(z, true, slope);
 }
 
 // A thread's parts of `rows` tokens of a tile of `cols` columns, V columns at a time
 template <typename T, int V, int ROWS, int COLS, int THREADS>
 struct Tile {
     static constexpr int vecs = COLS / V, all = ROWS * vecs, each = (all + THREADS - 1) / THREADS;
-    Pack<T, V> v[each];
+    Vec<T, V> v[each];
     // f(k, row, column) for the parts that there are
     template <class F>
     static __device__ __forceinline__ void parts(F&& f) {
@@ -144,38 +177,110 @@ struct Tile {
     // rows t0 .. t_end of p, columns up to `cols`; zeros elsewhere
     __device__ __forceinline__ void load(const T* p, long long sn, int t0, int t_end, int cols) {
         parts([&](int k, int r, int c) {
-            if (t0 + r < t_end && c < cols) v[k] = ld_pack<T, V>(p + (long long)(t0 + r) * sn + c);
-            else clear(v[k]);
+            v[k] = Vec<T, V>{};
+            if (t0 + r < t_end && c < cols) v[k] = ldvec<T, V>(p + (long long)(t0 + r) * sn + c);
         });
     }
 };
 
-// Sum over a channel's state lanes of the values of a thread's four channels; lane sl has channel sl % 4's, with two
-// lanes both of its two's in r[0], r[1].
-template <int SL>
-__device__ __forceinline__ void state_sum(F2 a01, F2 a23, int sl, float (&r)[2]) {
-    const bool up = SL == 2 ? sl & 1 : sl & 2;
-    float g0, g1, k0, k1;
-    split(up ? a01 : a23, g0, g1);
-    split(up ? a23 : a01, k0, k1);
-    constexpr int o = SL == 2 ? 1 : 2;
-    k0 += __shfl_xor_sync(0xffffffffu, g0, o);
-    k1 += __shfl_xor_sync(0xffffffffu, g1, o);
-    if constexpr (SL == 2) {
-        r[0] = k0, r[1] = k1;
+// V values as N of P to and from shared memory
+template <int V, typename P, int N>
+__device__ __forceinline__ void put_values(float* p, const P (&f)[N]) {
+    if constexpr (V == 1) *p = f[0];
+    else st4(p, {f[0], f[1]});
+}
+template <int V, typename P, int N>
+__device__ __forceinline__ void get_values(const float* p, P (&f)[N]) {
+    if constexpr (V == 1) {
+        f[0] = *p;
     } else {
-        const bool odd = sl & 1;
-        float s = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
-#pragma unroll
-        for (int m = 4; m < SL; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-        r[0] = s;
+        const SsmPair2 a = ld4(p);
+        f[0] = a.lo, f[1] = a.hi;
     }
 }
-template <int SL>
-__device__ __forceinline__ void put_state_sum(float* row, int cg, int sl, const float (&r)[2]) {
-    if constexpr (SL == 2) *reinterpret_cast<float2*>(row + 4 * cg + 2 * sl) = make_float2(r[0], r[1]);
-    else if (SL == 4 || sl < 4) row[4 * cg + (sl & 3)] = r[0];
+// each of them twice
+template <int V, typename P, int N>
+__device__ __forceinline__ void put_twice(float* p, const P (&f)[N]) {
+    if constexpr (V == 1) {
+        *reinterpret_cast<float2*>(p) = make_float2(f[0], f[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float lo, hi;
+            split(f[i], lo, hi);
+            *reinterpret_cast<float4*>(p + 4 * i) = make_float4(lo, lo, hi, hi);
+        }
+    }
 }
+
+// delta, delta x and, with DY, dout silu(gate) of a thread's part of a tile
+template <typename T, int V, bool DY>
+__device__ __forceinline__ void stage(const Vec<T, V>& x, const Vec<T, V>& dt, const Vec<T, V>& dout, const Vec<T, V>& z, bool gated,
+                                      bool softplus, bool on, const float* bias, float* sd, float* su, float* sy) {
+    using L = Lanes<V>;
+    using P = typename L::P;
+    P fx[L::N], v[L::N], fb[L::N], d[L::N], u[L::N];
+    unpack(x, fx);
+    unpack(dt, v);
+    get_values<V>(bias, fb);
+#pragma unroll
+    for (int i = 0; i < L::N; ++i) {
+        v[i] = fma_(v[i], all_<P>(1.f), fb[i]);
+        d[i] = !on ? all_<P>(0.f) : softplus ? softplus_of(v[i]) : v[i];
+        u[i] = d[i] * fx[i];
+    }
+    put_values<V>(sd, d);
+    put_values<V>(su, u);
+    if constexpr (DY) {
+        P g[L::N], fz[L::N];
+        unpack(dout, g);
+        if (gated) {
+            unpack(z, fz);
+#pragma unroll
+            for (int i = 0; i < L::N; ++i) g[i] = times_silu(g[i], fz[i]);
+        }
+        put_values<V>(sy, g);
+    }
+}
+
+// Sums over the state lanes of a channel go through shared memory: each thread leaves the values of its four channels in a
+// row of its lane (of at most four; with more lanes they first exchange halves), and the readers add the rows.  The rows are 8
+// floats more than the channels apart, which keeps the writers of two channel groups and four lanes on different banks.
+template <int N>
+struct LaneRows {
+    static constexpr int lanes = SsmShape<N>::lanes, rows = lanes < 4 ? lanes : 4, stride = kSsmChannels + 8, token = rows * stride;
+    static __device__ __forceinline__ void put(float* sums, int cg, int sl, F2 a01, F2 a23) {
+        if constexpr (lanes <= 4) {
+            st4(sums + sl * stride + 4 * cg, {a01, a23});
+        } else {
+            const bool up = sl & 4;
+            float g0, g1, k0, k1;
+            split(up ? a01 : a23, g0, g1);
+            split(up ? a23 : a01, k0, k1);
+            k0 += __shfl_xor_sync(0xffffffffu, g0, 4);
+            k1 += __shfl_xor_sync(0xffffffffu, g1, 4);
+            float* at = sums + (sl & 3) * stride + 4 * cg + (up ? 2 : 0);
+            if constexpr (lanes == 8) {
+                *reinterpret_cast<float2*>(at) = make_float2(k0, k1);
+            } else {
+                const bool second = sl & 8;
+                at[second] = (second ? k1 : k0) + __shfl_xor_sync(0xffffffffu, second ? k0 : k1, 8);
+            }
+        }
+    }
+    // the sums of V channels
+    template <int V, typename P, int M>
+    static __device__ __forceinline__ void get(const float* sums, P (&f)[M]) {
+        get_values<V>(sums, f);
+#pragma unroll
+        for (int r = 1; r < rows; ++r) {
+            P w[M];
+            get_values<V>(sums + r * stride, w);
+#pragma unroll
+            for (int i = 0; i < M; ++i) f[i] = fma_(w[i], all_<P>(1.f), f[i]);
+        }
+    }
+};
 
 // The state of a thread's tile: [state][pair of channels]
 struct SsmState {
@@ -241,6 +346,40 @@ struct SsmPlace {
     // of this sequence and tile, segment s
     __device__ __forceinline__ long long slot(const SsmPass& p, int s) const { return (long long)blockIdx.x * p.nseg + s; }
 };
+
+// The state s before a segment from those of the segments between, first to last by dir: sums from zero of each, and its decay
+// exp(a steps).  Four segments' loads are in flight together.
+template <int N>
+__device__ __forceinline__ void join_segments(const SsmPass& p, const SsmPlace& at, SsmState& s, const SsmState& a, const float* sums,
+                                              int cg, int first, int last, int dir) {
+    constexpr int NT = SsmShape<N>::threads, CT = kSsmChannels;
+    auto step = [&](const SsmPair2& steps, const SsmState& w) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            s.v[k][0] = fma_(ex2_(steps.lo * a.v[k][0]), s.v[k][0], w.v[k][0]);
+            s.v[k][1] = fma_(ex2_(steps.hi * a.v[k][1]), s.v[k][1], w.v[k][1]);
+        }
+    };
+    int i = first;
+    for (; (last - i) * dir >= 4; i += 4 * dir) {
+        SsmState w[4];
+        SsmPair2 steps[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const long long slot = at.slot(p, i + q * dir);
+            steps[q] = ld4(p.steps + slot * CT + 4 * cg);
+            w[q].get(sums + slot * (CT * N), NT);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) step(steps[q], w[q]);
+    }
+    for (; i != last; i += dir) {
+        const long long slot = at.slot(p, i);
+        SsmState w;
+        w.get(sums + slot * (CT * N), NT);
+        step(ld4(p.steps + slot * CT + 4 * cg), w);
+    }
+}
 
 }  // namespace
 }  // namespace hla2

@@ -19,35 +19,34 @@ namespace {
 constexpr int kMacro = kSsmTokens;  // tokens between marks
 constexpr int kBack = 4;            // tokens whose states are in registers
 
-__device__ __forceinline__ float silu_slope(float z, float s) { return s * fmaf(z, 1.f - s, 1.f); }
-
 // Marks and sums of a segment.  REV: there are several segments, the states start from zero and R's sums are formed too.
 template <typename T, int V, int N, bool REV>
 __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threads)
     ssm_marks_kernel(const SsmPass p, const SsmGrads g) {
     constexpr int NT = SsmShape<N>::threads, SL = SsmShape<N>::lanes, TT = SsmShape<N>::tokens, CT = kSsmChannels;
-    constexpr int VB = V > N ? N : V;
+    using L = Lanes<V>;
+    using P = typename L::P;
     __shared__ __align__(16) float sd[TT][CT], su[TT][CT], sy[REV ? TT : 1][CT], sb[TT][2 * N], sc[REV ? TT : 1][2 * N], sbias[CT];
     const int tid = threadIdx.x, sl = tid % SL, cg = tid / SL;
     pdl_wait();
     const SsmPlace at(p);
     const int chans = at.cols - 4 * cg;
     for (int i = tid; i < CT; i += NT) sbias[i] = p.dt_bias && i < at.cols ? p.dt_bias[at.c0 + i] : 0.f;
-    SsmState a, h, P, R;
+    SsmState a, h, W, R;  // W: the decay since the segment's start
     a.load(p.a + (long long)(at.c0 + 4 * cg) * N + 4 * sl, N, chans);
     a.scale(kLog2E);
     h.zero();
     if (!REV && p.init) h.load(p.init + ((long long)at.b * p.D + at.c0 + 4 * cg) * N + 4 * sl, N, chans);
     R.zero();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) P.v[k][0] = P.v[k][1] = pair(1.f, 1.f);
+    for (int k = 0; k < 4; ++k) W.v[k][0] = W.v[k][1] = pair(1.f, 1.f);
     const T *x = static_cast<const T*>(p.x.p) + at.b * p.x.sb + at.c0, *dt = static_cast<const T*>(p.dt.p) + at.b * p.dt.sb + at.c0,
             *z = p.gate.p ? static_cast<const T*>(p.gate.p) + at.b * p.gate.sb + at.c0 : nullptr,
             *dout = static_cast<const T*>(g.dout.p) + at.b * g.dout.sb + at.c0,
             *b = static_cast<const T*>(p.b.p) + at.b * p.b.sb + at.group * p.b.sh,
             *c = static_cast<const T*>(p.c.p) + at.b * p.c.sb + at.group * p.c.sh;
     using Chan = Tile<T, V, TT, CT, NT>;
-    using Stat = Tile<T, VB, TT, N, NT>;
+    using Stat = Tile<T, V, TT, N, NT>;
     const long long slot = at.slot(p, at.seg);
     F2 sum01 = pair(0.f, 0.f), sum23 = sum01;
     __syncthreads();
@@ -71,32 +70,16 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
                 cr.load(c, p.c.sn, t0, at.live_end, N);
             }
             Chan::parts([&](int k, int r, int ch) {
-                const bool on = t0 + r < at.live_end && ch < at.cols;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float v = to_f32(dr.v[k].v[i]) + sbias[ch + i];
-                    const float d = on ? p.softplus ? softplus_of(v) : v : 0.f;
-                    sd[r][ch + i] = d;
-                    su[r][ch + i] = d * to_f32(xr.v[k].v[i]);
-                    if (REV) {
-                        float dy = to_f32(or_.v[k].v[i]);
-                        if (z) {
-                            const float gv = to_f32(zr.v[k].v[i]);
-                            dy *= gv * sigmoid_of(gv);
-                        }
-                        sy[r][ch + i] = dy;
-                    }
-                }
+                stage<T, V, REV>(xr.v[k], dr.v[k], or_.v[k], zr.v[k], z, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
+                                 &sd[r][ch], &su[r][ch], &sy[REV ? r : 0][ch]);
             });
-            Stat::parts([&](int k, int r, int s) {
-#pragma unroll
-                for (int i = 0; i < VB; ++i) {
-                    const float fb = to_f32(br.v[k].v[i]);
-                    *reinterpret_cast<float2*>(&sb[r][2 * (s + i)]) = make_float2(fb, fb);
-                    if (REV) {
-                        const float fc = to_f32(cr.v[k].v[i]);
-                        *reinterpret_cast<float2*>(&sc[r][2 * (s + i)]) = make_float2(fc, fc);
-                    }
+            Stat::parts([&](int k, int r, int n) {
+                P f[L::N];
+                unpack(br.v[k], f);
+                put_twice<V>(&sb[r][2 * n], f);
+                if (REV) {
+                    unpack(cr.v[k], f);
+                    put_twice<V>(&sc[REV ? r : 0][2 * n], f);
                 }
             });
         }
@@ -118,10 +101,10 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
                     h.v[k + j][0] = fma_(e0, h.v[k + j][0], u.lo * bk);
                     h.v[k + j][1] = fma_(e1, h.v[k + j][1], u.hi * bk);
                     if (REV) {
-                        P.v[k + j][0] = P.v[k + j][0] * e0;
-                        P.v[k + j][1] = P.v[k + j][1] * e1;
-                        R.v[k + j][0] = fma_(P.v[k + j][0], dy.lo * ck, R.v[k + j][0]);
-                        R.v[k + j][1] = fma_(P.v[k + j][1], dy.hi * ck, R.v[k + j][1]);
+                        W.v[k + j][0] = W.v[k + j][0] * e0;
+                        W.v[k + j][1] = W.v[k + j][1] * e1;
+                        R.v[k + j][0] = fma_(W.v[k + j][0], dy.lo * ck, R.v[k + j][0]);
+                        R.v[k + j][1] = fma_(W.v[k + j][1], dy.hi * ck, R.v[k + j][1]);
                     }
                 }
             }
@@ -140,27 +123,30 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
 // Shared memory of the main pass, in floats
 template <int N>
 struct BackSmem {
-    static constexpr int threads = SsmShape<N>::threads;
-    static constexpr int d = 0, u = d + kMacro * kSsmChannels, y = u + kMacro * kSsmChannels, b = y + kMacro * kSsmChannels,
-                         c = b + kMacro * 2 * N, states = c + kMacro * 2 * N,
+    static constexpr int threads = SsmShape<N>::threads, rows = kMacro * kSsmChannels;
+    static constexpr int d = 0, u = d + rows, y = u + rows, b = y + rows, c = b + kMacro * 2 * N,
                          // the segment's first state, and those before each four tokens but the last
-                         sums = states + kMacro / kBack * threads * 16,
-                         // five values of four from each thread and token
-                         skip = sums + 5 * kBack * threads * 4, bias = skip + kSsmChannels, total = bias + kSsmChannels;
+                         states = c + kMacro * 2 * N,
+                         // of four tokens: dc and db of each thread's states, y, in and sum E a by lane rows
+                         dc = states + kMacro / kBack * threads * 16, db = dc + kBack * threads * 4, py = db + kBack * threads * 4,
+                         in = py + kBack * LaneRows<N>::token, e = in + kBack * LaneRows<N>::token,
+                         skip = e + kBack * LaneRows<N>::token, bias = skip + kSsmChannels, total = bias + kSsmChannels;
 };
 
 template <typename T, int V, int N>
 __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threads)
     ssm_backward_kernel(const SsmPass p, const SsmGrads g) {
     constexpr int NT = SsmShape<N>::threads, SL = SsmShape<N>::lanes, CT = kSsmChannels, MT = kMacro, TC = kBack;
-    constexpr int VB = V > N ? N : V, VE = V > 1 ? 4 : 1;  // vectors of the staging of b and c, and of the outputs
+    using L = Lanes<V>;
+    using P = typename L::P;
+    using Sums = LaneRows<N>;
+    constexpr int Q = 4 / V;  // vectors of an item, four channels of a token
     constexpr int items = TC * CT / 4 > NT ? TC * CT / 4 / NT : 1;
     using S = BackSmem<N>;
     extern __shared__ __align__(16) float sm[];
     float *sd = sm + S::d, *su = sm + S::u, *sy = sm + S::y, *sb = sm + S::b, *sc = sm + S::c, *sst = sm + S::states,
           *sskip = sm + S::skip, *sbias = sm + S::bias;
-    // [token][thread] four: dc, db of four states; y, in and sum E a of four channels, these as [token][lane][channel]
-    float *vdc = sm + S::sums, *vdb = vdc + TC * NT * 4, *vy = vdb + TC * NT * 4, *vin = vy + TC * NT * 4, *ve = vin + TC * NT * 4;
+    float *vdc = sm + S::dc, *vdb = sm + S::db, *vy = sm + S::py, *vin = sm + S::in, *ve = sm + S::e;
     const int tid = threadIdx.x, sl = tid % SL, cg = tid / SL;
     pdl_wait();
     const SsmPlace at(p);
@@ -178,19 +164,8 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
     E.zero();
     if (p.init) h.load(p.init + state_at, N, chans);
     if (g.dfinal) E.load(g.dfinal + state_at, N, chans);
-    auto join = [&](SsmState& s, const float* sums, int seg) {
-        const long long slot = at.slot(p, seg);
-        const SsmPair2 steps = ld4(p.steps + slot * CT + 4 * cg);
-        SsmState w;
-        w.get(sums + slot * (CT * N), NT);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            s.v[k][0] = fma_(ex2_(steps.lo * a.v[k][0]), s.v[k][0], w.v[k][0]);
-            s.v[k][1] = fma_(ex2_(steps.hi * a.v[k][1]), s.v[k][1], w.v[k][1]);
-        }
-    };
-    for (int s = 0; s < at.seg; ++s) join(h, p.sums, s);
-    for (int s = p.nseg - 1; s > at.seg; --s) join(E, g.rsums, s);
+    join_segments<N>(p, at, h, a, p.sums, cg, 0, at.seg, 1);
+    join_segments<N>(p, at, E, a, g.rsums, cg, p.nseg - 1, at.seg, -1);
     h.put(sst, NT);
     const T *x = static_cast<const T*>(p.x.p) + at.b * p.x.sb + at.c0, *dt = static_cast<const T*>(p.dt.p) + at.b * p.dt.sb + at.c0,
             *z = p.gate.p ? static_cast<const T*>(p.gate.p) + at.b * p.gate.sb + at.c0 : nullptr,
@@ -200,10 +175,12 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
     auto out = [&](const SsmRows& r) { return static_cast<T*>(const_cast<void*>(r.p)) + at.b * r.sb + at.c0; };
     T *dx = out(g.dx), *ddt = out(g.ddt), *dgate = z ? out(g.dgate) : nullptr;
     using Chan = Tile<T, V, MT, CT, NT>;
-    using Stat = Tile<T, VB, MT, N, NT>;
+    using Stat = Tile<T, V, MT, N, NT>;
     const long long slot = at.slot(p, at.seg);
     // sums of this thread's items' channels
-    float gskip[4] = {0.f, 0.f, 0.f, 0.f}, gbias[4] = {0.f, 0.f, 0.f, 0.f};
+    P gskip[Q * L::N], gbias[Q * L::N];
+#pragma unroll
+    for (int i = 0; i < Q * L::N; ++i) gskip[i] = gbias[i] = L::all(0.f);
     const int quad = tid % (CT / 4) * 4;
 
     const int macros = (at.live_end - at.t0 + MT - 1) / MT;
@@ -236,28 +213,15 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
             br.load(b, p.b.sn, t0, at.live_end, N);
             cr.load(c, p.c.sn, t0, at.live_end, N);
             Chan::parts([&](int k, int r, int ch) {
-                const bool on = t0 + r < at.live_end && ch < at.cols;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float v = to_f32(dr.v[k].v[i]) + sbias[ch + i];
-                    const float d = on ? p.softplus ? softplus_of(v) : v : 0.f;
-                    sd[r * CT + ch + i] = d;
-                    su[r * CT + ch + i] = d * to_f32(xr.v[k].v[i]);
-                    float dy = to_f32(or_.v[k].v[i]);
-                    if (z) {
-                        const float gv = to_f32(zr.v[k].v[i]);
-                        dy *= gv * sigmoid_of(gv);
-                    }
-                    sy[r * CT + ch + i] = dy;
-                }
+                stage<T, V, true>(xr.v[k], dr.v[k], or_.v[k], zr.v[k], z, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
+                                  sd + r * CT + ch, su + r * CT + ch, sy + r * CT + ch);
             });
-            Stat::parts([&](int k, int r, int s) {
-#pragma unroll
-                for (int i = 0; i < VB; ++i) {
-                    const float fb = to_f32(br.v[k].v[i]), fc = to_f32(cr.v[k].v[i]);
-                    *reinterpret_cast<float2*>(&sb[r * 2 * N + 2 * (s + i)]) = make_float2(fb, fb);
-                    *reinterpret_cast<float2*>(&sc[r * 2 * N + 2 * (s + i)]) = make_float2(fc, fc);
-                }
+            Stat::parts([&](int k, int r, int n) {
+                P f[L::N];
+                unpack(br.v[k], f);
+                put_twice<V>(sb + r * 2 * N + 2 * n, f);
+                unpack(cr.v[k], f);
+                put_twice<V>(sc + r * 2 * N + 2 * n, f);
             });
         }
         __syncthreads();
@@ -282,28 +246,24 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
         for (int t = MT - TC; t >= 0; t -= TC) {
             if (t < MT - TC) h.get(sst + (1 + t / TC) * (NT * 16), NT);
             // what the items of these tokens take from memory
-            Pack<T, VE> ix[items][4 / VE], id[items][4 / VE], iz[items][4 / VE], io[items][4 / VE];
-            auto each_item = [&](auto&& f) {
+            Vec<T, V> ix[items][Q], id[items][Q], iz[items][Q], io[items][Q];
+            auto each_item = [&](auto&& f) {  // f(item, vector, token of the four, its place, channel)
 #pragma unroll
                 for (int m = 0; m < items; ++m) {
                     const int i = tid + m * NT, r = i / (CT / 4);
-                    if (items == 1 && NT > TC * CT / 4 && i >= TC * CT / 4) continue;
-                    f(m, r, t0 + t + r);
+                    if (NT > TC * CT / 4 && i >= TC * CT / 4) continue;
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) f(m, q, r, t0 + t + r, quad + q * V);
                 }
             };
-            each_item([&](int m, int r, int tok) {
-#pragma unroll
-                for (int q = 0; q < 4 / VE; ++q) {
-                    const int ch = quad + q * VE;
-                    if (tok < at.live_end && ch < at.cols) {
-                        ix[m][q] = ld_pack<T, VE>(x + (long long)tok * p.x.sn + ch);
-                        id[m][q] = ld_pack<T, VE>(dt + (long long)tok * p.dt.sn + ch);
-                        if (z) {
-                            iz[m][q] = ld_pack<T, VE>(z + (long long)tok * p.gate.sn + ch);
-                            io[m][q] = ld_pack<T, VE>(dout + (long long)tok * g.dout.sn + ch);
-                        }
-                    } else {
-                        clear(ix[m][q]), clear(id[m][q]), clear(iz[m][q]), clear(io[m][q]);
+            each_item([&](int m, int q, int r, int tok, int ch) {
+                ix[m][q] = id[m][q] = iz[m][q] = io[m][q] = Vec<T, V>{};
+                if (tok < at.live_end && ch < at.cols) {
+                    ix[m][q] = ldvec<T, V>(x + (long long)tok * p.x.sn + ch);
+                    id[m][q] = ldvec<T, V>(dt + (long long)tok * p.dt.sn + ch);
+                    if (z) {
+                        iz[m][q] = ldvec<T, V>(z + (long long)tok * p.gate.sn + ch);
+                        io[m][q] = ldvec<T, V>(dout + (long long)tok * g.dout.sn + ch);
                     }
                 }
             });
@@ -329,7 +289,7 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
                     }
                 }
                 *reinterpret_cast<float4*>(vdc + (i * NT + tid) * 4) = make_float4(dc[0], dc[1], dc[2], dc[3]);
-                if (z) st4(vy + (i * SL + sl) * CT + 4 * cg, {y01, y23});
+                if (z) Sums::put(vy + i * Sums::token, cg, sl, y01, y23);
             }
 #pragma unroll
             for (int i = TC - 1; i >= 0; --i) {
@@ -356,8 +316,8 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
                     }
                 }
                 *reinterpret_cast<float4*>(vdb + (i * NT + tid) * 4) = make_float4(db[0], db[1], db[2], db[3]);
-                st4(vin + (i * SL + sl) * CT + 4 * cg, {in01, in23});
-                st4(ve + (i * SL + sl) * CT + 4 * cg, {e01, e23});
+                Sums::put(vin + i * Sums::token, cg, sl, in01, in23);
+                Sums::put(ve + i * Sums::token, cg, sl, e01, e23);
             }
             __syncthreads();
             // dc and db of these tokens: two threads a column of four states, eight channels' each
@@ -379,45 +339,43 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
                     *reinterpret_cast<float4*>(g.bc + (((long long)at.b * p.n + tok) * (p.G * p.tiles) + at.tile) * (2 * N) +
                                                which * N + 4 * lane) = f;
             }
-            each_item([&](int m, int r, int tok) {
-                float in[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-                auto add = [](float (&s)[4], const float* v) {
-                    const float4 f = *reinterpret_cast<const float4*>(v);
-                    s[0] += f.x, s[1] += f.y, s[2] += f.z, s[3] += f.w;
-                };
-#pragma unroll
-                for (int l = 0; l < SL; ++l) {
-                    add(in, vin + (r * SL + l) * CT + quad);
-                    add(e, ve + (r * SL + l) * CT + quad);
-                    if (z) add(y, vy + (r * SL + l) * CT + quad);
-                }
-                if (tok >= at.t_end) return;
+            each_item([&](int m, int q, int r, int tok, int ch) {
+                if (tok >= at.t_end || ch >= at.cols) return;
+                P in[L::N], e[L::N], xv[L::N], v[L::N], d[L::N], dy[L::N], fb[L::N], fs[L::N], dd[L::N], ox[L::N];
+                Sums::template get<V>(vin + r * Sums::token + ch, in);
+                Sums::template get<V>(ve + r * Sums::token + ch, e);
+                unpack(ix[m][q], xv);
+                unpack(id[m][q], v);
+                get_values<V>(sd + (t + r) * CT + ch, d);
+                get_values<V>(sy + (t + r) * CT + ch, dy);
+                get_values<V>(sbias + ch, fb);
+                get_values<V>(sskip + ch, fs);
                 const bool on = tok < at.live_end;
-                Pack<T, VE> ox[4 / VE], od[4 / VE], og[4 / VE];
+                const P zero = L::all(0.f), one = L::all(1.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int ch = quad + i;
-                    const float xv = to_f32(ix[m][i / VE].v[i % VE]), d = sd[(t + r) * CT + ch], dy = sy[(t + r) * CT + ch];
-                    float dd = fmaf(xv, in[i], e[i] * kLn2);
-                    if (p.softplus) dd *= sigmoid_of(to_f32(id[m][i / VE].v[i % VE]) + sbias[ch]);
-                    dd = on ? dd : 0.f;
-                    gbias[i] += dd;
-                    gskip[i] = fmaf(xv, dy, gskip[i]);
-                    ox[i / VE].v[i % VE] = from_f32<T>(on ? fmaf(d, in[i], sskip[ch] * dy) : 0.f);
-                    od[i / VE].v[i % VE] = from_f32<T>(dd);
-                    if (z) {
-                        const float zv = to_f32(iz[m][i / VE].v[i % VE]), s = sigmoid_of(zv);
-                        const float dg = to_f32(io[m][i / VE].v[i % VE]) * fmaf(sskip[ch], xv, y[i]) * silu_slope(zv, s);
-                        og[i / VE].v[i % VE] = from_f32<T>(on ? dg : 0.f);
-                    }
+                for (int i = 0; i < L::N; ++i) {
+                    dd[i] = fma_(xv[i], in[i], e[i] * L::all(kLn2));
+                    if (p.softplus) dd[i] = dd[i] * sigmoid_of(fma_(v[i], one, fb[i]));
+                    ox[i] = fma_(d[i], in[i], fs[i] * dy[i]);
+                    if (!on) dd[i] = ox[i] = zero;
+                    P &gb = gbias[q * L::N + i], &gs = gskip[q * L::N + i];
+                    gb = fma_(dd[i], one, gb);
+                    gs = fma_(xv[i], dy[i], gs);
                 }
+                stvec<T, V>(dx + (long long)tok * g.dx.sn + ch, ox);
+                stvec<T, V>(ddt + (long long)tok * g.ddt.sn + ch, dd);
+                if (z) {
+                    P y[L::N], fz[L::N], fo[L::N];
+                    Sums::template get<V>(vy + r * Sums::token + ch, y);
+                    unpack(iz[m][q], fz);
+                    unpack(io[m][q], fo);
 #pragma unroll
-                for (int q = 0; q < 4 / VE; ++q) {
-                    const int ch = quad + q * VE;
-                    if (ch >= at.cols) continue;
-                    *reinterpret_cast<Pack<T, VE>*>(dx + (long long)tok * g.dx.sn + ch) = ox[q];
-                    *reinterpret_cast<Pack<T, VE>*>(ddt + (long long)tok * g.ddt.sn + ch) = od[q];
-                    if (z) *reinterpret_cast<Pack<T, VE>*>(dgate + (long long)tok * g.dgate.sn + ch) = og[q];
+                    for (int i = 0; i < L::N; ++i) {
+                        P slope;
+                        gate_of(fz[i], true, slope);
+                        y[i] = on ? fo[i] * fma_(fs[i], xv[i], y[i]) * slope : zero;
+                    }
+                    stvec<T, V>(dgate + (long long)tok * g.dgate.sn + ch, y);
                 }
             });
             __syncthreads();
@@ -431,13 +389,15 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
     float* per_channel = g.params + (long long)p.B * p.nseg * p.D * N + 2 * row + at.c0;
     // the items of a quad are in threads 16 apart
     constexpr int who = items * NT > TC * CT / 4 ? TC : NT / (CT / 4);
-    float* sums = sm + S::sums;
-    __syncthreads();
+    float* sums = vdc;
     if (tid < TC * CT / 4) {
+        float* to = sums + tid / (CT / 4) * CT + quad;
+        if constexpr (V == 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sums[(tid / (CT / 4)) * CT + quad + i] = gskip[i];
-            sums[(TC + tid / (CT / 4)) * CT + quad + i] = gbias[i];
+            for (int i = 0; i < 4; ++i) to[i] = gskip[i], to[TC * CT + i] = gbias[i];
+        } else {
+            put_values<V>(to, gskip);
+            put_values<V>(to + TC * CT, gbias);
         }
     }
     __syncthreads();
@@ -449,15 +409,16 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
         if (ch < at.cols) per_channel[(long long)which * p.D + ch] = s;
     }
     // padding past the last tokens gone through
-    Pack<T, VE> zero;
-    clear(zero);
+    P zero[L::N];
+#pragma unroll
+    for (int i = 0; i < L::N; ++i) zero[i] = L::all(0.f);
     const int first = at.t0 + macros * MT;
-    for (long long i = tid; i < (long long)(at.t_end - first) * (CT / VE); i += NT) {
-        const int tok = first + (int)(i / (CT / VE)), ch = (int)(i % (CT / VE)) * VE;
+    for (long long i = tid; i < (long long)(at.t_end - first) * (CT / V); i += NT) {
+        const int tok = first + (int)(i / (CT / V)), ch = (int)(i % (CT / V)) * V;
         if (ch >= at.cols) continue;
-        *reinterpret_cast<Pack<T, VE>*>(dx + (long long)tok * g.dx.sn + ch) = zero;
-        *reinterpret_cast<Pack<T, VE>*>(ddt + (long long)tok * g.ddt.sn + ch) = zero;
-        if (z) *reinterpret_cast<Pack<T, VE>*>(dgate + (long long)tok * g.dgate.sn + ch) = zero;
+        stvec<T, V>(dx + (long long)tok * g.dx.sn + ch, zero);
+        stvec<T, V>(ddt + (long long)tok * g.ddt.sn + ch, zero);
+        if (z) stvec<T, V>(dgate + (long long)tok * g.dgate.sn + ch, zero);
     }
 }
 
@@ -544,7 +505,7 @@ int backward_v(const SsmPass& p, const SsmGrads& g, cudaStream_t st) {
 }  // namespace
 
 int launch_ssm_backward(const SsmPass& p, const SsmGrads& g, bool is_bf16, bool vec, cudaStream_t st) {
-    if (is_bf16) return vec ? backward_v<bf16, 8>(p, g, st) : backward_v<bf16, 1>(p, g, st);
+    if (is_bf16) return vec ? backward_v<bf16, 4>(p, g, st) : backward_v<bf16, 1>(p, g, st);
     return vec ? backward_v<float, 4>(p, g, st) : backward_v<float, 1>(p, g, st);
 }
 
