@@ -27,6 +27,14 @@ struct Entries {
     decltype(&hla2_block_join) block_join;
     decltype(&hla2_block_join_backward) block_join_backward;
     decltype(&hla2_w4_matvec) w4_matvec;
+    decltype(&hla2_ssm_forward) ssm_forward;
+    decltype(&hla2_ssm_backward) ssm_backward;
+    decltype(&hla2_ssm_decode_step) ssm_decode_step;
+    decltype(&hla2_short_conv_forward) short_conv_forward;
+    decltype(&hla2_short_conv_backward) short_conv_backward;
+    decltype(&hla2_short_conv_decode_step) short_conv_decode_step;
+    decltype(&hla2_layer_norm) layer_norm;
+    decltype(&hla2_layer_norm_backward) layer_norm_backward;
 } lib{};
 
 constexpr size_t kStatusBytes = 256;  // at a workspace's start, for the calls with bounded waits
@@ -329,6 +337,258 @@ PyObject* w4_matvec(PyObject*, PyObject* const* p, Py_ssize_t count) {
     });
 }
 
+// ---- selective state space layer -------------------------------------------------------------
+
+// [B, n, D] or, for single tokens, [B, D], with a contiguous last dimension
+bool token_rows(const Tensor& t, hla2_rows* r) {
+    const int64_t last = t.dim() - 1;
+    if (t.stride(last) != 1 && t.size(last) > 1) return false;
+    *r = {t.data_ptr(), t.stride(0), last == 2 ? t.stride(1) : 0};
+    return true;
+}
+hla2_rows rows_out(const Tensor& t) { return {t.data_ptr(), t.stride(0), t.dim() == 3 ? t.stride(1) : 0}; }
+
+// The scratch of a call behind its status word; None: none, which small calls do not need
+bool scratch_of(const Common& c, PyObject* o, void** p, size_t* bytes) {
+    *p = nullptr, *bytes = 0;
+    if (none(o)) return true;
+    const Tensor* ws = tensor(o);
+    if (!ws || !c.has(*ws, at::kByte) || (size_t)ws->numel() <= kStatusBytes) return false;
+    *p = static_cast<char*>(ws->data_ptr()) + kStatusBytes;
+    *bytes = (size_t)ws->numel() - kStatusBytes;
+    return true;
+}
+bool truth(PyObject* o, int* v) {
+    if (o != Py_True && o != Py_False) return false;
+    *v = o == Py_True;
+    return true;
+}
+void* at_(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+float* f32_at(const Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; }
+const Tensor* given(const Tensor& t) { return t.defined() ? &t : nullptr; }
+
+// x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state; `tokens`: x is [B, n, D], else [B, D]
+struct Ssm : Common {
+    hla2_ssm_args a{};
+    const Tensor *x, *b, *c, *gate = nullptr;
+    // b or c: [B, n, N] or [B, n, G, N], without n for single tokens
+    bool states(const Tensor& t, bool tokens, hla2_view* v) const {
+        const int64_t last = t.dim() - 1, at = tokens ? 2 : 1;
+        if (t.stride(last) != 1 && t.size(last) > 1) return false;
+        *v = {t.data_ptr(), t.stride(0), last == at ? 0 : t.stride(at), tokens ? t.stride(1) : 0};
+        return true;
+    }
+    bool read(PyObject* const* p, bool tokens) {
+        const int64_t lead = tokens ? 2 : 1;
+        x = tensor(p[0]), b = tensor(p[3]), c = tensor(p[4]);
+        const Tensor *dt = tensor(p[1]), *A = tensor(p[2]);
+        if (!x || !dt || !A || !b || !c || !of(*x) || !has(*dt) || !has(*b) || !has(*c) || !has(*A, at::kFloat) ||
+            x->dim() != lead + 1 || dt->sizes() != x->sizes() || A->dim() != 2 || (b->dim() != lead + 1 && b->dim() != lead + 2) ||
+            c->sizes() != b->sizes())
+            return false;
+        const int64_t B = x->size(0), n = tokens ? x->size(1) : 1, D = x->size(lead), N = A->size(1);
+        const int64_t G = b->dim() == lead + 2 ? b->size(lead) : 1;
+        if (B < 1 || n < 1 || D < 1 || G < 1 || !fits(B) || !fits(n) || !fits(D) || !fits(N) || A->size(0) != D || D % G ||
+            b->size(0) != B || (tokens && b->size(1) != n) || b->size(b->dim() - 1) != N || !A->is_contiguous())
+            return false;
+        const void *skip, *bias, *lengths, *init;
+        if (!optional(*this, p[5], at::kFloat, {D}, &skip) || !optional(*this, p[7], at::kFloat, {D}, &bias) ||
+            !truth(p[8], &a.softplus) || !optional(*this, p[9], at::kInt, {B}, &lengths) ||
+            !optional(*this, p[10], at::kFloat, {B, D, N}, &init))
+            return false;
+        if (!none(p[6])) {
+            gate = tensor(p[6]);
+            if (!gate || !has(*gate) || gate->sizes() != x->sizes() || !token_rows(*gate, &a.gate)) return false;
+        }
+        a.dtype = dtype, a.B = (int)B, a.n = (int)n, a.D = (int)D, a.N = (int)N, a.G = (int)G;
+        a.a = A->data_ptr<float>();
+        a.skip = static_cast<const float*>(skip), a.dt_bias = static_cast<const float*>(bias);
+        a.lengths = static_cast<const int*>(lengths);
+        a.init_state = static_cast<const float*>(init);
+        return token_rows(*x, &a.x) && token_rows(*dt, &a.dt) && states(*b, tokens, &a.b) && states(*c, tokens, &a.c);
+    }
+    Tensor floats(std::initializer_list<int64_t> sizes) const { return at::empty(at::IntArrayRef(sizes), x->options().dtype(at::kFloat)); }
+};
+
+// (x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state, want_final, workspace) -> out or (out, state)
+PyObject* ssm_forward(PyObject*, PyObject* const* p, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        Ssm s;
+        if (count != 13 || !s.read(p, true) || !scratch_of(s, p[12], &s.a.workspace, &s.a.workspace_bytes)) return nullptr;
+        const bool want = p[11] == Py_True;
+        const Tensor out = at::empty(s.x->sizes(), s.x->options());
+        Tensor fin;
+        if (want) fin = s.floats({s.a.B, s.a.D, s.a.N});
+        if (lib.ssm_forward(&s.a, rows_out(out), f32_at(fin), s.stream())) return nullptr;
+        return want ? wrap_all({&out, &fin}) : wrap(out);
+    });
+}
+
+// (x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state, dout, dfinal_state, workspace) -> the gradients in
+// SsmGrads' order, None where there is no such input
+PyObject* ssm_backward(PyObject*, PyObject* const* p, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        Ssm s;
+        if (count != 14 || !s.read(p, true) || !scratch_of(s, p[13], &s.a.workspace, &s.a.workspace_bytes)) return nullptr;
+        const Tensor* dout = tensor(p[11]);
+        const void* dfin;
+        hla2_rows dor;
+        const int64_t B = s.a.B, n = s.a.n, D = s.a.D, N = s.a.N, G = s.a.G;
+        if (!dout || !s.has(*dout) || dout->sizes() != s.x->sizes() || !token_rows(*dout, &dor) ||
+            !optional(s, p[12], at::kFloat, {B, D, N}, &dfin))
+            return nullptr;
+        const auto like = s.x->options();
+        const Tensor dx = at::empty({B, n, D}, like), ddt = at::empty({B, n, D}, like), da = s.floats({D, N});
+        const Tensor db = at::empty(s.b->sizes(), like), dc = at::empty(s.b->sizes(), like);
+        Tensor dskip, dgate, dbias, dinit;
+        if (s.a.skip) dskip = s.floats({D});
+        if (s.gate) dgate = at::empty({B, n, D}, like);
+        if (s.a.dt_bias) dbias = s.floats({D});
+        if (s.a.init_state) dinit = s.floats({B, D, N});
+        hla2_ssm_grads g{};
+        g.dx = rows_out(dx), g.ddt = rows_out(ddt);
+        if (s.gate) g.dgate = rows_out(dgate);
+        g.db = {db.data_ptr(), n * G * N, N, G * N}, g.dc = {dc.data_ptr(), n * G * N, N, G * N};
+        g.da = f32_at(da), g.dskip = f32_at(dskip), g.ddt_bias = f32_at(dbias), g.dinit_state = f32_at(dinit);
+        if (lib.ssm_backward(&s.a, dor, static_cast<const float*>(dfin), &g, s.stream())) return nullptr;
+        return wrap_all({&dx, &ddt, &da, &db, &dc, given(dskip), given(dgate), given(dbias), given(dinit)});
+    });
+}
+
+// (state, x, dt, a, b, c, skip, gate, dt_bias, dt_softplus) -> out
+PyObject* ssm_decode_step(PyObject*, PyObject* const* p, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        if (count != 10) return nullptr;
+        PyObject* q[11] = {p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], Py_None, Py_None};
+        const Tensor* st = tensor(p[0]);
+        Ssm s;
+        if (!st || !s.read(q, false) || !s.has(*st, at::kFloat) || !is(*st, {s.a.B, s.a.D, s.a.N}) || !st->is_contiguous()) return nullptr;
+        const Tensor out = at::empty(s.x->sizes(), s.x->options());
+        if (lib.ssm_decode_step(&s.a, st->data_ptr<float>(), rows_out(out), s.stream())) return nullptr;
+        return wrap(out);
+    });
+}
+
+// x, weight, bias, silu, lengths, init_state
+struct Conv : Common {
+    hla2_conv_args a{};
+    const Tensor* x;
+    bool read(PyObject* const* p, bool tokens) {
+        x = tensor(p[0]);
+        const Tensor* w = tensor(p[1]);
+        if (!x || !w || !of(*x) || !has(*w) || x->dim() != (tokens ? 3 : 2) || w->dim() != 2 || !w->is_contiguous()) return false;
+        const int64_t B = x->size(0), n = tokens ? x->size(1) : 1, D = x->size(x->dim() - 1), W = w->size(1);
+        const void *lengths;
+        if (B < 1 || n < 1 || D < 1 || !fits(B) || !fits(n) || !fits(D) || W < 2 || W > 4 || w->size(0) != D ||
+            !optional(*this, p[2], type, {D}, &a.bias) || !truth(p[3], &a.silu) || !optional(*this, p[4], at::kInt, {B}, &lengths) ||
+            !optional(*this, p[5], type, {B, W - 1, D}, &a.init_state))
+            return false;
+        a.dtype = dtype, a.B = (int)B, a.n = (int)n, a.D = (int)D, a.W = (int)W;
+        a.weight = w->data_ptr();
+        a.lengths = static_cast<const int*>(lengths);
+        return token_rows(*x, &a.x);
+    }
+    Tensor state() const { return at::empty({a.B, a.W - 1, a.D}, x->options()); }
+};
+
+// (x, weight, bias, silu, lengths, init_state, want_final) -> out or (out, state)
+PyObject* short_conv_forward(PyObject*, PyObject* const* p, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        Conv s;
+        if (count != 7 || !s.read(p, true)) return nullptr;
+        const bool want = p[6] == Py_True;
+        const Tensor out = at::empty(s.x->sizes(), s.x->options());
+        Tensor fin;
+        if (want) fin = s.state();
+        if (lib.short_conv_forward(&s.a, rows_out(out), at_(fin), s.stream())) return nullptr;
+        return want ? wrap_all({&out, &fin}) : wrap(out);
+    });
+}
+
+// (x, weight, bias, silu, lengths, init_state, dout, dfinal_state, workspace) -> the gradients in ShortConvGrads' order
+PyObject* short_conv_backward(PyObject*, PyObject* const* p, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        Conv s;
+        if (count != 9 || !s.read(p, true) || !scratch_of(s, p[8], &s.a.workspace, &s.a.workspace_bytes)) return nullptr;
+        const Tensor* dout = tensor(p[6]);
+        const void* dfin;
+        hla2_rows dor;
+        if (!dout || !s.has(*dout) || dout->sizes() != s.x->sizes() || !token_rows(*dout, &dor) ||
+            !optional(s, p[7], s.type, {s.a.B, s.a.W - 1, s.a.D}, &dfin))
+            return nullptr;
+        const Tensor dx = at::empty(s.x->sizes(), s.x->options()), dw = at::empty({s.a.D, s.a.W}, s.x->options().dtype(at::kFloat));
+        Tensor db, dinit;
+        if (s.a.bias) db = at::empty({s.a.D}, s.x->options().dtype(at::kFloat));
+        if (s.a.init_state) dinit = s.state();
+        if (lib.short_conv_backward(&s.a, dor, dfin, rows_out(dx), f32_at(dw), f32_at(db), at_(dinit), s.stream())) return nullptr;
+        return wrap_all({&dx, &dw, given(db), given(dinit)});
+    });
+}
+
+// (state, x, weight, bias, silu) -> out
+PyObject* short_conv_decode_step(PyObject*, PyObject* const* p, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        if (count != 5) return nullptr;
+        PyObject* q[6] = {p[1], p[2], p[3], p[4], Py_None, Py_None};
+        const Tensor* st = tensor(p[0]);
+        Conv s;
+        if (!st || !s.read(q, false) || !s.has(*st) || !is(*st, {s.a.B, s.a.W - 1, s.a.D}) || !st->is_contiguous()) return nullptr;
+        const Tensor out = at::empty(s.x->sizes(), s.x->options());
+        if (lib.short_conv_decode_step(&s.a, st->data_ptr(), rows_out(out), s.stream())) return nullptr;
+        return wrap(out);
+    });
+}
+
+// x, weight, bias, eps
+struct Norm : Common {
+    hla2_norm_args a{};
+    const Tensor* x;
+    bool read(PyObject* const* p) {
+        x = tensor(p[0]);
+        if (!x || !of(*x) || x->dim() < 2 || x->numel() == 0) return false;
+        const int64_t D = x->size(-1);
+        int64_t stride;
+        if (!fits(D) || !rows_of(*x, D, &stride) || none(p[1]) || !optional(*this, p[1], type, {D}, &a.weight) ||
+            !optional(*this, p[2], type, {D}, &a.bias))
+            return false;
+        const double eps = PyFloat_AsDouble(p[3]);
+        if (PyErr_Occurred()) return false;
+        a.dtype = dtype, a.rows = x->numel() / D, a.D = (int)D, a.eps = (float)eps;
+        a.x = x->data_ptr(), a.x_stride = stride;
+        return true;
+    }
+};
+
+// (x, weight, bias, eps) -> out
+PyObject* layer_norm(PyObject*, PyObject* const* p, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        Norm s;
+        if (count != 4 || !s.read(p)) return nullptr;
+        const Tensor out = at::empty(s.x->sizes(), s.x->options());
+        if (lib.layer_norm(&s.a, out.data_ptr(), s.stream())) return nullptr;
+        return wrap(out);
+    });
+}
+
+// (x, weight, dout, eps, workspace) -> (dx, dweight, dbias)
+PyObject* layer_norm_backward(PyObject*, PyObject* const* p, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        if (count != 5) return nullptr;
+        PyObject* q[4] = {p[0], p[1], Py_None, p[3]};
+        const Tensor* dout = tensor(p[2]);
+        Norm s;
+        void* ws;
+        size_t bytes;
+        if (!s.read(q) || !scratch_of(s, p[4], &ws, &bytes) || !dout || !s.has(*dout) || dout->sizes() != s.x->sizes() ||
+            !dout->is_contiguous())
+            return nullptr;
+        const auto sums = s.x->options().dtype(at::kFloat);
+        const Tensor dx = at::empty(s.x->sizes(), s.x->options()), dw = at::empty({s.a.D}, sums), db = at::empty({s.a.D}, sums);
+        if (lib.layer_norm_backward(&s.a, dout->data_ptr(), dx.data_ptr(), f32_at(dw), f32_at(db), ws, bytes, s.stream())) return nullptr;
+        return wrap_all({&dx, &dw, &db});
+    });
+}
+
 // (address of each entry point, in the order of Entries)
 PyObject* bind(PyObject*, PyObject* const* p, Py_ssize_t count) {
     constexpr Py_ssize_t kEntries = sizeof(Entries) / sizeof(void*);
@@ -357,6 +617,14 @@ PyMODINIT_FUNC PyInit__hla2_host() {
         {"block_join", fast(block_join), METH_FASTCALL, nullptr},
         {"block_join_backward", fast(block_join_backward), METH_FASTCALL, nullptr},
         {"w4_matvec", fast(w4_matvec), METH_FASTCALL, nullptr},
+        {"ssm_forward", fast(ssm_forward), METH_FASTCALL, nullptr},
+        {"ssm_backward", fast(ssm_backward), METH_FASTCALL, nullptr},
+        {"ssm_decode_step", fast(ssm_decode_step), METH_FASTCALL, nullptr},
+        {"short_conv_forward", fast(short_conv_forward), METH_FASTCALL, nullptr},
+        {"short_conv_backward", fast(short_conv_backward), METH_FASTCALL, nullptr},
+        {"short_conv_decode_step", fast(short_conv_decode_step), METH_FASTCALL, nullptr},
+        {"layer_norm", fast(layer_norm), METH_FASTCALL, nullptr},
+        {"layer_norm_backward", fast(layer_norm_backward), METH_FASTCALL, nullptr},
         {nullptr, nullptr, 0, nullptr}};
     static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hla2_host", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
     return PyModule_Create(&module);

@@ -1,5 +1,7 @@
 // C ABI of the selective scan: argument checks, the segmentation of the sequence and the passes of a call (ssm.cuh).
 // The declarations and their documentation are in include/hla2.h.
+#include <cmath>
+
 #include "rows.h"
 #include "ssm.cuh"
 
@@ -81,20 +83,33 @@ struct SsmPlan {
     int tiles, nseg, seg_tokens;
 };
 
-// Segments of each sequence.  Unit: sixteen tokens of the output pass by a CTA that has its SM nearly to itself.  CTAs
-// beside one another cost 0.35 of it each once they fill the SM.  More than one segment adds the pass of their sums,
-// about 0.7 of the output pass, a launch and the joining of the segments before, which a CTA reads one after another.
-SsmPlan ssm_plan(const hla2_ssm_args* a) {
+// Segments of each sequence, by the time in us of sixteen tokens in a CTA of the main pass: `alone` with the SM to itself,
+// and `beside` for each CTA once they fill it (measured at N = 16 over 1 to 128 segments of 32 to 512 tiles of channels;
+// the part of it that goes with the states, here 0.55 of it, goes with N).  An SM holds `most` CTAs (of 64 threads): up to
+// there the fullest SM counts, above it the waves count half, as they overlap.  More than one segment adds the pass of
+// their sums, a launch, and the joining of the segments before, which a CTA reads four at a time; the backward has a pass
+// of marks without them too.
+// (2 x 2048 x 2048, N = 16, forward: one segment 363 us, 8 105, 16 89, 64 107; backward 1299, 282, 274, 311.  8 x 4096 x 4096, which
+// fills the GPU by itself: forward 939 with one, 1050 with 8.)
+struct SsmCost {
+    double alone, beside, sums, marks;
+    int most;
+};
+constexpr SsmCost kForwardCost{2.8, 0.9, 0.55, 0.0, 7}, kBackwardCost{9.5, 3.0, 0.4, 0.2, 4};
+
+SsmPlan ssm_plan(const hla2_ssm_args* a, bool backward) {
     SsmPlan p{(a->D / a->G + kSsmChannels - 1) / kSsmChannels, 1, kSsmTokens};
+    const SsmCost& c = backward ? kBackwardCost : kForwardCost;
     const int steps = (a->n + kSsmTokens - 1) / kSsmTokens, sms = sm_count();
-    const long long ctas = (long long)a->B * a->G * p.tiles;
-    const double beside = 0.35 * a->N / 16;
+    const int most = c.most * 16 / a->N > 1 ? c.most * 16 / a->N : 1;
+    const double ctas = (double)a->B * a->G * p.tiles, beside = c.beside * (0.45 + 0.55 * a->N / 16);
     double best = 0;
     for (int want = 1; want <= steps && want <= 1024; want = want < 4 ? want + 1 : want * 5 / 4) {
         const int each = (steps + want - 1) / want, nseg = (steps + each - 1) / each;
-        const long long per_sm = (ctas * nseg + sms - 1) / sms;
-        const double load = per_sm * beside > 1 ? per_sm * beside : 1;
-        const double cost = nseg == 1 ? each * load : each * load * 1.7 + 3 + 0.1 * nseg;
+        const double per_sm = ctas * nseg / sms;
+        const double full = per_sm <= most ? std::ceil(per_sm) : 0.5 * (per_sm + most * std::ceil(per_sm / most));
+        const double load = full * beside > c.alone ? full * beside : c.alone;
+        const double cost = nseg == 1 ? each * load * (1 + c.marks) : each * load * (1 + c.sums) + 6 + 0.2 * nseg;
         if (want == 1 || cost < best) best = cost, p.nseg = nseg, p.seg_tokens = each * kSsmTokens;
     }
     return p;
@@ -149,7 +164,7 @@ size_t hla2_ssm_workspace_bytes(const hla2_ssm_args* a, int backward) {
     if (check_sizes("hla2_ssm_workspace_bytes", a) != HLA2_OK) return (size_t)-1;
     ok();
     if (a->D == 0 || (a->B == 0 && !backward)) return 0;
-    return scratch_of(a, ssm_plan(a), backward != 0).total;
+    return scratch_of(a, ssm_plan(a, backward != 0), backward != 0).total;
 }
 
 int hla2_ssm_forward(const hla2_ssm_args* a, hla2_rows out, float* final_state, hla2_stream_t stream) {
@@ -175,7 +190,7 @@ int hla2_ssm_forward(const hla2_ssm_args* a, hla2_rows out, float* final_state, 
         return ok();
     }
     if (in.meets(fin)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: final_state overlaps an input", fn);
-    const SsmPlan pl = ssm_plan(a);
+    const SsmPlan pl = ssm_plan(a, false);
     const Scratch s = scratch_of(a, pl, false);
     if (s.total > 0 && (!a->workspace || a->workspace_bytes < s.total || !al(a->workspace, 16)))
         return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, s.total);
@@ -244,7 +259,7 @@ int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfina
         for (int j = 0; j < i; ++j)
             if (meet(written[i], written[j])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: gradients overlap", fn);
     }
-    const SsmPlan pl = ssm_plan(a);
+    const SsmPlan pl = ssm_plan(a, true);
     const Scratch s = scratch_of(a, pl, true);
     if (s.total > 0 && (!a->workspace || a->workspace_bytes < s.total || !al(a->workspace, 16)))
         return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, s.total);

@@ -215,7 +215,9 @@ def _load_host(L):
         loader.exec_module(mod)
         mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.hla2_linattn_forward, L.hla2_linattn_backward, L.hla2_linattn_decode_step, L.hla2_block_join,
-            L.hla2_block_join_backward, L.hla2_w4_matvec)))
+            L.hla2_block_join_backward, L.hla2_w4_matvec, L.hla2_ssm_forward, L.hla2_ssm_backward, L.hla2_ssm_decode_step,
+            L.hla2_short_conv_forward, L.hla2_short_conv_backward, L.hla2_short_conv_decode_step, L.hla2_layer_norm,
+            L.hla2_layer_norm_backward)))
     except Exception as e:
         warnings.warn(f"{HOST_PATH} does not load, short calls take longer on the host: {e}", RuntimeWarning)
         return
@@ -1398,6 +1400,10 @@ def ssm_forward(x, dt, a, b, c, skip=None, gate=None, dt_bias=None, dt_softplus=
     padding, whatever they hold: 0 in the output, and not in the state.  init_state: float32 [B,D,N] to continue from.
     Returns out [B,n,D] and with ``return_final_state`` the float32 state after each sequence's last token,
     which ssm_decode_step goes on from."""
+    res = _quick_scratch("ssm_forward", x, x, dt, a, b, c, skip, gate, dt_bias, bool(dt_softplus), lengths, init_state,
+                         bool(return_final_state))
+    if res is not None:
+        return res
     return _ssm_forward(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init_state, return_final_state)
 
 
@@ -1416,6 +1422,10 @@ def ssm_backward(x, dt, a, b, c, dout, skip=None, gate=None, dt_bias=None, dt_so
                  init_state=None, dfinal_state=None):
     """SsmGrads of ssm_forward for the upstream gradient dout [B,n,D] of its output and dfinal_state (None: zero) of its
     final state.  Nothing is kept from the forward."""
+    res = _quick_scratch("ssm_backward", x, x, dt, a, b, c, skip, gate, dt_bias, bool(dt_softplus), lengths, init_state, dout,
+                         dfinal_state)
+    if res is not None:
+        return SsmGrads(*res)
     return _ssm_backward(x, dt, a, b, c, dout, skip, gate, dt_bias, dt_softplus, lengths, init_state, dfinal_state)
 
 
@@ -1444,6 +1454,9 @@ def _ssm_backward(x, dt, a, b, c, dout, skip, gate, dt_bias, dt_softplus, length
 def ssm_decode_step(state, x, dt, a, b, c, skip=None, gate=None, dt_bias=None, dt_softplus=True):
     """One token of the selective scan for each of B sequences: ``state`` [B,D,N] float32 on the GPU is updated in
     place.  x, dt, gate [B,D]; b, c [B,N] or [B,G,N]; the rest as ssm_forward has it.  Returns out [B,D]."""
+    res = _quick("ssm_decode_step", state, x, dt, a, b, c, skip, gate, dt_bias, bool(dt_softplus))
+    if res is not None:
+        return res
     return _ssm_decode_step(state, x, dt, a, b, c, skip, gate, dt_bias, dt_softplus)
 
 
@@ -1466,7 +1479,7 @@ def _ssm_decode_step(state, x, dt, a, b, c, skip, gate, dt_bias, dt_softplus):
 
 _CONV_ARGS = struct.Struct("@6iP2q4PPN")   # hla2_conv_args
 _NORM_ARGS = struct.Struct("@iqifPqPP")    # hla2_norm_args
-CONV_ACTS = {"silu": 1, "none": 0, None: 0}
+_SILU = {"silu": True, "none": False, None: False}
 
 
 class ShortConvGrads(NamedTuple):
@@ -1489,7 +1502,7 @@ def _same_state(name, t, shape, like):
 def _conv_args(x, weight, bias, act, lengths, init_state):
     """(device index, the fields of the argument block but for the workspace, tensors that they point into)"""
     index = _need_cuda(x, weight, bias)
-    if act not in CONV_ACTS:
+    if act not in _SILU:
         raise ValueError("act must be 'silu' or 'none'")
     if x.dim() != 3 or weight.dim() != 2 or weight.shape[0] != x.shape[2]:
         raise ValueError("x must be [B, n, D] and weight [D, W]")
@@ -1500,7 +1513,7 @@ def _conv_args(x, weight, bias, act, lengths, init_state):
     bias = _vector("bias", bias, D)
     lengths = _length_tensor(lengths, B, n, x.device)
     init = _same_state("init_state", init_state, (B, W - 1, D), x)
-    head = (_DTYPES[x.dtype], B, n, D, W, CONV_ACTS[act], *xr, weight.data_ptr(), _addr(bias), _addr(lengths), _addr(init))
+    head = (_DTYPES[x.dtype], B, n, D, W, int(_SILU[act]), *xr, weight.data_ptr(), _addr(bias), _addr(lengths), _addr(init))
     return index, head, (x, weight, bias, lengths, init)
 
 
@@ -1512,6 +1525,11 @@ def short_conv_forward(x, weight, bias=None, act="silu", lengths=None, init_stat
     None or B token counts; the rows past a sequence's length are padding, whatever they hold, and 0 in the
     output.  init_state [B,W-1,D] of x's type: the inputs before token 0, oldest first (None: zeros).  Returns out [B,n,D] and
     with ``return_final_state`` each sequence's last W-1 inputs, which short_conv_decode_step goes on from."""
+    silu = _SILU.get(act)
+    if silu is not None:
+        res = _quick("short_conv_forward", x, weight, bias, silu, lengths, init_state, bool(return_final_state))
+        if res is not None:
+            return res
     return _short_conv_forward(x, weight, bias, act, lengths, init_state, return_final_state)
 
 
@@ -1531,6 +1549,11 @@ def _short_conv_forward(x, weight, bias, act, lengths, init_state, return_final_
 def short_conv_backward(x, weight, dout, bias=None, act="silu", lengths=None, init_state=None, dfinal_state=None):
     """ShortConvGrads of short_conv_forward for the upstream gradient dout [B,n,D] of its output and dfinal_state (None:
     zero) of its final state.  Nothing is kept from the forward."""
+    silu = _SILU.get(act)
+    if silu is not None:
+        res = _quick_scratch("short_conv_backward", x, x, weight, bias, silu, lengths, init_state, dout, dfinal_state)
+        if res is not None:
+            return ShortConvGrads(*res)
     return _short_conv_backward(x, weight, dout, bias, act, lengths, init_state, dfinal_state)
 
 
@@ -1558,6 +1581,11 @@ def _short_conv_backward(x, weight, dout, bias, act, lengths, init_state, dfinal
 def short_conv_decode_step(state, x, weight, bias=None, act="silu"):
     """One token of the short convolution for each of B sequences: ``state`` [B,W-1,D] of x's type on the GPU is updated
     in place.  x [B,D]; the rest as short_conv_forward has it.  Returns out [B,D]."""
+    silu = _SILU.get(act)
+    if silu is not None:
+        res = _quick("short_conv_decode_step", state, x, weight, bias, silu)
+        if res is not None:
+            return res
     return _short_conv_decode_step(state, x, weight, bias, act)
 
 
@@ -1590,6 +1618,10 @@ def _norm_args(x, weight, bias, eps):
 def layer_norm(x, weight, bias=None, eps=1e-5, out=None):
     """Layer norm over the last dimension (1 to 8192 values; float32 or bfloat16 on the GPU): (x - mean) / sqrt(mean((x -
     mean)^2) + eps) * weight + bias.  weight and bias [D] of x's type.  out may be x itself."""
+    if out is None:
+        res = _quick("layer_norm", x, weight, bias, eps)
+        if res is not None:
+            return res
     return _layer_norm(x, weight, bias, eps, out)
 
 
@@ -1609,6 +1641,9 @@ def _layer_norm(x, weight, bias, eps, out):
 def layer_norm_backward(x, weight, dout, eps=1e-5):
     """(dx, dweight, dbias) of layer_norm; dweight and dbias are float32 sums over the rows.  They do not depend on the
     bias, and nothing is kept from the forward."""
+    res = _quick_scratch("layer_norm_backward", x, x, weight, dout, eps)
+    if res is not None:
+        return res
     return _layer_norm_backward(x, weight, dout, eps)
 
 
