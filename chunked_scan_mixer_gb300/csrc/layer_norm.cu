@@ -3,201 +3,208 @@
 // and for the gradient g = dy w of nx
 //   dx = inv (g - mean(g) - nx mean(g nx)),  dw += dy nx,  dbias += dy.
 //
-// The rows go through the ring and the launch shapes of the block norms (block_join.cuh): persistent CTAs, a thread with the
-// same columns of every row, copied ahead.  The squares are summed about the mean, in a second sum over the row in registers:
-// the difference of sums would lose the variance of rows far from zero.  The backward forms the statistics again; its two
-// sums over rows stay in registers, and each CTA writes one partial row, which a second kernel sums in a fixed order.
-#include "block_join.cuh"
+// Bytes bound it: two tensors forward, three backward, whose statistics are formed again.  A row has RW warps, few of them,
+// so that the two sums over it (the squares are summed about the mean: the difference of plain sums would lose the variance of
+// rows far from zero) cost little beside up to 64 values a lane; with one warp they need no barrier.  The next row's values
+// are on their way in registers while a row is worked on.  The backward's two sums over rows stay in registers; each
+// CTA writes one partial row, which a second kernel sums in a fixed order.
+#include <type_traits>
+
+#include "packed.cuh"
+#include "rows.h"
 
 namespace hla2 {
 namespace {
 
+constexpr int kMaxNormD = 8192;
+
 struct NormGrads {
     const void* dout;
     void* dx;
-    float* partial;  // [partials][2][D]: weight, bias
-    int partials;
+    float* partial;  // [CTAs][2][D]: weight, bias
 };
 
 // a b, which the compiler may not put into a sum that follows
 __device__ __forceinline__ float rounded_product(float a, float b) { return __fmul_rn(a, b); }
 __device__ __forceinline__ F2 rounded_product(F2 a, F2 b) { return a * b; }
 
-template <typename T, int VEC, int NV, int TPR, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 2)
-    layer_norm_kernel(const hla2_norm_args a, T* __restrict__ out, int stages) {
+// Rows of RW warps, as many of them to a CTA as make four warps
+template <int RW>
+struct NormShape {
+    static constexpr int rows = RW < 4 ? 4 / RW : 1, threads = 32 * RW * rows;
+};
+
+// Sums of K values over a row's warps; `red` alternates between two halves, so that one barrier a call is enough
+template <int RW, int K>
+__device__ __forceinline__ void norm_sum(float (&v)[K], float (*red)[NormShape<RW>::rows][RW][2], int& turn) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    if constexpr (RW > 1) {
+        const int warp = threadIdx.x >> 5, w = warp % RW, row = warp / RW;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k) red[turn][row][w][k] = v[k];
+        if constexpr (NormShape<RW>::rows == 1) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "n"(32 * RW) : "memory");
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            v[k] = red[turn][row][0][k];
+#pragma unroll
+            for (int i = 1; i < RW; ++i) v[k] += red[turn][row][i][k];
+        }
+        turn ^= 1;
+    }
+}
+
+// A lane's columns of a row: vectors t, t + 32 RW, ... of VEC values, NV of them
+template <typename T, int VEC, int NV, int RW>
+struct NormRow {
+    Vec<T, VEC> v[NV];
+    static __device__ __forceinline__ int column(int j) { return ((int)(threadIdx.x % (32 * RW)) + j * 32 * RW) * VEC; }
+    __device__ __forceinline__ void load(const T* p, int D) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            v[j] = Vec<T, VEC>{};
+            if (column(j) < D) v[j] = ldvec<T, VEC>(p + column(j));
+        }
+    }
+};
+
+template <typename T, int VEC, int NV, int RW>
+__global__ void __launch_bounds__(NormShape<RW>::threads) layer_norm_kernel(const hla2_norm_args a, T* __restrict__ out) {
     using L = Lanes<VEC>;
     using P = typename L::P;
-    constexpr int N = L::N;
-    extern __shared__ __align__(16) char ring_sm[];
-    __shared__ float red[2][16][1];
+    using Row = NormRow<T, VEC, NV, RW>;
+    constexpr int N = L::N, rows = NormShape<RW>::rows;
+    __shared__ float red[2][rows][RW][2];
     int turn = 0;
-    const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr, mine = threadIdx.x / tpr;
-    constexpr int per = TPR ? kSmallThreads / (TPR ? TPR : 1) : 1;
-    const float inv_d = 1.f / (float)a.D;
-    const int d_left = a.D - t * VEC;
-    const Ring<T, VEC, NV> ring(ring_sm, 1);
-    const long long stride = (long long)gridDim.x * per, row_first = (long long)blockIdx.x * per + mine;
-    const T* xf = static_cast<const T*>(a.x) + row_first * a.x_stride + t * VEC;
-    long long left = row_first < a.rows ? (a.rows - 1 - row_first) / stride + 1 : 0;
-    auto fetch = [&](int stage) {
-        if (left > 0) {
-            --left;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (j * tpr * VEC < d_left) ring.copy(stage, 0, j, xf + j * tpr * VEC);
-            xf += stride * a.x_stride;
-        }
-        cp_async_commit();
-    };
+    const int D = a.D;
+    const float inv_d = 1.f / (float)D;
+    const T *x = static_cast<const T*>(a.x), *w = static_cast<const T*>(a.weight), *bias = static_cast<const T*>(a.bias);
+    const long long stride = (long long)gridDim.x * rows;
+    long long r = (long long)blockIdx.x * rows + threadIdx.x / (32 * RW);
     pdl_wait();
-    for (int i = 0; i + 1 < stages; ++i) fetch(i);
-    const T *w = static_cast<const T*>(a.weight) + t * VEC, *bias = a.bias ? static_cast<const T*>(a.bias) + t * VEC : nullptr;
-    int stage = 0;
-    long long at = row_first * a.D + t * VEC;
-    for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows; row0 += stride, at += stride * a.D) {
-        const int cols = row0 + mine < a.rows ? d_left : 0;
-        fetch(stage == 0 ? stages - 1 : stage - 1);
-        cp_async_wait_but(stages - 1);
-        P x[NV][N], acc = L::all(0.f);
+    Row next;
+    if (r < a.rows) next.load(x + r * a.x_stride, D);
+    for (; r < a.rows; r += stride) {  // a row's warps stay together
+        P f[NV][N], acc = L::all(0.f);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (j * tpr * VEC < cols) {
-                ring.get(stage, 0, j, x[j]);
+        for (int j = 0; j < NV; ++j) {
+            unpack(next.v[j], f[j]);
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc = fma_(x[j][i], L::all(1.f), acc);
-            }
-        float sum[1] = {sum_of(acc)};
-        row_sum<TPR, 1>(sum, red, turn);
-        const P mean = L::all(-sum[0] * inv_d);
+            for (int i = 0; i < N; ++i) acc = fma_(f[j][i], L::all(1.f), acc);
+        }
+        if (r + stride < a.rows) next.load(x + (r + stride) * a.x_stride, D);
+        float s[1] = {sum_of(acc)};
+        norm_sum<RW, 1>(s, red, turn);
+        const P mean = L::all(-s[0] * inv_d);
         acc = L::all(0.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (j * tpr * VEC < cols) {
+            if (Row::column(j) < D) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    x[j][i] = fma_(x[j][i], L::all(1.f), mean);
-                    acc = fma_(x[j][i], x[j][i], acc);
+                    f[j][i] = fma_(f[j][i], L::all(1.f), mean);
+                    acc = fma_(f[j][i], f[j][i], acc);
                 }
             }
-        sum[0] = sum_of(acc);
-        row_sum<TPR, 1>(sum, red, turn);
-        const P inv = L::all(rsqrtf(sum[0] * inv_d + a.eps));
+        s[0] = sum_of(acc);
+        norm_sum<RW, 1>(s, red, turn);
+        const P inv = L::all(rsqrtf(s[0] * inv_d + a.eps));
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = j * tpr * VEC;
-            if (c < cols) {
+        for (int j = 0; j < NV; ++j)
+            if (Row::column(j) < D) {
                 P fw[N], fb[N], o[N];
-                unpack(ldvec<T, VEC>(w + c), fw);
-                if (bias) unpack(ldvec<T, VEC>(bias + c), fb);
+                unpack(ldvec<T, VEC>(w + Row::column(j)), fw);
+                if (bias) unpack(ldvec<T, VEC>(bias + Row::column(j)), fb);
 #pragma unroll
-                for (int i = 0; i < N; ++i) o[i] = fma_(x[j][i] * inv, fw[i], bias ? fb[i] : L::all(0.f));
-                stvec<T, VEC>(out + at + c, o);
+                for (int i = 0; i < N; ++i) o[i] = fma_(f[j][i] * inv, fw[i], bias ? fb[i] : L::all(0.f));
+                stvec<T, VEC>(out + r * D + Row::column(j), o);
             }
-        }
-        stage = stage + 1 == stages ? 0 : stage + 1;
     }
     pdl_trigger();
 }
 
-template <typename T, int VEC, int NV, int TPR, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : 3)
-    layer_norm_backward_kernel(const hla2_norm_args a, const NormGrads g, int stages) {
+template <typename T, int VEC, int NV, int RW>
+__global__ void __launch_bounds__(NormShape<RW>::threads, VEC == 8 && NV == 2 ? 512 / NormShape<RW>::threads : 1)
+    layer_norm_backward_kernel(const hla2_norm_args a, const NormGrads g) {
     using L = Lanes<VEC>;
     using P = typename L::P;
-    constexpr int N = L::N;
-    extern __shared__ __align__(16) char ring_sm[];  // the ring; at the end, in a sub-warp mapping, [2][D] sums
-    __shared__ float red[2][16][2];
+    using Row = NormRow<T, VEC, NV, RW>;
+    constexpr int N = L::N, rows = NormShape<RW>::rows;
+    __shared__ float red[2][rows][RW][2];
+    extern __shared__ float sums[];  // [2][D], where a CTA has several rows
     int turn = 0;
-    const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr, mine = threadIdx.x / tpr;
-    constexpr int per = TPR ? kSmallThreads / (TPR ? TPR : 1) : 1;
-    const int D = a.D, d_left = D - t * VEC;
+    const int D = a.D, mine = threadIdx.x / (32 * RW);
     const float inv_d = 1.f / (float)D;
-    const Ring<T, VEC, NV> ring(ring_sm, 2);
-    P gw[NV][N], gb[NV][N], w[NV][N];
+    const T *x = static_cast<const T*>(a.x), *w = static_cast<const T*>(a.weight), *dout = static_cast<const T*>(g.dout);
+    T* dx = static_cast<T*>(g.dx);
+    const long long stride = (long long)gridDim.x * rows;
+    long long r = (long long)blockIdx.x * rows + mine;
+    P gw[NV][N], gb[NV][N];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < N; ++i) gw[j][i] = gb[j][i] = L::all(0.f);
-    const long long stride = (long long)gridDim.x * per, row_first = (long long)blockIdx.x * per + mine;
-    const T *xf = static_cast<const T*>(a.x) + row_first * a.x_stride + t * VEC, *df = static_cast<const T*>(g.dout) + row_first * D + t * VEC;
-    long long left = row_first < a.rows ? (a.rows - 1 - row_first) / stride + 1 : 0;
-    auto fetch = [&](int stage) {
-        if (left > 0) {
-            --left;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = j * tpr * VEC;
-                if (c < d_left) ring.copy(stage, 0, j, xf + c), ring.copy(stage, 1, j, df + c);
-            }
-            xf += stride * a.x_stride, df += stride * D;
-        }
-        cp_async_commit();
-    };
     pdl_wait();
-    for (int i = 0; i + 1 < stages; ++i) fetch(i);
+    Row nx_, nd;
+    if (r < a.rows) nx_.load(x + r * a.x_stride, D), nd.load(dout + r * D, D);
+    for (; r < a.rows; r += stride) {
+        P f[NV][N], d[NV][N], sx = L::all(0.f), sg = L::all(0.f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-        if (j * tpr * VEC < d_left) unpack(ldvec<T, VEC>(static_cast<const T*>(a.weight) + (j * tpr + t) * VEC), w[j]);
-    int stage = 0;
-    long long at = row_first * D + t * VEC;
-    for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows; row0 += stride, at += stride * D) {
-        const int cols = row0 + mine < a.rows ? d_left : 0;
-        fetch(stage == 0 ? stages - 1 : stage - 1);
-        cp_async_wait_but(stages - 1);
-        // sums of x and of g
-        P x[NV][N], d[NV][N], sx = L::all(0.f), sg = L::all(0.f);
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (j * tpr * VEC < cols) {
-                ring.get(stage, 0, j, x[j]);
-                ring.get(stage, 1, j, d[j]);
+        for (int j = 0; j < NV; ++j) {
+            unpack(nx_.v[j], f[j]);
+            unpack(nd.v[j], d[j]);
+            if (Row::column(j) < D) {
+                P fw[N];
+                unpack(ldvec<T, VEC>(w + Row::column(j)), fw);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    sx = fma_(x[j][i], L::all(1.f), sx);
-                    sg = fma_(d[j][i], w[j][i], sg);
+                    sx = fma_(f[j][i], L::all(1.f), sx);
+                    sg = fma_(d[j][i], fw[i], sg);
                 }
             }
+        }
+        if (r + stride < a.rows) nx_.load(x + (r + stride) * a.x_stride, D), nd.load(dout + (r + stride) * D, D);
         float s[2] = {sum_of(sx), sum_of(sg)};
-        row_sum<TPR, 2>(s, red, turn);
-        const P mean = L::all(-s[0] * inv_d);
-        const float mean_g = s[1] * inv_d;
-        // sums of the squares about the mean, and of g times them
+        norm_sum<RW, 2>(s, red, turn);
+        const P mean = L::all(-s[0] * inv_d), minus = L::all(-s[1] * inv_d);
         P xx = L::all(0.f), gx = L::all(0.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (j * tpr * VEC < cols) {
+            if (Row::column(j) < D) {
+                P fw[N];
+                unpack(ldvec<T, VEC>(w + Row::column(j)), fw);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    x[j][i] = fma_(x[j][i], L::all(1.f), mean);
-                    xx = fma_(x[j][i], x[j][i], xx);
-                    gx = fma_(d[j][i] * w[j][i], x[j][i], gx);
+                    f[j][i] = fma_(f[j][i], L::all(1.f), mean);
+                    xx = fma_(f[j][i], f[j][i], xx);
+                    gx = fma_(d[j][i] * fw[i], f[j][i], gx);
                 }
             }
         s[0] = sum_of(xx), s[1] = sum_of(gx);
-        row_sum<TPR, 2>(s, red, turn);
+        norm_sum<RW, 2>(s, red, turn);
         const float inv = rsqrtf(s[0] * inv_d + a.eps);
-        const P dot = L::all(-s[1] * inv * inv_d), minus = L::all(-mean_g), pinv = L::all(inv);
+        const P dot = L::all(-s[1] * inv * inv_d), pinv = L::all(inv);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = j * tpr * VEC;
-            if (c < cols) {
-                P o[N];
+        for (int j = 0; j < NV; ++j)
+            if (Row::column(j) < D) {
+                P o[N], fw[N];
+                unpack(ldvec<T, VEC>(w + Row::column(j)), fw);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const P nx = x[j][i] * pinv;
+                    const P nx = f[j][i] * pinv;
                     gw[j][i] = fma_(d[j][i], nx, gw[j][i]);
                     gb[j][i] = fma_(d[j][i], L::all(1.f), gb[j][i]);
                     // the mean is taken off a rounded g, as it has been summed, and before the factor inv: in rows of one value that
                     // is large and the difference nothing
-                    o[i] = pinv * fma_(nx, dot, fma_(rounded_product(d[j][i], w[j][i]), L::all(1.f), minus));
+                    o[i] = pinv * fma_(nx, dot, fma_(rounded_product(d[j][i], fw[i]), L::all(1.f), minus));
                 }
-                stvec<T, VEC>(static_cast<T*>(g.dx) + at + c, o);
+                stvec<T, VEC>(dx + r * D + Row::column(j), o);
             }
-        }
-        stage = stage + 1 == stages ? 0 : stage + 1;
     }
-    cp_async_wait_all();
     pdl_trigger();
     auto at_of = [](const P (&v)[N], int i) {
         if constexpr (VEC == 1) {
@@ -209,31 +216,29 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : 3)
         }
     };
     float* dst = g.partial + (size_t)blockIdx.x * 2 * D;
-    if (TPR && TPR <= 32) {  // the CTA's row groups one after another, so that the order is fixed
-        float* acc = reinterpret_cast<float*>(ring_sm);
-        for (int who = 0; who < per; ++who) {
-            __syncthreads();
+    if constexpr (rows > 1) {  // the CTA's rows one after another, so that the order is fixed
+        for (int who = 0; who < rows; ++who) {
             if (mine == who) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
-                        const int c = (j * tpr + t) * VEC + i;
+                        const int c = Row::column(j) + i;
                         if (c < D) {
-                            acc[c] = (who ? acc[c] : 0.f) + at_of(gw[j], i);
-                            acc[D + c] = (who ? acc[D + c] : 0.f) + at_of(gb[j], i);
+                            sums[c] = (who ? sums[c] : 0.f) + at_of(gw[j], i);
+                            sums[D + c] = (who ? sums[D + c] : 0.f) + at_of(gb[j], i);
                         }
                     }
             }
+            __syncthreads();
         }
-        __syncthreads();
-        for (int c = threadIdx.x; c < 2 * D; c += kSmallThreads) dst[c] = acc[c];
+        for (int c = threadIdx.x; c < 2 * D; c += NormShape<RW>::threads) dst[c] = sums[c];
     } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const int c = (j * tpr + t) * VEC + i;
+                const int c = Row::column(j) + i;
                 if (c < D) dst[c] = at_of(gw[j], i), dst[D + c] = at_of(gb[j], i);
             }
     }
@@ -263,38 +268,86 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// The arguments as the block norms' launch choice has them: one row tensor, the weight, and what else has columns
-hla2_block_args as_block(const hla2_norm_args* a) {
-    hla2_block_args b{};
-    b.dtype = a->dtype, b.rows = a->rows, b.D = a->D, b.eps = a->eps;
-    b.x = a->x, b.x_stride = a->x_stride, b.next_weight = a->weight;
-    return b;
-}
+// ---- launch ----------------------------------------------------------------------------------
 
 int check_norm(const char* fn, const hla2_norm_args* a) {
     if (!a) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: args must not be NULL", fn);
+    if (a->dtype != HLA2_F32 && a->dtype != HLA2_BF16)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dtype must be HLA2_F32 or HLA2_BF16", fn);
+    if (a->D < 1 || a->D > kMaxNormD)
+        return set_last_error(a->D < 1 ? HLA2_ERR_INVALID_ARG : HLA2_ERR_UNSUPPORTED, "%s: D must be 1 .. %d (got %d)", fn,
+                              kMaxNormD, a->D);
+    if (a->rows < 0 || a->rows > 0x7fffffffLL)
+        return set_last_error(HLA2_ERR_INVALID_ARG, "%s: rows must be 0 .. 2^31 - 1", fn);
     if (!a->weight) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: weight must not be NULL", fn);
-    const hla2_block_args b = as_block(a);
-    if (int rc = check_join(fn, &b)) return rc;
-    if (!al(a->bias, a->dtype == HLA2_BF16 ? 2 : 4))
+    const int es = elem_size(a->dtype);
+    if (!al(a->x, es) || !al(a->weight, es) || !al(a->bias, es))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
+    if (a->rows > 0 && !a->x) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: x must not be NULL", fn);
+    if (a->rows > 1 && a->x_stride < 0) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: strides must not be negative", fn);
     return HLA2_OK;
 }
-
-Work norm_backward_work(const hla2_block_args* b, const Shape& s, int vec, int sms) {
-    return work_of(b, s, vec, 2, kNormBwdThreadsPerSm, s.tpr && s.tpr <= 32 ? 2 * (size_t)b->D * sizeof(float) : 0, sms);
+Extent norm_rows(const hla2_norm_args* a, const void* p, long long stride) {
+    return extent_of(p, (size_t)((a->rows - 1) * stride + a->D) * elem_size(a->dtype));
+}
+// Whether contiguous rows that are written overlap other rows in another way than as exactly the same ones: a row is read whole
+// before it is written, but its neighbours may be read earlier or later.
+bool norm_spoils(const hla2_norm_args* a, const void* out, const void* in, long long stride) {
+    return meet(norm_rows(a, out, a->D), norm_rows(a, in, stride)) && !(out == in && (stride == a->D || a->rows == 1));
+}
+// Elements a vector: 16 bytes where every row allows it, else one
+int norm_vec(const hla2_norm_args* a, const void* const* more, int count) {
+    const int v = 16 / elem_size(a->dtype);
+    bool fits = a->D % v == 0 && al(a->x, 16) && (a->rows <= 1 || a->x_stride % v == 0) && al(a->weight, 16);
+    for (int i = 0; i < count; ++i) fits = fits && al(more[i], 16);
+    return fits ? v : 1;
 }
 
-// f(VEC, NV, TPR, MAXT, zero of the type) as integral constants
-template <class F>
-int dispatch_norm(const hla2_block_args* b, int vec, const Shape& s, F&& f) {
-    return with_vec(b->D, vec, s, [&](auto v, auto nv, auto tpr, auto maxt) {
-        constexpr int VEC = decltype(v)::value;
-        if constexpr (VEC == 8 || VEC == 2) return f(v, nv, tpr, maxt, bf16{});
-        else if constexpr (VEC == 4) return f(v, nv, tpr, maxt, 0.f);
-        else return b->dtype == HLA2_BF16 ? f(v, nv, tpr, maxt, bf16{}) : f(v, nv, tpr, maxt, 0.f);
-    });
+template <int V> using Int = std::integral_constant<int, V>;
+// f(VEC, NV, RW, zero of the type) for the first shape that holds a row: one warp with 1, 2, .. MOST vectors a lane, then 2, 4, ..
+// CAP warps, then more vectors
+template <int VEC, int MOST, int CAP, int NV = 1, int RW = 1, class T, class F>
+int norm_shape(int D, T zero, F&& f) {
+    if constexpr (32 * NV * RW * VEC >= kMaxNormD) {
+        return f(Int<VEC>{}, Int<NV>{}, Int<RW>{}, zero);
+    } else {
+        if (D <= 32 * NV * RW * VEC) return f(Int<VEC>{}, Int<NV>{}, Int<RW>{}, zero);
+        if constexpr (NV < MOST) return norm_shape<VEC, MOST, CAP, 2 * NV, RW>(D, zero, f);
+        else if constexpr (RW < CAP) return norm_shape<VEC, MOST, CAP, NV, 2 * RW>(D, zero, f);
+        else return norm_shape<VEC, MOST, CAP, 2 * NV, RW>(D, zero, f);
+    }
 }
+// Forward: up to 64 bf16 or 32 float32 values a lane (32768 bf16 rows of 2048: 45 us, 64 with a CTA of one vector a lane).  Rows
+// that do not give every SM two of them are latency: one vector a lane, up to eight warps (4 x 2048: 3.7 -> 2.2 us).
+// Backward, whose sums are held too: 16 values (32768 x 2048: 81 us, 93 with 32, and 4 CTAs an SM instead of 2).
+// Single elements: 8 (5000 float32 rows of 999: 7.3 us, 10.5 with 16; backward 15.3 and 17.2).
+template <bool BACK, class F>
+int with_norm(const hla2_norm_args* a, int vec, F&& f) {
+    const bool bf = a->dtype == HLA2_BF16;
+    if (vec == 1) return bf ? norm_shape<1, 8, 16>(a->D, bf16{}, f) : norm_shape<1, 8, 16>(a->D, 0.f, f);
+    if constexpr (BACK) {
+        return bf ? norm_shape<8, 2, 8>(a->D, bf16{}, f) : norm_shape<4, 4, 16>(a->D, 0.f, f);
+    } else {
+        if (a->rows <= 2 * sm_count()) return bf ? norm_shape<8, 1, 8>(a->D, bf16{}, f) : norm_shape<4, 1, 8>(a->D, 0.f, f);
+        return bf ? norm_shape<8, 8, 8>(a->D, bf16{}, f) : norm_shape<4, 8, 8>(a->D, 0.f, f);
+    }
+}
+
+// CTAs of a call: what the GPU holds at once
+template <class K>
+int norm_ctas(K kernel, int threads, size_t smem, long long rows, int rows_each) {
+    const long long need = (rows + rows_each - 1) / rows_each;
+    if (need <= sm_count()) return (int)need;
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1) {
+        cudaGetLastError();
+        per_sm = 1;
+    }
+    const long long most = (long long)per_sm * sm_count();
+    return (int)(need < most ? need : most);
+}
+// that a backward has at most, whatever its shape
+constexpr int kMostCtasPerSm = 8;
 
 }  // namespace
 }  // namespace hla2
@@ -305,48 +358,39 @@ extern "C" {
 
 int hla2_layer_norm(const hla2_norm_args* a, void* out, hla2_stream_t stream) {
     static const char* const fn = "hla2_layer_norm";
+    Range range(fn);
     if (int rc = check_norm(fn, a)) return rc;
-    if (a->rows == 0) return join_ok();
-    const hla2_block_args b = as_block(a);
-    const size_t es = a->dtype == HLA2_BF16 ? 2 : 4;
+    if (a->rows == 0) return ok();
+    const size_t es = elem_size(a->dtype);
     if (!out || !al(out, es)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out must be an aligned address", fn);
-    const RowsOf o{out, a->D, a->D};
-    if (spoils(&b, o, nullptr, 0) || meet(rows_extent(&b, o), extent_of(a->bias, a->D * es)))
+    const Extent eo = norm_rows(a, out, a->D);
+    if (norm_spoils(a, out, a->x, a->x_stride) || meet(eo, extent_of(a->weight, a->D * es)) || meet(eo, extent_of(a->bias, a->D * es)))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps an input other than in its place", fn);
     const void* more[2] = {out, a->bias};
-    const int vec = vec_of(&b, more, 2);
-    const Shape s = shape_of(a->D, vec);
-    const Work w = work_of(&b, s, vec, 1, kFwdThreadsPerSm, 0, sm_count());
-    auto launch = [&](auto v, auto nv, auto tpr, auto maxt, auto zero) {
+    const int rc = with_norm<false>(a, norm_vec(a, more, 2), [&](auto v, auto nv, auto rw, auto zero) {
         using T = decltype(zero);
-        auto k = layer_norm_kernel<T, decltype(v)::value, decltype(nv)::value, decltype(tpr)::value, decltype(maxt)::value>;
-        if (!set_smem(k, w.smem)) return -1;
-        return launch_pdl(k, dim3(w.ctas), dim3(s.threads), w.smem, reinterpret_cast<cudaStream_t>(stream), *a, static_cast<T*>(out),
-                          w.stages) == cudaSuccess ? 0 : -1;
-    };
-    if (dispatch_norm(&b, vec, s, launch))
-        return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));
-    return join_ok();
+        constexpr int RW = decltype(rw)::value;
+        auto k = layer_norm_kernel<T, decltype(v)::value, decltype(nv)::value, RW>;
+        const int ctas = norm_ctas(k, NormShape<RW>::threads, 0, a->rows, NormShape<RW>::rows);
+        return launch_pdl(k, dim3(ctas), dim3(NormShape<RW>::threads), 0, reinterpret_cast<cudaStream_t>(stream), *a,
+                          static_cast<T*>(out)) == cudaSuccess ? 0 : -1;
+    });
+    return rc ? launch_failed("layer norm") : ok();
 }
 
 size_t hla2_layer_norm_backward_workspace_bytes(const hla2_norm_args* a) {
     if (check_norm("hla2_layer_norm_backward_workspace_bytes", a) != HLA2_OK) return (size_t)-1;
-    join_ok();
-    const hla2_block_args b = as_block(a);
-    size_t most = 0;
-    for (int vec : {1, 2, a->dtype == HLA2_BF16 ? 8 : 4}) {  // whichever the addresses allow
-        const size_t c = (size_t)norm_backward_work(&b, shape_of(a->D, vec), vec, sm_count()).ctas;
-        if (c > most) most = c;
-    }
-    return most * 2 * (size_t)a->D * sizeof(float);
+    ok();
+    const long long most = (long long)kMostCtasPerSm * sm_count();
+    return (size_t)(a->rows < most ? a->rows : most) * 2 * (size_t)a->D * sizeof(float);
 }
 
 int hla2_layer_norm_backward(const hla2_norm_args* a, const void* dout, void* dx, float* dweight, float* dbias,
                              void* workspace, size_t workspace_bytes, hla2_stream_t stream) {
     static const char* const fn = "hla2_layer_norm_backward";
+    Range range(fn);
     if (int rc = check_norm(fn, a)) return rc;
-    const hla2_block_args b = as_block(a);
-    const size_t es = a->dtype == HLA2_BF16 ? 2 : 4, vb = (size_t)a->D * sizeof(float);
+    const size_t es = elem_size(a->dtype), vb = (size_t)a->D * sizeof(float);
     if (!dweight || !al(dweight, 4) || !al(dbias, 4))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dweight is needed, and each sum aligned to its type", fn);
     const Extent sums[2] = {extent_of(dweight, vb), extent_of(dbias, vb)};
@@ -355,36 +399,37 @@ int hla2_layer_norm_backward(const hla2_norm_args* a, const void* dout, void* dx
     if (a->rows > 0) {
         if (!dout || !dx || !al(dout, es) || !al(dx, es))
             return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dout and dx must be aligned addresses", fn);
-        const RowsOf o{dx, a->D, a->D}, more[1] = {{dout, a->D, a->D}};
-        bad |= spoils(&b, o, more, 1) || meet(rows_extent(&b, o), extent_of(a->bias, a->D * es));
-        for (const RowsOf& t : {RowsOf{a->x, a->x_stride, a->D}, more[0], o})
-            for (const Extent& e : sums) bad |= meet(e, rows_extent(&b, t));
+        const Extent eo = norm_rows(a, dx, a->D);
+        bad |= norm_spoils(a, dx, a->x, a->x_stride) || norm_spoils(a, dx, dout, a->D);
+        bad |= meet(eo, extent_of(a->weight, a->D * es)) || meet(eo, extent_of(a->bias, a->D * es));
+        for (const Extent& e : sums)
+            bad |= meet(e, eo) || meet(e, norm_rows(a, a->x, a->x_stride)) || meet(e, norm_rows(a, dout, a->D));
     }
     if (bad) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps another tensor other than in its place", fn);
     const size_t need = hla2_layer_norm_backward_workspace_bytes(a);
     if (need > 0 && (!workspace || workspace_bytes < need || !al(workspace, 16)))
         return set_last_error(HLA2_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, need);
-    NormGrads g{dout, dx, static_cast<float*>(workspace), 0};
+    NormGrads g{dout, dx, static_cast<float*>(workspace)};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    int partials = 0;
     if (a->rows > 0) {
         const void* more[2] = {dout, dx};
-        const int vec = vec_of(&b, more, 2);
-        const Shape s = shape_of(a->D, vec);
-        const Work w = norm_backward_work(&b, s, vec, sm_count());
-        g.partials = w.ctas;
-        auto launch = [&](auto v, auto nv, auto tpr, auto maxt, auto zero) {
+        const int rc = with_norm<true>(a, norm_vec(a, more, 2), [&](auto v, auto nv, auto rw, auto zero) {
             using T = decltype(zero);
-            auto k = layer_norm_backward_kernel<T, decltype(v)::value, decltype(nv)::value, decltype(tpr)::value, decltype(maxt)::value>;
-            if (!set_smem(k, w.smem)) return -1;
-            return launch_pdl(k, dim3(w.ctas), dim3(s.threads), w.smem, st, *a, g, w.stages) == cudaSuccess ? 0 : -1;
-        };
-        if (dispatch_norm(&b, vec, s, launch))
-            return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));
+            constexpr int RW = decltype(rw)::value;
+            auto k = layer_norm_backward_kernel<T, decltype(v)::value, decltype(nv)::value, RW>;
+            const size_t smem = NormShape<RW>::rows > 1 ? 2 * vb : 0;
+            if (smem > 40 * 1024 && raise_smem(k, smem) != cudaSuccess) return -1;
+            partials = norm_ctas(k, NormShape<RW>::threads, smem, a->rows, NormShape<RW>::rows);
+            if (partials > kMostCtasPerSm * sm_count()) partials = kMostCtasPerSm * sm_count();
+            return launch_pdl(k, dim3(partials), dim3(NormShape<RW>::threads), smem, st, *a, g) == cudaSuccess ? 0 : -1;
+        });
+        if (rc) return launch_failed("layer norm gradients");
     }
-    if (launch_pdl(norm_sums_kernel, dim3((2 * a->D + 31) / 32), dim3(1024), 0, st, g.partial, g.partials, 2 * a->D, a->D, dweight,
+    if (launch_pdl(norm_sums_kernel, dim3((2 * a->D + 31) / 32), dim3(1024), 0, st, g.partial, partials, 2 * a->D, a->D, dweight,
                    dbias) != cudaSuccess)
-        return set_last_error(HLA2_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(cudaGetLastError()));
-    return join_ok();
+        return launch_failed("layer norm gradients");
+    return ok();
 }
 
 }  // extern "C"

@@ -27,29 +27,41 @@ struct ConvPass {
     float* partial;  // [rows][D][W + 1]
 };
 
-constexpr int kAhead = 8;  // tokens in flight
+constexpr int kAhead = 4;  // tokens of a block, whose loads go out while the block before is worked on
 
 __device__ __forceinline__ int length_of(const int* lengths, int b, int n) {
     return lengths ? max(0, min(__ldg(lengths + b), n)) : n;
 }
 
-// weights of VEC channels as N of P for each tap
+// weights of VEC channels as N of P for each tap: W vectors, since a channel's taps lie side by side
 template <typename T, int VEC, int W, typename P, int N>
 __device__ __forceinline__ void load_taps(const T* w, P (&taps)[W][N]) {
+    float f[VEC * W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        P v[N];
+        unpack(ldvec<T, VEC>(w + k * VEC), v);
+        if constexpr (VEC == 1) {
+            f[k] = v[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) split(v[i], f[k * VEC + 2 * i], f[k * VEC + 2 * i + 1]);
+        }
+    }
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if constexpr (VEC == 1) taps[j][i] = to_f32(w[j]);
-            else taps[j][i] = pair(to_f32(w[(2 * i) * W + j]), to_f32(w[(2 * i + 1) * W + j]));
+            if constexpr (VEC == 1) taps[j][i] = f[j];
+            else taps[j][i] = pair(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
         }
 }
 
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(128) conv_kernel(const ConvPass a) {
+__global__ void __launch_bounds__(128, 4) conv_kernel(const ConvPass a) {
     using L = Lanes<VEC>;
     using P = typename L::P;
-    constexpr int N = L::N;
+    constexpr int N = L::N, U = kAhead;
     pdl_wait();
     const long long i0 = (long long)blockIdx.x * 128 + threadIdx.x, i1 = i0 / a.cols;
     const int c = (int)(i0 - i1 * a.cols) * VEC, b = (int)(i1 / a.runs), run = (int)(i1 - (long long)b * a.runs);
@@ -65,45 +77,57 @@ __global__ void __launch_bounds__(128) conv_kernel(const ConvPass a) {
         else if (init) v = ldvec<T, VEC>(init + (long long)(t + W - 1) * a.D);
         return v;
     };
-    P taps[W][N], bias[N], win[W][N];
+    P taps[W][N], bias[N], in[W - 1 + U][N];  // in: the last W - 1 inputs, and those of a block
     load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
 #pragma unroll
     for (int i = 0; i < N; ++i) bias[i] = L::all(0.f);
     if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), bias);
     if (t0 < len) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) unpack(input(t0 - (W - 1) + j), win[j + 1]);
+        for (int j = 0; j < W - 1; ++j) unpack(input(t0 - (W - 1) + j), in[j]);
     }
-    for (int t = t0; t < t1; t += kAhead) {
-        Vec<T, VEC> v[kAhead];
+    const int live = min(len, t1);
+    Vec<T, VEC> next[U];
+    auto fetch = [&](int t) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (t + u < min(len, t1)) v[u] = ldvec<T, VEC>(x + (t + u) * a.x_sn);
+        for (int u = 0; u < U; ++u)
+            if (t + u < live) next[u] = ldvec<T, VEC>(x + (t + u) * a.x_sn);
+    };
+    // U tokens from t on; `whole`: all of them are there
+    auto block = [&](int t, auto whole) {
+        constexpr bool all = decltype(whole)::value;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (t + u >= t1) break;
+        for (int u = 0; u < U; ++u) unpack(next[u], in[W - 1 + u]);
+        fetch(t + U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!all && t + u >= live) break;
             P y[N];
-            if (t + u < len) {
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
+            for (int i = 0; i < N; ++i) {
+                y[i] = bias[i];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) win[j][i] = win[j + 1][i];
-                unpack(v[u], win[W - 1]);
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    y[i] = bias[i];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) y[i] = fma_(taps[j][i], win[j][i], y[i]);
-                    P slope;
-                    if (a.silu) y[i] = gate_of(y[i], true, slope);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) y[i] = L::all(0.f);
+                for (int j = 0; j < W; ++j) y[i] = fma_(taps[j][i], in[u + j][i], y[i]);
+                P slope;
+                if (a.silu) y[i] = gate_of(y[i], true, slope);
             }
             stvec<T, VEC>(out + (t + u) * a.o_sn, y);
         }
-    }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) in[j][i] = in[U + j][i];
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) next[u] = Vec<T, VEC>{};
+    fetch(t0);
+    int t = t0;
+    for (; t + U <= live; t += U) block(t, std::true_type{});
+    if (t < live) block(t, std::false_type{});
+    P zero[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) zero[i] = L::all(0.f);
+    for (t = max(t0, live); t < t1; ++t) stvec<T, VEC>(out + t * a.o_sn, zero);
     pdl_trigger();
     if (run == 0 && a.fin) {
         T* fin = static_cast<T*>(a.fin) + (long long)b * (W - 1) * a.D + c;
@@ -115,7 +139,7 @@ __global__ void __launch_bounds__(128) conv_kernel(const ConvPass a) {
 
 // Eight runs a CTA, 32 vectors of channels
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(256) conv_backward_kernel(const ConvPass a) {
+__global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a) {
     using L = Lanes<VEC>;
     using P = typename L::P;
     constexpr int N = L::N;
@@ -141,74 +165,98 @@ __global__ void __launch_bounds__(256) conv_backward_kernel(const ConvPass a) {
         T* dinit = a.fin ? static_cast<T*>(a.fin) + at : nullptr;
         load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
         if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), bias);
-        P win[W][N], dp[W][N];  // inputs up to t, and dp from s = t - W + 1 to t
+        constexpr int U = kAhead;
+        P in[W - 1 + U][N], dp[W - 1 + U][N];  // inputs and dp's: the last W - 1, and those of a block
 #pragma unroll
-        for (int j = 0; j < W; ++j)
+        for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-            for (int i = 0; i < N; ++i) win[j][i] = dp[j][i] = L::all(0.f);
+            for (int i = 0; i < N; ++i) in[j][i] = dp[j][i] = L::all(0.f);
         if (t0 < len) {
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
                 const int t = t0 - (W - 1) + j;
-                if (t >= 0) unpack(ldvec<T, VEC>(x + t * a.x_sn), win[j + 1]);
-                else if (init) unpack(ldvec<T, VEC>(init + (long long)(t + W - 1) * a.D), win[j + 1]);
+                if (t >= 0) unpack(ldvec<T, VEC>(x + t * a.x_sn), in[j]);
+                else if (init) unpack(ldvec<T, VEC>(init + (long long)(t + W - 1) * a.D), in[j]);
             }
         }
-        const int first = run == 0 ? -(W - 1) : t0, last = t1 + W - 1;  // s from first to t1
-        const int live = min(len, last);
-        constexpr int U = kAhead / 2;
-        for (int t = t0; t < last; t += U) {
-            Vec<T, VEC> vx[U], vg[U];
+        // dx_s is there with dp_t, t = s + W - 1
+        const int first = run == 0 ? -(W - 1) : t0, last = t1 + W - 1, live = min(len, last);
+        Vec<T, VEC> vx[U], vg[U];
+        auto fetch = [&](int t) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (t + u < live) vx[u] = ldvec<T, VEC>(x + (t + u) * a.x_sn), vg[u] = ldvec<T, VEC>(dout + (t + u) * a.g_sn);
+        };
+        // U tokens from t on; `inner`: all of them are this run's own, and so are the dx's
+        auto block = [&](int t, auto inner) {
+            constexpr bool all = decltype(inner)::value;
+            P g[U][N];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (t + u >= last) break;
+                unpack(vx[u], in[W - 1 + u]);
+                unpack(vg[u], g[u]);
+                if (!all && t + u >= live) {
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
+                    for (int i = 0; i < N; ++i) in[W - 1 + u][i] = g[u][i] = L::all(0.f);
+                }
+            }
+            fetch(t + U);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) win[j][i] = win[j + 1][i], dp[j][i] = dp[j + 1][i];
-                if (t + u < live) {
-                    P g[N];
-                    unpack(vx[u], win[W - 1]);
-                    unpack(vg[u], g);
+            for (int u = 0; u < U; ++u) {
+                const bool own = all || t + u < t1;
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        P p = bias[i], slope = L::all(1.f);
-                        if (a.silu) {
+                for (int i = 0; i < N; ++i) {
+                    P p = bias[i], slope = L::all(1.f);
+                    if (a.silu) {
 #pragma unroll
-                            for (int j = 0; j < W; ++j) p = fma_(taps[j][i], win[j][i], p);
-                            gate_of(p, true, slope);
-                        }
-                        dp[W - 1][i] = g[i] * slope;
-                        if (t + u < t1) {
-                            db[i] = fma_(dp[W - 1][i], L::all(1.f), db[i]);
-#pragma unroll
-                            for (int j = 0; j < W; ++j) dw[j][i] = fma_(dp[W - 1][i], win[j][i], dw[j][i]);
-                        }
+                        for (int j = 0; j < W; ++j) p = fma_(taps[j][i], in[u + j][i], p);
+                        gate_of(p, true, slope);
                     }
-                } else {
+                    const P d = !all && t + u >= live ? L::all(0.f) : g[u][i] * slope;
+                    dp[W - 1 + u][i] = d;
+                    if (own) {
+                        db[i] = fma_(d, L::all(1.f), db[i]);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) win[W - 1][i] = dp[W - 1][i] = L::all(0.f);
+                        for (int j = 0; j < W; ++j) dw[j][i] = fma_(d, in[u + j][i], dw[j][i]);
+                    }
                 }
                 const int s = t + u - (W - 1);
-                if (s < first) continue;
+                if (!all && (s < first || s >= t1)) continue;
                 P o[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) o[i] = L::all(0.f);
-                if (s < len) {
+                for (int i = 0; i < N; ++i) o[i] = taps[0][i] * dp[W - 1 + u][i];
+                if (!all) {
                     const int k = s - (len - (W - 1));  // its place in the state after the last token
-                    if (dfin && k >= 0) unpack(ldvec<T, VEC>(dfin + (long long)k * a.D), o);
+                    if (dfin && k >= 0 && s < len) {
+                        P f[N];
+                        unpack(ldvec<T, VEC>(dfin + (long long)k * a.D), f);
 #pragma unroll
-                    for (int i = 0; i < N; ++i)
-#pragma unroll
-                        for (int j = 0; j < W; ++j) o[i] = fma_(taps[j][i], dp[W - 1 - j][i], o[i]);
+                        for (int i = 0; i < N; ++i) o[i] = fma_(f[i], L::all(1.f), o[i]);
+                    }
                 }
-                if (s >= 0) stvec<T, VEC>(dx + s * a.o_sn, o);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int j = 1; j < W; ++j) o[i] = fma_(taps[j][i], dp[W - 1 + u - j][i], o[i]);
+                if (!all && s >= len) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) o[i] = L::all(0.f);
+                }
+                if (all || s >= 0) stvec<T, VEC>(dx + s * a.o_sn, o);
                 else if (dinit) stvec<T, VEC>(dinit + (long long)(s + W - 1) * a.D, o);
             }
-        }
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < N; ++i) in[j][i] = in[U + j][i], dp[j][i] = dp[U + j][i];
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) vx[u] = vg[u] = Vec<T, VEC>{};
+        fetch(t0);
+        block(t0, std::false_type{});
+        int t = t0 + U;
+        for (; t + U <= min(live, t1); t += U) block(t, std::true_type{});
+        for (; t < last; t += U) block(t, std::false_type{});
     }
     pdl_trigger();
     // the eight runs' sums, one tap after another
@@ -329,11 +377,11 @@ int check_conv(const char* fn, const hla2_conv_args* a) {
     return HLA2_OK;
 }
 
-// Tokens of a run: as many as leave `threads` threads an SM, 8 to 64
+// Tokens of a run: as many as leave `threads` threads an SM, 8 to 128
 int run_of(const hla2_conv_args* a, int vec, int threads) {
     const long long all = (long long)a->B * ((a->D + vec - 1) / vec) * a->n, want = (long long)threads * sm_count();
-    const long long run = (all / want + kAhead - 1) / kAhead * kAhead;
-    return run < kAhead ? kAhead : run > 64 ? 64 : (int)run;
+    const long long run = (all / want + 7) / 8 * 8;
+    return run < 8 ? 8 : run > 128 ? 128 : (int)run;
 }
 // of the backward, whose grid has a row for eight runs
 int backward_run(const hla2_conv_args* a) {
@@ -352,10 +400,10 @@ struct ConvInputs {
     bool vec = true;
     int es;
     explicit ConvInputs(const hla2_conv_args* a) : es(elem_size(a->dtype)) {}
-    // a contiguous tensor; `wide`: vectors of it are read
-    void add(const void* p, size_t elems, int D, bool wide) {
+    // a contiguous tensor, of which vectors are read
+    void add(const void* p, size_t elems, int D) {
         read[reads++] = extent_of(p, elems * es);
-        if (wide && p) vec = vec && al(p, 16) && D % (16 / es) == 0;
+        if (p) vec = vec && al(p, 16) && D % (16 / es) == 0;
     }
     bool meets(const Extent& e) const {
         for (int i = 0; i < reads; ++i)
@@ -372,9 +420,9 @@ struct ConvInputs {
         if (!a->weight) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: weight must not be NULL", fn);
         if (!al(a->weight, es) || !al(a->bias, es) || !al(a->init_state, es) || !al(a->lengths, 4))
             return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
-        add(a->weight, (size_t)a->D * a->W, a->D, false);
-        add(a->bias, a->D, a->D, true);
-        add(a->init_state, (size_t)a->B * (a->W - 1) * a->D, a->D, true);
+        add(a->weight, (size_t)a->D * a->W, a->D);
+        add(a->bias, a->D, a->D);
+        add(a->init_state, (size_t)a->B * (a->W - 1) * a->D, a->D);
         read[reads++] = extent_of(a->lengths, (size_t)a->B * sizeof(int));
         return HLA2_OK;
     }
@@ -420,7 +468,7 @@ int hla2_short_conv_forward(const hla2_conv_args* a, hla2_rows out, void* final_
     p.out = const_cast<void*>(out.p), p.o_sb = out.sb, p.o_sn = out.sn;
     p.fin = final_state;
     const int v = in.vec ? 16 / in.es : 1;
-    p.run = run_of(a, v, 2048);
+    p.run = run_of(a, v, 1024);
     p.runs = a->n > 0 ? (int)(((long long)a->n + p.run - 1) / p.run) : 1;
     p.cols = (a->D + v - 1) / v;
     const long long threads = (long long)p.cols * p.runs * a->B;
@@ -452,7 +500,7 @@ int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
     if (!dweight || (a->bias != nullptr) != (dbias != nullptr))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dweight is needed, dbias with bias, and only then", fn);
-    in.add(dfinal_state, state, a->D, true);
+    in.add(dfinal_state, state, a->D);
     if (dinit_state) in.vec = in.vec && al(dinit_state, 16) && a->D % (16 / in.es) == 0;
     Extent written[4] = {extent_of(dweight, (size_t)a->D * a->W * sizeof(float)), extent_of(dbias, (size_t)a->D * sizeof(float)),
                          extent_of(dinit_state, state * in.es), {0, 0}};
