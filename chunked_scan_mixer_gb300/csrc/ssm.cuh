@@ -8,6 +8,7 @@ namespace hla2 {
 
 constexpr int kSsmChannels = 64;  // of a CTA
 constexpr int kSsmTokens = 16;    // segments are multiples of it
+constexpr int kSsmMark = 16;      // tokens between the marks of a backward
 
 // One tensor [B, n, D]: address and the element strides of batch and token
 struct SsmRows {

@@ -129,7 +129,7 @@ Scratch scratch_of(const hla2_ssm_args* a, const SsmPlan& p, bool backward) {
         s.steps = s.total, s.total += up256(slots * kSsmChannels * sizeof(float));
     }
     if (backward) {
-        const size_t marks = slots * (p.seg_tokens / kSsmTokens), state = kSsmChannels * a->N * sizeof(float);
+        const size_t marks = slots * (p.seg_tokens / kSsmMark), state = kSsmChannels * a->N * sizeof(float);
         s.marks = s.total, s.total += up256(marks * state);
         if (p.nseg > 1) {
             s.mark_steps = s.total, s.total += up256(marks * kSsmChannels * sizeof(float));
@@ -270,7 +270,7 @@ int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfina
     if (a->gate.p) g.dgate = dev(o[5]);
     g.da = grads->da, g.dskip = grads->dskip, g.ddt_bias = grads->ddt_bias, g.dinit = grads->dinit_state;
     g.dfinal = dfinal_state;
-    g.macros = pl.seg_tokens / kSsmTokens;
+    g.macros = pl.seg_tokens / kSsmMark;
     auto at = [&](size_t offset) { return reinterpret_cast<float*>(static_cast<char*>(a->workspace) + offset); };
     g.marks = at(s.marks), g.bc = at(s.bc), g.params = at(s.params);
     if (pl.nseg > 1) p.sums = at(s.sums), p.steps = at(s.steps), g.mark_steps = at(s.mark_steps), g.rsums = at(s.rsums);

@@ -16,14 +16,14 @@
 namespace hla2 {
 namespace {
 
-constexpr int kMacro = kSsmTokens;  // tokens between marks
+constexpr int kMacro = kSsmMark;  // tokens between marks
 constexpr int kBack = 4;            // tokens whose states are in registers
 
 // Marks and sums of a segment.  REV: there are several segments, the states start from zero and R's sums are formed too.
 template <typename T, int V, int N, bool REV>
 __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threads)
     ssm_marks_kernel(const SsmPass p, const SsmGrads g) {
-    constexpr int NT = SsmShape<N>::threads, SL = SsmShape<N>::lanes, TT = SsmShape<N>::tokens, CT = kSsmChannels;
+    constexpr int NT = SsmShape<N>::threads, SL = SsmShape<N>::lanes, TT = SsmShape<N>::tokens < kMacro ? SsmShape<N>::tokens : kMacro, CT = kSsmChannels;
     using L = Lanes<V>;
     using P = typename L::P;
     __shared__ __align__(16) float sd[TT][CT], su[TT][CT], sy[REV ? TT : 1][CT], sb[TT][2 * N], sc[REV ? TT : 1][2 * N], sbias[CT];
