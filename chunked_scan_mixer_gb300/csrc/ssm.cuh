@@ -121,14 +121,10 @@ __device__ __forceinline__ P all_(float f) {
     else return pair(f, f);
 }
 
-// e^-|x| to about 2^-22 relative (e^-120 below that): x log2 e in two parts, as its rounding alone would cost |x| 2^-24.
-// P: a float, or a pair of them
+// e^-|x| (e^-120 below that), to 2^-22 + 2^-24 |x| relative.  P: a float, or a pair of them
 template <typename P>
 __device__ __forceinline__ P exp_neg_abs(P x) {
-    const P m = neg_abs(x), nt = m * all_<P>(-kLog2E);
-    const P lo = fma_(m, all_<P>(1.925963033500e-8f), fma_(m, all_<P>(kLog2E), nt));
-    const P e = ex2_neg(nt);
-    return fma_(e, lo * all_<P>(kLn2), e);
+    return ex2_neg(neg_abs(x) * all_<P>(-kLog2E));
 }
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x|; log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3: s times a polynomial
 // in s^2 fitted to 2 artanh(s) / s over that range, 8e-9 off at most.  (log of a rounded 1 + e would lose the small
@@ -177,10 +173,15 @@ struct Tile {
     }
     // rows t0 .. t_end of p, columns up to `cols`; zeros elsewhere
     __device__ __forceinline__ void load(const T* p, long long sn, int t0, int t_end, int cols) {
-        parts([&](int k, int r, int c) {
-            v[k] = Vec<T, V>{};
-            if (t0 + r < t_end && c < cols) v[k] = ldvec<T, V>(p + (long long)(t0 + r) * sn + c);
-        });
+        const T* at = p + t0 * sn;
+        if (t0 + ROWS <= t_end && cols == COLS) {  // the same for the whole CTA
+            parts([&](int k, int r, int c) { v[k] = ldvec<T, V>(at + r * sn + c); });
+        } else {
+            parts([&](int k, int r, int c) {
+                v[k] = Vec<T, V>{};
+                if (t0 + r < t_end && c < cols) v[k] = ldvec<T, V>(at + r * sn + c);
+            });
+        }
     }
 };
 
@@ -214,7 +215,7 @@ __device__ __forceinline__ void put_twice(float* p, const P (&f)[N]) {
     }
 }
 
-// delta, delta x and, with DY, dout silu(gate) of a thread's part of a tile
+// delta, delta x and, with DY, dout silu(gate) of a thread's part of a tile; delta 0 where there is no token or channel (`on`)
 template <typename T, int V, bool DY>
 __device__ __forceinline__ void stage(const Vec<T, V>& x, const Vec<T, V>& dt, const Vec<T, V>& dout, const Vec<T, V>& z, bool gated,
                                       bool softplus, bool on, const float* bias, float* sd, float* su, float* sy) {
