@@ -137,17 +137,15 @@ __global__ void __launch_bounds__(128, 4) conv_kernel(const ConvPass a) {
     }
 }
 
-// Eight runs a CTA, 32 vectors of channels
+// Eight runs a CTA at a time, 32 vectors of channels
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a) {
+__global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a, int rows) {
     using L = Lanes<VEC>;
     using P = typename L::P;
     constexpr int N = L::N;
     __shared__ float sums[8][32 * VEC + 1];
     pdl_wait();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = (blockIdx.x * 32 + lane) * VEC;
-    const int per_b = (a.runs + 7) / 8, b = blockIdx.y / per_b, run = (blockIdx.y - b * per_b) * 8 + w;
-    const bool on = c < a.D && run < a.runs;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = (blockIdx.y * 32 + lane) * VEC, per_b = (a.runs + 7) / 8;
     P taps[W][N], bias[N], dw[W][N], db[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -155,7 +153,13 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a)
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[j][i] = L::all(0.f);
     }
-    if (on) {
+    if (c < a.D) {
+        load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
+        if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), bias);
+    }
+    for (int row = blockIdx.x; row < rows; row += gridDim.x) {
+        const int b = row / per_b, run = (row - b * per_b) * 8 + w;
+        if (c >= a.D || run >= a.runs) continue;
         const int len = length_of(a.lengths, b, a.n), t0 = run * a.run, t1 = min(t0 + a.run, a.n);
         const T *x = static_cast<const T*>(a.x) + b * a.x_sb + c, *dout = static_cast<const T*>(a.dout) + b * a.g_sb + c;
         T* dx = static_cast<T*>(a.out) + b * a.o_sb + c;
@@ -163,8 +167,6 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a)
         const T *init = a.init ? static_cast<const T*>(a.init) + at : nullptr,
                 *dfin = a.dfinal ? static_cast<const T*>(a.dfinal) + at : nullptr;
         T* dinit = a.fin ? static_cast<T*>(a.fin) + at : nullptr;
-        load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
-        if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), bias);
         constexpr int U = kAhead;
         P in[W - 1 + U][N], dp[W - 1 + U][N];  // inputs and dp's: the last W - 1, and those of a block
 #pragma unroll
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a)
     }
     pdl_trigger();
     // the eight runs' sums, one tap after another
-    float* dst = a.partial + (long long)blockIdx.y * a.D * (W + 1);
+    float* dst = a.partial + (long long)blockIdx.x * a.D * (W + 1);
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
 #pragma unroll
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a)
             float s = 0.f;
 #pragma unroll
             for (int r = 0; r < 8; ++r) s += sums[r][k];
-            const int ch = (blockIdx.x * 32 + k % 32) * VEC + k / 32;
+            const int ch = (blockIdx.y * 32 + k % 32) * VEC + k / 32;
             if (ch < a.D) dst[(long long)j * a.D + ch] = s;
         }
         __syncthreads();
@@ -372,8 +374,9 @@ int check_conv(const char* fn, const hla2_conv_args* a) {
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: B, n and D must not be negative", fn);
     if (a->W < 2 || a->W > 4) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: W must be 2, 3 or 4 (got %d)", fn, a->W);
     if (a->silu != 0 && a->silu != 1) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: silu must be 0 or 1", fn);
-    if ((long long)a->B * a->D > 0x7fffffffLL || a->n > 1 << 30)
-        return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: B * D must fit in 31 bits, and n be at most 2^30", fn);
+    // the grids' limits: columns of 32 channels, and rows of at least 64 tokens or a sequence
+    if ((long long)a->B * a->D > 0x7fffffffLL || a->D > 1 << 20 || a->n > 1 << 30 || (long long)a->B * ((a->n + 63LL) / 64) > 0x7fffffffLL)
+        return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: B * D and B * n / 64 must fit in 31 bits, D be at most 2^20 and n 2^30", fn);
     return HLA2_OK;
 }
 
@@ -383,15 +386,20 @@ int run_of(const hla2_conv_args* a, int vec, int threads) {
     const long long run = (all / want + 7) / 8 * 8;
     return run < 8 ? 8 : run > 128 ? 128 : (int)run;
 }
-// of the backward, whose grid has a row for eight runs
-int backward_run(const hla2_conv_args* a) {
-    int run = run_of(a, 4, 768);
-    while ((long long)a->B * ((a->n + 8LL * run - 1) / (8LL * run)) > 65535) run *= 2;
-    return run;
-}
-int backward_rows(const hla2_conv_args* a) {
-    const int run = backward_run(a), runs = (int)(((long long)a->n + run - 1) / run);
-    return a->B * ((runs + 7) / 8);
+// The backward's runs, rows of eight of them, and the partial rows of its CTAs, who take several rows where there are more than
+// fill the GPU four times (two CTAs an SM): the partial rows would be larger than the inputs with many short sequences.
+struct ConvRows {
+    int run, runs, rows, partials;
+};
+ConvRows backward_rows(const hla2_conv_args* a) {
+    ConvRows r{};
+    r.run = run_of(a, 4, 768);
+    r.runs = (int)(((long long)a->n + r.run - 1) / r.run);
+    const long long rows = (long long)a->B * ((r.runs + 7) / 8), tiles = (a->D + 127) / 128;
+    const long long most = tiles ? (8LL * sm_count() + tiles - 1) / tiles : 0;
+    r.rows = (int)rows;
+    r.partials = (int)(rows < most ? rows : most);
+    return r;
 }
 
 struct ConvInputs {
@@ -484,7 +492,7 @@ int hla2_short_conv_forward(const hla2_conv_args* a, hla2_rows out, void* final_
 size_t hla2_short_conv_backward_workspace_bytes(const hla2_conv_args* a) {
     if (check_conv("hla2_short_conv_backward_workspace_bytes", a) != HLA2_OK) return (size_t)-1;
     ok();
-    return (size_t)backward_rows(a) * a->D * (a->W + 1) * sizeof(float);
+    return (size_t)backward_rows(a).partials * a->D * (a->W + 1) * sizeof(float);
 }
 
 int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void* dfinal_state, hla2_rows dx, float* dweight,
@@ -524,24 +532,23 @@ int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void
     p.dout = dout.p, p.g_sb = dout.sb, p.g_sn = dout.sn;
     p.fin = dinit_state, p.dfinal = dfinal_state;
     p.partial = static_cast<float*>(a->workspace);
-    p.run = backward_run(a);
-    p.runs = (int)(((long long)a->n + p.run - 1) / p.run);
-    const int grid_rows = backward_rows(a);
+    const ConvRows r = backward_rows(a);
+    p.run = r.run, p.runs = r.runs;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     int rc = 0;
-    if (grid_rows > 0)
+    if (r.partials > 0)
         rc = with_conv<4>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
             using T = decltype(zero);
             constexpr int V = decltype(vec)::value;
-            return launch_pdl(conv_backward_kernel<T, V, decltype(taps)::value>, dim3((a->D + 32 * V - 1) / (32 * V), grid_rows),
-                              dim3(256), 0, st, p) == cudaSuccess ? 0 : -1;
+            return launch_pdl(conv_backward_kernel<T, V, decltype(taps)::value>, dim3(r.partials, (a->D + 32 * V - 1) / (32 * V)),
+                              dim3(256), 0, st, p, r.rows) == cudaSuccess ? 0 : -1;
         });
     else if (dinit_state && a->B > 0)  // no tokens: the state after the last is the one before the first
         rc = (dfinal_state ? cudaMemcpyAsync(dinit_state, dfinal_state, state * in.es, cudaMemcpyDeviceToDevice, st)
                            : cudaMemsetAsync(dinit_state, 0, state * in.es, st)) == cudaSuccess ? 0 : -1;
     const long long cols = (long long)a->D * (a->W + 1);
     if (rc == 0)
-        rc = launch_pdl(conv_sums_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(512), 0, st, p, grid_rows, dweight, dbias) == cudaSuccess
+        rc = launch_pdl(conv_sums_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(512), 0, st, p, r.partials, dweight, dbias) == cudaSuccess
                  ? 0 : -1;
     return rc ? launch_failed("short convolution gradients") : ok();
 }

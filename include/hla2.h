@@ -620,7 +620,7 @@ int hla2_ssm_decode_step(const hla2_ssm_args* a, float* state, hla2_rows out, hl
  */
 typedef struct {
     int dtype;              /* HLA2_F32 | HLA2_BF16: every tensor but the sums of a backward */
-    int B, n, D, W;
+    int B, n, D, W;         /* 0 <= n <= 2^30, D <= 2^20                                      */
     int silu;               /* 0 or 1                                                         */
     hla2_rows x;            /* [B, n, D]                                                      */
     const void *weight, *bias; /* contiguous [D, W]; [D], nullable                            */

@@ -133,3 +133,21 @@ def test_captured():
         graph.replay()
         for u, w in zip((out, *grads), want):
             assert torch.equal(u, w)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_many_short_sequences(dtype):
+    """More sequences than a grid has rows, and so several to a CTA."""
+    c, dout, dfin = make(70_000, 1, 8, 4, dtype)
+    g = hla.short_conv_backward(dout=dout, dfinal_state=dfin, **c)
+    out, fin = hla.short_conv_forward(**c, return_final_state=True)
+    kw = dict(bias=f64(c["bias"]), init_state=f64(c["init_state"]))
+    want, wfin = O.conv_forward(f64(c["x"]), f64(c["weight"]), **kw)
+    close(out, want, "out", 1e-5)
+    assert np.array_equal(f64(fin), wfin)
+    w = O.conv_backward(f64(c["x"]), f64(c["weight"]), f64(dout), dfinal_state=f64(dfin), **kw)
+    for name in g._fields:  # 70000 terms in 152 * 8 partial sums and more: within the bound of 4000
+        close(getattr(g, name), w[name], name, 1e-5)
+    state = c["init_state"].clone()
+    assert torch.equal(hla.short_conv_decode_step(state, c["x"][:, 0], c["weight"], bias=c["bias"]), out[:, 0])
+    assert torch.equal(state, fin)

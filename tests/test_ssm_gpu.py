@@ -239,3 +239,25 @@ def test_captured():
         graph.replay()
         for u, v in zip((out, fin, *grads), want):
             assert torch.equal(u, v)
+
+
+def test_many_short_sequences():
+    """More sequences than a grid has rows."""
+    c = make_ssm(70_000, 1, 4, 8, gate=False)
+    out, fin = check_forward(c)
+    check_backward(c)
+    state = c["init_state"].clone()
+    one = {k: c[k][:, 0] for k in ("x", "dt", "b", "c")}
+    y = hla.ssm_decode_step(state, a=c["a"], skip=c["skip"], dt_bias=c["dt_bias"], **one)
+    close(y, f64(out[:, 0]), "step", 1e-5)
+    close(state, f64(fin), "state", 1e-5)
+    # and more than four to a CTA's sequences in one launch
+    c = make_ssm(4 * 65_535 + 3, 1, 64, 8, gate=False, state=False, seed=2)
+    one = {k: c[k][:, 0] for k in ("x", "dt", "b", "c")}
+    state = torch.zeros(4 * 65_535 + 3, 64, 8, device="cuda")
+    y = hla.ssm_decode_step(state, a=c["a"], skip=c["skip"], dt_bias=c["dt_bias"], **one)
+    tail = {k: v[-5:] for k, v in one.items()}
+    last = torch.zeros(5, 64, 8, device="cuda")
+    w = hla.ssm_decode_step(last, a=c["a"], skip=c["skip"], dt_bias=c["dt_bias"], **tail)
+    close(y[-5:], f64(w), "step", 1e-5)
+    close(state[-5:], f64(last), "state", 1e-5)
