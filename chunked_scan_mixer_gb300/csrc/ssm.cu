@@ -4,7 +4,8 @@
 // A CTA (ssm.cuh) walks over the tokens of one segment with its states in registers.  Sixteen tokens at a time are
 // staged: delta, delta x and the pairs of b and c in shared memory; x and the gate wait in registers for the output.
 // Where the channels alone do not fill the GPU the sequence is cut into segments: a first pass forms each segment's state
-// from zero and its sum of steps, and the output pass starts from exp(a sum) of those before (ssm_api.cu has the rule).
+// from zero and its sum of steps, and the output pass starts from those before, h before the next = exp(a sum) h + state
+// (ssm_api.cu has the rule).
 #include "ssm.cuh"
 
 namespace hla2 {
@@ -32,12 +33,11 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
     Chan xn, dn, xc, zc;
     Stat bn, cn;
     auto fetch = [&](int t0) {
-        xn.load(x, p.x.sn, t0, at.live_end, at.cols);
-        dn.load(dt, p.dt.sn, t0, at.live_end, at.cols);
-        bn.load(b, p.b.sn, t0, at.live_end, N);
-        if (!SUMS) cn.load(c, p.c.sn, t0, at.live_end, N);
+        xn.template load<false>(x, p.x.sn, t0, at.live_end, at.cols);
+        dn.template load<false>(dt, p.dt.sn, t0, at.live_end, at.cols);
+        bn.template load<false>(b, p.b.sn, t0, at.live_end, N);
+        if (!SUMS) cn.template load<false>(c, p.c.sn, t0, at.live_end, N);
     };
-    fetch(at.t0);
     for (int i = tid; i < CT; i += NT) {
         sskip[i] = p.skip && i < at.cols ? p.skip[at.c0 + i] : 0.f;
         sbias[i] = p.dt_bias && i < at.cols ? p.dt_bias[at.c0 + i] : 0.f;
@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
         if (p.init) h.load(p.init + ((long long)at.b * p.D + at.c0 + 4 * cg) * N + 4 * sl, N, chans);
         join_segments<N>(p, at, h, a, p.sums, cg, 0, at.seg, 1);
     }
+    fetch(at.t0);
     F2 sum01 = pair(0.f, 0.f), sum23 = sum01;
     __syncthreads();
     for (int t0 = at.t0; t0 < at.live_end; t0 += TT) {
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
         });
         if (!SUMS) {
             xc = xn;
-            if (z) zc.load(z, p.gate.sn, t0, at.live_end, at.cols);
+            if (z) zc.template load<false>(z, p.gate.sn, t0, at.live_end, at.cols);
         }
         fetch(t0 + TT);
         __syncthreads();
@@ -134,11 +135,64 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
     if (p.fin && at.seg == p.nseg - 1) h.store(p.fin + ((long long)at.b * p.D + at.c0 + 4 * cg) * N + 4 * sl, N, chans);
 }
 
+// ---- the states before the segments ---------------------------------------------------------
+//
+// A warp has one state of four channels, a thread's sixteen bytes in the sums, and its lanes are segments: 32 at a time, whose
+// pairs (decay, sum) join in five steps.  All loads of a batch are in flight together, where a CTA of the output pass that joins the
+// segments before it waits for them four at a time.
+template <int N>
+__global__ void __launch_bounds__(256) ssm_carry_kernel(const SsmPass p, float* __restrict__ rsums, const float* __restrict__ dfinal) {
+    constexpr int NT = SsmShape<N>::threads, SL = SsmShape<N>::lanes, CT = kSsmChannels;
+    const int lane = threadIdx.x & 31, unit = blockIdx.y * 8 + (threadIdx.x >> 5), k = unit / NT, t = unit % NT;
+    const int sl = t % SL, cg = t / SL, tiles = p.G * p.tiles, b = blockIdx.x / tiles, tile = blockIdx.x - b * tiles, group = tile / p.tiles;
+    const int in = (tile - group * p.tiles) * CT + 4 * cg, ch = group * p.per + in;
+    const bool rev = blockIdx.z;
+    float* sums = (rev ? rsums : p.sums) + ((long long)k * NT + t) * 4;
+    const float* from = rev ? dfinal : p.init;
+    pdl_wait();
+    float a[4], h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const bool on = in + j < p.per;
+        const long long at = (long long)(ch + j) * N + 4 * sl + k;
+        a[j] = on ? p.a[at] * kLog2E : 0.f;
+        h[j] = on && from ? from[(long long)b * p.D * N + at] : 0.f;
+    }
+    for (int first = 0; first < p.nseg; first += 32) {
+        const int i = first + lane, seg = rev ? p.nseg - 1 - i : i;
+        const long long slot = (long long)blockIdx.x * p.nseg + seg;
+        float d[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+        if (i < p.nseg - 1) {  // nothing comes after the last
+            const float4 v = *reinterpret_cast<const float4*>(sums + slot * (CT * N));
+            const float4 steps = *reinterpret_cast<const float4*>(p.steps + slot * CT + 4 * cg);
+            s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+            d[0] = fast_exp2(steps.x * a[0]), d[1] = fast_exp2(steps.y * a[1]), d[2] = fast_exp2(steps.z * a[2]), d[3] = fast_exp2(steps.w * a[3]);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float pd = __shfl_up_sync(0xffffffffu, d[j], o), ps = __shfl_up_sync(0xffffffffu, s[j], o);
+                if (lane >= o) s[j] = fmaf(d[j], ps, s[j]), d[j] *= pd;
+            }
+        float start[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float pd = __shfl_up_sync(0xffffffffu, d[j], 1), ps = __shfl_up_sync(0xffffffffu, s[j], 1);
+            start[j] = lane ? fmaf(pd, h[j], ps) : h[j];
+            h[j] = fmaf(__shfl_sync(0xffffffffu, d[j], 31), h[j], __shfl_sync(0xffffffffu, s[j], 31));
+        }
+        if (i < p.nseg) *reinterpret_cast<float4*>(sums + slot * (CT * N)) = make_float4(start[0], start[1], start[2], start[3]);
+    }
+    pdl_trigger();
+}
+
 template <typename T, int V, int N>
 int forward_n(const SsmPass& p, cudaStream_t st) {
     const dim3 block(SsmShape<N>::threads);
     if (p.nseg > 1 &&
-        launch_pdl(ssm_kernel<T, V, N, true>, dim3(p.B * p.G * p.tiles, p.nseg - 1), block, 0, st, p) != cudaSuccess)
+        (launch_pdl(ssm_kernel<T, V, N, true>, dim3(p.B * p.G * p.tiles, p.nseg - 1), block, 0, st, p) != cudaSuccess ||
+         (p.nseg > kSsmJoin && launch_ssm_carry(p, nullptr, nullptr, st))))
         return -1;
     return launch_pdl(ssm_kernel<T, V, N, false>, dim3(p.B * p.G * p.tiles, p.nseg), block, 0, st, p) == cudaSuccess ? 0 : -1;
 }
@@ -282,6 +336,19 @@ int step_v(const SsmPass& p, float* state, cudaStream_t st) {
 }
 
 }  // namespace
+
+int launch_ssm_carry(const SsmPass& p, float* rsums, const float* dfinal, cudaStream_t st) {
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3(p.B * p.G * p.tiles, 2 * p.N, rsums ? 2 : 1), dim3(256), 0, st, p, rsums, dfinal) == cudaSuccess ? 0 : -1;
+    };
+    switch (p.N) {
+        case 8: return go(ssm_carry_kernel<8>);
+        case 16: return go(ssm_carry_kernel<16>);
+        case 32: return go(ssm_carry_kernel<32>);
+        case 64: return go(ssm_carry_kernel<64>);
+        default: return -1;
+    }
+}
 
 int launch_ssm_forward(const SsmPass& p, bool is_bf16, bool vec, cudaStream_t st) {
     if (is_bf16) return vec ? forward_v<bf16, 4>(p, st) : forward_v<bf16, 1>(p, st);

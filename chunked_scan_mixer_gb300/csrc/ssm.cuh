@@ -46,6 +46,8 @@ struct SsmGrads {
 };
 
 // Launchers; 0, or -1 where a launch failed.
+// The segments' sums become the states before them; with rsums also the gradients of the states after them, dfinal after the last
+int launch_ssm_carry(const SsmPass& p, float* rsums, const float* dfinal, cudaStream_t st);
 int launch_ssm_backward(const SsmPass& p, const SsmGrads& g, bool is_bf16, bool vec, cudaStream_t st);
 int launch_ssm_forward(const SsmPass& p, bool is_bf16, bool vec, cudaStream_t st);
 int launch_ssm_step(const SsmPass& p, float* state, bool is_bf16, bool vec, cudaStream_t st);
@@ -171,10 +173,13 @@ struct Tile {
             if (all % THREADS == 0 || i < all) f(k, i / vecs, i % vecs * V);
         }
     }
-    // rows t0 .. t_end of p, columns up to `cols`; zeros elsewhere
+    // Rows t0 .. t_end of p, columns up to `cols`; zeros elsewhere.  SPLIT: whole tiles without conditions, a path of its own.  The
+    // backward gains by it, 4 x 4096 x 2048 937 -> 910 us; where the loads run ahead of the work, as in the forward, it costs: one
+    // segment of 2 x 2048 x 2048 350 -> 360, two 289 -> 340.
+    template <bool SPLIT>
     __device__ __forceinline__ void load(const T* p, long long sn, int t0, int t_end, int cols) {
         const T* at = p + t0 * sn;
-        if (t0 + ROWS <= t_end && cols == COLS) {  // the same for the whole CTA
+        if (SPLIT && t0 + ROWS <= t_end && cols == COLS) {  // the same for the whole CTA
             parts([&](int k, int r, int c) { v[k] = ldvec<T, V>(at + r * sn + c); });
         } else {
             parts([&](int k, int r, int c) {
@@ -349,8 +354,13 @@ struct SsmPlace {
     __device__ __forceinline__ long long slot(const SsmPass& p, int s) const { return (long long)blockIdx.x * p.nseg + s; }
 };
 
-// The state s before a segment from those of the segments between, first to last by dir: sums from zero of each, and its decay
-// exp(a steps).  Four segments' loads are in flight together.
+// Up to this many segments a CTA joins those before (or after) its own itself; more are joined by a scan of their own, which
+// writes each segment's state in the place of its sum.  (2 x 2048 x 2048, forward, 16 segments: 88 us and 93 with the scan; 32: 87
+// and 89; 1 x 8192 x 64, 128 segments: 42 and 25.)
+constexpr int kSsmJoin = 32;
+
+// The state s before segment `last` from those of the segments between, `first` on in the direction dir: sums from zero of each,
+// and its decay exp(a steps).  Four segments' loads are in flight together.
 template <int N>
 __device__ __forceinline__ void join_segments(const SsmPass& p, const SsmPlace& at, SsmState& s, const SsmState& a, const float* sums,
                                               int cg, int first, int last, int dir) {
@@ -363,6 +373,10 @@ __device__ __forceinline__ void join_segments(const SsmPass& p, const SsmPlace& 
         }
     };
     int i = first;
+    if (p.nseg > kSsmJoin) {
+        i = last;
+        s.get(sums + at.slot(p, last) * (CT * N), NT);
+    }
     for (; (last - i) * dir >= 4; i += 4 * dir) {
         SsmState w[4];
         SsmPair2 steps[4];

@@ -92,10 +92,10 @@ struct SsmPlan {
 // (2 x 2048 x 2048, N = 16, forward: one segment 363 us, 8 105, 16 89, 64 107; backward 1299, 282, 274, 311.  8 x 4096 x 4096, which
 // fills the GPU by itself: forward 939 with one, 1050 with 8.)
 struct SsmCost {
-    double alone, beside, sums, marks, join;
+    double alone, beside, sums, marks;
     int most;
 };
-constexpr SsmCost kForwardCost{2.8, 0.9, 0.55, 0.0, 0.012, 7}, kBackwardCost{9.5, 3.0, 0.4, 0.2, 0.01, 4};
+constexpr SsmCost kForwardCost{2.8, 0.9, 0.55, 0.0, 7}, kBackwardCost{9.5, 3.0, 0.4, 0.2, 4};
 
 SsmPlan ssm_plan(const hla2_ssm_args* a, bool backward) {
     SsmPlan p{(a->D / a->G + kSsmChannels - 1) / kSsmChannels, 1, kSsmTokens};
@@ -109,7 +109,8 @@ SsmPlan ssm_plan(const hla2_ssm_args* a, bool backward) {
         const double per_sm = ctas * nseg / sms;
         const double full = per_sm <= most ? std::ceil(per_sm) : 0.5 * (per_sm + most * std::ceil(per_sm / most));
         const double load = full * beside > c.alone ? full * beside : c.alone;
-        const double cost = nseg == 1 ? each * load * (1 + c.marks) : load * (each * (1 + c.sums) + c.join * nseg) + 6 + 0.2 * nseg;
+        const double cost = nseg == 1 ? each * load * (1 + c.marks)
+                                      : (each + 0.45) * load * (1 + c.sums) + 6 + (nseg <= kSsmJoin ? 0.2 * nseg : 6.0);
         if (want == 1 || cost < best) best = cost, p.nseg = nseg, p.seg_tokens = each * kSsmTokens;
     }
     return p;

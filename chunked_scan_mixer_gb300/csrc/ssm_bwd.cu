@@ -61,13 +61,13 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
         {
             Chan xr, dr, zr, or_;
             Stat br, cr;
-            xr.load(x, p.x.sn, t0, at.live_end, at.cols);
-            dr.load(dt, p.dt.sn, t0, at.live_end, at.cols);
-            br.load(b, p.b.sn, t0, at.live_end, N);
+            xr.template load<true>(x, p.x.sn, t0, at.live_end, at.cols);
+            dr.template load<true>(dt, p.dt.sn, t0, at.live_end, at.cols);
+            br.template load<true>(b, p.b.sn, t0, at.live_end, N);
             if (REV) {
-                or_.load(dout, g.dout.sn, t0, at.live_end, at.cols);
-                if (z) zr.load(z, p.gate.sn, t0, at.live_end, at.cols);
-                cr.load(c, p.c.sn, t0, at.live_end, N);
+                or_.template load<true>(dout, g.dout.sn, t0, at.live_end, at.cols);
+                if (z) zr.template load<true>(z, p.gate.sn, t0, at.live_end, at.cols);
+                cr.template load<true>(c, p.c.sn, t0, at.live_end, N);
             }
             Chan::parts([&](int k, int r, int ch) {
                 stage<T, V, REV>(xr.v[k], dr.v[k], or_.v[k], zr.v[k], z, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
@@ -164,8 +164,10 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
     E.zero();
     if (p.init) h.load(p.init + state_at, N, chans);
     if (g.dfinal) E.load(g.dfinal + state_at, N, chans);
-    join_segments<N>(p, at, h, a, p.sums, cg, 0, at.seg, 1);
-    join_segments<N>(p, at, E, a, g.rsums, cg, p.nseg - 1, at.seg, -1);
+    if (p.nseg > 1) {
+        join_segments<N>(p, at, h, a, p.sums, cg, 0, at.seg, 1);
+        join_segments<N>(p, at, E, a, g.rsums, cg, p.nseg - 1, at.seg, -1);
+    }
     h.put(sst, NT);
     const T *x = static_cast<const T*>(p.x.p) + at.b * p.x.sb + at.c0, *dt = static_cast<const T*>(p.dt.p) + at.b * p.dt.sb + at.c0,
             *z = p.gate.p ? static_cast<const T*>(p.gate.p) + at.b * p.gate.sb + at.c0 : nullptr,
@@ -206,12 +208,12 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
         {
             Chan xr, dr, zr, or_;
             Stat br, cr;
-            xr.load(x, p.x.sn, t0, at.live_end, at.cols);
-            dr.load(dt, p.dt.sn, t0, at.live_end, at.cols);
-            or_.load(dout, g.dout.sn, t0, at.live_end, at.cols);
-            if (z) zr.load(z, p.gate.sn, t0, at.live_end, at.cols);
-            br.load(b, p.b.sn, t0, at.live_end, N);
-            cr.load(c, p.c.sn, t0, at.live_end, N);
+            xr.template load<true>(x, p.x.sn, t0, at.live_end, at.cols);
+            dr.template load<true>(dt, p.dt.sn, t0, at.live_end, at.cols);
+            or_.template load<true>(dout, g.dout.sn, t0, at.live_end, at.cols);
+            if (z) zr.template load<true>(z, p.gate.sn, t0, at.live_end, at.cols);
+            br.template load<true>(b, p.b.sn, t0, at.live_end, N);
+            cr.template load<true>(c, p.c.sn, t0, at.live_end, N);
             Chan::parts([&](int k, int r, int ch) {
                 stage<T, V, true>(xr.v[k], dr.v[k], or_.v[k], zr.v[k], z, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
                                   sd + r * CT + ch, su + r * CT + ch, sy + r * CT + ch);
@@ -479,7 +481,9 @@ int backward_n(const SsmPass& p, const SsmGrads& g, cudaStream_t st) {
     if (p.B == 0) return params();  // zeros
     const dim3 block(SsmShape<N>::threads), grid(p.B * p.G * p.tiles, p.nseg);
     if (p.nseg > 1) {
-        if (launch_pdl(ssm_marks_kernel<T, V, N, true>, grid, block, 0, st, p, g) != cudaSuccess) return -1;
+        if (launch_pdl(ssm_marks_kernel<T, V, N, true>, grid, block, 0, st, p, g) != cudaSuccess ||
+            (p.nseg > kSsmJoin && launch_ssm_carry(p, g.rsums, g.dfinal, st)))
+            return -1;
     } else if (g.macros > 1) {
         if (launch_pdl(ssm_marks_kernel<T, V, N, false>, grid, block, 0, st, p, g) != cudaSuccess) return -1;
     }
