@@ -86,7 +86,7 @@ struct SsmPlan {
 // Segments of each sequence, by the time in us of sixteen tokens in a CTA of the main pass: `alone` with the SM to itself,
 // and `beside` for each CTA once they fill it (measured at N = 16 over 1 to 128 segments of 32 to 512 tiles of channels;
 // the part of it that goes with the states, here 0.55 of it, goes with N).  An SM holds `most` CTAs (of 64 threads): up to
-// there the fullest SM counts, above it the waves count half, as they overlap.  More than one segment adds the pass of
+// there the fullest SM counts, above it they follow one another without waves.  More than one segment adds the pass of
 // their sums, a launch, and the joining of the segments before, which a CTA reads four at a time; the backward has a pass
 // of marks without them too.
 // (2 x 2048 x 2048, N = 16, forward: one segment 363 us, 8 105, 16 89, 64 107; backward 1299, 282, 274, 311.  8 x 4096 x 4096, which
@@ -107,7 +107,7 @@ SsmPlan ssm_plan(const hla2_ssm_args* a, bool backward) {
     for (int want = 1; want <= steps && want <= 1024; want = want < 4 ? want + 1 : want * 5 / 4) {
         const int each = (steps + want - 1) / want, nseg = (steps + each - 1) / each;
         const double per_sm = ctas * nseg / sms;
-        const double full = per_sm <= most ? std::ceil(per_sm) : 0.5 * (per_sm + most * std::ceil(per_sm / most));
+        const double full = per_sm <= most ? std::ceil(per_sm) : 0.87 * per_sm + 1.2;
         const double load = full * beside > c.alone ? full * beside : c.alone;
         const double cost = nseg == 1 ? each * load * (1 + c.marks)
                                       : (each + 0.45) * load * (1 + c.sums) + 6 + (nseg <= kSsmJoin ? 0.2 * nseg : 6.0);
