@@ -7,6 +7,10 @@
 // A thread has one vector of channels and walks over a run of tokens with the last W - 1 inputs (and dp's) in registers,
 // several tokens' loads ahead; the runs' edges are read twice.  The backward's sums of a thread go through shared memory to
 // one partial row a CTA, which a second kernel adds in a fixed order.
+//
+// 65536 x 2048 bf16, W = 4: 93 us (5.7 TB/s, 85 % of the measured copy).  Four tokens a block without conditions, the inputs of a block
+// in place instead of a window that moves: 132 us before, with 35 instructions for two values instead of 16.  Backward of 8 x 4096 x 2048:
+// 102 us (4.0 TB/s): instructions, at two CTAs an SM (107 us; 137 with one, 325 with three, which spill).
 #include <type_traits>
 
 #include "packed.cuh"

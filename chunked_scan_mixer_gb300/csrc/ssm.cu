@@ -6,6 +6,11 @@
 // Where the channels alone do not fill the GPU the sequence is cut into segments: a first pass forms each segment's state
 // from zero and its sum of steps, and the output pass starts from those before, h before the next = exp(a sum) h + state
 // (ssm_api.cu has the rule).
+//
+// Instructions bound it, not bytes: a state and token take two products, two multiply-adds and an exponential, whose register reads
+// alone take half of the time, and a channel and token about 60 instructions more for its step, gate and staging.  4 x 4096
+// tokens of 2048 channels, N = 16, bf16: sums 114 us and outputs 188 (2.9e12 states a second; memory alone 40 us, the
+// exponentials 57); one segment of 8 x 4096 x 4096 924 us.
 #include "ssm.cuh"
 
 namespace hla2 {

