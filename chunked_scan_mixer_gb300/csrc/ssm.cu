@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
                 for (int j = 0; j < 2; ++j) {
                     F2(&hk)[2] = h.v[k + j];
                     const F2 bk = j ? bb.hi : bb.lo, ck = j ? cc.hi : cc.lo;
-                    hk[0] = fma_(ex2_(d.lo * a.v[k + j][0]), hk[0], u.lo * bk);
-                    hk[1] = fma_(ex2_(d.hi * a.v[k + j][1]), hk[1], u.hi * bk);
+                    hk[0] = fma_(decay_of(d.lo, a.v[k + j][0]), hk[0], u.lo * bk);
+                    hk[1] = fma_(decay_of(d.hi, a.v[k + j][1]), hk[1], u.hi * bk);
                     if (!SUMS) y01 = k + j ? fma_(hk[0], ck, y01) : hk[0] * ck, y23 = k + j ? fma_(hk[1], ck, y23) : hk[1] * ck;
                 }
             }
@@ -273,10 +273,10 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmPass p, float* _
         float bv[4], cv[4];
         four<T, V>(b + s * p.b.sb + g * p.b.sh + 4 * sl, bv);
         four<T, V>(c + s * p.c.sb + g * p.c.sh + 4 * sl, cv);
-        h[q].x = fmaf(fast_exp2(dq * a.x), h[q].x, uq * bv[0]);
-        h[q].y = fmaf(fast_exp2(dq * a.y), h[q].y, uq * bv[1]);
-        h[q].z = fmaf(fast_exp2(dq * a.z), h[q].z, uq * bv[2]);
-        h[q].w = fmaf(fast_exp2(dq * a.w), h[q].w, uq * bv[3]);
+        h[q].x = fmaf(decay_of(dq, a.x), h[q].x, uq * bv[0]);
+        h[q].y = fmaf(decay_of(dq, a.y), h[q].y, uq * bv[1]);
+        h[q].z = fmaf(decay_of(dq, a.z), h[q].z, uq * bv[2]);
+        h[q].w = fmaf(decay_of(dq, a.w), h[q].w, uq * bv[3]);
         if (on && s0 + q < p.B) __stcs(reinterpret_cast<float4*>(st + q * step), h[q]);
         y[q] = fmaf(h[q].x, cv[0], h[q].y * cv[1]) + fmaf(h[q].z, cv[2], h[q].w * cv[3]);
     }

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const F2 bk = j ? bb.hi : bb.lo, ck = j ? cc.hi : cc.lo;
-                    const F2 e0 = ex2_(d.lo * a.v[k + j][0]), e1 = ex2_(d.hi * a.v[k + j][1]);
+                    const F2 e0 = decay_of(d.lo, a.v[k + j][0]), e1 = decay_of(d.hi, a.v[k + j][1]);
                     h.v[k + j][0] = fma_(e0, h.v[k + j][0], u.lo * bk);
                     h.v[k + j][1] = fma_(e1, h.v[k + j][1], u.hi * bk);
                     if (REV) {
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const F2 bk = j ? bb.hi : bb.lo;
-                        h.v[k + j][0] = fma_(ex2_(d.lo * a.v[k + j][0]), h.v[k + j][0], u.lo * bk);
-                        h.v[k + j][1] = fma_(ex2_(d.hi * a.v[k + j][1]), h.v[k + j][1], u.hi * bk);
+                        h.v[k + j][0] = fma_(decay_of(d.lo, a.v[k + j][0]), h.v[k + j][0], u.lo * bk);
+                        h.v[k + j][1] = fma_(decay_of(d.hi, a.v[k + j][1]), h.v[k + j][1], u.hi * bk);
                     }
                 }
             }
@@ -287,8 +287,8 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
                     for (int j = 0; j < 2; ++j) {
                         const F2 bk = j ? bb.hi : bb.lo, ck = j ? cc.hi : cc.lo;
                         F2(&hk)[2] = h.v[k + j];
-                        hk[0] = fma_(ex2_(d.lo * a.v[k + j][0]), hk[0], u.lo * bk);
-                        hk[1] = fma_(ex2_(d.hi * a.v[k + j][1]), hk[1], u.hi * bk);
+                        hk[0] = fma_(decay_of(d.lo, a.v[k + j][0]), hk[0], u.lo * bk);
+                        hk[1] = fma_(decay_of(d.hi, a.v[k + j][1]), hk[1], u.hi * bk);
                         y01 = fma_(hk[0], ck, y01), y23 = fma_(hk[1], ck, y23);
                         dc[k + j] = sum_of(fma_(hk[0], dy.lo, hk[1] * dy.hi));
                     }
@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
                         const F2 R0 = fma_(dy.lo, ck, Ek[0]), R1 = fma_(dy.hi, ck, Ek[1]);
                         db[k + j] = sum_of(fma_(R0, u.lo, R1 * u.hi));
                         in01 = fma_(R0, bk, in01), in23 = fma_(R1, bk, in23);
-                        Ek[0] = R0 * ex2_(d.lo * a.v[k + j][0]);
-                        Ek[1] = R1 * ex2_(d.hi * a.v[k + j][1]);
+                        Ek[0] = R0 * decay_of(d.lo, a.v[k + j][0]);
+                        Ek[1] = R1 * decay_of(d.hi, a.v[k + j][1]);
                         const F2 q0 = Ek[0] * kept[i].v[k + j][0], q1 = Ek[1] * kept[i].v[k + j][1];
                         da.v[k + j][0] = fma_(q0, d.lo, da.v[k + j][0]);
                         da.v[k + j][1] = fma_(q1, d.hi, da.v[k + j][1]);

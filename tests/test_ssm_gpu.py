@@ -261,3 +261,29 @@ def test_many_short_sequences():
     w = hla.ssm_decode_step(last, a=c["a"], skip=c["skip"], dt_bias=c["dt_bias"], **tail)
     close(y[-5:], f64(w), "step", 1e-5)
     close(state[-5:], f64(last), "state", 1e-5)
+
+
+@pytest.mark.parametrize("n, step, steps_of", [(8192, 1e-3, "scan"), (8192, 1e-5, "scan"), (2048, 1e-3, "tokens")])
+def test_slow_decays_keep_their_rate(n, step, steps_of):
+    """A state that nothing enters decays by exp(a sum of the steps).  Each token's rounded decay is within 2^-23 of it at
+    worst, but what counts over thousands of tokens is the mean: it has to stay below 4e-9, an eighth of the decay's half
+    step of 2^-25.  Of the roundings to nearest, of the decays and the products, each token adds at most 2^-24.  They
+    change sign from channel to channel, so that the mean of 64 channels x 8 states has 2^-24 sqrt(2 n / 512), below
+    4e-9 n from n = 100 on."""
+    D, N = 64, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dt = step * (0.5 + torch.rand((1, n, D), generator=g, device="cuda"))
+    a = -0.05 - 0.1 * torch.rand((D, N), generator=g, device="cuda")
+    h0 = 1.0 + torch.rand((1, D, N), generator=g, device="cuda")
+    x, b = torch.zeros((1, n, D), device="cuda"), torch.zeros((1, n, 1, N), device="cuda")
+    if steps_of == "scan":
+        fin = hla.ssm_forward(x, dt, a, b, b, dt_softplus=False, init_state=h0, return_final_state=True)[1]
+    else:
+        fin = h0.clone()
+        for t in range(n):
+            hla.ssm_decode_step(fin, x[:, t], dt[:, t], a, b[:, t], b[:, t], dt_softplus=False)
+    want = h0.double() * torch.exp(dt.double().sum(1)[..., None] * a.double())
+    assert abs(((fin.double() - want) / want).mean().item()) <= 4e-9 * n
+    # no decay: a product with 1
+    none = hla.ssm_forward(x, dt, 0 * a, b, b, dt_softplus=False, init_state=h0, return_final_state=True)[1]
+    assert torch.equal(none, h0)
