@@ -418,8 +418,7 @@ int hla2_layer_norm_backward(const hla2_norm_args* a, const void* dout, void* dx
             using T = decltype(zero);
             constexpr int RW = decltype(rw)::value;
             auto k = layer_norm_backward_kernel<T, decltype(v)::value, decltype(nv)::value, RW>;
-            const size_t smem = NormShape<RW>::rows > 1 ? 2 * vb : 0;
-            if (smem > 40 * 1024 && raise_smem(k, smem) != cudaSuccess) return -1;
+            const size_t smem = NormShape<RW>::rows > 1 ? 2 * vb : 0;  // such rows have 1024 values at most
             partials = norm_ctas(k, NormShape<RW>::threads, smem, a->rows, NormShape<RW>::rows);
             if (partials > kMostCtasPerSm * sm_count()) partials = kMostCtasPerSm * sm_count();
             return launch_pdl(k, dim3(partials), dim3(NormShape<RW>::threads), smem, st, *a, g) == cudaSuccess ? 0 : -1;

@@ -355,7 +355,9 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvPass a, T* __r
 
 // ---- launch ----------------------------------------------------------------------------------
 
-// f(zero of the type, VEC, W) as integral constants; `wide` elements a vector where the tensors allow it
+constexpr int kWide = 8, kWideBack = 4;  // bf16 elements of a vector, forward and backward
+
+// f(zero of the type, VEC, W) as integral constants; BF_VEC bf16 or 4 float32 elements a vector where the tensors allow it
 template <int V> using Int = std::integral_constant<int, V>;
 template <int BF_VEC, class F>
 int with_conv(int dtype, bool vec, int W, F&& f) {
@@ -410,12 +412,15 @@ struct ConvInputs {
     Extent read[7];
     int reads = 0;
     bool vec = true;
-    int es;
-    explicit ConvInputs(const hla2_conv_args* a) : es(elem_size(a->dtype)) {}
-    // a contiguous tensor, of which vectors are read
+    int es, wide;  // bytes of an element, elements of a vector
+    ConvInputs(const hla2_conv_args* a, int bf_vec) : es(elem_size(a->dtype)), wide(es == 2 ? bf_vec : 4) {}
+    // a contiguous tensor, whose vectors are read or written
+    void vectors(const void* p, int D) {
+        if (p) vec = vec && al(p, wide * es) && D % wide == 0;
+    }
     void add(const void* p, size_t elems, int D) {
         read[reads++] = extent_of(p, elems * es);
-        if (p) vec = vec && al(p, 16) && D % (16 / es) == 0;
+        vectors(p, D);
     }
     bool meets(const Extent& e) const {
         for (int i = 0; i < reads; ++i)
@@ -424,7 +429,7 @@ struct ConvInputs {
     }
     int rows(const char* fn, const Tensor& t, bool written) {
         if (int rc = check_tensor(fn, t, es, written)) return rc;
-        vec = vec && t.vec(16 / es, es);
+        vec = vec && t.vec(wide, es);
         if (!written) read[reads++] = t.extent(es);
         return HLA2_OK;
     }
@@ -461,12 +466,12 @@ int hla2_short_conv_forward(const hla2_conv_args* a, hla2_rows out, void* final_
     Range range(fn);
     if (int rc = check_conv(fn, a)) return rc;
     if (a->B == 0 || a->D == 0) return ok();
-    ConvInputs in(a);
+    ConvInputs in(a, kWide);
     if (int rc = in.params(fn, a)) return rc;
     const Tensor o = rows("out", out, a->B, a->n, a->D);
     const Extent fin = extent_of(final_state, (size_t)a->B * (a->W - 1) * a->D * in.es);
     if (!al(final_state, in.es)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
-    if (final_state) in.vec = in.vec && al(final_state, 16);
+    in.vectors(final_state, a->D);
     if (a->n > 0) {
         if (int rc = in.rows(fn, rows("x", a->x, a->B, a->n, a->D), false)) return rc;
         if (int rc = in.rows(fn, o, true)) return rc;
@@ -479,13 +484,13 @@ int hla2_short_conv_forward(const hla2_conv_args* a, hla2_rows out, void* final_
     ConvPass p = base_pass(a);
     p.out = const_cast<void*>(out.p), p.o_sb = out.sb, p.o_sn = out.sn;
     p.fin = final_state;
-    const int v = in.vec ? 16 / in.es : 1;
+    const int v = in.vec ? in.wide : 1;
     p.run = run_of(a, v, 1024);
     p.runs = a->n > 0 ? (int)(((long long)a->n + p.run - 1) / p.run) : 1;
     p.cols = (a->D + v - 1) / v;
     const long long threads = (long long)p.cols * p.runs * a->B;
     if ((threads + 127) / 128 > 0x7fffffffLL) return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: too many values", fn);
-    const int rc = with_conv<8>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
+    const int rc = with_conv<kWide>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
         using T = decltype(zero);
         return launch_pdl(conv_kernel<T, decltype(vec)::value, decltype(taps)::value>, dim3((unsigned)((threads + 127) / 128)),
                           dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), p) == cudaSuccess ? 0 : -1;
@@ -505,7 +510,7 @@ int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void
     Range range(fn);
     if (int rc = check_conv(fn, a)) return rc;
     if (a->D == 0) return ok();
-    ConvInputs in(a);
+    ConvInputs in(a, kWideBack);
     if (int rc = in.params(fn, a)) return rc;
     const size_t state = (size_t)a->B * (a->W - 1) * a->D;
     if (!al(dfinal_state, in.es) || !al(dinit_state, in.es) || !al(dweight, 4) || !al(dbias, 4))
@@ -513,7 +518,7 @@ int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void
     if (!dweight || (a->bias != nullptr) != (dbias != nullptr))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dweight is needed, dbias with bias, and only then", fn);
     in.add(dfinal_state, state, a->D);
-    if (dinit_state) in.vec = in.vec && al(dinit_state, 16) && a->D % (16 / in.es) == 0;
+    in.vectors(dinit_state, a->D);
     Extent written[4] = {extent_of(dweight, (size_t)a->D * a->W * sizeof(float)), extent_of(dbias, (size_t)a->D * sizeof(float)),
                          extent_of(dinit_state, state * in.es), {0, 0}};
     if (a->n > 0 && a->B > 0) {
@@ -541,7 +546,7 @@ int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     int rc = 0;
     if (r.partials > 0)
-        rc = with_conv<4>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
+        rc = with_conv<kWideBack>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
             using T = decltype(zero);
             constexpr int V = decltype(vec)::value;
             return launch_pdl(conv_backward_kernel<T, V, decltype(taps)::value>, dim3(r.partials, (a->D + 32 * V - 1) / (32 * V)),
@@ -564,23 +569,23 @@ int hla2_short_conv_decode_step(const hla2_conv_args* a, void* state, hla2_rows 
     if (a->B == 0 || a->D == 0) return ok();
     if (a->lengths || a->init_state)
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: lengths and init_state must be NULL", fn);
-    ConvInputs in(a);
+    ConvInputs in(a, kWide);
     if (int rc = in.params(fn, a)) return rc;
     if (int rc = in.rows(fn, rows("x", a->x, a->B, 1, a->D), false)) return rc;
     const Tensor o = rows("out", out, a->B, 1, a->D);
     if (int rc = in.rows(fn, o, true)) return rc;
     if (!state || !al(state, in.es))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: the state must be an address aligned to its type", fn);
-    in.vec = in.vec && al(state, 16);
+    in.vectors(state, a->D);
     const Extent est = extent_of(state, (size_t)a->B * (a->W - 1) * a->D * in.es), eo = o.extent(in.es);
     if (meet(eo, est) || in.meets(eo) || in.meets(est))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out or the state overlaps another tensor", fn);
     ConvPass p = base_pass(a);
     p.out = const_cast<void*>(out.p), p.o_sb = out.sb;
-    const int v = in.vec ? 16 / in.es : 1;
+    const int v = in.vec ? in.wide : 1;
     p.cols = (a->D + v - 1) / v;
     const long long threads = (long long)p.cols * a->B;
-    const int rc = with_conv<8>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
+    const int rc = with_conv<kWide>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
         using T = decltype(zero);
         return launch_pdl(conv_step_kernel<T, decltype(vec)::value, decltype(taps)::value>, dim3((unsigned)((threads + 127) / 128)),
                           dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), p, static_cast<T*>(state)) == cudaSuccess ? 0 : -1;

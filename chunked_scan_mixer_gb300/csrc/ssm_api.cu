@@ -28,6 +28,8 @@ int check_sizes(const char* fn, const hla2_ssm_args* a) {
     return HLA2_OK;
 }
 
+constexpr int kSsmVec = 4;  // elements that a thread moves at a time, where the tensors allow it
+
 // The inputs of a call; the extents of everything that it reads
 struct Inputs {
     Tensor t[5] = {};
@@ -185,8 +187,7 @@ int hla2_ssm_forward(const hla2_ssm_args* a, hla2_rows out, float* final_state, 
         if (int rc = check_tensor(fn, o, es, true)) return rc;
         if (in.meets(o.extent(es)) || meet(o.extent(es), fin))
             return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps another tensor", fn);
-        const int v = 16 / es;
-        vec = in.vec(a, v) && o.vec(v, es);
+        vec = in.vec(a, kSsmVec) && o.vec(kSsmVec, es);
     } else if (!final_state) {
         return ok();
     }
@@ -245,12 +246,12 @@ int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfina
         o[outs++] = view("db", grads->db, a->B, a->G, a->n, a->N);
         o[outs++] = view("dc", grads->dc, a->B, a->G, a->n, a->N);
         if (a->gate.p) o[outs++] = rows("dgate", grads->dgate, a->B, a->n, a->D);
-        vec = in.vec(a, 16 / es);
+        vec = in.vec(a, kSsmVec);
         for (int i = 0; i < outs; ++i) {
             if (int rc = check_tensor(fn, o[i], es, i > 0)) return rc;
             if (i == 0) in.read[in.reads++] = o[i].extent(es);
             else written[count++] = o[i].extent(es);
-            vec = vec && o[i].vec(16 / es, es);
+            vec = vec && o[i].vec(kSsmVec, es);
         }
     }
     if ((a->gate.p != nullptr) != (grads->dgate.p != nullptr) && a->n > 0 && a->B > 0)
@@ -300,8 +301,7 @@ int hla2_ssm_decode_step(const hla2_ssm_args* a, float* state, hla2_rows out, hl
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out or the state overlaps another tensor", fn);
     SsmPass p = base_pass(a, in, SsmPlan{1, 1, 1});
     p.out = dev(o);
-    // four values of b and c at a time
-    const bool vec = in.t[2].vec(4, es) && in.t[3].vec(4, es);
+    const bool vec = in.t[2].vec(kSsmVec, es) && in.t[3].vec(kSsmVec, es);  // of b and c
     if (launch_ssm_step(p, state, a->dtype == HLA2_BF16, vec, reinterpret_cast<cudaStream_t>(stream)))
         return launch_failed("selective scan step");
     return ok();

@@ -151,3 +151,14 @@ def test_many_short_sequences(dtype):
     state = c["init_state"].clone()
     assert torch.equal(hla.short_conv_decode_step(state, c["x"][:, 0], c["weight"], bias=c["bias"]), out[:, 0])
     assert torch.equal(state, fin)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("D", [12, 132])
+def test_rows_of_four_channels_alignment(dtype, W, D):
+    """Widths and addresses that are multiples of four elements, not of eight."""
+    c, dout, dfin = make(2, 45, D, W, dtype, seed=D)
+    wide = torch.zeros((2, 45, 2 * D + 4), dtype=dtype, device="cuda")
+    wide[..., 4:4 + D] = c["x"]
+    check({**c, "x": wide[..., 4:4 + D]}, dout, dfin, lengths=[45, 7])

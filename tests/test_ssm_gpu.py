@@ -287,3 +287,15 @@ def test_slow_decays_keep_their_rate(n, step, steps_of):
     # no decay: a product with 1
     none = hla.ssm_forward(x, dt, 0 * a, b, b, dt_softplus=False, init_state=h0, return_final_state=True)[1]
     assert torch.equal(none, h0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("D, G", [(12, 1), (68, 1), (204, 3)])
+def test_rows_of_four_channels_alignment(dtype, D, G):
+    """Widths and addresses that are multiples of four elements, not of eight."""
+    c = make_ssm(2, 37, D, 16, G, dtype=dtype, seed=D)
+    wide = torch.zeros((2, 37, 2 * D + 4), dtype=dtype, device="cuda")
+    wide[..., 4:4 + D], wide[..., 4 + D:] = c["x"], c["gate"]
+    c["x"], c["gate"] = wide[..., 4:4 + D], wide[..., 4 + D:]
+    check_forward(c)
+    check_backward(c)
