@@ -16,11 +16,9 @@
 namespace hla2 {
 namespace {
 
-template <typename T, int V, int N, bool SUMS>
+template <typename T, int M, int N, bool SUMS>
 __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threads) ssm_kernel(const SsmPass p) {
     constexpr int SL = SsmShape<N>::lanes, NT = SsmShape<N>::threads, TT = SsmShape<N>::tokens, CT = kSsmChannels;
-    using L = Lanes<V>;
-    using P = typename L::P;
     using Sums = LaneRows<N>;
     __shared__ __align__(16) float sd[TT][CT], su[TT][CT], sy[SUMS ? 1 : TT][Sums::token], sb[TT][2 * N], sc[SUMS ? 1 : TT][2 * N],
         sskip[CT], sbias[CT];
@@ -33,8 +31,8 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
             *b = static_cast<const T*>(p.b.p) + at.b * p.b.sb + at.group * p.b.sh,
             *c = static_cast<const T*>(p.c.p) + at.b * p.c.sb + at.group * p.c.sh;
     T* out = SUMS ? nullptr : static_cast<T*>(const_cast<void*>(p.out.p)) + at.b * p.out.sb + at.c0;
-    using Chan = Tile<T, V, TT, CT, NT>;
-    using Stat = Tile<T, V, TT, N, NT>;
+    using Chan = Tile<T, M, TT, CT, NT>;
+    using Stat = Tile<T, M, TT, N, NT>;
     Chan xn, dn, xc, zc;
     Stat bn, cn;
     auto fetch = [&](int t0) {
@@ -60,16 +58,16 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
     __syncthreads();
     for (int t0 = at.t0; t0 < at.live_end; t0 += TT) {
         Chan::parts([&](int k, int r, int ch) {
-            stage<T, V, false>(xn.v[k], dn.v[k], xn.v[k], xn.v[k], false, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
+            stage<T, false>(xn.v[k], dn.v[k], xn.v[k], xn.v[k], false, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
                                &sd[r][ch], &su[r][ch], nullptr);
         });
         Stat::parts([&](int k, int r, int s) {
-            P f[L::N];
+            F2 f[2];
             unpack(bn.v[k], f);
-            put_twice<V>(&sb[r][2 * s], f);
+            put_twice(&sb[r][2 * s], f);
             if (!SUMS) {
                 unpack(cn.v[k], f);
-                put_twice<V>(&sc[r][2 * s], f);
+                put_twice(&sc[r][2 * s], f);
             }
         });
         if (!SUMS) {
@@ -103,22 +101,19 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
         if (!SUMS)
             Chan::parts([&](int k, int r, int ch) {
                 if (t0 + r >= at.t_end || ch >= at.cols) return;
-                P y[L::N], fx[L::N], fs[L::N];
-                Sums::template get<V>(&sy[r][ch], y);
+                F2 y[2], fx[2], fs[2];
+                Sums::get(&sy[r][ch], y);
                 unpack(xc.v[k], fx);
-                get_values<V>(sskip + ch, fs);
+                get_values(sskip + ch, fs);
 #pragma unroll
-                for (int i = 0; i < L::N; ++i) y[i] = fma_(fs[i], fx[i], y[i]);
+                for (int i = 0; i < 2; ++i) y[i] = fma_(fs[i], fx[i], y[i]);
                 if (z) {
                     unpack(zc.v[k], fx);
 #pragma unroll
-                    for (int i = 0; i < L::N; ++i) y[i] = times_silu(y[i], fx[i]);
+                    for (int i = 0; i < 2; ++i) y[i] = times_silu(y[i], fx[i]);
                 }
-                if (t0 + r >= at.live_end) {
-#pragma unroll
-                    for (int i = 0; i < L::N; ++i) y[i] = L::all(0.f);
-                }
-                stvec<T, V>(out + (long long)(t0 + r) * p.out.sn + ch, y);
+                if (t0 + r >= at.live_end) y[0] = y[1] = pair(0.f, 0.f);
+                strow<T, M>(out + (long long)(t0 + r) * p.out.sn + ch, y, at.cols - ch);
             });
     }
     pdl_trigger();
@@ -129,13 +124,11 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
         return;
     }
     // padding past the last staged token
-    P zero[L::N];
-#pragma unroll
-    for (int i = 0; i < L::N; ++i) zero[i] = L::all(0.f);
+    const F2 zero[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
     const int first = at.t0 + (at.live_end - at.t0 + TT - 1) / TT * TT;
-    for (long long i = tid; i < (long long)(at.t_end - first) * (CT / V); i += NT) {
-        const int t = first + (int)(i / (CT / V)), ch = (int)(i % (CT / V)) * V;
-        if (ch < at.cols) stvec<T, V>(out + (long long)t * p.out.sn + ch, zero);
+    for (long long i = tid; i < (long long)(at.t_end - first) * (CT / 4); i += NT) {
+        const int t = first + (int)(i / (CT / 4)), ch = (int)(i % (CT / 4)) * 4;
+        if (ch < at.cols) strow<T, M>(out + (long long)t * p.out.sn + ch, zero, at.cols - ch);
     }
     if (p.fin && at.seg == p.nseg - 1) h.store(p.fin + ((long long)at.b * p.D + at.c0 + 4 * cg) * N + 4 * sl, N, chans);
 }
@@ -192,22 +185,22 @@ __global__ void __launch_bounds__(256) ssm_carry_kernel(const SsmPass p, float* 
     pdl_trigger();
 }
 
-template <typename T, int V, int N>
+template <typename T, int M, int N>
 int forward_n(const SsmPass& p, cudaStream_t st) {
     const dim3 block(SsmShape<N>::threads);
     if (p.nseg > 1 &&
-        (launch_pdl(ssm_kernel<T, V, N, true>, dim3(p.B * p.G * p.tiles, p.nseg - 1), block, 0, st, p) != cudaSuccess ||
+        (launch_pdl(ssm_kernel<T, M, N, true>, dim3(p.B * p.G * p.tiles, p.nseg - 1), block, 0, st, p) != cudaSuccess ||
          (p.nseg > kSsmJoin && launch_ssm_carry(p, nullptr, nullptr, st))))
         return -1;
-    return launch_pdl(ssm_kernel<T, V, N, false>, dim3(p.B * p.G * p.tiles, p.nseg), block, 0, st, p) == cudaSuccess ? 0 : -1;
+    return launch_pdl(ssm_kernel<T, M, N, false>, dim3(p.B * p.G * p.tiles, p.nseg), block, 0, st, p) == cudaSuccess ? 0 : -1;
 }
-template <typename T, int V>
+template <typename T, int M>
 int forward_v(const SsmPass& p, cudaStream_t st) {
     switch (p.N) {
-        case 8: return forward_n<T, V, 8>(p, st);
-        case 16: return forward_n<T, V, 16>(p, st);
-        case 32: return forward_n<T, V, 32>(p, st);
-        case 64: return forward_n<T, V, 64>(p, st);
+        case 8: return forward_n<T, M, 8>(p, st);
+        case 16: return forward_n<T, M, 16>(p, st);
+        case 32: return forward_n<T, M, 32>(p, st);
+        case 64: return forward_n<T, M, 64>(p, st);
         default: return -1;
     }
 }

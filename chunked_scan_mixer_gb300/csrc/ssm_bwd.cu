@@ -23,12 +23,10 @@ constexpr int kMacro = kSsmMark;  // tokens between marks
 constexpr int kBack = 4;            // tokens whose states are in registers
 
 // Marks and sums of a segment.  REV: there are several segments, the states start from zero and R's sums are formed too.
-template <typename T, int V, int N, bool REV>
+template <typename T, int M, int N, bool REV>
 __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threads)
     ssm_marks_kernel(const SsmPass p, const SsmGrads g) {
     constexpr int NT = SsmShape<N>::threads, SL = SsmShape<N>::lanes, TT = SsmShape<N>::tokens < kMacro ? SsmShape<N>::tokens : kMacro, CT = kSsmChannels;
-    using L = Lanes<V>;
-    using P = typename L::P;
     __shared__ __align__(16) float sd[TT][CT], su[TT][CT], sy[REV ? TT : 1][CT], sb[TT][2 * N], sc[REV ? TT : 1][2 * N], sbias[CT];
     const int tid = threadIdx.x, sl = tid % SL, cg = tid / SL;
     pdl_wait();
@@ -48,8 +46,8 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
             *dout = static_cast<const T*>(g.dout.p) + at.b * g.dout.sb + at.c0,
             *b = static_cast<const T*>(p.b.p) + at.b * p.b.sb + at.group * p.b.sh,
             *c = static_cast<const T*>(p.c.p) + at.b * p.c.sb + at.group * p.c.sh;
-    using Chan = Tile<T, V, TT, CT, NT>;
-    using Stat = Tile<T, V, TT, N, NT>;
+    using Chan = Tile<T, M, TT, CT, NT>;
+    using Stat = Tile<T, M, TT, N, NT>;
     const long long slot = at.slot(p, at.seg);
     F2 sum01 = pair(0.f, 0.f), sum23 = sum01;
     __syncthreads();
@@ -73,16 +71,16 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
                 cr.template load<true>(c, p.c.sn, t0, at.live_end, N);
             }
             Chan::parts([&](int k, int r, int ch) {
-                stage<T, V, REV>(xr.v[k], dr.v[k], or_.v[k], zr.v[k], z, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
+                stage<T, REV>(xr.v[k], dr.v[k], or_.v[k], zr.v[k], z, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
                                  &sd[r][ch], &su[r][ch], &sy[REV ? r : 0][ch]);
             });
             Stat::parts([&](int k, int r, int n) {
-                P f[L::N];
+                F2 f[2];
                 unpack(br.v[k], f);
-                put_twice<V>(&sb[r][2 * n], f);
+                put_twice(&sb[r][2 * n], f);
                 if (REV) {
                     unpack(cr.v[k], f);
-                    put_twice<V>(&sc[REV ? r : 0][2 * n], f);
+                    put_twice(&sc[REV ? r : 0][2 * n], f);
                 }
             });
         }
@@ -136,14 +134,11 @@ struct BackSmem {
                          skip = e + kBack * LaneRows<N>::token, bias = skip + kSsmChannels, total = bias + kSsmChannels;
 };
 
-template <typename T, int V, int N>
+template <typename T, int M, int N>
 __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threads)
     ssm_backward_kernel(const SsmPass p, const SsmGrads g) {
     constexpr int NT = SsmShape<N>::threads, SL = SsmShape<N>::lanes, CT = kSsmChannels, MT = kMacro, TC = kBack;
-    using L = Lanes<V>;
-    using P = typename L::P;
     using Sums = LaneRows<N>;
-    constexpr int Q = 4 / V;  // vectors of an item, four channels of a token
     constexpr int items = TC * CT / 4 > NT ? TC * CT / 4 / NT : 1;
     using S = BackSmem<N>;
     extern __shared__ __align__(16) float sm[];
@@ -179,13 +174,12 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
             *c = static_cast<const T*>(p.c.p) + at.b * p.c.sb + at.group * p.c.sh;
     auto out = [&](const SsmRows& r) { return static_cast<T*>(const_cast<void*>(r.p)) + at.b * r.sb + at.c0; };
     T *dx = out(g.dx), *ddt = out(g.ddt), *dgate = z ? out(g.dgate) : nullptr;
-    using Chan = Tile<T, V, MT, CT, NT>;
-    using Stat = Tile<T, V, MT, N, NT>;
+    using Chan = Tile<T, M, MT, CT, NT>;
+    using Stat = Tile<T, M, MT, N, NT>;
     const long long slot = at.slot(p, at.seg);
     // sums of this thread's items' channels
-    P gskip[Q * L::N], gbias[Q * L::N];
-#pragma unroll
-    for (int i = 0; i < Q * L::N; ++i) gskip[i] = gbias[i] = L::all(0.f);
+    F2 gskip[2], gbias[2];
+    gskip[0] = gskip[1] = gbias[0] = gbias[1] = pair(0.f, 0.f);
     const int quad = tid % (CT / 4) * 4;
 
     const int macros = (at.live_end - at.t0 + MT - 1) / MT;
@@ -218,15 +212,15 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
             br.template load<true>(b, p.b.sn, t0, at.live_end, N);
             cr.template load<true>(c, p.c.sn, t0, at.live_end, N);
             Chan::parts([&](int k, int r, int ch) {
-                stage<T, V, true>(xr.v[k], dr.v[k], or_.v[k], zr.v[k], z, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
+                stage<T, true>(xr.v[k], dr.v[k], or_.v[k], zr.v[k], z, p.softplus, t0 + r < at.live_end && ch < at.cols, sbias + ch,
                                   sd + r * CT + ch, su + r * CT + ch, sy + r * CT + ch);
             });
             Stat::parts([&](int k, int r, int n) {
-                P f[L::N];
+                F2 f[2];
                 unpack(br.v[k], f);
-                put_twice<V>(sb + r * 2 * N + 2 * n, f);
+                put_twice(sb + r * 2 * N + 2 * n, f);
                 unpack(cr.v[k], f);
-                put_twice<V>(sc + r * 2 * N + 2 * n, f);
+                put_twice(sc + r * 2 * N + 2 * n, f);
             });
         }
         __syncthreads();
@@ -251,24 +245,24 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
         for (int t = MT - TC; t >= 0; t -= TC) {
             if (t < MT - TC) h.get(sst + (1 + t / TC) * (NT * 16), NT);
             // what the items of these tokens take from memory
-            Vec<T, V> ix[items][Q], id[items][Q], iz[items][Q], io[items][Q];
-            auto each_item = [&](auto&& f) {  // f(item, vector, token of the four, its place, channel)
+            Vec<T, 4> ix[items], id[items], iz[items], io[items];
+            auto each_item = [&](auto&& f) {  // f(item, token of the four, its place); an item is four channels of a token
 #pragma unroll
                 for (int m = 0; m < items; ++m) {
                     const int i = tid + m * NT, r = i / (CT / 4);
                     if (NT > TC * CT / 4 && i >= TC * CT / 4) continue;
-#pragma unroll
-                    for (int q = 0; q < Q; ++q) f(m, q, r, t0 + t + r, quad + q * V);
+                    f(m, r, t0 + t + r);
                 }
             };
-            each_item([&](int m, int q, int r, int tok, int ch) {
-                ix[m][q] = id[m][q] = iz[m][q] = io[m][q] = Vec<T, V>{};
-                if (tok < at.live_end && ch < at.cols) {
-                    ix[m][q] = ldvec<T, V>(x + (long long)tok * p.x.sn + ch);
-                    id[m][q] = ldvec<T, V>(dt + (long long)tok * p.dt.sn + ch);
+            each_item([&](int m, int, int tok) {
+                ix[m] = id[m] = iz[m] = io[m] = Vec<T, 4>{};
+                if (tok < at.live_end && quad < at.cols) {
+                    const int count = at.cols - quad;
+                    ix[m] = ldrow<T, M>(x + (long long)tok * p.x.sn + quad, count);
+                    id[m] = ldrow<T, M>(dt + (long long)tok * p.dt.sn + quad, count);
                     if (z) {
-                        iz[m][q] = ldvec<T, V>(z + (long long)tok * p.gate.sn + ch);
-                        io[m][q] = ldvec<T, V>(dout + (long long)tok * g.dout.sn + ch);
+                        iz[m] = ldrow<T, M>(z + (long long)tok * p.gate.sn + quad, count);
+                        io[m] = ldrow<T, M>(dout + (long long)tok * g.dout.sn + quad, count);
                     }
                 }
             });
@@ -344,43 +338,43 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
                     *reinterpret_cast<float4*>(g.bc + (((long long)at.b * p.n + tok) * (p.G * p.tiles) + at.tile) * (2 * N) +
                                                which * N + 4 * lane) = f;
             }
-            each_item([&](int m, int q, int r, int tok, int ch) {
-                if (tok >= at.t_end || ch >= at.cols) return;
-                P in[L::N], e[L::N], xv[L::N], v[L::N], d[L::N], dy[L::N], fb[L::N], fs[L::N], dd[L::N], ox[L::N];
-                Sums::template get<V>(vin + r * Sums::token + ch, in);
-                Sums::template get<V>(ve + r * Sums::token + ch, e);
-                unpack(ix[m][q], xv);
-                unpack(id[m][q], v);
-                get_values<V>(sd + (t + r) * CT + ch, d);
-                get_values<V>(sy + (t + r) * CT + ch, dy);
-                get_values<V>(sbias + ch, fb);
-                get_values<V>(sskip + ch, fs);
+            each_item([&](int m, int r, int tok) {
+                if (tok >= at.t_end || quad >= at.cols) return;
+                F2 in[2], e[2], xv[2], v[2], d[2], dy[2], fb[2], fs[2], dd[2], ox[2];
+                Sums::get(vin + r * Sums::token + quad, in);
+                Sums::get(ve + r * Sums::token + quad, e);
+                unpack(ix[m], xv);
+                unpack(id[m], v);
+                get_values(sd + (t + r) * CT + quad, d);
+                get_values(sy + (t + r) * CT + quad, dy);
+                get_values(sbias + quad, fb);
+                get_values(sskip + quad, fs);
                 const bool on = tok < at.live_end;
-                const P zero = L::all(0.f), one = L::all(1.f);
+                const int count = at.cols - quad;
+                const F2 zero = pair(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < L::N; ++i) {
-                    dd[i] = fma_(xv[i], in[i], e[i] * L::all(kLn2));
-                    if (p.softplus) dd[i] = dd[i] * sigmoid_of(fma_(v[i], one, fb[i]));
+                for (int i = 0; i < 2; ++i) {
+                    dd[i] = fma_(xv[i], in[i], e[i] * pair(kLn2, kLn2));
+                    if (p.softplus) dd[i] = dd[i] * sigmoid_of(v[i] + fb[i]);
                     ox[i] = fma_(d[i], in[i], fs[i] * dy[i]);
                     if (!on) dd[i] = ox[i] = zero;
-                    P &gb = gbias[q * L::N + i], &gs = gskip[q * L::N + i];
-                    gb = fma_(dd[i], one, gb);
-                    gs = fma_(xv[i], dy[i], gs);
+                    gbias[i] = dd[i] + gbias[i];
+                    gskip[i] = fma_(xv[i], dy[i], gskip[i]);
                 }
-                stvec<T, V>(dx + (long long)tok * g.dx.sn + ch, ox);
-                stvec<T, V>(ddt + (long long)tok * g.ddt.sn + ch, dd);
+                strow<T, M>(dx + (long long)tok * g.dx.sn + quad, ox, count);
+                strow<T, M>(ddt + (long long)tok * g.ddt.sn + quad, dd, count);
                 if (z) {
-                    P y[L::N], fz[L::N], fo[L::N];
-                    Sums::template get<V>(vy + r * Sums::token + ch, y);
-                    unpack(iz[m][q], fz);
-                    unpack(io[m][q], fo);
+                    F2 y[2], fz[2], fo[2];
+                    Sums::get(vy + r * Sums::token + quad, y);
+                    unpack(iz[m], fz);
+                    unpack(io[m], fo);
 #pragma unroll
-                    for (int i = 0; i < L::N; ++i) {
-                        P slope;
+                    for (int i = 0; i < 2; ++i) {
+                        F2 slope;
                         gate_of(fz[i], true, slope);
                         y[i] = on ? fo[i] * fma_(fs[i], xv[i], y[i]) * slope : zero;
                     }
-                    stvec<T, V>(dgate + (long long)tok * g.dgate.sn + ch, y);
+                    strow<T, M>(dgate + (long long)tok * g.dgate.sn + quad, y, count);
                 }
             });
             __syncthreads();
@@ -397,13 +391,8 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
     float* sums = vdc;
     if (tid < TC * CT / 4) {
         float* to = sums + tid / (CT / 4) * CT + quad;
-        if constexpr (V == 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) to[i] = gskip[i], to[TC * CT + i] = gbias[i];
-        } else {
-            put_values<V>(to, gskip);
-            put_values<V>(to + TC * CT, gbias);
-        }
+        put_values(to, gskip);
+        put_values(to + TC * CT, gbias);
     }
     __syncthreads();
     for (int i = tid; i < 2 * CT; i += NT) {
@@ -414,16 +403,14 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
         if (ch < at.cols) per_channel[(long long)which * p.D + ch] = s;
     }
     // padding past the last tokens gone through
-    P zero[L::N];
-#pragma unroll
-    for (int i = 0; i < L::N; ++i) zero[i] = L::all(0.f);
+    const F2 zero[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
     const int first = at.t0 + macros * MT;
-    for (long long i = tid; i < (long long)(at.t_end - first) * (CT / V); i += NT) {
-        const int tok = first + (int)(i / (CT / V)), ch = (int)(i % (CT / V)) * V;
-        if (ch >= at.cols) continue;
-        stvec<T, V>(dx + (long long)tok * g.dx.sn + ch, zero);
-        stvec<T, V>(ddt + (long long)tok * g.ddt.sn + ch, zero);
-        if (z) stvec<T, V>(dgate + (long long)tok * g.dgate.sn + ch, zero);
+    for (long long i = tid; i < (long long)(at.t_end - first) * (CT / 4); i += NT) {
+        const int tok = first + (int)(i / (CT / 4)), ch = (int)(i % (CT / 4)) * 4, count = at.cols - ch;
+        if (count <= 0) continue;
+        strow<T, M>(dx + (long long)tok * g.dx.sn + ch, zero, count);
+        strow<T, M>(ddt + (long long)tok * g.ddt.sn + ch, zero, count);
+        if (z) strow<T, M>(dgate + (long long)tok * g.dgate.sn + ch, zero, count);
     }
 }
 
@@ -475,7 +462,7 @@ __global__ void __launch_bounds__(256) ssm_params_kernel(const SsmPass p, const 
     else if (g.ddt_bias) g.ddt_bias[c - da - p.D] = s;
 }
 
-template <typename T, int V, int N>
+template <typename T, int M, int N>
 int backward_n(const SsmPass& p, const SsmGrads& g, cudaStream_t st) {
     const long long cols = (long long)p.D * (N + 2), quads = (long long)p.B * p.n * p.G * (2 * N / 4);
     auto params = [&]() {
@@ -484,13 +471,13 @@ int backward_n(const SsmPass& p, const SsmGrads& g, cudaStream_t st) {
     if (p.B == 0) return params();  // zeros
     const dim3 block(SsmShape<N>::threads), grid(p.B * p.G * p.tiles, p.nseg);
     if (p.nseg > 1) {
-        if (launch_pdl(ssm_marks_kernel<T, V, N, true>, grid, block, 0, st, p, g) != cudaSuccess ||
+        if (launch_pdl(ssm_marks_kernel<T, M, N, true>, grid, block, 0, st, p, g) != cudaSuccess ||
             (p.nseg > kSsmJoin && launch_ssm_carry(p, g.rsums, g.dfinal, st)))
             return -1;
     } else if (g.macros > 1) {
-        if (launch_pdl(ssm_marks_kernel<T, V, N, false>, grid, block, 0, st, p, g) != cudaSuccess) return -1;
+        if (launch_pdl(ssm_marks_kernel<T, M, N, false>, grid, block, 0, st, p, g) != cudaSuccess) return -1;
     }
-    auto kernel = ssm_backward_kernel<T, V, N>;
+    auto kernel = ssm_backward_kernel<T, M, N>;
     constexpr size_t smem = BackSmem<N>::total * sizeof(float);
     if (raise_smem(kernel, smem) != cudaSuccess) return -1;
     if (launch_pdl(kernel, grid, block, smem, st, p, g) != cudaSuccess) return -1;
@@ -498,13 +485,13 @@ int backward_n(const SsmPass& p, const SsmGrads& g, cudaStream_t st) {
         return -1;
     return params();
 }
-template <typename T, int V>
+template <typename T, int M>
 int backward_v(const SsmPass& p, const SsmGrads& g, cudaStream_t st) {
     switch (p.N) {
-        case 8: return backward_n<T, V, 8>(p, g, st);
-        case 16: return backward_n<T, V, 16>(p, g, st);
-        case 32: return backward_n<T, V, 32>(p, g, st);
-        case 64: return backward_n<T, V, 64>(p, g, st);
+        case 8: return backward_n<T, M, 8>(p, g, st);
+        case 16: return backward_n<T, M, 16>(p, g, st);
+        case 32: return backward_n<T, M, 32>(p, g, st);
+        case 64: return backward_n<T, M, 64>(p, g, st);
         default: return -1;
     }
 }
