@@ -416,10 +416,9 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
 
 // db and dc: the parts of a group's tiles, four states a thread
 template <typename T, int N>
-__global__ void __launch_bounds__(256) ssm_bc_kernel(const SsmPass p, const SsmGrads g) {
+__device__ __forceinline__ void add_bc(const SsmPass& p, const SsmGrads& g, int block) {
     constexpr int quads = 2 * N / 4;
-    pdl_wait();
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, tg = i / quads;
+    const long long i = (long long)block * 256 + threadIdx.x, tg = i / quads;
     const int q = (int)(i - tg * quads) * 4, which = q / N, n = q % N;  // db first
     const long long bt = tg / p.G;
     const int gr = (int)(tg - bt * p.G), b = (int)(bt / p.n), t = (int)(bt - (long long)b * p.n);
@@ -439,12 +438,11 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(const SsmPass p, const SsmG
 }
 
 // da, dskip and ddt_bias: the parts of the sequences and segments, 32 values a CTA with eight row lanes
-__global__ void __launch_bounds__(256) ssm_params_kernel(const SsmPass p, const SsmGrads g) {
+__device__ __forceinline__ void add_params(const SsmPass& p, const SsmGrads& g, int block) {
     __shared__ float sm[8][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const long long cols = (long long)p.D * (p.N + 2), c = (long long)blockIdx.x * 32 + lane;
+    const long long cols = (long long)p.D * (p.N + 2), c = (long long)block * 32 + lane;
     const int rows = p.B * p.nseg;
-    pdl_wait();
     const long long da = (long long)p.D * p.N;
     float s = 0.f;
     if (c < cols) {
@@ -462,13 +460,21 @@ __global__ void __launch_bounds__(256) ssm_params_kernel(const SsmPass p, const 
     else if (g.ddt_bias) g.ddt_bias[c - da - p.D] = s;
 }
 
+// Both in one launch, which spares the small calls some latency: the first `params` CTAs and those after them
+template <typename T, int N>
+__global__ void __launch_bounds__(256) ssm_parts_kernel(const SsmPass p, const SsmGrads g, int params) {
+    pdl_wait();
+    if ((int)blockIdx.x < params) add_params(p, g, blockIdx.x);
+    else add_bc<T, N>(p, g, blockIdx.x - params);
+}
+
 template <typename T, int M, int N>
 int backward_n(const SsmPass& p, const SsmGrads& g, cudaStream_t st) {
-    const long long cols = (long long)p.D * (N + 2), quads = (long long)p.B * p.n * p.G * (2 * N / 4);
-    auto params = [&]() {
-        return launch_pdl(ssm_params_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, st, p, g) == cudaSuccess ? 0 : -1;
+    const long long params = ((long long)p.D * (N + 2) + 31) / 32, bc = ((long long)p.B * p.n * p.G * (2 * N / 4) + 255) / 256;
+    auto parts = [&]() {
+        return launch_pdl(ssm_parts_kernel<T, N>, dim3((unsigned)(params + bc)), dim3(256), 0, st, p, g, (int)params) == cudaSuccess ? 0 : -1;
     };
-    if (p.B == 0) return params();  // zeros
+    if (p.B == 0) return parts();  // zeros
     const dim3 block(SsmShape<N>::threads), grid(p.B * p.G * p.tiles, p.nseg);
     if (p.nseg > 1) {
         if (launch_pdl(ssm_marks_kernel<T, M, N, true>, grid, block, 0, st, p, g) != cudaSuccess ||
@@ -481,9 +487,7 @@ int backward_n(const SsmPass& p, const SsmGrads& g, cudaStream_t st) {
     constexpr size_t smem = BackSmem<N>::total * sizeof(float);
     if (raise_smem(kernel, smem) != cudaSuccess) return -1;
     if (launch_pdl(kernel, grid, block, smem, st, p, g) != cudaSuccess) return -1;
-    if (quads > 0 && launch_pdl(ssm_bc_kernel<T, N>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, p, g) != cudaSuccess)
-        return -1;
-    return params();
+    return parts();
 }
 template <typename T, int M>
 int backward_v(const SsmPass& p, const SsmGrads& g, cudaStream_t st) {
