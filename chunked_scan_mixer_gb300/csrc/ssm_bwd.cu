@@ -9,11 +9,11 @@
 // first: it forms the states before each four from the mark, then for four tokens at a time forms the four states again
 // into registers and goes back through them.  The products that are summed over states or channels go through
 // shared memory: a thread adds its own four, and the others are added column by column, with fewer instructions than
-// exchanges between lanes take.  db and dc of a CTA's 64 channels and the parameters' sums go to scratch; two more kernels add
+// exchanges between lanes take.  db and dc of a CTA's 64 channels and the parameters' sums go to scratch; one more kernel adds
 // them in a fixed order.
 //
 // 4 x 4096 tokens of 2048 channels, N = 16, bf16: marks and sums 191 us, main pass 706 (349 instructions for a thread's 16 states of a
-// token, 1.7 a cycle and SM with the eight warps that four tokens' states in registers leave room for), db and dc 16, parameters 8.
+// token, 1.7 a cycle and SM with the eight warps that four tokens' states in registers leave room for), parts of db, dc and the parameters 22.
 #include "ssm.cuh"
 
 namespace hla2 {
@@ -460,7 +460,8 @@ __device__ __forceinline__ void add_params(const SsmPass& p, const SsmGrads& g, 
     else if (g.ddt_bias) g.ddt_bias[c - da - p.D] = s;
 }
 
-// Both in one launch, which spares the small calls some latency: the first `params` CTAs and those after them
+// Both in one launch, the first `params` CTAs and those after them (two launches: 100 tokens of 256 channels, forward and backward,
+// 39 us instead of 35.5)
 template <typename T, int N>
 __global__ void __launch_bounds__(256) ssm_parts_kernel(const SsmPass p, const SsmGrads g, int params) {
     pdl_wait();
