@@ -72,6 +72,23 @@ struct NormRow {
     }
 };
 
+// A lane's columns of the weight or the bias, which are the same in all its rows: held in registers where eight are enough, read
+// again with every row elsewhere.
+template <typename T, int VEC, int NV, int RW>
+struct NormParam {
+    static constexpr bool kept = NV * (VEC * sizeof(T) < 4 ? 4 : VEC * sizeof(T)) <= 32;
+    const T* p;
+    NormRow<T, VEC, kept ? NV : 1, RW> v;
+    __device__ __forceinline__ NormParam(const T* from, int D) : p(from) {
+        if (kept && p) v.load(p, D);
+    }
+    template <typename P, int N>
+    __device__ __forceinline__ void get(int j, P (&f)[N]) const {
+        if constexpr (kept) unpack(v.v[j], f);
+        else unpack(ldvec<T, VEC>(p + NormRow<T, VEC, NV, RW>::column(j)), f);
+    }
+};
+
 template <typename T, int VEC, int NV, int RW>
 __global__ void __launch_bounds__(NormShape<RW>::threads) layer_norm_kernel(const hla2_norm_args a, T* __restrict__ out) {
     using L = Lanes<VEC>;
@@ -82,10 +99,12 @@ __global__ void __launch_bounds__(NormShape<RW>::threads) layer_norm_kernel(cons
     int turn = 0;
     const int D = a.D;
     const float inv_d = 1.f / (float)D;
-    const T *x = static_cast<const T*>(a.x), *w = static_cast<const T*>(a.weight), *bias = static_cast<const T*>(a.bias);
+    const T* x = static_cast<const T*>(a.x);
     const long long stride = (long long)gridDim.x * rows;
     long long r = (long long)blockIdx.x * rows + threadIdx.x / (32 * RW);
     pdl_wait();
+    using Param = NormParam<T, VEC, NV, RW>;
+    const Param w(static_cast<const T*>(a.weight), D), bias(static_cast<const T*>(a.bias), D);
     Row next;
     if (r < a.rows) next.load(x + r * a.x_stride, D);
     for (; r < a.rows; r += stride) {  // a row's warps stay together
@@ -117,10 +136,10 @@ __global__ void __launch_bounds__(NormShape<RW>::threads) layer_norm_kernel(cons
         for (int j = 0; j < NV; ++j)
             if (Row::column(j) < D) {
                 P fw[N], fb[N], o[N];
-                unpack(ldvec<T, VEC>(w + Row::column(j)), fw);
-                if (bias) unpack(ldvec<T, VEC>(bias + Row::column(j)), fb);
+                w.get(j, fw);
+                if (bias.p) bias.get(j, fb);
 #pragma unroll
-                for (int i = 0; i < N; ++i) o[i] = fma_(f[j][i] * inv, fw[i], bias ? fb[i] : L::all(0.f));
+                for (int i = 0; i < N; ++i) o[i] = fma_(f[j][i] * inv, fw[i], bias.p ? fb[i] : L::all(0.f));
                 stvec<T, VEC>(out + r * D + Row::column(j), o);
             }
     }
@@ -139,7 +158,7 @@ __global__ void __launch_bounds__(NormShape<RW>::threads, VEC == 8 && NV == 2 ? 
     int turn = 0;
     const int D = a.D, mine = threadIdx.x / (32 * RW);
     const float inv_d = 1.f / (float)D;
-    const T *x = static_cast<const T*>(a.x), *w = static_cast<const T*>(a.weight), *dout = static_cast<const T*>(g.dout);
+    const T *x = static_cast<const T*>(a.x), *dout = static_cast<const T*>(g.dout);
     T* dx = static_cast<T*>(g.dx);
     const long long stride = (long long)gridDim.x * rows;
     long long r = (long long)blockIdx.x * rows + mine;
@@ -149,6 +168,7 @@ __global__ void __launch_bounds__(NormShape<RW>::threads, VEC == 8 && NV == 2 ? 
 #pragma unroll
         for (int i = 0; i < N; ++i) gw[j][i] = gb[j][i] = L::all(0.f);
     pdl_wait();
+    const NormParam<T, VEC, NV, RW> w(static_cast<const T*>(a.weight), D);
     Row nx_, nd;
     if (r < a.rows) nx_.load(x + r * a.x_stride, D), nd.load(dout + r * D, D);
     for (; r < a.rows; r += stride) {
@@ -159,7 +179,7 @@ __global__ void __launch_bounds__(NormShape<RW>::threads, VEC == 8 && NV == 2 ? 
             unpack(nd.v[j], d[j]);
             if (Row::column(j) < D) {
                 P fw[N];
-                unpack(ldvec<T, VEC>(w + Row::column(j)), fw);
+                w.get(j, fw);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     sx = fma_(f[j][i], L::all(1.f), sx);
@@ -176,7 +196,7 @@ __global__ void __launch_bounds__(NormShape<RW>::threads, VEC == 8 && NV == 2 ? 
         for (int j = 0; j < NV; ++j)
             if (Row::column(j) < D) {
                 P fw[N];
-                unpack(ldvec<T, VEC>(w + Row::column(j)), fw);
+                w.get(j, fw);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     f[j][i] = fma_(f[j][i], L::all(1.f), mean);
@@ -192,7 +212,7 @@ __global__ void __launch_bounds__(NormShape<RW>::threads, VEC == 8 && NV == 2 ? 
         for (int j = 0; j < NV; ++j)
             if (Row::column(j) < D) {
                 P o[N], fw[N];
-                unpack(ldvec<T, VEC>(w + Row::column(j)), fw);
+                w.get(j, fw);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     const P nx = f[j][i] * pinv;
