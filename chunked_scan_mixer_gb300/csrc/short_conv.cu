@@ -37,71 +37,126 @@ __device__ __forceinline__ int length_of(const int* lengths, int b, int n) {
     return lengths ? max(0, min(__ldg(lengths + b), n)) : n;
 }
 
-// weights of VEC channels as N of P for each tap: W vectors, since a channel's taps lie side by side
-template <typename T, int VEC, int W, typename P, int N>
-__device__ __forceinline__ void load_taps(const T* w, P (&taps)[W][N]) {
-    float f[VEC * W];
+// A thread's channels: VEC side by side, moved as a vector, or at odd widths and places (APART) two that are 32 apart, so that a warp
+// moves 32 neighbours with each single element.  Either way they are worked on as pairs.  (One channel a thread at odd widths: bf16 8 x
+// 4096 x 2047 92 us and with gradients 245, 74 and 226 so; a step of 256 x 4095 12.5 and 8.5.  Four channels 32 apart: 70, 213 and 8.5,
+// but 1.5 us more in calls of 10, and spills in the gradients.  Four neighbours moved one by one: 153 and 418.)
+template <typename T, int VEC, bool APART>
+struct ConvChannels {
+    static constexpr int N = VEC / 2, step = APART ? 32 : 1;
+    using Raw = Vec<T, VEC>;
+    explicit __device__ __forceinline__ ConvChannels(int) {}
+    // the first channel of thread q of a row
+    static __device__ __forceinline__ int first(int q) { return q * VEC; }
+    __device__ __forceinline__ Raw load(const T* p) const { return ldvec<T, VEC>(p); }
+    __device__ __forceinline__ void store(T* p, const Raw& a) const { *reinterpret_cast<Raw*>(p) = a; }
+    __device__ __forceinline__ void store(T* p, const F2 (&f)[N]) const { stvec<T, VEC>(p, f); }
+    static __device__ __forceinline__ void values(const Raw& a, F2 (&f)[N]) { unpack(a, f); }
+    // the weights of each tap; a channel's lie side by side
+    template <int W>
+    __device__ __forceinline__ void taps(const T* w, F2 (&t)[W][N]) const {
+        float f[VEC * W];
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-        P v[N];
-        unpack(ldvec<T, VEC>(w + k * VEC), v);
-        if constexpr (VEC == 1) {
-            f[k] = v[0];
-        } else {
+        for (int k = 0; k < W; ++k) {
+            F2 v[N];
+            unpack(ldvec<T, VEC>(w + k * VEC), v);
 #pragma unroll
             for (int i = 0; i < N; ++i) split(v[i], f[k * VEC + 2 * i], f[k * VEC + 2 * i + 1]);
         }
-    }
 #pragma unroll
-    for (int j = 0; j < W; ++j)
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) t[j][i] = pair(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
+    }
+};
+template <typename T, int VEC>
+struct ConvChannels<T, VEC, true> {
+    static constexpr int N = VEC / 2, step = 32;
+    struct Raw {  // as they come, so that nothing waits for them
+        T e[VEC];
+    };
+    int at[VEC];  // of each from the first; those that are not there read it again
+    int count;    // channels from the first on
+    explicit __device__ __forceinline__ ConvChannels(int count) : count(count) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) at[k] = 32 * k < count ? 32 * k : 0;
+    }
+    static __device__ __forceinline__ int first(int q) { return q / 32 * (32 * VEC) + q % 32; }
+    __device__ __forceinline__ Raw load(const T* p) const {
+        Raw r;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) r.e[k] = p[at[k]];
+        return r;
+    }
+    __device__ __forceinline__ void store(T* p, const Raw& a) const {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            if (32 * k < count) p[32 * k] = a.e[k];
+    }
+    __device__ __forceinline__ void store(T* p, const F2 (&f)[N]) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if constexpr (VEC == 1) taps[j][i] = f[j];
-            else taps[j][i] = pair(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
+            float lo, hi;
+            split(f[i], lo, hi);
+            if (64 * i < count) p[64 * i] = from_f32<T>(lo);
+            if (64 * i + 32 < count) p[64 * i + 32] = from_f32<T>(hi);
         }
-}
+    }
+    static __device__ __forceinline__ void values(const Raw& a, F2 (&f)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = pair(to_f32(a.e[2 * i]), to_f32(a.e[2 * i + 1]));
+    }
+    template <int W>
+    __device__ __forceinline__ void taps(const T* w, F2 (&t)[W][N]) const {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) t[j][i] = pair(to_f32(w[at[2 * i] * W + j]), to_f32(w[at[2 * i + 1] * W + j]));
+    }
+};
 
-template <typename T, int VEC, int W>
+template <typename T, int VEC, bool APART, int W>
 __global__ void __launch_bounds__(128, 4) conv_kernel(const ConvPass a) {
-    using L = Lanes<VEC>;
-    using P = typename L::P;
-    constexpr int N = L::N, U = kAhead;
+    using C = ConvChannels<T, VEC, APART>;
+    using P = F2;
+    constexpr int N = C::N, U = kAhead;
     pdl_wait();
     const long long i0 = (long long)blockIdx.x * 128 + threadIdx.x, i1 = i0 / a.cols;
-    const int c = (int)(i0 - i1 * a.cols) * VEC, b = (int)(i1 / a.runs), run = (int)(i1 - (long long)b * a.runs);
-    if (b >= a.B) return;
+    const int c = C::first((int)(i0 - i1 * a.cols)), b = (int)(i1 / a.runs), run = (int)(i1 - (long long)b * a.runs);
+    if (b >= a.B || c >= a.D) return;
+    const C mine(a.D - c);
     const int len = length_of(a.lengths, b, a.n);
     const int t0 = run * a.run, t1 = min(t0 + a.run, a.n);
     const T* x = static_cast<const T*>(a.x) + b * a.x_sb + c;
     T* out = static_cast<T*>(a.out) + b * a.o_sb + c;
     const T* init = a.init ? static_cast<const T*>(a.init) + (long long)b * (W - 1) * a.D + c : nullptr;
     auto input = [&](int t) {  // at a token that may be before the first, as the state has it
-        Vec<T, VEC> v{};
-        if (t >= 0) v = ldvec<T, VEC>(x + t * a.x_sn);
-        else if (init) v = ldvec<T, VEC>(init + (long long)(t + W - 1) * a.D);
+        typename C::Raw v{};
+        if (t >= 0) v = mine.load(x + t * a.x_sn);
+        else if (init) v = mine.load(init + (long long)(t + W - 1) * a.D);
         return v;
     };
     P taps[W][N], bias[N], in[W - 1 + U][N];  // in: the last W - 1 inputs, and those of a block
-    load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
+    mine.template taps<W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
 #pragma unroll
-    for (int i = 0; i < N; ++i) bias[i] = L::all(0.f);
-    if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), bias);
+    for (int i = 0; i < N; ++i) bias[i] = pair(0.f, 0.f);
+    if (a.bias) C::values(mine.load(static_cast<const T*>(a.bias) + c), bias);
     if (t0 < len) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) unpack(input(t0 - (W - 1) + j), in[j]);
+        for (int j = 0; j < W - 1; ++j) C::values(input(t0 - (W - 1) + j), in[j]);
     }
     const int live = min(len, t1);
-    Vec<T, VEC> next[U];
+    typename C::Raw next[U];
     auto fetch = [&](int t) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t + u < live) next[u] = ldvec<T, VEC>(x + (t + u) * a.x_sn);
+            if (t + u < live) next[u] = mine.load(x + (t + u) * a.x_sn);
     };
     // U tokens from t on; `whole`: all of them are there
     auto block = [&](int t, auto whole) {
         constexpr bool all = decltype(whole)::value;
 #pragma unroll
-        for (int u = 0; u < U; ++u) unpack(next[u], in[W - 1 + u]);
+        for (int u = 0; u < U; ++u) C::values(next[u], in[W - 1 + u]);
         fetch(t + U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -115,7 +170,7 @@ __global__ void __launch_bounds__(128, 4) conv_kernel(const ConvPass a) {
                 P slope;
                 if (a.silu) y[i] = gate_of(y[i], true, slope);
             }
-            stvec<T, VEC>(out + (t + u) * a.o_sn, y);
+            mine.store(out + (t + u) * a.o_sn, y);
         }
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
@@ -123,43 +178,44 @@ __global__ void __launch_bounds__(128, 4) conv_kernel(const ConvPass a) {
             for (int i = 0; i < N; ++i) in[j][i] = in[U + j][i];
     };
 #pragma unroll
-    for (int u = 0; u < U; ++u) next[u] = Vec<T, VEC>{};
+    for (int u = 0; u < U; ++u) next[u] = typename C::Raw{};
     fetch(t0);
     int t = t0;
     for (; t + U <= live; t += U) block(t, std::true_type{});
     if (t < live) block(t, std::false_type{});
     P zero[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) zero[i] = L::all(0.f);
-    for (t = max(t0, live); t < t1; ++t) stvec<T, VEC>(out + t * a.o_sn, zero);
+    for (int i = 0; i < N; ++i) zero[i] = pair(0.f, 0.f);
+    for (t = max(t0, live); t < t1; ++t) mine.store(out + t * a.o_sn, zero);
     pdl_trigger();
     if (run == 0 && a.fin) {
         T* fin = static_cast<T*>(a.fin) + (long long)b * (W - 1) * a.D + c;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            *reinterpret_cast<Vec<T, VEC>*>(fin + (long long)j * a.D) = input(len - (W - 1) + j);
+            mine.store(fin + (long long)j * a.D, input(len - (W - 1) + j));
     }
 }
 
 // Eight runs a CTA at a time, 32 vectors of channels
-template <typename T, int VEC, int W>
+template <typename T, int VEC, bool APART, int W>
 __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a, int rows) {
-    using L = Lanes<VEC>;
-    using P = typename L::P;
-    constexpr int N = L::N;
+    using C = ConvChannels<T, VEC, APART>;
+    using P = F2;
+    constexpr int N = C::N;
     __shared__ float sums[8][32 * VEC + 1];
     pdl_wait();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = (blockIdx.y * 32 + lane) * VEC, per_b = (a.runs + 7) / 8;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = C::first(blockIdx.y * 32 + lane), per_b = (a.runs + 7) / 8;
+    const C mine(a.D - c);
     P taps[W][N], bias[N], dw[W][N], db[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        bias[i] = db[i] = L::all(0.f);
+        bias[i] = db[i] = pair(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][i] = L::all(0.f);
+        for (int j = 0; j < W; ++j) dw[j][i] = pair(0.f, 0.f);
     }
     if (c < a.D) {
-        load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
-        if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), bias);
+        mine.template taps<W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
+        if (a.bias) C::values(mine.load(static_cast<const T*>(a.bias) + c), bias);
     }
     for (int row = blockIdx.x; row < rows; row += gridDim.x) {
         const int b = row / per_b, run = (row - b * per_b) * 8 + w;
@@ -176,22 +232,22 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a,
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-            for (int i = 0; i < N; ++i) in[j][i] = dp[j][i] = L::all(0.f);
+            for (int i = 0; i < N; ++i) in[j][i] = dp[j][i] = pair(0.f, 0.f);
         if (t0 < len) {
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
                 const int t = t0 - (W - 1) + j;
-                if (t >= 0) unpack(ldvec<T, VEC>(x + t * a.x_sn), in[j]);
-                else if (init) unpack(ldvec<T, VEC>(init + (long long)(t + W - 1) * a.D), in[j]);
+                if (t >= 0) C::values(mine.load(x + t * a.x_sn), in[j]);
+                else if (init) C::values(mine.load(init + (long long)(t + W - 1) * a.D), in[j]);
             }
         }
         // dx_s is there with dp_t, t = s + W - 1
         const int first = run == 0 ? -(W - 1) : t0, last = t1 + W - 1, live = min(len, last);
-        Vec<T, VEC> vx[U], vg[U];
+        typename C::Raw vx[U], vg[U];
         auto fetch = [&](int t) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (t + u < live) vx[u] = ldvec<T, VEC>(x + (t + u) * a.x_sn), vg[u] = ldvec<T, VEC>(dout + (t + u) * a.g_sn);
+                if (t + u < live) vx[u] = mine.load(x + (t + u) * a.x_sn), vg[u] = mine.load(dout + (t + u) * a.g_sn);
         };
         // U tokens from t on; `inner`: all of them are this run's own, and so are the dx's
         auto block = [&](int t, auto inner) {
@@ -199,11 +255,11 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a,
             P g[U][N];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                unpack(vx[u], in[W - 1 + u]);
-                unpack(vg[u], g[u]);
+                C::values(vx[u], in[W - 1 + u]);
+                C::values(vg[u], g[u]);
                 if (!all && t + u >= live) {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) in[W - 1 + u][i] = g[u][i] = L::all(0.f);
+                    for (int i = 0; i < N; ++i) in[W - 1 + u][i] = g[u][i] = pair(0.f, 0.f);
                 }
             }
             fetch(t + U);
@@ -212,16 +268,16 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a,
                 const bool own = all || t + u < t1;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    P p = bias[i], slope = L::all(1.f);
+                    P p = bias[i], slope = pair(1.f, 1.f);
                     if (a.silu) {
 #pragma unroll
                         for (int j = 0; j < W; ++j) p = fma_(taps[j][i], in[u + j][i], p);
                         gate_of(p, true, slope);
                     }
-                    const P d = !all && t + u >= live ? L::all(0.f) : g[u][i] * slope;
+                    const P d = !all && t + u >= live ? pair(0.f, 0.f) : g[u][i] * slope;
                     dp[W - 1 + u][i] = d;
                     if (own) {
-                        db[i] = fma_(d, L::all(1.f), db[i]);
+                        db[i] = fma_(d, pair(1.f, 1.f), db[i]);
 #pragma unroll
                         for (int j = 0; j < W; ++j) dw[j][i] = fma_(d, in[u + j][i], dw[j][i]);
                     }
@@ -235,9 +291,9 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a,
                     const int k = s - (len - (W - 1));  // its place in the state after the last token
                     if (dfin && k >= 0 && s < len) {
                         P f[N];
-                        unpack(ldvec<T, VEC>(dfin + (long long)k * a.D), f);
+                        C::values(mine.load(dfin + (long long)k * a.D), f);
 #pragma unroll
-                        for (int i = 0; i < N; ++i) o[i] = fma_(f[i], L::all(1.f), o[i]);
+                        for (int i = 0; i < N; ++i) o[i] = fma_(f[i], pair(1.f, 1.f), o[i]);
                     }
                 }
 #pragma unroll
@@ -246,10 +302,10 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a,
                     for (int j = 1; j < W; ++j) o[i] = fma_(taps[j][i], dp[W - 1 + u - j][i], o[i]);
                 if (!all && s >= len) {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) o[i] = L::all(0.f);
+                    for (int i = 0; i < N; ++i) o[i] = pair(0.f, 0.f);
                 }
-                if (all || s >= 0) stvec<T, VEC>(dx + s * a.o_sn, o);
-                else if (dinit) stvec<T, VEC>(dinit + (long long)(s + W - 1) * a.D, o);
+                if (all || s >= 0) mine.store(dx + s * a.o_sn, o);
+                else if (dinit) mine.store(dinit + (long long)(s + W - 1) * a.D, o);
             }
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
@@ -257,7 +313,7 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a,
                 for (int i = 0; i < N; ++i) in[j][i] = in[U + j][i], dp[j][i] = dp[U + j][i];
         };
 #pragma unroll
-        for (int u = 0; u < U; ++u) vx[u] = vg[u] = Vec<T, VEC>{};
+        for (int u = 0; u < U; ++u) vx[u] = vg[u] = typename C::Raw{};
         fetch(t0);
         block(t0, std::false_type{});
         int t = t0 + U;
@@ -271,23 +327,16 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a,
     for (int j = 0; j <= W; ++j) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const P v = j < W ? dw[j < W ? j : 0][i / 2 * (VEC > 1)] : db[i / 2 * (VEC > 1)];
-            float f;
-            if constexpr (VEC == 1) {
-                f = v;
-            } else {
-                float lo, hi;
-                split(v, lo, hi);
-                f = i % 2 ? hi : lo;
-            }
-            sums[w][i * 32 + lane] = f;
+            float lo, hi;
+            split(j < W ? dw[j < W ? j : 0][i / 2] : db[i / 2], lo, hi);
+            sums[w][i * 32 + lane] = i % 2 ? hi : lo;
         }
         __syncthreads();
         for (int k = threadIdx.x; k < 32 * VEC; k += 256) {
             float s = 0.f;
 #pragma unroll
             for (int r = 0; r < 8; ++r) s += sums[r][k];
-            const int ch = (blockIdx.y * 32 + k % 32) * VEC + k / 32;
+            const int ch = C::first(blockIdx.y * 32 + k % 32) + k / 32 * C::step;
             if (ch < a.D) dst[(long long)j * a.D + ch] = s;
         }
         __syncthreads();
@@ -318,58 +367,61 @@ __global__ void __launch_bounds__(512) conv_sums_kernel(const ConvPass a, int ro
 }
 
 // One token: the state moves up by one
-template <typename T, int VEC, int W>
+template <typename T, int VEC, bool APART, int W>
 __global__ void __launch_bounds__(128) conv_step_kernel(const ConvPass a, T* __restrict__ state) {
-    using L = Lanes<VEC>;
-    using P = typename L::P;
-    constexpr int N = L::N;
+    using C = ConvChannels<T, VEC, APART>;
+    using P = F2;
+    constexpr int N = C::N;
     pdl_trigger();
     pdl_wait();
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
-    const int b = (int)(i / a.cols), c = (int)(i - (long long)b * a.cols) * VEC;
-    if (b >= a.B) return;
+    const int b = (int)(i / a.cols), c = C::first((int)(i - (long long)b * a.cols));
+    if (b >= a.B || c >= a.D) return;
+    const C mine(a.D - c);
     T* st = state + (long long)b * (W - 1) * a.D + c;
-    Vec<T, VEC> v[W];
+    typename C::Raw v[W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) v[j] = ldvec<T, VEC>(st + (long long)j * a.D);
-    v[W - 1] = ldvec<T, VEC>(static_cast<const T*>(a.x) + b * a.x_sb + c);
+    for (int j = 0; j < W - 1; ++j) v[j] = mine.load(st + (long long)j * a.D);
+    v[W - 1] = mine.load(static_cast<const T*>(a.x) + b * a.x_sb + c);
     P taps[W][N], y[N];
-    load_taps<T, VEC, W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
+    mine.template taps<W>(static_cast<const T*>(a.weight) + (long long)c * W, taps);
 #pragma unroll
-    for (int k = 0; k < N; ++k) y[k] = L::all(0.f);
-    if (a.bias) unpack(ldvec<T, VEC>(static_cast<const T*>(a.bias) + c), y);
+    for (int k = 0; k < N; ++k) y[k] = pair(0.f, 0.f);
+    if (a.bias) C::values(mine.load(static_cast<const T*>(a.bias) + c), y);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
         P x[N];
-        unpack(v[j], x);
+        C::values(v[j], x);
 #pragma unroll
         for (int k = 0; k < N; ++k) y[k] = fma_(taps[j][k], x[k], y[k]);
-        if (j > 0) *reinterpret_cast<Vec<T, VEC>*>(st + (long long)(j - 1) * a.D) = v[j];
+        if (j > 0) mine.store(st + (long long)(j - 1) * a.D, v[j]);
     }
     P slope;
 #pragma unroll
     for (int k = 0; k < N; ++k)
         if (a.silu) y[k] = gate_of(y[k], true, slope);
-    stvec<T, VEC>(static_cast<T*>(a.out) + b * a.o_sb + c, y);
+    mine.store(static_cast<T*>(a.out) + b * a.o_sb + c, y);
 }
 
 // ---- launch ----------------------------------------------------------------------------------
 
 constexpr int kWide = 8, kWideBack = 4;  // bf16 elements of a vector, forward and backward
+constexpr int kApart = 2;                // channels of a thread without vectors
 
-// f(zero of the type, VEC, W) as integral constants; BF_VEC bf16 or 4 float32 elements a vector where the tensors allow it
+// f(zero of the type, VEC, APART, W) as integral constants: BF_VEC bf16 or 4 float32 channels a thread where the tensors allow vectors
+// of them
 template <int V> using Int = std::integral_constant<int, V>;
 template <int BF_VEC, class F>
 int with_conv(int dtype, bool vec, int W, F&& f) {
-    auto taps = [&](auto zero, auto v) {
+    auto taps = [&](auto zero, auto v, auto apart) {
         switch (W) {
-            case 2: return f(zero, v, Int<2>{});
-            case 3: return f(zero, v, Int<3>{});
-            default: return f(zero, v, Int<4>{});
+            case 2: return f(zero, v, apart, Int<2>{});
+            case 3: return f(zero, v, apart, Int<3>{});
+            default: return f(zero, v, apart, Int<4>{});
         }
     };
-    if (dtype == HLA2_BF16) return vec ? taps(bf16{}, Int<BF_VEC>{}) : taps(bf16{}, Int<1>{});
-    return vec ? taps(0.f, Int<4>{}) : taps(0.f, Int<1>{});
+    if (dtype == HLA2_BF16) return vec ? taps(bf16{}, Int<BF_VEC>{}, std::false_type{}) : taps(bf16{}, Int<kApart>{}, std::true_type{});
+    return vec ? taps(0.f, Int<4>{}, std::false_type{}) : taps(0.f, Int<kApart>{}, std::true_type{});
 }
 
 int check_conv(const char* fn, const hla2_conv_args* a) {
@@ -380,7 +432,7 @@ int check_conv(const char* fn, const hla2_conv_args* a) {
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: B, n and D must not be negative", fn);
     if (a->W < 2 || a->W > 4) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: W must be 2, 3 or 4 (got %d)", fn, a->W);
     if (a->silu != 0 && a->silu != 1) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: silu must be 0 or 1", fn);
-    // the grids' limits: columns of 32 channels, and rows of at least 64 tokens or a sequence
+    // the grids' limits: columns of 64 channels, and rows of at least 64 tokens or a sequence
     if ((long long)a->B * a->D > 0x7fffffffLL || a->D > 1 << 20 || a->n > 1 << 30 || (long long)a->B * ((a->n + 63LL) / 64) > 0x7fffffffLL)
         return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: B * D and B * n / 64 must fit in 31 bits, D be at most 2^20 and n 2^30", fn);
     return HLA2_OK;
@@ -392,6 +444,8 @@ int run_of(const hla2_conv_args* a, int vec, int threads) {
     const long long run = (all / want + 7) / 8 * 8;
     return run < 8 ? 8 : run > 128 ? 128 : (int)run;
 }
+// Threads of a row
+int conv_cols(const hla2_conv_args* a, bool vec, int wide) { return vec ? a->D / wide : (a->D + 32 * kApart - 1) / (32 * kApart) * 32; }
 // The backward's runs, rows of eight of them, and the partial rows of its CTAs, who take several rows where there are more than
 // fill the GPU four times (two CTAs an SM): the partial rows would be larger than the inputs with many short sequences.
 struct ConvRows {
@@ -484,15 +538,15 @@ int hla2_short_conv_forward(const hla2_conv_args* a, hla2_rows out, void* final_
     ConvPass p = base_pass(a);
     p.out = const_cast<void*>(out.p), p.o_sb = out.sb, p.o_sn = out.sn;
     p.fin = final_state;
-    const int v = in.vec ? in.wide : 1;
+    const int v = in.vec ? in.wide : kApart;
     p.run = run_of(a, v, 1024);
     p.runs = a->n > 0 ? (int)(((long long)a->n + p.run - 1) / p.run) : 1;
-    p.cols = (a->D + v - 1) / v;
+    p.cols = conv_cols(a, in.vec, in.wide);
     const long long threads = (long long)p.cols * p.runs * a->B;
     if ((threads + 127) / 128 > 0x7fffffffLL) return set_last_error(HLA2_ERR_UNSUPPORTED, "%s: too many values", fn);
-    const int rc = with_conv<kWide>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
+    const int rc = with_conv<kWide>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto apart, auto taps) {
         using T = decltype(zero);
-        return launch_pdl(conv_kernel<T, decltype(vec)::value, decltype(taps)::value>, dim3((unsigned)((threads + 127) / 128)),
+        return launch_pdl(conv_kernel<T, decltype(vec)::value, decltype(apart)::value, decltype(taps)::value>, dim3((unsigned)((threads + 127) / 128)),
                           dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), p) == cudaSuccess ? 0 : -1;
     });
     return rc ? launch_failed("short convolution") : ok();
@@ -546,10 +600,10 @@ int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     int rc = 0;
     if (r.partials > 0)
-        rc = with_conv<kWideBack>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
+        rc = with_conv<kWideBack>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto apart, auto taps) {
             using T = decltype(zero);
             constexpr int V = decltype(vec)::value;
-            return launch_pdl(conv_backward_kernel<T, V, decltype(taps)::value>, dim3(r.partials, (a->D + 32 * V - 1) / (32 * V)),
+            return launch_pdl(conv_backward_kernel<T, V, decltype(apart)::value, decltype(taps)::value>, dim3(r.partials, (a->D + 32 * V - 1) / (32 * V)),
                               dim3(256), 0, st, p, r.rows) == cudaSuccess ? 0 : -1;
         });
     else if (dinit_state && a->B > 0)  // no tokens: the state after the last is the one before the first
@@ -582,12 +636,11 @@ int hla2_short_conv_decode_step(const hla2_conv_args* a, void* state, hla2_rows 
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out or the state overlaps another tensor", fn);
     ConvPass p = base_pass(a);
     p.out = const_cast<void*>(out.p), p.o_sb = out.sb;
-    const int v = in.vec ? in.wide : 1;
-    p.cols = (a->D + v - 1) / v;
+    p.cols = conv_cols(a, in.vec, in.wide);
     const long long threads = (long long)p.cols * a->B;
-    const int rc = with_conv<kWide>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto taps) {
+    const int rc = with_conv<kWide>(a->dtype, in.vec, a->W, [&](auto zero, auto vec, auto apart, auto taps) {
         using T = decltype(zero);
-        return launch_pdl(conv_step_kernel<T, decltype(vec)::value, decltype(taps)::value>, dim3((unsigned)((threads + 127) / 128)),
+        return launch_pdl(conv_step_kernel<T, decltype(vec)::value, decltype(apart)::value, decltype(taps)::value>, dim3((unsigned)((threads + 127) / 128)),
                           dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), p, static_cast<T*>(state)) == cudaSuccess ? 0 : -1;
     });
     return rc ? launch_failed("short convolution step") : ok();
