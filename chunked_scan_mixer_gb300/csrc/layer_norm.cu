@@ -73,7 +73,8 @@ struct NormRow {
 };
 
 // A lane's columns of the weight or the bias, which are the same in all its rows: held in registers where eight are enough, read
-// again with every row elsewhere.  (5000 float32 rows of 999 with gradients: 26.5 us without, 22.8 so; 16384 bf16 rows of 2047: 123 and 105.)
+// again with every row elsewhere.  (5000 float32 rows of 999 with gradients: 26.5 us without, 22.8 so; 16384 bf16 rows of 2047:
+// 123 and 105.)
 template <typename T, int VEC, int NV, int RW>
 struct NormParam {
     static constexpr bool kept = NV * (VEC * sizeof(T) < 4 ? 4 : VEC * sizeof(T)) <= 32;

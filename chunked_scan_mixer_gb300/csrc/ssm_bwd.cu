@@ -13,7 +13,8 @@
 // them in a fixed order.
 //
 // 4 x 4096 tokens of 2048 channels, N = 16, bf16: marks and sums 191 us, main pass 706 (349 instructions for a thread's 16 states of a
-// token, 1.7 a cycle and SM with the eight warps that four tokens' states in registers leave room for), parts of db and dc 16 and of the parameters 8 before they shared a launch.
+// token, 1.7 a cycle and SM with the eight warps that four tokens' states in registers leave room for), parts of db and dc 16 and of
+// the parameters 8 before they shared a launch.
 #include "ssm.cuh"
 
 namespace hla2 {
