@@ -243,6 +243,8 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a,
         }
         // dx_s is there with dp_t, t = s + W - 1
         const int first = run == 0 ? -(W - 1) : t0, last = t1 + W - 1, live = min(len, last);
+        // the sums take this run's valid tokens: one past the length would add 0 times inputs before it, which may be infinite
+        const int own_end = min(t1, live);
         typename C::Raw vx[U], vg[U];
         auto fetch = [&](int t) {
 #pragma unroll
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(256, 2) conv_backward_kernel(const ConvPass a,
             fetch(t + U);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const bool own = all || t + u < t1;
+                const bool own = all || t + u < own_end;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     P p = bias[i], slope = pair(1.f, 1.f);

@@ -616,7 +616,9 @@ int hla2_ssm_decode_step(const hla2_ssm_args* a, float* state, hla2_rows out, hl
  *   out_t = act(bias + sum_j weight[j] x_{t - W + 1 + j}),  act the SiLU or none
  *
  * lengths as above.  The state of a sequence is its last W - 1 inputs, oldest first, contiguous [B, W - 1, D] of
- * the tensors' type (zeros before a first token).  Sums are float32.
+ * the tensors' type (zeros before a first token).  Sums are float32.  A non-finite input in a valid row reaches the W outputs that
+ * it is a term of; in a backward it may reach its channel's sums and the gradients of the inputs beside it, without an
+ * activation only the taps' sums that it is a term of.
  */
 typedef struct {
     int dtype;              /* HLA2_F32 | HLA2_BF16: every tensor but the sums of a backward */

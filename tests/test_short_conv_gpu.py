@@ -162,3 +162,25 @@ def test_rows_of_four_channels_alignment(dtype, W, D):
     wide = torch.zeros((2, 45, 2 * D + 4), dtype=dtype, device="cuda")
     wide[..., 4:4 + D] = c["x"]
     check({**c, "x": wide[..., 4:4 + D]}, dout, dfin, lengths=[45, 7])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("D", [47, 48])
+@pytest.mark.parametrize("m", [3, 16, 17, 40])
+def test_an_infinite_input_reaches_its_own_terms_only(dtype, W, D, m):
+    """dweight_j = sum_t dout_t x_{t - W + 1 + j}: an input among a sequence's last W - 1 tokens is in fewer than W taps' sums, as
+    the tokens after it are padding."""
+    c, dout, _ = make(2, 40, D, W, dtype, state=False)
+    bad = m - 1  # the last valid token: a term of the last tap alone
+    c["x"][1, bad, 5] = float("inf")
+    lens = torch.tensor([40, m], dtype=torch.int32, device="cuda")
+    g = hla.short_conv_backward(dout=dout, act="none", lengths=lens, **c)
+    want = O.conv_backward(f64(c["x"]), f64(c["weight"]), f64(dout), bias=f64(c["bias"]), act="none", lengths=[40, m])
+    got = f64(g.dweight)
+    assert np.isinf(want["dweight"]).sum() == 1 and np.isinf(want["dweight"][5, W - 1])
+    assert got[5, W - 1] == want["dweight"][5, W - 1]
+    g.dweight[5, W - 1] = want["dweight"][5, W - 1] = 0.0
+    close(g.dweight, want["dweight"], "dweight", 1e-5)
+    close(g.dx, want["dx"], "dx", 1e-5)
+    close(g.dbias, want["dbias"], "dbias", 1e-5)
