@@ -1440,6 +1440,8 @@ def _ssm_backward(x, dt, a, b, c, dout, skip, gate, dt_bias, dt_softplus, length
     dx, ddt = new(s.B, s.n, s.D), new(s.B, s.n, s.D)
     dgate = None if gate is None else new(s.B, s.n, s.D)
     db, dc = new(s.B, s.n, s.G, s.N), new(s.B, s.n, s.G, s.N)
+    if s.D == 0:  # sums over no channels, for which the library launches nothing
+        db.zero_(), dc.zero_()
     da = new(s.D, s.N, dtype=f32)
     dskip, dbias = (None if t is None else new(s.D, dtype=f32) for t in (skip, dt_bias))
     dinit = None if init_state is None else new(s.B, s.D, s.N, dtype=f32)

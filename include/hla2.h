@@ -594,7 +594,8 @@ int hla2_ssm_forward(const hla2_ssm_args* a, hla2_rows out, float* final_state, 
 
 /* Gradients of sum(out * dout) + sum(final_state * dfinal_state).  da [D, N], dskip and ddt_bias [D] are float32 sums over
  * sequences and tokens in a fixed order; dinit_state [B, D, N] float32.  db and dc are sums over the channels of a group.
- * dgate is needed with gate, dskip with skip, ddt_bias with dt_bias, and each is NULL without; dinit_state is nullable. */
+ * dgate is needed with gate, dskip with skip, ddt_bias with dt_bias, and each is NULL without; dinit_state is nullable.
+ * With D = 0 nothing is written, db and dc neither. */
 typedef struct {
     hla2_rows dx, ddt, dgate; /* [B, n, D]    */
     hla2_view db, dc;         /* [B, G, n, N] */

@@ -299,3 +299,16 @@ def test_rows_of_four_channels_alignment(dtype, D, G):
     c["x"], c["gate"] = wide[..., 4:4 + D], wide[..., 4 + D:]
     check_forward(c)
     check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_no_channels(dtype):
+    """Without channels the sums over a group's channels are zeros."""
+    c = make_ssm(2, 5, 0, 16, dtype=dtype)
+    out, fin = hla.ssm_forward(**c, return_final_state=True)
+    assert out.shape == (2, 5, 0) and fin.shape == (2, 0, 16)
+    dirty = [torch.full((2, 5, 1, 16), float("nan"), device="cuda", dtype=dtype) for _ in range(64)]
+    del dirty  # what the allocator hands out next
+    g = hla.ssm_backward(dout=out, **c)
+    assert g.db.shape == g.dc.shape == (2, 5, 1, 16) and g.da.shape == (0, 16) and g.dx.shape == (2, 5, 0)
+    assert (g.db == 0).all() and (g.dc == 0).all()
