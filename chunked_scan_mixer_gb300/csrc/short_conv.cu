@@ -621,6 +621,8 @@ int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void
 int hla2_short_conv_decode_step(const hla2_conv_args* a, void* state, hla2_rows out, hla2_stream_t stream) {
     static const char* const fn = "hla2_short_conv_decode_step";
     Range range(fn);
+    hla2_conv_args one;  // n is not looked at
+    if (a) one = *a, one.n = 1, a = &one;
     if (int rc = check_conv(fn, a)) return rc;
     if (a->B == 0 || a->D == 0) return ok();
     if (a->lengths || a->init_state)

@@ -284,6 +284,8 @@ int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfina
 int hla2_ssm_decode_step(const hla2_ssm_args* a, float* state, hla2_rows out, hla2_stream_t stream) {
     static const char* const fn = "hla2_ssm_decode_step";
     Range range(fn);
+    hla2_ssm_args one;  // n is not looked at
+    if (a) one = *a, one.n = 1, a = &one;
     if (int rc = check_sizes(fn, a)) return rc;
     if (a->B == 0 || a->D == 0) return ok();
     if (a->lengths || a->init_state)

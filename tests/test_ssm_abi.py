@@ -331,3 +331,18 @@ def test_bindings_refuse_what_does_not_fit():
         hla.layer_norm(x, z(16), out=z(2, 5, 15))
     with pytest.raises(ValueError):
         hla.layer_norm_backward(x, z(16), z(2, 5, 15))
+
+
+@pytest.mark.parametrize("n", [0, 1, -1, (1 << 30) + 1, -(1 << 31)])
+def test_steps_do_not_look_at_n(L, n):
+    out, state = Rows(0x20000000, D, 0), 0x21000000
+    none = dict(lengths=None, init_state=None, n=n)
+    steps = ((L.hla2_ssm_decode_step, ssm), (L.hla2_short_conv_decode_step, conv))
+    for step, args in steps:
+        assert step(ctypes.byref(args(B=0, **none)), state, out, None) == 0
+        assert step(ctypes.byref(args(D=0, **none)), state, out, None) == 0
+        assert step(ctypes.byref(args(**none)), None, out, None) == -1  # what it does look at
+        assert "state" in L.hla2_last_error().decode()
+        assert step(None, state, out, None) == -1
+        if NO_GPU:
+            assert step(ctypes.byref(args(**none)), state, out, None) == -4
