@@ -4,6 +4,8 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <numeric>
+
 #include "common.cuh"
 
 namespace hla2 {
@@ -38,18 +40,71 @@ struct Tensor {
     bool vec(int v, int es) const {
         return al(p, (size_t)v * es) && cols % v == 0 && sb % v == 0 && sh % v == 0 && sn % v == 0;
     }
-    // whether no element has two places
-    bool apart() const {
-        struct Dim { long long stride; int size; } d[3] = {{sn, n}, {sh, H}, {sb, B}};
+    struct Dim { long long stride; int size; };
+    // the dimensions but the columns, shorter strides first
+    void dims(Dim (&d)[3]) const {
+        d[0] = {sn, n}, d[1] = {sh, H}, d[2] = {sb, B};
         for (int i = 0; i < 2; ++i)
             for (int j = 0; j < 2 - i; ++j)
                 if (d[j].stride > d[j + 1].stride) { const Dim t = d[j]; d[j] = d[j + 1], d[j + 1] = t; }
+    }
+    // whether no element has two places
+    bool apart() const {
+        Dim d[3];
+        dims(d);
         long long span = cols;
         for (const Dim& x : d) {
             if (x.size > 1 && x.stride < span) return false;
             if (x.size > 1) span += (x.size - 1) * x.stride;
         }
         return true;
+    }
+    // elements that lie side by side at each of its rows, and the strides' greatest common divisor (0: one such block)
+    void blocks(long long* block, long long* divisor) const {
+        Dim d[3];
+        dims(d);
+        *block = cols, *divisor = 0;
+        for (const Dim& x : d) {
+            if (x.size <= 1) continue;
+            if (*divisor == 0 && x.stride == *block) *block *= x.size;
+            else *divisor = std::gcd(*divisor, x.stride);
+        }
+    }
+};
+// Whether two tensors of elements of es bytes share one.  Tensors whose address ranges meet may still lie side by side, as parts of the
+// rows of one buffer: modulo a common divisor of all strides an element's place is its column's alone, so that they are apart
+// where their columns are.  Tensors that interleave in another way count as sharing.
+bool meet(const Tensor& a, const Tensor& b, int es) {
+    if (!meet(a.extent(es), b.extent(es))) return false;
+    long long na, nb, ga, gb;
+    a.blocks(&na, &ga), b.blocks(&nb, &gb);
+    const long long g = std::gcd(ga, gb);
+    if (g == 0 || na > g || nb > g) return true;
+    const long long by = (static_cast<const char*>(b.p) - static_cast<const char*>(a.p)) / es % g, at = by < 0 ? by + g : by;
+    return at < na || at + nb > g;
+}
+// What a call reads, or writes
+struct Places {
+    int es;
+    Extent flat[8];
+    Tensor t[8];
+    int flats = 0, tensors = 0;
+    explicit Places(int es) : es(es) {}
+    void add(const Extent& e) { flat[flats++] = e; }
+    void add(const Tensor& e) { t[tensors++] = e; }
+    bool meets(const Extent& e) const {
+        for (int i = 0; i < flats; ++i)
+            if (meet(e, flat[i])) return true;
+        for (int i = 0; i < tensors; ++i)
+            if (meet(e, t[i].extent(es))) return true;
+        return false;
+    }
+    bool meets(const Tensor& e) const {
+        for (int i = 0; i < flats; ++i)
+            if (meet(e.extent(es), flat[i])) return true;
+        for (int i = 0; i < tensors; ++i)
+            if (meet(e, t[i], es)) return true;
+        return false;
     }
 };
 Tensor rows(const char* name, const hla2_rows& r, int B, int n, int cols) {

@@ -465,28 +465,22 @@ ConvRows backward_rows(const hla2_conv_args* a) {
 }
 
 struct ConvInputs {
-    Extent read[7];
-    int reads = 0;
-    bool vec = true;
     int es, wide;  // bytes of an element, elements of a vector
-    ConvInputs(const hla2_conv_args* a, int bf_vec) : es(elem_size(a->dtype)), wide(es == 2 ? bf_vec : 4) {}
+    Places read;
+    bool vec = true;
+    ConvInputs(const hla2_conv_args* a, int bf_vec) : es(elem_size(a->dtype)), wide(es == 2 ? bf_vec : 4), read(es) {}
     // a contiguous tensor, whose vectors are read or written
     void vectors(const void* p, int D) {
         if (p) vec = vec && al(p, wide * es) && D % wide == 0;
     }
     void add(const void* p, size_t elems, int D) {
-        read[reads++] = extent_of(p, elems * es);
+        read.add(extent_of(p, elems * es));
         vectors(p, D);
-    }
-    bool meets(const Extent& e) const {
-        for (int i = 0; i < reads; ++i)
-            if (meet(e, read[i])) return true;
-        return false;
     }
     int rows(const char* fn, const Tensor& t, bool written) {
         if (int rc = check_tensor(fn, t, es, written)) return rc;
         vec = vec && t.vec(wide, es);
-        if (!written) read[reads++] = t.extent(es);
+        if (!written) read.add(t);
         return HLA2_OK;
     }
     int params(const char* fn, const hla2_conv_args* a) {
@@ -496,7 +490,7 @@ struct ConvInputs {
         add(a->weight, (size_t)a->D * a->W, a->D);
         add(a->bias, a->D, a->D);
         add(a->init_state, (size_t)a->B * (a->W - 1) * a->D, a->D);
-        read[reads++] = extent_of(a->lengths, (size_t)a->B * sizeof(int));
+        read.add(extent_of(a->lengths, (size_t)a->B * sizeof(int)));
         return HLA2_OK;
     }
 };
@@ -531,12 +525,12 @@ int hla2_short_conv_forward(const hla2_conv_args* a, hla2_rows out, void* final_
     if (a->n > 0) {
         if (int rc = in.rows(fn, rows("x", a->x, a->B, a->n, a->D), false)) return rc;
         if (int rc = in.rows(fn, o, true)) return rc;
-        if (in.meets(o.extent(in.es)) || meet(o.extent(in.es), fin))
+        if (in.read.meets(o) || meet(o.extent(in.es), fin))
             return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps another tensor", fn);
     } else if (!final_state) {
         return ok();
     }
-    if (in.meets(fin)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: final_state overlaps an input", fn);
+    if (in.read.meets(fin)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: final_state overlaps an input", fn);
     ConvPass p = base_pass(a);
     p.out = const_cast<void*>(out.p), p.o_sb = out.sb, p.o_sn = out.sn;
     p.fin = final_state;
@@ -575,17 +569,19 @@ int hla2_short_conv_backward(const hla2_conv_args* a, hla2_rows dout, const void
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dweight is needed, dbias with bias, and only then", fn);
     in.add(dfinal_state, state, a->D);
     in.vectors(dinit_state, a->D);
-    Extent written[4] = {extent_of(dweight, (size_t)a->D * a->W * sizeof(float)), extent_of(dbias, (size_t)a->D * sizeof(float)),
-                         extent_of(dinit_state, state * in.es), {0, 0}};
+    const Extent written[3] = {extent_of(dweight, (size_t)a->D * a->W * sizeof(float)), extent_of(dbias, (size_t)a->D * sizeof(float)),
+                               extent_of(dinit_state, state * in.es)};
     if (a->n > 0 && a->B > 0) {
         if (int rc = in.rows(fn, rows("x", a->x, a->B, a->n, a->D), false)) return rc;
         if (int rc = in.rows(fn, rows("dout", dout, a->B, a->n, a->D), false)) return rc;
         const Tensor o = rows("dx", dx, a->B, a->n, a->D);
         if (int rc = in.rows(fn, o, true)) return rc;
-        written[3] = o.extent(in.es);
+        if (in.read.meets(o)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps an input", fn);
+        for (const Extent& e : written)
+            if (meet(e, o.extent(in.es))) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: gradients overlap", fn);
     }
-    for (int i = 0; i < 4; ++i) {
-        if (in.meets(written[i])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps an input", fn);
+    for (int i = 0; i < 3; ++i) {
+        if (in.read.meets(written[i])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps an input", fn);
         for (int j = 0; j < i; ++j)
             if (meet(written[i], written[j])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: gradients overlap", fn);
     }
@@ -635,8 +631,8 @@ int hla2_short_conv_decode_step(const hla2_conv_args* a, void* state, hla2_rows 
     if (!state || !al(state, in.es))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: the state must be an address aligned to its type", fn);
     in.vectors(state, a->D);
-    const Extent est = extent_of(state, (size_t)a->B * (a->W - 1) * a->D * in.es), eo = o.extent(in.es);
-    if (meet(eo, est) || in.meets(eo) || in.meets(est))
+    const Extent est = extent_of(state, (size_t)a->B * (a->W - 1) * a->D * in.es);
+    if (meet(o.extent(in.es), est) || in.read.meets(o) || in.read.meets(est))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out or the state overlaps another tensor", fn);
     ConvPass p = base_pass(a);
     p.out = const_cast<void*>(out.p), p.o_sb = out.sb;

@@ -30,12 +30,12 @@ int check_sizes(const char* fn, const hla2_ssm_args* a) {
 
 constexpr int kSsmVec = 4;  // elements that a thread moves at a time, where the tensors allow it
 
-// The inputs of a call; the extents of everything that it reads
+// The inputs of a call, and everything that it reads
 struct Inputs {
     Tensor t[5] = {};
     int count = 0;
-    Extent read[12];
-    int reads = 0;
+    Places read;
+    explicit Inputs(int es) : read(es) {}
     int check(const char* fn, const hla2_ssm_args* a, int n) {
         const int es = elem_size(a->dtype);
         t[count++] = rows("x", a->x, a->B, n, a->D);
@@ -45,7 +45,7 @@ struct Inputs {
         if (a->gate.p) t[count++] = rows("gate", a->gate, a->B, n, a->D);
         for (int i = 0; i < count; ++i) {
             if (int rc = check_tensor(fn, t[i], es, false)) return rc;
-            read[reads++] = t[i].extent(es);
+            read.add(t[i]);
         }
         return HLA2_OK;
     }
@@ -56,17 +56,12 @@ struct Inputs {
         if (!al(a->skip, 4) || !al(a->dt_bias, 4) || !al(a->lengths, 4))
             return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
         const size_t d = (size_t)a->D * sizeof(float);
-        read[reads++] = extent_of(a->a, d * a->N);
-        read[reads++] = extent_of(a->skip, d);
-        read[reads++] = extent_of(a->dt_bias, d);
-        read[reads++] = extent_of(a->lengths, (size_t)a->B * sizeof(int));
-        read[reads++] = extent_of(a->init_state, d * a->B * a->N);
+        read.add(extent_of(a->a, d * a->N));
+        read.add(extent_of(a->skip, d));
+        read.add(extent_of(a->dt_bias, d));
+        read.add(extent_of(a->lengths, (size_t)a->B * sizeof(int)));
+        read.add(extent_of(a->init_state, d * a->B * a->N));
         return HLA2_OK;
-    }
-    bool meets(const Extent& e) const {
-        for (int i = 0; i < reads; ++i)
-            if (meet(e, read[i])) return true;
-        return false;
     }
     // whether every tensor allows vectors of v elements of the staged rows, within a group's channels too
     bool vec(const hla2_ssm_args* a, int v) const {
@@ -176,7 +171,7 @@ int hla2_ssm_forward(const hla2_ssm_args* a, hla2_rows out, float* final_state, 
     if (int rc = check_sizes(fn, a)) return rc;
     if (a->B == 0 || a->D == 0) return ok();
     const int es = elem_size(a->dtype);
-    Inputs in;
+    Inputs in(es);
     if (int rc = in.check_params(fn, a)) return rc;
     const Extent fin = extent_of(final_state, (size_t)a->B * a->D * a->N * sizeof(float));
     if (!al(final_state, 16)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a and the states must be 16-byte aligned", fn);
@@ -185,13 +180,13 @@ int hla2_ssm_forward(const hla2_ssm_args* a, hla2_rows out, float* final_state, 
     if (a->n > 0) {
         if (int rc = in.check(fn, a, a->n)) return rc;
         if (int rc = check_tensor(fn, o, es, true)) return rc;
-        if (in.meets(o.extent(es)) || meet(o.extent(es), fin))
+        if (in.read.meets(o) || meet(o.extent(es), fin))
             return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out overlaps another tensor", fn);
         vec = in.vec(a, kSsmVec) && o.vec(kSsmVec, es);
     } else if (!final_state) {
         return ok();
     }
-    if (in.meets(fin)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: final_state overlaps an input", fn);
+    if (in.read.meets(fin)) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: final_state overlaps an input", fn);
     const SsmPlan pl = ssm_plan(a, false);
     const Scratch s = scratch_of(a, pl, false);
     if (s.total > 0 && (!a->workspace || a->workspace_bytes < s.total || !al(a->workspace, 16)))
@@ -217,10 +212,10 @@ int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfina
     if (!grads) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: grads must not be NULL", fn);
     if (a->D == 0) return ok();
     const int es = elem_size(a->dtype);
-    Inputs in;
+    Inputs in(es);
     if (int rc = in.check_params(fn, a)) return rc;
     const size_t db = (size_t)a->D * sizeof(float);
-    in.read[in.reads++] = extent_of(dfinal_state, db * a->B * a->N);
+    in.read.add(extent_of(dfinal_state, db * a->B * a->N));
     if (!grads->da || (a->skip != nullptr) != (grads->dskip != nullptr) ||
         (a->dt_bias != nullptr) != (grads->ddt_bias != nullptr))
         return set_last_error(HLA2_ERR_INVALID_ARG,
@@ -229,17 +224,13 @@ int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfina
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a and the states must be 16-byte aligned", fn);
     if (!al(grads->da, 4) || !al(grads->dskip, 4) || !al(grads->ddt_bias, 4))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", fn);
-    Extent written[9];
-    int count = 0;
-    written[count++] = extent_of(grads->da, db * a->N);
-    written[count++] = extent_of(grads->dskip, db);
-    written[count++] = extent_of(grads->ddt_bias, db);
-    written[count++] = extent_of(grads->dinit_state, db * a->B * a->N);
+    const Extent sums[4] = {extent_of(grads->da, db * a->N), extent_of(grads->dskip, db), extent_of(grads->ddt_bias, db),
+                            extent_of(grads->dinit_state, db * a->B * a->N)};
     bool vec = true;
     Tensor o[6] = {};
+    int outs = 0;
     if (a->n > 0 && a->B > 0) {
         if (int rc = in.check(fn, a, a->n)) return rc;
-        int outs = 0;
         o[outs++] = rows("dout", dout, a->B, a->n, a->D);
         o[outs++] = rows("dx", grads->dx, a->B, a->n, a->D);
         o[outs++] = rows("ddt", grads->ddt, a->B, a->n, a->D);
@@ -249,18 +240,23 @@ int hla2_ssm_backward(const hla2_ssm_args* a, hla2_rows dout, const float* dfina
         vec = in.vec(a, kSsmVec);
         for (int i = 0; i < outs; ++i) {
             if (int rc = check_tensor(fn, o[i], es, i > 0)) return rc;
-            if (i == 0) in.read[in.reads++] = o[i].extent(es);
-            else written[count++] = o[i].extent(es);
+            if (i == 0) in.read.add(o[i]);
             vec = vec && o[i].vec(kSsmVec, es);
         }
     }
     if ((a->gate.p != nullptr) != (grads->dgate.p != nullptr) && a->n > 0 && a->B > 0)
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: dgate is needed with gate, and only then", fn);
-    for (int i = 0; i < count; ++i) {
-        if (in.meets(written[i])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps an input", fn);
-        for (int j = 0; j < i; ++j)
-            if (meet(written[i], written[j])) return set_last_error(HLA2_ERR_INVALID_ARG, "%s: gradients overlap", fn);
-    }
+    Places written(es);
+    int rc = 0;
+    auto write = [&](const auto& e) {
+        if (rc) return;
+        if (in.read.meets(e)) rc = set_last_error(HLA2_ERR_INVALID_ARG, "%s: a gradient overlaps an input", fn);
+        else if (written.meets(e)) rc = set_last_error(HLA2_ERR_INVALID_ARG, "%s: gradients overlap", fn);
+        else written.add(e);
+    };
+    for (const Extent& e : sums) write(e);
+    for (int i = 1; i < outs; ++i) write(o[i]);
+    if (rc) return rc;
     const SsmPlan pl = ssm_plan(a, true);
     const Scratch s = scratch_of(a, pl, true);
     if (s.total > 0 && (!a->workspace || a->workspace_bytes < s.total || !al(a->workspace, 16)))
@@ -291,15 +287,15 @@ int hla2_ssm_decode_step(const hla2_ssm_args* a, float* state, hla2_rows out, hl
     if (a->lengths || a->init_state)
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: lengths and init_state must be NULL", fn);
     const int es = elem_size(a->dtype);
-    Inputs in;
+    Inputs in(es);
     if (int rc = in.check_params(fn, a)) return rc;
     if (int rc = in.check(fn, a, 1)) return rc;
     if (!state || !al(state, 16))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: the state must be a 16-byte aligned address", fn);
     const Tensor o = rows("out", out, a->B, 1, a->D);
     if (int rc = check_tensor(fn, o, es, true)) return rc;
-    const Extent eo = o.extent(es), est = extent_of(state, (size_t)a->B * a->D * a->N * sizeof(float));
-    if (meet(eo, est) || in.meets(eo) || in.meets(est))
+    const Extent est = extent_of(state, (size_t)a->B * a->D * a->N * sizeof(float));
+    if (meet(o.extent(es), est) || in.read.meets(o) || in.read.meets(est))
         return set_last_error(HLA2_ERR_INVALID_ARG, "%s: out or the state overlaps another tensor", fn);
     SsmPass p = base_pass(a, in, SsmPlan{1, 1, 1});
     p.out = dev(o);

@@ -563,6 +563,9 @@ int hla2_w4_matvec(const void* x, long long x_stride, const void* qweight, const
  *
  * Rows of tokens are a base address and the element strides of batch and token; the last dimension is
  * contiguous.  Inputs may have any non-negative strides and any alignment of an element; 16-byte ones are faster.
+ * What a call writes may share no element with its other tensors.  Tensors of tokens may lie side by side in one buffer, as parts of its
+ * rows (halves of [B, n, 2 D], b beside c): their columns have to be apart modulo a common divisor of all their strides.  Other
+ * tensors whose ranges from first to last element meet count as sharing.
  * These calls have no device-side waits; their workspace has no status word and needs no initial contents.
  */
 typedef struct {

@@ -4,6 +4,7 @@ any launch, empty calls succeed, and the packed arguments have the header's layo
 Addresses are made up and never dereferenced: a call that passes the checks would be launched, so those are made only where
 there is no device to launch on (-4)."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -346,3 +347,65 @@ def test_steps_do_not_look_at_n(L, n):
         assert step(None, state, out, None) == -1
         if NO_GPU:
             assert step(ctypes.byref(args(**none)), state, out, None) == -4
+
+
+def test_gradients_may_lie_side_by_side(L):
+    """Parts of the rows of one buffer share no element, though their address ranges meet."""
+    wide = lambda p, at=0, d=2 * D: Rows(p + 2 * at, N * d, d)  # noqa: E731
+    both = lambda p, at, each=16, d=2 * G * 16: View(p + 2 * at, N * d, each, d)  # noqa: E731
+    ok = [dict(dx=wide(0x40000000), dgate=wide(0x40000000, D)),
+          dict(dx=wide(0x40000000, D), dgate=wide(0x40000000)),
+          dict(dx=wide(0x40000000, 0, 3 * D), ddt=wide(0x40000000, D, 3 * D), dgate=wide(0x40000000, 2 * D, 3 * D)),
+          dict(db=both(0x40000000, 0), dc=both(0x40000000, G * 16)),
+          dict(db=both(0x40000000, 0, 32), dc=both(0x40000000, 16, 32)),  # group by group
+          dict(dx=Rows(0x40000000, 2 * D, 2 * B * D), dgate=Rows(0x40000000 + 2 * D, 2 * D, 2 * B * D))]  # tokens before sequences
+    for kw in ok:
+        assert backward(L, ssm(), grads(**kw)) == -3, kw
+    bad = [dict(dx=wide(0x40000000), dgate=wide(0x40000000, D - 1)), dict(dx=wide(0x40000000, 1), dgate=wide(0x40000000, D + 2)),
+           dict(dx=wide(0x40000000), dgate=wide(0x40000000)), dict(dx=wide(0x40000000), dgate=wide(0x40000000, D, 2 * D + 1)),
+           dict(db=both(0x40000000, 0), dc=both(0x40000000, G * 16 - 1)), dict(db=both(0x40000000, 0, 32), dc=both(0x40000000, 24, 32)),
+           dict(dx=wide(0x40000000), da=0x40000000 + 16 * D)]  # the sums have no place in a row
+    for kw in bad:
+        assert backward(L, ssm(), grads(**kw)) == -1, kw
+    # outputs beside inputs
+    assert forward(L, ssm(x=wide(0x40000000)), wide(0x40000000, D)) == -3
+    assert forward(L, ssm(x=wide(0x40000000)), wide(0x40000000, D + 1)) == -1
+    assert backward(L, ssm(x=wide(0x40000000)), grads(dx=wide(0x40000000, D))) == -3
+    assert conv_backward(L, conv(x=wide(0x40000000)), dx=wide(0x40000000, D)) == -3
+    assert conv_backward(L, conv(x=wide(0x40000000)), dx=wide(0x40000000, D // 2)) == -1
+    assert conv_backward(L, conv(), dx=wide(0x40000000), dw=0x40000000 + 4 * D) == -1
+    if NO_GPU:
+        assert conv_forward(L, conv(x=wide(0x40000000)), wide(0x40000000, D)) == -4
+        a = conv(lengths=None, init_state=None, x=Rows(0x40000000, 2 * D, 0))
+        assert L.hla2_short_conv_decode_step(ctypes.byref(a), 0x21000000, Rows(0x40000000 + 2 * D, 2 * D, 0), None) == -4
+        a = ssm(lengths=None, init_state=None, x=Rows(0x40000000, 2 * D, 0))
+        assert L.hla2_ssm_decode_step(ctypes.byref(a), 0x21000000, Rows(0x40000000 + 2 * D, 2 * D, 0), None) == -4
+
+
+def test_no_shared_element_passes(L):
+    """Random layouts of two gradients in one buffer: those that share an element are refused, whatever their strides."""
+    rng = random.Random(3)
+    seen = {-1: 0, -3: 0}
+    for _ in range(4000):
+        b, n, d = rng.randint(1, 3), rng.randint(1, 4), rng.choice([4, 6])
+        unit = rng.choice([d, d + 2, 2 * d, 3 * d])
+        sn = rng.choice([unit, unit * rng.randint(1, 3), unit + rng.randint(0, 3)])
+        sb = rng.choice([sn * n, sn * n + unit, sn * n + rng.randint(0, 5)])
+        first = Rows(0x40000000, sb, sn)
+        if rng.random() < 0.3:
+            sn, sb = sn * 2, sb * rng.choice([1, 2])
+        second = Rows(0x40000000 + 2 * rng.randint(0, 3 * unit), sb, sn)
+
+        def places(r):
+            return [r.p + 2 * (i * r.sb + t * r.sn + k) for i in range(b) for t in range(n) for k in range(d)]
+
+        one, two = places(first), places(second)
+        args = ssm(B=b, n=n, D=d, G=1, gate=rows(0x12000000, n, d), x=rows(0x10000000, n, d), dt=rows(0x11000000, n, d),
+                   b=View(0x13000000, n * 16, 16, 16), c=View(0x14000000, n * 16, 16, 16))
+        g = grads(dx=first, dgate=second, ddt=rows(0x31000000, n, d), db=View(0x33000000, n * 16, 16, 16),
+                  dc=View(0x34000000, n * 16, 16, 16))
+        rc = backward(L, args, g, dout=rows(0x22000000, n, d))
+        seen[rc] += 1
+        shared = len(set(one + two)) < len(one) + len(two)
+        assert rc == -1 or not shared, (b, n, d, first.sb, first.sn, second.p - first.p, second.sb, second.sn)
+    assert min(seen.values()) > 300, seen
