@@ -913,6 +913,24 @@ class _Lin(NamedTuple):
             _check(fn.__name__, rc)
 
 
+def _length_tensor(lengths, B, n, device):
+    """Token counts as the kernels read them: int32 on the device."""
+    if lengths is None:
+        return None
+    given = lengths
+    if not (isinstance(lengths, torch.Tensor) and lengths.dtype == torch.int32 and lengths.device == device
+            and lengths.is_contiguous()):
+        lengths = torch.as_tensor(lengths, device=device)
+        if lengths.numel() == 0 and not isinstance(given, torch.Tensor):  # a list's type is its elements'
+            lengths = lengths.to(torch.int32)
+        if lengths.dtype not in (torch.int32, torch.int64):
+            raise ValueError("lengths must be integers")
+        lengths = (lengths.clamp(0, n) if lengths.dtype == torch.int64 else lengths).to(torch.int32).contiguous()
+    if lengths.shape != (B,):
+        raise ValueError("lengths must be B integers")
+    return lengths
+
+
 def _linattn_args(q, k, v, gamma, scale, lengths, init_state):
     index = _need_cuda(q, k, v)
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
@@ -925,14 +943,7 @@ def _linattn_args(q, k, v, gamma, scale, lengths, init_state):
     if (Hk == 0) != (H == 0) or (Hk and H % Hk):
         raise ValueError("the query heads must be a multiple of the key heads")
     g = _float_vector(gamma, Hk, device)
-    if lengths is not None and not (isinstance(lengths, torch.Tensor) and lengths.dtype == torch.int32
-                                    and lengths.device == device and lengths.is_contiguous()):
-        lengths = torch.as_tensor(lengths, device=device)
-        if lengths.dtype not in (torch.int32, torch.int64):
-            raise ValueError("lengths must be integers")
-        lengths = (lengths.clamp(0, n) if lengths.dtype == torch.int64 else lengths).to(torch.int32).contiguous()
-    if lengths is not None and lengths.shape != (B,):
-        raise ValueError("lengths must be B integers")
+    lengths = _length_tensor(lengths, B, n, device)
     init = _state_arg("init_state", init_state, (B, Hk, d, dv), device)
     qt, *qv = _view4(q)
     kt, *kv = _view4(k)
@@ -1315,21 +1326,6 @@ def _float_param(name, t, shape, index):
     if tuple(t.shape) != shape or t.get_device() != index:
         raise ValueError(f"{name} must be {shape} on the inputs' device")
     return _packed16(t.to(torch.float32))
-
-
-def _length_tensor(lengths, B, n, device):
-    """Token counts as the kernels read them: int32 on the device."""
-    if lengths is None:
-        return None
-    if not (isinstance(lengths, torch.Tensor) and lengths.dtype == torch.int32 and lengths.device == device
-            and lengths.is_contiguous()):
-        lengths = torch.as_tensor(lengths, device=device)
-        if lengths.dtype not in (torch.int32, torch.int64):
-            raise ValueError("lengths must be integers")
-        lengths = (lengths.clamp(0, n) if lengths.dtype == torch.int64 else lengths).to(torch.int32).contiguous()
-    if lengths.shape != (B,):
-        raise ValueError("lengths must be B integers")
-    return lengths
 
 
 def _run_on_scratch(fn, index, call, query):

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import chunked_scan_mixer_gb300 as hla
-from chunked_scan_mixer_gb300.hla2 import _CONV_ARGS, _NORM_ARGS, _SSM_ARGS, _SSM_GRADS, Rows, View
+from chunked_scan_mixer_gb300.hla2 import _CONV_ARGS, _NORM_ARGS, _SSM_ARGS, _SSM_GRADS, Rows, View, _length_tensor
 
 NO_GPU = not torch.cuda.is_available()
 I, P, Q, Z = ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_size_t
@@ -409,3 +409,12 @@ def test_no_shared_element_passes(L):
         shared = len(set(one + two)) < len(one) + len(two)
         assert rc == -1 or not shared, (b, n, d, first.sb, first.sn, second.p - first.p, second.sb, second.sn)
     assert min(seen.values()) > 300, seen
+
+
+def test_lengths_of_no_sequences():
+    none = _length_tensor([], 0, 5, torch.device("cpu"))
+    assert none.dtype == torch.int32 and none.shape == (0,)
+    assert _length_tensor([7, -1, 1 << 40], 3, 5, torch.device("cpu")).tolist() == [5, 0, 5]
+    for bad in ([1.0], [True], torch.zeros(1), torch.zeros(0), [], [1, 2], torch.zeros(2, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            _length_tensor(bad, 1, 5, torch.device("cpu"))
