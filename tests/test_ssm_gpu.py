@@ -312,3 +312,86 @@ def test_no_channels(dtype):
     g = hla.ssm_backward(dout=out, **c)
     assert g.db.shape == g.dc.shape == (2, 5, 1, 16) and g.da.shape == (0, 16) and g.dx.shape == (2, 5, 0)
     assert (g.db == 0).all() and (g.dc == 0).all()
+
+
+def small_steps(n, dtype=F32):
+    """Channels with steps softplus(v) of about e^-30 to e^-3, and positive values throughout, so that no sum cancels; each channel is a
+    group of its own, so that b's and c's gradients are its alone."""
+    v = torch.linspace(-30.0, -3.0, 28, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rand = lambda *s: 0.9 + 0.2 * torch.rand(s, generator=g, device="cuda")  # noqa: E731
+    D, N = len(v), 8
+    c = dict(x=rand(1, n, D), dt=v.expand(1, n, D).clone(), b=rand(1, n, D, N), c=rand(1, n, D, N))
+    c = {k: t.to(dtype) for k, t in c.items()}
+    c["a"] = -0.1 * torch.arange(1, N + 1, device="cuda", dtype=F32).repeat(D, 1)
+    return c, rand(1, n, D).to(dtype), v.double().cpu().numpy()
+
+
+def relative(got, want, tol, what):
+    """Every element within tol of its own value; tol over the channels, the dimension of size 28."""
+    g = f64(got)
+    assert g.shape == want.shape and (want != 0).all(), what
+    shape = [1] * g.ndim
+    shape[list(g.shape).index(len(tol))] = len(tol)
+    err = np.abs(g / want - 1.0) / tol.reshape(shape)
+    assert (err <= 1.0).all(), f"{what}: {err.max():.3g} of the tolerance at {np.unravel_index(err.argmax(), err.shape)}"
+
+
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("softplus", [True, False])
+def test_small_steps_keep_their_relative_accuracy(n, softplus):
+    """Nothing here but terms that are proportional to a step, each compared with its own value.
+
+    e^-|v| by the unit is good to 2^-22; its argument |v| log2 e is rounded twice, to half a step of the product and of the constant,
+    together 1.25 2^-24 |v| of the result.  A reciprocal (2^-23), the polynomial (1e-8) and six roundings give the step
+    (4 + 2 + 1 + 6) 2^-24; delta x, its product with b or c, a decay (4 and 1) for each of up to three tokens, and eight terms' sums
+    another 2 + 15 + 8.  With the decays, whose share of a gradient of the step is of the other sign and at most 2 tokens x 0.8 x
+    softplus(-3) x (1.1 / 0.9)^2 = 0.12 of it, 1.3 times that: 50 + 1.7 |v|.  da is a product of two steps: twice."""
+    c, dout, v = small_steps(n)
+    if not softplus:
+        c["dt"] = torch.exp(c["dt"])
+    tol = (50 + 1.7 * np.abs(v)) * 2.0 ** -24
+    out, fin = hla.ssm_forward(**c, dt_softplus=softplus, return_final_state=True)
+    args = oracle_args(c, dt_softplus=softplus)
+    want, wfin = O.ssm_forward(**args)
+    relative(out, want, tol, "out")
+    relative(fin, wfin, tol, "final state")
+    got, w = hla.ssm_backward(dout=dout, dt_softplus=softplus, **c), O.ssm_backward(dout=f64(dout), **args)
+    for name in ("dx", "ddt", "db", "dc"):
+        relative(getattr(got, name), w[name], tol, name)
+    if n > 1:  # one token from a zero state has no decay to differentiate
+        relative(got.da, w["da"], 2 * tol, "da")
+    state = torch.zeros_like(fin)
+    for t in range(n):
+        y = hla.ssm_decode_step(state, c["x"][:, t], c["dt"][:, t], c["a"], c["b"][:, t], c["c"][:, t], dt_softplus=softplus)
+        relative(y, want[:, t], tol, f"step {t}")
+    relative(state, wfin, tol, "state of the steps")
+
+
+def test_small_steps_in_bfloat16():
+    """States are float32 whatever the tensors' type: the bounds above, and one rounding more for what is bfloat16."""
+    c, dout, v = small_steps(3, BF)
+    tol = (50 + 1.7 * np.abs(f64(c["dt"])[0, 0])) * 2.0 ** -24
+    out, fin = hla.ssm_forward(**c, return_final_state=True)
+    want, wfin = O.ssm_forward(**oracle_args(c))
+    relative(fin, wfin, tol, "final state")
+    relative(out, want, tol + 2.0 ** -8, "out")
+    got, w = hla.ssm_backward(dout=dout, **c), O.ssm_backward(dout=f64(dout), **oracle_args(c))
+    relative(got.da, w["da"], 2 * tol, "da")
+    for name in ("dx", "ddt", "db", "dc"):
+        relative(getattr(got, name), w[name], tol + 2.0 ** -8, name)
+
+
+@pytest.mark.parametrize("N", [16, 64])
+def test_gradients_of_fast_states(N):
+    """The decays' gradients and the states fall off with the state's index, -1 .. -N; each index is held against its own
+    size (the bound of `close` is per state: a rounding of each token that it remembers)."""
+    c = make_ssm(2, 100, 72, N, seed=21)
+    dout = torch.randn_like(c["x"])
+    out, fin = hla.ssm_forward(**c, return_final_state=True)
+    wfin = O.ssm_forward(**oracle_args(c))[1]
+    g, w = hla.ssm_backward(dout=dout, **c), O.ssm_backward(dout=f64(dout), **oracle_args(c))
+    for k in range(N):
+        close(fin[..., k], wfin[..., k], f"state {k}")
+        close(g.da[:, k], w["da"][:, k], f"da {k}")
+        close(g.dinit_state[..., k], w["dinit_state"][..., k], f"dinit {k}")
