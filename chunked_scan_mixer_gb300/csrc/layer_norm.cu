@@ -147,6 +147,9 @@ __global__ void __launch_bounds__(NormShape<RW>::threads) layer_norm_kernel(cons
     pdl_trigger();
 }
 
+// Two vectors of eight a lane are held to 128 registers, 16 warps an SM: 16384 x 4096 113 -> 91 us (with 64 bytes of spills), 16384 x 2560
+// 101 -> 72, 32768 x 2048 95 -> 89, 200000 x 512 127 -> 115; rows that do not fill the GPU lose by it, 1000 x 4096 21 -> 25.  Shapes
+// without the bound: four float32 vectors of four take 158 to 174 registers, four bf16 vectors of eight 218, all others at most 128.
 template <typename T, int VEC, int NV, int RW>
 __global__ void __launch_bounds__(NormShape<RW>::threads, VEC == 8 && NV == 2 ? 512 / NormShape<RW>::threads : 1)
     layer_norm_backward_kernel(const hla2_norm_args a, const NormGrads g) {
