@@ -4,7 +4,8 @@ Every translation unit is compiled by nvcc in parallel, then linked into
 ``chunked_scan_mixer_gb300/_build/libhla2.so``.  Nothing is installed.  ``--debug`` builds
 the bounds-checking variant (HLA2_DEBUG: global-memory indices checked against the buffer
 extents, a failed check recorded and the access skipped; see hla2_debug_status) into
-``chunked_scan_mixer_gb300/_build_debug/libhla2.so``.  The normal build also makes the Python module of
+``chunked_scan_mixer_gb300/_build_debug/libhla2.so``.  The HLA kernels have these checks; those around a layer
+(linear attention, block norms, 4-bit products) and of a selective state space layer have none.  The normal build also makes the Python module of
 the short calls' host side (csrc/host_calls.cpp), which the binding goes without where it cannot be
 built.
 

@@ -3,14 +3,15 @@
 //   p_t = bias + sum_j w_j x_{t - W + 1 + j},  y_t = act(p_t)
 //   dp = dy act'(p),  dx_s = sum_j w_j dp_{s + W - 1 - j},  dw_j = sum_t dp_t x_{t - W + 1 + j},  dbias = sum_t dp_t.
 //
-// Bytes bound all of them: x read and y written once, x and dy read and dx written in the backward, which forms p again.
+// Bytes are the floor of all of them: x read and y written once, x and dy read and dx written in the backward, which forms p again.
 // A thread has one vector of channels and walks over a run of tokens with the last W - 1 inputs (and dp's) in registers,
 // several tokens' loads ahead; the runs' edges are read twice.  The backward's sums of a thread go through shared memory to
 // one partial row a CTA, which a second kernel adds in a fixed order.
 //
 // 65536 x 2048 bf16, W = 4: 93 us (5.7 TB/s, 85 % of the measured copy).  Four tokens a block without conditions, the inputs of a block
-// in place instead of a window that moves: 132 us before, with 35 instructions for two values instead of 16.  Backward of 8 x 4096 x 2048:
-// 102 us (4.0 TB/s): instructions, at two CTAs an SM (107 us; 137 with one, 325 with three, which spill).
+// in place instead of a window that moves: 132 us before, with 35 instructions for two values instead of 16.  Backward of 8 x 4096 x 2048,
+// bf16: 102 us (4.0 TB/s), 100 of them this kernel, at two CTAs an SM (137 with one, 325 with three): 128 registers of which W = 4 spills
+// 88 bytes (164 read back), float32 252 (588; W = 3 84 and 204), and 2.0 warp instructions a cycle and SM at 14 warps (float32 1.3).
 #include <type_traits>
 
 #include "packed.cuh"

@@ -86,6 +86,9 @@ struct SsmPlan {
 // there the fullest SM counts, above it they follow one another without waves.  More than one segment adds the pass of
 // their sums, a launch, and the joining of the segments before, which a CTA reads four at a time; the backward has a pass
 // of marks without them too.
+// The scaling to other N foretells the forward to an eighth up to N = 32, and too little beyond and in the backward: 4 x 2048 x 2048 with N = 8, 16,
+// 32 and 64 takes 115, 155, 275 and 463 us for 123, 162, 245 and 358 foretold, backward 390, 472, 927 and 1980 for 342, 468, 720 and
+// 1224.  (The output kernels hold 16, 7, 4 and 2 CTAs an SM there, by threads and shared memory, where `most` has 14, 7, 3 and 1.)
 // (2 x 2048 x 2048, N = 16, forward: one segment 363 us, 8 105, 16 89, 64 107; backward 1299, 282, 274, 311.  8 x 4096 x 4096, which
 // fills the GPU by itself: forward 939 with one, 1050 with 8.)
 struct SsmCost {

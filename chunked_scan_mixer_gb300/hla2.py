@@ -1417,7 +1417,8 @@ def _ssm_forward(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, lengths, init
 def ssm_backward(x, dt, a, b, c, dout, skip=None, gate=None, dt_bias=None, dt_softplus=True, lengths=None,
                  init_state=None, dfinal_state=None):
     """SsmGrads of ssm_forward for the upstream gradient dout [B,n,D] of its output and dfinal_state (None: zero) of its
-    final state.  Nothing is kept from the forward."""
+    final state.  Nothing is kept from the forward.  Scratch of about 3 N / 8 bytes for each token and channel (7 at N = 16, 27 at N =
+    64) stays allocated for the stream's next calls."""
     res = _quick_scratch("ssm_backward", x, x, dt, a, b, c, skip, gate, dt_bias, bool(dt_softplus), lengths, init_state, dout,
                          dfinal_state)
     if res is not None:

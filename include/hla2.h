@@ -566,6 +566,8 @@ int hla2_w4_matvec(const void* x, long long x_stride, const void* qweight, const
  * What a call writes may share no element with its other tensors.  Tensors of tokens may lie side by side in one buffer, as parts of its
  * rows (halves of [B, n, 2 D], b beside c): their columns have to be apart modulo a common divisor of all their strides.  Other
  * tensors whose ranges from first to last element meet count as sharing.
+ * Negative values of a decay.  Positive ones grow; where exp(a sum of the steps) of a part of a sequence passes float32's range,
+ * its states are not finite even from a state of zero.
  * These calls have no device-side waits; their workspace has no status word and needs no initial contents.
  */
 typedef struct {
@@ -588,7 +590,9 @@ typedef struct {
 } hla2_ssm_args;
 
 /* Scratch bytes of a forward (backward = 0) or a backward (1); the addresses in *a are not looked at.
- * (size_t)-1 for arguments that the call would reject. */
+ * (size_t)-1 for arguments that the call would reject.  A backward takes a state for every sixteen tokens and the parts of db and dc
+ * of each 64 channels, 3 N / 8 bytes and a little for each token and channel (7 at N = 16, 27 at N = 64: 7.2 GB for 65536 tokens of
+ * 4096 channels); a forward at most 1024 segments' states. */
 size_t hla2_ssm_workspace_bytes(const hla2_ssm_args* a, int backward);
 
 /* out [B, n, D]; final_state (nullable) receives the contiguous [B, D, N] state after each sequence's last token.
