@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
     }
     SsmState a, h;
     a.load(p.a + (long long)(at.c0 + 4 * cg) * N + 4 * sl, N, chans);
-    a.scale(kLog2E);
+    a.exponents();
     h.zero();
     if (!SUMS) {
         if (p.init) h.load(p.init + ((long long)at.b * p.D + at.c0 + 4 * cg) * N + 4 * sl, N, chans);
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(256) ssm_carry_kernel(const SsmPass p, float* 
     for (int j = 0; j < 4; ++j) {
         const bool on = in + j < p.per;
         const long long at = (long long)(ch + j) * N + 4 * sl + k;
-        a[j] = on ? p.a[at] * kLog2E : 0.f;
+        a[j] = on ? exponent_of(p.a[at]) : 0.f;
         h[j] = on && from ? from[(long long)b * p.D * N + at] : 0.f;
     }
     for (int first = 0; first < p.nseg; first += 32) {
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmPass p, float* _
         if (on && s0 + q < p.B) h[q] = __ldcs(reinterpret_cast<const float4*>(st + q * step));
         else h[q] = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 a = *reinterpret_cast<const float4*>(p.a + (long long)dc * N + 4 * sl);
-    a.x *= kLog2E, a.y *= kLog2E, a.z *= kLog2E, a.w *= kLog2E;
+    a.x = exponent_of(a.x), a.y = exponent_of(a.y), a.z = exponent_of(a.z), a.w = exponent_of(a.w);
     const float skip = p.skip ? p.skip[dc] : 0.f, bias = p.dt_bias ? p.dt_bias[dc] : 0.f;
     // this lane's sequences: lane + LQ m of the Q (all lanes one, where there is one)
     float delta[own], u[own], xv[own], zv[own];

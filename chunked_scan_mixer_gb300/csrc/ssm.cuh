@@ -94,6 +94,13 @@ __device__ __forceinline__ F2 ex2_(F2 a) {
 
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// a log2(e), finite where a is -inf or as low: the tokens that fill up a tile have delta 0, and 0 times -inf would make their decay NaN
+// instead of 1, and a gradient of the step NaN where the decay is 0
+__device__ __forceinline__ float exponent_of(float a) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0fFF7FFFFF;" : "=f"(r) : "f"(a * kLog2E));
+    return r;
+}
 // A token's decay exp(delta a), from a log2(e).  The instruction's results are a little low: for exponents of -4e-6 .. -2e-3 by 5e-9 to
 // 1e-8 on average (measured), which a product over thousands of tokens adds up.  1e-8 more in the exponent leaves 3e-9 there and
 // less than before everywhere, and 1 for an exponent of 0.
@@ -351,9 +358,16 @@ struct SsmState {
 #pragma unroll
         for (int s = 0; s < 4; ++s) st4(p + ((long long)s * threads + threadIdx.x) * 4, {v[s][0], v[s][1]});
     }
-    __device__ __forceinline__ void scale(float f) {
+    // of a, exponents of the decays
+    __device__ __forceinline__ void exponents() {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) v[s][0] = v[s][0] * pair(f, f), v[s][1] = v[s][1] * pair(f, f);
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float lo, hi;
+                split(v[s][i], lo, hi);
+                v[s][i] = pair(exponent_of(lo), exponent_of(hi));
+            }
     }
 };
 

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 512 / SsmShape<N>::threa
     for (int i = tid; i < CT; i += NT) sbias[i] = p.dt_bias && i < at.cols ? p.dt_bias[at.c0 + i] : 0.f;
     SsmState a, h, W, R;  // W: the decay since the segment's start
     a.load(p.a + (long long)(at.c0 + 4 * cg) * N + 4 * sl, N, chans);
-    a.scale(kLog2E);
+    a.exponents();
     h.zero();
     if (!REV && p.init) h.load(p.init + ((long long)at.b * p.D + at.c0 + 4 * cg) * N + 4 * sl, N, chans);
     R.zero();
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(SsmShape<N>::threads, 256 / SsmShape<N>::threa
     const long long state_at = ((long long)at.b * p.D + at.c0 + 4 * cg) * N + 4 * sl;
     SsmState a, h, E, da;
     a.load(p.a + (long long)(at.c0 + 4 * cg) * N + 4 * sl, N, chans);
-    a.scale(kLog2E);
+    a.exponents();
     da.zero();
     h.zero();
     E.zero();

@@ -566,7 +566,7 @@ int hla2_w4_matvec(const void* x, long long x_stride, const void* qweight, const
  * What a call writes may share no element with its other tensors.  Tensors of tokens may lie side by side in one buffer, as parts of its
  * rows (halves of [B, n, 2 D], b beside c): their columns have to be apart modulo a common divisor of all their strides.  Other
  * tensors whose ranges from first to last element meet count as sharing.
- * Negative values of a decay.  Positive ones grow; where exp(a sum of the steps) of a part of a sequence passes float32's range,
+ * Negative values of a decay (-inf: at once).  Positive ones grow; where exp(a sum of the steps) of a part of a sequence passes float32's range,
  * its states are not finite even from a state of zero.
  * These calls have no device-side waits; their workspace has no status word and needs no initial contents.
  */

@@ -395,3 +395,29 @@ def test_gradients_of_fast_states(N):
         close(fin[..., k], wfin[..., k], f"state {k}")
         close(g.da[:, k], w["da"][:, k], f"da {k}")
         close(g.dinit_state[..., k], w["dinit_state"][..., k], f"dinit {k}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("n, lengths", [(5, None), (16, None), (37, [37, 20]), (700, [1, 699])])
+def test_states_that_forget_at_once(dtype, N, n, lengths):
+    """a = -inf (or so low that a log2 e is): the state is the last token's input alone.  The tokens that fill up a tile, with steps of
+    zero, leave it as it is."""
+    c = make_ssm(2, n, 40, N, dtype=dtype, seed=n)
+    far = {**c, "a": c["a"].clone()}
+    far["a"][3], far["a"][7, 1::2] = -1e30, -1e30  # finite, so that the oracle's gradients are
+    out, fin = check_forward(far, lengths)
+    lens = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    dout, dfin = torch.randn_like(c["x"]), torch.randn_like(c["init_state"])
+    grads = hla.ssm_backward(dout=dout, dfinal_state=dfin, lengths=lens, **far)
+    if n < 100:
+        check_backward(far, lengths)
+    for low in (-float("inf"), torch.finfo(F32).min):
+        v = {**c, "a": far["a"].masked_fill(far["a"] == -1e30, low)}
+        got = hla.ssm_forward(**v, lengths=lens, return_final_state=True)
+        assert torch.equal(got[0], out) and torch.equal(got[1], fin)
+        for name, a, b in zip(grads._fields, hla.ssm_backward(dout=dout, dfinal_state=dfin, lengths=lens, **v), grads):
+            assert torch.equal(a, b), name
+        one = {k: v[k][:, 0] if k in ("x", "dt", "b", "c", "gate") else v[k] for k in v if k != "init_state"}
+        s, t = c["init_state"].clone(), c["init_state"].clone()
+        assert torch.equal(hla.ssm_decode_step(s, **one), hla.ssm_decode_step(t, **{**one, "a": far["a"]})) and torch.equal(s, t)
